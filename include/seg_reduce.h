@@ -49,7 +49,8 @@ extern "C" {
 /* Same type as the CUDA runtime's cudaStream_t; NULL is the legacy default stream. */
 typedef struct CUstream_st *seg_stream_t;
 
-typedef enum { SEG_U32 = 0, SEG_S32 = 1, SEG_F32 = 2 } seg_dtype_t;
+/* SEG_F16 and SEG_BF16 are types of the products (seg_matmul and after) alone. */
+typedef enum { SEG_U32 = 0, SEG_S32 = 1, SEG_F32 = 2, SEG_F16 = 3, SEG_BF16 = 4 } seg_dtype_t;
 typedef enum { SEG_OFF_U32 = 0, SEG_OFF_I64 = 1 } seg_offset_dtype_t;
 typedef enum { SEG_SUM = 0, SEG_MIN = 1, SEG_MAX = 2, SEG_MEAN = 3 } seg_op_t;
 
@@ -397,6 +398,97 @@ seg_status_t seg_rle(const uint32_t *keys, int64_t n, uint32_t *values, uint32_t
  */
 seg_status_t seg_flags_to_offsets(const uint8_t *flags, int64_t n, int64_t *offsets,
                                   int64_t *count, seg_stream_t stream);
+
+/*
+ * seg_matmul -- the rows of every segment times the segment's own matrix.
+ *
+ * The pages have no counterpart: it is the product that follows a grouping
+ * (rows sorted by relation type, by expert), over the same segments.
+ *   out[r, n] = sum_k x[r, k] * w[s, k, n]   for a row r of segment s,
+ * and out[r, :] = 0 for a row in no segment.  With transpose_w the matrices
+ * are stored [N, K]: w[s, n, k].  The gradient of x is therefore the same
+ * call on dy with the other value of transpose_w.
+ *
+ *   x             device, [num_rows, K], rows ldx elements apart (ldx >= K),
+ *                 of `dtype`.
+ *   dtype         SEG_F32, SEG_F16 or SEG_BF16: the type of x, w and out.
+ *   num_rows      0 <= R < 2^31.
+ *   K, N          0 <= K, 0 <= N, both at most SEG_MAX_PRODUCT_COLUMNS.  K == 0
+ *                 gives zeros; R == 0 or N == 0 launches nothing.
+ *   w             device, num_segments matrices stride_w elements apart, each
+ *                 [K, N] (transpose_w: [N, K]) with rows ldw elements apart.
+ *   offsets, offsets_dtype, num_segments: as for seg_reduce (clamped to
+ *                 [0, num_rows] on the device); at most 2^31 - 1 segments.
+ *   out           device, [num_rows, N], rows ldo elements apart (ldo >= N).
+ *
+ * Every pointer is aligned to its element; 16-byte aligned x and w whose row
+ * strides are multiples of 16 bytes enable the tensor-copy path of the
+ * 16-bit types.  w may hold any values for empty segments, and x for rows in
+ * no segment (NaN and infinities included): neither reaches the output.
+ *
+ * Numerics.  Sums are float32 in an order that is a pure function of the
+ * sizes, the offsets and the SM count (calls repeat bit for bit), rounded
+ * once to `dtype`.  The products of 16-bit types are exact.  float32 is
+ * multiplied on the tensor cores as three bfloat16 parts per value that hold
+ * it exactly; the parts' products below 2^-21 of the full one are left out.
+ * Before the last rounding the error of an output of n terms is below
+ * (n * 2^-24 + 2^-20) * sum(|x w|).  A float32 row or matrix that holds an
+ * infinity gives NaN where IEEE arithmetic would give an infinity.
+ */
+#define SEG_MAX_PRODUCT_COLUMNS 1048576
+
+seg_status_t seg_matmul(const void *x, seg_dtype_t dtype, int64_t num_rows, int64_t K, int64_t ldx,
+                        const void *w, int64_t N, int64_t ldw, int64_t stride_w, int32_t transpose_w,
+                        const void *offsets, seg_offset_dtype_t offsets_dtype, int64_t num_segments,
+                        void *out, int64_t ldo, seg_stream_t stream);
+
+/*
+ * seg_matmul_grad_w -- the gradient of seg_matmul's matrices.
+ *   out[s, k, n] = sum over the rows r of segment s of x[r, k] * dy[r, n];
+ * an empty segment gives zeros.  (For matrices stored [N, K] call it with x
+ * and dy exchanged.)
+ *
+ *   x, dtype, num_rows, K, ldx: as for seg_matmul.
+ *   dy            device, [num_rows, N], rows ldy elements apart, of `dtype`.
+ *   offsets, offsets_dtype, num_segments: as for seg_matmul.
+ *   out           device, [num_segments, K, N], contiguous, of out_dtype:
+ *                 `dtype`, or SEG_F32 to keep the sums as they are.
+ *
+ * Alignment and numerics as for seg_matmul.  Rows in no segment are not used.
+ */
+seg_status_t seg_matmul_grad_w(const void *x, seg_dtype_t dtype, int64_t num_rows, int64_t K, int64_t ldx,
+                               const void *dy, int64_t N, int64_t ldy, const void *offsets,
+                               seg_offset_dtype_t offsets_dtype, int64_t num_segments, void *out,
+                               seg_dtype_t out_dtype, seg_stream_t stream);
+
+/*
+ * seg_lora -- a shared projection with the low-rank adapters of many requests.
+ * Segment s holds the rows of request s, which uses adapter l = adapter[s]:
+ *   out[r, n] = sum_k x[r, k] * w[n, k]
+ *             + scale[l] * sum_j (sum_k x[r, k] * a[l, j, k]) * b[l, n, j].
+ * A request whose adapter is outside [0, num_adapters), and a row in no
+ * segment, take the shared product alone.
+ *
+ *   x, dtype, num_rows, K, ldx: as for seg_matmul (x, w, a, b and out share dtype).
+ *   w             device, [N, K], rows ldw elements apart.
+ *   a, b          device, [num_adapters, rank, K] and [num_adapters, N, rank],
+ *                 contiguous.  May be NULL when num_adapters == 0.
+ *   rank          1 <= rank <= SEG_MAX_RANK (else SEG_ERR_UNSUPPORTED).
+ *   offsets, offsets_dtype, num_segments: as for seg_matmul.
+ *   adapter       device, [num_segments] int32.
+ *   scale         device, [num_adapters] float32, or NULL for 1.
+ *   out           device, [num_rows, N], rows ldo elements apart.
+ *
+ * The inner products with a are kept in float32; the whole sum is rounded
+ * once.  Alignment and numerics otherwise as for seg_matmul.
+ */
+#define SEG_MAX_RANK 128
+
+seg_status_t seg_lora(const void *x, seg_dtype_t dtype, int64_t num_rows, int64_t K, int64_t ldx,
+                      const void *w, int64_t N, int64_t ldw, const void *a, const void *b,
+                      int64_t num_adapters, int64_t rank, const void *offsets,
+                      seg_offset_dtype_t offsets_dtype, int64_t num_segments, const int32_t *adapter,
+                      const float *scale, void *out, int64_t ldo, seg_stream_t stream);
 
 /*
  * seg_selftest_wait_timeout -- exercise the failure path of the bounded

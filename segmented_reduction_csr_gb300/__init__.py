@@ -24,7 +24,11 @@ Beside the reduction (``seg_reduce``, ``segment_*_csr``, ``seg_reduce_noalloc``)
 * ``seg_scan`` / ``segment_cumsum_csr``: segmented inclusive / exclusive scan;
 * ``seg_rle`` / ``rle`` / ``unique`` and ``seg_flags_to_offsets`` /
   ``flags_to_offsets``: producers of offsets (GPURunLengthEncode, GPUUnique,
-  GPUSegmentedLayout).
+  GPUSegmentedLayout);
+* ``seg_matmul`` / ``seg_matmul_grad_w`` / ``segment_matmul``: the rows of
+  every segment times the segment's own matrix, the matrices' gradient, and
+  the two as one differentiable call; ``seg_lora``: a shared projection with
+  the low-rank adapters of many requests (float32, float16, bfloat16).
 """
 from __future__ import annotations
 
@@ -39,13 +43,14 @@ __all__ = [
     "seg_rle", "rle", "unique", "seg_flags_to_offsets", "flags_to_offsets",
     "seg_reduce_sequential", "scatter", "scatter_sum", "scatter_add", "scatter_mean",
     "scatter_max", "scatter_min", "seg_scan", "segment_cumsum_csr",
+    "seg_matmul", "seg_matmul_grad_w", "segment_matmul", "seg_lora",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "lib", "libsegreduce.so")
 
 # Codes of include/seg_reduce.h
-SEG_U32, SEG_S32, SEG_F32 = 0, 1, 2
+SEG_U32, SEG_S32, SEG_F32, SEG_F16, SEG_BF16 = 0, 1, 2, 3, 4
 SEG_OFF_U32, SEG_OFF_I64 = 0, 1
 OPS = {"sum": 0, "min": 1, "max": 2, "mean": 3}
 STATUS = {0: "SEG_OK", 1: "SEG_ERR_INVALID_ARGUMENT", 2: "SEG_ERR_UNSUPPORTED",
@@ -54,6 +59,7 @@ STATUS = {0: "SEG_OK", 1: "SEG_ERR_INVALID_ARGUMENT", 2: "SEG_ERR_UNSUPPORTED",
 EXPORTED = ("seg_reduce", "seg_reduce_strerror", "seg_reduce_device_status",
             "seg_reduce_plan", "seg_reduce_version", "seg_reduce_noalloc", "seg_rle",
             "seg_flags_to_offsets", "seg_reduce_sequential", "seg_scatter", "seg_scatter_sorted", "seg_scan",
+            "seg_matmul", "seg_matmul_grad_w", "seg_lora",
             "seg_selftest_wait_timeout")
 NOALLOC_SCRATCH_BYTES = 2 << 20   # SEG_NOALLOC_SCRATCH_BYTES
 
@@ -121,6 +127,15 @@ def load_library(path: str | None = None):
         lib.seg_scatter.argtypes = [vp, ctypes.c_int, i64, i64, vp, i64, ctypes.c_int, vp, vp, vp]
         lib.seg_reduce_sequential.restype = ctypes.c_int
         lib.seg_reduce_sequential.argtypes = [vp, i64, i64, vp, ctypes.c_int, i64, ctypes.c_int, vp, vp]
+        lib.seg_matmul.restype = ctypes.c_int
+        lib.seg_matmul.argtypes = [vp, ctypes.c_int, i64, i64, i64, vp, i64, i64, i64, i32,
+                                   vp, ctypes.c_int, i64, vp, i64, vp]
+        lib.seg_matmul_grad_w.restype = ctypes.c_int
+        lib.seg_matmul_grad_w.argtypes = [vp, ctypes.c_int, i64, i64, i64, vp, i64, i64, vp, ctypes.c_int, i64,
+                                          vp, ctypes.c_int, vp]
+        lib.seg_lora.restype = ctypes.c_int
+        lib.seg_lora.argtypes = [vp, ctypes.c_int, i64, i64, i64, vp, i64, i64, vp, vp, i64, i64,
+                                 vp, ctypes.c_int, i64, vp, vp, vp, i64, vp]
         if path is None:
             _lib = lib
         return lib
@@ -549,6 +564,199 @@ def flags_to_offsets(flags):
     """``seg_flags_to_offsets`` trimmed to ``count + 1`` entries (synchronises)."""
     offsets, count = seg_flags_to_offsets(flags)
     return offsets[:int(count.item()) + 1]
+
+
+def _product_code(t):
+    torch = _torch()
+    codes = {torch.float32: SEG_F32, torch.float16: SEG_F16, torch.bfloat16: SEG_BF16}
+    if t.dtype not in codes:
+        raise TypeError(f"values must be float32, float16 or bfloat16, not {t.dtype}")
+    return codes[t.dtype]
+
+
+def _check_rows(name, t, offsets):
+    """The row tensor of a product and its offsets; returns the rows' stride."""
+    if not t.is_cuda or not offsets.is_cuda:
+        raise ValueError(f"{name} and offsets must be CUDA tensors (there is no CPU path)")
+    if t.device != offsets.device:
+        raise ValueError(f"{name} and offsets must be on the same device")
+    if t.dim() != 2 or offsets.dim() != 1 or offsets.numel() < 1:
+        raise ValueError(f"{name} must be [R, columns] and offsets [S+1]")
+    if not offsets.is_contiguous():
+        raise ValueError("offsets must be contiguous")
+    return _row_stride(name, t)
+
+
+def _row_stride(name, t):
+    """Elements from one row to the next of a tensor whose rows are contiguous."""
+    rows, cols = t.shape[-2], t.shape[-1]
+    if (cols > 1 and t.stride(-1) != 1) or (rows > 1 and t.stride(-2) < cols):
+        raise ValueError(f"{name} must have contiguous rows that do not overlap")
+    return t.stride(-2) if rows > 1 else max(cols, 1)
+
+
+def _same(name, t, like, shape, dtype=None):
+    dtype = like.dtype if dtype is None else dtype
+    if t.device != like.device:
+        raise ValueError(f"{name} must be on {like.device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
+
+
+def seg_matmul(x, w, offsets, transpose_w: bool = False, out=None, stream=None):
+    """The rows of every segment times the segment's own matrix: for a row r
+    of segment s, ``out[r] = x[r] @ w[s]``; a row in no segment gives 0.
+
+    ``x`` is ``[R, K]`` (float32, float16 or bfloat16, CUDA; rows contiguous,
+    any stride between them), ``w`` ``[S, K, N]``, or ``[S, N, K]`` with
+    ``transpose_w``, ``offsets`` ``[S+1]`` int64 or uint32.  Sums are float32
+    and are rounded once to ``x``'s type.  The gradient of ``x`` is
+    ``seg_matmul(dy, w, offsets, not transpose_w)``, that of ``w``
+    ``seg_matmul_grad_w``.  Not synchronised."""
+    torch = _torch()
+    ldx = _check_rows("x", x, offsets)
+    code, s, k = _product_code(x), offsets.numel() - 1, x.shape[1]
+    if w.dim() != 3:
+        raise ValueError("w must be [S, K, N] (transpose_w: [S, N, K])")
+    n = w.shape[1] if transpose_w else w.shape[2]
+    _same("w", w, x, (s, n, k) if transpose_w else (s, k, n))
+    ldw = _row_stride("w", w)
+    oshape = (x.shape[0], n)
+    if out is None:
+        out = torch.empty(oshape, dtype=x.dtype, device=x.device)
+    else:
+        _same("out", out, x, oshape)
+    ldo = _row_stride("out", out)
+    if stream is None:
+        stream = torch.cuda.current_stream(x.device)
+    with torch.cuda.device(x.device):
+        rc = load_library().seg_matmul(
+            x.data_ptr() or None, code, x.shape[0], k, ldx, w.data_ptr() or None, n, ldw,
+            w.stride(0) if s > 1 else 0, 1 if transpose_w else 0, offsets.data_ptr(), _offset_code(offsets), s,
+            out.data_ptr() or None, ldo, ctypes.c_void_p(stream.cuda_stream))
+    if rc != 0:
+        raise SegReduceError(rc, "seg_matmul")
+    return out
+
+
+def seg_matmul_grad_w(x, dy, offsets, out_dtype=None, out=None, stream=None):
+    """The gradient of ``seg_matmul``'s matrices: ``out[s] = x[rows of s].T @
+    dy[rows of s]``, ``[S, K, N]``; zeros for an empty segment.
+
+    ``x`` is ``[R, K]`` and ``dy`` ``[R, N]`` of one type; ``out_dtype`` is that
+    type (the default) or float32.  For matrices stored ``[S, N, K]`` call it
+    with ``x`` and ``dy`` exchanged.  Not synchronised."""
+    torch = _torch()
+    ldx = _check_rows("x", x, offsets)
+    code, s = _product_code(x), offsets.numel() - 1
+    if dy.dim() != 2:
+        raise ValueError("dy must be [R, N]")
+    k, n = x.shape[1], dy.shape[1]
+    _same("dy", dy, x, (x.shape[0], n))
+    ldy = _row_stride("dy", dy)
+    if out_dtype is None:
+        out_dtype = x.dtype if out is None else out.dtype
+    if out_dtype not in (x.dtype, torch.float32):
+        raise TypeError(f"out_dtype must be {x.dtype} or torch.float32, not {out_dtype}")
+    if out is None:
+        out = torch.empty((s, k, n), dtype=out_dtype, device=x.device)
+    else:
+        _same("out", out, x, (s, k, n), out_dtype)
+        if not out.is_contiguous():
+            raise ValueError("out must be contiguous")
+    if stream is None:
+        stream = torch.cuda.current_stream(x.device)
+    with torch.cuda.device(x.device):
+        rc = load_library().seg_matmul_grad_w(
+            x.data_ptr() or None, code, x.shape[0], k, ldx, dy.data_ptr() or None, n, ldy, offsets.data_ptr(),
+            _offset_code(offsets), s, out.data_ptr() or None, SEG_F32 if out_dtype == torch.float32 else code,
+            ctypes.c_void_p(stream.cuda_stream))
+    if rc != 0:
+        raise SegReduceError(rc, "seg_matmul_grad_w")
+    return out
+
+
+def segment_matmul(x, w, indptr):
+    """Differentiable ``seg_matmul``: ``x`` ``[R, K]``, ``w`` ``[S, K, N]``.
+    Its backward pass is one ``seg_matmul`` (the gradient of ``x``) and one
+    ``seg_matmul_grad_w`` (that of ``w``), each where it is asked for."""
+    return _segment_matmul_function().apply(x, w, indptr)
+
+
+_segment_matmul_fn = None
+
+
+def _segment_matmul_function():
+    global _segment_matmul_fn
+    if _segment_matmul_fn is None:
+        torch = _torch()
+
+        class SegmentMatmul(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, x, w, indptr):
+                ctx.save_for_backward(x, w, indptr)
+                return seg_matmul(x, w, indptr)
+
+            @staticmethod
+            @torch.autograd.function.once_differentiable
+            def backward(ctx, dy):
+                x, w, indptr = ctx.saved_tensors
+                dy = dy.contiguous()   # the gradient of a sum comes with strides of 0
+                dx = seg_matmul(dy, w, indptr, transpose_w=True) if ctx.needs_input_grad[0] else None
+                dw = seg_matmul_grad_w(x, dy, indptr) if ctx.needs_input_grad[1] else None
+                return dx, dw, None
+
+        _segment_matmul_fn = SegmentMatmul
+    return _segment_matmul_fn
+
+
+def seg_lora(x, w, a, b, offsets, adapter, scale=None, out=None, stream=None):
+    """A shared projection with the low-rank adapters of many requests: for a
+    row r of request s that uses adapter ``l = adapter[s]``,
+    ``out[r] = x[r] @ w.T + scale[l] * (x[r] @ a[l].T) @ b[l].T``.
+
+    ``x`` is ``[R, K]``, ``w`` ``[N, K]``, ``a`` ``[L, rank, K]`` and ``b``
+    ``[L, N, rank]`` (contiguous), all of one type (float32, float16 or
+    bfloat16); ``offsets`` ``[S+1]`` delimits the requests' rows, ``adapter``
+    ``[S]`` is int32 and ``scale`` ``[L]`` float32 (default 1).  A request with
+    an adapter outside ``[0, L)`` (-1: none) and a row in no request take the
+    shared product alone.  The whole sum is float32 and is rounded once.  Not
+    synchronised."""
+    torch = _torch()
+    ldx = _check_rows("x", x, offsets)
+    code, s, k = _product_code(x), offsets.numel() - 1, x.shape[1]
+    if w.dim() != 2 or a.dim() != 3 or b.dim() != 3:
+        raise ValueError("w must be [N, K], a [L, rank, K] and b [L, N, rank]")
+    n, count, rank = w.shape[0], a.shape[0], a.shape[1]
+    _same("w", w, x, (n, k))
+    _same("a", a, x, (count, rank, k))
+    _same("b", b, x, (count, n, rank))
+    _same("adapter", adapter, x, (s,), torch.int32)
+    if scale is not None:
+        _same("scale", scale, x, (count,), torch.float32)
+    for name, t in (("a", a), ("b", b), ("adapter", adapter), ("scale", scale)):
+        if t is not None and not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    ldw = _row_stride("w", w)
+    oshape = (x.shape[0], n)
+    if out is None:
+        out = torch.empty(oshape, dtype=x.dtype, device=x.device)
+    else:
+        _same("out", out, x, oshape)
+    ldo = _row_stride("out", out)
+    if stream is None:
+        stream = torch.cuda.current_stream(x.device)
+    with torch.cuda.device(x.device):
+        rc = load_library().seg_lora(
+            x.data_ptr() or None, code, x.shape[0], k, ldx, w.data_ptr() or None, n, ldw, a.data_ptr() or None,
+            b.data_ptr() or None, count, rank, offsets.data_ptr(), _offset_code(offsets), s,
+            adapter.data_ptr() or None, _ptr(scale) or None, out.data_ptr() or None, ldo,
+            ctypes.c_void_p(stream.cuda_stream))
+    if rc != 0:
+        raise SegReduceError(rc, "seg_lora")
+    return out
 
 
 def selftest_wait_timeout(limit_ms: int = 50, stream=None) -> None:

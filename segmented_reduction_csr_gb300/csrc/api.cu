@@ -13,6 +13,7 @@
 #include "../../include/seg_reduce.h"
 #include "seg_pick.cuh"
 #include "seg_plan.cuh"
+#include "seg_product.cuh"
 #include "seg_rle.cuh"
 #include "seg_scan.cuh"
 #include "seg_scatter.cuh"
@@ -60,6 +61,8 @@ std::map<std::pair<int, cudaStream_t>, Scratch> g_scratch;
 // buffer of their own per (device, stream), so that the reduction it runs
 // keeps its scratch (and its ticket words) to itself.
 std::map<std::pair<int, cudaStream_t>, Scratch> g_sort_scratch;
+// The products' scratch: a buffer of their own per (device, stream).
+std::map<std::pair<int, cudaStream_t>, Scratch> g_product_scratch;
 
 seg_status_t device_state(int dev, DeviceState** out) {
     if (dev < 0 || dev >= kMaxDevices) return SEG_ERR_CUDA;
@@ -209,6 +212,27 @@ seg_status_t run_producer(RleParams& p, int64_t n, int64_t* count, cudaStream_t 
         cudaGetLastError();
         return SEG_ERR_CUDA;
     }
+    return SEG_OK;
+}
+
+// Checks that the products share.  Nothing is launched when one fails.
+int64_t product_size(seg_dtype_t dtype) { return dtype == SEG_F32 ? 4 : 2; }
+
+bool bad_product_type(seg_dtype_t dtype) { return dtype != SEG_F32 && dtype != SEG_F16 && dtype != SEG_BF16; }
+
+bool misaligned(const void* ptr, int64_t to) { return reinterpret_cast<uintptr_t>(ptr) % to != 0; }
+
+seg_status_t check_product(seg_dtype_t dtype, int64_t num_rows, int64_t K, int64_t N, int64_t ldx,
+                           const void* x, const void* offsets, seg_offset_dtype_t offsets_dtype, int64_t S) {
+    if (bad_product_type(dtype)) return SEG_ERR_INVALID_ARGUMENT;
+    if (offsets_dtype != SEG_OFF_U32 && offsets_dtype != SEG_OFF_I64) return SEG_ERR_INVALID_ARGUMENT;
+    if (num_rows < 0 || K < 0 || N < 0 || S < 0 || ldx < K) return SEG_ERR_INVALID_ARGUMENT;
+    if (num_rows > INT32_MAX || S > INT32_MAX || K > SEG_MAX_PRODUCT_COLUMNS || N > SEG_MAX_PRODUCT_COLUMNS)
+        return SEG_ERR_UNSUPPORTED;
+    if (num_rows > 0 && K > 0 && !x) return SEG_ERR_INVALID_ARGUMENT;
+    if (S > 0 && !offsets) return SEG_ERR_INVALID_ARGUMENT;
+    if (misaligned(x, product_size(dtype)) || misaligned(offsets, offsets_dtype == SEG_OFF_U32 ? 4 : 8))
+        return SEG_ERR_INVALID_ARGUMENT;
     return SEG_OK;
 }
 
@@ -680,6 +704,137 @@ seg_status_t seg_scan(const void* values, seg_dtype_t dtype, int64_t num_values,
     p.cta_flag = reinterpret_cast<int32_t*>(p.carryi + RS_MAX_CTAS);
     p.bitmap = reinterpret_cast<unsigned long long*>(ws + cta_bytes);
     if (launch_scan(p, stream) != cudaSuccess) {
+        cudaGetLastError();
+        return SEG_ERR_CUDA;
+    }
+    return SEG_OK;
+}
+
+seg_status_t seg_matmul(const void* x, seg_dtype_t dtype, int64_t num_rows, int64_t K, int64_t ldx,
+                        const void* w, int64_t N, int64_t ldw, int64_t stride_w, int32_t transpose_w,
+                        const void* offsets, seg_offset_dtype_t offsets_dtype, int64_t num_segments,
+                        void* out, int64_t ldo, seg_stream_t stream) {
+    const seg_status_t st = check_product(dtype, num_rows, K, N, ldx, x, offsets, offsets_dtype, num_segments);
+    if (st != SEG_OK) return st;
+    const int64_t wrows = transpose_w ? N : K, wcols = transpose_w ? K : N;
+    if ((transpose_w != 0 && transpose_w != 1) || ldo < N || ldw < wcols || stride_w < 0) return SEG_ERR_INVALID_ARGUMENT;
+    if (num_segments > 1 && wrows > 0 && stride_w < (wrows - 1) * ldw + wcols) return SEG_ERR_INVALID_ARGUMENT;
+    if (num_rows == 0 || N == 0) return SEG_OK;
+    if (!out || (num_segments > 0 && K > 0 && !w)) return SEG_ERR_INVALID_ARGUMENT;
+    if (misaligned(w, product_size(dtype)) || misaligned(out, product_size(dtype))) return SEG_ERR_INVALID_ARGUMENT;
+    ProductParams p{};
+    p.x = x;
+    p.w = w;
+    p.offsets = offsets;
+    p.out = out;
+    p.R = num_rows;
+    p.K = K;
+    p.N = N;
+    p.S = num_segments;
+    p.ldx = ldx;
+    p.ldw = ldw;
+    p.stride_w = stride_w;
+    p.ldo = ldo;
+    p.off64 = offsets_dtype == SEG_OFF_I64 ? 1 : 0;
+    p.trans = transpose_w;
+    p.type = p.out_type = dtype;
+    if (launch_product(p, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) {
+        cudaGetLastError();
+        return SEG_ERR_CUDA;
+    }
+    return SEG_OK;
+}
+
+seg_status_t seg_matmul_grad_w(const void* x, seg_dtype_t dtype, int64_t num_rows, int64_t K, int64_t ldx,
+                               const void* dy, int64_t N, int64_t ldy, const void* offsets,
+                               seg_offset_dtype_t offsets_dtype, int64_t num_segments, void* out,
+                               seg_dtype_t out_dtype, seg_stream_t stream) {
+    const seg_status_t st = check_product(dtype, num_rows, K, N, ldx, x, offsets, offsets_dtype, num_segments);
+    if (st != SEG_OK) return st;
+    if ((out_dtype != dtype && out_dtype != SEG_F32) || ldy < N) return SEG_ERR_INVALID_ARGUMENT;
+    if (num_segments == 0 || K == 0 || N == 0) return SEG_OK;
+    if (!out || (num_rows > 0 && !dy)) return SEG_ERR_INVALID_ARGUMENT;
+    if (misaligned(dy, product_size(dtype)) || misaligned(out, product_size(out_dtype))) return SEG_ERR_INVALID_ARGUMENT;
+    ProductParams p{};
+    p.x = x;
+    p.w = dy;
+    p.offsets = offsets;
+    p.out = out;
+    p.R = num_rows;
+    p.K = K;
+    p.N = N;
+    p.S = num_segments;
+    p.ldx = ldx;
+    p.ldw = ldy;
+    p.off64 = offsets_dtype == SEG_OFF_I64 ? 1 : 0;
+    p.type = dtype;
+    p.out_type = out_dtype;
+    if (launch_product_grad(p, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) {
+        cudaGetLastError();
+        return SEG_ERR_CUDA;
+    }
+    return SEG_OK;
+}
+
+seg_status_t seg_lora(const void* x, seg_dtype_t dtype, int64_t num_rows, int64_t K, int64_t ldx,
+                      const void* w, int64_t N, int64_t ldw, const void* a, const void* b,
+                      int64_t num_adapters, int64_t rank, const void* offsets,
+                      seg_offset_dtype_t offsets_dtype, int64_t num_segments, const int32_t* adapter,
+                      const float* scale, void* out, int64_t ldo, seg_stream_t stream_) {
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    seg_status_t st = check_product(dtype, num_rows, K, N, ldx, x, offsets, offsets_dtype, num_segments);
+    if (st != SEG_OK) return st;
+    if (ldw < K || ldo < N || num_adapters < 0 || rank < 1) return SEG_ERR_INVALID_ARGUMENT;
+    if (rank > SEG_MAX_RANK || num_adapters > INT32_MAX) return SEG_ERR_UNSUPPORTED;
+    if (num_rows == 0 || N == 0) return SEG_OK;
+    if (!out || (K > 0 && !w)) return SEG_ERR_INVALID_ARGUMENT;
+    if (num_segments > 0 && !adapter) return SEG_ERR_INVALID_ARGUMENT;
+    if (num_adapters > 0 && (!b || (K > 0 && !a))) return SEG_ERR_INVALID_ARGUMENT;
+    const int64_t size = product_size(dtype);
+    if (misaligned(w, size) || misaligned(a, size) || misaligned(b, size) || misaligned(out, size) ||
+        misaligned(adapter, 4) || misaligned(scale, 4))
+        return SEG_ERR_INVALID_ARGUMENT;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return SEG_ERR_CUDA;
+    std::lock_guard<std::mutex> lock(g_mu);
+    Scratch* sc = nullptr;
+    st = scratch_in(g_product_scratch, dev, stream, static_cast<size_t>(num_rows * rank * 4), &sc);
+    if (st != SEG_OK) return st;
+    // u = scale * x a^T, in float32
+    ProductParams p{};
+    p.x = x;
+    p.w = a;
+    p.offsets = offsets;
+    p.index = adapter;
+    p.scale = scale;
+    p.out = sc->ptr;
+    p.R = num_rows;
+    p.K = K;
+    p.N = rank;
+    p.S = num_segments;
+    p.ldx = ldx;
+    p.ldw = K;
+    p.stride_w = rank * K;
+    p.ldo = rank;
+    p.L = num_adapters;
+    p.off64 = offsets_dtype == SEG_OFF_I64 ? 1 : 0;
+    p.trans = 1;
+    p.type = dtype;
+    p.out_type = SEG_F32;
+    cudaError_t e = launch_product(p, stream);
+    if (e == cudaSuccess) {
+        p.w = w;
+        p.out = out;
+        p.N = N;
+        p.ldw = ldw;
+        p.ldo = ldo;
+        p.out_type = dtype;
+        p.u = static_cast<const float*>(sc->ptr);
+        p.b = b;
+        p.rank = rank;
+        e = launch_lora(p, stream);
+    }
+    if (e != cudaSuccess) {
         cudaGetLastError();
         return SEG_ERR_CUDA;
     }
