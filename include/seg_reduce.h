@@ -418,7 +418,7 @@ seg_status_t seg_flags_to_offsets(const uint8_t *flags, int64_t n, int64_t *offs
  *   w             device, num_segments matrices stride_w elements apart, each
  *                 [K, N] (transpose_w: [N, K]) with rows ldw elements apart.
  *   offsets, offsets_dtype, num_segments: as for seg_reduce (clamped to
- *                 [0, num_rows] on the device); at most 2^31 - 1 segments.
+ *                 [0, num_rows] on the device); at most 2^30 segments.
  *   out           device, [num_rows, N], rows ldo elements apart (ldo >= N).
  *
  * Every pointer is aligned to its element; 16-byte aligned x and w whose row

@@ -227,13 +227,40 @@ seg_status_t check_product(seg_dtype_t dtype, int64_t num_rows, int64_t K, int64
     if (bad_product_type(dtype)) return SEG_ERR_INVALID_ARGUMENT;
     if (offsets_dtype != SEG_OFF_U32 && offsets_dtype != SEG_OFF_I64) return SEG_ERR_INVALID_ARGUMENT;
     if (num_rows < 0 || K < 0 || N < 0 || S < 0 || ldx < K) return SEG_ERR_INVALID_ARGUMENT;
-    if (num_rows > INT32_MAX || S > INT32_MAX || K > SEG_MAX_PRODUCT_COLUMNS || N > SEG_MAX_PRODUCT_COLUMNS)
+    if (num_rows > INT32_MAX || S > (int64_t(1) << 30) || K > SEG_MAX_PRODUCT_COLUMNS || N > SEG_MAX_PRODUCT_COLUMNS)
         return SEG_ERR_UNSUPPORTED;
     if (num_rows > 0 && K > 0 && !x) return SEG_ERR_INVALID_ARGUMENT;
     if (S > 0 && !offsets) return SEG_ERR_INVALID_ARGUMENT;
     if (misaligned(x, product_size(dtype)) || misaligned(offsets, offsets_dtype == SEG_OFF_U32 ? 4 : 8))
         return SEG_ERR_INVALID_ARGUMENT;
     return SEG_OK;
+}
+
+// Enqueues one product on scratch that is large enough.  The ticket words at the scratch's start are
+// written by products alone, each with a new generation.
+seg_status_t run_product(int mode, ProductParams p, cudaStream_t stream, Scratch* sc, DeviceState* ds) {
+    p.sms = ds->sm_count;
+    p.status = ds->status;
+    p.ws = static_cast<unsigned char*>(sc->ptr);
+    p.gen = ++sc->gen;
+    if (launch_product(mode, p, plan_product(mode, p), stream) != cudaSuccess) {
+        cudaGetLastError();
+        return SEG_ERR_CUDA;
+    }
+    return SEG_OK;
+}
+
+seg_status_t run_product(int mode, ProductParams p, cudaStream_t stream) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return SEG_ERR_CUDA;
+    std::lock_guard<std::mutex> lock(g_mu);
+    DeviceState* ds = nullptr;
+    seg_status_t st = device_state(dev, &ds);
+    if (st != SEG_OK) return st;
+    p.sms = ds->sm_count;
+    Scratch* sc = nullptr;
+    st = scratch_in(g_product_scratch, dev, stream, static_cast<size_t>(plan_product(mode, p).bytes()), &sc);
+    return st != SEG_OK ? st : run_product(mode, p, stream, sc, ds);
 }
 
 }  // namespace
@@ -738,11 +765,7 @@ seg_status_t seg_matmul(const void* x, seg_dtype_t dtype, int64_t num_rows, int6
     p.off64 = offsets_dtype == SEG_OFF_I64 ? 1 : 0;
     p.trans = transpose_w;
     p.type = p.out_type = dtype;
-    if (launch_product(p, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) {
-        cudaGetLastError();
-        return SEG_ERR_CUDA;
-    }
-    return SEG_OK;
+    return run_product(PRODUCT_FORWARD, p, reinterpret_cast<cudaStream_t>(stream));
 }
 
 seg_status_t seg_matmul_grad_w(const void* x, seg_dtype_t dtype, int64_t num_rows, int64_t K, int64_t ldx,
@@ -769,11 +792,7 @@ seg_status_t seg_matmul_grad_w(const void* x, seg_dtype_t dtype, int64_t num_row
     p.off64 = offsets_dtype == SEG_OFF_I64 ? 1 : 0;
     p.type = dtype;
     p.out_type = out_dtype;
-    if (launch_product_grad(p, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) {
-        cudaGetLastError();
-        return SEG_ERR_CUDA;
-    }
-    return SEG_OK;
+    return run_product(PRODUCT_WEIGHTS, p, reinterpret_cast<cudaStream_t>(stream));
 }
 
 seg_status_t seg_lora(const void* x, seg_dtype_t dtype, int64_t num_rows, int64_t K, int64_t ldx,
@@ -797,48 +816,55 @@ seg_status_t seg_lora(const void* x, seg_dtype_t dtype, int64_t num_rows, int64_
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return SEG_ERR_CUDA;
     std::lock_guard<std::mutex> lock(g_mu);
-    Scratch* sc = nullptr;
-    st = scratch_in(g_product_scratch, dev, stream, static_cast<size_t>(num_rows * rank * 4), &sc);
+    DeviceState* ds = nullptr;
+    st = device_state(dev, &ds);
     if (st != SEG_OK) return st;
-    // u = scale * x a^T, in float32
-    ProductParams p{};
-    p.x = x;
-    p.w = a;
-    p.offsets = offsets;
-    p.index = adapter;
-    p.scale = scale;
-    p.out = sc->ptr;
-    p.R = num_rows;
-    p.K = K;
-    p.N = rank;
-    p.S = num_segments;
-    p.ldx = ldx;
-    p.ldw = K;
-    p.stride_w = rank * K;
-    p.ldo = rank;
-    p.L = num_adapters;
-    p.off64 = offsets_dtype == SEG_OFF_I64 ? 1 : 0;
-    p.trans = 1;
-    p.type = dtype;
-    p.out_type = SEG_F32;
-    cudaError_t e = launch_product(p, stream);
-    if (e == cudaSuccess) {
-        p.w = w;
-        p.out = out;
-        p.N = N;
-        p.ldw = ldw;
-        p.ldo = ldo;
-        p.out_type = dtype;
-        p.u = static_cast<const float*>(sc->ptr);
-        p.b = b;
-        p.rank = rank;
-        e = launch_lora(p, stream);
+    // the products with a, scaled, in float32: u = scale * x a^T
+    ProductParams pa{};
+    pa.x = x;
+    pa.w = a;
+    pa.offsets = offsets;
+    pa.index = adapter;
+    pa.scale = scale;
+    pa.R = num_rows;
+    pa.K = K;
+    pa.N = rank;
+    pa.S = num_segments;
+    pa.ldx = ldx;
+    pa.ldw = K;
+    pa.stride_w = rank * K;
+    pa.ldo = rank;
+    pa.L = num_adapters;
+    pa.off64 = offsets_dtype == SEG_OFF_I64 ? 1 : 0;
+    pa.trans = 1;
+    pa.type = dtype;
+    pa.out_type = SEG_F32;
+    pa.sms = ds->sm_count;
+    // the shared product, to which the low-rank part is added
+    ProductParams p = pa;
+    p.w = w;
+    p.scale = nullptr;
+    p.out = out;
+    p.N = N;
+    p.ldw = ldw;
+    p.stride_w = 0;
+    p.ldo = ldo;
+    p.out_type = dtype;
+    p.b = b;
+    p.rank = rank;
+    const bool low = num_segments > 0 && num_adapters > 0;
+    const int64_t own = std::max(low ? plan_product(PRODUCT_FORWARD, pa).bytes() : 0, plan_product(PRODUCT_ADAPTERS, p).bytes());
+    Scratch* sc = nullptr;
+    st = scratch_in(g_product_scratch, dev, stream, static_cast<size_t>(own + num_rows * rank * 4), &sc);
+    if (st != SEG_OK) return st;
+    float* u = reinterpret_cast<float*>(static_cast<unsigned char*>(sc->ptr) + own);
+    if (low) {
+        pa.out = u;
+        st = run_product(PRODUCT_FORWARD, pa, stream, sc, ds);
+        if (st != SEG_OK) return st;
     }
-    if (e != cudaSuccess) {
-        cudaGetLastError();
-        return SEG_ERR_CUDA;
-    }
-    return SEG_OK;
+    p.u = u;
+    return run_product(PRODUCT_ADAPTERS, p, stream, sc, ds);
 }
 
 seg_status_t seg_selftest_wait_timeout(uint32_t limit_ms, seg_stream_t stream_) {

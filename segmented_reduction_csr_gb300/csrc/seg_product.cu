@@ -1,182 +1,911 @@
-// seg_product.cu -- products over the rows of segments (see seg_product.cuh).
+// seg_product.cu -- products over the rows of segments (see seg_product.cuh)
+// on the tensor cores (tcgen05, accumulators in tensor memory).
+//
+// One kernel shape serves all three products.  A tile is D[m, n] with m (128
+// lanes of tensor memory) along the output's contiguous dimension and n (its
+// columns, up to NT) along the other one:
+//   forward, adapters  m: output columns, n: rows of one segment, sum over K;
+//   weights            m: columns of dy,  n: columns of x,        sum over rows.
+// With the rows of a segment on n, whose extent an MMA takes in steps of 16,
+// a ragged tail or a single row costs 16 columns, not a whole 128-row tile;
+// and a warp's 32 lanes are 32 neighbouring output columns, so results leave
+// the registers coalesced whatever the alignment.
+//
+// Roles per CTA (persistent, one CTA per SM, tiles dealt round robin):
+//   a producer fills a ring of shared-memory stages (64 steps of the sum
+//   each, 128-byte swizzled rows): one thread that issues tensor copies, or,
+//   for float32 and for strides that tensor copies cannot take, eight loader
+//   warps; one thread issues the MMAs; four warps drain one of two
+//   accumulators while the other fills.
+// float32: the loader splits every value into three bfloat16 parts by
+// truncation (8 + 8 + 8 bits, exact) and six of the nine part products are
+// accumulated; the other three are below 2^-21 of the whole.
+// The tensor cores cut what an addition shifts out of the accumulator (a bias
+// of about 2^-26 of it per 16 steps, measured), so for float32 the five small
+// part products have an accumulator of their own, and where the result is
+// float32 the accumulators are added to it, rounded, every 512 (float32) or
+// 768 (16-bit operands) steps: the bias then stays below 1e-6.
+// Long sums with few tiles are cut into parts that leave float32 partials in
+// scratch, added in order.  Forward: each part takes a ticket and the last
+// one to finish adds them (no CTA waits for another); weights, whose segments
+// can have hundreds of parts: a second kernel adds them.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <algorithm>
+
+#include "seg_common.cuh"
 #include "seg_product.cuh"
+#include "tc.cuh"
 
 namespace segred {
 namespace {
 
-constexpr int PT = 64;    // output tile side
-constexpr int PK = 16;    // contraction step
+constexpr int KB = 64;                    // steps of the sum per stage: 128-byte rows of 16-bit values
+constexpr int MT = 128;                   // lanes of a tile
+constexpr int NEAR_SEGMENTS = 1024;       // up to here every CTA keeps the offsets in shared memory
+constexpr int EPI_WARP = 4;               // warps 4..7 drain (their index mod 4 names their lanes)
+constexpr int LOAD_WARP = 8, LOAD_WARPS = 8;
+constexpr int NEVER_FLUSH = 1 << 28;         // more blocks than any sum has
+constexpr unsigned STATUS_PRODUCT_TIMEOUT = 8u;
 
-__device__ __forceinline__ float to_f(float v) { return v; }
-__device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
-__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
-template <class T> __device__ __forceinline__ T from_f(float v);
-template <> __device__ __forceinline__ float from_f<float>(float v) { return v; }
-template <> __device__ __forceinline__ __half from_f<__half>(float v) { return __float2half_rn(v); }
-template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+// Stage ring of a kernel shape: PL 16-bit planes per operand.
+template <int NT, int PL>
+struct Ring {
+    static constexpr int A_PLANE = MT * 128, B_PLANE = NT * 128;
+    static constexpr int STAGE = PL * (A_PLANE + B_PLANE);
+    static constexpr int STAGES = std::min(8, 221184 / STAGE);
+    static constexpr int ACC = PL == 1 ? NT : 2 * NT;            // tensor-memory columns of one accumulator
+    static constexpr int BARS = 2 * STAGES + 5;
+    static constexpr int FIXED = 2 * (NEAR_SEGMENTS + 1) * 4 + BARS * 8 + 64 + NT * 4;
+    static constexpr int SMEM = STAGES * STAGE + FIXED + 1024;   // 1024: alignment of the stages
+    static_assert(SMEM <= 232448, "shared memory of an SM");
+};
 
-__device__ __forceinline__ int64_t offset_at(const ProductParams& p, int64_t s) {
-    int64_t o = p.off64 ? __ldg(static_cast<const int64_t*>(p.offsets) + s)
-                        : static_cast<int64_t>(__ldg(static_cast<const uint32_t*>(p.offsets) + s));
-    o = o < 0 ? 0 : o;
-    return o > p.R ? p.R : o;
+struct KernelArgs {
+    ProductParams p;
+    int32_t mtiles, ntiles, parts, part_blocks, kblocks;
+    int32_t flush;      // blocks of the sum after which the accumulators go to the result
+    int64_t chunk, row_tiles, cols_m, cols_n;   // cols_*: extent of the tile dimensions (forward: cols_n unused)
+    unsigned long long* tickets;
+    int* far;          // offsets and tile prefix of more than NEAR_SEGMENTS segments
+    float* partials;
+};
+
+__device__ __forceinline__ int offset_at(const ProductParams& p, int64_t s) {
+    const int64_t o = p.off64 ? __ldg(static_cast<const int64_t*>(p.offsets) + s)
+                              : static_cast<int64_t>(__ldg(static_cast<const uint32_t*>(p.offsets) + s));
+    return static_cast<int>(clamp_off(o, p.R));
 }
 
-// acc[i][j] += sum_k A(m0 + 4 ty + i, k) * B(k, n0 + 4 tx + j) for k < kn
-template <class FA, class FB>
-__device__ __forceinline__ void tile_product(FA fa, FB fb, int64_t kn, float (&acc)[4][4]) {
-    __shared__ float as[PK][PT + 4], bs[PK][PT + 4];
-    const int t = threadIdx.x, tx = t % 16, ty = t / 16;
-    for (int64_t k0 = 0; k0 < kn; k0 += PK) {
-        for (int i = t; i < PK * PT; i += 256) {
-            as[i / PT][i % PT] = k0 + i / PT < kn ? fa(i % PT, k0 + i / PT) : 0.0f;
-            bs[i / PT][i % PT] = k0 + i / PT < kn ? fb(i % PT, k0 + i / PT) : 0.0f;
+// Tiles of rows (forward) or parts of the rows (weights) of segment s.
+template <int MODE, int NT>
+__device__ __forceinline__ int segment_items(const KernelArgs& a, int64_t s, int b, int e) {
+    const int len = e > b ? e - b : 0;
+    if (MODE == PRODUCT_WEIGHTS) return len == 0 ? 1 : static_cast<int>((len + a.chunk - 1) / a.chunk);
+    if (a.p.index) {
+        const int l = __ldg(a.p.index + s);
+        if (l < 0 || l >= a.p.L) return 0;
+    }
+    return (len + NT - 1) / NT;
+}
+
+// beg[s] = offset s, pre[s] = items of the segments before s (s = 0 .. S), by all threads of the CTA.
+template <int MODE, int NT>
+__device__ void fill_prefix(const KernelArgs& a, int* beg, int* pre) {
+    __shared__ int64_t warp_sum[32];
+    __shared__ int64_t carry;
+    const int t = threadIdx.x, nth = blockDim.x, lane = t & 31, warp = t >> 5;
+    const int64_t S = a.p.S;
+    if (t == 0) carry = 0;
+    for (int64_t s = t; s <= S; s += nth) beg[s] = offset_at(a.p, s);
+    __syncthreads();
+    for (int64_t s0 = 0; s0 < S; s0 += nth) {
+        const int64_t s = s0 + t;
+        const int v = s < S ? segment_items<MODE, NT>(a, s, beg[s], beg[s + 1]) : 0;
+        int64_t x = v;   // 64 bits: offsets that go back and forth add up to more than the rows
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
+            if (lane >= d) x += y;
         }
+        if (lane == 31) warp_sum[warp] = x;
         __syncthreads();
-        for (int k = 0; k < PK; ++k)
-            for (int i = 0; i < 4; ++i)
-                for (int j = 0; j < 4; ++j) acc[i][j] += as[k][4 * ty + i] * bs[k][4 * tx + j];
+        int64_t before = carry;
+        for (int w = 0; w < warp; ++w) before += warp_sum[w];
+        if (s < S) pre[s] = static_cast<int>(min(before + x - v, int64_t(INT_MAX)));
         __syncthreads();
+        if (t == nth - 1) carry = before + x;
+        __syncthreads();
+    }
+    if (t == 0) pre[S] = static_cast<int>(min(carry, int64_t(INT_MAX)));
+    __syncthreads();
+}
+
+// The offsets and prefix of many segments, once per call.
+template <int MODE, int NT>
+__global__ void __launch_bounds__(1024) prefix_kernel(const __grid_constant__ KernelArgs a) {
+    fill_prefix<MODE, NT>(a, a.far, a.far + a.p.S + 1);
+}
+
+struct Item {
+    int seg;
+    int row0, rows;     // forward: the tile's rows; weights: the rows it sums over
+    int m0, n0;
+    int kb0, kb1;       // 64-wide blocks of the sum
+    int part, parts;
+    int64_t slot, ticket;
+};
+
+template <int MODE, int NT>
+__device__ __forceinline__ Item item_at(const KernelArgs& a, const int* beg, const int* pre, int64_t i) {
+    Item t;
+    int q;
+    if (MODE == PRODUCT_WEIGHTS) {
+        const int per = a.mtiles * a.ntiles;
+        q = static_cast<int>(i / per);
+        const int r = static_cast<int>(i - int64_t(q) * per);
+        t.m0 = r % a.mtiles * MT;
+        t.n0 = r / a.mtiles * NT;
+    } else {
+        const int64_t tile = i / a.parts;
+        t.part = static_cast<int>(i - tile * a.parts);
+        q = static_cast<int>(tile / a.mtiles);
+        t.m0 = static_cast<int>(tile - int64_t(q) * a.mtiles) * MT;
+        t.n0 = 0;
+    }
+    int b = 0, e = static_cast<int>(a.p.R), first = 0, count;
+    if (MODE == PRODUCT_ADAPTERS) {
+        t.seg = 0;
+        count = static_cast<int>(a.row_tiles);
+    } else {
+        int lo = 0, hi = static_cast<int>(a.p.S);   // the last segment whose items start at or before q
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (pre[mid] <= q) lo = mid; else hi = mid;
+        }
+        t.seg = lo;
+        b = beg[lo];
+        e = beg[lo + 1];
+        first = pre[lo];
+        count = pre[lo + 1] - first;
+    }
+    const int len = e > b ? e - b : 0, j = q - first;
+    if (MODE == PRODUCT_WEIGHTS) {
+        const int64_t at = j * a.chunk;
+        t.row0 = static_cast<int>(b + at);
+        t.rows = static_cast<int>(len - at < a.chunk ? len - at : a.chunk);
+        t.kb0 = 0;
+        t.kb1 = (t.rows + KB - 1) / KB;
+        t.part = j;
+        t.parts = count;
+        // parts of one split segment start `chunk` rows apart, and a block of
+        // `chunk` rows holds the starts of at most two split segments' parts,
+        // one of them a first part: so these numbers are each used once
+        const int per = a.mtiles * a.ntiles, r = t.m0 / MT + t.n0 / NT * a.mtiles;
+        t.slot = (2 * (t.row0 / a.chunk) + (j == 0 ? 1 : 0)) * per + r;
+        t.ticket = 0;
+    } else {
+        // the segment's rows in equal tiles of a multiple of 16
+        int each = ((len + count - 1) / count + 15) & ~15;
+        each = each < NT ? each : NT;
+        t.row0 = b + j * each;
+        t.rows = len - j * each < each ? len - j * each : each;
+        t.kb0 = t.part * a.part_blocks;
+        t.kb1 = min(t.kb0 + a.part_blocks, a.kblocks);
+        t.parts = a.parts;
+        t.slot = i;
+        t.ticket = i / a.parts;
+    }
+    return t;
+}
+
+__device__ __forceinline__ void bar_drain() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// The same, and whether `ok` holds in all four warps: they give up together or not at all.
+__device__ __forceinline__ bool bar_drain_all(bool ok) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.and.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(ok ? 1u : 0u)
+        : "memory");
+    return r != 0;
+}
+// A wait of a whole warp.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, unsigned int* status) {
+    return __all_sync(0xffffffffu, wait_bounded(bar, parity, status, STATUS_PRODUCT_TIMEOUT));
+}
+
+__device__ __forceinline__ float value_at(const void* base, int64_t i, int type) {
+    if (type == PT_F32) return __ldg(static_cast<const float*>(base) + i);
+    if (type == PT_F16) return __half2float(static_cast<const __half*>(base)[i]);
+    return __bfloat162float(static_cast<const __nv_bfloat16*>(base)[i]);
+}
+
+// Stores one tile column group: value i to row `at + i * step` of `out` for i < n.
+__device__ __forceinline__ void store_rows(void* out, int type, int64_t at, int64_t step, const float (&v)[32], int n) {
+    if (type == PT_F32) {
+        float* o = static_cast<float*>(out) + at;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (i < n) o[i * step] = v[i];
+    } else if (type == PT_F16) {
+        __half* o = static_cast<__half*>(out) + at;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (i < n) o[i * step] = __float2half_rn(v[i]);
+    } else {
+        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(out) + at;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (i < n) o[i * step] = __float2bfloat16_rn(v[i]);
     }
 }
 
-// One CTA per (64 columns of the output, segment); row S is the rows in no segment.
-template <class T, class TO>
-__global__ void __launch_bounds__(256) forward_kernel(ProductParams p) {
-    const int64_t n0 = int64_t(blockIdx.x) * PT;
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    const T* x = static_cast<const T*>(p.x);
-    TO* out = static_cast<TO*>(p.out);
-    for (int64_t s = blockIdx.y; s <= p.S; s += gridDim.y) {
-        if (s == p.S) {
-            const int64_t b = p.S > 0 ? offset_at(p, 0) : 0, e = p.S > 0 ? offset_at(p, p.S) : 0;
-            for (int64_t i = threadIdx.x; i < p.R * PT; i += 256) {
-                const int64_t r = i / PT, n = n0 + i % PT;
-                if ((r < b || r >= e) && n < p.N) out[r * p.ldo + n] = from_f<TO>(0.0f);
-            }
-            continue;
-        }
-        const int64_t b = offset_at(p, s), e = offset_at(p, s + 1);
-        const int64_t m = p.index ? __ldg(p.index + s) : s;
-        const bool have = !p.index || (m >= 0 && m < p.L);
-        const T* w = static_cast<const T*>(p.w) + (have ? m : 0) * p.stride_w;
-        const float sc = have && p.scale ? __ldg(p.scale + m) : 1.0f;
-        for (int64_t r0 = b; r0 < e; r0 += PT) {
-            float acc[4][4] = {};
-            tile_product([&](int i, int64_t k) { return r0 + i < e ? to_f(x[(r0 + i) * p.ldx + k]) : 0.0f; },
-                         [&](int j, int64_t k) {
-                             return n0 + j < p.N ? to_f(p.trans ? w[(n0 + j) * p.ldw + k] : w[k * p.ldw + n0 + j]) : 0.0f;
-                         },
-                         have ? p.K : 0, acc);
-            for (int i = 0; i < 4; ++i)
-                for (int j = 0; j < 4; ++j) {
-                    const int64_t r = r0 + 4 * ty + i, n = n0 + 4 * tx + j;
-                    if (r < e && n < p.N) out[r * p.ldo + n] = from_f<TO>(acc[i][j] * sc);
+// What is left to do to finished sums: the scale of an indexed matrix, or the
+// adapters' low-rank part.  v[j] is row c + j of the tile, column m.
+template <int MODE>
+__device__ __forceinline__ void finish(const ProductParams& p, float (&v)[32], int c, int rows, const Item& t,
+                                       const int* tile_adapter, int64_t m, float factor) {
+    if constexpr (MODE == PRODUCT_FORWARD) {
+        if (p.scale)
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] *= factor;
+    }
+    if constexpr (MODE == PRODUCT_ADAPTERS) {
+        for (int q = 0; q < p.rank; q += 8) {
+            const int width = static_cast<int>(p.rank - q < 8 ? p.rank - q : 8);
+            float bv[8];
+            int have = -1;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+                const int l = c + j < rows ? tile_adapter[c + j] : -1;
+                if (l < 0) continue;
+                if (l != have) {
+                    have = l;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        bv[k] = k < width ? value_at(p.b, (int64_t(l) * p.N + m) * p.rank + q + k, p.type) : 0.0f;
                 }
+                const float* u = p.u + (int64_t(t.row0) + c + j) * p.rank + q;
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (k < width) v[j] += __ldg(u + k) * bv[k];
+            }
         }
     }
 }
 
-// One CTA per (64 x 64 tile of dw, segment).
-template <class T, class TO>
-__global__ void __launch_bounds__(256) grad_kernel(ProductParams p) {
-    const int64_t n0 = int64_t(blockIdx.x) * PT, k0 = int64_t(blockIdx.y) * PT;
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    const T* x = static_cast<const T*>(p.x);
-    const T* dy = static_cast<const T*>(p.w);
-    for (int64_t s = blockIdx.z; s < p.S; s += gridDim.z) {
-        const int64_t b = offset_at(p, s), e = offset_at(p, s + 1);
-        float acc[4][4] = {};
-        tile_product([&](int i, int64_t r) { return k0 + i < p.K ? to_f(x[(b + r) * p.ldx + k0 + i]) : 0.0f; },
-                     [&](int j, int64_t r) { return n0 + j < p.N ? to_f(dy[(b + r) * p.ldw + n0 + j]) : 0.0f; },
-                     e > b ? e - b : 0, acc);
-        TO* out = static_cast<TO*>(p.out) + s * p.K * p.N;
-        for (int i = 0; i < 4; ++i)
-            for (int j = 0; j < 4; ++j) {
-                const int64_t k = k0 + 4 * ty + i, n = n0 + 4 * tx + j;
-                if (k < p.K && n < p.N) out[k * p.N + n] = from_f<TO>(acc[i][j]);
+// ---------------------------------------------------------------------------
+// The loader warps: boxes of `rows` x 64 values of a row-major matrix into
+// 128-byte swizzled rows, zero outside [.., row_end) x [.., col_end).
+
+struct Box {
+    const void* base;
+    int64_t ld;
+    int64_t row0, row_end;
+    int64_t col0, col_end;
+};
+
+__device__ __forceinline__ uint32_t swizzled(int row, int unit) {
+    return static_cast<uint32_t>(row * 128 + ((unit ^ (row & 7)) << 4));
+}
+
+// One unit: 8 values of one row, as PL planes of 16 bytes each.
+template <int PL>
+__device__ __forceinline__ void load_unit(const Box& x, int row, int unit, uint4 (&v)[PL]) {
+    const int64_t r = x.row0 + row, c = x.col0 + unit * 8;
+#pragma unroll
+    for (int i = 0; i < PL; ++i) v[i] = make_uint4(0, 0, 0, 0);
+    if (r >= x.row_end || c >= x.col_end) return;
+    if constexpr (PL == 1) {
+        const uint16_t* src = static_cast<const uint16_t*>(x.base) + r * x.ld + c;
+        if (c + 8 <= x.col_end && (reinterpret_cast<uintptr_t>(src) & 15) == 0) {
+            v[0] = __ldg(reinterpret_cast<const uint4*>(src));
+        } else {
+            uint32_t h[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) h[i] = c + i < x.col_end ? __ldg(src + i) : 0;
+            v[0] = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+        }
+    } else {
+        const float* src = static_cast<const float*>(x.base) + r * x.ld + c;
+        float f[8];
+        if (c + 8 <= x.col_end && (reinterpret_cast<uintptr_t>(src) & 15) == 0) {
+            const float4 a = __ldg(reinterpret_cast<const float4*>(src)), b = __ldg(reinterpret_cast<const float4*>(src) + 1);
+            f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = c + i < x.col_end ? __ldg(src + i) : 0.0f;
+        }
+        uint32_t part[PL][8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+#pragma unroll
+            for (int k = 0; k < PL; ++k) {
+                part[k][i] = __float_as_uint(f[i]) >> 16;          // truncation: the rest is exact
+                f[i] -= __uint_as_float(part[k][i] << 16);
             }
+        }
+#pragma unroll
+        for (int k = 0; k < PL; ++k)
+            v[k] = make_uint4(part[k][0] | part[k][1] << 16, part[k][2] | part[k][3] << 16,
+                              part[k][4] | part[k][5] << 16, part[k][6] | part[k][7] << 16);
     }
 }
 
-// The shared product and the low-rank part: one CTA per 64 x 64 tile of the output.
-template <class T>
-__global__ void __launch_bounds__(256) lora_kernel(ProductParams p) {
-    const int64_t n0 = int64_t(blockIdx.x) * PT;
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    const T* x = static_cast<const T*>(p.x);
-    const T* w = static_cast<const T*>(p.w);
-    T* out = static_cast<T*>(p.out);
-    for (int64_t r0 = int64_t(blockIdx.y) * PT; r0 < p.R; r0 += int64_t(gridDim.y) * PT) {
-        float acc[4][4] = {};
-        tile_product([&](int i, int64_t k) { return r0 + i < p.R ? to_f(x[(r0 + i) * p.ldx + k]) : 0.0f; },
-                     [&](int j, int64_t k) { return n0 + j < p.N ? to_f(w[(n0 + j) * p.ldw + k]) : 0.0f; }, p.K, acc);
+// `units` (8 per row) of a box into `dst`, planes `plane` bytes apart, by the loader's 256 threads.
+template <int PL>
+__device__ __forceinline__ void load_box(const Box& x, int units, unsigned char* dst, int plane) {
+    constexpr int AHEAD = 4;
+    const int t = threadIdx.x - LOAD_WARP * 32;
+    for (int u0 = t; u0 < units; u0 += AHEAD * LOAD_WARPS * 32) {
+        uint4 v[AHEAD][PL];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const int u = u0 + i * LOAD_WARPS * 32;
+            if (u < units) load_unit<PL>(x, u >> 3, u & 7, v[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const int u = u0 + i * LOAD_WARPS * 32;
+            if (u < units)
+#pragma unroll
+                for (int k = 0; k < PL; ++k) *reinterpret_cast<uint4*>(dst + k * plane + swizzled(u >> 3, u & 7)) = v[i][k];
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+
+template <int MODE, bool TENSOR, int NT, int PL>
+__global__ void __launch_bounds__(TENSOR ? 256 : 512, 1)
+product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUtensorMap map_a,
+               const __grid_constant__ CUtensorMap map_b) {
+    using R = Ring<NT, PL>;
+    constexpr int BOX_ROWS = NT <= 64 ? 16 : 64;     // rows of one copy of x (forward)
+    extern __shared__ unsigned char raw[];
+    unsigned char* stages = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+    uint64_t* full = reinterpret_cast<uint64_t*>(stages + R::STAGES * R::STAGE);
+    uint64_t* empty = full + R::STAGES;
+    uint64_t* acc_full = empty + R::STAGES;
+    uint64_t* acc_empty = acc_full + 2;
+    uint64_t* drain = acc_empty + 2;
+    uint32_t* tmem_at = reinterpret_cast<uint32_t*>(drain + 1);
+    int* last_part = reinterpret_cast<int*>(tmem_at + 1);
+    int* tile_adapter = reinterpret_cast<int*>(tmem_at + 16);    // [NT]
+    int* near = tile_adapter + NT;
+    const ProductParams& p = a.p;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    const bool is_near = p.S <= NEAR_SEGMENTS;
+    const int* beg = is_near ? near : a.far;
+    const int* pre = is_near ? near + NEAR_SEGMENTS + 1 : a.far + p.S + 1;
+    if (warp == 0) tmem_alloc(tmem_at, 2 * R::ACC);
+    if (tid == 0) {
+        for (int i = 0; i < R::STAGES; ++i) {
+            mbar_init(full + i, TENSOR ? 1 : LOAD_WARPS);
+            mbar_init(empty + i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(acc_full + i, 1);
+            mbar_init(acc_empty + i, 4);
+        }
+        mbar_init(drain, 1);
+        fence_mbarrier_init();
+        if (TENSOR) {
+            tensor_prefetch(&map_a);
+            tensor_prefetch(&map_b);
+        }
+    }
+    if (is_near && MODE != PRODUCT_ADAPTERS && p.S > 0) fill_prefix<MODE, NT>(a, near, near + NEAR_SEGMENTS + 1);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_at;
+
+    int64_t items;
+    // (the caps: offsets that decrease name more items than there can be)
+    if (MODE == PRODUCT_WEIGHTS) items = min(int64_t(pre[p.S]), p.S + p.R / a.chunk) * (a.mtiles * a.ntiles);
+    else if (MODE == PRODUCT_ADAPTERS) items = a.row_tiles * a.mtiles * a.parts;
+    else items = (p.S > 0 ? min(int64_t(pre[p.S]), a.row_tiles) : 0) * a.mtiles * a.parts;
+    const bool a_outer = MODE == PRODUCT_WEIGHTS || !p.trans;    // the operand's contiguous dimension is m, not the sum
+    constexpr bool b_outer = MODE == PRODUCT_WEIGHTS;
+
+    if (TENSOR ? warp == 1 : warp >= LOAD_WARP) {
+        // ---- producer ----
+        if (!TENSOR || lane == 0) {
+            uint32_t st = 0, ph = 1;
+            int64_t issued = 0;
+            bool ok = true;
+            for (int64_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
+                const Item t = item_at<MODE, NT>(a, beg, pre, i);
+                const int m_left = static_cast<int>(a.cols_m - t.m0 < MT ? a.cols_m - t.m0 : MT);
+                const int n_left = MODE == PRODUCT_WEIGHTS ? static_cast<int>(a.cols_n - t.n0 < NT ? a.cols_n - t.n0 : NT) : t.rows;
+                const int a_boxes = a_outer ? (m_left + 63) / 64 : 1;
+                const int b_boxes = b_outer ? (n_left + 63) / 64 : (n_left + BOX_ROWS - 1) / BOX_ROWS;
+                const uint32_t bytes = (a_outer ? a_boxes * 8192 : R::A_PLANE) + b_boxes * (b_outer ? 8192 : BOX_ROWS * 128);
+                int64_t m = t.seg;
+                if (MODE == PRODUCT_FORWARD && p.index) m = __ldg(p.index + t.seg);
+                for (int kb = t.kb0; kb < t.kb1; ++kb) {
+                    ok = TENSOR ? wait_bounded(empty + st, ph, p.status, STATUS_PRODUCT_TIMEOUT) : warp_wait(empty + st, ph, p.status);
+                    if (!ok) break;
+                    unsigned char* sa = stages + st * R::STAGE;
+                    unsigned char* sb = sa + PL * R::A_PLANE;
+                    if constexpr (TENSOR) {
+                        mbar_arrive_expect_tx(full + st, bytes);
+                        if (MODE == PRODUCT_WEIGHTS) {
+                            const int r = t.row0 + kb * KB;
+                            for (int x = 0; x < a_boxes; ++x) tensor_load_2d(sa + x * 8192, &map_a, t.m0 + x * 64, r, full + st);
+                            for (int x = 0; x < b_boxes; ++x) tensor_load_2d(sb + x * 8192, &map_b, t.n0 + x * 64, r, full + st);
+                        } else {
+                            if (a_outer) {
+                                for (int x = 0; x < a_boxes; ++x)
+                                    tensor_load_3d(sa + x * 8192, &map_a, t.m0 + x * 64, kb * KB, static_cast<int>(m), full + st);
+                            } else {
+                                tensor_load_3d(sa, &map_a, kb * KB, t.m0, static_cast<int>(m), full + st);
+                            }
+                            for (int x = 0; x < b_boxes; ++x)
+                                tensor_load_2d(sb + x * BOX_ROWS * 128, &map_b, kb * KB, t.row0 + x * BOX_ROWS, full + st);
+                        }
+                        ++issued;
+                    } else {
+                        constexpr int64_t size = PL == 1 ? 2 : 4;
+                        if (MODE == PRODUCT_WEIGHTS) {
+                            const int64_t r = t.row0 + kb * KB, re = t.row0 + t.rows;
+                            for (int x = 0; x < a_boxes; ++x)
+                                load_box<PL>(Box{p.w, p.ldw, r, re, t.m0 + x * 64, a.cols_m}, KB * 8, sa + x * 8192, R::A_PLANE);
+                            for (int x = 0; x < b_boxes; ++x)
+                                load_box<PL>(Box{p.x, p.ldx, r, re, t.n0 + x * 64, a.cols_n}, KB * 8, sb + x * 8192, R::B_PLANE);
+                        } else {
+                            const void* w = static_cast<const unsigned char*>(p.w) + m * p.stride_w * size;
+                            const int64_t k = int64_t(kb) * KB;
+                            if (a_outer) {
+                                for (int x = 0; x < a_boxes; ++x)
+                                    load_box<PL>(Box{w, p.ldw, k, p.K, t.m0 + x * 64, a.cols_m}, KB * 8, sa + x * 8192, R::A_PLANE);
+                            } else {
+                                load_box<PL>(Box{w, p.ldw, t.m0, a.cols_m, k, p.K}, MT * 8, sa, R::A_PLANE);
+                            }
+                            load_box<PL>(Box{p.x, p.ldx, t.row0, t.row0 + t.rows, k, p.K}, ((t.rows + 15) & ~15) * 8, sb, R::B_PLANE);
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(full + st);
+                    }
+                    if (++st == R::STAGES) {
+                        st = 0;
+                        ph ^= 1;
+                    }
+                }
+            }
+            if (TENSOR && !ok) {
+                // something gave up: the copies in flight still land before this CTA's shared memory goes away
+                for (int64_t j = issued > R::STAGES ? issued - R::STAGES : 0; j < issued; ++j)
+                    wait_bounded(full + j % R::STAGES, static_cast<uint32_t>((j / R::STAGES) & 1), p.status, STATUS_PRODUCT_TIMEOUT);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 0) {
+        // ---- MMA ----
+        uint32_t st = 0, ph = 0, buf = 0, bph = 1;
+        bool ok = true;
+        const uint32_t type = p.type == PT_F16 ? 0 : 1;
+        const uint32_t a_step = a_outer ? 2048 : 32, b_step = b_outer ? 2048 : 32;
+        for (int64_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
+            const Item t = item_at<MODE, NT>(a, beg, pre, i);
+            if (t.kb1 <= t.kb0) continue;
+            const int n_left = MODE == PRODUCT_WEIGHTS ? static_cast<int>(a.cols_n - t.n0 < NT ? a.cols_n - t.n0 : NT) : t.rows;
+            const uint32_t idesc = tc_idesc(type, MT, (n_left + 15) & ~15, a_outer, b_outer);
+            const int m_left = static_cast<int>(a.cols_m - t.m0 < MT ? a.cols_m - t.m0 : MT);
+            for (int piece = t.kb0; ok && piece < t.kb1; piece += a.flush) {
+                const int piece_end = t.kb1 - piece < a.flush ? t.kb1 : piece + a.flush;
+                ok = warp_wait(acc_empty + buf, bph, p.status);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t acc = tmem + buf * R::ACC;
+                for (int kb = piece; kb < piece_end; ++kb) {
+                    ok = warp_wait(full + st, ph, p.status);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const int64_t left = (MODE == PRODUCT_WEIGHTS ? t.rows : p.K) - int64_t(kb) * KB;
+                    const int steps = left >= KB ? 4 : static_cast<int>((left + 15) / 16);
+                    const uint32_t sa = smem_u32(stages + st * R::STAGE), sb = sa + PL * R::A_PLANE;
+                    if (MODE == PRODUCT_WEIGHTS && TENSOR && left < steps * 16) {
+                        // rows past the segment's end belong to others: zero them up to the last step's end
+                        const int tail = static_cast<int>(left), zero = (steps * 16 - tail) * 8;
+                        const int boxes_a = (m_left + 63) / 64, boxes = boxes_a + (n_left + 63) / 64;
+                        for (int u = lane; u < zero * boxes; u += 32) {
+                            const int x = u / zero, q = u - x * zero;
+                            unsigned char* box = stages + st * R::STAGE + (x < boxes_a ? x * 8192 : PL * R::A_PLANE + (x - boxes_a) * 8192);
+                            *reinterpret_cast<uint4*>(box + tail * 128 + q * 16) = make_uint4(0, 0, 0, 0);
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                    if (lane == 0) {
+                        for (int k = 0; k < steps; ++k) {
+                            const bool add = kb > piece || k > 0;
+                            if constexpr (PL == 1) {
+                                tc_mma(acc, tc_smem_desc(sa + k * a_step, 8192), tc_smem_desc(sb + k * b_step, 8192), idesc, add);
+                            } else {
+                                // the products of parts: the largest alone, the others together
+                                constexpr int pa[6] = {0, 2, 0, 1, 1, 0}, pb[6] = {0, 0, 2, 1, 0, 1};
+#pragma unroll
+                                for (int q = 0; q < 6; ++q)
+                                    tc_mma(q == 0 ? acc : acc + NT, tc_smem_desc(sa + pa[q] * R::A_PLANE + k * a_step, 8192),
+                                           tc_smem_desc(sb + pb[q] * R::B_PLANE + k * b_step, 8192), idesc, add || q > 1);
+                            }
+                        }
+                        tc_commit(empty + st);
+                        if (kb + 1 == piece_end) tc_commit(acc_full + buf);
+                    }
+                    __syncwarp();
+                    if (++st == R::STAGES) {
+                        st = 0;
+                        ph ^= 1;
+                    }
+                }
+                if ((buf ^= 1) == 0) bph ^= 1;
+            }
+        }
+        // nothing of this CTA's MMAs is in flight when its memory goes away
+        if (lane == 0) {
+            tc_commit(drain);
+            wait_bounded(drain, 0, p.status, STATUS_PRODUCT_TIMEOUT);
+        }
+        __syncwarp();
+    } else if (warp >= EPI_WARP && warp < EPI_WARP + 4) {
+        // ---- drain ----
+        const int quarter = warp - EPI_WARP, t128 = quarter * 32 + lane;
+        if (MODE == PRODUCT_FORWARD && !p.index) {
+            // rows in no segment
+            const int b = p.S > 0 ? beg[0] : 0, e = p.S > 0 ? beg[p.S] : 0;
+            const int64_t none = b + (p.R - (e > b ? e : b));
+            const int64_t each = static_cast<int64_t>(gridDim.x) * 128;
+            for (int64_t i = blockIdx.x * 128 + t128; i < none * p.N; i += each) {
+                const int64_t q = i / p.N, c = i - q * p.N, r = q < b ? q : (e > b ? e : b) + (q - b);
+                if (p.out_type == PT_F32) static_cast<float*>(p.out)[r * p.ldo + c] = 0.0f;
+                else static_cast<uint16_t*>(p.out)[r * p.ldo + c] = 0;
+            }
+        }
+        uint32_t buf = 0, bph = 0;
+        for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
+            const Item t = item_at<MODE, NT>(a, beg, pre, i);
+            const bool summed = t.kb1 > t.kb0;
+            const int n_left = MODE == PRODUCT_WEIGHTS ? static_cast<int>(a.cols_n - t.n0 < NT ? a.cols_n - t.n0 : NT) : t.rows;
+            const int64_t m = t.m0 + t128;
+            if constexpr (MODE == PRODUCT_ADAPTERS) {
+                bar_drain();       // the table of the tile before has been read
+                for (int r = t128; r < t.rows; r += 128) {
+                    const int row = t.row0 + r;
+                    int64_t lo = 0, hi = p.S;      // the last segment that starts at or before the row
+                    while (hi - lo > 1) {
+                        const int64_t mid = (lo + hi) >> 1;
+                        if (offset_at(p, mid) <= row) lo = mid; else hi = mid;
+                    }
+                    int l = -1;
+                    if (p.S > 0 && offset_at(p, lo) <= row && row < offset_at(p, lo + 1)) l = __ldg(p.index + lo);
+                    tile_adapter[r] = l >= 0 && l < p.L ? l : -1;
+                }
+                bar_drain();
+            }
+            float factor = 1.0f;
+            if (MODE == PRODUCT_FORWARD && p.scale) factor = __ldg(p.scale + __ldg(p.index + t.seg));
+            bool ok = true;
+            int piece = t.kb0;
+            do {
+                const bool first = piece == t.kb0, final = t.kb1 - piece <= a.flush;
+                if (summed) {
+                    ok = bar_drain_all(wait_bounded(acc_full + buf, bph, p.status, STATUS_PRODUCT_TIMEOUT));
+                    if (!ok) break;
+                    tc_fence_after();
+                }
+                const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * R::ACC;
+                // where the tile goes: its result, or (a part of a split sum) scratch
+                const bool partial = t.parts > 1;
+                const int64_t step = partial ? MT : (MODE == PRODUCT_WEIGHTS ? a.cols_m : p.ldo);
+                const int64_t at = partial ? t.slot * NT * MT + t128
+                                           : (MODE == PRODUCT_WEIGHTS ? (t.seg * a.cols_n + t.n0) * a.cols_m : t.row0 * p.ldo) + m;
+                for (int c = 0; c < n_left; c += 32) {
+                    float v[32];
+                    if (summed) {
+                        tmem_load_32(from + c, v);
+                        if constexpr (PL > 1) {
+                            float lo[32];
+                            tmem_load_32(from + NT + c, lo);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) v[j] += lo[j];
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+                    }
+                    if (!first && (partial || m < a.cols_m)) {
+                        // the sum so far, float32 wherever there is more than one piece
+                        const float* so_far = (partial ? a.partials : static_cast<const float*>(p.out)) + at + c * step;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (c + j < n_left) v[j] += so_far[j * step];
+                    }
+                    if (partial) {
+                        store_rows(a.partials, PT_F32, at + c * step, step, v, n_left - c);
+                    } else if (m < a.cols_m) {
+                        if (final) finish<MODE>(p, v, c, n_left, t, tile_adapter, m, factor);
+                        store_rows(p.out, p.out_type, at + c * step, step, v, n_left - c);
+                    }
+                }
+                if (summed) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(acc_empty + buf);
+                    if ((buf ^= 1) == 0) bph ^= 1;
+                }
+                piece = final ? t.kb1 : piece + a.flush;
+            } while (piece < t.kb1);
+            if (!ok) break;
+            if (MODE != PRODUCT_WEIGHTS && t.parts > 1) {
+                __threadfence();
+                bar_drain();
+                if (t128 == 0) {
+                    unsigned long long* ticket = a.tickets + t.ticket;
+                    red_max_relaxed_gpu(ticket, static_cast<unsigned long long>(p.gen) << 32);
+                    const unsigned long long old = atom_add_release_gpu(ticket, 1);
+                    fence_acq_rel_gpu();
+                    *last_part = static_cast<uint32_t>(old) + 1 == static_cast<uint32_t>(t.parts);
+                }
+                bar_drain();
+                if (*last_part && m < a.cols_m) {
+                    __threadfence();
+                    for (int c = 0; c < n_left; c += 32) {
+                        float v[32];
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+                        for (int q = 0; q < t.parts; ++q) {
+                            const float* part = a.partials + ((t.slot - t.part + q) * NT + c) * MT + t128;
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (c + j < n_left) v[j] += __ldcg(part + j * MT);
+                        }
+                        finish<MODE>(p, v, c, n_left, t, tile_adapter, m, factor);
+                        store_rows(p.out, p.out_type, (int64_t(t.row0) + c) * p.ldo + m, p.ldo, v, n_left - c);
+                    }
+                }
+            }
+        }
+        tc_fence_before();
+    }
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_free(tmem, 2 * R::ACC);
+    }
+}
+
+// Adds the parts of the split segments of the weights' product: block
+// (x, y) takes 16 columns of one tile of the split segment, if there is one,
+// that starts in chunk x / tiles.  With few parts each warp adds whole
+// columns; with many the eight warps share a column's parts.  Either order
+// is a function of the number of parts alone.
+constexpr int ADD_COLS = 16;
+
+template <int NT>
+__global__ void __launch_bounds__(256) add_parts_kernel(const __grid_constant__ KernelArgs a) {
+    __shared__ float4 part_sum[8][32];
+    const ProductParams& p = a.p;
+    const int per = a.mtiles * a.ntiles, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t j = blockIdx.x / per;
+    const int r = static_cast<int>(blockIdx.x - j * per);
+    int64_t lo = 0, hi = p.S;        // the last segment that starts before the chunk's end
+    while (hi - lo > 1) {
+        const int64_t mid = (lo + hi) >> 1;
+        if (offset_at(p, mid) < (j + 1) * a.chunk) lo = mid; else hi = mid;
+    }
+    const int64_t b = offset_at(p, lo), e = offset_at(p, lo + 1);
+    if (b / a.chunk != j || e - b <= a.chunk) return;
+    const int parts = static_cast<int>((e - b + a.chunk - 1) / a.chunk);
+    const int64_t m = r % a.mtiles * MT + lane * 4;
+    const int n0 = r / a.mtiles * NT;
+    auto part = [&](int q, int c) {
+        const int64_t slot = (2 * (j + q) + (q == 0 ? 1 : 0)) * per + r;
+        return __ldcg(reinterpret_cast<const float4*>(a.partials + (slot * NT + c) * MT) + lane);
+    };
+    auto add = [](float4& x, const float4& y) { x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w; };
+    auto put = [&](int c, const float4& v) {
+        const float f[4] = {v.x, v.y, v.z, v.w};
+        const int64_t at = (lo * a.cols_n + n0 + c) * a.cols_m + m;
         for (int i = 0; i < 4; ++i) {
-            const int64_t r = r0 + 4 * ty + i;
-            if (r >= p.R) continue;
-            int64_t lo = 0, hi = p.S;   // the last segment that starts at or before r
-            while (hi - lo > 1) {
-                const int64_t mid = (lo + hi) / 2;
-                if (offset_at(p, mid) <= r) lo = mid; else hi = mid;
+            if (m + i >= a.cols_m) break;
+            if (p.out_type == PT_F32) static_cast<float*>(p.out)[at + i] = f[i];
+            else if (p.out_type == PT_F16) static_cast<__half*>(p.out)[at + i] = __float2half_rn(f[i]);
+            else static_cast<__nv_bfloat16*>(p.out)[at + i] = __float2bfloat16_rn(f[i]);
+        }
+    };
+    const bool shared = parts > 16;
+    const int c1 = static_cast<int>(min(int64_t(blockIdx.y + 1) * ADD_COLS, a.cols_n - n0));
+    for (int c = blockIdx.y * ADD_COLS + (shared ? 0 : warp); c < c1; c += shared ? 1 : 8) {
+        float4 v = make_float4(0, 0, 0, 0);
+#pragma unroll 8
+        for (int q = shared ? warp : 0; q < parts; q += shared ? 8 : 1) add(v, part(q, c));
+        if (shared) {
+            part_sum[warp][lane] = v;
+            __syncthreads();
+            if (warp == 0) {
+                for (int w = 1; w < 8; ++w) add(v, part_sum[w][lane]);
+                put(c, v);
             }
-            int64_t l = -1;
-            if (p.S > 0 && offset_at(p, lo) <= r && r < offset_at(p, lo + 1)) l = __ldg(p.index + lo);
-            for (int j = 0; j < 4; ++j) {
-                const int64_t n = n0 + 4 * tx + j;
-                if (n >= p.N) continue;
-                float v = acc[i][j];
-                if (l >= 0 && l < p.L)
-                    for (int64_t q = 0; q < p.rank; ++q)
-                        v += p.u[r * p.rank + q] * to_f(static_cast<const T*>(p.b)[(l * p.N + n) * p.rank + q]);
-                out[r * p.ldo + n] = from_f<T>(v);
-            }
+            __syncthreads();
+        } else {
+            put(c, v);
         }
     }
 }
 
-template <class F>
-cudaError_t by_type(int type, F f) {
-    if (type == PT_F32) return f(float());
-    if (type == PT_F16) return f(__half());
-    return f(__nv_bfloat16());
+int64_t ceil_to(int64_t n, int64_t d) { return (n + d - 1) / d; }
+
+// ---------------------------------------------------------------------------
+// Tensor maps: 16-bit values, boxes of 64 columns, 128-byte swizzle.
+
+typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                             const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+    static const EncodeFn fn = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            return EncodeFn(nullptr);
+        return reinterpret_cast<EncodeFn>(f);
+    }();
+    return fn;
 }
 
-unsigned tiles(int64_t n, int64_t most = 65535) {
-    const int64_t t = (n + PT - 1) / PT;
-    return static_cast<unsigned>(t < most ? (t < 1 ? 1 : t) : most);
+bool make_map(CUtensorMap* map, int type, const void* base, int64_t cols, int64_t rows, int64_t ld, int64_t mats,
+              int64_t stride, int box_rows) {
+    const EncodeFn fn = encode_fn();
+    if (!fn) return false;
+    const int rank = mats > 0 ? 3 : 2;
+    const cuuint64_t dims[3] = {cuuint64_t(cols), cuuint64_t(rows), cuuint64_t(mats)};
+    const cuuint64_t strides[2] = {cuuint64_t(ld) * 2, cuuint64_t(stride) * 2};
+    const cuuint32_t box[3] = {KB, cuuint32_t(box_rows), 1}, each[3] = {1, 1, 1};
+    return fn(map, type == PT_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank,
+              const_cast<void*>(base), dims, strides, box, each, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+
+// What a tensor map can describe: 16-byte aligned, strides multiples of 16 bytes and below 2^40.
+bool tensor_copyable(const void* base, int64_t stride) {
+    return reinterpret_cast<uintptr_t>(base) % 16 == 0 && stride % 8 == 0 && stride < (int64_t(1) << 38);
+}
+
+template <int MODE, bool TENSOR, int NT, int PL>
+cudaError_t launch_shape(const KernelArgs& a, const ProductPlan& plan, cudaStream_t stream) {
+    CUtensorMap ma{}, mb{};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (TENSOR) {
+        // the driver call below needs the context, which a thread that has not
+        // called the runtime yet (an autograd thread) does not have current
+        e = cudaSetDevice(dev);
+        if (e != cudaSuccess) return e;
+        const ProductParams& p = a.p;
+        const int rows_box = NT <= 64 ? 16 : 64;
+        bool ok;
+        if (MODE == PRODUCT_WEIGHTS) {
+            ok = make_map(&ma, p.type, p.w, p.N, p.R, p.ldw, 0, 0, KB) && make_map(&mb, p.type, p.x, p.K, p.R, p.ldx, 0, 0, KB);
+        } else {
+            const int64_t mats = MODE == PRODUCT_ADAPTERS ? 1 : (p.index ? p.L : p.S);
+            const int64_t rows = p.trans ? p.N : p.K, cols = p.trans ? p.K : p.N;
+            ok = make_map(&ma, p.type, p.w, cols, rows, p.ldw, mats, mats > 1 ? p.stride_w : rows * p.ldw, p.trans ? MT : KB) &&
+                 make_map(&mb, p.type, p.x, p.K, p.R, p.ldx, 0, 0, rows_box);
+        }
+        if (!ok) return cudaErrorInvalidValue;
+    }
+    if (a.p.S > NEAR_SEGMENTS && MODE != PRODUCT_ADAPTERS) {
+        prefix_kernel<MODE, NT><<<1, 1024, 0, stream>>>(a);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    auto* kernel = product_kernel<MODE, TENSOR, NT, PL>;
+    constexpr int smem = Ring<NT, PL>::SMEM;
+    static uint64_t configured = 0;     // a bit per device; callers hold the library's lock
+    if (!(configured >> dev & 1)) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        configured |= uint64_t(1) << dev;
+    }
+    kernel<<<plan.grid, TENSOR ? 256 : 512, smem, stream>>>(a, ma, mb);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || plan.add_blocks == 0) return e;
+    if constexpr (MODE == PRODUCT_WEIGHTS) {
+        const int64_t cols = std::min<int64_t>(a.cols_n, NT);
+        add_parts_kernel<NT><<<dim3(plan.add_blocks, static_cast<unsigned>(ceil_to(cols, ADD_COLS))), 256, 0, stream>>>(a);
+        e = cudaGetLastError();
+    }
+    return e;
+}
+
+template <int MODE>
+cudaError_t launch_mode(const KernelArgs& a, const ProductPlan& plan, cudaStream_t stream) {
+    if (a.p.type == PT_F32)
+        return plan.narrow ? launch_shape<MODE, false, 64, 3>(a, plan, stream) : launch_shape<MODE, false, 128, 3>(a, plan, stream);
+    if (plan.tensor)
+        return plan.narrow ? launch_shape<MODE, true, 64, 1>(a, plan, stream) : launch_shape<MODE, true, 256, 1>(a, plan, stream);
+    return plan.narrow ? launch_shape<MODE, false, 64, 1>(a, plan, stream) : launch_shape<MODE, false, 256, 1>(a, plan, stream);
+}
+
+int tile_columns(const ProductParams& p, bool narrow) { return narrow ? 64 : (p.type == PT_F32 ? 128 : 256); }
 
 }  // namespace
 
-cudaError_t launch_product(const ProductParams& p, cudaStream_t stream) {
-    return by_type(p.type, [&](auto t) {
-        using T = decltype(t);
-        const dim3 grid(tiles(p.N, 1 << 30), static_cast<unsigned>(p.S < 65000 ? p.S + 1 : 65000));
-        if (p.out_type == PT_F32) forward_kernel<T, float><<<grid, 256, 0, stream>>>(p);
-        else forward_kernel<T, T><<<grid, 256, 0, stream>>>(p);
-        return cudaGetLastError();
-    });
+ProductPlan plan_product(int mode, const ProductParams& p) {
+    ProductPlan d{};
+    const bool weights = mode == PRODUCT_WEIGHTS;
+    const int64_t mats = mode == PRODUCT_FORWARD ? (p.index ? p.L : p.S) : 1;
+    d.tensor = p.type != PT_F32 && p.K > 0 && p.R > 0 && mats > 0 && tensor_copyable(p.x, p.ldx) &&
+               tensor_copyable(p.w, p.ldw) && (mats == 1 || tensor_copyable(p.w, p.stride_w));
+    const int64_t segments = mode == PRODUCT_ADAPTERS ? 1 : p.S;
+    // few rows per segment: small tiles and a deeper ring; weights: few columns of x
+    d.narrow = weights ? p.K <= 64 : p.R <= 64 * segments;
+    const int NT = tile_columns(p, d.narrow);
+    d.mtiles = static_cast<int32_t>(ceil_to(p.N, MT));
+    d.ntiles = weights ? static_cast<int32_t>(ceil_to(p.K, NT)) : 1;
+    d.parts = 1;
+    d.part_blocks = static_cast<int32_t>(ceil_to(p.K, KB));
+    d.chunk = std::max<int64_t>(p.R, 1);
+    int64_t slots = 0, items;
+    if (weights) {
+        const int64_t per = int64_t(d.mtiles) * d.ntiles;
+        // parts of at least so many rows that storing a part costs a fraction of them
+        const int64_t least = 8 * std::min<int64_t>(p.K, NT);
+        if (segments * per < 8 * p.sms) {
+            const int64_t chunk = std::max(least, ceil_to(ceil_to(p.R * per, 4 * p.sms), KB) * KB);
+            if (chunk < p.R) {
+                d.chunk = chunk;
+                d.add_blocks = static_cast<int32_t>((p.R / chunk + 1) * per);
+                slots = 2 * int64_t(d.add_blocks);
+            }
+        }
+        items = (segments + p.R / d.chunk) * per;
+    } else {
+        d.row_tiles = mode == PRODUCT_ADAPTERS ? ceil_to(p.R, NT) : std::min(segments, p.R) + p.R / NT;
+        items = d.row_tiles * d.mtiles;
+        if (items * 2 <= p.sms && d.part_blocks >= 8) {
+            const int64_t parts = std::min<int64_t>(p.sms / items, d.part_blocks / 4);
+            d.part_blocks = static_cast<int32_t>(ceil_to(d.part_blocks, parts));
+            d.parts = static_cast<int32_t>(ceil_to(ceil_to(p.K, KB), d.part_blocks));
+            if (d.parts > 1) slots = items * d.parts;
+            items *= d.parts;
+        }
+    }
+    d.grid = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(items, p.sms)));
+    d.ticket_bytes = PRODUCT_TICKETS * 8;
+    d.prefix_bytes = mode != PRODUCT_ADAPTERS && p.S > NEAR_SEGMENTS ? ceil_to((p.S + 1) * 8, 256) * 256 : 0;
+    d.partial_bytes = slots * NT * MT * 4;
+    return d;
 }
 
-cudaError_t launch_product_grad(const ProductParams& p, cudaStream_t stream) {
-    return by_type(p.type, [&](auto t) {
-        using T = decltype(t);
-        const dim3 grid(tiles(p.N, 1 << 30), tiles(p.K), static_cast<unsigned>(p.S < 65000 ? p.S : 65000));
-        if (p.out_type == PT_F32) grad_kernel<T, float><<<grid, 256, 0, stream>>>(p);
-        else grad_kernel<T, T><<<grid, 256, 0, stream>>>(p);
-        return cudaGetLastError();
-    });
-}
-
-cudaError_t launch_lora(const ProductParams& p, cudaStream_t stream) {
-    return by_type(p.type, [&](auto t) {
-        using T = decltype(t);
-        lora_kernel<T><<<dim3(tiles(p.N, 1 << 30), tiles(p.R)), 256, 0, stream>>>(p);
-        return cudaGetLastError();
-    });
+cudaError_t launch_product(int mode, const ProductParams& p, const ProductPlan& plan, cudaStream_t stream) {
+    KernelArgs a{};
+    a.p = p;
+    a.mtiles = plan.mtiles;
+    a.ntiles = plan.ntiles;
+    a.parts = plan.parts;
+    a.part_blocks = plan.part_blocks;
+    a.kblocks = static_cast<int32_t>(ceil_to(p.K, KB));
+    a.flush = p.type == PT_F32 ? 8 : (p.out_type == PT_F32 && !p.index ? 12 : NEVER_FLUSH);
+    a.chunk = plan.chunk;
+    a.row_tiles = plan.row_tiles;
+    a.cols_m = p.N;
+    a.cols_n = p.K;
+    a.tickets = reinterpret_cast<unsigned long long*>(p.ws);
+    a.far = reinterpret_cast<int*>(p.ws + plan.ticket_bytes);
+    a.partials = reinterpret_cast<float*>(p.ws + plan.ticket_bytes + plan.prefix_bytes);
+    if (mode == PRODUCT_FORWARD) return launch_mode<PRODUCT_FORWARD>(a, plan, stream);
+    if (mode == PRODUCT_WEIGHTS) return launch_mode<PRODUCT_WEIGHTS>(a, plan, stream);
+    return launch_mode<PRODUCT_ADAPTERS>(a, plan, stream);
 }
 
 }  // namespace segred

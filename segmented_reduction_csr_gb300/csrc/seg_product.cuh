@@ -19,23 +19,48 @@ enum : int { PT_F32 = 2, PT_F16 = 3, PT_BF16 = 4 };
 
 struct ProductParams {
     const void* x;          // [R, K], row stride ldx
-    const void* w;          // forward: [S][K, N] or [S][N, K] (trans); weights: dy [R, N]
+    const void* w;          // forward: [S][K, N] or [S][N, K] (trans); weights: dy [R, N]; adapters: [N, K]
     const void* offsets;    // [S + 1]
-    const int32_t* index;   // forward: the matrix of segment s is w[index[s]] (negative: none), or NULL: w[s]
-    const float* scale;     // forward with index: the products are scaled by scale[index[s]], or NULL
+    const int32_t* index;   // forward: the matrix of segment s is w[index[s]] (outside [0, L): none), or NULL: w[s]
+    const float* scale;     // forward with index: products are scaled by scale[index[s]], or NULL
     void* out;              // forward: [R, N], row stride ldo; weights: [S][K, N]
     int64_t R, K, N, S;
     int64_t ldx, ldw, stride_w, ldo;
-    int64_t L;              // forward with index: matrices in w
+    int64_t L;              // matrices that index names
     int32_t off64, trans, type, out_type;
     // adapters: the low-rank part added to the shared product
     const float* u;         // [R, rank] scaled products with a
     const void* b;          // [L][N, rank]
     int64_t rank;
+    // library-owned
+    unsigned char* ws;      // see ProductPlan
+    unsigned int* status;   // device status word
+    uint32_t gen;           // call generation of the ticket words
+    int32_t sms;
 };
 
-cudaError_t launch_product(const ProductParams& p, cudaStream_t stream);
-cudaError_t launch_product_grad(const ProductParams& p, cudaStream_t stream);
-cudaError_t launch_lora(const ProductParams& p, cudaStream_t stream);
+// How a call is launched; a pure function of sizes, strides, alignment and the SM count.
+struct ProductPlan {
+    int32_t grid;
+    int32_t tensor;         // 1: operands come by tensor copies, 0: by the loader warps
+    int32_t narrow;         // 1: at most 64 rows per tile and a deeper ring
+    int32_t mtiles, ntiles; // tiles of the output's contiguous / other dimension (forward: rows vary by segment)
+    int32_t parts;          // forward: parts of the contraction
+    int32_t part_blocks;    // forward: 64-wide blocks per part
+    int64_t chunk;          // weights: rows per part of a segment
+    int32_t add_blocks;     // weights: blocks of the kernel that adds the parts (0: no segment can be split)
+    int64_t row_tiles;      // forward: most row tiles there can be
+    int64_t ticket_bytes, prefix_bytes, partial_bytes;   // the workspace, in this order
+    int64_t bytes() const { return ticket_bytes + prefix_bytes + partial_bytes; }
+};
+
+// Ticket words sit at the start of the products' scratch, whatever the call:
+// nothing else is ever written there.
+constexpr int64_t PRODUCT_TICKETS = 1024;
+
+enum : int { PRODUCT_FORWARD = 0, PRODUCT_WEIGHTS = 1, PRODUCT_ADAPTERS = 2 };
+
+ProductPlan plan_product(int mode, const ProductParams& p);
+cudaError_t launch_product(int mode, const ProductParams& p, const ProductPlan& plan, cudaStream_t stream);
 
 }  // namespace segred
