@@ -49,14 +49,14 @@ constexpr int LOAD_WARP = 8, LOAD_WARPS = 8;
 constexpr int NEVER_FLUSH = 1 << 28;         // more blocks than any sum has
 constexpr unsigned STATUS_PRODUCT_TIMEOUT = 8u;
 
-// Stage ring of a kernel shape: PL 16-bit planes per operand.
-template <int NT, int PL>
+// Stage ring of a kernel shape: PL 16-bit planes per operand, CG CTAs that share a tile.
+template <int NT, int PL, int CG>
 struct Ring {
-    static constexpr int A_PLANE = MT * 128, B_PLANE = NT * 128;
+    static constexpr int A_PLANE = MT * 128, B_PLANE = NT / CG * 128;
     static constexpr int STAGE = PL * (A_PLANE + B_PLANE);
     static constexpr int STAGES = std::min(8, 221184 / STAGE);
     static constexpr int ACC = PL == 1 ? NT : 2 * NT;            // tensor-memory columns of one accumulator
-    static constexpr int BARS = 2 * STAGES + 5;
+    static constexpr int BARS = 3 * STAGES + 5;
     static constexpr int FIXED = 2 * (NEAR_SEGMENTS + 1) * 4 + BARS * 8 + 64 + NT * 4;
     static constexpr int SMEM = STAGES * STAGE + FIXED + 1024;   // 1024: alignment of the stages
     static_assert(SMEM <= 232448, "shared memory of an SM");
@@ -136,7 +136,7 @@ struct Item {
     int64_t slot, ticket;
 };
 
-template <int MODE, int NT>
+template <int MODE, int NT, int CG>
 __device__ __forceinline__ Item item_at(const KernelArgs& a, const int* beg, const int* pre, int64_t i) {
     Item t;
     int q;
@@ -144,13 +144,13 @@ __device__ __forceinline__ Item item_at(const KernelArgs& a, const int* beg, con
         const int per = a.mtiles * a.ntiles;
         q = static_cast<int>(i / per);
         const int r = static_cast<int>(i - int64_t(q) * per);
-        t.m0 = r % a.mtiles * MT;
+        t.m0 = r % a.mtiles * (MT * CG);
         t.n0 = r / a.mtiles * NT;
     } else {
         const int64_t tile = i / a.parts;
         t.part = static_cast<int>(i - tile * a.parts);
         q = static_cast<int>(tile / a.mtiles);
-        t.m0 = static_cast<int>(tile - int64_t(q) * a.mtiles) * MT;
+        t.m0 = static_cast<int>(tile - int64_t(q) * a.mtiles) * (MT * CG);
         t.n0 = 0;
     }
     int b = 0, e = static_cast<int>(a.p.R), first = 0, count;
@@ -181,7 +181,7 @@ __device__ __forceinline__ Item item_at(const KernelArgs& a, const int* beg, con
         // parts of one split segment start `chunk` rows apart, and a block of
         // `chunk` rows holds the starts of at most two split segments' parts,
         // one of them a first part: so these numbers are each used once
-        const int per = a.mtiles * a.ntiles, r = t.m0 / MT + t.n0 / NT * a.mtiles;
+        const int per = a.mtiles * a.ntiles, r = t.m0 / (MT * CG) + t.n0 / NT * a.mtiles;
         t.slot = (2 * (t.row0 / a.chunk) + (j == 0 ? 1 : 0)) * per + r;
         t.ticket = 0;
     } else {
@@ -211,9 +211,26 @@ __device__ __forceinline__ bool bar_drain_all(bool ok) {
         : "memory");
     return r != 0;
 }
-// A wait of a whole warp.
+// A bounded wait; CG == 2: for arrivals of both CTAs.  The clock is read only
+// after a few hundred tries: a read takes longer than a stage does.
+template <int CG>
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, unsigned int* status) {
+    uint64_t t0 = 0;
+    for (uint32_t i = 1;; ++i) {
+        if (CG == 2 ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
+        if ((i & 255) == 0) {
+            const uint64_t now = globaltimer_ns();
+            if (t0 == 0) t0 = now;
+            if (now - t0 > WAIT_LIMIT_NS) break;
+        }
+    }
+    atomicOr(status, STATUS_PRODUCT_TIMEOUT);
+    return false;
+}
+// The same for a whole warp.
+template <int CG>
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, unsigned int* status) {
-    return __all_sync(0xffffffffu, wait_bounded(bar, parity, status, STATUS_PRODUCT_TIMEOUT));
+    return __all_sync(0xffffffffu, wait_for<CG>(bar, parity, status));
 }
 
 __device__ __forceinline__ float value_at(const void* base, int64_t i, int type) {
@@ -358,18 +375,20 @@ __device__ __forceinline__ void load_box(const Box& x, int units, unsigned char*
 
 // ---------------------------------------------------------------------------
 
-template <int MODE, bool TENSOR, int NT, int PL>
+template <int MODE, bool TENSOR, int NT, int PL, int CG>
 __global__ void __launch_bounds__(TENSOR ? 256 : 512, 1)
 product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUtensorMap map_a,
                const __grid_constant__ CUtensorMap map_b) {
-    using R = Ring<NT, PL>;
+    using R = Ring<NT, PL, CG>;
+    static_assert(CG == 1 || TENSOR, "pairs load by tensor copies");
     constexpr int BOX_ROWS = NT <= 64 ? 16 : 64;     // rows of one copy of x (forward)
     extern __shared__ unsigned char raw[];
     unsigned char* stages = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
-    uint64_t* full = reinterpret_cast<uint64_t*>(stages + R::STAGES * R::STAGE);
+    uint64_t* full = reinterpret_cast<uint64_t*>(stages + R::STAGES * R::STAGE);   // CG == 2: CTA 0's count
     uint64_t* empty = full + R::STAGES;
-    uint64_t* acc_full = empty + R::STAGES;
-    uint64_t* acc_empty = acc_full + 2;
+    uint64_t* landed = empty + R::STAGES;          // a stage whose tail has to be zeroed has arrived
+    uint64_t* acc_full = landed + R::STAGES;
+    uint64_t* acc_empty = acc_full + 2;            // CG == 2: CTA 0's count
     uint64_t* drain = acc_empty + 2;
     uint32_t* tmem_at = reinterpret_cast<uint32_t*>(drain + 1);
     int* last_part = reinterpret_cast<int*>(tmem_at + 1);
@@ -377,19 +396,22 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
     int* near = tile_adapter + NT;
     const ProductParams& p = a.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = CG == 2 ? static_cast<int>(cluster_rank()) : 0;
+    const int64_t first = blockIdx.x / CG, stride = gridDim.x / CG;
 
     const bool is_near = p.S <= NEAR_SEGMENTS;
     const int* beg = is_near ? near : a.far;
     const int* pre = is_near ? near + NEAR_SEGMENTS + 1 : a.far + p.S + 1;
-    if (warp == 0) tmem_alloc(tmem_at, 2 * R::ACC);
+    if (warp == 0) tmem_alloc<CG>(tmem_at, 2 * R::ACC);
     if (tid == 0) {
         for (int i = 0; i < R::STAGES; ++i) {
-            mbar_init(full + i, TENSOR ? 1 : LOAD_WARPS);
+            mbar_init(full + i, TENSOR ? CG : LOAD_WARPS);
             mbar_init(empty + i, 1);
+            mbar_init(landed + i, 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(acc_full + i, 1);
-            mbar_init(acc_empty + i, 4);
+            mbar_init(acc_empty + i, 4 * CG);
         }
         mbar_init(drain, 1);
         fence_mbarrier_init();
@@ -401,6 +423,7 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
     if (is_near && MODE != PRODUCT_ADAPTERS && p.S > 0) fill_prefix<MODE, NT>(a, near, near + NEAR_SEGMENTS + 1);
     tc_fence_before();
     __syncthreads();
+    if (CG == 2) cluster_sync();
     tc_fence_after();
     const uint32_t tmem = *tmem_at;
 
@@ -412,41 +435,66 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
     const bool a_outer = MODE == PRODUCT_WEIGHTS || !p.trans;    // the operand's contiguous dimension is m, not the sum
     constexpr bool b_outer = MODE == PRODUCT_WEIGHTS;
 
+    // Extents of a tile: lanes of this CTA that exist, columns, and columns per CTA.
+    auto lanes_of = [&](const Item& t) {
+        const int64_t left = a.cols_m - t.m0 - rank * MT;
+        return static_cast<int>(left < MT ? (left < 0 ? 0 : left) : MT);
+    };
+    auto columns_of = [&](const Item& t) {
+        return MODE == PRODUCT_WEIGHTS ? static_cast<int>(a.cols_n - t.n0 < NT ? a.cols_n - t.n0 : NT) : t.rows;
+    };
+    auto share_of = [&](int columns) { return ((columns + CG - 1) / CG + 15) & ~15; };
+    // The last block of a weights' sum reaches past the segment: those rows are zeroed once they have arrived.
+    auto has_tail = [&](const Item& t, int kb) { return MODE == PRODUCT_WEIGHTS && kb + 1 == t.kb1 && (t.rows & 15) != 0; };
+
     if (TENSOR ? warp == 1 : warp >= LOAD_WARP) {
         // ---- producer ----
-        if (!TENSOR || lane == 0) {
+        if (!TENSOR || elect_one()) {
             uint32_t st = 0, ph = 1;
             int64_t issued = 0;
             bool ok = true;
-            for (int64_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
-                const Item t = item_at<MODE, NT>(a, beg, pre, i);
-                const int m_left = static_cast<int>(a.cols_m - t.m0 < MT ? a.cols_m - t.m0 : MT);
-                const int n_left = MODE == PRODUCT_WEIGHTS ? static_cast<int>(a.cols_n - t.n0 < NT ? a.cols_n - t.n0 : NT) : t.rows;
-                const int a_boxes = a_outer ? (m_left + 63) / 64 : 1;
-                const int b_boxes = b_outer ? (n_left + 63) / 64 : (n_left + BOX_ROWS - 1) / BOX_ROWS;
-                const uint32_t bytes = (a_outer ? a_boxes * 8192 : R::A_PLANE) + b_boxes * (b_outer ? 8192 : BOX_ROWS * 128);
+            for (int64_t i = first; ok && i < items; i += stride) {
+                const Item t = item_at<MODE, NT, CG>(a, beg, pre, i);
+                const int columns = columns_of(t), share = share_of(columns), lanes = lanes_of(t);
+                const int a_boxes = a_outer ? (lanes + 63) / 64 : (lanes + MT - 1) / MT;
+                const int b_boxes = b_outer ? (share + 63) / 64 : (share + BOX_ROWS - 1) / BOX_ROWS;
+                const uint32_t b_bytes = b_boxes * (b_outer ? 8192 : BOX_ROWS * 128);
+                const uint32_t bytes = a_boxes * (a_outer ? 8192 : R::A_PLANE) + b_bytes;
+                const int m0 = t.m0 + rank * MT;
+                uint32_t other_bytes = 0;
+                if (CG == 2) {
+                    const int64_t left = a.cols_m - t.m0 - MT;
+                    const int other = static_cast<int>(left < MT ? (left < 0 ? 0 : left) : MT);
+                    other_bytes = b_bytes + (a_outer ? (other + 63) / 64 * 8192 : (other + MT - 1) / MT * R::A_PLANE);
+                }
                 int64_t m = t.seg;
                 if (MODE == PRODUCT_FORWARD && p.index) m = __ldg(p.index + t.seg);
                 for (int kb = t.kb0; kb < t.kb1; ++kb) {
-                    ok = TENSOR ? wait_bounded(empty + st, ph, p.status, STATUS_PRODUCT_TIMEOUT) : warp_wait(empty + st, ph, p.status);
+                    ok = TENSOR ? wait_for<CG>(empty + st, ph, p.status) : warp_wait<CG>(empty + st, ph, p.status);
                     if (!ok) break;
                     unsigned char* sa = stages + st * R::STAGE;
                     unsigned char* sb = sa + PL * R::A_PLANE;
                     if constexpr (TENSOR) {
-                        mbar_arrive_expect_tx(full + st, bytes);
+                        const bool tail = has_tail(t, kb);
+                        const uint32_t bar = tail ? smem_u32(landed + st) : lead_addr<CG>(full + st);
+                        if (tail) {
+                            mbar_arrive_expect_tx(landed + st, bytes);
+                        } else if (rank == 0) {      // both arrivals, and the bytes of both CTAs
+                            mbar_arrive_expect_tx(full + st, bytes + other_bytes);
+                            if (CG == 2) mbar_arrive(full + st);
+                        }
                         if (MODE == PRODUCT_WEIGHTS) {
-                            const int r = t.row0 + kb * KB;
-                            for (int x = 0; x < a_boxes; ++x) tensor_load_2d(sa + x * 8192, &map_a, t.m0 + x * 64, r, full + st);
-                            for (int x = 0; x < b_boxes; ++x) tensor_load_2d(sb + x * 8192, &map_b, t.n0 + x * 64, r, full + st);
+                            const int r = t.row0 + kb * KB, n0 = t.n0 + rank * share;
+                            for (int x = 0; x < a_boxes; ++x) tensor_load_2d<CG>(sa + x * 8192, &map_a, m0 + x * 64, r, bar);
+                            for (int x = 0; x < b_boxes; ++x) tensor_load_2d<CG>(sb + x * 8192, &map_b, n0 + x * 64, r, bar);
                         } else {
-                            if (a_outer) {
-                                for (int x = 0; x < a_boxes; ++x)
-                                    tensor_load_3d(sa + x * 8192, &map_a, t.m0 + x * 64, kb * KB, static_cast<int>(m), full + st);
-                            } else {
-                                tensor_load_3d(sa, &map_a, kb * KB, t.m0, static_cast<int>(m), full + st);
+                            const int r0 = t.row0 + rank * share;
+                            for (int x = 0; x < a_boxes; ++x) {
+                                if (a_outer) tensor_load_3d<CG>(sa + x * 8192, &map_a, m0 + x * 64, kb * KB, static_cast<int>(m), bar);
+                                else tensor_load_3d<CG>(sa, &map_a, kb * KB, m0, static_cast<int>(m), bar);
                             }
                             for (int x = 0; x < b_boxes; ++x)
-                                tensor_load_2d(sb + x * BOX_ROWS * 128, &map_b, kb * KB, t.row0 + x * BOX_ROWS, full + st);
+                                tensor_load_2d<CG>(sb + x * BOX_ROWS * 128, &map_b, kb * KB, r0 + x * BOX_ROWS, bar);
                         }
                         ++issued;
                     } else {
@@ -454,7 +502,7 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                         if (MODE == PRODUCT_WEIGHTS) {
                             const int64_t r = t.row0 + kb * KB, re = t.row0 + t.rows;
                             for (int x = 0; x < a_boxes; ++x)
-                                load_box<PL>(Box{p.w, p.ldw, r, re, t.m0 + x * 64, a.cols_m}, KB * 8, sa + x * 8192, R::A_PLANE);
+                                load_box<PL>(Box{p.w, p.ldw, r, re, m0 + x * 64, a.cols_m}, KB * 8, sa + x * 8192, R::A_PLANE);
                             for (int x = 0; x < b_boxes; ++x)
                                 load_box<PL>(Box{p.x, p.ldx, r, re, t.n0 + x * 64, a.cols_n}, KB * 8, sb + x * 8192, R::B_PLANE);
                         } else {
@@ -462,15 +510,15 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                             const int64_t k = int64_t(kb) * KB;
                             if (a_outer) {
                                 for (int x = 0; x < a_boxes; ++x)
-                                    load_box<PL>(Box{w, p.ldw, k, p.K, t.m0 + x * 64, a.cols_m}, KB * 8, sa + x * 8192, R::A_PLANE);
+                                    load_box<PL>(Box{w, p.ldw, k, p.K, m0 + x * 64, a.cols_m}, KB * 8, sa + x * 8192, R::A_PLANE);
                             } else {
-                                load_box<PL>(Box{w, p.ldw, t.m0, a.cols_m, k, p.K}, MT * 8, sa, R::A_PLANE);
+                                load_box<PL>(Box{w, p.ldw, m0, a.cols_m, k, p.K}, MT * 8, sa, R::A_PLANE);
                             }
-                            load_box<PL>(Box{p.x, p.ldx, t.row0, t.row0 + t.rows, k, p.K}, ((t.rows + 15) & ~15) * 8, sb, R::B_PLANE);
+                            load_box<PL>(Box{p.x, p.ldx, t.row0, t.row0 + t.rows, k, p.K}, share * 8, sb, R::B_PLANE);
                         }
                         fence_proxy_async_smem();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(full + st);
+                        if (lane == 0) lead_arrive<CG>(full + st, true);
                     }
                     if (++st == R::STAGES) {
                         st = 0;
@@ -478,80 +526,93 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                     }
                 }
             }
-            if (TENSOR && !ok) {
+            if (TENSOR && rank == 0 && !ok) {
                 // something gave up: the copies in flight still land before this CTA's shared memory goes away
                 for (int64_t j = issued > R::STAGES ? issued - R::STAGES : 0; j < issued; ++j)
-                    wait_bounded(full + j % R::STAGES, static_cast<uint32_t>((j / R::STAGES) & 1), p.status, STATUS_PRODUCT_TIMEOUT);
+                    wait_for<CG>(full + j % R::STAGES, static_cast<uint32_t>((j / R::STAGES) & 1), p.status);
             }
         }
         __syncwarp();
-    } else if (warp == 0) {
-        // ---- MMA ----
-        uint32_t st = 0, ph = 0, buf = 0, bph = 1;
+    } else if (TENSOR && MODE == PRODUCT_WEIGHTS && warp == 2) {
+        // ---- tails ----
+        uint32_t st = 0, seen = 0;        // a parity per stage
         bool ok = true;
-        const uint32_t type = p.type == PT_F16 ? 0 : 1;
-        const uint32_t a_step = a_outer ? 2048 : 32, b_step = b_outer ? 2048 : 32;
-        for (int64_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
-            const Item t = item_at<MODE, NT>(a, beg, pre, i);
+        for (int64_t i = first; ok && i < items; i += stride) {
+            const Item t = item_at<MODE, NT, CG>(a, beg, pre, i);
             if (t.kb1 <= t.kb0) continue;
-            const int n_left = MODE == PRODUCT_WEIGHTS ? static_cast<int>(a.cols_n - t.n0 < NT ? a.cols_n - t.n0 : NT) : t.rows;
-            const uint32_t idesc = tc_idesc(type, MT, (n_left + 15) & ~15, a_outer, b_outer);
-            const int m_left = static_cast<int>(a.cols_m - t.m0 < MT ? a.cols_m - t.m0 : MT);
-            for (int piece = t.kb0; ok && piece < t.kb1; piece += a.flush) {
-                const int piece_end = t.kb1 - piece < a.flush ? t.kb1 : piece + a.flush;
-                ok = warp_wait(acc_empty + buf, bph, p.status);
+            st = (st + (t.kb1 - t.kb0 - 1)) % R::STAGES;
+            if (has_tail(t, t.kb1 - 1)) {
+                ok = warp_wait<CG>(landed + st, seen >> st & 1, p.status);
                 if (!ok) break;
-                tc_fence_after();
-                const uint32_t acc = tmem + buf * R::ACC;
-                for (int kb = piece; kb < piece_end; ++kb) {
-                    ok = warp_wait(full + st, ph, p.status);
+                seen ^= 1u << st;
+                // rows past the segment's end belong to others: zero them up to the last step's end
+                const int boxes_a = (lanes_of(t) + 63) / 64, boxes = boxes_a + (share_of(columns_of(t)) + 63) / 64;
+                const int tail = t.rows & (KB - 1), zero = (16 - (t.rows & 15)) * 8;
+                for (int u = lane; u < zero * boxes; u += 32) {
+                    const int x = u / zero, q = u - x * zero;
+                    unsigned char* box = stages + st * R::STAGE + (x < boxes_a ? x * 8192 : PL * R::A_PLANE + (x - boxes_a) * 8192);
+                    *reinterpret_cast<uint4*>(box + tail * 128 + q * 16) = make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) lead_arrive<CG>(full + st, true);
+            }
+            if (++st == R::STAGES) st = 0;
+        }
+    } else if (warp == 0 && rank == 0) {
+        // ---- MMA ----
+        if (elect_one()) {
+            uint32_t st = 0, ph = 0, buf = 0, bph = 1;
+            bool ok = true;
+            const uint32_t type = p.type == PT_F16 ? 0 : 1;
+            // descriptors of the first stage; a step of 16 and a stage add to the address field
+            const uint32_t a_step = (a_outer ? 2048 : 32) >> 4, b_step = (b_outer ? 2048 : 32) >> 4;
+            const uint64_t a_desc = tc_smem_desc(smem_u32(stages), 8192);
+            const uint64_t b_desc = tc_smem_desc(smem_u32(stages) + PL * R::A_PLANE, 8192);
+            for (int64_t i = first; ok && i < items; i += stride) {
+                const Item t = item_at<MODE, NT, CG>(a, beg, pre, i);
+                const uint32_t idesc = tc_idesc(type, MT * CG, CG * share_of(columns_of(t)), a_outer, b_outer);
+                const int64_t sum = MODE == PRODUCT_WEIGHTS ? t.rows : p.K;
+                for (int piece = t.kb0; ok && piece < t.kb1; piece += a.flush) {
+                    const int piece_end = t.kb1 - piece < a.flush ? t.kb1 : piece + a.flush;
+                    ok = wait_for<CG>(acc_empty + buf, bph, p.status);
                     if (!ok) break;
                     tc_fence_after();
-                    const int64_t left = (MODE == PRODUCT_WEIGHTS ? t.rows : p.K) - int64_t(kb) * KB;
-                    const int steps = left >= KB ? 4 : static_cast<int>((left + 15) / 16);
-                    const uint32_t sa = smem_u32(stages + st * R::STAGE), sb = sa + PL * R::A_PLANE;
-                    if (MODE == PRODUCT_WEIGHTS && TENSOR && left < steps * 16) {
-                        // rows past the segment's end belong to others: zero them up to the last step's end
-                        const int tail = static_cast<int>(left), zero = (steps * 16 - tail) * 8;
-                        const int boxes_a = (m_left + 63) / 64, boxes = boxes_a + (n_left + 63) / 64;
-                        for (int u = lane; u < zero * boxes; u += 32) {
-                            const int x = u / zero, q = u - x * zero;
-                            unsigned char* box = stages + st * R::STAGE + (x < boxes_a ? x * 8192 : PL * R::A_PLANE + (x - boxes_a) * 8192);
-                            *reinterpret_cast<uint4*>(box + tail * 128 + q * 16) = make_uint4(0, 0, 0, 0);
-                        }
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                    }
-                    if (lane == 0) {
-                        for (int k = 0; k < steps; ++k) {
+                    const uint32_t acc = tmem + buf * R::ACC;
+                    for (int kb = piece; kb < piece_end; ++kb) {
+                        ok = wait_for<CG>(full + st, ph, p.status);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const int64_t left = sum - int64_t(kb) * KB;
+                        const uint64_t da = a_desc + st * (R::STAGE >> 4), db = b_desc + st * (R::STAGE >> 4);
+#pragma unroll
+                        for (int k = 0; k < KB / 16; ++k) {
+                            if (k > 0 && k * 16 >= left) break;
                             const bool add = kb > piece || k > 0;
                             if constexpr (PL == 1) {
-                                tc_mma(acc, tc_smem_desc(sa + k * a_step, 8192), tc_smem_desc(sb + k * b_step, 8192), idesc, add);
+                                tc_mma<CG>(acc, da + k * a_step, db + k * b_step, idesc, add);
                             } else {
                                 // the products of parts: the largest alone, the others together
                                 constexpr int pa[6] = {0, 2, 0, 1, 1, 0}, pb[6] = {0, 0, 2, 1, 0, 1};
 #pragma unroll
                                 for (int q = 0; q < 6; ++q)
-                                    tc_mma(q == 0 ? acc : acc + NT, tc_smem_desc(sa + pa[q] * R::A_PLANE + k * a_step, 8192),
-                                           tc_smem_desc(sb + pb[q] * R::B_PLANE + k * b_step, 8192), idesc, add || q > 1);
+                                    tc_mma<CG>(q == 0 ? acc : acc + NT, da + pa[q] * (R::A_PLANE >> 4) + k * a_step,
+                                               db + pb[q] * (R::B_PLANE >> 4) + k * b_step, idesc, add || q > 1);
                             }
                         }
-                        tc_commit(empty + st);
-                        if (kb + 1 == piece_end) tc_commit(acc_full + buf);
+                        tc_commit<CG>(empty + st);
+                        if (kb + 1 == piece_end) tc_commit<CG>(acc_full + buf);
+                        if (++st == R::STAGES) {
+                            st = 0;
+                            ph ^= 1;
+                        }
                     }
-                    __syncwarp();
-                    if (++st == R::STAGES) {
-                        st = 0;
-                        ph ^= 1;
-                    }
+                    if ((buf ^= 1) == 0) bph ^= 1;
                 }
-                if ((buf ^= 1) == 0) bph ^= 1;
             }
-        }
-        // nothing of this CTA's MMAs is in flight when its memory goes away
-        if (lane == 0) {
-            tc_commit(drain);
-            wait_bounded(drain, 0, p.status, STATUS_PRODUCT_TIMEOUT);
+            // no MMA is in flight when the memory goes away
+            tc_commit<CG>(drain, false);
+            wait_for<CG>(drain, 0, p.status);
         }
         __syncwarp();
     } else if (warp >= EPI_WARP && warp < EPI_WARP + 4) {
@@ -569,11 +630,12 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
             }
         }
         uint32_t buf = 0, bph = 0;
-        for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
-            const Item t = item_at<MODE, NT>(a, beg, pre, i);
+        for (int64_t i = first; i < items; i += stride) {
+            const Item t = item_at<MODE, NT, CG>(a, beg, pre, i);
             const bool summed = t.kb1 > t.kb0;
-            const int n_left = MODE == PRODUCT_WEIGHTS ? static_cast<int>(a.cols_n - t.n0 < NT ? a.cols_n - t.n0 : NT) : t.rows;
-            const int64_t m = t.m0 + t128;
+            const int n_left = columns_of(t);
+            const int64_t m = t.m0 + rank * MT + t128;
+            const int64_t slot = (t.slot * CG + rank) * NT * MT;      // in floats
             if constexpr (MODE == PRODUCT_ADAPTERS) {
                 bar_drain();       // the table of the tile before has been read
                 for (int r = t128; r < t.rows; r += 128) {
@@ -594,9 +656,9 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
             bool ok = true;
             int piece = t.kb0;
             do {
-                const bool first = piece == t.kb0, final = t.kb1 - piece <= a.flush;
+                const bool fresh = piece == t.kb0, final = t.kb1 - piece <= a.flush;
                 if (summed) {
-                    ok = bar_drain_all(wait_bounded(acc_full + buf, bph, p.status, STATUS_PRODUCT_TIMEOUT));
+                    ok = bar_drain_all(wait_for<CG>(acc_full + buf, bph, p.status));
                     if (!ok) break;
                     tc_fence_after();
                 }
@@ -604,7 +666,7 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                 // where the tile goes: its result, or (a part of a split sum) scratch
                 const bool partial = t.parts > 1;
                 const int64_t step = partial ? MT : (MODE == PRODUCT_WEIGHTS ? a.cols_m : p.ldo);
-                const int64_t at = partial ? t.slot * NT * MT + t128
+                const int64_t at = partial ? slot + t128
                                            : (MODE == PRODUCT_WEIGHTS ? (t.seg * a.cols_n + t.n0) * a.cols_m : t.row0 * p.ldo) + m;
                 for (int c = 0; c < n_left; c += 32) {
                     float v[32];
@@ -620,7 +682,7 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
 #pragma unroll
                         for (int j = 0; j < 32; ++j) v[j] = 0.0f;
                     }
-                    if (!first && (partial || m < a.cols_m)) {
+                    if (!fresh && (partial || m < a.cols_m)) {
                         // the sum so far, float32 wherever there is more than one piece
                         const float* so_far = (partial ? a.partials : static_cast<const float*>(p.out)) + at + c * step;
 #pragma unroll
@@ -637,7 +699,7 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                 if (summed) {
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(acc_empty + buf);
+                    if (lane == 0) lead_arrive<CG>(acc_empty + buf, false);
                     if ((buf ^= 1) == 0) bph ^= 1;
                 }
                 piece = final ? t.kb1 : piece + a.flush;
@@ -647,7 +709,7 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                 __threadfence();
                 bar_drain();
                 if (t128 == 0) {
-                    unsigned long long* ticket = a.tickets + t.ticket;
+                    unsigned long long* ticket = a.tickets + t.ticket * CG + rank;
                     red_max_relaxed_gpu(ticket, static_cast<unsigned long long>(p.gen) << 32);
                     const unsigned long long old = atom_add_release_gpu(ticket, 1);
                     fence_acq_rel_gpu();
@@ -661,7 +723,7 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
 #pragma unroll
                         for (int j = 0; j < 32; ++j) v[j] = 0.0f;
                         for (int q = 0; q < t.parts; ++q) {
-                            const float* part = a.partials + ((t.slot - t.part + q) * NT + c) * MT + t128;
+                            const float* part = a.partials + slot + (int64_t(q - t.part) * CG * NT + c) * MT + t128;
 #pragma unroll
                             for (int j = 0; j < 32; ++j)
                                 if (c + j < n_left) v[j] += __ldcg(part + j * MT);
@@ -675,9 +737,10 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
         tc_fence_before();
     }
     __syncthreads();
+    if (CG == 2) cluster_sync();      // the other CTA's MMAs and copies use this one's memory
     if (warp == 0) {
         tc_fence_after();
-        tmem_free(tmem, 2 * R::ACC);
+        tmem_free<CG>(tmem, 2 * R::ACC);
     }
 }
 
@@ -688,7 +751,7 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
 // is a function of the number of parts alone.
 constexpr int ADD_COLS = 16;
 
-template <int NT>
+template <int NT, int CG>
 __global__ void __launch_bounds__(256) add_parts_kernel(const __grid_constant__ KernelArgs a) {
     __shared__ float4 part_sum[8][32];
     const ProductParams& p = a.p;
@@ -703,11 +766,12 @@ __global__ void __launch_bounds__(256) add_parts_kernel(const __grid_constant__ 
     const int64_t b = offset_at(p, lo), e = offset_at(p, lo + 1);
     if (b / a.chunk != j || e - b <= a.chunk) return;
     const int parts = static_cast<int>((e - b + a.chunk - 1) / a.chunk);
-    const int64_t m = r % a.mtiles * MT + lane * 4;
+    const int rank = blockIdx.z;
+    const int64_t m = (r % a.mtiles * CG + rank) * MT + lane * 4;
     const int n0 = r / a.mtiles * NT;
     auto part = [&](int q, int c) {
         const int64_t slot = (2 * (j + q) + (q == 0 ? 1 : 0)) * per + r;
-        return __ldcg(reinterpret_cast<const float4*>(a.partials + (slot * NT + c) * MT) + lane);
+        return __ldcg(reinterpret_cast<const float4*>(a.partials + ((slot * CG + rank) * NT + c) * MT) + lane);
     };
     auto add = [](float4& x, const float4& y) { x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w; };
     auto put = [&](int c, const float4& v) {
@@ -779,7 +843,7 @@ bool tensor_copyable(const void* base, int64_t stride) {
     return reinterpret_cast<uintptr_t>(base) % 16 == 0 && stride % 8 == 0 && stride < (int64_t(1) << 38);
 }
 
-template <int MODE, bool TENSOR, int NT, int PL>
+template <int MODE, bool TENSOR, int NT, int PL, int CG>
 cudaError_t launch_shape(const KernelArgs& a, const ProductPlan& plan, cudaStream_t stream) {
     CUtensorMap ma{}, mb{};
     int dev = 0;
@@ -808,20 +872,37 @@ cudaError_t launch_shape(const KernelArgs& a, const ProductPlan& plan, cudaStrea
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
-    auto* kernel = product_kernel<MODE, TENSOR, NT, PL>;
-    constexpr int smem = Ring<NT, PL>::SMEM;
-    static uint64_t configured = 0;     // a bit per device; callers hold the library's lock
-    if (!(configured >> dev & 1)) {
+    auto* kernel = product_kernel<MODE, TENSOR, NT, PL, CG>;
+    constexpr int smem = Ring<NT, PL, CG>::SMEM;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = CG;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(plan.grid);
+    cfg.blockDim = dim3(TENSOR ? 256 : 512);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = CG > 1 ? 1 : 0;
+    static int resident[64] = {};       // most CTAs at a time, per device; callers hold the library's lock
+    if (resident[dev] == 0) {
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
-        configured |= uint64_t(1) << dev;
+        int clusters = a.p.sms;
+        if (CG > 1) {
+            e = cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg);
+            if (e != cudaSuccess) return e;
+            if (clusters < 1) return cudaErrorInvalidConfiguration;
+        }
+        resident[dev] = clusters * CG;
     }
-    kernel<<<plan.grid, TENSOR ? 256 : 512, smem, stream>>>(a, ma, mb);
-    e = cudaGetLastError();
+    cfg.gridDim = dim3(std::min(plan.grid, resident[dev]));
+    e = cudaLaunchKernelEx(&cfg, kernel, a, ma, mb);
     if (e != cudaSuccess || plan.add_blocks == 0) return e;
     if constexpr (MODE == PRODUCT_WEIGHTS) {
         const int64_t cols = std::min<int64_t>(a.cols_n, NT);
-        add_parts_kernel<NT><<<dim3(plan.add_blocks, static_cast<unsigned>(ceil_to(cols, ADD_COLS))), 256, 0, stream>>>(a);
+        add_parts_kernel<NT, CG><<<dim3(plan.add_blocks, static_cast<unsigned>(ceil_to(cols, ADD_COLS)), CG), 256, 0, stream>>>(a);
         e = cudaGetLastError();
     }
     return e;
@@ -830,10 +911,11 @@ cudaError_t launch_shape(const KernelArgs& a, const ProductPlan& plan, cudaStrea
 template <int MODE>
 cudaError_t launch_mode(const KernelArgs& a, const ProductPlan& plan, cudaStream_t stream) {
     if (a.p.type == PT_F32)
-        return plan.narrow ? launch_shape<MODE, false, 64, 3>(a, plan, stream) : launch_shape<MODE, false, 128, 3>(a, plan, stream);
-    if (plan.tensor)
-        return plan.narrow ? launch_shape<MODE, true, 64, 1>(a, plan, stream) : launch_shape<MODE, true, 256, 1>(a, plan, stream);
-    return plan.narrow ? launch_shape<MODE, false, 64, 1>(a, plan, stream) : launch_shape<MODE, false, 256, 1>(a, plan, stream);
+        return plan.narrow ? launch_shape<MODE, false, 64, 3, 1>(a, plan, stream) : launch_shape<MODE, false, 128, 3, 1>(a, plan, stream);
+    if (!plan.tensor)
+        return plan.narrow ? launch_shape<MODE, false, 64, 1, 1>(a, plan, stream) : launch_shape<MODE, false, 256, 1, 1>(a, plan, stream);
+    if (plan.narrow) return launch_shape<MODE, true, 64, 1, 1>(a, plan, stream);
+    return plan.pair ? launch_shape<MODE, true, 256, 1, 2>(a, plan, stream) : launch_shape<MODE, true, 256, 1, 1>(a, plan, stream);
 }
 
 int tile_columns(const ProductParams& p, bool narrow) { return narrow ? 64 : (p.type == PT_F32 ? 128 : 256); }
@@ -850,7 +932,10 @@ ProductPlan plan_product(int mode, const ProductParams& p) {
     // few rows per segment: small tiles and a deeper ring; weights: few columns of x
     d.narrow = weights ? p.K <= 64 : p.R <= 64 * segments;
     const int NT = tile_columns(p, d.narrow);
-    d.mtiles = static_cast<int32_t>(ceil_to(p.N, MT));
+    // two CTAs on a tile of twice the lanes, unless that leaves one of them without lanes
+    d.pair = d.tensor && !d.narrow && (p.N > 1024 || ceil_to(p.N, MT) % 2 == 0);
+    const int cg = d.pair ? 2 : 1;
+    d.mtiles = static_cast<int32_t>(ceil_to(p.N, MT * cg));
     d.ntiles = weights ? static_cast<int32_t>(ceil_to(p.K, NT)) : 1;
     d.parts = 1;
     d.part_blocks = static_cast<int32_t>(ceil_to(p.K, KB));
@@ -860,8 +945,8 @@ ProductPlan plan_product(int mode, const ProductParams& p) {
         const int64_t per = int64_t(d.mtiles) * d.ntiles;
         // parts of at least so many rows that storing a part costs a fraction of them
         const int64_t least = 8 * std::min<int64_t>(p.K, NT);
-        if (segments * per < 8 * p.sms) {
-            const int64_t chunk = std::max(least, ceil_to(ceil_to(p.R * per, 4 * p.sms), KB) * KB);
+        if (segments * per * cg < 8 * p.sms) {
+            const int64_t chunk = std::max(least, ceil_to(ceil_to(p.R * per * cg, 4 * p.sms), KB) * KB);
             if (chunk < p.R) {
                 d.chunk = chunk;
                 d.add_blocks = static_cast<int32_t>((p.R / chunk + 1) * per);
@@ -872,18 +957,18 @@ ProductPlan plan_product(int mode, const ProductParams& p) {
     } else {
         d.row_tiles = mode == PRODUCT_ADAPTERS ? ceil_to(p.R, NT) : std::min(segments, p.R) + p.R / NT;
         items = d.row_tiles * d.mtiles;
-        if (items * 2 <= p.sms && d.part_blocks >= 8) {
-            const int64_t parts = std::min<int64_t>(p.sms / items, d.part_blocks / 4);
+        if (items * cg * 2 <= p.sms && d.part_blocks >= 8) {
+            const int64_t parts = std::min<int64_t>(p.sms / (items * cg), d.part_blocks / 4);
             d.part_blocks = static_cast<int32_t>(ceil_to(d.part_blocks, parts));
             d.parts = static_cast<int32_t>(ceil_to(ceil_to(p.K, KB), d.part_blocks));
             if (d.parts > 1) slots = items * d.parts;
             items *= d.parts;
         }
     }
-    d.grid = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(items, p.sms)));
+    d.grid = static_cast<int32_t>(std::max<int64_t>(cg, std::min<int64_t>(items * cg, p.sms / cg * cg)));
     d.ticket_bytes = PRODUCT_TICKETS * 8;
     d.prefix_bytes = mode != PRODUCT_ADAPTERS && p.S > NEAR_SEGMENTS ? ceil_to((p.S + 1) * 8, 256) * 256 : 0;
-    d.partial_bytes = slots * NT * MT * 4;
+    d.partial_bytes = slots * cg * NT * MT * 4;
     return d;
 }
 

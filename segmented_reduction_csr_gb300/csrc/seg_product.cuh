@@ -44,6 +44,7 @@ struct ProductPlan {
     int32_t grid;
     int32_t tensor;         // 1: operands come by tensor copies, 0: by the loader warps
     int32_t narrow;         // 1: at most 64 rows per tile and a deeper ring
+    int32_t pair;           // 1: two CTAs share a tile
     int32_t mtiles, ntiles; // tiles of the output's contiguous / other dimension (forward: rows vary by segment)
     int32_t parts;          // forward: parts of the contraction
     int32_t part_blocks;    // forward: 64-wide blocks per part
