@@ -243,7 +243,9 @@ seg_status_t run_product(int mode, ProductParams p, cudaStream_t stream, Scratch
     p.status = ds->status;
     p.ws = static_cast<unsigned char*>(sc->ptr);
     p.gen = ++sc->gen;
-    if (launch_product(mode, p, plan_product(mode, p), stream) != cudaSuccess) {
+    const ProductPlan plan = plan_product(mode, p);
+    if (plan.too_many) return SEG_ERR_UNSUPPORTED;
+    if (launch_product(mode, p, plan, stream) != cudaSuccess) {
         cudaGetLastError();
         return SEG_ERR_CUDA;
     }

@@ -44,8 +44,9 @@ namespace {
 constexpr int KB = 64;                    // steps of the sum per stage: 128-byte rows of 16-bit values
 constexpr int MT = 128;                   // lanes of a tile
 constexpr int NEAR_SEGMENTS = 1024;       // up to here every CTA keeps the offsets in shared memory
-constexpr int EPI_WARP = 4;               // warps 4..7 drain (their index mod 4 names their lanes)
-constexpr int LOAD_WARP = 8, LOAD_WARPS = 8;
+constexpr int EPI_WARP = 4;               // the drain warps start here (their index mod 4 names their lanes)
+constexpr int LOAD_WARP = 8, LOAD_GROUP = 4;   // loader warps: two groups of four that take turns at the stages
+constexpr int STAGING = 2048;             // bytes of a drain warp's own shared memory
 constexpr int NEVER_FLUSH = 1 << 28;         // more blocks than any sum has
 constexpr unsigned STATUS_PRODUCT_TIMEOUT = 8u;
 
@@ -54,17 +55,21 @@ template <int NT, int PL, int CG>
 struct Ring {
     static constexpr int A_PLANE = MT * 128, B_PLANE = NT / CG * 128;
     static constexpr int STAGE = PL * (A_PLANE + B_PLANE);
-    static constexpr int STAGES = std::min(8, 221184 / STAGE);
+    static constexpr int STAGES = std::min(8, (PL == 1 ? 200704 : 221184) / STAGE);
     static constexpr int ACC = PL == 1 ? NT : 2 * NT;            // tensor-memory columns of one accumulator
     static constexpr int BARS = 3 * STAGES + 5;
-    static constexpr int FIXED = 2 * (NEAR_SEGMENTS + 1) * 4 + BARS * 8 + 64 + NT * 4;
-    static constexpr int SMEM = STAGES * STAGE + FIXED + 1024;   // 1024: alignment of the stages
+    // the drain warps' staging; PL == 3 keeps it (adapters alone need it there) in the space of the offsets
+    static constexpr int STAGED = PL == 1 ? 8 * STAGING : 0;
+    static constexpr int NEAR = 2 * (NEAR_SEGMENTS + 1) * 4;
+    static_assert(NEAR >= 4 * STAGING, "room for the staging of four warps");
+    static constexpr int SMEM = STAGES * STAGE + STAGED + NEAR + BARS * 8 + 64 + NT * 4 + 1024;   // 1024: alignment of the stages
     static_assert(SMEM <= 232448, "shared memory of an SM");
 };
 
 struct KernelArgs {
     ProductParams p;
     int32_t mtiles, ntiles, parts, part_blocks, kblocks;
+    int32_t wide_rows;  // 16-bit results: 16-byte stores fit
     int32_t flush;      // blocks of the sum after which the accumulators go to the result
     int64_t chunk, row_tiles, cols_m, cols_n;   // cols_*: extent of the tile dimensions (forward: cols_n unused)
     unsigned long long* tickets;
@@ -128,7 +133,7 @@ __global__ void __launch_bounds__(1024) prefix_kernel(const __grid_constant__ Ke
 }
 
 struct Item {
-    int seg;
+    int seg = 0;
     int row0, rows;     // forward: the tile's rows; weights: the rows it sums over
     int m0, n0;
     int kb0, kb1;       // 64-wide blocks of the sum
@@ -136,21 +141,22 @@ struct Item {
     int64_t slot, ticket;
 };
 
+// Item i; `t` holds the item before it (seg 0 at the start): a CTA's items
+// come in order, so its segments are found by going on from there.
 template <int MODE, int NT, int CG>
-__device__ __forceinline__ Item item_at(const KernelArgs& a, const int* beg, const int* pre, int64_t i) {
-    Item t;
+__device__ __forceinline__ void item_at(const KernelArgs& a, const int* beg, const int* pre, uint32_t i, Item& t) {
     int q;
+    const uint32_t mtiles = a.mtiles;
     if (MODE == PRODUCT_WEIGHTS) {
-        const int per = a.mtiles * a.ntiles;
+        const uint32_t per = mtiles * a.ntiles, r = i % per;
         q = static_cast<int>(i / per);
-        const int r = static_cast<int>(i - int64_t(q) * per);
-        t.m0 = r % a.mtiles * (MT * CG);
-        t.n0 = r / a.mtiles * NT;
+        t.m0 = static_cast<int>(r % mtiles) * (MT * CG);
+        t.n0 = static_cast<int>(r / mtiles) * NT;
     } else {
-        const int64_t tile = i / a.parts;
+        const uint32_t tile = a.parts > 1 ? i / a.parts : i;
         t.part = static_cast<int>(i - tile * a.parts);
-        q = static_cast<int>(tile / a.mtiles);
-        t.m0 = static_cast<int>(tile - int64_t(q) * a.mtiles) * (MT * CG);
+        q = static_cast<int>(mtiles > 1 ? tile / mtiles : tile);
+        t.m0 = static_cast<int>(tile - q * mtiles) * (MT * CG);
         t.n0 = 0;
     }
     int b = 0, e = static_cast<int>(a.p.R), first = 0, count;
@@ -158,10 +164,14 @@ __device__ __forceinline__ Item item_at(const KernelArgs& a, const int* beg, con
         t.seg = 0;
         count = static_cast<int>(a.row_tiles);
     } else {
-        int lo = 0, hi = static_cast<int>(a.p.S);   // the last segment whose items start at or before q
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (pre[mid] <= q) lo = mid; else hi = mid;
+        int lo = t.seg;                             // the last segment whose items start at or before q
+        for (int k = 0; k < 4 && pre[lo + 1] <= q; ++k) ++lo;
+        if (pre[lo + 1] <= q) {
+            int hi = static_cast<int>(a.p.S);
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (pre[mid] <= q) lo = mid; else hi = mid;
+            }
         }
         t.seg = lo;
         b = beg[lo];
@@ -196,18 +206,19 @@ __device__ __forceinline__ Item item_at(const KernelArgs& a, const int* beg, con
         t.slot = i;
         t.ticket = i / a.parts;
     }
-    return t;
 }
 
-__device__ __forceinline__ void bar_drain() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
-// The same, and whether `ok` holds in all four warps: they give up together or not at all.
+template <int EPW>
+__device__ __forceinline__ void bar_drain() { asm volatile("bar.sync 1, %0;" ::"n"(EPW * 32) : "memory"); }
+// The same, and whether `ok` holds in all the drain warps: they give up together or not at all.
+template <int EPW>
 __device__ __forceinline__ bool bar_drain_all(bool ok) {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.and.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        "barrier.cta.red.and.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(r)
-        : "r"(ok ? 1u : 0u)
+        : "r"(ok ? 1u : 0u), "n"(EPW * 32)
         : "memory");
     return r != 0;
 }
@@ -233,61 +244,158 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, unsign
     return __all_sync(0xffffffffu, wait_for<CG>(bar, parity, status));
 }
 
-__device__ __forceinline__ float value_at(const void* base, int64_t i, int type) {
-    if (type == PT_F32) return __ldg(static_cast<const float*>(base) + i);
-    if (type == PT_F16) return __half2float(static_cast<const __half*>(base)[i]);
-    return __bfloat162float(static_cast<const __nv_bfloat16*>(base)[i]);
-}
-
-// Stores one tile column group: value i to row `at + i * step` of `out` for i < n.
-__device__ __forceinline__ void store_rows(void* out, int type, int64_t at, int64_t step, const float (&v)[32], int n) {
-    if (type == PT_F32) {
-        float* o = static_cast<float*>(out) + at;
+// Value i of every lane to row i of `out`, rows `step` apart, for i < n.
+template <class T, int W, class F>
+__device__ __forceinline__ void store_rows(T* out, int64_t step, const float (&v)[W], int n, F narrow) {
+    if (n >= W) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (i < n) o[i * step] = v[i];
-    } else if (type == PT_F16) {
-        __half* o = static_cast<__half*>(out) + at;
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (i < n) o[i * step] = __float2half_rn(v[i]);
+        for (int i = 0; i < W; i += 4) {
+            T* o = out + i * step;
+            o[0] = narrow(v[i]);
+            o[step] = narrow(v[i + 1]);
+            o[2 * step] = narrow(v[i + 2]);
+            o[3 * step] = narrow(v[i + 3]);
+        }
     } else {
-        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(out) + at;
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (i < n) o[i * step] = __float2bfloat16_rn(v[i]);
+        for (int i = 0; i < W; ++i)
+            if (i < n) out[i * step] = narrow(v[i]);
     }
 }
 
-// What is left to do to finished sums: the scale of an indexed matrix, or the
-// adapters' low-rank part.  v[j] is row c + j of the tile, column m.
-template <int MODE>
-__device__ __forceinline__ void finish(const ProductParams& p, float (&v)[32], int c, int rows, const Item& t,
-                                       const int* tile_adapter, int64_t m, float factor) {
-    if constexpr (MODE == PRODUCT_FORWARD) {
-        if (p.scale)
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] *= factor;
+__device__ __forceinline__ uint32_t narrow_pair(float a, float b, int type) {
+    uint32_t r;
+    if (type == PT_F16) asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(r) : "f"(a), "f"(b));
+    else asm("cvt.rn.bf16x2.f32 %0, %2, %1;" : "=r"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// W columns of the tile of this warp's 32 lanes to the result: `at` is lane
+// 0's place in the first of n rows.  16-bit rows that allow it are turned in
+// the warp's staging (rows of 64 bytes) and leave 16 bytes per thread: a
+// store of 2 bytes per lane took 70 cycles a row.
+template <int W>
+__device__ __forceinline__ void store_result(const KernelArgs& a, int64_t at, int64_t step, const float (&v)[W], int n,
+                                             int lanes, int lane, unsigned char* staging) {
+    const int type = a.p.out_type;
+    if (type == PT_F32) {
+        if (lane < lanes) store_rows(static_cast<float*>(a.p.out) + at + lane, step, v, n, [](float x) { return x; });
+        return;
     }
-    if constexpr (MODE == PRODUCT_ADAPTERS) {
-        for (int q = 0; q < p.rank; q += 8) {
-            const int width = static_cast<int>(p.rank - q < 8 ? p.rank - q : 8);
-            float bv[8];
-            int have = -1;
+    if (!a.wide_rows) {
+        if (lane >= lanes) return;
+        uint16_t* o = static_cast<uint16_t*>(a.p.out) + at + lane;
+        store_rows(o, step, v, n, [type](float x) { return static_cast<uint16_t>(narrow_pair(x, 0.0f, type)); });
+        return;
+    }
+    uint16_t* s = reinterpret_cast<uint16_t*>(staging) + lane;
+    __syncwarp();
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-                const int l = c + j < rows ? tile_adapter[c + j] : -1;
+    for (int i = 0; i < W; i += 2) {
+        const uint32_t two = narrow_pair(v[i], v[i + 1], type);
+        s[i * 32] = static_cast<uint16_t>(two);
+        s[i * 32 + 32] = static_cast<uint16_t>(two >> 16);
+    }
+    __syncwarp();
+    const int unit = lane & 3;
+    uint16_t* o = static_cast<uint16_t*>(a.p.out) + at + unit * 8;
+#pragma unroll
+    for (int i = 0; i < W / 8; ++i) {
+        const int row = i * 8 + (lane >> 2);
+        if (row < n && unit * 8 < lanes) *reinterpret_cast<uint4*>(o + row * step) = *reinterpret_cast<const uint4*>(staging + row * 64 + unit * 16);
+    }
+}
+
+// The adapters' part of 8 rows of this lane's column m, by the float32 pipes
+// while the tensor cores work on: v[j] = sum_k u[row c + j, k] b[l_j, m, k].
+// 16 ranks at a time: the rows' u go through the warp's staging, b straight
+// to the registers of the column's lane, for several rows before the first
+// is used (a decode step has another adapter in every row).
+template <int PL>
+__device__ __forceinline__ void low_rank(const ProductParams& p, float (&v)[8], int row0, int c, int rows,
+                                         const int* tile_adapter, int64_t m, int lane, unsigned char* staging) {
+    constexpr int AHEAD = PL == 1 ? 8 : 2;
+    constexpr int UNITS = PL == 1 ? 2 : 4;               // of 16 bytes, for 16 ranks
+    const int rank = static_cast<int>(p.rank);
+    const bool vec_b = rank % (PL == 1 ? 8 : 4) == 0 && (reinterpret_cast<uintptr_t>(p.b) & 15) == 0;
+    float4* su = reinterpret_cast<float4*>(staging);     // [8 rows][4]
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+    const int row = lane >> 2, unit = lane & 3;          // of u, this lane's to fetch
+    const int mine = c + row < rows ? tile_adapter[c + row] : -1;
+    if (!__any_sync(0xffffffffu, mine >= 0)) return;
+    for (int q = 0; q < rank; q += 16) {
+        const int width = rank - q < 16 ? rank - q : 16;
+        float4 uv = make_float4(0, 0, 0, 0);
+        if (mine >= 0 && unit * 4 < width) {
+            const float* u = p.u + (int64_t(row0) + c + row) * rank + q + unit * 4;
+            if (rank % 4 == 0) {
+                uv = __ldg(reinterpret_cast<const float4*>(u));
+            } else {
+                uv.x = __ldg(u);
+                if (unit * 4 + 1 < width) uv.y = __ldg(u + 1);
+                if (unit * 4 + 2 < width) uv.z = __ldg(u + 2);
+                if (unit * 4 + 3 < width) uv.w = __ldg(u + 3);
+            }
+        }
+        __syncwarp();
+        su[lane] = uv;
+        __syncwarp();
+        float bf[16];
+        int have = -1;
+#pragma unroll
+        for (int j0 = 0; j0 < 8; j0 += AHEAD) {
+            uint32_t raw[AHEAD][UNITS * 4];
+            int before = have;
+#pragma unroll
+            for (int j = 0; j < AHEAD; ++j) {
+                const int l = __shfl_sync(0xffffffffu, mine, (j0 + j) * 4);
+                if (l < 0 || l == before) continue;
+                before = l;
+#pragma unroll
+                for (int k = 0; k < UNITS * 4; ++k) raw[j][k] = 0;
+                if (m >= p.N) continue;
+                const int64_t at = (int64_t(l) * p.N + m) * rank + q;
+                if (vec_b) {
+                    const uint4* b = reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(p.b) + at * (PL == 1 ? 2 : 4));
+#pragma unroll
+                    for (int k = 0; k < UNITS; ++k)
+                        if (k * (PL == 1 ? 8 : 4) < width) {
+                            const uint4 x = __ldg(b + k);
+                            raw[j][4 * k] = x.x, raw[j][4 * k + 1] = x.y, raw[j][4 * k + 2] = x.z, raw[j][4 * k + 3] = x.w;
+                        }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        if (k >= width) continue;
+                        if constexpr (PL == 1) raw[j][k / 2] |= static_cast<uint32_t>(__ldg(static_cast<const uint16_t*>(p.b) + at + k)) << (k % 2 * 16);
+                        else raw[j][k] = __ldg(static_cast<const uint32_t*>(p.b) + at + k);
+                    }
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < AHEAD; ++j) {
+                const int l = __shfl_sync(0xffffffffu, mine, (j0 + j) * 4);
                 if (l < 0) continue;
                 if (l != have) {
                     have = l;
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        bv[k] = k < width ? value_at(p.b, (int64_t(l) * p.N + m) * p.rank + q + k, p.type) : 0.0f;
+                    for (int k = 0; k < 16; ++k) {
+                        if constexpr (PL == 3) bf[k] = __uint_as_float(raw[j][k]);
+                        else if (p.type == PT_BF16) bf[k] = __uint_as_float(k % 2 ? raw[j][k / 2] & 0xffff0000u : raw[j][k / 2] << 16);
+                        else bf[k] = __half2float(__ushort_as_half(static_cast<uint16_t>(k % 2 ? raw[j][k / 2] >> 16 : raw[j][k / 2])));
+                    }
                 }
-                const float* u = p.u + (int64_t(t.row0) + c + j) * p.rank + q;
+                float s = v[j0 + j], s2 = 0.0f;
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (k < width) v[j] += __ldg(u + k) * bv[k];
+                for (int k = 0; k < 4; ++k) {
+                    const float4 x = su[(j0 + j) * 4 + k];
+                    s = fmaf(x.x, bf[4 * k], s);
+                    s2 = fmaf(x.y, bf[4 * k + 1], s2);
+                    s = fmaf(x.z, bf[4 * k + 2], s);
+                    s2 = fmaf(x.w, bf[4 * k + 3], s2);
+                }
+                v[j0 + j] = s + s2;
             }
         }
     }
@@ -351,21 +459,21 @@ __device__ __forceinline__ void load_unit(const Box& x, int row, int unit, uint4
     }
 }
 
-// `units` (8 per row) of a box into `dst`, planes `plane` bytes apart, by the loader's 256 threads.
+// `units` (8 per row) of a box into `dst`, planes `plane` bytes apart, by a loader group's 128 threads.
 template <int PL>
 __device__ __forceinline__ void load_box(const Box& x, int units, unsigned char* dst, int plane) {
     constexpr int AHEAD = 4;
-    const int t = threadIdx.x - LOAD_WARP * 32;
-    for (int u0 = t; u0 < units; u0 += AHEAD * LOAD_WARPS * 32) {
+    const int t = threadIdx.x & (LOAD_GROUP * 32 - 1);
+    for (int u0 = t; u0 < units; u0 += AHEAD * LOAD_GROUP * 32) {
         uint4 v[AHEAD][PL];
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
-            const int u = u0 + i * LOAD_WARPS * 32;
+            const int u = u0 + i * LOAD_GROUP * 32;
             if (u < units) load_unit<PL>(x, u >> 3, u & 7, v[i]);
         }
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
-            const int u = u0 + i * LOAD_WARPS * 32;
+            const int u = u0 + i * LOAD_GROUP * 32;
             if (u < units)
 #pragma unroll
                 for (int k = 0; k < PL; ++k) *reinterpret_cast<uint4*>(dst + k * plane + swizzled(u >> 3, u & 7)) = v[i][k];
@@ -376,15 +484,18 @@ __device__ __forceinline__ void load_box(const Box& x, int units, unsigned char*
 // ---------------------------------------------------------------------------
 
 template <int MODE, bool TENSOR, int NT, int PL, int CG>
-__global__ void __launch_bounds__(TENSOR ? 256 : 512, 1)
+__global__ void __launch_bounds__(TENSOR ? 384 : 512, 1)
 product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUtensorMap map_a,
                const __grid_constant__ CUtensorMap map_b) {
     using R = Ring<NT, PL, CG>;
     static_assert(CG == 1 || TENSOR, "pairs load by tensor copies");
     constexpr int BOX_ROWS = NT <= 64 ? 16 : 64;     // rows of one copy of x (forward)
+    constexpr int EPW = TENSOR ? 8 : 4;              // drain warps: pairs of them share lanes and take turns at the columns
     extern __shared__ unsigned char raw[];
     unsigned char* stages = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
-    uint64_t* full = reinterpret_cast<uint64_t*>(stages + R::STAGES * R::STAGE);   // CG == 2: CTA 0's count
+    unsigned char* staging = stages + R::STAGES * R::STAGE;      // 16-byte aligned, as all that follows it
+    int* near = reinterpret_cast<int*>(staging + R::STAGED);
+    uint64_t* full = reinterpret_cast<uint64_t*>(staging + R::STAGED + R::NEAR);   // CG == 2: CTA 0's count
     uint64_t* empty = full + R::STAGES;
     uint64_t* landed = empty + R::STAGES;          // a stage whose tail has to be zeroed has arrived
     uint64_t* acc_full = landed + R::STAGES;
@@ -393,11 +504,11 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
     uint32_t* tmem_at = reinterpret_cast<uint32_t*>(drain + 1);
     int* last_part = reinterpret_cast<int*>(tmem_at + 1);
     int* tile_adapter = reinterpret_cast<int*>(tmem_at + 16);    // [NT]
-    int* near = tile_adapter + NT;
+    if (PL > 1) staging = reinterpret_cast<unsigned char*>(near);
     const ProductParams& p = a.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = CG == 2 ? static_cast<int>(cluster_rank()) : 0;
-    const int64_t first = blockIdx.x / CG, stride = gridDim.x / CG;
+    const uint32_t first = blockIdx.x / CG, stride = gridDim.x / CG;
 
     const bool is_near = p.S <= NEAR_SEGMENTS;
     const int* beg = is_near ? near : a.far;
@@ -405,13 +516,13 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
     if (warp == 0) tmem_alloc<CG>(tmem_at, 2 * R::ACC);
     if (tid == 0) {
         for (int i = 0; i < R::STAGES; ++i) {
-            mbar_init(full + i, TENSOR ? CG : LOAD_WARPS);
+            mbar_init(full + i, TENSOR ? CG : LOAD_GROUP);
             mbar_init(empty + i, 1);
             mbar_init(landed + i, 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(acc_full + i, 1);
-            mbar_init(acc_empty + i, 4 * CG);
+            mbar_init(acc_empty + i, EPW * CG);
         }
         mbar_init(drain, 1);
         fence_mbarrier_init();
@@ -427,11 +538,11 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
     tc_fence_after();
     const uint32_t tmem = *tmem_at;
 
-    int64_t items;
+    uint32_t items;
     // (the caps: offsets that decrease name more items than there can be)
-    if (MODE == PRODUCT_WEIGHTS) items = min(int64_t(pre[p.S]), p.S + p.R / a.chunk) * (a.mtiles * a.ntiles);
-    else if (MODE == PRODUCT_ADAPTERS) items = a.row_tiles * a.mtiles * a.parts;
-    else items = (p.S > 0 ? min(int64_t(pre[p.S]), a.row_tiles) : 0) * a.mtiles * a.parts;
+    if (MODE == PRODUCT_WEIGHTS) items = static_cast<uint32_t>(min(int64_t(pre[p.S]), p.S + p.R / a.chunk) * (a.mtiles * a.ntiles));
+    else if (MODE == PRODUCT_ADAPTERS) items = static_cast<uint32_t>(a.row_tiles * a.mtiles * a.parts);
+    else items = static_cast<uint32_t>((p.S > 0 ? min(int64_t(pre[p.S]), a.row_tiles) : 0) * a.mtiles * a.parts);
     const bool a_outer = MODE == PRODUCT_WEIGHTS || !p.trans;    // the operand's contiguous dimension is m, not the sum
     constexpr bool b_outer = MODE == PRODUCT_WEIGHTS;
 
@@ -450,11 +561,13 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
     if (TENSOR ? warp == 1 : warp >= LOAD_WARP) {
         // ---- producer ----
         if (!TENSOR || elect_one()) {
-            uint32_t st = 0, ph = 1;
+            uint32_t st = 0, ph = 1, turn = 0;
             int64_t issued = 0;
+            int held_seg = -1, held_m0 = 0, held_kb = 0;     // the A operand that this group's stage holds (two stages)
             bool ok = true;
-            for (int64_t i = first; ok && i < items; i += stride) {
-                const Item t = item_at<MODE, NT, CG>(a, beg, pre, i);
+            Item t;
+            for (uint32_t i = first; ok && i < items; i += stride) {
+                item_at<MODE, NT, CG>(a, beg, pre, i, t);
                 const int columns = columns_of(t), share = share_of(columns), lanes = lanes_of(t);
                 const int a_boxes = a_outer ? (lanes + 63) / 64 : (lanes + MT - 1) / MT;
                 const int b_boxes = b_outer ? (share + 63) / 64 : (share + BOX_ROWS - 1) / BOX_ROWS;
@@ -470,6 +583,13 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                 int64_t m = t.seg;
                 if (MODE == PRODUCT_FORWARD && p.index) m = __ldg(p.index + t.seg);
                 for (int kb = t.kb0; kb < t.kb1; ++kb) {
+                    if (!TENSOR && static_cast<int>(turn++ & 1) != (warp - LOAD_WARP) / LOAD_GROUP) {
+                        if (++st == R::STAGES) {
+                            st = 0;
+                            ph ^= 1;
+                        }
+                        continue;
+                    }
                     ok = TENSOR ? wait_for<CG>(empty + st, ph, p.status) : warp_wait<CG>(empty + st, ph, p.status);
                     if (!ok) break;
                     unsigned char* sa = stages + st * R::STAGE;
@@ -508,7 +628,11 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                         } else {
                             const void* w = static_cast<const unsigned char*>(p.w) + m * p.stride_w * size;
                             const int64_t k = int64_t(kb) * KB;
-                            if (a_outer) {
+                            // a short sum over many tiles of a segment: its matrix is split and stored once
+                            const bool held = R::STAGES == 2 && held_seg == t.seg && held_m0 == t.m0 && held_kb == kb;
+                            held_seg = t.seg, held_m0 = t.m0, held_kb = kb;
+                            if (held) {
+                            } else if (a_outer) {
                                 for (int x = 0; x < a_boxes; ++x)
                                     load_box<PL>(Box{w, p.ldw, k, p.K, m0 + x * 64, a.cols_m}, KB * 8, sa + x * 8192, R::A_PLANE);
                             } else {
@@ -537,8 +661,9 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
         // ---- tails ----
         uint32_t st = 0, seen = 0;        // a parity per stage
         bool ok = true;
-        for (int64_t i = first; ok && i < items; i += stride) {
-            const Item t = item_at<MODE, NT, CG>(a, beg, pre, i);
+        Item t;
+        for (uint32_t i = first; ok && i < items; i += stride) {
+            item_at<MODE, NT, CG>(a, beg, pre, i, t);
             if (t.kb1 <= t.kb0) continue;
             st = (st + (t.kb1 - t.kb0 - 1)) % R::STAGES;
             if (has_tail(t, t.kb1 - 1)) {
@@ -569,8 +694,9 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
             const uint32_t a_step = (a_outer ? 2048 : 32) >> 4, b_step = (b_outer ? 2048 : 32) >> 4;
             const uint64_t a_desc = tc_smem_desc(smem_u32(stages), 8192);
             const uint64_t b_desc = tc_smem_desc(smem_u32(stages) + PL * R::A_PLANE, 8192);
-            for (int64_t i = first; ok && i < items; i += stride) {
-                const Item t = item_at<MODE, NT, CG>(a, beg, pre, i);
+            Item t;
+            for (uint32_t i = first; ok && i < items; i += stride) {
+                item_at<MODE, NT, CG>(a, beg, pre, i, t);
                 const uint32_t idesc = tc_idesc(type, MT * CG, CG * share_of(columns_of(t)), a_outer, b_outer);
                 const int64_t sum = MODE == PRODUCT_WEIGHTS ? t.rows : p.K;
                 for (int piece = t.kb0; ok && piece < t.kb1; piece += a.flush) {
@@ -615,30 +741,35 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
             wait_for<CG>(drain, 0, p.status);
         }
         __syncwarp();
-    } else if (warp >= EPI_WARP && warp < EPI_WARP + 4) {
+    } else if (warp >= EPI_WARP && warp < EPI_WARP + EPW) {
         // ---- drain ----
-        const int quarter = warp - EPI_WARP, t128 = quarter * 32 + lane;
+        const int quarter = (warp - EPI_WARP) & 3, group = (warp - EPI_WARP) / 4;   // which lanes; which columns
+        const int td = tid - EPI_WARP * 32;
+        constexpr int W = MODE == PRODUCT_ADAPTERS ? 8 : 32;      // columns at a time
+        staging += (warp - EPI_WARP) * STAGING;
         if (MODE == PRODUCT_FORWARD && !p.index) {
             // rows in no segment
             const int b = p.S > 0 ? beg[0] : 0, e = p.S > 0 ? beg[p.S] : 0;
             const int64_t none = b + (p.R - (e > b ? e : b));
-            const int64_t each = static_cast<int64_t>(gridDim.x) * 128;
-            for (int64_t i = blockIdx.x * 128 + t128; i < none * p.N; i += each) {
+            const int64_t each = static_cast<int64_t>(gridDim.x) * (EPW * 32);
+            for (int64_t i = blockIdx.x * (EPW * 32) + td; i < none * p.N; i += each) {
                 const int64_t q = i / p.N, c = i - q * p.N, r = q < b ? q : (e > b ? e : b) + (q - b);
                 if (p.out_type == PT_F32) static_cast<float*>(p.out)[r * p.ldo + c] = 0.0f;
                 else static_cast<uint16_t*>(p.out)[r * p.ldo + c] = 0;
             }
         }
         uint32_t buf = 0, bph = 0;
-        for (int64_t i = first; i < items; i += stride) {
-            const Item t = item_at<MODE, NT, CG>(a, beg, pre, i);
+        Item t;
+        for (uint32_t i = first; i < items; i += stride) {
+            item_at<MODE, NT, CG>(a, beg, pre, i, t);
             const bool summed = t.kb1 > t.kb0;
             const int n_left = columns_of(t);
-            const int64_t m = t.m0 + rank * MT + t128;
-            const int64_t slot = (t.slot * CG + rank) * NT * MT;      // in floats
+            const int64_t m = t.m0 + rank * MT + quarter * 32;           // the warp's first lane
+            const int lanes = static_cast<int>(a.cols_m - m < 32 ? a.cols_m - m : 32);   // may be negative
+            const int64_t slot = (t.slot * CG + rank) * NT * MT + quarter * 32 + lane;      // in floats
             if constexpr (MODE == PRODUCT_ADAPTERS) {
-                bar_drain();       // the table of the tile before has been read
-                for (int r = t128; r < t.rows; r += 128) {
+                bar_drain<EPW>();       // the table of the tile before has been read
+                for (int r = td; r < t.rows; r += EPW * 32) {
                     const int row = t.row0 + r;
                     int64_t lo = 0, hi = p.S;      // the last segment that starts at or before the row
                     while (hi - lo > 1) {
@@ -649,90 +780,109 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                     if (p.S > 0 && offset_at(p, lo) <= row && row < offset_at(p, lo + 1)) l = __ldg(p.index + lo);
                     tile_adapter[r] = l >= 0 && l < p.L ? l : -1;
                 }
-                bar_drain();
+                bar_drain<EPW>();
             }
             float factor = 1.0f;
             if (MODE == PRODUCT_FORWARD && p.scale) factor = __ldg(p.scale + __ldg(p.index + t.seg));
-            bool ok = true;
+            // where the tile goes: its result, or (a part of a split sum) scratch
+            const bool partial = t.parts > 1;
+            const int64_t step = MODE == PRODUCT_WEIGHTS ? a.cols_m : p.ldo;
+            const int64_t at = (MODE == PRODUCT_WEIGHTS ? (t.seg * a.cols_n + t.n0) * a.cols_m : t.row0 * p.ldo) + m;
+            bool ok = true, adding = false;      // adding: the last of a tile's parts adds them all
             int piece = t.kb0;
             do {
                 const bool fresh = piece == t.kb0, final = t.kb1 - piece <= a.flush;
-                if (summed) {
-                    ok = bar_drain_all(wait_for<CG>(acc_full + buf, bph, p.status));
-                    if (!ok) break;
-                    tc_fence_after();
-                }
+                const bool to_part = partial && !adding;
                 const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * R::ACC;
-                // where the tile goes: its result, or (a part of a split sum) scratch
-                const bool partial = t.parts > 1;
-                const int64_t step = partial ? MT : (MODE == PRODUCT_WEIGHTS ? a.cols_m : p.ldo);
-                const int64_t at = partial ? slot + t128
-                                           : (MODE == PRODUCT_WEIGHTS ? (t.seg * a.cols_n + t.n0) * a.cols_m : t.row0 * p.ldo) + m;
-                for (int c = 0; c < n_left; c += 32) {
-                    float v[32];
-                    if (summed) {
-                        tmem_load_32(from + c, v);
-                        if constexpr (PL > 1) {
-                            float lo[32];
-                            tmem_load_32(from + NT + c, lo);
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) v[j] += lo[j];
-                        }
+                bool waiting = summed && !adding;
+                int c = group * W;
+                for (;;) {
+                    float v[W];
+                    if (MODE == PRODUCT_ADAPTERS && final && !to_part && c < n_left) {
+                        if constexpr (MODE == PRODUCT_ADAPTERS) low_rank<PL>(p, v, t.row0, c, t.rows, tile_adapter, m + lane, lane, staging);
                     } else {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+                        for (int j = 0; j < W; ++j) v[j] = 0.0f;
                     }
-                    if (!fresh && (partial || m < a.cols_m)) {
-                        // the sum so far, float32 wherever there is more than one piece
-                        const float* so_far = (partial ? a.partials : static_cast<const float*>(p.out)) + at + c * step;
+                    if (waiting) {
+                        ok = bar_drain_all<EPW>(wait_for<CG>(acc_full + buf, bph, p.status));
+                        if (!ok) break;
+                        tc_fence_after();
+                        waiting = false;
+                    }
+                    if (c >= n_left) break;
+                    const int n = n_left - c < W ? n_left - c : W;
+                    if (adding) {
+                        float d[W];
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (c + j < n_left) v[j] += so_far[j * step];
+                        for (int j = 0; j < W; ++j) d[j] = 0.0f;
+                        for (int q = 0; q < t.parts; ++q) {
+                            const float* part = a.partials + slot + (int64_t(q - t.part) * CG * NT + c) * MT;
+#pragma unroll
+                            for (int j = 0; j < W; ++j)
+                                if (j < n) d[j] += __ldcg(part + j * MT);
+                        }
+#pragma unroll
+                        for (int j = 0; j < W; ++j) v[j] += d[j];
+                    } else if (summed) {
+                        float d[W];
+                        tmem_load(from + c, d);
+#pragma unroll
+                        for (int j = 0; j < W; ++j) v[j] += d[j];
+                        if constexpr (PL > 1) {
+                            tmem_load(from + NT + c, d);
+#pragma unroll
+                            for (int j = 0; j < W; ++j) v[j] += d[j];
+                        }
+                        if (!fresh && (to_part || lane < lanes)) {
+                            // the sum so far, float32 wherever there is more than one piece
+                            const float* so_far = to_part ? a.partials + slot + int64_t(c) * MT : static_cast<const float*>(p.out) + at + c * step + lane;
+                            const int64_t s1 = to_part ? MT : step;
+#pragma unroll
+                            for (int j = 0; j < W; ++j)
+                                if (j < n) v[j] += so_far[j * s1];
+                        }
                     }
-                    if (partial) {
-                        store_rows(a.partials, PT_F32, at + c * step, step, v, n_left - c);
-                    } else if (m < a.cols_m) {
-                        if (final) finish<MODE>(p, v, c, n_left, t, tile_adapter, m, factor);
-                        store_rows(p.out, p.out_type, at + c * step, step, v, n_left - c);
+                    if (to_part) {
+                        store_rows(a.partials + slot + int64_t(c) * MT, MT, v, n, [](float x) { return x; });
+                    } else {
+                        if (MODE == PRODUCT_FORWARD && p.scale && final)
+#pragma unroll
+                            for (int j = 0; j < W; ++j) v[j] *= factor;
+                        store_result(a, at + c * step, step, v, n, lanes, lane, staging);
                     }
+                    c += W * (EPW / 4);
+                    if (c >= n_left) break;
                 }
-                if (summed) {
+                if (!ok) break;
+                if (summed && !adding) {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) lead_arrive<CG>(acc_empty + buf, false);
                     if ((buf ^= 1) == 0) bph ^= 1;
                 }
                 piece = final ? t.kb1 : piece + a.flush;
+                if (MODE != PRODUCT_WEIGHTS && to_part && final) {
+                    __threadfence();
+                    bar_drain<EPW>();
+                    if (td == 0) {
+                        unsigned long long* ticket = a.tickets + t.ticket * CG + rank;
+                        red_max_relaxed_gpu(ticket, static_cast<unsigned long long>(p.gen) << 32);
+                        const unsigned long long old = atom_add_release_gpu(ticket, 1);
+                        fence_acq_rel_gpu();
+                        *last_part = static_cast<uint32_t>(old) + 1 == static_cast<uint32_t>(t.parts);
+                    }
+                    bar_drain<EPW>();
+                    adding = *last_part;
+                    if (adding) {
+                        __threadfence();
+                        piece = t.kb1 - 1;      // once more around, as the final piece
+                    }
+                } else {
+                    adding = false;
+                }
             } while (piece < t.kb1);
             if (!ok) break;
-            if (MODE != PRODUCT_WEIGHTS && t.parts > 1) {
-                __threadfence();
-                bar_drain();
-                if (t128 == 0) {
-                    unsigned long long* ticket = a.tickets + t.ticket * CG + rank;
-                    red_max_relaxed_gpu(ticket, static_cast<unsigned long long>(p.gen) << 32);
-                    const unsigned long long old = atom_add_release_gpu(ticket, 1);
-                    fence_acq_rel_gpu();
-                    *last_part = static_cast<uint32_t>(old) + 1 == static_cast<uint32_t>(t.parts);
-                }
-                bar_drain();
-                if (*last_part && m < a.cols_m) {
-                    __threadfence();
-                    for (int c = 0; c < n_left; c += 32) {
-                        float v[32];
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) v[j] = 0.0f;
-                        for (int q = 0; q < t.parts; ++q) {
-                            const float* part = a.partials + slot + (int64_t(q - t.part) * CG * NT + c) * MT + t128;
-#pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                if (c + j < n_left) v[j] += __ldcg(part + j * MT);
-                        }
-                        finish<MODE>(p, v, c, n_left, t, tile_adapter, m, factor);
-                        store_rows(p.out, p.out_type, (int64_t(t.row0) + c) * p.ldo + m, p.ldo, v, n_left - c);
-                    }
-                }
-            }
         }
         tc_fence_before();
     }
@@ -880,7 +1030,7 @@ cudaError_t launch_shape(const KernelArgs& a, const ProductPlan& plan, cudaStrea
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(plan.grid);
-    cfg.blockDim = dim3(TENSOR ? 256 : 512);
+    cfg.blockDim = dim3(TENSOR ? 384 : 512);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = attr;
@@ -965,6 +1115,7 @@ ProductPlan plan_product(int mode, const ProductParams& p) {
             items *= d.parts;
         }
     }
+    d.too_many = items > INT32_MAX;
     d.grid = static_cast<int32_t>(std::max<int64_t>(cg, std::min<int64_t>(items * cg, p.sms / cg * cg)));
     d.ticket_bytes = PRODUCT_TICKETS * 8;
     d.prefix_bytes = mode != PRODUCT_ADAPTERS && p.S > NEAR_SEGMENTS ? ceil_to((p.S + 1) * 8, 256) * 256 : 0;
@@ -981,6 +1132,8 @@ cudaError_t launch_product(int mode, const ProductParams& p, const ProductPlan& 
     a.part_blocks = plan.part_blocks;
     a.kblocks = static_cast<int32_t>(ceil_to(p.K, KB));
     a.flush = p.type == PT_F32 ? 8 : (p.out_type == PT_F32 && !p.index ? 12 : NEVER_FLUSH);
+    const int64_t out_step = mode == PRODUCT_WEIGHTS ? p.N : p.ldo;
+    a.wide_rows = p.N % 8 == 0 && out_step % 8 == 0 && reinterpret_cast<uintptr_t>(p.out) % 16 == 0;
     a.chunk = plan.chunk;
     a.row_tiles = plan.row_tiles;
     a.cols_m = p.N;

@@ -42,6 +42,7 @@ struct ProductParams {
 // How a call is launched; a pure function of sizes, strides, alignment and the SM count.
 struct ProductPlan {
     int32_t grid;
+    int32_t too_many;       // 1: more tiles than 31 bits count
     int32_t tensor;         // 1: operands come by tensor copies, 0: by the loader warps
     int32_t narrow;         // 1: at most 64 rows per tile and a deeper ring
     int32_t pair;           // 1: two CTAs share a tile
