@@ -306,100 +306,143 @@ __device__ __forceinline__ void store_result(const KernelArgs& a, int64_t at, in
     }
 }
 
-// The adapters' part of 8 rows of this lane's column m, by the float32 pipes
-// while the tensor cores work on: v[j] = sum_k u[row c + j, k] b[l_j, m, k].
-// 16 ranks at a time: the rows' u go through the warp's staging, b straight
-// to the registers of the column's lane, for several rows before the first
-// is used (a decode step has another adapter in every row).
+// The adapters' part of a tile, by the float32 pipes while the tensor cores
+// work on: v[j] = sum_k u[row c + j, k] b[l_j, m, k] for 8 rows of this
+// lane's column m at a time, 16 ranks a step.  The rows' u go through the
+// warp's staging, b to the registers of the column's lane.  What a step needs
+// is fetched during the step before; where the 8 rows have different
+// adapters (a decode step), their b are fetched together at the step itself.
 template <int PL>
-__device__ __forceinline__ void low_rank(const ProductParams& p, float (&v)[8], int row0, int c, int rows,
-                                         const int* tile_adapter, int64_t m, int lane, unsigned char* staging) {
-    constexpr int AHEAD = PL == 1 ? 8 : 2;
-    constexpr int UNITS = PL == 1 ? 2 : 4;               // of 16 bytes, for 16 ranks
-    const int rank = static_cast<int>(p.rank);
-    const bool vec_b = rank % (PL == 1 ? 8 : 4) == 0 && (reinterpret_cast<uintptr_t>(p.b) & 15) == 0;
-    float4* su = reinterpret_cast<float4*>(staging);     // [8 rows][4]
+struct LowRank {
+    static constexpr int SIZE = PL == 1 ? 2 : 4;
+    static constexpr int WORDS = 16 * SIZE / 4;          // of 16 ranks
+    static constexpr int AHEAD = PL == 1 ? 8 : 2;        // rows whose b are fetched together
+    const ProductParams& p;
+    const int* tile_adapter;
+    float4* su;                                          // [8 rows][4]
+    int64_t m;
+    int row0, rows, lane, rank;
+    bool vec;
+    // the next step
+    float4 u;
+    uint32_t b[WORDS];
+    int mine, one;       // the adapter of row lane / 4; of all 8 rows, -1: none has one, -2: they differ
+
+    __device__ __forceinline__ LowRank(const ProductParams& p_, const int* table, unsigned char* staging, int lane_)
+        : p(p_), tile_adapter(table), su(reinterpret_cast<float4*>(staging)), lane(lane_), rank(static_cast<int>(p_.rank)) {
+        vec = rank * SIZE % 16 == 0 && (reinterpret_cast<uintptr_t>(p.b) & 15) == 0;
+    }
+
+    __device__ __forceinline__ void fetch_b(uint32_t (&r)[WORDS], int l, int q) const {
+        const int width = rank - q;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-    const int row = lane >> 2, unit = lane & 3;          // of u, this lane's to fetch
-    const int mine = c + row < rows ? tile_adapter[c + row] : -1;
-    if (!__any_sync(0xffffffffu, mine >= 0)) return;
-    for (int q = 0; q < rank; q += 16) {
-        const int width = rank - q < 16 ? rank - q : 16;
-        float4 uv = make_float4(0, 0, 0, 0);
-        if (mine >= 0 && unit * 4 < width) {
-            const float* u = p.u + (int64_t(row0) + c + row) * rank + q + unit * 4;
-            if (rank % 4 == 0) {
-                uv = __ldg(reinterpret_cast<const float4*>(u));
-            } else {
-                uv.x = __ldg(u);
-                if (unit * 4 + 1 < width) uv.y = __ldg(u + 1);
-                if (unit * 4 + 2 < width) uv.z = __ldg(u + 2);
-                if (unit * 4 + 3 < width) uv.w = __ldg(u + 3);
-            }
-        }
-        __syncwarp();
-        su[lane] = uv;
-        __syncwarp();
-        float bf[16];
-        int have = -1;
+        for (int k = 0; k < WORDS; ++k) r[k] = 0;
+        if (m >= p.N) return;
+        const unsigned char* src = static_cast<const unsigned char*>(p.b) + ((int64_t(l) * p.N + m) * rank + q) * SIZE;
+        if (vec) {
 #pragma unroll
-        for (int j0 = 0; j0 < 8; j0 += AHEAD) {
-            uint32_t raw[AHEAD][UNITS * 4];
-            int before = have;
-#pragma unroll
-            for (int j = 0; j < AHEAD; ++j) {
-                const int l = __shfl_sync(0xffffffffu, mine, (j0 + j) * 4);
-                if (l < 0 || l == before) continue;
-                before = l;
-#pragma unroll
-                for (int k = 0; k < UNITS * 4; ++k) raw[j][k] = 0;
-                if (m >= p.N) continue;
-                const int64_t at = (int64_t(l) * p.N + m) * rank + q;
-                if (vec_b) {
-                    const uint4* b = reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(p.b) + at * (PL == 1 ? 2 : 4));
-#pragma unroll
-                    for (int k = 0; k < UNITS; ++k)
-                        if (k * (PL == 1 ? 8 : 4) < width) {
-                            const uint4 x = __ldg(b + k);
-                            raw[j][4 * k] = x.x, raw[j][4 * k + 1] = x.y, raw[j][4 * k + 2] = x.z, raw[j][4 * k + 3] = x.w;
-                        }
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        if (k >= width) continue;
-                        if constexpr (PL == 1) raw[j][k / 2] |= static_cast<uint32_t>(__ldg(static_cast<const uint16_t*>(p.b) + at + k)) << (k % 2 * 16);
-                        else raw[j][k] = __ldg(static_cast<const uint32_t*>(p.b) + at + k);
-                    }
+            for (int k = 0; k < WORDS / 4; ++k)
+                if (k * 16 < width * SIZE) {
+                    const uint4 x = __ldg(reinterpret_cast<const uint4*>(src) + k);
+                    r[4 * k] = x.x, r[4 * k + 1] = x.y, r[4 * k + 2] = x.z, r[4 * k + 3] = x.w;
                 }
-            }
+        } else {
 #pragma unroll
-            for (int j = 0; j < AHEAD; ++j) {
-                const int l = __shfl_sync(0xffffffffu, mine, (j0 + j) * 4);
-                if (l < 0) continue;
-                if (l != have) {
-                    have = l;
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        if constexpr (PL == 3) bf[k] = __uint_as_float(raw[j][k]);
-                        else if (p.type == PT_BF16) bf[k] = __uint_as_float(k % 2 ? raw[j][k / 2] & 0xffff0000u : raw[j][k / 2] << 16);
-                        else bf[k] = __half2float(__ushort_as_half(static_cast<uint16_t>(k % 2 ? raw[j][k / 2] >> 16 : raw[j][k / 2])));
-                    }
-                }
-                float s = v[j0 + j], s2 = 0.0f;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float4 x = su[(j0 + j) * 4 + k];
-                    s = fmaf(x.x, bf[4 * k], s);
-                    s2 = fmaf(x.y, bf[4 * k + 1], s2);
-                    s = fmaf(x.z, bf[4 * k + 2], s);
-                    s2 = fmaf(x.w, bf[4 * k + 3], s2);
-                }
-                v[j0 + j] = s + s2;
+            for (int k = 0; k < 16; ++k) {
+                if (k >= width) continue;
+                if constexpr (PL == 1) r[k / 2] |= static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(src) + k)) << (k % 2 * 16);
+                else r[k] = __ldg(reinterpret_cast<const uint32_t*>(src) + k);
             }
         }
     }
-}
+
+    __device__ __forceinline__ void fetch(int c, int q) {
+        const int row = lane >> 2, unit = lane & 3, width = rank - q - unit * 4;
+        if (q == 0) {
+            mine = c + row < rows ? tile_adapter[c + row] : -1;
+            const bool in = c + row < rows;
+            const int l0 = __shfl_sync(0xffffffffu, mine, 0);
+            one = __all_sync(0xffffffffu, !in || mine == l0) ? l0 : -2;
+        }
+        u = make_float4(0, 0, 0, 0);
+        if (mine >= 0 && width > 0) {
+            const float* src = p.u + (int64_t(row0) + c + row) * rank + q + unit * 4;
+            if (rank % 4 == 0) {
+                u = __ldg(reinterpret_cast<const float4*>(src));
+            } else {
+                u.x = __ldg(src);
+                if (width > 1) u.y = __ldg(src + 1);
+                if (width > 2) u.z = __ldg(src + 2);
+                if (width > 3) u.w = __ldg(src + 3);
+            }
+        }
+        if (one >= 0) fetch_b(b, one, q);
+    }
+
+    __device__ __forceinline__ void begin(int row0_, int rows_, int64_t m_, int c) {
+        row0 = row0_, rows = rows_, m = m_;
+        if (c < rows) fetch(c, 0);
+    }
+
+    __device__ __forceinline__ void widen(float (&f)[16], const uint32_t (&r)[WORDS]) const {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            if constexpr (PL == 3) f[k] = __uint_as_float(r[k]);
+            else if (p.type == PT_BF16) f[k] = __uint_as_float(k % 2 ? r[k / 2] & 0xffff0000u : r[k / 2] << 16);
+            else f[k] = __half2float(__ushort_as_half(static_cast<uint16_t>(k % 2 ? r[k / 2] >> 16 : r[k / 2])));
+        }
+    }
+
+    __device__ __forceinline__ float dot(float s, int j, const float (&f)[16]) const {
+        float s2 = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float4 x = su[j * 4 + k];
+            s = fmaf(x.x, f[4 * k], s);
+            s2 = fmaf(x.y, f[4 * k + 1], s2);
+            s = fmaf(x.z, f[4 * k + 2], s);
+            s2 = fmaf(x.w, f[4 * k + 3], s2);
+        }
+        return s + s2;
+    }
+
+    // Rows c .. c + 7, fetched before; then rows `next` are.
+    __device__ __forceinline__ void rows_of(float (&v)[8], int c, int next) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+        for (int q = 0; q < rank; q += 16) {
+            const int l_mine = mine, l_one = one;
+            float f[16];
+            __syncwarp();
+            su[lane] = u;
+            if (l_one >= 0) widen(f, b);
+            __syncwarp();
+            if (q + 16 < rank && l_one != -1) fetch(c, q + 16);
+            else if (next < rows) fetch(next, 0);
+            if (l_one == -1) return;
+            if (l_one >= 0) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = dot(v[j], j, f);
+                continue;
+            }
+#pragma unroll
+            for (int j0 = 0; j0 < 8; j0 += AHEAD) {
+                uint32_t raw[AHEAD][WORDS];
+#pragma unroll
+                for (int j = 0; j < AHEAD; ++j) {
+                    const int l = __shfl_sync(0xffffffffu, l_mine, (j0 + j) * 4);
+                    if (l >= 0) fetch_b(raw[j], l, q);
+                }
+#pragma unroll
+                for (int j = 0; j < AHEAD; ++j) {
+                    if (__shfl_sync(0xffffffffu, l_mine, (j0 + j) * 4) < 0) continue;
+                    widen(f, raw[j]);
+                    v[j0 + j] = dot(v[j0 + j], j0 + j, f);
+                }
+            }
+        }
+    }
+};
 
 // ---------------------------------------------------------------------------
 // The loader warps: boxes of `rows` x 64 values of a row-major matrix into
@@ -416,68 +459,88 @@ __device__ __forceinline__ uint32_t swizzled(int row, int unit) {
     return static_cast<uint32_t>(row * 128 + ((unit ^ (row & 7)) << 4));
 }
 
-// One unit: 8 values of one row, as PL planes of 16 bytes each.
+// The three parts of 8 float32 values.
+__device__ __forceinline__ void split(float (&f)[8], uint4 (&v)[3]) {
+    uint32_t part[3][8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            part[k][i] = __float_as_uint(f[i]);                      // its upper half: the rest is exact
+            f[i] -= __uint_as_float(part[k][i] & 0xffff0000u);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+        v[k] = make_uint4(__byte_perm(part[k][0], part[k][1], 0x7632), __byte_perm(part[k][2], part[k][3], 0x7632),
+                          __byte_perm(part[k][4], part[k][5], 0x7632), __byte_perm(part[k][6], part[k][7], 0x7632));
+}
+
+// One unit (8 values of one row), value by value.
 template <int PL>
 __device__ __forceinline__ void load_unit(const Box& x, int row, int unit, uint4 (&v)[PL]) {
     const int64_t r = x.row0 + row, c = x.col0 + unit * 8;
-#pragma unroll
-    for (int i = 0; i < PL; ++i) v[i] = make_uint4(0, 0, 0, 0);
-    if (r >= x.row_end || c >= x.col_end) return;
+    const bool in = r < x.row_end;
     if constexpr (PL == 1) {
         const uint16_t* src = static_cast<const uint16_t*>(x.base) + r * x.ld + c;
-        if (c + 8 <= x.col_end && (reinterpret_cast<uintptr_t>(src) & 15) == 0) {
-            v[0] = __ldg(reinterpret_cast<const uint4*>(src));
-        } else {
-            uint32_t h[8];
+        uint32_t h[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) h[i] = c + i < x.col_end ? __ldg(src + i) : 0;
-            v[0] = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
-        }
+        for (int i = 0; i < 8; ++i) h[i] = in && c + i < x.col_end ? __ldg(src + i) : 0;
+        v[0] = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
     } else {
         const float* src = static_cast<const float*>(x.base) + r * x.ld + c;
         float f[8];
-        if (c + 8 <= x.col_end && (reinterpret_cast<uintptr_t>(src) & 15) == 0) {
-            const float4 a = __ldg(reinterpret_cast<const float4*>(src)), b = __ldg(reinterpret_cast<const float4*>(src) + 1);
-            f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-        } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = c + i < x.col_end ? __ldg(src + i) : 0.0f;
-        }
-        uint32_t part[PL][8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-#pragma unroll
-            for (int k = 0; k < PL; ++k) {
-                part[k][i] = __float_as_uint(f[i]) >> 16;          // truncation: the rest is exact
-                f[i] -= __uint_as_float(part[k][i] << 16);
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < PL; ++k)
-            v[k] = make_uint4(part[k][0] | part[k][1] << 16, part[k][2] | part[k][3] << 16,
-                              part[k][4] | part[k][5] << 16, part[k][6] | part[k][7] << 16);
+        for (int i = 0; i < 8; ++i) f[i] = in && c + i < x.col_end ? __ldg(src + i) : 0.0f;
+        split(f, v);
     }
 }
 
-// `units` (8 per row) of a box into `dst`, planes `plane` bytes apart, by a loader group's 128 threads.
+// `units` (8 per row) of a box into `dst`, planes `plane` bytes apart, by a
+// loader group's 128 threads.  Where every unit is whole and aligned, the
+// loads of AHEAD units go out together, without branches between them.
 template <int PL>
 __device__ __forceinline__ void load_box(const Box& x, int units, unsigned char* dst, int plane) {
-    constexpr int AHEAD = 4;
-    const int t = threadIdx.x & (LOAD_GROUP * 32 - 1);
-    for (int u0 = t; u0 < units; u0 += AHEAD * LOAD_GROUP * 32) {
-        uint4 v[AHEAD][PL];
+    constexpr int AHEAD = 8, NT = LOAD_GROUP * 32, SIZE = PL == 1 ? 2 : 4;
+    const int t = threadIdx.x & (NT - 1);
+    if (((reinterpret_cast<uintptr_t>(x.base) | static_cast<uint64_t>(x.ld * SIZE)) & 15) == 0 && x.col_end % 8 == 0 && x.row_end > x.row0) {
+        for (int u0 = t; u0 < units; u0 += AHEAD * NT) {
+            uint4 raw[AHEAD][SIZE / 2];
+            bool in[AHEAD];
 #pragma unroll
-        for (int i = 0; i < AHEAD; ++i) {
-            const int u = u0 + i * LOAD_GROUP * 32;
-            if (u < units) load_unit<PL>(x, u >> 3, u & 7, v[i]);
+            for (int i = 0; i < AHEAD; ++i) {
+                const int u = u0 + i * NT;
+                const int64_t r = x.row0 + (u >> 3), c = x.col0 + (u & 7) * 8;
+                in[i] = u < units && r < x.row_end && c < x.col_end;
+                // elsewhere the matrix's first unit, and zeros instead of it
+                const uint4* src = reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(x.base) + (in[i] ? (r * x.ld + c) * SIZE : 0));
+#pragma unroll
+                for (int k = 0; k < SIZE / 2; ++k) raw[i][k] = __ldg(src + k);
+            }
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) {
+                const int u = u0 + i * NT;
+                if (u >= units) break;
+                uint4 v[PL];
+                if constexpr (PL == 1) {
+                    v[0] = raw[i][0];
+                } else {
+                    float f[8] = {__uint_as_float(raw[i][0].x), __uint_as_float(raw[i][0].y), __uint_as_float(raw[i][0].z), __uint_as_float(raw[i][0].w),
+                                  __uint_as_float(raw[i][1].x), __uint_as_float(raw[i][1].y), __uint_as_float(raw[i][1].z), __uint_as_float(raw[i][1].w)};
+                    split(f, v);
+                }
+#pragma unroll
+                for (int k = 0; k < PL; ++k)
+                    *reinterpret_cast<uint4*>(dst + k * plane + swizzled(u >> 3, u & 7)) = in[i] ? v[k] : make_uint4(0, 0, 0, 0);
+            }
         }
+        return;
+    }
+    for (int u = t; u < units; u += NT) {
+        uint4 v[PL];
+        load_unit<PL>(x, u >> 3, u & 7, v);
 #pragma unroll
-        for (int i = 0; i < AHEAD; ++i) {
-            const int u = u0 + i * LOAD_GROUP * 32;
-            if (u < units)
-#pragma unroll
-                for (int k = 0; k < PL; ++k) *reinterpret_cast<uint4*>(dst + k * plane + swizzled(u >> 3, u & 7)) = v[i][k];
-        }
+        for (int k = 0; k < PL; ++k) *reinterpret_cast<uint4*>(dst + k * plane + swizzled(u >> 3, u & 7)) = v[k];
     }
 }
 
@@ -558,8 +621,8 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
     // The last block of a weights' sum reaches past the segment: those rows are zeroed once they have arrived.
     auto has_tail = [&](const Item& t, int kb) { return MODE == PRODUCT_WEIGHTS && kb + 1 == t.kb1 && (t.rows & 15) != 0; };
 
-    if (TENSOR ? warp == 1 : warp >= LOAD_WARP) {
-        // ---- producer ----
+    if (TENSOR ? (warp == 1 || warp == 3) : warp >= LOAD_WARP) {
+        // ---- producers: warp 1 copies A, warp 3 B (one thread's chain of waits and copies for both took longer than the MMAs) ----
         if (!TENSOR || elect_one()) {
             uint32_t st = 0, ph = 1, turn = 0;
             int64_t issued = 0;
@@ -597,26 +660,25 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                     if constexpr (TENSOR) {
                         const bool tail = has_tail(t, kb);
                         const uint32_t bar = tail ? smem_u32(landed + st) : lead_addr<CG>(full + st);
-                        if (tail) {
-                            mbar_arrive_expect_tx(landed + st, bytes);
-                        } else if (rank == 0) {      // both arrivals, and the bytes of both CTAs
-                            mbar_arrive_expect_tx(full + st, bytes + other_bytes);
-                            if (CG == 2) mbar_arrive(full + st);
-                        }
-                        if (MODE == PRODUCT_WEIGHTS) {
-                            const int r = t.row0 + kb * KB, n0 = t.n0 + rank * share;
-                            for (int x = 0; x < a_boxes; ++x) tensor_load_2d<CG>(sa + x * 8192, &map_a, m0 + x * 64, r, bar);
-                            for (int x = 0; x < b_boxes; ++x) tensor_load_2d<CG>(sb + x * 8192, &map_b, n0 + x * 64, r, bar);
-                        } else {
-                            const int r0 = t.row0 + rank * share;
+                        if (warp == 1) {
+                            if (tail) {
+                                mbar_arrive_expect_tx(landed + st, bytes);
+                            } else if (rank == 0) {      // both arrivals, and the bytes of both CTAs
+                                mbar_arrive_expect_tx(full + st, bytes + other_bytes);
+                                if (CG == 2) mbar_arrive(full + st);
+                            }
                             for (int x = 0; x < a_boxes; ++x) {
-                                if (a_outer) tensor_load_3d<CG>(sa + x * 8192, &map_a, m0 + x * 64, kb * KB, static_cast<int>(m), bar);
+                                if (MODE == PRODUCT_WEIGHTS) tensor_load_2d<CG>(sa + x * 8192, &map_a, m0 + x * 64, t.row0 + kb * KB, bar);
+                                else if (a_outer) tensor_load_3d<CG>(sa + x * 8192, &map_a, m0 + x * 64, kb * KB, static_cast<int>(m), bar);
                                 else tensor_load_3d<CG>(sa, &map_a, kb * KB, m0, static_cast<int>(m), bar);
                             }
-                            for (int x = 0; x < b_boxes; ++x)
-                                tensor_load_2d<CG>(sb + x * BOX_ROWS * 128, &map_b, kb * KB, r0 + x * BOX_ROWS, bar);
+                            ++issued;
+                        } else {
+                            for (int x = 0; x < b_boxes; ++x) {
+                                if (MODE == PRODUCT_WEIGHTS) tensor_load_2d<CG>(sb + x * 8192, &map_b, t.n0 + rank * share + x * 64, t.row0 + kb * KB, bar);
+                                else tensor_load_2d<CG>(sb + x * BOX_ROWS * 128, &map_b, kb * KB, t.row0 + rank * share + x * BOX_ROWS, bar);
+                            }
                         }
-                        ++issued;
                     } else {
                         constexpr int64_t size = PL == 1 ? 2 : 4;
                         if (MODE == PRODUCT_WEIGHTS) {
@@ -747,6 +809,7 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
         const int td = tid - EPI_WARP * 32;
         constexpr int W = MODE == PRODUCT_ADAPTERS ? 8 : 32;      // columns at a time
         staging += (warp - EPI_WARP) * STAGING;
+        LowRank<PL> low(p, tile_adapter, staging, lane);
         if (MODE == PRODUCT_FORWARD && !p.index) {
             // rows in no segment
             const int b = p.S > 0 ? beg[0] : 0, e = p.S > 0 ? beg[p.S] : 0;
@@ -796,10 +859,12 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                 const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * R::ACC;
                 bool waiting = summed && !adding;
                 int c = group * W;
+                if constexpr (MODE == PRODUCT_ADAPTERS)
+                    if (final && !to_part) low.begin(t.row0, t.rows, m + lane, c);
                 for (;;) {
                     float v[W];
                     if (MODE == PRODUCT_ADAPTERS && final && !to_part && c < n_left) {
-                        if constexpr (MODE == PRODUCT_ADAPTERS) low_rank<PL>(p, v, t.row0, c, t.rows, tile_adapter, m + lane, lane, staging);
+                        if constexpr (MODE == PRODUCT_ADAPTERS) low.rows_of(v, c, c + W * (EPW / 4));
                     } else {
 #pragma unroll
                         for (int j = 0; j < W; ++j) v[j] = 0.0f;
