@@ -89,6 +89,8 @@ def library_path() -> str:
 def load_library(path: str | None = None):
     """Load libsegreduce.so (raises OSError if it has not been built)."""
     global _lib
+    if _lib is not None and path is None:
+        return _lib
     with _lock:
         if _lib is not None and path is None:
             return _lib
@@ -161,9 +163,15 @@ def plan(dtype: str, feat: int, num_values: int, offsets_dtype: str, num_segment
     return {f: getattr(pl, f) for f, _ in _Plan._fields_}
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _value_code(t):
@@ -566,12 +574,22 @@ def flags_to_offsets(flags):
     return offsets[:int(count.item()) + 1]
 
 
+# The products' calls are short (a decode step's kernel takes 8 us), so their
+# host side is kept so: types and the raw-stream function are looked up once,
+# and the device guard is entered only where the device changes.
+
+_product_types = None
+
+
 def _product_code(t):
-    torch = _torch()
-    codes = {torch.float32: SEG_F32, torch.float16: SEG_F16, torch.bfloat16: SEG_BF16}
-    if t.dtype not in codes:
+    global _product_types
+    if _product_types is None:
+        torch = _torch()
+        _product_types = {torch.float32: SEG_F32, torch.float16: SEG_F16, torch.bfloat16: SEG_BF16}
+    code = _product_types.get(t.dtype)
+    if code is None:
         raise TypeError(f"values must be float32, float16 or bfloat16, not {t.dtype}")
-    return codes[t.dtype]
+    return code
 
 
 def _check_rows(name, t, offsets):
@@ -589,10 +607,11 @@ def _check_rows(name, t, offsets):
 
 def _row_stride(name, t):
     """Elements from one row to the next of a tensor whose rows are contiguous."""
-    rows, cols = t.shape[-2], t.shape[-1]
-    if (cols > 1 and t.stride(-1) != 1) or (rows > 1 and t.stride(-2) < cols):
+    rows, cols = t.shape[-2:]
+    step, one = t.stride()[-2:]
+    if (one != 1 and cols > 1) or (rows > 1 and step < cols):
         raise ValueError(f"{name} must have contiguous rows that do not overlap")
-    return t.stride(-2) if rows > 1 else max(cols, 1)
+    return step if rows > 1 else max(cols, 1)
 
 
 def _same(name, t, like, shape, dtype=None):
@@ -601,8 +620,26 @@ def _same(name, t, like, shape, dtype=None):
         raise ValueError(f"{name} must be on {like.device}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
+
+
+def _enqueue(where, device, stream, fn, *args):
+    """Calls a product of the library on ``stream`` (default: ``device``'s current one)."""
+    torch = _torch()
+    if stream is not None:
+        raw = stream.cuda_stream
+    elif hasattr(torch._C, "_cuda_getCurrentRawStream"):
+        raw = torch._C._cuda_getCurrentRawStream(device.index)
+    else:
+        raw = torch.cuda.current_stream(device).cuda_stream
+    if torch.cuda.current_device() == device.index:
+        rc = fn(*args, raw)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, raw)
+    if rc != 0:
+        raise SegReduceError(rc, where)
 
 
 def seg_matmul(x, w, offsets, transpose_w: bool = False, out=None, stream=None):
@@ -615,29 +652,22 @@ def seg_matmul(x, w, offsets, transpose_w: bool = False, out=None, stream=None):
     and are rounded once to ``x``'s type.  The gradient of ``x`` is
     ``seg_matmul(dy, w, offsets, not transpose_w)``, that of ``w``
     ``seg_matmul_grad_w``.  Not synchronised."""
-    torch = _torch()
     ldx = _check_rows("x", x, offsets)
-    code, s, k = _product_code(x), offsets.numel() - 1, x.shape[1]
+    code, s, (r, k) = _product_code(x), offsets.shape[0] - 1, x.shape
     if w.dim() != 3:
         raise ValueError("w must be [S, K, N] (transpose_w: [S, N, K])")
     n = w.shape[1] if transpose_w else w.shape[2]
     _same("w", w, x, (s, n, k) if transpose_w else (s, k, n))
     ldw = _row_stride("w", w)
-    oshape = (x.shape[0], n)
     if out is None:
-        out = torch.empty(oshape, dtype=x.dtype, device=x.device)
+        out = _torch().empty((r, n), dtype=x.dtype, device=x.device)
+        ldo = max(n, 1)
     else:
-        _same("out", out, x, oshape)
-    ldo = _row_stride("out", out)
-    if stream is None:
-        stream = torch.cuda.current_stream(x.device)
-    with torch.cuda.device(x.device):
-        rc = load_library().seg_matmul(
-            x.data_ptr() or None, code, x.shape[0], k, ldx, w.data_ptr() or None, n, ldw,
-            w.stride(0) if s > 1 else 0, 1 if transpose_w else 0, offsets.data_ptr(), _offset_code(offsets), s,
-            out.data_ptr() or None, ldo, ctypes.c_void_p(stream.cuda_stream))
-    if rc != 0:
-        raise SegReduceError(rc, "seg_matmul")
+        _same("out", out, x, (r, n))
+        ldo = _row_stride("out", out)
+    _enqueue("seg_matmul", x.device, stream, load_library().seg_matmul,
+             x.data_ptr() or None, code, r, k, ldx, w.data_ptr() or None, n, ldw, w.stride(0) if s > 1 else 0,
+             1 if transpose_w else 0, offsets.data_ptr(), _offset_code(offsets), s, out.data_ptr() or None, ldo)
     return out
 
 
@@ -650,7 +680,7 @@ def seg_matmul_grad_w(x, dy, offsets, out_dtype=None, out=None, stream=None):
     with ``x`` and ``dy`` exchanged.  Not synchronised."""
     torch = _torch()
     ldx = _check_rows("x", x, offsets)
-    code, s = _product_code(x), offsets.numel() - 1
+    code, s = _product_code(x), offsets.shape[0] - 1
     if dy.dim() != 2:
         raise ValueError("dy must be [R, N]")
     k, n = x.shape[1], dy.shape[1]
@@ -666,15 +696,9 @@ def seg_matmul_grad_w(x, dy, offsets, out_dtype=None, out=None, stream=None):
         _same("out", out, x, (s, k, n), out_dtype)
         if not out.is_contiguous():
             raise ValueError("out must be contiguous")
-    if stream is None:
-        stream = torch.cuda.current_stream(x.device)
-    with torch.cuda.device(x.device):
-        rc = load_library().seg_matmul_grad_w(
-            x.data_ptr() or None, code, x.shape[0], k, ldx, dy.data_ptr() or None, n, ldy, offsets.data_ptr(),
-            _offset_code(offsets), s, out.data_ptr() or None, SEG_F32 if out_dtype == torch.float32 else code,
-            ctypes.c_void_p(stream.cuda_stream))
-    if rc != 0:
-        raise SegReduceError(rc, "seg_matmul_grad_w")
+    _enqueue("seg_matmul_grad_w", x.device, stream, load_library().seg_matmul_grad_w,
+             x.data_ptr() or None, code, x.shape[0], k, ldx, dy.data_ptr() or None, n, ldy, offsets.data_ptr(),
+             _offset_code(offsets), s, out.data_ptr() or None, SEG_F32 if out_dtype == torch.float32 else code)
     return out
 
 
@@ -726,7 +750,7 @@ def seg_lora(x, w, a, b, offsets, adapter, scale=None, out=None, stream=None):
     synchronised."""
     torch = _torch()
     ldx = _check_rows("x", x, offsets)
-    code, s, k = _product_code(x), offsets.numel() - 1, x.shape[1]
+    code, s, (r, k) = _product_code(x), offsets.shape[0] - 1, x.shape
     if w.dim() != 2 or a.dim() != 3 or b.dim() != 3:
         raise ValueError("w must be [N, K], a [L, rank, K] and b [L, N, rank]")
     n, count, rank = w.shape[0], a.shape[0], a.shape[1]
@@ -740,22 +764,16 @@ def seg_lora(x, w, a, b, offsets, adapter, scale=None, out=None, stream=None):
         if t is not None and not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
     ldw = _row_stride("w", w)
-    oshape = (x.shape[0], n)
     if out is None:
-        out = torch.empty(oshape, dtype=x.dtype, device=x.device)
+        out = torch.empty((r, n), dtype=x.dtype, device=x.device)
+        ldo = max(n, 1)
     else:
-        _same("out", out, x, oshape)
-    ldo = _row_stride("out", out)
-    if stream is None:
-        stream = torch.cuda.current_stream(x.device)
-    with torch.cuda.device(x.device):
-        rc = load_library().seg_lora(
-            x.data_ptr() or None, code, x.shape[0], k, ldx, w.data_ptr() or None, n, ldw, a.data_ptr() or None,
-            b.data_ptr() or None, count, rank, offsets.data_ptr(), _offset_code(offsets), s,
-            adapter.data_ptr() or None, _ptr(scale) or None, out.data_ptr() or None, ldo,
-            ctypes.c_void_p(stream.cuda_stream))
-    if rc != 0:
-        raise SegReduceError(rc, "seg_lora")
+        _same("out", out, x, (r, n))
+        ldo = _row_stride("out", out)
+    _enqueue("seg_lora", x.device, stream, load_library().seg_lora,
+             x.data_ptr() or None, code, r, k, ldx, w.data_ptr() or None, n, ldw, a.data_ptr() or None,
+             b.data_ptr() or None, count, rank, offsets.data_ptr(), _offset_code(offsets), s,
+             adapter.data_ptr() or None, _ptr(scale) or None, out.data_ptr() or None, ldo)
     return out
 
 

@@ -445,14 +445,22 @@ struct LowRank {
 };
 
 // ---------------------------------------------------------------------------
-// The loader warps: boxes of `rows` x 64 values of a row-major matrix into
-// 128-byte swizzled rows, zero outside [.., row_end) x [.., col_end).
+// The loader warps: blocks of a row-major matrix into 128-byte swizzled rows,
+// zero outside [.., row_end) x [.., col_end).
 
-struct Box {
+// One operand of a stage.  `units` of 8 values each; 8 units to a 128-byte
+// row of shared memory, 64 rows to 8,192 bytes.  outer: every 64 rows are
+// the block's 64 steps of the sum for the next 64 columns; else unit u is
+// columns of row u / 8.
+struct Operand {
     const void* base;
     int64_t ld;
     int64_t row0, row_end;
     int64_t col0, col_end;
+    int units;
+    bool outer;
+    __device__ __forceinline__ int64_t row(int u) const { return row0 + (outer ? u >> 3 & 63 : u >> 3); }
+    __device__ __forceinline__ int64_t col(int u) const { return col0 + (u & 7) * 8 + (outer ? u >> 9 << 6 : 0); }
 };
 
 __device__ __forceinline__ uint32_t swizzled(int row, int unit) {
@@ -476,10 +484,10 @@ __device__ __forceinline__ void split(float (&f)[8], uint4 (&v)[3]) {
                           __byte_perm(part[k][4], part[k][5], 0x7632), __byte_perm(part[k][6], part[k][7], 0x7632));
 }
 
-// One unit (8 values of one row), value by value.
+// One unit, value by value.
 template <int PL>
-__device__ __forceinline__ void load_unit(const Box& x, int row, int unit, uint4 (&v)[PL]) {
-    const int64_t r = x.row0 + row, c = x.col0 + unit * 8;
+__device__ __forceinline__ void load_unit(const Operand& x, int u, uint4 (&v)[PL]) {
+    const int64_t r = x.row(u), c = x.col(u);
     const bool in = r < x.row_end;
     if constexpr (PL == 1) {
         const uint16_t* src = static_cast<const uint16_t*>(x.base) + r * x.ld + c;
@@ -496,26 +504,37 @@ __device__ __forceinline__ void load_unit(const Box& x, int row, int unit, uint4
     }
 }
 
-// `units` (8 per row) of a box into `dst`, planes `plane` bytes apart, by a
-// loader group's 128 threads.  Where every unit is whole and aligned, the
-// loads of AHEAD units go out together, without branches between them.
+// Where the units of an operand are whole and 16-byte aligned.
 template <int PL>
-__device__ __forceinline__ void load_box(const Box& x, int units, unsigned char* dst, int plane) {
+__device__ __forceinline__ bool whole_units(const Operand& x) {
+    return ((reinterpret_cast<uintptr_t>(x.base) | static_cast<uint64_t>(x.ld * (PL == 1 ? 2 : 4))) & 15) == 0 && x.col_end % 8 == 0;
+}
+
+// Both operands of a stage, planes a_plane and b_plane bytes apart, by a
+// loader group's 128 threads.  Where every unit is whole, the loads of AHEAD
+// units, of either operand, go out together without branches between them.
+template <int PL>
+__device__ __forceinline__ void load_operands(const Operand& a, const Operand& b, unsigned char* sa, int a_plane,
+                                              unsigned char* sb, int b_plane) {
     constexpr int AHEAD = 8, NT = LOAD_GROUP * 32, SIZE = PL == 1 ? 2 : 4;
-    const int t = threadIdx.x & (NT - 1);
-    if (((reinterpret_cast<uintptr_t>(x.base) | static_cast<uint64_t>(x.ld * SIZE)) & 15) == 0 && x.col_end % 8 == 0 && x.row_end > x.row0) {
+    const int t = threadIdx.x & (NT - 1), units = a.units + b.units;
+    auto place = [](int u) { return (u >> 9) * 8192 + swizzled(u >> 3 & 63, u & 7); };
+    if (whole_units<PL>(a) && whole_units<PL>(b)) {
         for (int u0 = t; u0 < units; u0 += AHEAD * NT) {
             uint4 raw[AHEAD][SIZE / 2];
             bool in[AHEAD];
 #pragma unroll
             for (int i = 0; i < AHEAD; ++i) {
                 const int u = u0 + i * NT;
-                const int64_t r = x.row0 + (u >> 3), c = x.col0 + (u & 7) * 8;
-                in[i] = u < units && r < x.row_end && c < x.col_end;
-                // elsewhere the matrix's first unit, and zeros instead of it
-                const uint4* src = reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(x.base) + (in[i] ? (r * x.ld + c) * SIZE : 0));
+                const bool is_a = u < a.units;
+                const int q = is_a ? u : u - a.units;
+                const int64_t r = is_a ? a.row(q) : b.row(q), c = is_a ? a.col(q) : b.col(q);
+                in[i] = u < units && r < (is_a ? a.row_end : b.row_end) && c < (is_a ? a.col_end : b.col_end);
+                // elsewhere no load, and zeros instead of it
+                const int64_t at = (r * (is_a ? a.ld : b.ld) + c) * SIZE;
+                const uint4* src = reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(is_a ? a.base : b.base) + at);
 #pragma unroll
-                for (int k = 0; k < SIZE / 2; ++k) raw[i][k] = __ldg(src + k);
+                for (int k = 0; k < SIZE / 2; ++k) raw[i][k] = in[i] ? __ldg(src + k) : make_uint4(0, 0, 0, 0);
             }
 #pragma unroll
             for (int i = 0; i < AHEAD; ++i) {
@@ -529,18 +548,22 @@ __device__ __forceinline__ void load_box(const Box& x, int units, unsigned char*
                                   __uint_as_float(raw[i][1].x), __uint_as_float(raw[i][1].y), __uint_as_float(raw[i][1].z), __uint_as_float(raw[i][1].w)};
                     split(f, v);
                 }
+                const bool is_a = u < a.units;
+                unsigned char* dst = (is_a ? sa : sb) + place(is_a ? u : u - a.units);
 #pragma unroll
-                for (int k = 0; k < PL; ++k)
-                    *reinterpret_cast<uint4*>(dst + k * plane + swizzled(u >> 3, u & 7)) = in[i] ? v[k] : make_uint4(0, 0, 0, 0);
+                for (int k = 0; k < PL; ++k) *reinterpret_cast<uint4*>(dst + k * (is_a ? a_plane : b_plane)) = v[k];
             }
         }
         return;
     }
     for (int u = t; u < units; u += NT) {
+        const bool is_a = u < a.units;
         uint4 v[PL];
-        load_unit<PL>(x, u >> 3, u & 7, v);
+        if (is_a) load_unit<PL>(a, u, v);
+        else load_unit<PL>(b, u - a.units, v);
+        unsigned char* dst = (is_a ? sa : sb) + place(is_a ? u : u - a.units);
 #pragma unroll
-        for (int k = 0; k < PL; ++k) *reinterpret_cast<uint4*>(dst + k * plane + swizzled(u >> 3, u & 7)) = v[k];
+        for (int k = 0; k < PL; ++k) *reinterpret_cast<uint4*>(dst + k * (is_a ? a_plane : b_plane)) = v[k];
     }
 }
 
@@ -622,15 +645,18 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
     auto has_tail = [&](const Item& t, int kb) { return MODE == PRODUCT_WEIGHTS && kb + 1 == t.kb1 && (t.rows & 15) != 0; };
 
     if (TENSOR ? (warp == 1 || warp == 3) : warp >= LOAD_WARP) {
-        // ---- producers: warp 1 copies A, warp 3 B (one thread's chain of waits and copies for both took longer than the MMAs) ----
+        // ---- producers: two, which take turns at the blocks (one thread's
+        // chain of wait, expect and copies for a block took longer than its MMAs) ----
+        const uint32_t turn = TENSOR ? warp >> 1 : (warp - LOAD_WARP) / LOAD_GROUP;
         if (!TENSOR || elect_one()) {
-            uint32_t st = 0, ph = 1, turn = 0;
-            int64_t issued = 0;
-            int held_seg = -1, held_m0 = 0, held_kb = 0;     // the A operand that this group's stage holds (two stages)
+            uint32_t next = turn, base = 0;                // this producer's next block; the item's first
+            uint32_t st = turn % R::STAGES, ph = turn < R::STAGES ? 1 : 0;
             bool ok = true;
+            int held_seg = -1, held_m0 = 0, held_kb = 0;   // the A operand that the producer's stage holds (two stages)
             Item t;
             for (uint32_t i = first; ok && i < items; i += stride) {
                 item_at<MODE, NT, CG>(a, beg, pre, i, t);
+                const uint32_t blocks = t.kb1 > t.kb0 ? t.kb1 - t.kb0 : 0;
                 const int columns = columns_of(t), share = share_of(columns), lanes = lanes_of(t);
                 const int a_boxes = a_outer ? (lanes + 63) / 64 : (lanes + MT - 1) / MT;
                 const int b_boxes = b_outer ? (share + 63) / 64 : (share + BOX_ROWS - 1) / BOX_ROWS;
@@ -645,14 +671,8 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                 }
                 int64_t m = t.seg;
                 if (MODE == PRODUCT_FORWARD && p.index) m = __ldg(p.index + t.seg);
-                for (int kb = t.kb0; kb < t.kb1; ++kb) {
-                    if (!TENSOR && static_cast<int>(turn++ & 1) != (warp - LOAD_WARP) / LOAD_GROUP) {
-                        if (++st == R::STAGES) {
-                            st = 0;
-                            ph ^= 1;
-                        }
-                        continue;
-                    }
+                for (; next - base < blocks; next += 2) {
+                    const int kb = t.kb0 + static_cast<int>(next - base);
                     ok = TENSOR ? wait_for<CG>(empty + st, ph, p.status) : warp_wait<CG>(empty + st, ph, p.status);
                     if (!ok) break;
                     unsigned char* sa = stages + st * R::STAGE;
@@ -660,62 +680,59 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                     if constexpr (TENSOR) {
                         const bool tail = has_tail(t, kb);
                         const uint32_t bar = tail ? smem_u32(landed + st) : lead_addr<CG>(full + st);
-                        if (warp == 1) {
-                            if (tail) {
-                                mbar_arrive_expect_tx(landed + st, bytes);
-                            } else if (rank == 0) {      // both arrivals, and the bytes of both CTAs
-                                mbar_arrive_expect_tx(full + st, bytes + other_bytes);
-                                if (CG == 2) mbar_arrive(full + st);
-                            }
-                            for (int x = 0; x < a_boxes; ++x) {
-                                if (MODE == PRODUCT_WEIGHTS) tensor_load_2d<CG>(sa + x * 8192, &map_a, m0 + x * 64, t.row0 + kb * KB, bar);
-                                else if (a_outer) tensor_load_3d<CG>(sa + x * 8192, &map_a, m0 + x * 64, kb * KB, static_cast<int>(m), bar);
-                                else tensor_load_3d<CG>(sa, &map_a, kb * KB, m0, static_cast<int>(m), bar);
-                            }
-                            ++issued;
+                        if (tail) {
+                            mbar_arrive_expect_tx(landed + st, bytes);
+                        } else if (rank == 0) {      // both arrivals, and the bytes of both CTAs
+                            mbar_arrive_expect_tx(full + st, bytes + other_bytes);
+                            if (CG == 2) mbar_arrive(full + st);
+                        }
+                        if (MODE == PRODUCT_WEIGHTS) {
+                            const int r = t.row0 + kb * KB, n0 = t.n0 + rank * share;
+                            for (int x = 0; x < a_boxes; ++x) tensor_load_2d<CG>(sa + x * 8192, &map_a, m0 + x * 64, r, bar);
+                            for (int x = 0; x < b_boxes; ++x) tensor_load_2d<CG>(sb + x * 8192, &map_b, n0 + x * 64, r, bar);
                         } else {
-                            for (int x = 0; x < b_boxes; ++x) {
-                                if (MODE == PRODUCT_WEIGHTS) tensor_load_2d<CG>(sb + x * 8192, &map_b, t.n0 + rank * share + x * 64, t.row0 + kb * KB, bar);
-                                else tensor_load_2d<CG>(sb + x * BOX_ROWS * 128, &map_b, kb * KB, t.row0 + rank * share + x * BOX_ROWS, bar);
+                            const int r0 = t.row0 + rank * share;
+                            if (a_outer) {
+                                for (int x = 0; x < a_boxes; ++x)
+                                    tensor_load_3d<CG>(sa + x * 8192, &map_a, m0 + x * 64, kb * KB, static_cast<int>(m), bar);
+                            } else if (a_boxes > 0) {
+                                tensor_load_3d<CG>(sa, &map_a, kb * KB, m0, static_cast<int>(m), bar);
                             }
+                            for (int x = 0; x < b_boxes; ++x)
+                                tensor_load_2d<CG>(sb + x * BOX_ROWS * 128, &map_b, kb * KB, r0 + x * BOX_ROWS, bar);
                         }
                     } else {
-                        constexpr int64_t size = PL == 1 ? 2 : 4;
+                        Operand oa, ob;
                         if (MODE == PRODUCT_WEIGHTS) {
                             const int64_t r = t.row0 + kb * KB, re = t.row0 + t.rows;
-                            for (int x = 0; x < a_boxes; ++x)
-                                load_box<PL>(Box{p.w, p.ldw, r, re, m0 + x * 64, a.cols_m}, KB * 8, sa + x * 8192, R::A_PLANE);
-                            for (int x = 0; x < b_boxes; ++x)
-                                load_box<PL>(Box{p.x, p.ldx, r, re, t.n0 + x * 64, a.cols_n}, KB * 8, sb + x * 8192, R::B_PLANE);
+                            oa = Operand{p.w, p.ldw, r, re, m0, a.cols_m, a_boxes * KB * 8, true};
+                            ob = Operand{p.x, p.ldx, r, re, t.n0, a.cols_n, b_boxes * KB * 8, true};
                         } else {
-                            const void* w = static_cast<const unsigned char*>(p.w) + m * p.stride_w * size;
+                            const void* w = static_cast<const unsigned char*>(p.w) + m * p.stride_w * (PL == 1 ? 2 : 4);
                             const int64_t k = int64_t(kb) * KB;
+                            if (a_outer) oa = Operand{w, p.ldw, k, p.K, m0, a.cols_m, a_boxes * KB * 8, true};
+                            else oa = Operand{w, p.ldw, m0, a.cols_m, k, p.K, MT * 8, false};
+                            ob = Operand{p.x, p.ldx, t.row0, t.row0 + t.rows, k, p.K, share * 8, false};
                             // a short sum over many tiles of a segment: its matrix is split and stored once
-                            const bool held = R::STAGES == 2 && held_seg == t.seg && held_m0 == t.m0 && held_kb == kb;
+                            if (R::STAGES == 2 && held_seg == t.seg && held_m0 == t.m0 && held_kb == kb) oa.units = 0;
                             held_seg = t.seg, held_m0 = t.m0, held_kb = kb;
-                            if (held) {
-                            } else if (a_outer) {
-                                for (int x = 0; x < a_boxes; ++x)
-                                    load_box<PL>(Box{w, p.ldw, k, p.K, m0 + x * 64, a.cols_m}, KB * 8, sa + x * 8192, R::A_PLANE);
-                            } else {
-                                load_box<PL>(Box{w, p.ldw, m0, a.cols_m, k, p.K}, MT * 8, sa, R::A_PLANE);
-                            }
-                            load_box<PL>(Box{p.x, p.ldx, t.row0, t.row0 + t.rows, k, p.K}, share * 8, sb, R::B_PLANE);
                         }
+                        load_operands<PL>(oa, ob, sa, R::A_PLANE, sb, R::B_PLANE);
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) lead_arrive<CG>(full + st, true);
                     }
-                    if (++st == R::STAGES) {
-                        st = 0;
+                    if ((st += 2) >= R::STAGES) {
+                        st -= R::STAGES;
                         ph ^= 1;
                     }
                 }
+                base += blocks;
             }
             if (TENSOR && rank == 0 && !ok) {
                 // something gave up: the copies in flight still land before this CTA's shared memory goes away
-                for (int64_t j = issued > R::STAGES ? issued - R::STAGES : 0; j < issued; ++j)
-                    wait_for<CG>(full + j % R::STAGES, static_cast<uint32_t>((j / R::STAGES) & 1), p.status);
+                for (uint32_t j = next > R::STAGES ? next - R::STAGES : 0; j < next; ++j)
+                    wait_for<CG>(full + j % R::STAGES, (j / R::STAGES) & 1, p.status);
             }
         }
         __syncwarp();
@@ -890,15 +907,13 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
 #pragma unroll
                         for (int j = 0; j < W; ++j) v[j] += d[j];
                     } else if (summed) {
-                        float d[W];
+                        float d[W], lo[W];
                         tmem_load(from + c, d);
+                        if constexpr (PL > 1) tmem_load(from + NT + c, lo);
+                        tmem_wait(d);
+                        if constexpr (PL > 1) tmem_wait(lo);
 #pragma unroll
-                        for (int j = 0; j < W; ++j) v[j] += d[j];
-                        if constexpr (PL > 1) {
-                            tmem_load(from + NT + c, d);
-#pragma unroll
-                            for (int j = 0; j < W; ++j) v[j] += d[j];
-                        }
+                        for (int j = 0; j < W; ++j) v[j] += PL > 1 ? d[j] + lo[j] : d[j];
                         if (!fresh && (to_part || lane < lanes)) {
                             // the sum so far, float32 wherever there is more than one piece
                             const float* so_far = to_part ? a.partials + slot + int64_t(c) * MT : static_cast<const float*>(p.out) + at + c * step + lane;
@@ -928,8 +943,7 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                 }
                 piece = final ? t.kb1 : piece + a.flush;
                 if (MODE != PRODUCT_WEIGHTS && to_part && final) {
-                    __threadfence();
-                    bar_drain<EPW>();
+                    bar_drain<EPW>();     // the release below covers what the others wrote before it
                     if (td == 0) {
                         unsigned long long* ticket = a.tickets + t.ticket * CG + rank;
                         red_max_relaxed_gpu(ticket, static_cast<unsigned long long>(p.gen) << 32);
@@ -940,7 +954,6 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                     bar_drain<EPW>();
                     adding = *last_part;
                     if (adding) {
-                        __threadfence();
                         piece = t.kb1 - 1;      // once more around, as the final piece
                     }
                 } else {
