@@ -855,17 +855,25 @@ seg_status_t seg_lora(const void* x, seg_dtype_t dtype, int64_t num_rows, int64_
     p.b = b;
     p.rank = rank;
     const bool low = num_segments > 0 && num_adapters > 0;
-    const int64_t own = std::max(low ? plan_product(PRODUCT_FORWARD, pa).bytes() : 0, plan_product(PRODUCT_ADAPTERS, p).bytes());
+    const bool by_rows = lora_by_rows(pa);
+    const int64_t own = std::max(low && !by_rows ? plan_product(PRODUCT_FORWARD, pa).bytes() : 0, plan_product(PRODUCT_ADAPTERS, p).bytes());
     Scratch* sc = nullptr;
     st = scratch_in(g_product_scratch, dev, stream, static_cast<size_t>(own + num_rows * rank * 4), &sc);
     if (st != SEG_OK) return st;
     float* u = reinterpret_cast<float*>(static_cast<unsigned char*>(sc->ptr) + own);
     if (low) {
         pa.out = u;
-        st = run_product(PRODUCT_FORWARD, pa, stream, sc, ds);
-        if (st != SEG_OK) return st;
+        if (by_rows) {
+            if (launch_lora_rows(pa, stream) != cudaSuccess) {
+                cudaGetLastError();
+                return SEG_ERR_CUDA;
+            }
+        } else {
+            st = run_product(PRODUCT_FORWARD, pa, stream, sc, ds);
+            if (st != SEG_OK) return st;
+        }
+        p.u = u;
     }
-    p.u = u;
     return run_product(PRODUCT_ADAPTERS, p, stream, sc, ds);
 }
 

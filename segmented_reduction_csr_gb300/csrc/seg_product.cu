@@ -320,7 +320,7 @@ struct LowRank {
     const ProductParams& p;
     const int* tile_adapter;
     float4* su;                                          // [8 rows][4]
-    int64_t m;
+    int64_t m, stride;                                   // the lane's column; bytes from one adapter's b to the next
     int row0, rows, lane, rank;
     bool vec;
     // the next step
@@ -330,23 +330,23 @@ struct LowRank {
 
     __device__ __forceinline__ LowRank(const ProductParams& p_, const int* table, unsigned char* staging, int lane_)
         : p(p_), tile_adapter(table), su(reinterpret_cast<float4*>(staging)), lane(lane_), rank(static_cast<int>(p_.rank)) {
+        stride = p.N * rank * SIZE;
         vec = rank * SIZE % 16 == 0 && (reinterpret_cast<uintptr_t>(p.b) & 15) == 0;
     }
 
     __device__ __forceinline__ void fetch_b(uint32_t (&r)[WORDS], int l, int q) const {
-        const int width = rank - q;
+        const bool in = m < p.N && l >= 0;
+        const int width = in ? rank - q : 0;
+        const unsigned char* src = static_cast<const unsigned char*>(p.b) + (in ? l * stride + (m * rank + q) * SIZE : 0);
+        if (vec) {       // predicated loads, no branch between those of several rows
 #pragma unroll
-        for (int k = 0; k < WORDS; ++k) r[k] = 0;
-        if (m >= p.N) return;
-        const unsigned char* src = static_cast<const unsigned char*>(p.b) + ((int64_t(l) * p.N + m) * rank + q) * SIZE;
-        if (vec) {
-#pragma unroll
-            for (int k = 0; k < WORDS / 4; ++k)
-                if (k * 16 < width * SIZE) {
-                    const uint4 x = __ldg(reinterpret_cast<const uint4*>(src) + k);
-                    r[4 * k] = x.x, r[4 * k + 1] = x.y, r[4 * k + 2] = x.z, r[4 * k + 3] = x.w;
-                }
+            for (int k = 0; k < WORDS / 4; ++k) {
+                const uint4 x = k * 16 < width * SIZE ? __ldg(reinterpret_cast<const uint4*>(src) + k) : make_uint4(0, 0, 0, 0);
+                r[4 * k] = x.x, r[4 * k + 1] = x.y, r[4 * k + 2] = x.z, r[4 * k + 3] = x.w;
+            }
         } else {
+#pragma unroll
+            for (int k = 0; k < WORDS; ++k) r[k] = 0;
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
                 if (k >= width) continue;
@@ -368,12 +368,12 @@ struct LowRank {
         if (mine >= 0 && width > 0) {
             const float* src = p.u + (int64_t(row0) + c + row) * rank + q + unit * 4;
             if (rank % 4 == 0) {
-                u = __ldg(reinterpret_cast<const float4*>(src));
+                u = *reinterpret_cast<const float4*>(src);
             } else {
-                u.x = __ldg(src);
-                if (width > 1) u.y = __ldg(src + 1);
-                if (width > 2) u.z = __ldg(src + 2);
-                if (width > 3) u.w = __ldg(src + 3);
+                u.x = src[0];
+                if (width > 1) u.y = src[1];
+                if (width > 2) u.z = src[2];
+                if (width > 3) u.w = src[3];
             }
         }
         if (one >= 0) fetch_b(b, one, q);
@@ -430,8 +430,7 @@ struct LowRank {
                 uint32_t raw[AHEAD][WORDS];
 #pragma unroll
                 for (int j = 0; j < AHEAD; ++j) {
-                    const int l = __shfl_sync(0xffffffffu, l_mine, (j0 + j) * 4);
-                    if (l >= 0) fetch_b(raw[j], l, q);
+                    fetch_b(raw[j], __shfl_sync(0xffffffffu, l_mine, (j0 + j) * 4), q);
                 }
 #pragma unroll
                 for (int j = 0; j < AHEAD; ++j) {
@@ -484,30 +483,60 @@ __device__ __forceinline__ void split(float (&f)[8], uint4 (&v)[3]) {
                           __byte_perm(part[k][4], part[k][5], 0x7632), __byte_perm(part[k][6], part[k][7], 0x7632));
 }
 
-// One unit, value by value.
-template <int PL>
-__device__ __forceinline__ void load_unit(const Operand& x, int u, uint4 (&v)[PL]) {
-    const int64_t r = x.row(u), c = x.col(u);
-    const bool in = r < x.row_end;
-    if constexpr (PL == 1) {
-        const uint16_t* src = static_cast<const uint16_t*>(x.base) + r * x.ld + c;
-        uint32_t h[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) h[i] = in && c + i < x.col_end ? __ldg(src + i) : 0;
-        v[0] = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
-    } else {
-        const float* src = static_cast<const float*>(x.base) + r * x.ld + c;
-        float f[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = in && c + i < x.col_end ? __ldg(src + i) : 0.0f;
-        split(f, v);
-    }
-}
-
 // Where the units of an operand are whole and 16-byte aligned.
 template <int PL>
 __device__ __forceinline__ bool whole_units(const Operand& x) {
     return ((reinterpret_cast<uintptr_t>(x.base) | static_cast<uint64_t>(x.ld * (PL == 1 ? 2 : 4))) & 15) == 0 && x.col_end % 8 == 0;
+}
+
+__device__ __forceinline__ int unit_place(int u) { return (u >> 9) * 8192 + swizzled(u >> 3 & 63, u & 7); }
+
+// An operand of any alignment, value by value (16-bit: in pairs where its
+// rows allow that), the loads of AHEAD units together.
+template <int PL>
+__device__ __forceinline__ void load_any(const Operand& x, unsigned char* dst, int plane) {
+    constexpr int AHEAD = 2, NT = LOAD_GROUP * 32;
+    const int t = threadIdx.x & (NT - 1);
+    const bool pairs = PL == 1 && (reinterpret_cast<uintptr_t>(x.base) & 3) == 0 && x.ld % 2 == 0 && x.col_end % 2 == 0;
+    for (int u0 = t; u0 < x.units; u0 += AHEAD * NT) {
+        uint32_t raw[AHEAD][8];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const int u = u0 + i * NT;
+            const int64_t r = x.row(u), c = x.col(u);
+            const bool in = u < x.units && r < x.row_end;
+            const int64_t at = r * x.ld + c;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                if constexpr (PL == 1) {
+                    if (pairs) {
+                        if (k < 4) raw[i][k] = in && c + 2 * k < x.col_end ? __ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(x.base) + at) + k) : 0;
+                    } else {
+                        raw[i][k] = in && c + k < x.col_end ? __ldg(static_cast<const uint16_t*>(x.base) + at + k) : 0;
+                    }
+                } else {
+                    raw[i][k] = in && c + k < x.col_end ? __ldg(static_cast<const uint32_t*>(x.base) + at + k) : 0;
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const int u = u0 + i * NT;
+            if (u >= x.units) break;
+            uint4 v[PL];
+            if constexpr (PL == 1) {
+                v[0] = pairs ? make_uint4(raw[i][0], raw[i][1], raw[i][2], raw[i][3])
+                             : make_uint4(raw[i][0] | raw[i][1] << 16, raw[i][2] | raw[i][3] << 16, raw[i][4] | raw[i][5] << 16, raw[i][6] | raw[i][7] << 16);
+            } else {
+                float f[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) f[k] = __uint_as_float(raw[i][k]);
+                split(f, v);
+            }
+#pragma unroll
+            for (int k = 0; k < PL; ++k) *reinterpret_cast<uint4*>(dst + k * plane + unit_place(u)) = v[k];
+        }
+    }
 }
 
 // Both operands of a stage, planes a_plane and b_plane bytes apart, by a
@@ -517,53 +546,42 @@ template <int PL>
 __device__ __forceinline__ void load_operands(const Operand& a, const Operand& b, unsigned char* sa, int a_plane,
                                               unsigned char* sb, int b_plane) {
     constexpr int AHEAD = 8, NT = LOAD_GROUP * 32, SIZE = PL == 1 ? 2 : 4;
-    const int t = threadIdx.x & (NT - 1), units = a.units + b.units;
-    auto place = [](int u) { return (u >> 9) * 8192 + swizzled(u >> 3 & 63, u & 7); };
-    if (whole_units<PL>(a) && whole_units<PL>(b)) {
-        for (int u0 = t; u0 < units; u0 += AHEAD * NT) {
-            uint4 raw[AHEAD][SIZE / 2];
-            bool in[AHEAD];
+    const int t = threadIdx.x & (NT - 1);
+    const bool whole_a = whole_units<PL>(a), whole_b = whole_units<PL>(b);
+    if (!whole_a) load_any<PL>(a, sa, a_plane);
+    if (!whole_b) load_any<PL>(b, sb, b_plane);
+    const int a_units = whole_a ? a.units : 0, units = a_units + (whole_b ? b.units : 0);
+    for (int u0 = t; u0 < units; u0 += AHEAD * NT) {
+        uint4 raw[AHEAD][SIZE / 2];
 #pragma unroll
-            for (int i = 0; i < AHEAD; ++i) {
-                const int u = u0 + i * NT;
-                const bool is_a = u < a.units;
-                const int q = is_a ? u : u - a.units;
-                const int64_t r = is_a ? a.row(q) : b.row(q), c = is_a ? a.col(q) : b.col(q);
-                in[i] = u < units && r < (is_a ? a.row_end : b.row_end) && c < (is_a ? a.col_end : b.col_end);
-                // elsewhere no load, and zeros instead of it
-                const int64_t at = (r * (is_a ? a.ld : b.ld) + c) * SIZE;
-                const uint4* src = reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(is_a ? a.base : b.base) + at);
+        for (int i = 0; i < AHEAD; ++i) {
+            const int u = u0 + i * NT;
+            const bool is_a = u < a_units;
+            const int q = is_a ? u : u - a_units;
+            const int64_t r = is_a ? a.row(q) : b.row(q), c = is_a ? a.col(q) : b.col(q);
+            const bool in = u < units && r < (is_a ? a.row_end : b.row_end) && c < (is_a ? a.col_end : b.col_end);
+            const int64_t at = (r * (is_a ? a.ld : b.ld) + c) * SIZE;
+            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(is_a ? a.base : b.base) + at);
 #pragma unroll
-                for (int k = 0; k < SIZE / 2; ++k) raw[i][k] = in[i] ? __ldg(src + k) : make_uint4(0, 0, 0, 0);
-            }
-#pragma unroll
-            for (int i = 0; i < AHEAD; ++i) {
-                const int u = u0 + i * NT;
-                if (u >= units) break;
-                uint4 v[PL];
-                if constexpr (PL == 1) {
-                    v[0] = raw[i][0];
-                } else {
-                    float f[8] = {__uint_as_float(raw[i][0].x), __uint_as_float(raw[i][0].y), __uint_as_float(raw[i][0].z), __uint_as_float(raw[i][0].w),
-                                  __uint_as_float(raw[i][1].x), __uint_as_float(raw[i][1].y), __uint_as_float(raw[i][1].z), __uint_as_float(raw[i][1].w)};
-                    split(f, v);
-                }
-                const bool is_a = u < a.units;
-                unsigned char* dst = (is_a ? sa : sb) + place(is_a ? u : u - a.units);
-#pragma unroll
-                for (int k = 0; k < PL; ++k) *reinterpret_cast<uint4*>(dst + k * (is_a ? a_plane : b_plane)) = v[k];
-            }
+            for (int k = 0; k < SIZE / 2; ++k) raw[i][k] = in ? __ldg(src + k) : make_uint4(0, 0, 0, 0);
         }
-        return;
-    }
-    for (int u = t; u < units; u += NT) {
-        const bool is_a = u < a.units;
-        uint4 v[PL];
-        if (is_a) load_unit<PL>(a, u, v);
-        else load_unit<PL>(b, u - a.units, v);
-        unsigned char* dst = (is_a ? sa : sb) + place(is_a ? u : u - a.units);
 #pragma unroll
-        for (int k = 0; k < PL; ++k) *reinterpret_cast<uint4*>(dst + k * (is_a ? a_plane : b_plane)) = v[k];
+        for (int i = 0; i < AHEAD; ++i) {
+            const int u = u0 + i * NT;
+            if (u >= units) break;
+            uint4 v[PL];
+            if constexpr (PL == 1) {
+                v[0] = raw[i][0];
+            } else {
+                float f[8] = {__uint_as_float(raw[i][0].x), __uint_as_float(raw[i][0].y), __uint_as_float(raw[i][0].z), __uint_as_float(raw[i][0].w),
+                              __uint_as_float(raw[i][1].x), __uint_as_float(raw[i][1].y), __uint_as_float(raw[i][1].z), __uint_as_float(raw[i][1].w)};
+                split(f, v);
+            }
+            const bool is_a = u < a_units;
+            unsigned char* dst = (is_a ? sa : sb) + unit_place(is_a ? u : u - a_units);
+#pragma unroll
+            for (int k = 0; k < PL; ++k) *reinterpret_cast<uint4*>(dst + k * (is_a ? a_plane : b_plane)) = v[k];
+        }
     }
 }
 
@@ -596,6 +614,7 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
     const int rank = CG == 2 ? static_cast<int>(cluster_rank()) : 0;
     const uint32_t first = blockIdx.x / CG, stride = gridDim.x / CG;
 
+    if (MODE == PRODUCT_FORWARD && p.index) grid_trigger();      // the adapters' kernel may start beside this one
     const bool is_near = p.S <= NEAR_SEGMENTS;
     const int* beg = is_near ? near : a.far;
     const int* pre = is_near ? near + NEAR_SEGMENTS + 1 : a.far + p.S + 1;
@@ -824,7 +843,7 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
         // ---- drain ----
         const int quarter = (warp - EPI_WARP) & 3, group = (warp - EPI_WARP) / 4;   // which lanes; which columns
         const int td = tid - EPI_WARP * 32;
-        constexpr int W = MODE == PRODUCT_ADAPTERS ? 8 : 32;      // columns at a time
+        constexpr int W = MODE == PRODUCT_ADAPTERS ? 8 : 32, ROWS = W * (EPW / 4);    // columns at a time; of all warps
         staging += (warp - EPI_WARP) * STAGING;
         LowRank<PL> low(p, tile_adapter, staging, lane);
         if (MODE == PRODUCT_FORWARD && !p.index) {
@@ -838,6 +857,9 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                 else static_cast<uint16_t*>(p.out)[r * p.ldo + c] = 0;
             }
         }
+        // the adapters' kernel starts beside the one that computes u, and
+        // copies and multiplies meanwhile; u and the scratch are used from here on
+        if (MODE == PRODUCT_ADAPTERS) grid_wait();
         uint32_t buf = 0, bph = 0;
         Item t;
         for (uint32_t i = first; i < items; i += stride) {
@@ -846,7 +868,7 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
             const int n_left = columns_of(t);
             const int64_t m = t.m0 + rank * MT + quarter * 32;           // the warp's first lane
             const int lanes = static_cast<int>(a.cols_m - m < 32 ? a.cols_m - m : 32);   // may be negative
-            const int64_t slot = (t.slot * CG + rank) * NT * MT + quarter * 32 + lane;      // in floats
+            const int64_t slot = (t.slot * CG + rank) * NT * MT + quarter * 32;      // in floats
             if constexpr (MODE == PRODUCT_ADAPTERS) {
                 bar_drain<EPW>();       // the table of the tile before has been read
                 for (int r = td; r < t.rows; r += EPW * 32) {
@@ -877,15 +899,14 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                 bool waiting = summed && !adding;
                 int c = group * W;
                 if constexpr (MODE == PRODUCT_ADAPTERS)
-                    if (final && !to_part) low.begin(t.row0, t.rows, m + lane, c);
+                    if (final && !adding) low.begin(t.row0, t.rows, m + lane, c + t.part * ROWS);
                 for (;;) {
                     float v[W];
-                    if (MODE == PRODUCT_ADAPTERS && final && !to_part && c < n_left) {
-                        if constexpr (MODE == PRODUCT_ADAPTERS) low.rows_of(v, c, c + W * (EPW / 4));
-                    } else {
 #pragma unroll
-                        for (int j = 0; j < W; ++j) v[j] = 0.0f;
-                    }
+                    for (int j = 0; j < W; ++j) v[j] = 0.0f;
+                    // the parts of a tile share its low-rank part
+                    if constexpr (MODE == PRODUCT_ADAPTERS)
+                        if (final && !adding && c < n_left && c / ROWS % t.parts == t.part) low.rows_of(v, c, c + ROWS * t.parts);
                     if (waiting) {
                         ok = bar_drain_all<EPW>(wait_for<CG>(acc_full + buf, bph, p.status));
                         if (!ok) break;
@@ -902,7 +923,7 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                             const float* part = a.partials + slot + (int64_t(q - t.part) * CG * NT + c) * MT;
 #pragma unroll
                             for (int j = 0; j < W; ++j)
-                                if (j < n) d[j] += __ldcg(part + j * MT);
+                                if (j < n) d[j] += __ldcg(part + j * MT + lane);
                         }
 #pragma unroll
                         for (int j = 0; j < W; ++j) v[j] += d[j];
@@ -916,22 +937,22 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                         for (int j = 0; j < W; ++j) v[j] += PL > 1 ? d[j] + lo[j] : d[j];
                         if (!fresh && (to_part || lane < lanes)) {
                             // the sum so far, float32 wherever there is more than one piece
-                            const float* so_far = to_part ? a.partials + slot + int64_t(c) * MT : static_cast<const float*>(p.out) + at + c * step + lane;
+                            const float* so_far = to_part ? a.partials + slot + int64_t(c) * MT : static_cast<const float*>(p.out) + at + c * step;
                             const int64_t s1 = to_part ? MT : step;
 #pragma unroll
                             for (int j = 0; j < W; ++j)
-                                if (j < n) v[j] += so_far[j * s1];
+                                if (j < n) v[j] += so_far[j * s1 + lane];
                         }
                     }
                     if (to_part) {
-                        store_rows(a.partials + slot + int64_t(c) * MT, MT, v, n, [](float x) { return x; });
+                        store_rows(a.partials + slot + int64_t(c) * MT + lane, MT, v, n, [](float x) { return x; });
                     } else {
                         if (MODE == PRODUCT_FORWARD && p.scale && final)
 #pragma unroll
                             for (int j = 0; j < W; ++j) v[j] *= factor;
                         store_result(a, at + c * step, step, v, n, lanes, lane, staging);
                     }
-                    c += W * (EPW / 4);
+                    c += ROWS;
                     if (c >= n_left) break;
                 }
                 if (!ok) break;
@@ -1035,6 +1056,58 @@ __global__ void __launch_bounds__(256) add_parts_kernel(const __grid_constant__ 
 int64_t ceil_to(int64_t n, int64_t d) { return (n + d - 1) / d; }
 
 // ---------------------------------------------------------------------------
+// u[r, j] = scale * sum_k x[r, k] a[l, j, k] where requests have a row or a
+// few: a warp per dot product, so that a's bytes (rank x K per request, bound
+// by latency and L2) are spread over the whole GPU; a 128-lane tile per
+// request would use 16 of its lanes and stream K through one SM.  96 rows of
+// 4,096 columns, rank 16: see launch_lora_rows.
+
+constexpr int DOT_RANKS = 8;      // warps of a block: ranks of one row
+
+template <class T> __device__ __forceinline__ float to_float(T v);
+template <> __device__ __forceinline__ float to_float<float>(float v) { return v; }
+template <> __device__ __forceinline__ float to_float<__half>(__half v) { return __half2float(v); }
+template <> __device__ __forceinline__ float to_float<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+template <class T>
+__global__ void __launch_bounds__(DOT_RANKS * 32) lora_rows_kernel(const __grid_constant__ ProductParams p) {
+    __shared__ int adapter;
+    grid_trigger();
+    const int64_t row = blockIdx.x;
+    const int lane = threadIdx.x & 31;
+    const int64_t j = int64_t(blockIdx.y) * DOT_RANKS + (threadIdx.x >> 5);
+    if (threadIdx.x == 0) adapter = -1;
+    __syncthreads();
+    for (int64_t s = threadIdx.x; s < p.S; s += DOT_RANKS * 32)
+        if (offset_at(p, s) <= row && row < offset_at(p, s + 1)) adapter = __ldg(p.index + s);
+    __syncthreads();
+    const int l = adapter;
+    if (l < 0 || l >= p.L || j >= p.N) return;
+    const T* x = static_cast<const T*>(p.x) + row * p.ldx;
+    const T* a = static_cast<const T*>(p.w) + (int64_t(l) * p.N + j) * p.K;
+    constexpr int V = 16 / sizeof(T);
+    float sum = 0.0f, sum2 = 0.0f;
+    if (((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(a)) & 15) == 0 && p.K % V == 0) {
+#pragma unroll 4
+        for (int64_t k = lane * V; k < p.K; k += 32 * V) {
+            const uint4 xr = __ldg(reinterpret_cast<const uint4*>(x + k)), ar = __ldg(reinterpret_cast<const uint4*>(a + k));
+            const T *xv = reinterpret_cast<const T*>(&xr), *av = reinterpret_cast<const T*>(&ar);
+#pragma unroll
+            for (int i = 0; i < V; i += 2) {
+                sum = fmaf(to_float(xv[i]), to_float(av[i]), sum);
+                sum2 = fmaf(to_float(xv[i + 1]), to_float(av[i + 1]), sum2);
+            }
+        }
+    } else {
+        for (int64_t k = lane; k < p.K; k += 32) sum = fmaf(to_float(__ldg(x + k)), to_float(__ldg(a + k)), sum);
+    }
+    sum += sum2;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    if (lane == 0) static_cast<float*>(p.out)[row * p.ldo + j] = sum * (p.scale ? __ldg(p.scale + l) : 1.0f);
+}
+
+// ---------------------------------------------------------------------------
 // Tensor maps: 16-bit values, boxes of 64 columns, 128-byte swizzle.
 
 typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
@@ -1102,17 +1175,27 @@ cudaError_t launch_shape(const KernelArgs& a, const ProductPlan& plan, cudaStrea
     }
     auto* kernel = product_kernel<MODE, TENSOR, NT, PL, CG>;
     constexpr int smem = Ring<NT, PL, CG>::SMEM;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = CG;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    int attrs = 0;
+    if (CG > 1) {
+        attr[attrs].id = cudaLaunchAttributeClusterDimension;
+        attr[attrs].val.clusterDim.x = CG;
+        attr[attrs].val.clusterDim.y = attr[attrs].val.clusterDim.z = 1;
+        ++attrs;
+    }
+    const bool overlap = MODE == PRODUCT_ADAPTERS && a.p.u;
+    if (overlap) {
+        attr[attrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[attrs].val.programmaticStreamSerializationAllowed = 1;
+        ++attrs;
+    }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(plan.grid);
     cfg.blockDim = dim3(TENSOR ? 384 : 512);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = attr;
-    cfg.numAttrs = CG > 1 ? 1 : 0;
+    cfg.numAttrs = CG > 1 ? 1 : 0;     // for the occupancy query
     static int resident[64] = {};       // most CTAs at a time, per device; callers hold the library's lock
     if (resident[dev] == 0) {
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -1125,6 +1208,7 @@ cudaError_t launch_shape(const KernelArgs& a, const ProductPlan& plan, cudaStrea
         }
         resident[dev] = clusters * CG;
     }
+    cfg.numAttrs = attrs;
     cfg.gridDim = dim3(std::min(plan.grid, resident[dev]));
     e = cudaLaunchKernelEx(&cfg, kernel, a, ma, mb);
     if (e != cudaSuccess || plan.add_blocks == 0) return e;
@@ -1199,6 +1283,16 @@ ProductPlan plan_product(int mode, const ProductParams& p) {
     d.prefix_bytes = mode != PRODUCT_ADAPTERS && p.S > NEAR_SEGMENTS ? ceil_to((p.S + 1) * 8, 256) * 256 : 0;
     d.partial_bytes = slots * cg * NT * MT * 4;
     return d;
+}
+
+bool lora_by_rows(const ProductParams& p) { return p.R <= 4 * p.S && p.S <= 4096; }
+
+cudaError_t launch_lora_rows(const ProductParams& p, cudaStream_t stream) {
+    const dim3 grid(static_cast<unsigned>(p.R), static_cast<unsigned>(ceil_to(p.N, DOT_RANKS)));
+    if (p.type == PT_F32) lora_rows_kernel<float><<<grid, DOT_RANKS * 32, 0, stream>>>(p);
+    else if (p.type == PT_F16) lora_rows_kernel<__half><<<grid, DOT_RANKS * 32, 0, stream>>>(p);
+    else lora_rows_kernel<__nv_bfloat16><<<grid, DOT_RANKS * 32, 0, stream>>>(p);
+    return cudaGetLastError();
 }
 
 cudaError_t launch_product(int mode, const ProductParams& p, const ProductPlan& plan, cudaStream_t stream) {

@@ -65,4 +65,9 @@ enum : int { PRODUCT_FORWARD = 0, PRODUCT_WEIGHTS = 1, PRODUCT_ADAPTERS = 2 };
 ProductPlan plan_product(int mode, const ProductParams& p);
 cudaError_t launch_product(int mode, const ProductParams& p, const ProductPlan& plan, cudaStream_t stream);
 
+// u of the adapters (forward with index, rank columns, float32 result) for
+// calls with a few rows per segment at most.
+bool lora_by_rows(const ProductParams& p);
+cudaError_t launch_lora_rows(const ProductParams& p, cudaStream_t stream);
+
 }  // namespace segred

@@ -204,6 +204,10 @@ __device__ __forceinline__ void tmem_wait(float (&v)[8]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]) : : "memory");
 }
 
+// Lets the next kernel of the stream start, if it was launched to overlap; waits for the kernel before.
+__device__ __forceinline__ void grid_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Shared-memory matrix descriptor, 128-byte swizzle: rows of 128 bytes in
 // groups of 8 (1,024 bytes).  Contraction-major operand: `lead` unused.
 // Otherwise a row holds 64 values of the outer dimension and `lead` is the
