@@ -44,9 +44,9 @@ namespace {
 constexpr int KB = 64;                    // steps of the sum per stage: 128-byte rows of 16-bit values
 constexpr int MT = 128;                   // lanes of a tile
 constexpr int NEAR_SEGMENTS = 1024;       // up to here every CTA keeps the offsets in shared memory
-constexpr int EPI_WARP = 4;               // the drain warps start here (their index mod 4 names their lanes)
-constexpr int LOAD_WARP = 8, LOAD_GROUP = 4;   // loader warps: two groups of four that take turns at the stages
-constexpr int STAGING = 2048;             // bytes of a drain warp's own shared memory
+constexpr int EPI_WARP = 4, EPW = 8;      // drain warps: their index mod 4 names their lanes, and the two of a quarter take turns at the columns
+constexpr int LOAD_WARP = 12, LOAD_GROUP = 4;   // loader warps: two groups of four that take turns at the stages
+constexpr int TENSOR_THREADS = 384, LOADER_THREADS = 640;
 constexpr int NEVER_FLUSH = 1 << 28;         // more blocks than any sum has
 constexpr unsigned STATUS_PRODUCT_TIMEOUT = 8u;
 
@@ -59,9 +59,10 @@ struct Ring {
     static constexpr int ACC = PL == 1 ? NT : 2 * NT;            // tensor-memory columns of one accumulator
     static constexpr int BARS = 3 * STAGES + 5;
     // the drain warps' staging; PL == 3 keeps it (adapters alone need it there) in the space of the offsets
-    static constexpr int STAGED = PL == 1 ? 8 * STAGING : 0;
+    static constexpr int STAGING = PL == 1 ? 2048 : 1024;
+    static constexpr int STAGED = PL == 1 ? EPW * STAGING : 0;
     static constexpr int NEAR = 2 * (NEAR_SEGMENTS + 1) * 4;
-    static_assert(NEAR >= 4 * STAGING, "room for the staging of four warps");
+    static_assert(NEAR >= EPW * 1024, "room for that staging");
     static constexpr int SMEM = STAGES * STAGE + STAGED + NEAR + BARS * 8 + 64 + NT * 4 + 1024;   // 1024: alignment of the stages
     static_assert(SMEM <= 232448, "shared memory of an SM");
 };
@@ -134,6 +135,7 @@ __global__ void __launch_bounds__(1024) prefix_kernel(const __grid_constant__ Ke
 
 struct Item {
     int seg = 0;
+    int each_of = -1, each = 0;      // forward: rows of a tile of segment each_of
     int row0, rows;     // forward: the tile's rows; weights: the rows it sums over
     int m0, n0;
     int kb0, kb1;       // 64-wide blocks of the sum
@@ -196,22 +198,24 @@ __device__ __forceinline__ void item_at(const KernelArgs& a, const int* beg, con
         t.ticket = 0;
     } else {
         // the segment's rows in equal tiles of a multiple of 16
-        int each = ((len + count - 1) / count + 15) & ~15;
-        each = each < NT ? each : NT;
+        if (t.each_of != t.seg) {
+            t.each_of = t.seg;
+            t.each = ((len + count - 1) / count + 15) & ~15;
+            t.each = t.each < NT ? t.each : NT;
+        }
+        const int each = t.each;
         t.row0 = b + j * each;
         t.rows = len - j * each < each ? len - j * each : each;
         t.kb0 = t.part * a.part_blocks;
         t.kb1 = min(t.kb0 + a.part_blocks, a.kblocks);
         t.parts = a.parts;
         t.slot = i;
-        t.ticket = i / a.parts;
+        t.ticket = a.parts > 1 ? i / a.parts : 0;
     }
 }
 
-template <int EPW>
 __device__ __forceinline__ void bar_drain() { asm volatile("bar.sync 1, %0;" ::"n"(EPW * 32) : "memory"); }
 // The same, and whether `ok` holds in all the drain warps: they give up together or not at all.
-template <int EPW>
 __device__ __forceinline__ bool bar_drain_all(bool ok) {
     uint32_t r;
     asm volatile(
@@ -312,11 +316,11 @@ __device__ __forceinline__ void store_result(const KernelArgs& a, int64_t at, in
 // warp's staging, b to the registers of the column's lane.  What a step needs
 // is fetched during the step before; where the 8 rows have different
 // adapters (a decode step), their b are fetched together at the step itself.
-template <int PL>
+template <int PL, bool TENSOR>
 struct LowRank {
     static constexpr int SIZE = PL == 1 ? 2 : 4;
     static constexpr int WORDS = 16 * SIZE / 4;          // of 16 ranks
-    static constexpr int AHEAD = PL == 1 ? 8 : 2;        // rows whose b are fetched together
+    static constexpr int AHEAD = TENSOR ? 8 : 2;         // rows whose b are fetched together (as registers allow)
     const ProductParams& p;
     const int* tile_adapter;
     float4* su;                                          // [8 rows][4]
@@ -545,7 +549,7 @@ __device__ __forceinline__ void load_any(const Operand& x, unsigned char* dst, i
 template <int PL>
 __device__ __forceinline__ void load_operands(const Operand& a, const Operand& b, unsigned char* sa, int a_plane,
                                               unsigned char* sb, int b_plane) {
-    constexpr int AHEAD = 8, NT = LOAD_GROUP * 32, SIZE = PL == 1 ? 2 : 4;
+    constexpr int AHEAD = PL == 1 ? 8 : 4, NT = LOAD_GROUP * 32, SIZE = PL == 1 ? 2 : 4;
     const int t = threadIdx.x & (NT - 1);
     const bool whole_a = whole_units<PL>(a), whole_b = whole_units<PL>(b);
     if (!whole_a) load_any<PL>(a, sa, a_plane);
@@ -588,13 +592,12 @@ __device__ __forceinline__ void load_operands(const Operand& a, const Operand& b
 // ---------------------------------------------------------------------------
 
 template <int MODE, bool TENSOR, int NT, int PL, int CG>
-__global__ void __launch_bounds__(TENSOR ? 384 : 512, 1)
+__global__ void __launch_bounds__(TENSOR ? TENSOR_THREADS : LOADER_THREADS, 1)
 product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUtensorMap map_a,
                const __grid_constant__ CUtensorMap map_b) {
     using R = Ring<NT, PL, CG>;
     static_assert(CG == 1 || TENSOR, "pairs load by tensor copies");
     constexpr int BOX_ROWS = NT <= 64 ? 16 : 64;     // rows of one copy of x (forward)
-    constexpr int EPW = TENSOR ? 8 : 4;              // drain warps: pairs of them share lanes and take turns at the columns
     extern __shared__ unsigned char raw[];
     unsigned char* stages = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
     unsigned char* staging = stages + R::STAGES * R::STAGE;      // 16-byte aligned, as all that follows it
@@ -843,9 +846,9 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
         // ---- drain ----
         const int quarter = (warp - EPI_WARP) & 3, group = (warp - EPI_WARP) / 4;   // which lanes; which columns
         const int td = tid - EPI_WARP * 32;
-        constexpr int W = MODE == PRODUCT_ADAPTERS ? 8 : 32, ROWS = W * (EPW / 4);    // columns at a time; of all warps
-        staging += (warp - EPI_WARP) * STAGING;
-        LowRank<PL> low(p, tile_adapter, staging, lane);
+        constexpr int W = MODE == PRODUCT_ADAPTERS ? 8 : (TENSOR ? 32 : 16), ROWS = W * (EPW / 4);    // columns at a time; of all warps
+        staging += (warp - EPI_WARP) * R::STAGING;
+        LowRank<PL, TENSOR> low(p, tile_adapter, staging, lane);
         if (MODE == PRODUCT_FORWARD && !p.index) {
             // rows in no segment
             const int b = p.S > 0 ? beg[0] : 0, e = p.S > 0 ? beg[p.S] : 0;
@@ -870,7 +873,7 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
             const int lanes = static_cast<int>(a.cols_m - m < 32 ? a.cols_m - m : 32);   // may be negative
             const int64_t slot = (t.slot * CG + rank) * NT * MT + quarter * 32;      // in floats
             if constexpr (MODE == PRODUCT_ADAPTERS) {
-                bar_drain<EPW>();       // the table of the tile before has been read
+                bar_drain();       // the table of the tile before has been read
                 for (int r = td; r < t.rows; r += EPW * 32) {
                     const int row = t.row0 + r;
                     int64_t lo = 0, hi = p.S;      // the last segment that starts at or before the row
@@ -882,7 +885,7 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                     if (p.S > 0 && offset_at(p, lo) <= row && row < offset_at(p, lo + 1)) l = __ldg(p.index + lo);
                     tile_adapter[r] = l >= 0 && l < p.L ? l : -1;
                 }
-                bar_drain<EPW>();
+                bar_drain();
             }
             float factor = 1.0f;
             if (MODE == PRODUCT_FORWARD && p.scale) factor = __ldg(p.scale + __ldg(p.index + t.seg));
@@ -908,7 +911,7 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                     if constexpr (MODE == PRODUCT_ADAPTERS)
                         if (final && !adding && c < n_left && c / ROWS % t.parts == t.part) low.rows_of(v, c, c + ROWS * t.parts);
                     if (waiting) {
-                        ok = bar_drain_all<EPW>(wait_for<CG>(acc_full + buf, bph, p.status));
+                        ok = bar_drain_all(wait_for<CG>(acc_full + buf, bph, p.status));
                         if (!ok) break;
                         tc_fence_after();
                         waiting = false;
@@ -964,7 +967,7 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                 }
                 piece = final ? t.kb1 : piece + a.flush;
                 if (MODE != PRODUCT_WEIGHTS && to_part && final) {
-                    bar_drain<EPW>();     // the release below covers what the others wrote before it
+                    bar_drain();     // the release below covers what the others wrote before it
                     if (td == 0) {
                         unsigned long long* ticket = a.tickets + t.ticket * CG + rank;
                         red_max_relaxed_gpu(ticket, static_cast<unsigned long long>(p.gen) << 32);
@@ -972,7 +975,7 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                         fence_acq_rel_gpu();
                         *last_part = static_cast<uint32_t>(old) + 1 == static_cast<uint32_t>(t.parts);
                     }
-                    bar_drain<EPW>();
+                    bar_drain();
                     adding = *last_part;
                     if (adding) {
                         piece = t.kb1 - 1;      // once more around, as the final piece
@@ -1191,7 +1194,7 @@ cudaError_t launch_shape(const KernelArgs& a, const ProductPlan& plan, cudaStrea
     }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(plan.grid);
-    cfg.blockDim = dim3(TENSOR ? 384 : 512);
+    cfg.blockDim = dim3(TENSOR ? TENSOR_THREADS : LOADER_THREADS);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = attr;
