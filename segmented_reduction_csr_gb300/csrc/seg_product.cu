@@ -45,17 +45,18 @@ constexpr int KB = 64;                    // steps of the sum per stage: 128-byt
 constexpr int MT = 128;                   // lanes of a tile
 constexpr int NEAR_SEGMENTS = 1024;       // up to here every CTA keeps the offsets in shared memory
 constexpr int EPI_WARP = 4, EPW = 8;      // drain warps: their index mod 4 names their lanes, and the two of a quarter take turns at the columns
-constexpr int LOAD_WARP = 12, LOAD_GROUP = 4;   // loader warps: two groups of four that take turns at the stages
+constexpr int LOAD_WARP = 12, LOADERS = 256;    // loader warps start here; their threads
 constexpr int TENSOR_THREADS = 384, LOADER_THREADS = 640;
 constexpr int NEVER_FLUSH = 1 << 28;         // more blocks than any sum has
 constexpr unsigned STATUS_PRODUCT_TIMEOUT = 8u;
 
 // Stage ring of a kernel shape: PL 16-bit planes per operand, CG CTAs that share a tile.
-template <int NT, int PL, int CG>
+template <int NT, int PL, int CG, bool TENSOR>
 struct Ring {
     static constexpr int A_PLANE = MT * 128, B_PLANE = NT / CG * 128;
     static constexpr int STAGE = PL * (A_PLANE + B_PLANE);
-    static constexpr int STAGES = std::min(8, (PL == 1 ? 200704 : 221184) / STAGE);
+    // (the loaders' plain loads are tracked in the L1 that shared memory leaves)
+    static constexpr int STAGES = std::min(8, (PL == 3 ? 221184 : TENSOR ? 200704 : 98304) / STAGE);
     static constexpr int ACC = PL == 1 ? NT : 2 * NT;            // tensor-memory columns of one accumulator
     static constexpr int BARS = 3 * STAGES + 5;
     // the drain warps' staging; PL == 3 keeps it (adapters alone need it there) in the space of the offsets
@@ -316,11 +317,11 @@ __device__ __forceinline__ void store_result(const KernelArgs& a, int64_t at, in
 // warp's staging, b to the registers of the column's lane.  What a step needs
 // is fetched during the step before; where the 8 rows have different
 // adapters (a decode step), their b are fetched together at the step itself.
-template <int PL, bool TENSOR>
+template <int PL, bool WIDE>
 struct LowRank {
     static constexpr int SIZE = PL == 1 ? 2 : 4;
     static constexpr int WORDS = 16 * SIZE / 4;          // of 16 ranks
-    static constexpr int AHEAD = TENSOR ? 8 : 2;         // rows whose b are fetched together (as registers allow)
+    static constexpr int AHEAD = WIDE ? 8 : 2;           // rows whose b are fetched together (as registers allow)
     const ProductParams& p;
     const int* tile_adapter;
     float4* su;                                          // [8 rows][4]
@@ -451,64 +452,66 @@ struct LowRank {
 // The loader warps: blocks of a row-major matrix into 128-byte swizzled rows,
 // zero outside [.., row_end) x [.., col_end).
 
-// One operand of a stage.  `units` of 8 values each; 8 units to a 128-byte
-// row of shared memory, 64 rows to 8,192 bytes.  outer: every 64 rows are
-// the block's 64 steps of the sum for the next 64 columns; else unit u is
-// columns of row u / 8.
+// One operand of a stage: `rows` 128-byte rows of shared memory, 64 values
+// each.  outer: every 64 rows are the block's 64 steps of the sum for the
+// next 64 columns; else they are rows of the matrix.
 struct Operand {
     const void* base;
     int64_t ld;
     int64_t row0, row_end;
     int64_t col0, col_end;
-    int units;
+    int rows;
     bool outer;
-    __device__ __forceinline__ int64_t row(int u) const { return row0 + (outer ? u >> 3 & 63 : u >> 3); }
-    __device__ __forceinline__ int64_t col(int u) const { return col0 + (u & 7) * 8 + (outer ? u >> 9 << 6 : 0); }
 };
 
-__device__ __forceinline__ uint32_t swizzled(int row, int unit) {
-    return static_cast<uint32_t>(row * 128 + ((unit ^ (row & 7)) << 4));
-}
-
-// The three parts of 8 float32 values.
-__device__ __forceinline__ void split(float (&f)[8], uint4 (&v)[3]) {
-    uint32_t part[3][8];
+// The three bfloat16 parts of two values: by truncation, each rest exact.
+__device__ __forceinline__ void split_pair(float x, float y, uint32_t (&r)[3]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-#pragma unroll
-        for (int k = 0; k < 3; ++k) {
-            part[k][i] = __float_as_uint(f[i]);                      // its upper half: the rest is exact
-            f[i] -= __uint_as_float(part[k][i] & 0xffff0000u);
-        }
+    for (int k = 0; k < 3; ++k) {
+        r[k] = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
+        x -= __uint_as_float(r[k] << 16);
+        y -= __uint_as_float(r[k] & 0xffff0000u);
     }
+}
+
+// float32 rows of 64 values that tensor copies left in the second (values 0
+// to 31) and third plane, into their parts in all three.  A warp takes two
+// whole rows at a time, and writes when all of it has been read.
+__device__ __forceinline__ void split_rows(int rows, int valid, unsigned char* dst, int plane) {
+    const int t = threadIdx.x - LOAD_WARP * 32, q = t & 15, row = t >> 4;      // 16 bytes q of the row; 8 units of 8 values
+    const unsigned char* from = dst + row * 128 + (1 + (q >> 3)) * plane + (((q & 7) ^ (row & 7)) << 4);
+    unsigned char* to = dst + row * 128 + (((q >> 1) ^ (row & 7)) << 4) + (q & 1) * 8;
+    constexpr int STEP = LOADERS / 16;
+#pragma unroll 2
+    for (int r = row; r - row < rows; r += STEP) {
+        float4 x = *reinterpret_cast<const float4*>(from);
+        if ((r & 63) >= valid) x = make_float4(0, 0, 0, 0);
+        __syncwarp();
+        uint32_t a[3], b[3];
+        split_pair(x.x, x.y, a);
+        split_pair(x.z, x.w, b);
 #pragma unroll
-    for (int k = 0; k < 3; ++k)
-        v[k] = make_uint4(__byte_perm(part[k][0], part[k][1], 0x7632), __byte_perm(part[k][2], part[k][3], 0x7632),
-                          __byte_perm(part[k][4], part[k][5], 0x7632), __byte_perm(part[k][6], part[k][7], 0x7632));
+        for (int k = 0; k < 3; ++k) *reinterpret_cast<uint2*>(to + k * plane) = make_uint2(a[k], b[k]);
+        from += STEP * 128;
+        to += STEP * 128;
+    }
 }
 
-// Where the units of an operand are whole and 16-byte aligned.
-template <int PL>
-__device__ __forceinline__ bool whole_units(const Operand& x) {
-    return ((reinterpret_cast<uintptr_t>(x.base) | static_cast<uint64_t>(x.ld * (PL == 1 ? 2 : 4))) & 15) == 0 && x.col_end % 8 == 0;
-}
-
-__device__ __forceinline__ int unit_place(int u) { return (u >> 9) * 8192 + swizzled(u >> 3 & 63, u & 7); }
-
-// An operand of any alignment, value by value (16-bit: in pairs where its
-// rows allow that), the loads of AHEAD units together.
+// An operand of any alignment, by all loaders: 8 values of a row per thread,
+// one by one (16-bit: in pairs where its rows allow that), the loads of two
+// units together.
 template <int PL>
 __device__ __forceinline__ void load_any(const Operand& x, unsigned char* dst, int plane) {
-    constexpr int AHEAD = 2, NT = LOAD_GROUP * 32;
-    const int t = threadIdx.x & (NT - 1);
+    constexpr int AHEAD = 2;
+    const int t = threadIdx.x - LOAD_WARP * 32, unit = t & 7;
     const bool pairs = PL == 1 && (reinterpret_cast<uintptr_t>(x.base) & 3) == 0 && x.ld % 2 == 0 && x.col_end % 2 == 0;
-    for (int u0 = t; u0 < x.units; u0 += AHEAD * NT) {
+    for (int row0 = t >> 3; row0 < x.rows; row0 += AHEAD * LOADERS / 8) {
         uint32_t raw[AHEAD][8];
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
-            const int u = u0 + i * NT;
-            const int64_t r = x.row(u), c = x.col(u);
-            const bool in = u < x.units && r < x.row_end;
+            const int row = row0 + i * LOADERS / 8;
+            const int64_t r = x.row0 + (x.outer ? row & 63 : row), c = x.col0 + unit * 8 + (x.outer ? row & ~63 : 0);
+            const bool in = row < x.rows && r < x.row_end;
             const int64_t at = r * x.ld + c;
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
@@ -525,78 +528,54 @@ __device__ __forceinline__ void load_any(const Operand& x, unsigned char* dst, i
         }
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
-            const int u = u0 + i * NT;
-            if (u >= x.units) break;
-            uint4 v[PL];
+            const int row = row0 + i * LOADERS / 8;
+            if (row >= x.rows) break;
+            unsigned char* to = dst + row * 128 + ((unit ^ (row & 7)) << 4);
             if constexpr (PL == 1) {
-                v[0] = pairs ? make_uint4(raw[i][0], raw[i][1], raw[i][2], raw[i][3])
-                             : make_uint4(raw[i][0] | raw[i][1] << 16, raw[i][2] | raw[i][3] << 16, raw[i][4] | raw[i][5] << 16, raw[i][6] | raw[i][7] << 16);
+                *reinterpret_cast<uint4*>(to) =
+                    pairs ? make_uint4(raw[i][0], raw[i][1], raw[i][2], raw[i][3])
+                          : make_uint4(raw[i][0] | raw[i][1] << 16, raw[i][2] | raw[i][3] << 16, raw[i][4] | raw[i][5] << 16, raw[i][6] | raw[i][7] << 16);
             } else {
-                float f[8];
+                uint32_t part[4][3];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) f[k] = __uint_as_float(raw[i][k]);
-                split(f, v);
+                for (int k = 0; k < 4; ++k) split_pair(__uint_as_float(raw[i][2 * k]), __uint_as_float(raw[i][2 * k + 1]), part[k]);
+#pragma unroll
+                for (int k = 0; k < 3; ++k) *reinterpret_cast<uint4*>(to + k * plane) = make_uint4(part[0][k], part[1][k], part[2][k], part[3][k]);
             }
-#pragma unroll
-            for (int k = 0; k < PL; ++k) *reinterpret_cast<uint4*>(dst + k * plane + unit_place(u)) = v[k];
         }
     }
 }
 
-// Both operands of a stage, planes a_plane and b_plane bytes apart, by a
-// loader group's 128 threads.  Where every unit is whole, the loads of AHEAD
-// units, of either operand, go out together without branches between them.
-template <int PL>
-__device__ __forceinline__ void load_operands(const Operand& a, const Operand& b, unsigned char* sa, int a_plane,
-                                              unsigned char* sb, int b_plane) {
-    constexpr int AHEAD = PL == 1 ? 8 : 4, NT = LOAD_GROUP * 32, SIZE = PL == 1 ? 2 : 4;
-    const int t = threadIdx.x & (NT - 1);
-    const bool whole_a = whole_units<PL>(a), whole_b = whole_units<PL>(b);
-    if (!whole_a) load_any<PL>(a, sa, a_plane);
-    if (!whole_b) load_any<PL>(b, sb, b_plane);
-    const int a_units = whole_a ? a.units : 0, units = a_units + (whole_b ? b.units : 0);
-    for (int u0 = t; u0 < units; u0 += AHEAD * NT) {
-        uint4 raw[AHEAD][SIZE / 2];
+// Whether the stage of a block already holds its A operand: with two stages
+// and a sum of one or two blocks, every tile of a segment and the one before
+// use the same.  STREAMS: 1 for a role that sees every second block, which is
+// always in one stage, 2 for one that sees all.
+template <int MODE, bool ON, int STREAMS>
+struct Kept {
+    int seg[STREAMS], m0[STREAMS], kb[STREAMS];
+    __device__ __forceinline__ Kept() {
 #pragma unroll
-        for (int i = 0; i < AHEAD; ++i) {
-            const int u = u0 + i * NT;
-            const bool is_a = u < a_units;
-            const int q = is_a ? u : u - a_units;
-            const int64_t r = is_a ? a.row(q) : b.row(q), c = is_a ? a.col(q) : b.col(q);
-            const bool in = u < units && r < (is_a ? a.row_end : b.row_end) && c < (is_a ? a.col_end : b.col_end);
-            const int64_t at = (r * (is_a ? a.ld : b.ld) + c) * SIZE;
-            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(is_a ? a.base : b.base) + at);
-#pragma unroll
-            for (int k = 0; k < SIZE / 2; ++k) raw[i][k] = in ? __ldg(src + k) : make_uint4(0, 0, 0, 0);
-        }
-#pragma unroll
-        for (int i = 0; i < AHEAD; ++i) {
-            const int u = u0 + i * NT;
-            if (u >= units) break;
-            uint4 v[PL];
-            if constexpr (PL == 1) {
-                v[0] = raw[i][0];
-            } else {
-                float f[8] = {__uint_as_float(raw[i][0].x), __uint_as_float(raw[i][0].y), __uint_as_float(raw[i][0].z), __uint_as_float(raw[i][0].w),
-                              __uint_as_float(raw[i][1].x), __uint_as_float(raw[i][1].y), __uint_as_float(raw[i][1].z), __uint_as_float(raw[i][1].w)};
-                split(f, v);
-            }
-            const bool is_a = u < a_units;
-            unsigned char* dst = (is_a ? sa : sb) + unit_place(is_a ? u : u - a_units);
-#pragma unroll
-            for (int k = 0; k < PL; ++k) *reinterpret_cast<uint4*>(dst + k * (is_a ? a_plane : b_plane)) = v[k];
-        }
+        for (int i = 0; i < STREAMS; ++i) seg[i] = -1;
     }
-}
+    __device__ __forceinline__ bool a(const Item& t, int block) {
+        if (!ON || MODE == PRODUCT_WEIGHTS) return false;
+        const bool same = seg[0] == t.seg && m0[0] == t.m0 && kb[0] == block;
+#pragma unroll
+        for (int i = 0; i + 1 < STREAMS; ++i) seg[i] = seg[i + 1], m0[i] = m0[i + 1], kb[i] = kb[i + 1];
+        seg[STREAMS - 1] = t.seg, m0[STREAMS - 1] = t.m0, kb[STREAMS - 1] = block;
+        return same;
+    }
+};
 
 // ---------------------------------------------------------------------------
 
 template <int MODE, bool TENSOR, int NT, int PL, int CG>
-__global__ void __launch_bounds__(TENSOR ? TENSOR_THREADS : LOADER_THREADS, 1)
+__global__ void __launch_bounds__(TENSOR && PL == 1 ? TENSOR_THREADS : LOADER_THREADS, 1)
 product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUtensorMap map_a,
                const __grid_constant__ CUtensorMap map_b) {
-    using R = Ring<NT, PL, CG>;
-    static_assert(CG == 1 || TENSOR, "pairs load by tensor copies");
+    using R = Ring<NT, PL, CG, TENSOR>;
+    static_assert(CG == 1 || (TENSOR && PL == 1), "pairs take their operands as they are copied");
+    constexpr int HALVES = PL == 1 ? 1 : 2;          // copies of 128 bytes that make 64 values
     constexpr int BOX_ROWS = NT <= 64 ? 16 : 64;     // rows of one copy of x (forward)
     extern __shared__ unsigned char raw[];
     unsigned char* stages = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
@@ -624,7 +603,7 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
     if (warp == 0) tmem_alloc<CG>(tmem_at, 2 * R::ACC);
     if (tid == 0) {
         for (int i = 0; i < R::STAGES; ++i) {
-            mbar_init(full + i, TENSOR ? CG : LOAD_GROUP);
+            mbar_init(full + i, TENSOR && PL == 1 ? CG : LOADERS / 32);
             mbar_init(empty + i, 1);
             mbar_init(landed + i, 1);
         }
@@ -664,17 +643,17 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
     };
     auto share_of = [&](int columns) { return ((columns + CG - 1) / CG + 15) & ~15; };
     // The last block of a weights' sum reaches past the segment: those rows are zeroed once they have arrived.
-    auto has_tail = [&](const Item& t, int kb) { return MODE == PRODUCT_WEIGHTS && kb + 1 == t.kb1 && (t.rows & 15) != 0; };
+    auto has_tail = [&](const Item& t, int kb) { return PL == 1 && MODE == PRODUCT_WEIGHTS && kb + 1 == t.kb1 && (t.rows & 15) != 0; };
 
-    if (TENSOR ? (warp == 1 || warp == 3) : warp >= LOAD_WARP) {
+    if (TENSOR && (warp == 1 || warp == 3)) {
         // ---- producers: two, which take turns at the blocks (one thread's
         // chain of wait, expect and copies for a block took longer than its MMAs) ----
-        const uint32_t turn = TENSOR ? warp >> 1 : (warp - LOAD_WARP) / LOAD_GROUP;
-        if (!TENSOR || elect_one()) {
+        const uint32_t turn = warp >> 1;
+        if (elect_one()) {
             uint32_t next = turn, base = 0;                // this producer's next block; the item's first
             uint32_t st = turn % R::STAGES, ph = turn < R::STAGES ? 1 : 0;
             bool ok = true;
-            int held_seg = -1, held_m0 = 0, held_kb = 0;   // the A operand that the producer's stage holds (two stages)
+            Kept<MODE, R::STAGES == 2 && PL == 3, 1> keeps;
             Item t;
             for (uint32_t i = first; ok && i < items; i += stride) {
                 item_at<MODE, NT, CG>(a, beg, pre, i, t);
@@ -682,8 +661,7 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                 const int columns = columns_of(t), share = share_of(columns), lanes = lanes_of(t);
                 const int a_boxes = a_outer ? (lanes + 63) / 64 : (lanes + MT - 1) / MT;
                 const int b_boxes = b_outer ? (share + 63) / 64 : (share + BOX_ROWS - 1) / BOX_ROWS;
-                const uint32_t b_bytes = b_boxes * (b_outer ? 8192 : BOX_ROWS * 128);
-                const uint32_t bytes = a_boxes * (a_outer ? 8192 : R::A_PLANE) + b_bytes;
+                const uint32_t a_bytes = a_boxes * (a_outer ? 8192 : R::A_PLANE) * HALVES, b_bytes = b_boxes * (b_outer ? 8192 : BOX_ROWS * 128) * HALVES;
                 const int m0 = t.m0 + rank * MT;
                 uint32_t other_bytes = 0;
                 if (CG == 2) {
@@ -695,54 +673,39 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                 if (MODE == PRODUCT_FORWARD && p.index) m = __ldg(p.index + t.seg);
                 for (; next - base < blocks; next += 2) {
                     const int kb = t.kb0 + static_cast<int>(next - base);
-                    ok = TENSOR ? wait_for<CG>(empty + st, ph, p.status) : warp_wait<CG>(empty + st, ph, p.status);
+                    ok = wait_for<CG>(empty + st, ph, p.status);
                     if (!ok) break;
                     unsigned char* sa = stages + st * R::STAGE;
                     unsigned char* sb = sa + PL * R::A_PLANE;
-                    if constexpr (TENSOR) {
-                        const bool tail = has_tail(t, kb);
-                        const uint32_t bar = tail ? smem_u32(landed + st) : lead_addr<CG>(full + st);
-                        if (tail) {
-                            mbar_arrive_expect_tx(landed + st, bytes);
-                        } else if (rank == 0) {      // both arrivals, and the bytes of both CTAs
-                            mbar_arrive_expect_tx(full + st, bytes + other_bytes);
-                            if (CG == 2) mbar_arrive(full + st);
-                        }
+                    const bool tail = has_tail(t, kb);
+                    const uint32_t bar = tail || PL > 1 ? smem_u32(landed + st) : lead_addr<CG>(full + st);
+                    const bool keep = keeps.a(t, kb);
+                    if (tail || PL > 1) {
+                        mbar_arrive_expect_tx(landed + st, (keep ? 0 : a_bytes) + b_bytes);
+                    } else if (rank == 0) {      // both arrivals, and the bytes of both CTAs
+                        mbar_arrive_expect_tx(full + st, a_bytes + b_bytes + other_bytes);
+                        if (CG == 2) mbar_arrive(full + st);
+                    }
+#pragma unroll
+                    for (int h = 0; h < HALVES; ++h) {
+                        unsigned char* da = sa + (PL == 1 ? 0 : (1 + h) * R::A_PLANE);
+                        unsigned char* db = sb + (PL == 1 ? 0 : (1 + h) * R::B_PLANE);
                         if (MODE == PRODUCT_WEIGHTS) {
-                            const int r = t.row0 + kb * KB, n0 = t.n0 + rank * share;
-                            for (int x = 0; x < a_boxes; ++x) tensor_load_2d<CG>(sa + x * 8192, &map_a, m0 + x * 64, r, bar);
-                            for (int x = 0; x < b_boxes; ++x) tensor_load_2d<CG>(sb + x * 8192, &map_b, n0 + x * 64, r, bar);
+                            const int r = t.row0 + kb * KB, n0 = t.n0 + rank * share + h * 32;
+                            for (int x = 0; x < a_boxes; ++x) tensor_load_2d<CG>(da + x * 8192, &map_a, m0 + x * 64 + h * 32, r, bar);
+                            for (int x = 0; x < b_boxes; ++x) tensor_load_2d<CG>(db + x * 8192, &map_b, n0 + x * 64, r, bar);
                         } else {
-                            const int r0 = t.row0 + rank * share;
-                            if (a_outer) {
+                            const int r0 = t.row0 + rank * share, k0 = kb * KB;
+                            if (keep) {
+                            } else if (a_outer) {
                                 for (int x = 0; x < a_boxes; ++x)
-                                    tensor_load_3d<CG>(sa + x * 8192, &map_a, m0 + x * 64, kb * KB, static_cast<int>(m), bar);
+                                    tensor_load_3d<CG>(da + x * 8192, &map_a, m0 + x * 64 + h * 32, k0, static_cast<int>(m), bar);
                             } else if (a_boxes > 0) {
-                                tensor_load_3d<CG>(sa, &map_a, kb * KB, m0, static_cast<int>(m), bar);
+                                tensor_load_3d<CG>(da, &map_a, k0 + h * 32, m0, static_cast<int>(m), bar);
                             }
                             for (int x = 0; x < b_boxes; ++x)
-                                tensor_load_2d<CG>(sb + x * BOX_ROWS * 128, &map_b, kb * KB, r0 + x * BOX_ROWS, bar);
+                                tensor_load_2d<CG>(db + x * BOX_ROWS * 128, &map_b, k0 + h * 32, r0 + x * BOX_ROWS, bar);
                         }
-                    } else {
-                        Operand oa, ob;
-                        if (MODE == PRODUCT_WEIGHTS) {
-                            const int64_t r = t.row0 + kb * KB, re = t.row0 + t.rows;
-                            oa = Operand{p.w, p.ldw, r, re, m0, a.cols_m, a_boxes * KB * 8, true};
-                            ob = Operand{p.x, p.ldx, r, re, t.n0, a.cols_n, b_boxes * KB * 8, true};
-                        } else {
-                            const void* w = static_cast<const unsigned char*>(p.w) + m * p.stride_w * (PL == 1 ? 2 : 4);
-                            const int64_t k = int64_t(kb) * KB;
-                            if (a_outer) oa = Operand{w, p.ldw, k, p.K, m0, a.cols_m, a_boxes * KB * 8, true};
-                            else oa = Operand{w, p.ldw, m0, a.cols_m, k, p.K, MT * 8, false};
-                            ob = Operand{p.x, p.ldx, t.row0, t.row0 + t.rows, k, p.K, share * 8, false};
-                            // a short sum over many tiles of a segment: its matrix is split and stored once
-                            if (R::STAGES == 2 && held_seg == t.seg && held_m0 == t.m0 && held_kb == kb) oa.units = 0;
-                            held_seg = t.seg, held_m0 = t.m0, held_kb = kb;
-                        }
-                        load_operands<PL>(oa, ob, sa, R::A_PLANE, sb, R::B_PLANE);
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) lead_arrive<CG>(full + st, true);
                     }
                     if ((st += 2) >= R::STAGES) {
                         st -= R::STAGES;
@@ -751,14 +714,62 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                 }
                 base += blocks;
             }
-            if (TENSOR && rank == 0 && !ok) {
+            if (rank == 0 && !ok) {
                 // something gave up: the copies in flight still land before this CTA's shared memory goes away
                 for (uint32_t j = next > R::STAGES ? next - R::STAGES : 0; j < next; ++j)
-                    wait_for<CG>(full + j % R::STAGES, (j / R::STAGES) & 1, p.status);
+                    wait_for<CG>((PL > 1 ? landed : full) + j % R::STAGES, (j / R::STAGES) & 1, p.status);
             }
         }
         __syncwarp();
-    } else if (TENSOR && MODE == PRODUCT_WEIGHTS && warp == 2) {
+    } else if ((!TENSOR || PL > 1) && warp >= LOAD_WARP) {
+        // ---- loaders: split what the producers copied, or load by themselves ----
+        uint32_t st = 0, ph = 0;
+        bool ok = true;
+        Kept<MODE, R::STAGES == 2 && PL == 3, 2> keeps;
+        Item t;
+        for (uint32_t i = first; ok && i < items; i += stride) {
+            item_at<MODE, NT, CG>(a, beg, pre, i, t);
+            const int share = share_of(columns_of(t)), lanes = lanes_of(t);
+            const int a_rows = a_outer ? (lanes + 63) & ~63 : MT, b_rows = b_outer ? (share + 63) & ~63 : share;
+            int64_t m = t.seg;
+            if (MODE == PRODUCT_FORWARD && p.index) m = __ldg(p.index + t.seg);
+            for (int kb = t.kb0; kb < t.kb1; ++kb) {
+                // (an empty stage's barrier is a phase behind a copied one's)
+                ok = warp_wait<CG>((TENSOR ? landed : empty) + st, TENSOR ? ph : ph ^ 1, p.status);
+                if (!ok) break;
+                unsigned char* sa = stages + st * R::STAGE;
+                unsigned char* sb = sa + PL * R::A_PLANE;
+                const bool keep = keeps.a(t, kb);
+                if constexpr (TENSOR) {
+                    // rows past the segment's end belong to others: they count as zeros
+                    const int valid = MODE == PRODUCT_WEIGHTS ? t.rows - kb * KB : KB;
+                    if (!keep) split_rows(a_rows, valid, sa, R::A_PLANE);
+                    split_rows(b_rows, valid, sb, R::B_PLANE);
+                } else if (MODE == PRODUCT_WEIGHTS) {
+                    const int64_t r = t.row0 + kb * KB, re = t.row0 + t.rows;
+                    load_any<PL>(Operand{p.w, p.ldw, r, re, t.m0, a.cols_m, a_rows, true}, sa, R::A_PLANE);
+                    load_any<PL>(Operand{p.x, p.ldx, r, re, t.n0, a.cols_n, b_rows, true}, sb, R::B_PLANE);
+                } else {
+                    const void* w = static_cast<const unsigned char*>(p.w) + m * p.stride_w * (PL == 1 ? 2 : 4);
+                    const int64_t k = int64_t(kb) * KB;
+                    if (keep) {
+                    } else if (a_outer) {
+                        load_any<PL>(Operand{w, p.ldw, k, p.K, t.m0, a.cols_m, a_rows, true}, sa, R::A_PLANE);
+                    } else {
+                        load_any<PL>(Operand{w, p.ldw, t.m0, a.cols_m, k, p.K, a_rows, false}, sa, R::A_PLANE);
+                    }
+                    load_any<PL>(Operand{p.x, p.ldx, t.row0, t.row0 + t.rows, k, p.K, b_rows, false}, sb, R::B_PLANE);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) lead_arrive<CG>(full + st, true);
+                if (++st == R::STAGES) {
+                    st = 0;
+                    ph ^= 1;
+                }
+            }
+        }
+    } else if (TENSOR && PL == 1 && MODE == PRODUCT_WEIGHTS && warp == 2) {
         // ---- tails ----
         uint32_t st = 0, seen = 0;        // a parity per stage
         bool ok = true;
@@ -846,9 +857,9 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
         // ---- drain ----
         const int quarter = (warp - EPI_WARP) & 3, group = (warp - EPI_WARP) / 4;   // which lanes; which columns
         const int td = tid - EPI_WARP * 32;
-        constexpr int W = MODE == PRODUCT_ADAPTERS ? 8 : (TENSOR ? 32 : 16), ROWS = W * (EPW / 4);    // columns at a time; of all warps
+        constexpr int W = MODE == PRODUCT_ADAPTERS ? 8 : (TENSOR && PL == 1 ? 32 : 16), ROWS = W * (EPW / 4);    // columns at a time; of all warps
         staging += (warp - EPI_WARP) * R::STAGING;
-        LowRank<PL, TENSOR> low(p, tile_adapter, staging, lane);
+        LowRank<PL, TENSOR && PL == 1> low(p, tile_adapter, staging, lane);
         if (MODE == PRODUCT_FORWARD && !p.index) {
             // rows in no segment
             const int b = p.S > 0 ? beg[0] : 0, e = p.S > 0 ? beg[p.S] : 0;
@@ -1129,22 +1140,24 @@ EncodeFn encode_fn() {
     return fn;
 }
 
+// 128-byte rows of boxes: 64 16-bit or 32 float32 values.
 bool make_map(CUtensorMap* map, int type, const void* base, int64_t cols, int64_t rows, int64_t ld, int64_t mats,
               int64_t stride, int box_rows) {
     const EncodeFn fn = encode_fn();
     if (!fn) return false;
     const int rank = mats > 0 ? 3 : 2;
     const cuuint64_t dims[3] = {cuuint64_t(cols), cuuint64_t(rows), cuuint64_t(mats)};
-    const cuuint64_t strides[2] = {cuuint64_t(ld) * 2, cuuint64_t(stride) * 2};
-    const cuuint32_t box[3] = {KB, cuuint32_t(box_rows), 1}, each[3] = {1, 1, 1};
-    return fn(map, type == PT_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank,
+    const int size = type == PT_F32 ? 4 : 2;
+    const cuuint64_t strides[2] = {cuuint64_t(ld) * size, cuuint64_t(stride) * size};
+    const cuuint32_t box[3] = {cuuint32_t(128 / size), cuuint32_t(box_rows), 1}, each[3] = {1, 1, 1};
+    return fn(map, type == PT_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : type == PT_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank,
               const_cast<void*>(base), dims, strides, box, each, CU_TENSOR_MAP_INTERLEAVE_NONE,
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // What a tensor map can describe: 16-byte aligned, strides multiples of 16 bytes and below 2^40.
-bool tensor_copyable(const void* base, int64_t stride) {
-    return reinterpret_cast<uintptr_t>(base) % 16 == 0 && stride % 8 == 0 && stride < (int64_t(1) << 38);
+bool tensor_copyable(const void* base, int64_t stride, int type) {
+    return reinterpret_cast<uintptr_t>(base) % 16 == 0 && stride % (type == PT_F32 ? 4 : 8) == 0 && stride < (int64_t(1) << 37);
 }
 
 template <int MODE, bool TENSOR, int NT, int PL, int CG>
@@ -1177,7 +1190,7 @@ cudaError_t launch_shape(const KernelArgs& a, const ProductPlan& plan, cudaStrea
         if (e != cudaSuccess) return e;
     }
     auto* kernel = product_kernel<MODE, TENSOR, NT, PL, CG>;
-    constexpr int smem = Ring<NT, PL, CG>::SMEM;
+    constexpr int smem = Ring<NT, PL, CG, TENSOR>::SMEM;
     cudaLaunchAttribute attr[2];
     int attrs = 0;
     if (CG > 1) {
@@ -1194,7 +1207,7 @@ cudaError_t launch_shape(const KernelArgs& a, const ProductPlan& plan, cudaStrea
     }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(plan.grid);
-    cfg.blockDim = dim3(TENSOR ? TENSOR_THREADS : LOADER_THREADS);
+    cfg.blockDim = dim3(TENSOR && PL == 1 ? TENSOR_THREADS : LOADER_THREADS);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = attr;
@@ -1225,6 +1238,8 @@ cudaError_t launch_shape(const KernelArgs& a, const ProductPlan& plan, cudaStrea
 
 template <int MODE>
 cudaError_t launch_mode(const KernelArgs& a, const ProductPlan& plan, cudaStream_t stream) {
+    if (a.p.type == PT_F32 && plan.tensor)
+        return plan.narrow ? launch_shape<MODE, true, 64, 3, 1>(a, plan, stream) : launch_shape<MODE, true, 128, 3, 1>(a, plan, stream);
     if (a.p.type == PT_F32)
         return plan.narrow ? launch_shape<MODE, false, 64, 3, 1>(a, plan, stream) : launch_shape<MODE, false, 128, 3, 1>(a, plan, stream);
     if (!plan.tensor)
@@ -1241,14 +1256,14 @@ ProductPlan plan_product(int mode, const ProductParams& p) {
     ProductPlan d{};
     const bool weights = mode == PRODUCT_WEIGHTS;
     const int64_t mats = mode == PRODUCT_FORWARD ? (p.index ? p.L : p.S) : 1;
-    d.tensor = p.type != PT_F32 && p.K > 0 && p.R > 0 && mats > 0 && tensor_copyable(p.x, p.ldx) &&
-               tensor_copyable(p.w, p.ldw) && (mats == 1 || tensor_copyable(p.w, p.stride_w));
+    d.tensor = p.K > 0 && p.R > 0 && mats > 0 && tensor_copyable(p.x, p.ldx, p.type) && tensor_copyable(p.w, p.ldw, p.type) &&
+               (mats == 1 || tensor_copyable(p.w, p.stride_w, p.type));
     const int64_t segments = mode == PRODUCT_ADAPTERS ? 1 : p.S;
     // few rows per segment: small tiles and a deeper ring; weights: few columns of x
     d.narrow = weights ? p.K <= 64 : p.R <= 64 * segments;
     const int NT = tile_columns(p, d.narrow);
     // two CTAs on a tile of twice the lanes, unless that leaves one of them without lanes
-    d.pair = d.tensor && !d.narrow && (p.N > 1024 || ceil_to(p.N, MT) % 2 == 0);
+    d.pair = d.tensor && p.type != PT_F32 && !d.narrow && (p.N > 1024 || ceil_to(p.N, MT) % 2 == 0);
     const int cg = d.pair ? 2 : 1;
     d.mtiles = static_cast<int32_t>(ceil_to(p.N, MT * cg));
     d.ntiles = weights ? static_cast<int32_t>(ceil_to(p.K, NT)) : 1;
