@@ -46,25 +46,33 @@ constexpr int MT = 128;                   // lanes of a tile
 constexpr int NEAR_SEGMENTS = 1024;       // up to here every CTA keeps the offsets in shared memory
 constexpr int EPI_WARP = 4, EPW = 8;      // drain warps: their index mod 4 names their lanes, and the two of a quarter take turns at the columns
 constexpr int LOAD_WARP = 12, LOADERS = 256;    // loader warps start here; their threads
-constexpr int TENSOR_THREADS = 384, LOADER_THREADS = 640;
+constexpr int LOW_WARP = 12;              // four warps that lay out the adapters' part for the tensor cores
+template <int MODE, bool TENSOR, int PL>
+constexpr int threads_of() { return TENSOR && PL == 1 ? (MODE == PRODUCT_ADAPTERS ? 512 : 384) : 640; }
+// Rows of a tile per run of rows with one adapter from which on the tile's
+// low-rank part goes to the tensor cores (an MMA takes 16 columns at least;
+// a run costs them a pass over the whole tile).
+constexpr int LOW_RUN = 16;
 constexpr int NEVER_FLUSH = 1 << 28;         // more blocks than any sum has
 constexpr unsigned STATUS_PRODUCT_TIMEOUT = 8u;
 
 // Stage ring of a kernel shape: PL 16-bit planes per operand, CG CTAs that share a tile.
-template <int NT, int PL, int CG, bool TENSOR>
+template <int MODE, int NT, int PL, int CG, bool TENSOR>
 struct Ring {
+    static constexpr bool LOW = MODE == PRODUCT_ADAPTERS && TENSOR && PL == 1;   // a stage of its own for the low-rank part
     static constexpr int A_PLANE = MT * 128, B_PLANE = NT / CG * 128;
     static constexpr int STAGE = PL * (A_PLANE + B_PLANE);
     // (the loaders' plain loads are tracked in the L1 that shared memory leaves)
-    static constexpr int STAGES = std::min(8, (PL == 3 ? 221184 : TENSOR ? 200704 : 98304) / STAGE);
+    static constexpr int ALL_STAGES = std::min(8, (PL == 3 ? 221184 : TENSOR ? 200704 : 98304) / STAGE);
+    static constexpr int STAGES = ALL_STAGES - (LOW ? 1 : 0);
     static constexpr int ACC = PL == 1 ? NT : 2 * NT;            // tensor-memory columns of one accumulator
-    static constexpr int BARS = 3 * STAGES + 5;
+    static constexpr int BARS = 3 * STAGES + 7;
     // the drain warps' staging; PL == 3 keeps it (adapters alone need it there) in the space of the offsets
     static constexpr int STAGING = PL == 1 ? 2048 : 1024;
     static constexpr int STAGED = PL == 1 ? EPW * STAGING : 0;
     static constexpr int NEAR = 2 * (NEAR_SEGMENTS + 1) * 4;
     static_assert(NEAR >= EPW * 1024, "room for that staging");
-    static constexpr int SMEM = STAGES * STAGE + STAGED + NEAR + BARS * 8 + 64 + NT * 4 + 1024;   // 1024: alignment of the stages
+    static constexpr int SMEM = ALL_STAGES * STAGE + STAGED + NEAR + BARS * 8 + 128 + NT * 4 * (LOW ? 2 : 1) + 1024;   // 1024: alignment of the stages
     static_assert(SMEM <= 232448, "shared memory of an SM");
 };
 
@@ -227,6 +235,42 @@ __device__ __forceinline__ bool bar_drain_all(bool ok) {
         : "memory");
     return r != 0;
 }
+// In how many of the drain warps' threads `yes` holds.
+__device__ __forceinline__ int bar_drain_count(bool yes) {
+    int r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.popc.u32 %0, 1, %2, p;\n\t}"
+        : "=r"(r)
+        : "r"(yes ? 1u : 0u), "n"(EPW * 32)
+        : "memory");
+    return r;
+}
+// The four low-rank warps, as bar_drain and bar_drain_all.
+__device__ __forceinline__ void bar_low() { asm volatile("bar.sync 2, 128;" ::: "memory"); }
+__device__ __forceinline__ bool bar_low_all(bool ok) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.and.pred q, 2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(ok ? 1u : 0u)
+        : "memory");
+    return r != 0;
+}
+
+// The adapter of a row: its segment's, or -1.
+__device__ __forceinline__ int adapter_of(const ProductParams& p, int row) {
+    int64_t lo = 0, hi = p.S;      // the last segment that starts at or before the row
+    while (hi - lo > 1) {
+        const int64_t mid = (lo + hi) >> 1;
+        if (offset_at(p, mid) <= row) lo = mid; else hi = mid;
+    }
+    int l = -1;
+    if (p.S > 0 && offset_at(p, lo) <= row && row < offset_at(p, lo + 1)) l = __ldg(p.index + lo);
+    return l >= 0 && l < p.L ? l : -1;
+}
+
 // A bounded wait; CG == 2: for arrivals of both CTAs.  The clock is read only
 // after a few hundred tries: a read takes longer than a stage does.
 template <int CG>
@@ -321,7 +365,7 @@ template <int PL, bool WIDE>
 struct LowRank {
     static constexpr int SIZE = PL == 1 ? 2 : 4;
     static constexpr int WORDS = 16 * SIZE / 4;          // of 16 ranks
-    static constexpr int AHEAD = WIDE ? 8 : 2;           // rows whose b are fetched together (as registers allow)
+    static constexpr int AHEAD = WIDE ? 4 : 2;           // rows whose b are fetched together (as registers allow)
     const ProductParams& p;
     const int* tile_adapter;
     float4* su;                                          // [8 rows][4]
@@ -546,6 +590,94 @@ __device__ __forceinline__ void load_any(const Operand& x, unsigned char* dst, i
     }
 }
 
+// Where the run counts of 32 rows each are kept: behind the turns.
+__device__ __forceinline__ int* low_adapter_runs(uint32_t* turns) { return reinterpret_cast<int*>(turns + 8); }
+
+// bfloat16 part `part` of 16 float32 values (by truncation, each rest exact).
+__device__ __forceinline__ void part_of_16(float (&f)[16], int part, uint4 (&v)[2]) {
+    uint32_t r[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        uint32_t k[3];
+        split_pair(f[2 * i], f[2 * i + 1], k);
+        r[i] = part == 0 ? k[0] : part == 1 ? k[1] : k[2];
+    }
+    v[0] = make_uint4(r[0], r[1], r[2], r[3]);
+    v[1] = make_uint4(r[4], r[5], r[6], r[7]);
+}
+
+// One block of an adapter's part of the sum, for the rows [row, end) of the
+// tile: up to four steps of 16 ranks, each one product of a part of b (A: a
+// thread per lane of the tile) and a part of u (B: a thread per row, zeros
+// outside the run).  bfloat16 b: parts (b, u) = (0, 0), (0, 1), (0, 2);
+// float16 b has two parts: and (1, 0), (1, 1); what is left out is below 2^-21.
+__device__ __forceinline__ void lay_adapter(const ProductParams& p, int s0, int total, int slices, int l, int64_t m, int row0, int base,
+                                            int share, int row, int end, unsigned char* sa, unsigned char* sb, int tl) {
+    const int rank = static_cast<int>(p.rank);
+    const bool vec_b = rank % 8 == 0 && (reinterpret_cast<uintptr_t>(p.b) & 15) == 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int s = s0 + i;
+        if (s >= total) break;
+        const int pair = s / slices, q = (s - pair * slices) * 16, width = rank - q;
+        const int pb = pair >= 3 ? 1 : 0, pu = pair >= 3 ? pair - 3 : pair;
+        // A
+        uint32_t raw[8];
+        const uint16_t* b = static_cast<const uint16_t*>(p.b) + (int64_t(l) * p.N + m) * rank + q;
+        if (vec_b) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const uint4 x = m < p.N && k * 8 < width ? __ldg(reinterpret_cast<const uint4*>(b) + k) : make_uint4(0, 0, 0, 0);
+                raw[4 * k] = x.x, raw[4 * k + 1] = x.y, raw[4 * k + 2] = x.z, raw[4 * k + 3] = x.w;
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                raw[k] = m < p.N && 2 * k < width ? __ldg(b + 2 * k) : 0;
+                if (m < p.N && 2 * k + 1 < width) raw[k] |= static_cast<uint32_t>(__ldg(b + 2 * k + 1)) << 16;
+            }
+        }
+        uint4 v[2];
+        if (p.type == PT_F16) {
+            float f[16];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&raw[k]));
+                f[2 * k] = x.x, f[2 * k + 1] = x.y;
+            }
+            part_of_16(f, pb, v);
+        } else {
+            v[0] = make_uint4(raw[0], raw[1], raw[2], raw[3]);
+            v[1] = make_uint4(raw[4], raw[5], raw[6], raw[7]);
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) *reinterpret_cast<uint4*>(sa + tl * 128 + (((2 * i + k) ^ (tl & 7)) << 4)) = v[k];
+        // B
+        for (int r = tl; r < share; r += 128) {
+            float f[16];
+            const bool in = base + r >= row && base + r < end;
+            const float* u = p.u + (int64_t(row0) + base + r) * rank + q;
+#pragma unroll
+            for (int k = 0; k < 16; ++k) f[k] = 0.0f;
+            if (in && rank % 4 == 0) {
+#pragma unroll
+                for (int k = 0; k < 16; k += 4)
+                    if (k < width) {
+                        const float4 x = *reinterpret_cast<const float4*>(u + k);
+                        f[k] = x.x, f[k + 1] = x.y, f[k + 2] = x.z, f[k + 3] = x.w;
+                    }
+            } else if (in) {
+#pragma unroll
+                for (int k = 0; k < 16; ++k)
+                    if (k < width) f[k] = u[k];
+            }
+            part_of_16(f, pu, v);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) *reinterpret_cast<uint4*>(sb + r * 128 + (((2 * i + k) ^ (r & 7)) << 4)) = v[k];
+        }
+    }
+}
+
 // Whether the stage of a block already holds its A operand: with two stages
 // and a sum of one or two blocks, every tile of a segment and the one before
 // use the same.  STREAMS: 1 for a role that sees every second block, which is
@@ -570,16 +702,16 @@ struct Kept {
 // ---------------------------------------------------------------------------
 
 template <int MODE, bool TENSOR, int NT, int PL, int CG>
-__global__ void __launch_bounds__(TENSOR && PL == 1 ? TENSOR_THREADS : LOADER_THREADS, 1)
+__global__ void __launch_bounds__(threads_of<MODE, TENSOR, PL>(), 1)
 product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUtensorMap map_a,
                const __grid_constant__ CUtensorMap map_b) {
-    using R = Ring<NT, PL, CG, TENSOR>;
+    using R = Ring<MODE, NT, PL, CG, TENSOR>;
     static_assert(CG == 1 || (TENSOR && PL == 1), "pairs take their operands as they are copied");
     constexpr int HALVES = PL == 1 ? 1 : 2;          // copies of 128 bytes that make 64 values
     constexpr int BOX_ROWS = NT <= 64 ? 16 : 64;     // rows of one copy of x (forward)
     extern __shared__ unsigned char raw[];
     unsigned char* stages = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
-    unsigned char* staging = stages + R::STAGES * R::STAGE;      // 16-byte aligned, as all that follows it
+    unsigned char* staging = stages + R::ALL_STAGES * R::STAGE;      // 16-byte aligned, as all that follows it
     int* near = reinterpret_cast<int*>(staging + R::STAGED);
     uint64_t* full = reinterpret_cast<uint64_t*>(staging + R::STAGED + R::NEAR);   // CG == 2: CTA 0's count
     uint64_t* empty = full + R::STAGES;
@@ -587,9 +719,14 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
     uint64_t* acc_full = landed + R::STAGES;
     uint64_t* acc_empty = acc_full + 2;            // CG == 2: CTA 0's count
     uint64_t* drain = acc_empty + 2;
-    uint32_t* tmem_at = reinterpret_cast<uint32_t*>(drain + 1);
+    uint64_t* low_full = drain + 1;                // CG == 2: CTA 0's count
+    uint64_t* low_empty = low_full + 1;
+    uint32_t* tmem_at = reinterpret_cast<uint32_t*>(low_empty + 1);
     int* last_part = reinterpret_cast<int*>(tmem_at + 1);
-    int* tile_adapter = reinterpret_cast<int*>(tmem_at + 16);    // [NT]
+    int* low_steps = last_part + 1;                // steps of 16 in the low-rank stage; + 8: the tile's last
+    uint32_t* low_turns = reinterpret_cast<uint32_t*>(low_steps + 1);          // [8]: rows with another adapter than the one before
+    int* tile_adapter = reinterpret_cast<int*>(tmem_at + 32);    // [NT], the drain warps'
+    int* low_adapter = tile_adapter + NT;                        // [NT], the low-rank warps'
     if (PL > 1) staging = reinterpret_cast<unsigned char*>(near);
     const ProductParams& p = a.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -612,6 +749,8 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
             mbar_init(acc_empty + i, EPW * CG);
         }
         mbar_init(drain, 1);
+        mbar_init(low_full, 4 * CG);
+        mbar_init(low_empty, 1);
         fence_mbarrier_init();
         if (TENSOR) {
             tensor_prefetch(&map_a);
@@ -796,10 +935,77 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
             }
             if (++st == R::STAGES) st = 0;
         }
+    } else if (R::LOW && warp >= LOW_WARP) {
+        // ---- the adapters' part of tiles with few runs of rows, as further blocks of the sum ----
+        if (p.u) {
+            grid_wait();
+            const int tl = tid - LOW_WARP * 32;
+            unsigned char* sa = stages + R::STAGES * R::STAGE;
+            unsigned char* sb = sa + R::A_PLANE;
+            const int slices = static_cast<int>((p.rank + 15) / 16), total = slices * (p.type == PT_BF16 ? 3 : 5);
+            uint32_t ph = 1;
+            bool ok = true;
+            Item t;
+            for (uint32_t i = first; ok && i < items; i += stride) {
+                item_at<MODE, NT, CG>(a, beg, pre, i, t);
+                if (t.kb1 <= t.kb0 || t.part != 0) continue;
+                for (int r = tl; r < t.rows; r += 128) low_adapter[r] = adapter_of(p, t.row0 + r);
+                bar_low();
+                int runs = 0;
+                for (int r = tl; r - tl < NT; r += 128) {
+                    const int l = r < t.rows ? low_adapter[r] : -2, before = r > 0 && r < t.rows ? low_adapter[r - 1] : -2;
+                    const uint32_t turns = __ballot_sync(0xffffffffu, r < t.rows && l != before);
+                    const uint32_t starts = __ballot_sync(0xffffffffu, r < t.rows && l >= 0 && l != before);
+                    if (lane == 0) low_turns[r >> 5] = turns, low_adapter_runs(low_turns)[r >> 5] = __popc(starts);
+                }
+                bar_low();
+                for (int k = 0; k < NT / 32; ++k) runs += low_adapter_runs(low_turns)[k];
+                const bool mine = runs > 0 && runs * LOW_RUN <= t.rows;
+                int row = 0;                           // the next run's first row
+                bool last = false;
+                do {
+                    int end = 0, l = -1;
+                    if (mine) {
+                        // the next run with an adapter
+                        do {
+                            l = low_adapter[row];
+                            end = t.rows;
+                            for (int k = (row + 1) >> 5; k < NT / 32; ++k) {
+                                const uint32_t m = low_turns[k] & (k == (row + 1) >> 5 ? ~0u << ((row + 1) & 31) : ~0u);
+                                if (m) {
+                                    end = min(t.rows, k * 32 + __ffs(m) - 1);
+                                    break;
+                                }
+                            }
+                            if (l < 0) row = end;
+                        } while (l < 0);
+                        --runs;
+                    }
+                    for (int s0 = 0; ok && s0 < (mine ? total : 1); s0 += 4) {
+                        ok = bar_low_all(wait_for<CG>(low_empty, ph, p.status));
+                        if (!ok) break;
+                        ph ^= 1;
+                        last = runs == 0 && s0 + 4 >= total;
+                        if (!mine) last = true;
+                        if (mine) {
+                            lay_adapter(p, s0, total, slices, l, t.m0 + rank * MT + tl, t.row0, rank * share_of(t.rows), share_of(t.rows),
+                                        row, end, sa, sb, tl);
+                        }
+                        if (tl == 0) *low_steps = (mine ? min(4, total - s0) : 0) | (last ? 8 : 0);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) lead_arrive<CG>(low_full, true);
+                    }
+                    row = end;
+                } while (ok && !last);
+                bar_low();        // the table has been read
+            }
+        }
+        __syncwarp();
     } else if (warp == 0 && rank == 0) {
         // ---- MMA ----
         if (elect_one()) {
-            uint32_t st = 0, ph = 0, buf = 0, bph = 1;
+            uint32_t st = 0, ph = 0, buf = 0, bph = 1, low_ph = 0;
             bool ok = true;
             const uint32_t type = p.type == PT_F16 ? 0 : 1;
             // descriptors of the first stage; a step of 16 and a stage add to the address field
@@ -839,6 +1045,22 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                             }
                         }
                         tc_commit<CG>(empty + st);
+                        if (R::LOW && p.u && t.part == 0 && kb + 1 == t.kb1) {
+                            // the low-rank part, from a stage of its own: bfloat16 parts, whatever the type
+                            const uint32_t low_idesc = tc_idesc(1, MT * CG, CG * share_of(columns_of(t)), false, false);
+                            const uint64_t la = tc_smem_desc(smem_u32(stages + R::STAGES * R::STAGE), 8192);
+                            const uint64_t lb = tc_smem_desc(smem_u32(stages + R::STAGES * R::STAGE) + R::A_PLANE, 8192);
+                            for (int last = 0; !last; low_ph ^= 1) {
+                                ok = wait_for<CG>(low_full, low_ph, p.status);
+                                if (!ok) break;
+                                tc_fence_after();
+                                const int steps = *reinterpret_cast<volatile int*>(low_steps);
+                                last = steps & 8;
+                                for (int k = 0; k < (steps & 7); ++k) tc_mma<CG>(acc, la + 2 * k, lb + 2 * k, low_idesc, true);
+                                tc_commit<CG>(low_empty);
+                            }
+                            if (!ok) break;
+                        }
                         if (kb + 1 == piece_end) tc_commit<CG>(acc_full + buf);
                         if (++st == R::STAGES) {
                             st = 0;
@@ -859,7 +1081,7 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
         const int td = tid - EPI_WARP * 32;
         constexpr int W = MODE == PRODUCT_ADAPTERS ? 8 : (TENSOR && PL == 1 ? 32 : 16), ROWS = W * (EPW / 4);    // columns at a time; of all warps
         staging += (warp - EPI_WARP) * R::STAGING;
-        LowRank<PL, TENSOR && PL == 1> low(p, tile_adapter, staging, lane);
+        LowRank<PL, R::LOW> low(p, tile_adapter, staging, lane);
         if (MODE == PRODUCT_FORWARD && !p.index) {
             // rows in no segment
             const int b = p.S > 0 ? beg[0] : 0, e = p.S > 0 ? beg[p.S] : 0;
@@ -883,20 +1105,21 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
             const int64_t m = t.m0 + rank * MT + quarter * 32;           // the warp's first lane
             const int lanes = static_cast<int>(a.cols_m - m < 32 ? a.cols_m - m : 32);   // may be negative
             const int64_t slot = (t.slot * CG + rank) * NT * MT + quarter * 32;      // in floats
+            bool scattered = true;      // the drain warps compute the tile's low-rank part
             if constexpr (MODE == PRODUCT_ADAPTERS) {
                 bar_drain();       // the table of the tile before has been read
                 for (int r = td; r < t.rows; r += EPW * 32) {
-                    const int row = t.row0 + r;
-                    int64_t lo = 0, hi = p.S;      // the last segment that starts at or before the row
-                    while (hi - lo > 1) {
-                        const int64_t mid = (lo + hi) >> 1;
-                        if (offset_at(p, mid) <= row) lo = mid; else hi = mid;
-                    }
-                    int l = -1;
-                    if (p.S > 0 && offset_at(p, lo) <= row && row < offset_at(p, lo + 1)) l = __ldg(p.index + lo);
-                    tile_adapter[r] = l >= 0 && l < p.L ? l : -1;
+                    tile_adapter[r] = adapter_of(p, t.row0 + r);
                 }
                 bar_drain();
+                if (R::LOW) {
+                    int runs = 0;
+                    for (int r = td; r - td < t.rows; r += EPW * 32) {
+                        const bool starts = r < t.rows && tile_adapter[r] >= 0 && (r == 0 || tile_adapter[r - 1] != tile_adapter[r]);
+                        runs += bar_drain_count(starts);
+                    }
+                    scattered = runs * LOW_RUN > t.rows;
+                }
             }
             float factor = 1.0f;
             if (MODE == PRODUCT_FORWARD && p.scale) factor = __ldg(p.scale + __ldg(p.index + t.seg));
@@ -913,14 +1136,14 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                 bool waiting = summed && !adding;
                 int c = group * W;
                 if constexpr (MODE == PRODUCT_ADAPTERS)
-                    if (final && !adding) low.begin(t.row0, t.rows, m + lane, c + t.part * ROWS);
+                    if (final && !adding && scattered) low.begin(t.row0, t.rows, m + lane, c + t.part * ROWS);
                 for (;;) {
                     float v[W];
 #pragma unroll
                     for (int j = 0; j < W; ++j) v[j] = 0.0f;
                     // the parts of a tile share its low-rank part
                     if constexpr (MODE == PRODUCT_ADAPTERS)
-                        if (final && !adding && c < n_left && c / ROWS % t.parts == t.part) low.rows_of(v, c, c + ROWS * t.parts);
+                        if (final && !adding && scattered && c < n_left && c / ROWS % t.parts == t.part) low.rows_of(v, c, c + ROWS * t.parts);
                     if (waiting) {
                         ok = bar_drain_all(wait_for<CG>(acc_full + buf, bph, p.status));
                         if (!ok) break;
@@ -1190,7 +1413,8 @@ cudaError_t launch_shape(const KernelArgs& a, const ProductPlan& plan, cudaStrea
         if (e != cudaSuccess) return e;
     }
     auto* kernel = product_kernel<MODE, TENSOR, NT, PL, CG>;
-    constexpr int smem = Ring<NT, PL, CG, TENSOR>::SMEM;
+    using R = Ring<MODE, NT, PL, CG, TENSOR>;
+    constexpr int smem = R::SMEM;
     cudaLaunchAttribute attr[2];
     int attrs = 0;
     if (CG > 1) {
@@ -1207,7 +1431,7 @@ cudaError_t launch_shape(const KernelArgs& a, const ProductPlan& plan, cudaStrea
     }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(plan.grid);
-    cfg.blockDim = dim3(TENSOR && PL == 1 ? TENSOR_THREADS : LOADER_THREADS);
+    cfg.blockDim = dim3(threads_of<MODE, TENSOR, PL>());
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = attr;
