@@ -53,6 +53,7 @@ constexpr int threads_of() { return TENSOR && PL == 1 ? (MODE == PRODUCT_ADAPTER
 // low-rank part goes to the tensor cores (an MMA takes 16 columns at least;
 // a run costs them a pass over the whole tile).
 constexpr int LOW_RUN = 16;
+constexpr int LOW_EVERY = 10;             // blocks of the sum between two of the low-rank part: about the time one takes to lay out
 constexpr int NEVER_FLUSH = 1 << 28;         // more blocks than any sum has
 constexpr unsigned STATUS_PRODUCT_TIMEOUT = 8u;
 
@@ -79,6 +80,7 @@ struct Ring {
 struct KernelArgs {
     ProductParams p;
     int32_t mtiles, ntiles, parts, part_blocks, kblocks;
+    int32_t a_rows;     // rows of one copy of A whose sum is contiguous
     int32_t wide_rows;  // 16-bit results: 16-byte stores fit
     int32_t flush;      // blocks of the sum after which the accumulators go to the result
     int64_t chunk, row_tiles, cols_m, cols_n;   // cols_*: extent of the tile dimensions (forward: cols_n unused)
@@ -260,14 +262,15 @@ __device__ __forceinline__ bool bar_low_all(bool ok) {
 }
 
 // The adapter of a row: its segment's, or -1.
-__device__ __forceinline__ int adapter_of(const ProductParams& p, int row) {
+__device__ __forceinline__ int adapter_of(const ProductParams& p, const int* near, int row) {
+    auto offset = [&](int64_t s) { return near ? near[s] : offset_at(p, s); };
     int64_t lo = 0, hi = p.S;      // the last segment that starts at or before the row
     while (hi - lo > 1) {
         const int64_t mid = (lo + hi) >> 1;
-        if (offset_at(p, mid) <= row) lo = mid; else hi = mid;
+        if (offset(mid) <= row) lo = mid; else hi = mid;
     }
     int l = -1;
-    if (p.S > 0 && offset_at(p, lo) <= row && row < offset_at(p, lo + 1)) l = __ldg(p.index + lo);
+    if (p.S > 0 && offset(lo) <= row && row < offset(lo + 1)) l = __ldg(p.index + lo);
     return l >= 0 && l < p.L ? l : -1;
 }
 
@@ -733,7 +736,6 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
     const int rank = CG == 2 ? static_cast<int>(cluster_rank()) : 0;
     const uint32_t first = blockIdx.x / CG, stride = gridDim.x / CG;
 
-    if (MODE == PRODUCT_FORWARD && p.index) grid_trigger();      // the adapters' kernel may start beside this one
     const bool is_near = p.S <= NEAR_SEGMENTS;
     const int* beg = is_near ? near : a.far;
     const int* pre = is_near ? near + NEAR_SEGMENTS + 1 : a.far + p.S + 1;
@@ -758,6 +760,10 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
         }
     }
     if (is_near && MODE != PRODUCT_ADAPTERS && p.S > 0) fill_prefix<MODE, NT>(a, near, near + NEAR_SEGMENTS + 1);
+    // (PL == 3: that space is the staging)
+    const int* near_offsets = MODE == PRODUCT_ADAPTERS && PL == 1 && is_near ? near : nullptr;
+    if (near_offsets && p.S > 0)
+        for (int64_t s = tid; s <= p.S; s += blockDim.x) near[s] = offset_at(p, s);
     tc_fence_before();
     __syncthreads();
     if (CG == 2) cluster_sync();
@@ -800,13 +806,13 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                 const int columns = columns_of(t), share = share_of(columns), lanes = lanes_of(t);
                 const int a_boxes = a_outer ? (lanes + 63) / 64 : (lanes + MT - 1) / MT;
                 const int b_boxes = b_outer ? (share + 63) / 64 : (share + BOX_ROWS - 1) / BOX_ROWS;
-                const uint32_t a_bytes = a_boxes * (a_outer ? 8192 : R::A_PLANE) * HALVES, b_bytes = b_boxes * (b_outer ? 8192 : BOX_ROWS * 128) * HALVES;
+                const uint32_t a_bytes = a_boxes * (a_outer ? 8192 : a.a_rows * 128) * HALVES, b_bytes = b_boxes * (b_outer ? 8192 : BOX_ROWS * 128) * HALVES;
                 const int m0 = t.m0 + rank * MT;
                 uint32_t other_bytes = 0;
                 if (CG == 2) {
                     const int64_t left = a.cols_m - t.m0 - MT;
                     const int other = static_cast<int>(left < MT ? (left < 0 ? 0 : left) : MT);
-                    other_bytes = b_bytes + (a_outer ? (other + 63) / 64 * 8192 : (other + MT - 1) / MT * R::A_PLANE);
+                    other_bytes = b_bytes + (a_outer ? (other + 63) / 64 * 8192 : (other + MT - 1) / MT * a.a_rows * 128);
                 }
                 int64_t m = t.seg;
                 if (MODE == PRODUCT_FORWARD && p.index) m = __ldg(p.index + t.seg);
@@ -869,7 +875,7 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
         for (uint32_t i = first; ok && i < items; i += stride) {
             item_at<MODE, NT, CG>(a, beg, pre, i, t);
             const int share = share_of(columns_of(t)), lanes = lanes_of(t);
-            const int a_rows = a_outer ? (lanes + 63) & ~63 : MT, b_rows = b_outer ? (share + 63) & ~63 : share;
+            const int a_rows = a_outer ? (lanes + 63) & ~63 : a.a_rows, b_rows = b_outer ? (share + 63) & ~63 : share;
             int64_t m = t.seg;
             if (MODE == PRODUCT_FORWARD && p.index) m = __ldg(p.index + t.seg);
             for (int kb = t.kb0; kb < t.kb1; ++kb) {
@@ -949,7 +955,7 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
             for (uint32_t i = first; ok && i < items; i += stride) {
                 item_at<MODE, NT, CG>(a, beg, pre, i, t);
                 if (t.kb1 <= t.kb0 || t.part != 0) continue;
-                for (int r = tl; r < t.rows; r += 128) low_adapter[r] = adapter_of(p, t.row0 + r);
+                for (int r = tl; r < t.rows; r += 128) low_adapter[r] = adapter_of(p, near_offsets, t.row0 + r);
                 bar_low();
                 int runs = 0;
                 for (int r = tl; r - tl < NT; r += 128) {
@@ -1017,6 +1023,7 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                 item_at<MODE, NT, CG>(a, beg, pre, i, t);
                 const uint32_t idesc = tc_idesc(type, MT * CG, CG * share_of(columns_of(t)), a_outer, b_outer);
                 const int64_t sum = MODE == PRODUCT_WEIGHTS ? t.rows : p.K;
+                bool low_left = R::LOW && p.u && t.part == 0;
                 for (int piece = t.kb0; ok && piece < t.kb1; piece += a.flush) {
                     const int piece_end = t.kb1 - piece < a.flush ? t.kb1 : piece + a.flush;
                     ok = wait_for<CG>(acc_empty + buf, bph, p.status);
@@ -1045,20 +1052,23 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                             }
                         }
                         tc_commit<CG>(empty + st);
-                        if (R::LOW && p.u && t.part == 0 && kb + 1 == t.kb1) {
-                            // the low-rank part, from a stage of its own: bfloat16 parts, whatever the type
+                        if (R::LOW && low_left && ((kb - t.kb0) % LOW_EVERY == LOW_EVERY - 1 || kb + 1 == t.kb1)) {
+                            // the low-rank part's blocks, from a stage of their own, in
+                            // between (a fixed order), so that they are laid out meanwhile;
+                            // bfloat16 parts, whatever the type
                             const uint32_t low_idesc = tc_idesc(1, MT * CG, CG * share_of(columns_of(t)), false, false);
                             const uint64_t la = tc_smem_desc(smem_u32(stages + R::STAGES * R::STAGE), 8192);
                             const uint64_t lb = tc_smem_desc(smem_u32(stages + R::STAGES * R::STAGE) + R::A_PLANE, 8192);
-                            for (int last = 0; !last; low_ph ^= 1) {
+                            do {
                                 ok = wait_for<CG>(low_full, low_ph, p.status);
                                 if (!ok) break;
+                                low_ph ^= 1;
                                 tc_fence_after();
                                 const int steps = *reinterpret_cast<volatile int*>(low_steps);
-                                last = steps & 8;
+                                low_left = (steps & 8) == 0;
                                 for (int k = 0; k < (steps & 7); ++k) tc_mma<CG>(acc, la + 2 * k, lb + 2 * k, low_idesc, true);
                                 tc_commit<CG>(low_empty);
-                            }
+                            } while (low_left && kb + 1 == t.kb1);
                             if (!ok) break;
                         }
                         if (kb + 1 == piece_end) tc_commit<CG>(acc_full + buf);
@@ -1109,7 +1119,7 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
             if constexpr (MODE == PRODUCT_ADAPTERS) {
                 bar_drain();       // the table of the tile before has been read
                 for (int r = td; r < t.rows; r += EPW * 32) {
-                    tile_adapter[r] = adapter_of(p, t.row0 + r);
+                    tile_adapter[r] = adapter_of(p, near_offsets, t.row0 + r);
                 }
                 bar_drain();
                 if (R::LOW) {
@@ -1402,7 +1412,7 @@ cudaError_t launch_shape(const KernelArgs& a, const ProductPlan& plan, cudaStrea
         } else {
             const int64_t mats = MODE == PRODUCT_ADAPTERS ? 1 : (p.index ? p.L : p.S);
             const int64_t rows = p.trans ? p.N : p.K, cols = p.trans ? p.K : p.N;
-            ok = make_map(&ma, p.type, p.w, cols, rows, p.ldw, mats, mats > 1 ? p.stride_w : rows * p.ldw, p.trans ? MT : KB) &&
+            ok = make_map(&ma, p.type, p.w, cols, rows, p.ldw, mats, mats > 1 ? p.stride_w : rows * p.ldw, p.trans ? a.a_rows : KB) &&
                  make_map(&mb, p.type, p.x, p.K, p.R, p.ldx, 0, 0, rows_box);
         }
         if (!ok) return cudaErrorInvalidValue;
@@ -1423,7 +1433,7 @@ cudaError_t launch_shape(const KernelArgs& a, const ProductPlan& plan, cudaStrea
         attr[attrs].val.clusterDim.y = attr[attrs].val.clusterDim.z = 1;
         ++attrs;
     }
-    const bool overlap = MODE == PRODUCT_ADAPTERS && a.p.u;
+    const bool overlap = MODE == PRODUCT_ADAPTERS && a.p.overlap;
     if (overlap) {
         attr[attrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[attrs].val.programmaticStreamSerializationAllowed = 1;
@@ -1483,8 +1493,9 @@ ProductPlan plan_product(int mode, const ProductParams& p) {
     d.tensor = p.K > 0 && p.R > 0 && mats > 0 && tensor_copyable(p.x, p.ldx, p.type) && tensor_copyable(p.w, p.ldw, p.type) &&
                (mats == 1 || tensor_copyable(p.w, p.stride_w, p.type));
     const int64_t segments = mode == PRODUCT_ADAPTERS ? 1 : p.S;
-    // few rows per segment: small tiles and a deeper ring; weights: few columns of x
-    d.narrow = weights ? p.K <= 64 : p.R <= 64 * segments;
+    // few rows per segment, or too few tiles to go round: small tiles and a
+    // deeper ring; weights: few columns of x
+    d.narrow = weights ? p.K <= 64 : p.R <= 64 * segments || (p.N <= MT && p.R <= 128 * p.sms);
     const int NT = tile_columns(p, d.narrow);
     // two CTAs on a tile of twice the lanes, unless that leaves one of them without lanes
     d.pair = d.tensor && p.type != PT_F32 && !d.narrow && (p.N > 1024 || ceil_to(p.N, MT) % 2 == 0);
@@ -1545,6 +1556,7 @@ cudaError_t launch_product(int mode, const ProductParams& p, const ProductPlan& 
     a.parts = plan.parts;
     a.part_blocks = plan.part_blocks;
     a.kblocks = static_cast<int32_t>(ceil_to(p.K, KB));
+    a.a_rows = static_cast<int32_t>(std::min<int64_t>(MT, ceil_to(p.N, 16) * 16));
     a.flush = p.type == PT_F32 ? 8 : (p.out_type == PT_F32 && !p.index ? 12 : NEVER_FLUSH);
     const int64_t out_step = mode == PRODUCT_WEIGHTS ? p.N : p.ldo;
     a.wide_rows = p.N % 8 == 0 && out_step % 8 == 0 && reinterpret_cast<uintptr_t>(p.out) % 16 == 0;

@@ -32,6 +32,7 @@ struct ProductParams {
     const float* u;         // [R, rank] scaled products with a
     const void* b;          // [L][N, rank]
     int64_t rank;
+    int32_t overlap;        // u's kernel lets this one start beside it
     // library-owned
     unsigned char* ws;      // see ProductPlan
     unsigned int* status;   // device status word
