@@ -80,6 +80,7 @@ struct Ring {
 struct KernelArgs {
     ProductParams p;
     int32_t mtiles, ntiles, parts, part_blocks, kblocks;
+    int32_t box_rows;   // rows of one copy of x
     int32_t a_rows;     // rows of one copy of A whose sum is contiguous
     int32_t wide_rows;  // 16-bit results: 16-byte stores fit
     int32_t flush;      // blocks of the sum after which the accumulators go to the result
@@ -261,7 +262,7 @@ __device__ __forceinline__ bool bar_low_all(bool ok) {
     return r != 0;
 }
 
-// The adapter of a row: its segment's, or -1.
+// The adapter of a row: its segment's, or -1.  near: the offsets and then the adapters in shared memory, or NULL.
 __device__ __forceinline__ int adapter_of(const ProductParams& p, const int* near, int row) {
     auto offset = [&](int64_t s) { return near ? near[s] : offset_at(p, s); };
     int64_t lo = 0, hi = p.S;      // the last segment that starts at or before the row
@@ -270,7 +271,7 @@ __device__ __forceinline__ int adapter_of(const ProductParams& p, const int* nea
         if (offset(mid) <= row) lo = mid; else hi = mid;
     }
     int l = -1;
-    if (p.S > 0 && offset(lo) <= row && row < offset(lo + 1)) l = __ldg(p.index + lo);
+    if (p.S > 0 && offset(lo) <= row && row < offset(lo + 1)) l = near ? near[NEAR_SEGMENTS + 1 + lo] : __ldg(p.index + lo);
     return l >= 0 && l < p.L ? l : -1;
 }
 
@@ -609,72 +610,91 @@ __device__ __forceinline__ void part_of_16(float (&f)[16], int part, uint4 (&v)[
     v[1] = make_uint4(r[4], r[5], r[6], r[7]);
 }
 
+// 16 ranks of an adapter's b in column m, from q on, and of a row's u.
+__device__ __forceinline__ void ranks_of_b(const ProductParams& p, int l, int64_t m, int q, uint32_t (&raw)[8]) {
+    const int rank = static_cast<int>(p.rank), width = m < p.N ? rank - q : 0;
+    const uint16_t* b = static_cast<const uint16_t*>(p.b) + (width > 0 ? (int64_t(l) * p.N + m) * rank + q : 0);
+    if (rank % 8 == 0 && (reinterpret_cast<uintptr_t>(p.b) & 15) == 0) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const uint4 x = k * 8 < width ? __ldg(reinterpret_cast<const uint4*>(b) + k) : make_uint4(0, 0, 0, 0);
+            raw[4 * k] = x.x, raw[4 * k + 1] = x.y, raw[4 * k + 2] = x.z, raw[4 * k + 3] = x.w;
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            raw[k] = 2 * k < width ? __ldg(b + 2 * k) : 0;
+            if (2 * k + 1 < width) raw[k] |= static_cast<uint32_t>(__ldg(b + 2 * k + 1)) << 16;
+        }
+    }
+}
+__device__ __forceinline__ void ranks_of_u(const ProductParams& p, bool in, int64_t row, int q, float (&f)[16]) {
+    const int rank = static_cast<int>(p.rank), width = in ? rank - q : 0;
+    const float* u = p.u + (width > 0 ? row * rank + q : 0);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) f[k] = 0.0f;
+    if (rank % 4 == 0) {
+#pragma unroll
+        for (int k = 0; k < 16; k += 4) {
+            const float4 x = k < width ? *reinterpret_cast<const float4*>(u + k) : make_float4(0, 0, 0, 0);
+            f[k] = x.x, f[k + 1] = x.y, f[k + 2] = x.z, f[k + 3] = x.w;
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+            if (k < width) f[k] = u[k];
+    }
+}
+
 // One block of an adapter's part of the sum, for the rows [row, end) of the
 // tile: up to four steps of 16 ranks, each one product of a part of b (A: a
 // thread per lane of the tile) and a part of u (B: a thread per row, zeros
-// outside the run).  bfloat16 b: parts (b, u) = (0, 0), (0, 1), (0, 2);
-// float16 b has two parts: and (1, 0), (1, 1); what is left out is below 2^-21.
-__device__ __forceinline__ void lay_adapter(const ProductParams& p, int s0, int total, int slices, int l, int64_t m, int row0, int base,
+// outside the run).  The steps of 16 ranks follow one another: bfloat16 b:
+// parts (b, u) = (0, 0), (0, 1), (0, 2); float16 b has two parts: and (1, 0),
+// (1, 1); what is left out is below 2^-21.  A block's steps touch two groups
+// of 16 ranks at most, which are loaded together.
+__device__ __forceinline__ void lay_adapter(const ProductParams& p, int s0, int total, int pairs, int l, int64_t m, int row0, int base,
                                             int share, int row, int end, unsigned char* sa, unsigned char* sb, int tl) {
-    const int rank = static_cast<int>(p.rank);
-    const bool vec_b = rank % 8 == 0 && (reinterpret_cast<uintptr_t>(p.b) & 15) == 0;
+    const int j0 = s0 / pairs;
+    {
+        uint32_t raw[2][8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int s = s0 + i;
-        if (s >= total) break;
-        const int pair = s / slices, q = (s - pair * slices) * 16, width = rank - q;
-        const int pb = pair >= 3 ? 1 : 0, pu = pair >= 3 ? pair - 3 : pair;
-        // A
-        uint32_t raw[8];
-        const uint16_t* b = static_cast<const uint16_t*>(p.b) + (int64_t(l) * p.N + m) * rank + q;
-        if (vec_b) {
+        for (int k = 0; k < 2; ++k) ranks_of_b(p, l, m, (j0 + k) * 16, raw[k]);
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const uint4 x = m < p.N && k * 8 < width ? __ldg(reinterpret_cast<const uint4*>(b) + k) : make_uint4(0, 0, 0, 0);
-                raw[4 * k] = x.x, raw[4 * k + 1] = x.y, raw[4 * k + 2] = x.z, raw[4 * k + 3] = x.w;
+        for (int i = 0; i < 4; ++i) {
+            const int s = s0 + i, second = s >= (j0 + 1) * pairs ? 1 : 0, pair = s - (j0 + second) * pairs;
+            if (s >= total) break;
+            uint32_t r[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) r[k] = second ? raw[1][k] : raw[0][k];
+            uint4 v[2] = {make_uint4(r[0], r[1], r[2], r[3]), make_uint4(r[4], r[5], r[6], r[7])};
+            if (p.type == PT_F16) {
+                float f[16];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&r[k]));
+                    f[2 * k] = x.x, f[2 * k + 1] = x.y;
+                }
+                part_of_16(f, pair >= 3 ? 1 : 0, v);
             }
-        } else {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                raw[k] = m < p.N && 2 * k < width ? __ldg(b + 2 * k) : 0;
-                if (m < p.N && 2 * k + 1 < width) raw[k] |= static_cast<uint32_t>(__ldg(b + 2 * k + 1)) << 16;
-            }
+            for (int k = 0; k < 2; ++k) *reinterpret_cast<uint4*>(sa + tl * 128 + (((2 * i + k) ^ (tl & 7)) << 4)) = v[k];
         }
-        uint4 v[2];
-        if (p.type == PT_F16) {
-            float f[16];
+    }
+    for (int r = tl; r < share; r += 128) {
+        const bool in = base + r >= row && base + r < end;
+        float f[2][16];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&raw[k]));
-                f[2 * k] = x.x, f[2 * k + 1] = x.y;
-            }
-            part_of_16(f, pb, v);
-        } else {
-            v[0] = make_uint4(raw[0], raw[1], raw[2], raw[3]);
-            v[1] = make_uint4(raw[4], raw[5], raw[6], raw[7]);
-        }
+        for (int k = 0; k < 2; ++k) ranks_of_u(p, in, int64_t(row0) + base + r, (j0 + k) * 16, f[k]);
 #pragma unroll
-        for (int k = 0; k < 2; ++k) *reinterpret_cast<uint4*>(sa + tl * 128 + (((2 * i + k) ^ (tl & 7)) << 4)) = v[k];
-        // B
-        for (int r = tl; r < share; r += 128) {
-            float f[16];
-            const bool in = base + r >= row && base + r < end;
-            const float* u = p.u + (int64_t(row0) + base + r) * rank + q;
+        for (int i = 0; i < 4; ++i) {
+            const int s = s0 + i, second = s >= (j0 + 1) * pairs ? 1 : 0, pair = s - (j0 + second) * pairs;
+            if (s >= total) break;
+            float g[16];
 #pragma unroll
-            for (int k = 0; k < 16; ++k) f[k] = 0.0f;
-            if (in && rank % 4 == 0) {
-#pragma unroll
-                for (int k = 0; k < 16; k += 4)
-                    if (k < width) {
-                        const float4 x = *reinterpret_cast<const float4*>(u + k);
-                        f[k] = x.x, f[k + 1] = x.y, f[k + 2] = x.z, f[k + 3] = x.w;
-                    }
-            } else if (in) {
-#pragma unroll
-                for (int k = 0; k < 16; ++k)
-                    if (k < width) f[k] = u[k];
-            }
-            part_of_16(f, pu, v);
+            for (int k = 0; k < 16; ++k) g[k] = second ? f[1][k] : f[0][k];
+            uint4 v[2];
+            part_of_16(g, pair >= 3 ? pair - 3 : pair, v);
 #pragma unroll
             for (int k = 0; k < 2; ++k) *reinterpret_cast<uint4*>(sb + r * 128 + (((2 * i + k) ^ (r & 7)) << 4)) = v[k];
         }
@@ -711,7 +731,6 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
     using R = Ring<MODE, NT, PL, CG, TENSOR>;
     static_assert(CG == 1 || (TENSOR && PL == 1), "pairs take their operands as they are copied");
     constexpr int HALVES = PL == 1 ? 1 : 2;          // copies of 128 bytes that make 64 values
-    constexpr int BOX_ROWS = NT <= 64 ? 16 : 64;     // rows of one copy of x (forward)
     extern __shared__ unsigned char raw[];
     unsigned char* stages = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
     unsigned char* staging = stages + R::ALL_STAGES * R::STAGE;      // 16-byte aligned, as all that follows it
@@ -763,7 +782,10 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
     // (PL == 3: that space is the staging)
     const int* near_offsets = MODE == PRODUCT_ADAPTERS && PL == 1 && is_near ? near : nullptr;
     if (near_offsets && p.S > 0)
-        for (int64_t s = tid; s <= p.S; s += blockDim.x) near[s] = offset_at(p, s);
+        for (int64_t s = tid; s <= p.S; s += blockDim.x) {
+            near[s] = offset_at(p, s);
+            if (s < p.S) near[NEAR_SEGMENTS + 1 + s] = __ldg(p.index + s);
+        }
     tc_fence_before();
     __syncthreads();
     if (CG == 2) cluster_sync();
@@ -805,8 +827,8 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                 const uint32_t blocks = t.kb1 > t.kb0 ? t.kb1 - t.kb0 : 0;
                 const int columns = columns_of(t), share = share_of(columns), lanes = lanes_of(t);
                 const int a_boxes = a_outer ? (lanes + 63) / 64 : (lanes + MT - 1) / MT;
-                const int b_boxes = b_outer ? (share + 63) / 64 : (share + BOX_ROWS - 1) / BOX_ROWS;
-                const uint32_t a_bytes = a_boxes * (a_outer ? 8192 : a.a_rows * 128) * HALVES, b_bytes = b_boxes * (b_outer ? 8192 : BOX_ROWS * 128) * HALVES;
+                const int b_boxes = b_outer ? (share + 63) / 64 : (share + a.box_rows - 1) / a.box_rows;
+                const uint32_t a_bytes = a_boxes * (a_outer ? 8192 : a.a_rows * 128) * HALVES, b_bytes = b_boxes * (b_outer ? 8192 : a.box_rows * 128) * HALVES;
                 const int m0 = t.m0 + rank * MT;
                 uint32_t other_bytes = 0;
                 if (CG == 2) {
@@ -849,7 +871,7 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                                 tensor_load_3d<CG>(da, &map_a, k0 + h * 32, m0, static_cast<int>(m), bar);
                             }
                             for (int x = 0; x < b_boxes; ++x)
-                                tensor_load_2d<CG>(db + x * BOX_ROWS * 128, &map_b, k0 + h * 32, r0 + x * BOX_ROWS, bar);
+                                tensor_load_2d<CG>(db + x * a.box_rows * 128, &map_b, k0 + h * 32, r0 + x * a.box_rows, bar);
                         }
                     }
                     if ((st += 2) >= R::STAGES) {
@@ -948,7 +970,7 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
             const int tl = tid - LOW_WARP * 32;
             unsigned char* sa = stages + R::STAGES * R::STAGE;
             unsigned char* sb = sa + R::A_PLANE;
-            const int slices = static_cast<int>((p.rank + 15) / 16), total = slices * (p.type == PT_BF16 ? 3 : 5);
+            const int pairs = p.type == PT_BF16 ? 3 : 5, total = static_cast<int>((p.rank + 15) / 16) * pairs;
             uint32_t ph = 1;
             bool ok = true;
             Item t;
@@ -994,7 +1016,7 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                         last = runs == 0 && s0 + 4 >= total;
                         if (!mine) last = true;
                         if (mine) {
-                            lay_adapter(p, s0, total, slices, l, t.m0 + rank * MT + tl, t.row0, rank * share_of(t.rows), share_of(t.rows),
+                            lay_adapter(p, s0, total, pairs, l, t.m0 + rank * MT + tl, t.row0, rank * share_of(t.rows), share_of(t.rows),
                                         row, end, sa, sb, tl);
                         }
                         if (tl == 0) *low_steps = (mine ? min(4, total - s0) : 0) | (last ? 8 : 0);
@@ -1405,7 +1427,6 @@ cudaError_t launch_shape(const KernelArgs& a, const ProductPlan& plan, cudaStrea
         e = cudaSetDevice(dev);
         if (e != cudaSuccess) return e;
         const ProductParams& p = a.p;
-        const int rows_box = NT <= 64 ? 16 : 64;
         bool ok;
         if (MODE == PRODUCT_WEIGHTS) {
             ok = make_map(&ma, p.type, p.w, p.N, p.R, p.ldw, 0, 0, KB) && make_map(&mb, p.type, p.x, p.K, p.R, p.ldx, 0, 0, KB);
@@ -1413,7 +1434,7 @@ cudaError_t launch_shape(const KernelArgs& a, const ProductPlan& plan, cudaStrea
             const int64_t mats = MODE == PRODUCT_ADAPTERS ? 1 : (p.index ? p.L : p.S);
             const int64_t rows = p.trans ? p.N : p.K, cols = p.trans ? p.K : p.N;
             ok = make_map(&ma, p.type, p.w, cols, rows, p.ldw, mats, mats > 1 ? p.stride_w : rows * p.ldw, p.trans ? a.a_rows : KB) &&
-                 make_map(&mb, p.type, p.x, p.K, p.R, p.ldx, 0, 0, rows_box);
+                 make_map(&mb, p.type, p.x, p.K, p.R, p.ldx, 0, 0, a.box_rows);
         }
         if (!ok) return cudaErrorInvalidValue;
     }
@@ -1556,6 +1577,7 @@ cudaError_t launch_product(int mode, const ProductParams& p, const ProductPlan& 
     a.parts = plan.parts;
     a.part_blocks = plan.part_blocks;
     a.kblocks = static_cast<int32_t>(ceil_to(p.K, KB));
+    a.box_rows = plan.narrow && p.R <= 32 * (mode == PRODUCT_FORWARD ? p.S : 1) ? 16 : 64;
     a.a_rows = static_cast<int32_t>(std::min<int64_t>(MT, ceil_to(p.N, 16) * 16));
     a.flush = p.type == PT_F32 ? 8 : (p.out_type == PT_F32 && !p.index ? 12 : NEVER_FLUSH);
     const int64_t out_step = mode == PRODUCT_WEIGHTS ? p.N : p.ldo;
