@@ -510,6 +510,7 @@ struct Operand {
     int64_t col0, col_end;
     int rows;
     bool outer;
+    int steps;       // outer: of a block's 64 steps, those that are used (a multiple of 16)
 };
 
 // The three bfloat16 parts of two values: by truncation, each rest exact.
@@ -553,11 +554,13 @@ __device__ __forceinline__ void load_any(const Operand& x, unsigned char* dst, i
     constexpr int AHEAD = 2;
     const int t = threadIdx.x - LOAD_WARP * 32, unit = t & 7;
     const bool pairs = PL == 1 && (reinterpret_cast<uintptr_t>(x.base) & 3) == 0 && x.ld % 2 == 0 && x.col_end % 2 == 0;
-    for (int row0 = t >> 3; row0 < x.rows; row0 += AHEAD * LOADERS / 8) {
+    const int count = x.outer ? (x.rows >> 6) * x.steps : x.rows;
+    auto row_of = [&](int i) { return x.outer && x.steps < 64 ? i / x.steps * 64 + i % x.steps : i; };
+    for (int row0 = t >> 3; row0 < count; row0 += AHEAD * LOADERS / 8) {
         uint32_t raw[AHEAD][8];
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
-            const int row = row0 + i * LOADERS / 8;
+            const int at_row = row0 + i * LOADERS / 8, row = at_row < count ? row_of(at_row) : x.rows;
             const int64_t r = x.row0 + (x.outer ? row & 63 : row), c = x.col0 + unit * 8 + (x.outer ? row & ~63 : 0);
             const bool in = row < x.rows && r < x.row_end;
             const int64_t at = r * x.ld + c;
@@ -576,8 +579,8 @@ __device__ __forceinline__ void load_any(const Operand& x, unsigned char* dst, i
         }
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
-            const int row = row0 + i * LOADERS / 8;
-            if (row >= x.rows) break;
+            if (row0 + i * LOADERS / 8 >= count) break;
+            const int row = row_of(row0 + i * LOADERS / 8);
             unsigned char* to = dst + row * 128 + ((unit ^ (row & 7)) << 4);
             if constexpr (PL == 1) {
                 *reinterpret_cast<uint4*>(to) =
@@ -907,6 +910,8 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                 unsigned char* sa = stages + st * R::STAGE;
                 unsigned char* sb = sa + PL * R::A_PLANE;
                 const bool keep = keeps.a(t, kb);
+                const int64_t left = (MODE == PRODUCT_WEIGHTS ? t.rows : p.K) - int64_t(kb) * KB;
+                const int used = left < KB ? static_cast<int>(left + 15) & ~15 : KB;
                 if constexpr (TENSOR) {
                     // rows past the segment's end belong to others: they count as zeros
                     const int valid = MODE == PRODUCT_WEIGHTS ? t.rows - kb * KB : KB;
@@ -914,18 +919,18 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                     split_rows(b_rows, valid, sb, R::B_PLANE);
                 } else if (MODE == PRODUCT_WEIGHTS) {
                     const int64_t r = t.row0 + kb * KB, re = t.row0 + t.rows;
-                    load_any<PL>(Operand{p.w, p.ldw, r, re, t.m0, a.cols_m, a_rows, true}, sa, R::A_PLANE);
-                    load_any<PL>(Operand{p.x, p.ldx, r, re, t.n0, a.cols_n, b_rows, true}, sb, R::B_PLANE);
+                    load_any<PL>(Operand{p.w, p.ldw, r, re, t.m0, a.cols_m, a_rows, true, used}, sa, R::A_PLANE);
+                    load_any<PL>(Operand{p.x, p.ldx, r, re, t.n0, a.cols_n, b_rows, true, used}, sb, R::B_PLANE);
                 } else {
                     const void* w = static_cast<const unsigned char*>(p.w) + m * p.stride_w * (PL == 1 ? 2 : 4);
                     const int64_t k = int64_t(kb) * KB;
                     if (keep) {
                     } else if (a_outer) {
-                        load_any<PL>(Operand{w, p.ldw, k, p.K, t.m0, a.cols_m, a_rows, true}, sa, R::A_PLANE);
+                        load_any<PL>(Operand{w, p.ldw, k, p.K, t.m0, a.cols_m, a_rows, true, used}, sa, R::A_PLANE);
                     } else {
-                        load_any<PL>(Operand{w, p.ldw, t.m0, a.cols_m, k, p.K, a_rows, false}, sa, R::A_PLANE);
+                        load_any<PL>(Operand{w, p.ldw, t.m0, a.cols_m, k, p.K, a_rows, false, used}, sa, R::A_PLANE);
                     }
-                    load_any<PL>(Operand{p.x, p.ldx, t.row0, t.row0 + t.rows, k, p.K, b_rows, false}, sb, R::B_PLANE);
+                    load_any<PL>(Operand{p.x, p.ldx, t.row0, t.row0 + t.rows, k, p.K, b_rows, false, used}, sb, R::B_PLANE);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -1185,17 +1190,22 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                     if (c >= n_left) break;
                     const int n = n_left - c < W ? n_left - c : W;
                     if (adding) {
-                        float d[W];
+                        const float* part = a.partials + slot + (int64_t(-t.part) * CG * NT + c) * MT + lane;
 #pragma unroll
-                        for (int j = 0; j < W; ++j) d[j] = 0.0f;
-                        for (int q = 0; q < t.parts; ++q) {
-                            const float* part = a.partials + slot + (int64_t(q - t.part) * CG * NT + c) * MT;
+                        for (int j0 = 0; j0 < W; j0 += 8) {
+                            if (j0 >= n) break;
+                            float d[8];
 #pragma unroll
-                            for (int j = 0; j < W; ++j)
-                                if (j < n) d[j] += __ldcg(part + j * MT + lane);
+                            for (int j = 0; j < 8; ++j) d[j] = 0.0f;
+#pragma unroll 4
+                            for (int q = 0; q < t.parts; ++q) {
+#pragma unroll
+                                for (int j = 0; j < 8; ++j)
+                                    if (j0 + j < n) d[j] += __ldcg(part + (int64_t(q) * CG * NT + j0 + j) * MT);
+                            }
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) v[j0 + j] += d[j];
                         }
-#pragma unroll
-                        for (int j = 0; j < W; ++j) v[j] += d[j];
                     } else if (summed) {
                         float d[W], lo[W];
                         tmem_load(from + c, d);
@@ -1262,63 +1272,47 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
     }
 }
 
-// Adds the parts of the split segments of the weights' product: block
-// (x, y) takes 16 columns of one tile of the split segment, if there is one,
-// that starts in chunk x / tiles.  With few parts each warp adds whole
-// columns; with many the eight warps share a column's parts.  Either order
-// is a function of the number of parts alone.
-constexpr int ADD_COLS = 16;
+// Adds the parts of the split segments of the weights' product: a block per
+// tile of a segment (blockIdx.x) and four of its columns; warps w and w + 4
+// each add half of a column's parts, in order, and then the halves.
+constexpr int ADD_COLS = 4;
 
 template <int NT, int CG>
 __global__ void __launch_bounds__(256) add_parts_kernel(const __grid_constant__ KernelArgs a) {
-    __shared__ float4 part_sum[8][32];
+    __shared__ float4 half_sum[ADD_COLS][32];
     const ProductParams& p = a.p;
     const int per = a.mtiles * a.ntiles, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t j = blockIdx.x / per;
-    const int r = static_cast<int>(blockIdx.x - j * per);
-    int64_t lo = 0, hi = p.S;        // the last segment that starts before the chunk's end
-    while (hi - lo > 1) {
-        const int64_t mid = (lo + hi) >> 1;
-        if (offset_at(p, mid) < (j + 1) * a.chunk) lo = mid; else hi = mid;
-    }
-    const int64_t b = offset_at(p, lo), e = offset_at(p, lo + 1);
-    if (b / a.chunk != j || e - b <= a.chunk) return;
-    const int parts = static_cast<int>((e - b + a.chunk - 1) / a.chunk);
+    const int64_t s = blockIdx.x / per;
+    const int r = static_cast<int>(blockIdx.x - s * per);
+    const int64_t b = offset_at(p, s), e = offset_at(p, s + 1);
+    if (e - b <= a.chunk) return;
+    const int parts = static_cast<int>((e - b + a.chunk - 1) / a.chunk), half = (parts + 1) / 2;
     const int rank = blockIdx.z;
     const int64_t m = (r % a.mtiles * CG + rank) * MT + lane * 4;
-    const int n0 = r / a.mtiles * NT;
-    auto part = [&](int q, int c) {
-        const int64_t slot = (2 * (j + q) + (q == 0 ? 1 : 0)) * per + r;
-        return __ldcg(reinterpret_cast<const float4*>(a.partials + ((slot * CG + rank) * NT + c) * MT) + lane);
-    };
-    auto add = [](float4& x, const float4& y) { x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w; };
-    auto put = [&](int c, const float4& v) {
-        const float f[4] = {v.x, v.y, v.z, v.w};
-        const int64_t at = (lo * a.cols_n + n0 + c) * a.cols_m + m;
-        for (int i = 0; i < 4; ++i) {
-            if (m + i >= a.cols_m) break;
-            if (p.out_type == PT_F32) static_cast<float*>(p.out)[at + i] = f[i];
-            else if (p.out_type == PT_F16) static_cast<__half*>(p.out)[at + i] = __float2half_rn(f[i]);
-            else static_cast<__nv_bfloat16*>(p.out)[at + i] = __float2bfloat16_rn(f[i]);
-        }
-    };
-    const bool shared = parts > 16;
-    const int c1 = static_cast<int>(min(int64_t(blockIdx.y + 1) * ADD_COLS, a.cols_n - n0));
-    for (int c = blockIdx.y * ADD_COLS + (shared ? 0 : warp); c < c1; c += shared ? 1 : 8) {
-        float4 v = make_float4(0, 0, 0, 0);
+    const int n0 = r / a.mtiles * NT, c = blockIdx.y * ADD_COLS + (warp & 3);
+    const bool in = m < a.cols_m && n0 + c < a.cols_n && c < NT;
+    const int q0 = warp < 4 ? 0 : half, q1 = warp < 4 ? half : parts;
+    const int64_t j = b / a.chunk;
+    float4 v = make_float4(0, 0, 0, 0);
+    if (in) {
 #pragma unroll 8
-        for (int q = shared ? warp : 0; q < parts; q += shared ? 8 : 1) add(v, part(q, c));
-        if (shared) {
-            part_sum[warp][lane] = v;
-            __syncthreads();
-            if (warp == 0) {
-                for (int w = 1; w < 8; ++w) add(v, part_sum[w][lane]);
-                put(c, v);
-            }
-            __syncthreads();
-        } else {
-            put(c, v);
+        for (int q = q0; q < q1; ++q) {
+            const int64_t slot = (2 * (j + q) + (q == 0 ? 1 : 0)) * per + r;
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(a.partials + ((slot * CG + rank) * NT + c) * MT) + lane);
+            v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
         }
+    }
+    if (warp >= 4) half_sum[warp - 4][lane] = v;
+    __syncthreads();
+    if (warp >= 4 || !in) return;
+    const float4 x = half_sum[warp][lane];
+    const float f[4] = {v.x + x.x, v.y + x.y, v.z + x.z, v.w + x.w};
+    const int64_t at = (s * a.cols_n + n0 + c) * a.cols_m + m;
+    for (int i = 0; i < 4; ++i) {
+        if (m + i >= a.cols_m) break;
+        if (p.out_type == PT_F32) static_cast<float*>(p.out)[at + i] = f[i];
+        else if (p.out_type == PT_F16) static_cast<__half*>(p.out)[at + i] = __float2half_rn(f[i]);
+        else static_cast<__nv_bfloat16*>(p.out)[at + i] = __float2bfloat16_rn(f[i]);
     }
 }
 
@@ -1357,7 +1351,7 @@ __global__ void __launch_bounds__(DOT_RANKS * 32) lora_rows_kernel(const __grid_
     constexpr int V = 16 / sizeof(T);
     float sum = 0.0f, sum2 = 0.0f;
     if (((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(a)) & 15) == 0 && p.K % V == 0) {
-#pragma unroll 4
+#pragma unroll 8
         for (int64_t k = lane * V; k < p.K; k += 32 * V) {
             const uint4 xr = __ldg(reinterpret_cast<const uint4*>(x + k)), ar = __ldg(reinterpret_cast<const uint4*>(a + k));
             const T *xv = reinterpret_cast<const T*>(&xr), *av = reinterpret_cast<const T*>(&ar);
@@ -1535,8 +1529,8 @@ ProductPlan plan_product(int mode, const ProductParams& p) {
             const int64_t chunk = std::max(least, ceil_to(ceil_to(p.R * per * cg, 4 * p.sms), KB) * KB);
             if (chunk < p.R) {
                 d.chunk = chunk;
-                d.add_blocks = static_cast<int32_t>((p.R / chunk + 1) * per);
-                slots = 2 * int64_t(d.add_blocks);
+                d.add_blocks = static_cast<int32_t>(segments * per);
+                slots = 2 * (p.R / chunk + 1) * per;
             }
         }
         items = (segments + p.R / d.chunk) * per;
