@@ -61,7 +61,9 @@ std::map<std::pair<int, cudaStream_t>, Scratch> g_scratch;
 // buffer of their own per (device, stream), so that the reduction it runs
 // keeps its scratch (and its ticket words) to itself.
 std::map<std::pair<int, cudaStream_t>, Scratch> g_sort_scratch;
-// The products' scratch: a buffer of their own per (device, stream).
+// The products' scratch: a buffer of their own per (device, stream).  A graph
+// captured from a stream holds its address, so a buffer that has become too
+// small is kept beside the larger one (each is at least twice the one before).
 std::map<std::pair<int, cudaStream_t>, Scratch> g_product_scratch;
 
 seg_status_t device_state(int dev, DeviceState** out) {
@@ -111,6 +113,37 @@ seg_status_t scratch_in(std::map<std::pair<int, cudaStream_t>, Scratch>& cache, 
 
 seg_status_t scratch_for(int dev, cudaStream_t stream, size_t bytes, Scratch** out) {
     return scratch_in(g_scratch, dev, stream, bytes, out);
+}
+
+// Scratch of the products: ordinary device memory, zeroed ticket words, made
+// outside of any capture of `stream` (a buffer that a capture allocates
+// belongs to its graph).
+seg_status_t product_scratch(int dev, cudaStream_t stream, size_t bytes, Scratch** out) {
+    Scratch& sc = g_product_scratch[std::make_pair(dev, stream)];
+    if (sc.bytes < bytes) {
+        const size_t want = std::max(std::max<size_t>(bytes, size_t(1) << 20), 2 * sc.bytes);
+        cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+        if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) return SEG_ERR_CUDA;
+        void* ptr = nullptr;
+        cudaStream_t own = nullptr;
+        cudaError_t e = cudaMalloc(&ptr, want);
+        const bool full = e != cudaSuccess;
+        if (!full) e = cudaStreamCreateWithFlags(&own, cudaStreamNonBlocking);
+        if (e == cudaSuccess) e = cudaMemsetAsync(ptr, 0, PRODUCT_TICKETS * 8, own);
+        if (e == cudaSuccess) e = cudaStreamSynchronize(own);
+        if (own) cudaStreamDestroy(own);
+        cudaThreadExchangeStreamCaptureMode(&mode);
+        if (e != cudaSuccess) {
+            cudaGetLastError();
+            if (ptr) cudaFree(ptr);
+            return full ? SEG_ERR_OUT_OF_MEMORY : SEG_ERR_CUDA;
+        }
+        sc.ptr = ptr;
+        sc.bytes = want;
+        sc.gen = 0;
+    }
+    *out = &sc;
+    return SEG_OK;
 }
 
 // ---------------------------------------------------------------------------
@@ -242,6 +275,7 @@ seg_status_t run_product(int mode, ProductParams p, cudaStream_t stream, Scratch
     p.sms = ds->sm_count;
     p.status = ds->status;
     p.ws = static_cast<unsigned char*>(sc->ptr);
+    // (after 2^32 calls the tag starts over: the counts are back at zero after every call)
     p.gen = ++sc->gen;
     const ProductPlan plan = plan_product(mode, p);
     if (plan.too_many) return SEG_ERR_UNSUPPORTED;
@@ -261,7 +295,7 @@ seg_status_t run_product(int mode, ProductParams p, cudaStream_t stream) {
     if (st != SEG_OK) return st;
     p.sms = ds->sm_count;
     Scratch* sc = nullptr;
-    st = scratch_in(g_product_scratch, dev, stream, static_cast<size_t>(plan_product(mode, p).bytes()), &sc);
+    st = product_scratch(dev, stream, static_cast<size_t>(plan_product(mode, p).bytes()), &sc);
     return st != SEG_OK ? st : run_product(mode, p, stream, sc, ds);
 }
 
@@ -858,7 +892,7 @@ seg_status_t seg_lora(const void* x, seg_dtype_t dtype, int64_t num_rows, int64_
     const bool by_rows = lora_by_rows(pa);
     const int64_t own = std::max(low && !by_rows ? plan_product(PRODUCT_FORWARD, pa).bytes() : 0, plan_product(PRODUCT_ADAPTERS, p).bytes());
     Scratch* sc = nullptr;
-    st = scratch_in(g_product_scratch, dev, stream, static_cast<size_t>(own + num_rows * rank * 4), &sc);
+    st = product_scratch(dev, stream, static_cast<size_t>(own + num_rows * rank * 4), &sc);
     if (st != SEG_OK) return st;
     float* u = reinterpret_cast<float*>(static_cast<unsigned char*>(sc->ptr) + own);
     if (low) {

@@ -1249,7 +1249,10 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                         red_max_relaxed_gpu(ticket, static_cast<unsigned long long>(p.gen) << 32);
                         const unsigned long long old = atom_add_release_gpu(ticket, 1);
                         fence_acq_rel_gpu();
-                        *last_part = static_cast<uint32_t>(old) + 1 == static_cast<uint32_t>(t.parts);
+                        const bool last = static_cast<uint32_t>(old) + 1 == static_cast<uint32_t>(t.parts);
+                        // the count starts at zero again: a replayed graph comes with the same generation
+                        if (last) atomicExch(ticket, old >> 32 << 32);
+                        *last_part = last;
                     }
                     bar_drain();
                     adding = *last_part;

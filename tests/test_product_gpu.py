@@ -92,7 +92,7 @@ def ref_grad(x, dy, off):
     return w, a
 
 
-SIZES = [(64, 64), (1, 1), (7, 5), (16, 128), (63, 129), (65, 127), (72, 136), (200, 300), (256, 8), (8, 256), (520, 264)]
+SIZES = [(64, 64), (1, 1), (7, 5), (16, 128), (63, 129), (65, 127), (72, 136), (200, 300), (256, 8), (8, 256), (520, 264), (136, 1104)]
 
 
 @pytest.mark.parametrize("dtype", TYPES)
@@ -439,3 +439,120 @@ def test_refusals():
             sr.seg_lora(*args)
     with pytest.raises(sr.SegReduceError):      # a rank above the limit
         sr.seg_lora(x, shared, torch.ones(1, 129, 8, device="cuda"), torch.ones(1, 16, 129, device="cuda"), off, ids)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rank", (8, 12, 40, 128))
+def test_lora_runs_of_rows(dtype, rank):
+    """Tiles of one adapter, of a few runs (an adapter twice among them) and of many, in one call and across its tiles."""
+    torch, sr = mods()
+    lens = [500, 20, 20, 300, 1, 1, 1, 2, 1, 1, 130, 0, 64] + [1] * 60 + [700]
+    off = np.concatenate([[0], np.cumsum(lens)]).astype(np.int64) + 2
+    rows = int(off[-1]) + 5
+    do = torch.from_numpy(off).cuda()
+    g = torch.Generator(device="cuda")
+    g.manual_seed(rank)
+    k, n, adapters = 1104, 264, 4
+    x, w = normal(g, (rows, k), dtype), normal(g, (n, k), dtype, k ** -0.5)
+    a, b = normal(g, (adapters, rank, k), dtype, k ** -0.5), normal(g, (adapters, n, rank), dtype, rank ** -0.5)
+    ids = np.arange(len(lens)) % (adapters + 1) - 1
+    ids[:4] = [1, 3, 1, -1]
+    adapter = torch.from_numpy(ids.astype(np.int32)).cuda()
+    scale = torch.tensor([0.5, -3.0, 1.0, 40.0], device="cuda")
+    got = sr.seg_lora(x, w, a, b, do, adapter, scale)
+    y, m = ref_lora(x, w, a, b, off, ids, scale)
+    check(got, y, m, k + rank, (dtype, rank))
+    for rep in range(3):
+        assert torch.equal(got, sr.seg_lora(x, w, a, b, do, adapter, scale))
+    assert sr.device_status() == 0
+
+
+def test_lora_many_requests():
+    """More requests than a CTA keeps offsets of, one row or none each."""
+    torch, sr = mods()
+    off, rows, do, g = case("many", 14)
+    k, n, rank, adapters = 72, 136, 16, 7
+    x, w = normal(g, (rows, k), "bfloat16"), normal(g, (n, k), "bfloat16", k ** -0.5)
+    a, b = normal(g, (adapters, rank, k), "bfloat16", k ** -0.5), normal(g, (adapters, n, rank), "bfloat16")
+    ids = np.random.default_rng(1).integers(-1, adapters, size=len(off) - 1)
+    adapter = torch.from_numpy(ids.astype(np.int32)).cuda()
+    got = sr.seg_lora(x, w, a, b, do, adapter)
+    y, m = ref_lora(x, w, a, b, off, ids, None)
+    check(got, y, m, k + rank, "many")
+    bad = do.clone()
+    bad[3], bad[5], bad[700] = 1 << 40, -9, 0        # malformed: unspecified, but nothing else is written
+    big = torch.full((rows + 2, n), 7.0, device="cuda", dtype=torch.bfloat16)
+    sr.seg_lora(x, w, a, b, bad, adapter, out=big[1:-1])
+    torch.cuda.synchronize()
+    assert bool((big[0] == 7).all() and (big[-1] == 7).all()) and sr.device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_large_tiles(dtype):
+    """Several tiles of rows, lanes and blocks of every kind, and a segment in hundreds of parts."""
+    torch, sr = mods()
+    rng = np.random.default_rng(5)
+    lens = rng.multinomial(9000, [0.5, 0.3, 0.1, 0.05, 0.05])
+    off = np.concatenate([[0], np.cumsum(lens)]).astype(np.int64)
+    do = torch.from_numpy(off).cuda()
+    g = torch.Generator(device="cuda")
+    g.manual_seed(6)
+    k, n = 584, 1288
+    x, w, dy = normal(g, (9000, k), dtype), normal(g, (5, k, n), dtype, k ** -0.5), normal(g, (9000, n), dtype)
+    y, a = ref_forward(x, w, off, False)
+    check(sr.seg_matmul(x, w, do), y, a, k, dtype)
+    y, a = ref_forward(dy, w, off, True)
+    check(sr.seg_matmul(dy, w, do, transpose_w=True), y, a, n, (dtype, "dx"))
+    y, a = ref_grad(x, dy, off)
+    check(sr.seg_matmul_grad_w(x, dy, do, out_dtype=torch.float32), y, a, int(max(lens)), (dtype, "dw"))
+    long_x, long_dy = normal(g, (400000, 40), dtype), normal(g, (400000, 72), dtype)
+    loff = np.array([0, 3, 399000, 400000])
+    y, a = ref_grad(long_x, long_dy, loff)
+    got = sr.seg_matmul_grad_w(long_x, long_dy, torch.from_numpy(loff).cuda(), out_dtype=torch.float32)
+    check(got, y, a, 398997, (dtype, "long"))
+    assert sr.device_status() == 0
+
+
+def test_products_in_a_graph():
+    """Captured and replayed, the calls give what they give outside."""
+    torch, sr = mods()
+    off, rows, do, g = case("skewed", 15)
+    x, w = normal(g, (rows, 512), "bfloat16"), normal(g, (len(off) - 1, 512, 136), "bfloat16", 0.05)
+    dy = normal(g, (rows, 136), "bfloat16")
+    shared = normal(g, (136, 512), "bfloat16", 0.05)
+    a, b = normal(g, (3, 16, 512), "bfloat16", 0.05), normal(g, (3, 136, 16), "bfloat16")
+    adapter = torch.tensor([0, 1, 2, -1, 0], dtype=torch.int32, device="cuda")
+    one = torch.arange(6, device="cuda")
+    calls = [lambda: sr.seg_matmul(x, w, do), lambda: sr.seg_matmul_grad_w(x, dy, do), lambda: sr.seg_lora(x, shared, a, b, do, adapter),
+             lambda: sr.seg_lora(x[:5], shared, a, b, one, adapter)]
+    want = [c() for c in calls]
+    torch.cuda.synchronize()
+    stream = torch.cuda.Stream()        # whose scratch is first needed while it captures
+    with torch.cuda.stream(stream):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            got = [c() for c in calls]
+        for rep in range(3):
+            for v in got:
+                v.zero_()
+            graph.replay()
+            stream.synchronize()
+            assert all(torch.equal(u, v) for u, v in zip(want, got)), rep
+            for c, u in zip(calls, want):       # calls of the stream between the replays
+                assert torch.equal(c(), u)
+            if rep == 0:                        # and one that needs far more scratch
+                big, many = normal(g, (200000, 128), "bfloat16"), normal(g, (200000, 136), "bfloat16")
+                sr.seg_matmul_grad_w(big, many, torch.tensor([0, 200000], device="cuda"))
+    assert sr.device_status() == 0
+
+
+def test_example_layer():
+    torch, sr = mods()
+    from examples import expert_layer as ex
+    losses = ex.train(tokens=513, width=128, hidden=136, experts=7, steps=4)
+    assert losses[-1] < losses[0] and all(np.isfinite(losses))
+    assert losses == ex.train(tokens=513, width=128, hidden=136, experts=7, steps=4)     # every sum has a fixed order
+    prompts, tokens, offsets = ex.serve()
+    same = prompts[offsets[1:] - 1].double()
+    # the same sums in another order, then rounded to bfloat16
+    assert bool(((same - tokens.double()).abs() <= 2.0 ** -8 * same.abs() + 1e-3).all())
