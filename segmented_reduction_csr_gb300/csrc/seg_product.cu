@@ -917,10 +917,6 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                     const int valid = MODE == PRODUCT_WEIGHTS ? t.rows - kb * KB : KB;
                     if (!keep) split_rows(a_rows, valid, sa, R::A_PLANE);
                     split_rows(b_rows, valid, sb, R::B_PLANE);
-                } else if (MODE == PRODUCT_WEIGHTS) {
-                    const int64_t r = t.row0 + kb * KB, re = t.row0 + t.rows;
-                    load_any<PL>(Operand{p.w, p.ldw, r, re, t.m0, a.cols_m, a_rows, true, used}, sa, R::A_PLANE);
-                    load_any<PL>(Operand{p.x, p.ldx, r, re, t.n0, a.cols_n, b_rows, true, used}, sb, R::B_PLANE);
                 } else {
                     const void* w = static_cast<const unsigned char*>(p.w) + m * p.stride_w * (PL == 1 ? 2 : 4);
                     const int64_t k = int64_t(kb) * KB;
@@ -1131,8 +1127,8 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
             }
         }
         // the adapters' kernel starts beside the one that computes u, and
-        // copies and multiplies meanwhile; u and the scratch are used from here on
-        if (MODE == PRODUCT_ADAPTERS) grid_wait();
+        // copies and multiplies meanwhile
+        bool u_there = MODE != PRODUCT_ADAPTERS;
         uint32_t buf = 0, bph = 0;
         Item t;
         for (uint32_t i = first; i < items; i += stride) {
@@ -1156,6 +1152,17 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                         runs += bar_drain_count(starts);
                     }
                     scattered = runs * LOW_RUN > t.rows;
+                }
+                if (!u_there) {
+                    // u and the scratch are used from here on; b is asked for before
+                    if (scattered && p.u && lane < lanes)
+                        for (int c = group * W + t.part * ROWS; c < t.rows; c += ROWS * t.parts)
+                            for (int j = 0; j < W && c + j < t.rows; ++j) {
+                                const int l = tile_adapter[c + j];
+                                if (l >= 0) prefetch_l2(static_cast<const unsigned char*>(p.b) + ((l * p.N + m + lane) * p.rank) * (PL == 1 ? 2 : 4));
+                            }
+                    grid_wait();
+                    u_there = true;
                 }
             }
             float factor = 1.0f;
@@ -1322,6 +1329,39 @@ __global__ void __launch_bounds__(256) add_parts_kernel(const __grid_constant__ 
 int64_t ceil_to(int64_t n, int64_t d) { return (n + d - 1) / d; }
 
 // ---------------------------------------------------------------------------
+// Rows of any alignment to rows of whole 16-byte units: `lanes` threads a
+// row, each 16 bytes of it at a time.  What a tile's loader warps did with such
+// rows was bound by the loads in flight that the L1 beside 200 KB of stages
+// tracks, for every tile again.
+
+struct PackArgs {
+    const void* src;
+    unsigned char* dst;
+    int64_t ld, stride, rows, total, cols, row_bytes;   // elements; rows of a matrix and of all; bytes of a packed row
+    int lanes;
+};
+
+template <class T>
+__global__ void __launch_bounds__(256) pack_kernel(const __grid_constant__ PackArgs a) {
+    constexpr int V = 16 / sizeof(T);
+    const int lane = threadIdx.x % a.lanes;
+    const int64_t step = int64_t(gridDim.x) * 256 / a.lanes;
+    for (int64_t r = (int64_t(blockIdx.x) * 256 + threadIdx.x) / a.lanes; r < a.total; r += step) {
+        const int64_t mat = a.total == a.rows ? 0 : r / a.rows;
+        const T* src = static_cast<const T*>(a.src) + mat * a.stride + (r - mat * a.rows) * a.ld;
+        for (int64_t c = int64_t(lane) * V; c < a.cols; c += a.lanes * V) {
+            union {
+                T v[V];
+                uint4 u;
+            } x;
+#pragma unroll
+            for (int i = 0; i < V; ++i) x.v[i] = c + i < a.cols ? __ldg(src + c + i) : T(0);
+            *reinterpret_cast<uint4*>(a.dst + r * a.row_bytes + c * static_cast<int64_t>(sizeof(T))) = x.u;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
 // u[r, j] = scale * sum_k x[r, k] a[l, j, k] where requests have a row or a
 // few: a warp per dot product, so that a's bytes (rank x K per request, bound
 // by latency and L2) are spread over the whole GPU; a 128-lane tile per
@@ -1451,7 +1491,8 @@ cudaError_t launch_shape(const KernelArgs& a, const ProductPlan& plan, cudaStrea
         attr[attrs].val.clusterDim.y = attr[attrs].val.clusterDim.z = 1;
         ++attrs;
     }
-    const bool overlap = MODE == PRODUCT_ADAPTERS && a.p.overlap;
+    // (not after a packing kernel: the producers read what it writes without waiting)
+    const bool overlap = MODE == PRODUCT_ADAPTERS && a.p.overlap && !plan.pack_x && !plan.pack_w;
     if (overlap) {
         attr[attrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[attrs].val.programmaticStreamSerializationAllowed = 1;
@@ -1492,10 +1533,9 @@ template <int MODE>
 cudaError_t launch_mode(const KernelArgs& a, const ProductPlan& plan, cudaStream_t stream) {
     if (a.p.type == PT_F32 && plan.tensor)
         return plan.narrow ? launch_shape<MODE, true, 64, 3, 1>(a, plan, stream) : launch_shape<MODE, true, 128, 3, 1>(a, plan, stream);
-    if (a.p.type == PT_F32)
-        return plan.narrow ? launch_shape<MODE, false, 64, 3, 1>(a, plan, stream) : launch_shape<MODE, false, 128, 3, 1>(a, plan, stream);
-    if (!plan.tensor)
-        return plan.narrow ? launch_shape<MODE, false, 64, 1, 1>(a, plan, stream) : launch_shape<MODE, false, 256, 1, 1>(a, plan, stream);
+    if constexpr (MODE != PRODUCT_WEIGHTS) {
+        if (!plan.tensor) return a.p.type == PT_F32 ? launch_shape<MODE, false, 64, 3, 1>(a, plan, stream) : launch_shape<MODE, false, 64, 1, 1>(a, plan, stream);
+    }
     if (plan.narrow) return launch_shape<MODE, true, 64, 1, 1>(a, plan, stream);
     return plan.pair ? launch_shape<MODE, true, 256, 1, 2>(a, plan, stream) : launch_shape<MODE, true, 256, 1, 1>(a, plan, stream);
 }
@@ -1504,13 +1544,39 @@ int tile_columns(const ProductParams& p, bool narrow) { return narrow ? 64 : (p.
 
 }  // namespace
 
+namespace {
+
+// The second operand as matrices of contiguous rows.
+struct MatShape {
+    int64_t mats, rows, cols;
+};
+MatShape w_shape(int mode, const ProductParams& p) {
+    if (mode == PRODUCT_WEIGHTS) return {1, p.R, p.N};
+    if (mode == PRODUCT_ADAPTERS) return {1, p.N, p.K};
+    return {p.index ? p.L : p.S, p.trans ? p.N : p.K, p.trans ? p.K : p.N};
+}
+
+int64_t packed_row(int64_t cols, int type) { return ceil_to(cols * (type == PT_F32 ? 4 : 2), 16) * 16; }   // bytes
+
+}  // namespace
+
 ProductPlan plan_product(int mode, const ProductParams& p) {
     ProductPlan d{};
     const bool weights = mode == PRODUCT_WEIGHTS;
     const int64_t mats = mode == PRODUCT_FORWARD ? (p.index ? p.L : p.S) : 1;
-    d.tensor = p.K > 0 && p.R > 0 && mats > 0 && tensor_copyable(p.x, p.ldx, p.type) && tensor_copyable(p.w, p.ldw, p.type) &&
-               (mats == 1 || tensor_copyable(p.w, p.stride_w, p.type));
+    d.empty = p.K == 0 || p.R == 0 || mats == 0;
+    const bool copy_x = tensor_copyable(p.x, p.ldx, p.type);
+    const bool copy_w = tensor_copyable(p.w, p.ldw, p.type) && (mats == 1 || tensor_copyable(p.w, p.stride_w, p.type));
     const int64_t segments = mode == PRODUCT_ADAPTERS ? 1 : p.S;
+    // An operand that tensor copies cannot take is laid out again first (one
+    // more pass over it), except for a few rows per segment, where that pass
+    // would read matrices that no row needs: the loader warps take it as it is.
+    // 8,192 rows in 8 segments, 1,023 x 1,021 bfloat16: see pack_kernel.
+    if (!d.empty && !(copy_x && copy_w) && (weights || p.R > 64 * segments)) {
+        d.pack_x = !copy_x;
+        d.pack_w = !copy_w;
+    }
+    d.tensor = !d.empty && (copy_x || d.pack_x) && (copy_w || d.pack_w);
     // few rows per segment, or too few tiles to go round: small tiles and a
     // deeper ring; weights: few columns of x
     d.narrow = weights ? p.K <= 64 : p.R <= 64 * segments || (p.N <= MT && p.R <= 128 * p.sms);
@@ -1552,11 +1618,35 @@ ProductPlan plan_product(int mode, const ProductParams& p) {
     d.grid = static_cast<int32_t>(std::max<int64_t>(cg, std::min<int64_t>(items * cg, p.sms / cg * cg)));
     d.ticket_bytes = PRODUCT_TICKETS * 8;
     d.prefix_bytes = mode != PRODUCT_ADAPTERS && p.S > NEAR_SEGMENTS ? ceil_to((p.S + 1) * 8, 256) * 256 : 0;
-    d.partial_bytes = slots * cg * NT * MT * 4;
+    d.partial_bytes = ceil_to(slots * cg * NT * MT * 4, 256) * 256;
+    if (d.pack_x) d.pack_x_bytes = ceil_to(packed_row(p.K, p.type) * p.R, 256) * 256;
+    if (d.pack_w) d.pack_w_bytes = packed_row(w_shape(mode, p).cols, p.type) * w_shape(mode, p).rows * w_shape(mode, p).mats;
     return d;
 }
 
 bool lora_by_rows(const ProductParams& p) { return p.R <= 4 * p.S && p.S <= 4096; }
+
+namespace {
+
+cudaError_t launch_pack(const void* src, int64_t ld, int64_t stride, const MatShape& m, int size, void* dst, int sms, cudaStream_t stream) {
+    PackArgs a{};
+    a.src = src;
+    a.dst = static_cast<unsigned char*>(dst);
+    a.ld = ld;
+    a.stride = stride;
+    a.rows = m.rows;
+    a.total = m.rows * m.mats;
+    a.cols = m.cols;
+    a.row_bytes = packed_row(m.cols, size == 4 ? PT_F32 : PT_F16);
+    a.lanes = 4;
+    while (a.lanes < 32 && a.lanes * 16 < a.row_bytes) a.lanes *= 2;
+    const int64_t blocks = std::min<int64_t>(ceil_to(a.total * a.lanes, 256), int64_t(sms) * 16);
+    if (size == 4) pack_kernel<uint32_t><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(a);
+    else pack_kernel<uint16_t><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace
 
 cudaError_t launch_lora_rows(const ProductParams& p, cudaStream_t stream) {
     const dim3 grid(static_cast<unsigned>(p.R), static_cast<unsigned>(ceil_to(p.N, DOT_RANKS)));
@@ -1566,7 +1656,31 @@ cudaError_t launch_lora_rows(const ProductParams& p, cudaStream_t stream) {
     return cudaGetLastError();
 }
 
-cudaError_t launch_product(int mode, const ProductParams& p, const ProductPlan& plan, cudaStream_t stream) {
+cudaError_t launch_product(int mode, const ProductParams& given, const ProductPlan& plan, cudaStream_t stream) {
+    ProductParams p = given;
+    if (plan.empty) {
+        // nothing to sum: zeros
+        const size_t size = p.out_type == PT_F32 ? 4 : 2;
+        if (mode == PRODUCT_WEIGHTS) return cudaMemsetAsync(p.out, 0, size * p.S * p.K * p.N, stream);
+        return cudaMemset2DAsync(p.out, size * p.ldo, 0, size * p.N, p.R, stream);
+    }
+    unsigned char* packed = p.ws + plan.ticket_bytes + plan.prefix_bytes + plan.partial_bytes;
+    const int size = p.type == PT_F32 ? 4 : 2;
+    if (plan.pack_x) {
+        const cudaError_t e = launch_pack(p.x, p.ldx, 0, {1, p.R, p.K}, size, packed, p.sms, stream);
+        if (e != cudaSuccess) return e;
+        p.x = packed;
+        p.ldx = packed_row(p.K, p.type) / size;
+        packed += plan.pack_x_bytes;
+    }
+    if (plan.pack_w) {
+        const MatShape m = w_shape(mode, p);
+        const cudaError_t e = launch_pack(p.w, p.ldw, p.stride_w, m, size, packed, p.sms, stream);
+        if (e != cudaSuccess) return e;
+        p.w = packed;
+        p.ldw = packed_row(m.cols, p.type) / size;
+        p.stride_w = m.rows * p.ldw;
+    }
     KernelArgs a{};
     a.p = p;
     a.mtiles = plan.mtiles;

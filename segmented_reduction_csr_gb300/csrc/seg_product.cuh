@@ -47,14 +47,16 @@ struct ProductPlan {
     int32_t tensor;         // 1: operands come by tensor copies, 0: by the loader warps
     int32_t narrow;         // 1: at most 64 rows per tile and a deeper ring
     int32_t pair;           // 1: two CTAs share a tile
+    int32_t empty;          // 1: no sum has a term
+    int32_t pack_x, pack_w; // 1: the operand is first laid out in 16-byte aligned rows
     int32_t mtiles, ntiles; // tiles of the output's contiguous / other dimension (forward: rows vary by segment)
     int32_t parts;          // forward: parts of the contraction
     int32_t part_blocks;    // forward: 64-wide blocks per part
     int64_t chunk;          // weights: rows per part of a segment
     int32_t add_blocks;     // weights: blocks of the kernel that adds the parts (0: no segment can be split)
     int64_t row_tiles;      // forward: most row tiles there can be
-    int64_t ticket_bytes, prefix_bytes, partial_bytes;   // the workspace, in this order
-    int64_t bytes() const { return ticket_bytes + prefix_bytes + partial_bytes; }
+    int64_t ticket_bytes, prefix_bytes, partial_bytes, pack_x_bytes, pack_w_bytes;   // the workspace, in this order
+    int64_t bytes() const { return ticket_bytes + prefix_bytes + partial_bytes + pack_x_bytes + pack_w_bytes; }
 };
 
 // Ticket words sit at the start of the products' scratch, whatever the call:
