@@ -115,9 +115,8 @@ seg_status_t scratch_for(int dev, cudaStream_t stream, size_t bytes, Scratch** o
     return scratch_in(g_scratch, dev, stream, bytes, out);
 }
 
-// Scratch of the products: ordinary device memory, zeroed ticket words, made
-// outside of any capture of `stream` (a buffer that a capture allocates
-// belongs to its graph).
+// Scratch of the products: ordinary device memory, allocated outside of any
+// capture of `stream` (a buffer that a capture allocates belongs to its graph).
 seg_status_t product_scratch(int dev, cudaStream_t stream, size_t bytes, Scratch** out) {
     Scratch& sc = g_product_scratch[std::make_pair(dev, stream)];
     if (sc.bytes < bytes) {
@@ -125,18 +124,11 @@ seg_status_t product_scratch(int dev, cudaStream_t stream, size_t bytes, Scratch
         cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
         if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) return SEG_ERR_CUDA;
         void* ptr = nullptr;
-        cudaStream_t own = nullptr;
-        cudaError_t e = cudaMalloc(&ptr, want);
-        const bool full = e != cudaSuccess;
-        if (!full) e = cudaStreamCreateWithFlags(&own, cudaStreamNonBlocking);
-        if (e == cudaSuccess) e = cudaMemsetAsync(ptr, 0, PRODUCT_TICKETS * 8, own);
-        if (e == cudaSuccess) e = cudaStreamSynchronize(own);
-        if (own) cudaStreamDestroy(own);
+        const cudaError_t e = cudaMalloc(&ptr, want);
         cudaThreadExchangeStreamCaptureMode(&mode);
         if (e != cudaSuccess) {
             cudaGetLastError();
-            if (ptr) cudaFree(ptr);
-            return full ? SEG_ERR_OUT_OF_MEMORY : SEG_ERR_CUDA;
+            return SEG_ERR_OUT_OF_MEMORY;
         }
         sc.ptr = ptr;
         sc.bytes = want;
@@ -269,14 +261,11 @@ seg_status_t check_product(seg_dtype_t dtype, int64_t num_rows, int64_t K, int64
     return SEG_OK;
 }
 
-// Enqueues one product on scratch that is large enough.  The ticket words at the scratch's start are
-// written by products alone, each with a new generation.
+// Enqueues one product on scratch that is large enough.
 seg_status_t run_product(int mode, ProductParams p, cudaStream_t stream, Scratch* sc, DeviceState* ds) {
     p.sms = ds->sm_count;
     p.status = ds->status;
     p.ws = static_cast<unsigned char*>(sc->ptr);
-    // (after 2^32 calls the tag starts over: the counts are back at zero after every call)
-    p.gen = ++sc->gen;
     const ProductPlan plan = plan_product(mode, p);
     if (plan.too_many) return SEG_ERR_UNSUPPORTED;
     if (launch_product(mode, p, plan, stream) != cudaSuccess) {

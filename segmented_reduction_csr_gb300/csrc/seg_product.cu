@@ -25,10 +25,10 @@
 // part products have an accumulator of their own, and where the result is
 // float32 the accumulators are added to it, rounded, every 512 (float32) or
 // 768 (16-bit operands) steps: the bias then stays below 1e-6.
-// Long sums with few tiles are cut into parts that leave float32 partials in
-// scratch, added in order.  Forward: each part takes a ticket and the last
-// one to finish adds them (no CTA waits for another); weights, whose segments
-// can have hundreds of parts: a second kernel adds them.
+// Long sums with few tiles are cut into parts, added in order.  Forward: the
+// parts of a tile are a cluster and add through its shared memory.  Weights,
+// whose segments can have hundreds of parts: float32 partials in scratch, and
+// a second kernel adds them.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -85,7 +85,6 @@ struct KernelArgs {
     int32_t wide_rows;  // 16-bit results: 16-byte stores fit
     int32_t flush;      // blocks of the sum after which the accumulators go to the result
     int64_t chunk, row_tiles, cols_m, cols_n;   // cols_*: extent of the tile dimensions (forward: cols_n unused)
-    unsigned long long* tickets;
     int* far;          // offsets and tile prefix of more than NEAR_SEGMENTS segments
     float* partials;
 };
@@ -152,7 +151,7 @@ struct Item {
     int m0, n0;
     int kb0, kb1;       // 64-wide blocks of the sum
     int part, parts;
-    int64_t slot, ticket;
+    int64_t slot;
 };
 
 // Item i; `t` holds the item before it (seg 0 at the start): a CTA's items
@@ -207,7 +206,6 @@ __device__ __forceinline__ void item_at(const KernelArgs& a, const int* beg, con
         // one of them a first part: so these numbers are each used once
         const int per = a.mtiles * a.ntiles, r = t.m0 / (MT * CG) + t.n0 / NT * a.mtiles;
         t.slot = (2 * (t.row0 / a.chunk) + (j == 0 ? 1 : 0)) * per + r;
-        t.ticket = 0;
     } else {
         // the segment's rows in equal tiles of a multiple of 16
         if (t.each_of != t.seg) {
@@ -221,8 +219,7 @@ __device__ __forceinline__ void item_at(const KernelArgs& a, const int* beg, con
         t.kb0 = t.part * a.part_blocks;
         t.kb1 = min(t.kb0 + a.part_blocks, a.kblocks);
         t.parts = a.parts;
-        t.slot = i;
-        t.ticket = a.parts > 1 ? i / a.parts : 0;
+        t.slot = 0;
     }
 }
 
@@ -747,15 +744,20 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
     uint64_t* low_full = drain + 1;                // CG == 2: CTA 0's count
     uint64_t* low_empty = low_full + 1;
     uint32_t* tmem_at = reinterpret_cast<uint32_t*>(low_empty + 1);
-    int* last_part = reinterpret_cast<int*>(tmem_at + 1);
-    int* low_steps = last_part + 1;                // steps of 16 in the low-rank stage; + 8: the tile's last
+    int* low_steps = reinterpret_cast<int*>(tmem_at + 1);                // steps of 16 in the low-rank stage; + 8: the tile's last
     uint32_t* low_turns = reinterpret_cast<uint32_t*>(low_steps + 1);          // [8]: rows with another adapter than the one before
     int* tile_adapter = reinterpret_cast<int*>(tmem_at + 32);    // [NT], the drain warps'
     int* low_adapter = tile_adapter + NT;                        // [NT], the low-rank warps'
     if (PL > 1) staging = reinterpret_cast<unsigned char*>(near);
+    // a part of a split tile's sum [columns][128 lanes], where the stages were once its MMAs are done
+    float* cluster_part = reinterpret_cast<float*>(stages);
+    static_assert(R::STAGES * R::STAGE >= NT * MT * 4, "room for a part");
     const ProductParams& p = a.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int rank = CG == 2 ? static_cast<int>(cluster_rank()) : 0;
+    const bool split = a.parts > 1;                // the parts of a tile are a cluster
+    const uint32_t in_cluster = CG == 2 || split ? cluster_rank() : 0;
+    const int rank = CG == 2 ? static_cast<int>(in_cluster & 1) : 0;
+    const uint32_t lead = in_cluster & ~1u;
     const uint32_t first = blockIdx.x / CG, stride = gridDim.x / CG;
 
     const bool is_near = p.S <= NEAR_SEGMENTS;
@@ -791,7 +793,7 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
         }
     tc_fence_before();
     __syncthreads();
-    if (CG == 2) cluster_sync();
+    if (CG == 2 || split) cluster_sync();
     tc_fence_after();
     const uint32_t tmem = *tmem_at;
 
@@ -848,7 +850,7 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                     unsigned char* sa = stages + st * R::STAGE;
                     unsigned char* sb = sa + PL * R::A_PLANE;
                     const bool tail = has_tail(t, kb);
-                    const uint32_t bar = tail || PL > 1 ? smem_u32(landed + st) : lead_addr<CG>(full + st);
+                    const uint32_t bar = tail || PL > 1 ? smem_u32(landed + st) : lead_addr<CG>(full + st, lead);
                     const bool keep = keeps.a(t, kb);
                     if (tail || PL > 1) {
                         mbar_arrive_expect_tx(landed + st, (keep ? 0 : a_bytes) + b_bytes);
@@ -930,7 +932,7 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) lead_arrive<CG>(full + st, true);
+                if (lane == 0) lead_arrive<CG>(full + st, lead, true);
                 if (++st == R::STAGES) {
                     st = 0;
                     ph ^= 1;
@@ -960,7 +962,7 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) lead_arrive<CG>(full + st, true);
+                if (lane == 0) lead_arrive<CG>(full + st, lead, true);
             }
             if (++st == R::STAGES) st = 0;
         }
@@ -1023,7 +1025,7 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                         if (tl == 0) *low_steps = (mine ? min(4, total - s0) : 0) | (last ? 8 : 0);
                         fence_proxy_async_smem();
                         __syncwarp();
-                        if (lane == 0) lead_arrive<CG>(low_full, true);
+                        if (lane == 0) lead_arrive<CG>(low_full, lead, true);
                     }
                     row = end;
                 } while (ok && !last);
@@ -1074,7 +1076,7 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                                                db + pb[q] * (R::B_PLANE >> 4) + k * b_step, idesc, add || q > 1);
                             }
                         }
-                        tc_commit<CG>(empty + st);
+                        tc_commit<CG>(empty + st, lead);
                         if (R::LOW && low_left && ((kb - t.kb0) % LOW_EVERY == LOW_EVERY - 1 || kb + 1 == t.kb1)) {
                             // the low-rank part's blocks, from a stage of their own, in
                             // between (a fixed order), so that they are laid out meanwhile;
@@ -1090,11 +1092,11 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                                 const int steps = *reinterpret_cast<volatile int*>(low_steps);
                                 low_left = (steps & 8) == 0;
                                 for (int k = 0; k < (steps & 7); ++k) tc_mma<CG>(acc, la + 2 * k, lb + 2 * k, low_idesc, true);
-                                tc_commit<CG>(low_empty);
+                                tc_commit<CG>(low_empty, lead);
                             } while (low_left && kb + 1 == t.kb1);
                             if (!ok) break;
                         }
-                        if (kb + 1 == piece_end) tc_commit<CG>(acc_full + buf);
+                        if (kb + 1 == piece_end) tc_commit<CG>(acc_full + buf, lead);
                         if (++st == R::STAGES) {
                             st = 0;
                             ph ^= 1;
@@ -1104,7 +1106,7 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                 }
             }
             // no MMA is in flight when the memory goes away
-            tc_commit<CG>(drain, false);
+            tc_commit<CG>(drain, lead, true);
             wait_for<CG>(drain, 0, p.status);
         }
         __syncwarp();
@@ -1113,8 +1115,8 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
         const int quarter = (warp - EPI_WARP) & 3, group = (warp - EPI_WARP) / 4;   // which lanes; which columns
         const int td = tid - EPI_WARP * 32;
         constexpr int W = MODE == PRODUCT_ADAPTERS ? 8 : (TENSOR && PL == 1 ? 32 : 16), ROWS = W * (EPW / 4);    // columns at a time; of all warps
-        staging += (warp - EPI_WARP) * R::STAGING;
-        LowRank<PL, R::LOW> low(p, tile_adapter, staging, lane);
+        unsigned char* const own_staging = staging + (warp - EPI_WARP) * R::STAGING;
+        LowRank<PL, R::LOW> low(p, tile_adapter, own_staging, lane);
         if (MODE == PRODUCT_FORWARD && !p.index) {
             // rows in no segment
             const int b = p.S > 0 ? beg[0] : 0, e = p.S > 0 ? beg[p.S] : 0;
@@ -1171,23 +1173,22 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
             const bool partial = t.parts > 1;
             const int64_t step = MODE == PRODUCT_WEIGHTS ? a.cols_m : p.ldo;
             const int64_t at = (MODE == PRODUCT_WEIGHTS ? (t.seg * a.cols_n + t.n0) * a.cols_m : t.row0 * p.ldo) + m;
-            bool ok = true, adding = false;      // adding: the last of a tile's parts adds them all
+            bool ok = true;
             int piece = t.kb0;
             do {
                 const bool fresh = piece == t.kb0, final = t.kb1 - piece <= a.flush;
-                const bool to_part = partial && !adding;
                 const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * R::ACC;
-                bool waiting = summed && !adding;
+                bool waiting = summed;
                 int c = group * W;
                 if constexpr (MODE == PRODUCT_ADAPTERS)
-                    if (final && !adding && scattered) low.begin(t.row0, t.rows, m + lane, c + t.part * ROWS);
+                    if (final && scattered) low.begin(t.row0, t.rows, m + lane, c + t.part * ROWS);
                 for (;;) {
                     float v[W];
 #pragma unroll
                     for (int j = 0; j < W; ++j) v[j] = 0.0f;
                     // the parts of a tile share its low-rank part
                     if constexpr (MODE == PRODUCT_ADAPTERS)
-                        if (final && !adding && scattered && c < n_left && c / ROWS % t.parts == t.part) low.rows_of(v, c, c + ROWS * t.parts);
+                        if (final && scattered && c < n_left && c / ROWS % t.parts == t.part) low.rows_of(v, c, c + ROWS * t.parts);
                     if (waiting) {
                         ok = bar_drain_all(wait_for<CG>(acc_full + buf, bph, p.status));
                         if (!ok) break;
@@ -1196,24 +1197,7 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                     }
                     if (c >= n_left) break;
                     const int n = n_left - c < W ? n_left - c : W;
-                    if (adding) {
-                        const float* part = a.partials + slot + (int64_t(-t.part) * CG * NT + c) * MT + lane;
-#pragma unroll
-                        for (int j0 = 0; j0 < W; j0 += 8) {
-                            if (j0 >= n) break;
-                            float d[8];
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) d[j] = 0.0f;
-#pragma unroll 4
-                            for (int q = 0; q < t.parts; ++q) {
-#pragma unroll
-                                for (int j = 0; j < 8; ++j)
-                                    if (j0 + j < n) d[j] += __ldcg(part + (int64_t(q) * CG * NT + j0 + j) * MT);
-                            }
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) v[j0 + j] += d[j];
-                        }
-                    } else if (summed) {
+                    if (summed) {
                         float d[W], lo[W];
                         tmem_load(from + c, d);
                         if constexpr (PL > 1) tmem_load(from + NT + c, lo);
@@ -1221,61 +1205,73 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                         if constexpr (PL > 1) tmem_wait(lo);
 #pragma unroll
                         for (int j = 0; j < W; ++j) v[j] += PL > 1 ? d[j] + lo[j] : d[j];
-                        if (!fresh && (to_part || lane < lanes)) {
+                        if (!fresh && (partial || lane < lanes)) {
                             // the sum so far, float32 wherever there is more than one piece
-                            const float* so_far = to_part ? a.partials + slot + int64_t(c) * MT : static_cast<const float*>(p.out) + at + c * step;
-                            const int64_t s1 = to_part ? MT : step;
+                            const float* so_far = partial ? a.partials + slot + int64_t(c) * MT : static_cast<const float*>(p.out) + at + c * step;
+                            const int64_t s1 = partial ? MT : step;
 #pragma unroll
                             for (int j = 0; j < W; ++j)
                                 if (j < n) v[j] += so_far[j * s1 + lane];
                         }
                     }
-                    if (to_part) {
-                        store_rows(a.partials + slot + int64_t(c) * MT + lane, MT, v, n, [](float x) { return x; });
+                    if (partial) {
+                        store_rows((MODE == PRODUCT_WEIGHTS ? a.partials + slot : cluster_part + quarter * 32) + int64_t(c) * MT + lane, MT, v, n,
+                                   [](float x) { return x; });
                     } else {
                         if (MODE == PRODUCT_FORWARD && p.scale && final)
 #pragma unroll
                             for (int j = 0; j < W; ++j) v[j] *= factor;
-                        store_result(a, at + c * step, step, v, n, lanes, lane, staging);
+                        store_result(a, at + c * step, step, v, n, lanes, lane, own_staging);
                     }
                     c += ROWS;
                     if (c >= n_left) break;
                 }
                 if (!ok) break;
-                if (summed && !adding) {
+                if (summed) {
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) lead_arrive<CG>(acc_empty + buf, false);
+                    if (lane == 0) lead_arrive<CG>(acc_empty + buf, lead, false);
                     if ((buf ^= 1) == 0) bph ^= 1;
                 }
                 piece = final ? t.kb1 : piece + a.flush;
-                if (MODE != PRODUCT_WEIGHTS && to_part && final) {
-                    bar_drain();     // the release below covers what the others wrote before it
-                    if (td == 0) {
-                        unsigned long long* ticket = a.tickets + t.ticket * CG + rank;
-                        red_max_relaxed_gpu(ticket, static_cast<unsigned long long>(p.gen) << 32);
-                        const unsigned long long old = atom_add_release_gpu(ticket, 1);
-                        fence_acq_rel_gpu();
-                        const bool last = static_cast<uint32_t>(old) + 1 == static_cast<uint32_t>(t.parts);
-                        // the count starts at zero again: a replayed graph comes with the same generation
-                        if (last) atomicExch(ticket, old >> 32 << 32);
-                        *last_part = last;
-                    }
-                    bar_drain();
-                    adding = *last_part;
-                    if (adding) {
-                        piece = t.kb1 - 1;      // once more around, as the final piece
-                    }
-                } else {
-                    adding = false;
-                }
             } while (piece < t.kb1);
             if (!ok) break;
         }
         tc_fence_before();
     }
     __syncthreads();
-    if (CG == 2) cluster_sync();      // the other CTA's MMAs and copies use this one's memory
+    if (MODE != PRODUCT_WEIGHTS && split) {
+        // The parts of a tile (a CTA, or a pair, has one) lie in the shared
+        // memory of the cluster's CTAs; each CTA adds some of the rows, always
+        // in the order of the parts.
+        cluster_sync();
+        if (first < items && warp >= EPI_WARP && warp < EPI_WARP + EPW) {
+            constexpr int W = 8;
+            const int quarter = (warp - EPI_WARP) & 3, group = (warp - EPI_WARP) / 4;
+            Item t;
+            item_at<MODE, NT, CG>(a, beg, pre, first, t);
+            const int64_t m = t.m0 + rank * MT + quarter * 32;
+            const int lanes = static_cast<int>(a.cols_m - m < 32 ? a.cols_m - m : 32);
+            const float factor = MODE == PRODUCT_FORWARD && p.scale ? __ldg(p.scale + __ldg(p.index + t.seg)) : 1.0f;
+            for (int c = (t.part * (EPW / 4) + group) * W; c < t.rows; c += t.parts * (EPW / 4) * W) {
+                const int n = t.rows - c < W ? t.rows - c : W;
+                float v[W];
+#pragma unroll
+                for (int j = 0; j < W; ++j) v[j] = 0.0f;
+#pragma unroll 4
+                for (int q = 0; q < t.parts; ++q) {
+                    const uint32_t from = cluster_addr(cluster_part + c * MT + quarter * 32 + lane, q * CG + rank);
+#pragma unroll
+                    for (int j = 0; j < W; ++j)
+                        if (j < n) v[j] += cluster_load(from + j * MT * 4);
+                }
+#pragma unroll
+                for (int j = 0; j < W; ++j) v[j] *= factor;
+                store_result(a, (int64_t(t.row0) + c) * p.ldo + m, p.ldo, v, n, lanes, lane, staging + (warp - EPI_WARP) * R::STAGING);
+            }
+        }
+    }
+    if (CG == 2 || split) cluster_sync();      // the others' MMAs, copies and sums use this CTA's memory
     if (warp == 0) {
         tc_fence_after();
         tmem_free<CG>(tmem, 2 * R::ACC);
@@ -1485,9 +1481,9 @@ cudaError_t launch_shape(const KernelArgs& a, const ProductPlan& plan, cudaStrea
     constexpr int smem = R::SMEM;
     cudaLaunchAttribute attr[2];
     int attrs = 0;
-    if (CG > 1) {
+    if (CG > 1 || plan.parts > 1) {
         attr[attrs].id = cudaLaunchAttributeClusterDimension;
-        attr[attrs].val.clusterDim.x = CG;
+        attr[attrs].val.clusterDim.x = CG * plan.parts;
         attr[attrs].val.clusterDim.y = attr[attrs].val.clusterDim.z = 1;
         ++attrs;
     }
@@ -1511,14 +1507,17 @@ cudaError_t launch_shape(const KernelArgs& a, const ProductPlan& plan, cudaStrea
         if (e != cudaSuccess) return e;
         int clusters = a.p.sms;
         if (CG > 1) {
+            attr[0].val.clusterDim.x = CG;
             e = cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg);
+            attr[0].val.clusterDim.x = CG * plan.parts;
             if (e != cudaSuccess) return e;
             if (clusters < 1) return cudaErrorInvalidConfiguration;
         }
         resident[dev] = clusters * CG;
     }
     cfg.numAttrs = attrs;
-    cfg.gridDim = dim3(std::min(plan.grid, resident[dev]));
+    // (a part has a CTA or a pair of its own)
+    if (plan.parts == 1) cfg.gridDim = dim3(std::min(plan.grid, resident[dev]));
     e = cudaLaunchKernelEx(&cfg, kernel, a, ma, mb);
     if (e != cudaSuccess || plan.add_blocks == 0) return e;
     if constexpr (MODE == PRODUCT_WEIGHTS) {
@@ -1582,7 +1581,10 @@ ProductPlan plan_product(int mode, const ProductParams& p) {
     d.narrow = weights ? p.K <= 64 : p.R <= 64 * segments || (p.N <= MT && p.R <= 128 * p.sms);
     const int NT = tile_columns(p, d.narrow);
     // two CTAs on a tile of twice the lanes, unless that leaves one of them without lanes
+    // or so few tiles that their sums are split
     d.pair = d.tensor && p.type != PT_F32 && !d.narrow && (p.N > 1024 || ceil_to(p.N, MT) % 2 == 0);
+    d.row_tiles = mode == PRODUCT_ADAPTERS ? ceil_to(p.R, NT) : std::min(segments, p.R) + p.R / NT;
+    if (!weights && d.row_tiles * ceil_to(p.N, MT) * 2 <= p.sms * 27 / 32) d.pair = 0;
     const int cg = d.pair ? 2 : 1;
     d.mtiles = static_cast<int32_t>(ceil_to(p.N, MT * cg));
     d.ntiles = weights ? static_cast<int32_t>(ceil_to(p.K, NT)) : 1;
@@ -1604,19 +1606,20 @@ ProductPlan plan_product(int mode, const ProductParams& p) {
         }
         items = (segments + p.R / d.chunk) * per;
     } else {
-        d.row_tiles = mode == PRODUCT_ADAPTERS ? ceil_to(p.R, NT) : std::min(segments, p.R) + p.R / NT;
         items = d.row_tiles * d.mtiles;
-        if (items * cg * 2 <= p.sms && d.part_blocks >= 8) {
-            const int64_t parts = std::min<int64_t>(p.sms / (items * cg), d.part_blocks / 4);
+        // parts of a tile: a cluster of 4 CTAs at most (8: slower than none by
+        // half, one token's adapters 14.7 us against 9.0 with 4), which fit 27
+        // of 32 SMs.  float32 parts are short enough to need no flushing.
+        int64_t parts = 1;
+        while (parts < 4 && items * cg * parts * 2 <= p.sms * 27 / 32 && d.part_blocks / (parts * 2) >= 4) parts *= 2;
+        if (parts > 1 && (p.type != PT_F32 || ceil_to(d.part_blocks, parts) <= 16)) {
             d.part_blocks = static_cast<int32_t>(ceil_to(d.part_blocks, parts));
-            d.parts = static_cast<int32_t>(ceil_to(ceil_to(p.K, KB), d.part_blocks));
-            if (d.parts > 1) slots = items * d.parts;
-            items *= d.parts;
+            d.parts = static_cast<int32_t>(parts);
+            items *= parts;
         }
     }
     d.too_many = items > INT32_MAX;
     d.grid = static_cast<int32_t>(std::max<int64_t>(cg, std::min<int64_t>(items * cg, p.sms / cg * cg)));
-    d.ticket_bytes = PRODUCT_TICKETS * 8;
     d.prefix_bytes = mode != PRODUCT_ADAPTERS && p.S > NEAR_SEGMENTS ? ceil_to((p.S + 1) * 8, 256) * 256 : 0;
     d.partial_bytes = ceil_to(slots * cg * NT * MT * 4, 256) * 256;
     if (d.pack_x) d.pack_x_bytes = ceil_to(packed_row(p.K, p.type) * p.R, 256) * 256;
@@ -1664,7 +1667,7 @@ cudaError_t launch_product(int mode, const ProductParams& given, const ProductPl
         if (mode == PRODUCT_WEIGHTS) return cudaMemsetAsync(p.out, 0, size * p.S * p.K * p.N, stream);
         return cudaMemset2DAsync(p.out, size * p.ldo, 0, size * p.N, p.R, stream);
     }
-    unsigned char* packed = p.ws + plan.ticket_bytes + plan.prefix_bytes + plan.partial_bytes;
+    unsigned char* packed = p.ws + plan.prefix_bytes + plan.partial_bytes;
     const int size = p.type == PT_F32 ? 4 : 2;
     if (plan.pack_x) {
         const cudaError_t e = launch_pack(p.x, p.ldx, 0, {1, p.R, p.K}, size, packed, p.sms, stream);
@@ -1690,16 +1693,15 @@ cudaError_t launch_product(int mode, const ProductParams& given, const ProductPl
     a.kblocks = static_cast<int32_t>(ceil_to(p.K, KB));
     a.box_rows = plan.narrow && p.R <= 32 * (mode == PRODUCT_FORWARD ? p.S : 1) ? 16 : 64;
     a.a_rows = static_cast<int32_t>(std::min<int64_t>(MT, ceil_to(p.N, 16) * 16));
-    a.flush = p.type == PT_F32 ? 8 : (p.out_type == PT_F32 && !p.index ? 12 : NEVER_FLUSH);
+    a.flush = plan.parts > 1 ? NEVER_FLUSH : p.type == PT_F32 ? 8 : (p.out_type == PT_F32 && !p.index ? 12 : NEVER_FLUSH);
     const int64_t out_step = mode == PRODUCT_WEIGHTS ? p.N : p.ldo;
     a.wide_rows = p.N % 8 == 0 && out_step % 8 == 0 && reinterpret_cast<uintptr_t>(p.out) % 16 == 0;
     a.chunk = plan.chunk;
     a.row_tiles = plan.row_tiles;
     a.cols_m = p.N;
     a.cols_n = p.K;
-    a.tickets = reinterpret_cast<unsigned long long*>(p.ws);
-    a.far = reinterpret_cast<int*>(p.ws + plan.ticket_bytes);
-    a.partials = reinterpret_cast<float*>(p.ws + plan.ticket_bytes + plan.prefix_bytes);
+    a.far = reinterpret_cast<int*>(p.ws);
+    a.partials = reinterpret_cast<float*>(p.ws + plan.prefix_bytes);
     if (mode == PRODUCT_FORWARD) return launch_mode<PRODUCT_FORWARD>(a, plan, stream);
     if (mode == PRODUCT_WEIGHTS) return launch_mode<PRODUCT_WEIGHTS>(a, plan, stream);
     return launch_mode<PRODUCT_ADAPTERS>(a, plan, stream);

@@ -36,7 +36,6 @@ struct ProductParams {
     // library-owned
     unsigned char* ws;      // see ProductPlan
     unsigned int* status;   // device status word
-    uint32_t gen;           // call generation of the ticket words
     int32_t sms;
 };
 
@@ -55,13 +54,9 @@ struct ProductPlan {
     int64_t chunk;          // weights: rows per part of a segment
     int32_t add_blocks;     // weights: blocks of the kernel that adds the parts (0: no segment can be split)
     int64_t row_tiles;      // forward: most row tiles there can be
-    int64_t ticket_bytes, prefix_bytes, partial_bytes, pack_x_bytes, pack_w_bytes;   // the workspace, in this order
-    int64_t bytes() const { return ticket_bytes + prefix_bytes + partial_bytes + pack_x_bytes + pack_w_bytes; }
+    int64_t prefix_bytes, partial_bytes, pack_x_bytes, pack_w_bytes;   // the workspace, in this order
+    int64_t bytes() const { return prefix_bytes + partial_bytes + pack_x_bytes + pack_w_bytes; }
 };
-
-// Ticket words sit at the start of the products' scratch, whatever the call:
-// nothing else is ever written there.
-constexpr int64_t PRODUCT_TICKETS = 1024;
 
 enum : int { PRODUCT_FORWARD = 0, PRODUCT_WEIGHTS = 1, PRODUCT_ADAPTERS = 2 };
 

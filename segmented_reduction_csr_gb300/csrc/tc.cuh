@@ -21,15 +21,16 @@ __device__ __forceinline__ bool elect_one() {
     return r != 0;
 }
 
-// Pairs: with CG == 2 the two CTAs of a cluster work on one tile.  CTA 0
-// issues the MMAs for both; its barriers count both CTAs' operands.
+// Pairs: with CG == 2 two neighbouring CTAs of a cluster work on one tile.
+// The first (rank `lead` of the cluster) issues the MMAs for both; its
+// barriers count both CTAs' operands.
 
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
-// All threads of both CTAs; memory written before is visible after.
+// All threads of the cluster; memory written before is visible after.
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
@@ -53,19 +54,26 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t pa
     return ok != 0;
 }
 
+// A float32 of another CTA's shared memory (an address of cluster_addr).
+__device__ __forceinline__ float cluster_load(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
 template <int CG>
-__device__ __forceinline__ uint32_t lead_addr(const void* p) {
-    return CG == 2 ? cluster_addr(p, 0) : smem_u32(p);
+__device__ __forceinline__ uint32_t lead_addr(const void* p, uint32_t lead) {
+    return CG == 2 ? cluster_addr(p, lead) : smem_u32(p);
 }
 
 // One arrival at the first CTA's barrier, from either CTA.  `memory`: this
 // CTA's earlier writes have to be visible to the cluster first (a fence that
 // waits for them, so it is left out where tensor memory alone is handed over).
 template <int CG>
-__device__ __forceinline__ void lead_arrive(uint64_t* bar, bool memory) {
+__device__ __forceinline__ void lead_arrive(uint64_t* bar, uint32_t lead, bool memory) {
     if constexpr (CG == 2) {
-        if (memory) asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(lead_addr<CG>(bar)) : "memory");
-        else asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(lead_addr<CG>(bar)) : "memory");
+        if (memory) asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(lead_addr<CG>(bar, lead)) : "memory");
+        else asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(lead_addr<CG>(bar, lead)) : "memory");
     } else {
         asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
     }
@@ -132,14 +140,15 @@ __device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t columns) {
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-// Arrives on `bar` (CG == 2 and `both`: in both CTAs) when this thread's earlier tcgen05.mma have finished.
+// Arrives on `bar` (CG == 2: in both CTAs of the pair, or `alone` in this one)
+// when this thread's earlier tcgen05.mma have finished.
 template <int CG>
-__device__ __forceinline__ void tc_commit(uint64_t* bar, bool both = true) {
+__device__ __forceinline__ void tc_commit(uint64_t* bar, uint32_t lead, bool alone = false) {
     if constexpr (CG == 2) {
-        if (both)
+        if (!alone)
             asm volatile(
                 "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
-                "h"(static_cast<uint16_t>(3))
+                "h"(static_cast<uint16_t>(3u << lead))
                 : "memory");
         else
             asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
