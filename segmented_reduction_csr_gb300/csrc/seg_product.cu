@@ -1,25 +1,40 @@
 // seg_product.cu -- products over the rows of segments (see seg_product.cuh)
 // on the tensor cores (tcgen05, accumulators in tensor memory).
 //
-// One kernel shape serves all three products.  A tile is D[m, n] with m (128
-// lanes of tensor memory) along the output's contiguous dimension and n (its
-// columns, up to NT) along the other one:
+// One kernel serves all three products.  A tile is D[m, n] with m (128 lanes
+// of tensor memory, 256 for a pair of CTAs) along the output's contiguous
+// dimension and n (its columns, up to NT) along the other one:
 //   forward, adapters  m: output columns, n: rows of one segment, sum over K;
 //   weights            m: columns of dy,  n: columns of x,        sum over rows.
 // With the rows of a segment on n, whose extent an MMA takes in steps of 16,
 // a ragged tail or a single row costs 16 columns, not a whole 128-row tile;
 // and a warp's 32 lanes are 32 neighbouring output columns, so results leave
-// the registers coalesced whatever the alignment.
+// coalesced whatever the alignment.
 //
-// Roles per CTA (persistent, one CTA per SM, tiles dealt round robin):
-//   a producer fills a ring of shared-memory stages (64 steps of the sum
-//   each, 128-byte swizzled rows): one thread that issues tensor copies, or,
-//   for float32 and for strides that tensor copies cannot take, eight loader
-//   warps; one thread issues the MMAs; four warps drain one of two
-//   accumulators while the other fills.
-// float32: the loader splits every value into three bfloat16 parts by
-// truncation (8 + 8 + 8 bits, exact) and six of the nine part products are
-// accumulated; the other three are below 2^-21 of the whole.
+// Roles per CTA (persistent, one CTA per SM, tiles dealt round robin): two
+// elected threads copy operands (tensor copies) into a ring of shared-memory
+// stages, 64 steps of the sum each, rows of 128 bytes, swizzled; one thread
+// issues the MMAs; eight warps drain one of two accumulators while the other
+// fills.  Further warps where there is need: one that zeroes the rows of a
+// weights' sum past the segment's end; eight that split float32; four that lay
+// out the adapters' part.  Every wait has a time limit; a role that gives up
+// says so in the device status word and all leave.
+//
+// What bounds it (GB300, 6,680 GB/s and 1,937 TFLOP/s measured peaks):
+//   training shapes: the tensor cores' clock and power.  32,768 rows, 32
+//     segments, 2,048 x 4,096 bfloat16: forward 314 us = 1,750 TFLOP/s (a
+//     long-running library product reaches 1,749 here), weights 361 us;
+//   decode: reading the matrices.  128 rows over 64 matrices of 2,048 x 1,024:
+//     35 us = 6.6 TB/s of the matrices that are used;
+//   single tokens: launch, one round trip to memory and the parts' exchange,
+//     9 us for 2 rows and two 2,048 x 2,048 matrices;
+//   float32: shared memory (every value is there as float32 and as parts, and
+//     the six part products read them again).  1,000,000 x 64 times 64 x 64 in
+//     50 segments: 139 us = 3.7 TB/s.
+//
+// float32: every value is split into three bfloat16 parts by truncation (8 + 8
+// + 8 bits, exact) and six of the nine part products are accumulated; the
+// other three are below 2^-21 of the whole.
 // The tensor cores cut what an addition shifts out of the accumulator (a bias
 // of about 2^-26 of it per 16 steps, measured), so for float32 the five small
 // part products have an accumulator of their own, and where the result is
@@ -1115,6 +1130,7 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
         const int quarter = (warp - EPI_WARP) & 3, group = (warp - EPI_WARP) / 4;   // which lanes; which columns
         const int td = tid - EPI_WARP * 32;
         constexpr int W = MODE == PRODUCT_ADAPTERS ? 8 : (TENSOR && PL == 1 ? 32 : 16), ROWS = W * (EPW / 4);    // columns at a time; of all warps
+        constexpr bool AHEAD = PL == 1;      // the next ones are loaded before these are stored, where registers allow
         unsigned char* const own_staging = staging + (warp - EPI_WARP) * R::STAGING;
         LowRank<PL, R::LOW> low(p, tile_adapter, own_staging, lane);
         if (MODE == PRODUCT_FORWARD && !p.index) {
@@ -1179,7 +1195,12 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                 const bool fresh = piece == t.kb0, final = t.kb1 - piece <= a.flush;
                 const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * R::ACC;
                 bool waiting = summed;
-                int c = group * W;
+                int c = lanes > 0 ? group * W : n_left;
+                float d[W], lo[W];       // the accumulators' next columns
+                auto load = [&](int at_c) {
+                    tmem_load(from + at_c, d);
+                    if constexpr (PL > 1) tmem_load(from + NT + at_c, lo);
+                };
                 if constexpr (MODE == PRODUCT_ADAPTERS)
                     if (final && scattered) low.begin(t.row0, t.rows, m + lane, c + t.part * ROWS);
                 for (;;) {
@@ -1190,21 +1211,23 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                     if constexpr (MODE == PRODUCT_ADAPTERS)
                         if (final && scattered && c < n_left && c / ROWS % t.parts == t.part) low.rows_of(v, c, c + ROWS * t.parts);
                     if (waiting) {
-                        ok = bar_drain_all(wait_for<CG>(acc_full + buf, bph, p.status));
+                        // (where the drain warps meet at barriers, they give up together)
+                        if (MODE == PRODUCT_ADAPTERS) ok = bar_drain_all(wait_for<CG>(acc_full + buf, bph, p.status));
+                        else ok = warp_wait<CG>(acc_full + buf, bph, p.status);
                         if (!ok) break;
                         tc_fence_after();
                         waiting = false;
+                        if (AHEAD && c < n_left) load(c);
                     }
                     if (c >= n_left) break;
                     const int n = n_left - c < W ? n_left - c : W;
                     if (summed) {
-                        float d[W], lo[W];
-                        tmem_load(from + c, d);
-                        if constexpr (PL > 1) tmem_load(from + NT + c, lo);
+                        if (!AHEAD) load(c);
                         tmem_wait(d);
                         if constexpr (PL > 1) tmem_wait(lo);
 #pragma unroll
                         for (int j = 0; j < W; ++j) v[j] += PL > 1 ? d[j] + lo[j] : d[j];
+                        if (AHEAD && c + ROWS < n_left) load(c + ROWS);
                         if (!fresh && (partial || lane < lanes)) {
                             // the sum so far, float32 wherever there is more than one piece
                             const float* so_far = partial ? a.partials + slot + int64_t(c) * MT : static_cast<const float*>(p.out) + at + c * step;
@@ -1364,7 +1387,7 @@ __global__ void __launch_bounds__(256) pack_kernel(const __grid_constant__ PackA
 // request would use 16 of its lanes and stream K through one SM.  96 rows of
 // 4,096 columns, rank 16: see launch_lora_rows.
 
-constexpr int DOT_RANKS = 8;      // warps of a block: ranks of one row
+constexpr int DOT_RANKS = 4;      // ranks of a block, of one row; two warps each
 
 template <class T> __device__ __forceinline__ float to_float(T v);
 template <> __device__ __forceinline__ float to_float<float>(float v) { return v; }
@@ -1372,41 +1395,65 @@ template <> __device__ __forceinline__ float to_float<__half>(__half v) { return
 template <> __device__ __forceinline__ float to_float<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
 
 template <class T>
-__global__ void __launch_bounds__(DOT_RANKS * 32) lora_rows_kernel(const __grid_constant__ ProductParams p) {
+__global__ void __launch_bounds__(DOT_RANKS * 64, 3) lora_rows_kernel(const __grid_constant__ ProductParams p) {
     __shared__ int adapter;
+    __shared__ float other[DOT_RANKS];
     grid_trigger();
     const int64_t row = blockIdx.x;
-    const int lane = threadIdx.x & 31;
-    const int64_t j = int64_t(blockIdx.y) * DOT_RANKS + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31, slot = threadIdx.x >> 6, half = threadIdx.x >> 5 & 1;
+    const int64_t j = int64_t(blockIdx.y) * DOT_RANKS + slot;
+    const T* x = static_cast<const T*>(p.x) + row * p.ldx;
+    // The row's first values are asked for before its adapter is known.
+    constexpr int V = 16 / sizeof(T), AHEAD = 8, STEP = 64 * V;
+    const bool whole_x = (reinterpret_cast<uintptr_t>(x) & 15) == 0 && p.K % V == 0;
+    const int64_t k0 = (half * 32 + lane) * V;
+    uint4 xr[AHEAD];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+        xr[i] = whole_x && k0 + i * STEP < p.K ? __ldg(reinterpret_cast<const uint4*>(x + k0 + i * STEP)) : make_uint4(0, 0, 0, 0);
     if (threadIdx.x == 0) adapter = -1;
     __syncthreads();
-    for (int64_t s = threadIdx.x; s < p.S; s += DOT_RANKS * 32)
-        if (offset_at(p, s) <= row && row < offset_at(p, s + 1)) adapter = __ldg(p.index + s);
+    for (int64_t s = threadIdx.x; s < p.S; s += DOT_RANKS * 64) {
+        const int l = __ldg(p.index + s);
+        if (offset_at(p, s) <= row && row < offset_at(p, s + 1)) adapter = l;
+    }
     __syncthreads();
     const int l = adapter;
-    if (l < 0 || l >= p.L || j >= p.N) return;
-    const T* x = static_cast<const T*>(p.x) + row * p.ldx;
-    const T* a = static_cast<const T*>(p.w) + (int64_t(l) * p.N + j) * p.K;
-    constexpr int V = 16 / sizeof(T);
+    if (l < 0 || l >= p.L) return;
     float sum = 0.0f, sum2 = 0.0f;
-    if (((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(a)) & 15) == 0 && p.K % V == 0) {
-#pragma unroll 8
-        for (int64_t k = lane * V; k < p.K; k += 32 * V) {
-            const uint4 xr = __ldg(reinterpret_cast<const uint4*>(x + k)), ar = __ldg(reinterpret_cast<const uint4*>(a + k));
-            const T *xv = reinterpret_cast<const T*>(&xr), *av = reinterpret_cast<const T*>(&ar);
+    if (j < p.N) {
+        const T* a = static_cast<const T*>(p.w) + (int64_t(l) * p.N + j) * p.K;
+        if (whole_x && (reinterpret_cast<uintptr_t>(a) & 15) == 0) {
+            for (int64_t k = k0; k < p.K; k += AHEAD * STEP) {
+                uint4 ar[AHEAD];
 #pragma unroll
-            for (int i = 0; i < V; i += 2) {
-                sum = fmaf(to_float(xv[i]), to_float(av[i]), sum);
-                sum2 = fmaf(to_float(xv[i + 1]), to_float(av[i + 1]), sum2);
+                for (int i = 0; i < AHEAD; ++i)
+                    ar[i] = k + i * STEP < p.K ? __ldg(reinterpret_cast<const uint4*>(a + k + i * STEP)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int i = 0; i < AHEAD; ++i) {
+                    const T *xv = reinterpret_cast<const T*>(&xr[i]), *av = reinterpret_cast<const T*>(&ar[i]);
+                    // (a beyond the row's end counts as zero, whatever x holds there)
+                    if (k + i * STEP < p.K)
+#pragma unroll
+                        for (int v = 0; v < V; v += 2) {
+                            sum = fmaf(to_float(xv[v]), to_float(av[v]), sum);
+                            sum2 = fmaf(to_float(xv[v + 1]), to_float(av[v + 1]), sum2);
+                        }
+                    const int64_t next = k + (AHEAD + i) * STEP;
+                    if (next < p.K) xr[i] = __ldg(reinterpret_cast<const uint4*>(x + next));
+                }
             }
+        } else {
+            for (int64_t k = half * 32 + lane; k < p.K; k += 64) sum = fmaf(to_float(__ldg(x + k)), to_float(__ldg(a + k)), sum);
         }
-    } else {
-        for (int64_t k = lane; k < p.K; k += 32) sum = fmaf(to_float(__ldg(x + k)), to_float(__ldg(a + k)), sum);
     }
     sum += sum2;
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    if (lane == 0) static_cast<float*>(p.out)[row * p.ldo + j] = sum * (p.scale ? __ldg(p.scale + l) : 1.0f);
+    if (half == 1 && lane == 0) other[slot] = sum;
+    __syncthreads();
+    if (half == 0 && lane == 0 && j < p.N)
+        static_cast<float*>(p.out)[row * p.ldo + j] = (sum + other[slot]) * (p.scale ? __ldg(p.scale + l) : 1.0f);
 }
 
 // ---------------------------------------------------------------------------
@@ -1532,7 +1579,7 @@ template <int MODE>
 cudaError_t launch_mode(const KernelArgs& a, const ProductPlan& plan, cudaStream_t stream) {
     if (a.p.type == PT_F32 && plan.tensor)
         return plan.narrow ? launch_shape<MODE, true, 64, 3, 1>(a, plan, stream) : launch_shape<MODE, true, 128, 3, 1>(a, plan, stream);
-    if constexpr (MODE != PRODUCT_WEIGHTS) {
+    if constexpr (MODE == PRODUCT_FORWARD) {
         if (!plan.tensor) return a.p.type == PT_F32 ? launch_shape<MODE, false, 64, 3, 1>(a, plan, stream) : launch_shape<MODE, false, 64, 1, 1>(a, plan, stream);
     }
     if (plan.narrow) return launch_shape<MODE, true, 64, 1, 1>(a, plan, stream);
@@ -1568,10 +1615,11 @@ ProductPlan plan_product(int mode, const ProductParams& p) {
     const bool copy_w = tensor_copyable(p.w, p.ldw, p.type) && (mats == 1 || tensor_copyable(p.w, p.stride_w, p.type));
     const int64_t segments = mode == PRODUCT_ADAPTERS ? 1 : p.S;
     // An operand that tensor copies cannot take is laid out again first (one
-    // more pass over it), except for a few rows per segment, where that pass
-    // would read matrices that no row needs: the loader warps take it as it is.
-    // 8,192 rows in 8 segments, 1,023 x 1,021 bfloat16: see pack_kernel.
-    if (!d.empty && !(copy_x && copy_w) && (weights || p.R > 64 * segments)) {
+    // more pass over it), except where most matrices are in no use: then the
+    // loader warps take what is used as it is, at about a sixth of the speed.
+    // (8,192 rows in 8 segments, 1,023 x 1,021 bfloat16: 40 us, by the loader
+    // warps 174; 128 rows in 64 segments, 2,047 x 1,023: 152 us against 252.)
+    if (!d.empty && !(copy_x && copy_w) && (weights || 2 * p.R >= mats)) {
         d.pack_x = !copy_x;
         d.pack_w = !copy_w;
     }
@@ -1653,9 +1701,9 @@ cudaError_t launch_pack(const void* src, int64_t ld, int64_t stride, const MatSh
 
 cudaError_t launch_lora_rows(const ProductParams& p, cudaStream_t stream) {
     const dim3 grid(static_cast<unsigned>(p.R), static_cast<unsigned>(ceil_to(p.N, DOT_RANKS)));
-    if (p.type == PT_F32) lora_rows_kernel<float><<<grid, DOT_RANKS * 32, 0, stream>>>(p);
-    else if (p.type == PT_F16) lora_rows_kernel<__half><<<grid, DOT_RANKS * 32, 0, stream>>>(p);
-    else lora_rows_kernel<__nv_bfloat16><<<grid, DOT_RANKS * 32, 0, stream>>>(p);
+    if (p.type == PT_F32) lora_rows_kernel<float><<<grid, DOT_RANKS * 64, 0, stream>>>(p);
+    else if (p.type == PT_F16) lora_rows_kernel<__half><<<grid, DOT_RANKS * 64, 0, stream>>>(p);
+    else lora_rows_kernel<__nv_bfloat16><<<grid, DOT_RANKS * 64, 0, stream>>>(p);
     return cudaGetLastError();
 }
 

@@ -224,6 +224,29 @@ def test_few_rows_and_long_sums(dtype, rows, segments, k, n):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("trans", (False, True))
+@pytest.mark.parametrize("rows,k,n", ((1, 63, 65), (3, 1023, 130), (7, 513, 301), (2, 200, 5)))
+def test_odd_rows_of_few_of_many_matrices(dtype, trans, rows, k, n):
+    """Operands that tensor copies cannot take and most matrices in no use (those hold NaN)."""
+    torch, sr = mods()
+    segments = 16
+    rng = np.random.default_rng(k)
+    lens = np.zeros(segments, dtype=np.int64)
+    lens[rng.choice(segments, size=min(rows, 3), replace=False)] = 1
+    lens[np.flatnonzero(lens)[-1]] += rows - lens.sum()
+    off = np.concatenate([[0], np.cumsum(lens)]) + 1
+    g = torch.Generator(device="cuda")
+    g.manual_seed(n)
+    x = normal(g, (rows + 2, k), dtype)
+    w = normal(g, (segments, n, k) if trans else (segments, k, n), dtype, k ** -0.5)
+    w[torch.from_numpy(lens == 0).cuda()] = float("nan")
+    got = sr.seg_matmul(x, w, torch.from_numpy(off).cuda(), transpose_w=trans)
+    y, a = ref_forward(x, w, off, trans)
+    check(got, y, a, k, (dtype, trans, rows, k, n))
+    assert sr.device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 def test_positive_values(dtype):
     """Sums that only grow show a bias in how they are added."""
     torch, sr = mods()
