@@ -421,10 +421,20 @@ seg_status_t seg_flags_to_offsets(const uint8_t *flags, int64_t n, int64_t *offs
  *                 [0, num_rows] on the device); at most 2^30 segments.
  *   out           device, [num_rows, N], rows ldo elements apart (ldo >= N).
  *
- * Every pointer is aligned to its element; 16-byte aligned x and w whose row
- * strides are multiples of 16 bytes enable the tensor-copy path of the
- * 16-bit types.  w may hold any values for empty segments, and x for rows in
+ * Every pointer is aligned to its element.  16-byte aligned x and w whose row
+ * (and matrix) strides are multiples of 16 bytes are read as they are; others
+ * are first copied to such rows in scratch, except w where most matrices
+ * are in no use.  w may hold any values for empty segments, and x for rows in
  * no segment (NaN and infinities included): neither reaches the output.
+ *
+ * Scratch is the library's, one buffer per (device, stream) for all products:
+ * nothing but those copies for seg_matmul, up to about 0.5 GB of float32
+ * partial sums for seg_matmul_grad_w (few columns, many rows), num_rows * rank
+ * float32 values for seg_lora.  It is allocated (cudaMalloc) when a call needs
+ * more than the calls before on its stream, and kept.  Captured into a graph,
+ * a call keeps using the scratch of the stream that it was captured from:
+ * replays must not overlap other products on that stream.
+ * Enqueues one to four kernel launches and returns without synchronising.
  *
  * Numerics.  Sums are float32 in an order that is a pure function of the
  * sizes, the offsets and the SM count (calls repeat bit for bit), rounded

@@ -371,6 +371,46 @@ __device__ __forceinline__ void store_result(const KernelArgs& a, int64_t at, in
     }
 }
 
+// This warp's columns of a finished tile, from tensor memory to 16-bit rows
+// that take 16-byte stores: 32 columns at a time, in 8 x 8 blocks that the
+// store to the warp's staging transposes (2-byte stores there, 32 a column
+// group, took twice the time), its 16-byte units turned by the row against
+// bank conflicts.
+template <int STRIDE>
+__device__ __forceinline__ void store_tile(const KernelArgs& a, uint32_t from, bool summed, int c, int columns, int64_t at, int64_t step,
+                                           int lanes, int lane, unsigned char* staging) {
+    const int type = a.p.out_type;
+    float v[32];
+    if (c < columns && summed) tmem_load_blocks(from + c, v);
+    for (; c < columns; c += STRIDE) {
+        uint32_t two[16];
+        if (summed) {
+            tmem_wait(v);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) two[i] = narrow_pair(v[2 * i], v[2 * i + 1], type);
+            if (c + STRIDE < columns) tmem_load_blocks(from + c + STRIDE, v);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) two[i] = 0;
+        }
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int row = 8 * k + (lane & 7);
+            store_blocks_t(staging + row * 64 + (((lane >> 3) ^ (row >> 1 & 3)) << 4), two[2 * k], two[2 * k + 1], two[8 + 2 * k], two[8 + 2 * k + 1]);
+        }
+        __syncwarp();
+        const int unit = lane & 3;
+        uint16_t* o = static_cast<uint16_t*>(a.p.out) + at + c * step + unit * 8;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int row = i * 8 + (lane >> 2);
+            if (c + row < columns && unit * 8 < lanes)
+                *reinterpret_cast<uint4*>(o + row * step) = *reinterpret_cast<const uint4*>(staging + row * 64 + ((unit ^ (row >> 1 & 3)) << 4));
+        }
+    }
+}
+
 // The adapters' part of a tile, by the float32 pipes while the tensor cores
 // work on: v[j] = sum_k u[row c + j, k] b[l_j, m, k] for 8 rows of this
 // lane's column m at a time, 16 ranks a step.  The rows' u go through the
@@ -1130,9 +1170,10 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
         const int quarter = (warp - EPI_WARP) & 3, group = (warp - EPI_WARP) / 4;   // which lanes; which columns
         const int td = tid - EPI_WARP * 32;
         constexpr int W = MODE == PRODUCT_ADAPTERS ? 8 : (TENSOR && PL == 1 ? 32 : 16), ROWS = W * (EPW / 4);    // columns at a time; of all warps
+        constexpr bool BLOCKS = TENSOR && PL == 1 && MODE != PRODUCT_ADAPTERS;
         constexpr bool AHEAD = PL == 1;      // the next ones are loaded before these are stored, where registers allow
         unsigned char* const own_staging = staging + (warp - EPI_WARP) * R::STAGING;
-        LowRank<PL, R::LOW> low(p, tile_adapter, own_staging, lane);
+        [[maybe_unused]] LowRank<PL, R::LOW> low(p, tile_adapter, own_staging, lane);
         if (MODE == PRODUCT_FORWARD && !p.index) {
             // rows in no segment
             const int b = p.S > 0 ? beg[0] : 0, e = p.S > 0 ? beg[p.S] : 0;
@@ -1194,6 +1235,23 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
             do {
                 const bool fresh = piece == t.kb0, final = t.kb1 - piece <= a.flush;
                 const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * R::ACC;
+                if constexpr (BLOCKS) {
+                    if (!partial && a.wide_rows && p.out_type != PT_F32) {
+                        if (summed) {
+                            ok = warp_wait<CG>(acc_full + buf, bph, p.status);
+                            if (!ok) break;
+                            tc_fence_after();
+                        }
+                        if (lanes > 0) store_tile<EPW / 4 * 32>(a, from, summed, group * 32, n_left, at, step, lanes, lane, own_staging);
+                        if (summed) {
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) lead_arrive<CG>(acc_empty + buf, lead, false);
+                            if ((buf ^= 1) == 0) bph ^= 1;
+                        }
+                        break;       // one piece: 16-bit results take the sums as they are
+                    }
+                }
                 bool waiting = summed;
                 int c = lanes > 0 ? group * W : n_left;
                 float d[W], lo[W];       // the accumulators' next columns

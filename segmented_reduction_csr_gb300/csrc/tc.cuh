@@ -209,6 +209,29 @@ __device__ __forceinline__ void tmem_load(uint32_t addr, float (&v)[16]) {
         : "r"(addr)
         : "memory");
 }
+// 32 columns of 32 lanes as 8 x 8 blocks: registers 16 h + 4 k + 2 e and + 1
+// hold lane 16 h + 8 e + t / 4, columns 8 k + 2 (t % 4) and + 1 (t = threadIdx % 32).
+__device__ __forceinline__ void tmem_load_blocks(uint32_t addr, float (&v)[32]) {
+    uint32_t* r = reinterpret_cast<uint32_t*>(v);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr)
+        : "memory");
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr + (16u << 16))
+        : "memory");
+}
+// Four 8 x 8 blocks of 16-bit values, transposed: lane 8 b + i names the 16 bytes that get column i of block b.
+__device__ __forceinline__ void store_blocks_t(const void* where, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(smem_u32(where)), "r"(a), "r"(b), "r"(c),
+                 "r"(d)
+                 : "memory");
+}
 // Registers of tmem_load may be read after this.
 __device__ __forceinline__ void tmem_wait(float (&v)[32]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
