@@ -428,8 +428,8 @@ seg_status_t seg_flags_to_offsets(const uint8_t *flags, int64_t n, int64_t *offs
  * no segment (NaN and infinities included): neither reaches the output.
  *
  * Scratch is the library's, one buffer per (device, stream) for all products:
- * nothing but those copies for seg_matmul, up to about 0.5 GB of float32
- * partial sums for seg_matmul_grad_w (few columns, many rows), num_rows * rank
+ * those copies (and 8 bytes per segment above 1,024) for seg_matmul, also up
+ * to about 0.5 GB of float32 partial sums for seg_matmul_grad_w (few columns, many rows), num_rows * rank
  * float32 values for seg_lora.  It is allocated (cudaMalloc) when a call needs
  * more than the calls before on its stream, and kept.  Captured into a graph,
  * a call keeps using the scratch of the stream that it was captured from:
