@@ -412,7 +412,7 @@ seg_status_t seg_flags_to_offsets(const uint8_t *flags, int64_t n, int64_t *offs
  *   x             device, [num_rows, K], rows ldx elements apart (ldx >= K),
  *                 of `dtype`.
  *   dtype         SEG_F32, SEG_F16 or SEG_BF16: the type of x, w and out.
- *   num_rows      0 <= R < 2^31.
+ *   num_rows      0 <= R <= 2^31 - 4096.
  *   K, N          0 <= K, 0 <= N, both at most SEG_MAX_PRODUCT_COLUMNS.  K == 0
  *                 gives zeros; R == 0 or N == 0 launches nothing.
  *   w             device, num_segments matrices stride_w elements apart, each

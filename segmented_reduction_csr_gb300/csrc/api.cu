@@ -252,13 +252,24 @@ seg_status_t check_product(seg_dtype_t dtype, int64_t num_rows, int64_t K, int64
     if (bad_product_type(dtype)) return SEG_ERR_INVALID_ARGUMENT;
     if (offsets_dtype != SEG_OFF_U32 && offsets_dtype != SEG_OFF_I64) return SEG_ERR_INVALID_ARGUMENT;
     if (num_rows < 0 || K < 0 || N < 0 || S < 0 || ldx < K) return SEG_ERR_INVALID_ARGUMENT;
-    if (num_rows > INT32_MAX || S > (int64_t(1) << 30) || K > SEG_MAX_PRODUCT_COLUMNS || N > SEG_MAX_PRODUCT_COLUMNS)
+    if (num_rows > INT32_MAX - 4095 || S > (int64_t(1) << 30) || K > SEG_MAX_PRODUCT_COLUMNS || N > SEG_MAX_PRODUCT_COLUMNS)
         return SEG_ERR_UNSUPPORTED;
     if (num_rows > 0 && K > 0 && !x) return SEG_ERR_INVALID_ARGUMENT;
     if (S > 0 && !offsets) return SEG_ERR_INVALID_ARGUMENT;
     if (misaligned(x, product_size(dtype)) || misaligned(offsets, offsets_dtype == SEG_OFF_U32 ? 4 : 8))
         return SEG_ERR_INVALID_ARGUMENT;
     return SEG_OK;
+}
+
+// No exception leaves a product's entry point (the containers allocate, the
+// lock can fail).
+template <class F>
+seg_status_t guarded(F f) {
+    try {
+        return f();
+    } catch (...) {
+        return SEG_ERR_OUT_OF_MEMORY;
+    }
 }
 
 // Enqueues one product on scratch that is large enough.
@@ -790,7 +801,7 @@ seg_status_t seg_matmul(const void* x, seg_dtype_t dtype, int64_t num_rows, int6
     p.off64 = offsets_dtype == SEG_OFF_I64 ? 1 : 0;
     p.trans = transpose_w;
     p.type = p.out_type = dtype;
-    return run_product(PRODUCT_FORWARD, p, reinterpret_cast<cudaStream_t>(stream));
+    return guarded([&] { return run_product(PRODUCT_FORWARD, p, reinterpret_cast<cudaStream_t>(stream)); });
 }
 
 seg_status_t seg_matmul_grad_w(const void* x, seg_dtype_t dtype, int64_t num_rows, int64_t K, int64_t ldx,
@@ -817,7 +828,7 @@ seg_status_t seg_matmul_grad_w(const void* x, seg_dtype_t dtype, int64_t num_row
     p.off64 = offsets_dtype == SEG_OFF_I64 ? 1 : 0;
     p.type = dtype;
     p.out_type = out_dtype;
-    return run_product(PRODUCT_WEIGHTS, p, reinterpret_cast<cudaStream_t>(stream));
+    return guarded([&] { return run_product(PRODUCT_WEIGHTS, p, reinterpret_cast<cudaStream_t>(stream)); });
 }
 
 seg_status_t seg_lora(const void* x, seg_dtype_t dtype, int64_t num_rows, int64_t K, int64_t ldx,
@@ -838,69 +849,71 @@ seg_status_t seg_lora(const void* x, seg_dtype_t dtype, int64_t num_rows, int64_
     if (misaligned(w, size) || misaligned(a, size) || misaligned(b, size) || misaligned(out, size) ||
         misaligned(adapter, 4) || misaligned(scale, 4))
         return SEG_ERR_INVALID_ARGUMENT;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return SEG_ERR_CUDA;
-    std::lock_guard<std::mutex> lock(g_mu);
-    DeviceState* ds = nullptr;
-    st = device_state(dev, &ds);
-    if (st != SEG_OK) return st;
-    // the products with a, scaled, in float32: u = scale * x a^T
-    ProductParams pa{};
-    pa.x = x;
-    pa.w = a;
-    pa.offsets = offsets;
-    pa.index = adapter;
-    pa.scale = scale;
-    pa.R = num_rows;
-    pa.K = K;
-    pa.N = rank;
-    pa.S = num_segments;
-    pa.ldx = ldx;
-    pa.ldw = K;
-    pa.stride_w = rank * K;
-    pa.ldo = rank;
-    pa.L = num_adapters;
-    pa.off64 = offsets_dtype == SEG_OFF_I64 ? 1 : 0;
-    pa.trans = 1;
-    pa.type = dtype;
-    pa.out_type = SEG_F32;
-    pa.sms = ds->sm_count;
-    // the shared product, to which the low-rank part is added
-    ProductParams p = pa;
-    p.w = w;
-    p.scale = nullptr;
-    p.out = out;
-    p.N = N;
-    p.ldw = ldw;
-    p.stride_w = 0;
-    p.ldo = ldo;
-    p.out_type = dtype;
-    p.b = b;
-    p.rank = rank;
-    const bool low = num_segments > 0 && num_adapters > 0;
-    const bool by_rows = lora_by_rows(pa);
-    const int64_t own = std::max(low && !by_rows ? plan_product(PRODUCT_FORWARD, pa).bytes() : 0, plan_product(PRODUCT_ADAPTERS, p).bytes());
-    Scratch* sc = nullptr;
-    st = product_scratch(dev, stream, static_cast<size_t>(own + num_rows * rank * 4), &sc);
-    if (st != SEG_OK) return st;
-    float* u = reinterpret_cast<float*>(static_cast<unsigned char*>(sc->ptr) + own);
-    if (low) {
-        pa.out = u;
-        if (by_rows) {
-            if (launch_lora_rows(pa, stream) != cudaSuccess) {
-                cudaGetLastError();
-                return SEG_ERR_CUDA;
+    return guarded([&]() -> seg_status_t {
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess) return SEG_ERR_CUDA;
+        std::lock_guard<std::mutex> lock(g_mu);
+        DeviceState* ds = nullptr;
+        st = device_state(dev, &ds);
+        if (st != SEG_OK) return st;
+        // the products with a, scaled, in float32: u = scale * x a^T
+        ProductParams pa{};
+        pa.x = x;
+        pa.w = a;
+        pa.offsets = offsets;
+        pa.index = adapter;
+        pa.scale = scale;
+        pa.R = num_rows;
+        pa.K = K;
+        pa.N = rank;
+        pa.S = num_segments;
+        pa.ldx = ldx;
+        pa.ldw = K;
+        pa.stride_w = rank * K;
+        pa.ldo = rank;
+        pa.L = num_adapters;
+        pa.off64 = offsets_dtype == SEG_OFF_I64 ? 1 : 0;
+        pa.trans = 1;
+        pa.type = dtype;
+        pa.out_type = SEG_F32;
+        pa.sms = ds->sm_count;
+        // the shared product, to which the low-rank part is added
+        ProductParams p = pa;
+        p.w = w;
+        p.scale = nullptr;
+        p.out = out;
+        p.N = N;
+        p.ldw = ldw;
+        p.stride_w = 0;
+        p.ldo = ldo;
+        p.out_type = dtype;
+        p.b = b;
+        p.rank = rank;
+        const bool low = num_segments > 0 && num_adapters > 0;
+        const bool by_rows = lora_by_rows(pa);
+        const int64_t own = std::max(low && !by_rows ? plan_product(PRODUCT_FORWARD, pa).bytes() : 0, plan_product(PRODUCT_ADAPTERS, p).bytes());
+        Scratch* sc = nullptr;
+        st = product_scratch(dev, stream, static_cast<size_t>(own + num_rows * rank * 4), &sc);
+        if (st != SEG_OK) return st;
+        float* u = reinterpret_cast<float*>(static_cast<unsigned char*>(sc->ptr) + own);
+        if (low) {
+            pa.out = u;
+            if (by_rows) {
+                if (launch_lora_rows(pa, stream) != cudaSuccess) {
+                    cudaGetLastError();
+                    return SEG_ERR_CUDA;
+                }
+            } else {
+                st = run_product(PRODUCT_FORWARD, pa, stream, sc, ds);
+                if (st != SEG_OK) return st;
             }
-        } else {
-            st = run_product(PRODUCT_FORWARD, pa, stream, sc, ds);
-            if (st != SEG_OK) return st;
+            p.u = u;
+            // beside a kernel of short dot products; the tensor-core one needs the
+            // memory to itself (prompts of 8,193 rows: 238 us together, 211 one after the other)
+            p.overlap = by_rows ? 1 : 0;
         }
-        p.u = u;
-        // beside a kernel of short dot products; the tensor-core one needs the
-        // memory to itself (prompts of 8,193 rows: 238 us together, 211 one after the other)
-        p.overlap = by_rows ? 1 : 0;
-    }
-    return run_product(PRODUCT_ADAPTERS, p, stream, sc, ds);
+        return run_product(PRODUCT_ADAPTERS, p, stream, sc, ds);
+    });
 }
 
 seg_status_t seg_selftest_wait_timeout(uint32_t limit_ms, seg_stream_t stream_) {

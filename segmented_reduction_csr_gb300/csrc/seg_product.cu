@@ -122,8 +122,9 @@ __device__ __forceinline__ int segment_items(const KernelArgs& a, int64_t s, int
     return (len + NT - 1) / NT;
 }
 
-// beg[s] = offset s, pre[s] = items of the segments before s (s = 0 .. S), by all threads of the CTA.
-template <int MODE, int NT>
+// beg[s] = offset s, pre[s] = items of the segments before s (s = 0 .. S), by
+// all threads of the CTA, PER segments a thread at a time.
+template <int MODE, int NT, int PER>
 __device__ void fill_prefix(const KernelArgs& a, int* beg, int* pre) {
     __shared__ int64_t warp_sum[32];
     __shared__ int64_t carry;
@@ -132,21 +133,31 @@ __device__ void fill_prefix(const KernelArgs& a, int* beg, int* pre) {
     if (t == 0) carry = 0;
     for (int64_t s = t; s <= S; s += nth) beg[s] = offset_at(a.p, s);
     __syncthreads();
-    for (int64_t s0 = 0; s0 < S; s0 += nth) {
-        const int64_t s = s0 + t;
-        const int v = s < S ? segment_items<MODE, NT>(a, s, beg[s], beg[s + 1]) : 0;
-        int64_t x = v;   // 64 bits: offsets that go back and forth add up to more than the rows
+    for (int64_t s0 = 0; s0 < S; s0 += nth * PER) {
+        const int64_t s = s0 + t * PER;
+        int v[PER];
+        int64_t own = 0;   // 64 bits: offsets that go back and forth add up to more than the rows
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            v[i] = s + i < S ? segment_items<MODE, NT>(a, s + i, beg[s + i], beg[s + i + 1]) : 0;
+            own += v[i];
+        }
+        int64_t x = own;
         for (int d = 1; d < 32; d <<= 1) {
             const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
             if (lane >= d) x += y;
         }
         if (lane == 31) warp_sum[warp] = x;
         __syncthreads();
-        int64_t before = carry;
+        int64_t before = carry + x - own;
         for (int w = 0; w < warp; ++w) before += warp_sum[w];
-        if (s < S) pre[s] = static_cast<int>(min(before + x - v, int64_t(INT_MAX)));
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            if (s + i < S) pre[s + i] = static_cast<int>(min(before, int64_t(INT_MAX)));
+            before += v[i];
+        }
         __syncthreads();
-        if (t == nth - 1) carry = before + x;
+        if (t == nth - 1) carry = before;
         __syncthreads();
     }
     if (t == 0) pre[S] = static_cast<int>(min(carry, int64_t(INT_MAX)));
@@ -156,7 +167,7 @@ __device__ void fill_prefix(const KernelArgs& a, int* beg, int* pre) {
 // The offsets and prefix of many segments, once per call.
 template <int MODE, int NT>
 __global__ void __launch_bounds__(1024) prefix_kernel(const __grid_constant__ KernelArgs a) {
-    fill_prefix<MODE, NT>(a, a.far, a.far + a.p.S + 1);
+    fill_prefix<MODE, NT, 8>(a, a.far, a.far + a.p.S + 1);
 }
 
 struct Item {
@@ -813,7 +824,7 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
     const uint32_t in_cluster = CG == 2 || split ? cluster_rank() : 0;
     const int rank = CG == 2 ? static_cast<int>(in_cluster & 1) : 0;
     const uint32_t lead = in_cluster & ~1u;
-    const uint32_t first = blockIdx.x / CG, stride = gridDim.x / CG;
+    uint32_t first = blockIdx.x / CG, stride = gridDim.x / CG;
 
     const bool is_near = p.S <= NEAR_SEGMENTS;
     const int* beg = is_near ? near : a.far;
@@ -838,7 +849,7 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
             tensor_prefetch(&map_b);
         }
     }
-    if (is_near && MODE != PRODUCT_ADAPTERS && p.S > 0) fill_prefix<MODE, NT>(a, near, near + NEAR_SEGMENTS + 1);
+    if (is_near && MODE != PRODUCT_ADAPTERS && p.S > 0) fill_prefix<MODE, NT, 1>(a, near, near + NEAR_SEGMENTS + 1);
     // (PL == 3: that space is the staging)
     const int* near_offsets = MODE == PRODUCT_ADAPTERS && PL == 1 && is_near ? near : nullptr;
     if (near_offsets && p.S > 0)
@@ -857,6 +868,14 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
     if (MODE == PRODUCT_WEIGHTS) items = static_cast<uint32_t>(min(int64_t(pre[p.S]), p.S + p.R / a.chunk) * (a.mtiles * a.ntiles));
     else if (MODE == PRODUCT_ADAPTERS) items = static_cast<uint32_t>(a.row_tiles * a.mtiles * a.parts);
     else items = static_cast<uint32_t>((p.S > 0 ? min(int64_t(pre[p.S]), a.row_tiles) : 0) * a.mtiles * a.parts);
+    if (MODE != PRODUCT_ADAPTERS && !is_near) {
+        // many segments, whose prefix is in memory: neighbouring items, so that
+        // the next one's segment is found by a step or two instead of a search
+        const uint32_t each = (items + stride - 1) / stride;
+        first *= each;
+        items = min(items, first + each);
+        stride = 1;
+    }
     const bool a_outer = MODE == PRODUCT_WEIGHTS || !p.trans;    // the operand's contiguous dimension is m, not the sum
     constexpr bool b_outer = MODE == PRODUCT_WEIGHTS;
 
