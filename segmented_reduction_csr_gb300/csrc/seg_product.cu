@@ -588,24 +588,30 @@ __device__ __forceinline__ void split_pair(float x, float y, uint32_t (&r)[3]) {
 
 // float32 rows of 64 values that tensor copies left in the second (values 0
 // to 31) and third plane, into their parts in all three.  A warp takes two
-// whole rows at a time, and writes when all of it has been read.
+// whole rows at a time, four times over, and writes when all have been read.
 __device__ __forceinline__ void split_rows(int rows, int valid, unsigned char* dst, int plane) {
+    constexpr int STEP = LOADERS / 16, AHEAD = 4;
     const int t = threadIdx.x - LOAD_WARP * 32, q = t & 15, row = t >> 4;      // 16 bytes q of the row; 8 units of 8 values
     const unsigned char* from = dst + row * 128 + (1 + (q >> 3)) * plane + (((q & 7) ^ (row & 7)) << 4);
     unsigned char* to = dst + row * 128 + (((q >> 1) ^ (row & 7)) << 4) + (q & 1) * 8;
-    constexpr int STEP = LOADERS / 16;
-#pragma unroll 2
-    for (int r = row; r - row < rows; r += STEP) {
-        float4 x = *reinterpret_cast<const float4*>(from);
-        if ((r & 63) >= valid) x = make_float4(0, 0, 0, 0);
-        __syncwarp();
-        uint32_t a[3], b[3];
-        split_pair(x.x, x.y, a);
-        split_pair(x.z, x.w, b);
+    for (int r = row; r - row < rows; r += AHEAD * STEP) {
+        float4 x[AHEAD];
 #pragma unroll
-        for (int k = 0; k < 3; ++k) *reinterpret_cast<uint2*>(to + k * plane) = make_uint2(a[k], b[k]);
-        from += STEP * 128;
-        to += STEP * 128;
+        for (int i = 0; i < AHEAD; ++i)
+            if (r - row + i * STEP < rows) x[i] = *reinterpret_cast<const float4*>(from + i * STEP * 128);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            if (r - row + i * STEP >= rows) break;
+            if (((r + i * STEP) & 63) >= valid) x[i] = make_float4(0, 0, 0, 0);
+            uint32_t a[3], b[3];
+            split_pair(x[i].x, x[i].y, a);
+            split_pair(x[i].z, x[i].w, b);
+#pragma unroll
+            for (int k = 0; k < 3; ++k) *reinterpret_cast<uint2*>(to + k * plane + i * STEP * 128) = make_uint2(a[k], b[k]);
+        }
+        from += AHEAD * STEP * 128;
+        to += AHEAD * STEP * 128;
     }
 }
 
