@@ -97,6 +97,7 @@ struct KernelArgs {
     int32_t mtiles, ntiles, parts, part_blocks, kblocks;
     int32_t box_rows;   // rows of one copy of x
     int32_t a_rows;     // rows of one copy of A whose sum is contiguous
+    int32_t twin;       // at most 64 lanes, laid out twice: the drain warps of the second 64 share the first's work
     int32_t wide_rows;  // 16-bit results: 16-byte stores fit
     int32_t flush;      // blocks of the sum after which the accumulators go to the result
     int64_t chunk, row_tiles, cols_m, cols_n;   // cols_*: extent of the tile dimensions (forward: cols_n unused)
@@ -897,6 +898,9 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
     // The last block of a weights' sum reaches past the segment: those rows are zeroed once they have arrived.
     auto has_tail = [&](const Item& t, int kb) { return PL == 1 && MODE == PRODUCT_WEIGHTS && kb + 1 == t.kb1 && (t.rows & 15) != 0; };
 
+    constexpr bool TWIN = MODE == PRODUCT_FORWARD && TENSOR && PL == 3;
+    const bool twin = TWIN && a.twin;
+
     if (TENSOR && (warp == 1 || warp == 3)) {
         // ---- producers: two, which take turns at the blocks (one thread's
         // chain of wait, expect and copies for a block took longer than its MMAs) ----
@@ -913,7 +917,7 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                 const int columns = columns_of(t), share = share_of(columns), lanes = lanes_of(t);
                 const int a_boxes = a_outer ? (lanes + 63) / 64 : (lanes + MT - 1) / MT;
                 const int b_boxes = b_outer ? (share + 63) / 64 : (share + a.box_rows - 1) / a.box_rows;
-                const uint32_t a_bytes = a_boxes * (a_outer ? 8192 : a.a_rows * 128) * HALVES, b_bytes = b_boxes * (b_outer ? 8192 : a.box_rows * 128) * HALVES;
+                const uint32_t a_bytes = a_boxes * (a_outer ? 8192 : a.a_rows * 128) * HALVES * (twin ? 2 : 1), b_bytes = b_boxes * (b_outer ? 8192 : a.box_rows * 128) * HALVES;
                 const int m0 = t.m0 + rank * MT;
                 uint32_t other_bytes = 0;
                 if (CG == 2) {
@@ -949,6 +953,9 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                         } else {
                             const int r0 = t.row0 + rank * share, k0 = kb * KB;
                             if (keep) {
+                            } else if (twin) {
+                                for (int x = 0; x < 2; ++x)
+                                    tensor_load_3d<CG>(da + x * 8192, &map_a, a_outer ? m0 + h * 32 : k0 + h * 32, a_outer ? k0 : m0, static_cast<int>(m), bar);
                             } else if (a_outer) {
                                 for (int x = 0; x < a_boxes; ++x)
                                     tensor_load_3d<CG>(da + x * 8192, &map_a, m0 + x * 64 + h * 32, k0, static_cast<int>(m), bar);
@@ -982,7 +989,7 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
         for (uint32_t i = first; ok && i < items; i += stride) {
             item_at<MODE, NT, CG>(a, beg, pre, i, t);
             const int share = share_of(columns_of(t)), lanes = lanes_of(t);
-            const int a_rows = a_outer ? (lanes + 63) & ~63 : a.a_rows, b_rows = b_outer ? (share + 63) & ~63 : share;
+            const int a_rows = twin ? (a_outer ? MT : 64 + a.a_rows) : a_outer ? (lanes + 63) & ~63 : a.a_rows, b_rows = b_outer ? (share + 63) & ~63 : share;
             int64_t m = t.seg;
             if (MODE == PRODUCT_FORWARD && p.index) m = __ldg(p.index + t.seg);
             for (int kb = t.kb0; kb < t.kb1; ++kb) {
@@ -1219,7 +1226,7 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
             item_at<MODE, NT, CG>(a, beg, pre, i, t);
             const bool summed = t.kb1 > t.kb0;
             const int n_left = columns_of(t);
-            const int64_t m = t.m0 + rank * MT + quarter * 32;           // the warp's first lane
+            const int64_t m = t.m0 + rank * MT + (twin ? quarter & 1 : quarter) * 32;           // the warp's first lane
             const int lanes = static_cast<int>(a.cols_m - m < 32 ? a.cols_m - m : 32);   // may be negative
             const int64_t slot = (t.slot * CG + rank) * NT * MT + quarter * 32;      // in floats
             bool scattered = true;      // the drain warps compute the tile's low-rank part
@@ -1278,7 +1285,8 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                     }
                 }
                 bool waiting = summed;
-                int c = lanes > 0 ? group * W : n_left;
+                const int stride_c = twin ? 2 * ROWS : ROWS;
+                int c = lanes > 0 ? (twin ? group + (quarter & 2) : group) * W : n_left;
                 float d[W], lo[W];       // the accumulators' next columns
                 auto load = [&](int at_c) {
                     tmem_load(from + at_c, d);
@@ -1310,7 +1318,7 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                         if constexpr (PL > 1) tmem_wait(lo);
 #pragma unroll
                         for (int j = 0; j < W; ++j) v[j] += PL > 1 ? d[j] + lo[j] : d[j];
-                        if (AHEAD && c + ROWS < n_left) load(c + ROWS);
+                        if (AHEAD && c + stride_c < n_left) load(c + stride_c);
                         if (!fresh && (partial || lane < lanes)) {
                             // the sum so far, float32 wherever there is more than one piece
                             const float* so_far = partial ? a.partials + slot + int64_t(c) * MT : static_cast<const float*>(p.out) + at + c * step;
@@ -1329,7 +1337,7 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                             for (int j = 0; j < W; ++j) v[j] *= factor;
                         store_result(a, at + c * step, step, v, n, lanes, lane, own_staging);
                     }
-                    c += ROWS;
+                    c += stride_c;
                     if (c >= n_left) break;
                 }
                 if (!ok) break;
@@ -1830,6 +1838,7 @@ cudaError_t launch_product(int mode, const ProductParams& given, const ProductPl
     a.flush = plan.parts > 1 ? NEVER_FLUSH : p.type == PT_F32 ? 8 : (p.out_type == PT_F32 && !p.index ? 12 : NEVER_FLUSH);
     const int64_t out_step = mode == PRODUCT_WEIGHTS ? p.N : p.ldo;
     a.wide_rows = p.N % 8 == 0 && out_step % 8 == 0 && reinterpret_cast<uintptr_t>(p.out) % 16 == 0;
+    a.twin = p.type == PT_F32 && p.N <= MT / 2 && plan.parts == 1;
     a.chunk = plan.chunk;
     a.row_tiles = plan.row_tiles;
     a.cols_m = p.N;
