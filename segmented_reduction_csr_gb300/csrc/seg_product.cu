@@ -81,7 +81,8 @@ struct Ring {
     // (the loaders' plain loads are tracked in the L1 that shared memory leaves)
     static constexpr int ALL_STAGES = std::min(8, (PL == 3 ? 221184 : TENSOR ? 200704 : 98304) / STAGE);
     static constexpr int STAGES = ALL_STAGES - (LOW ? 1 : 0);
-    static constexpr int ACC = PL == 1 ? NT : 2 * NT;            // tensor-memory columns of one accumulator
+    static constexpr bool ROW3 = PL == 3 && NT == 64;            // a part of A times several parts of B at once
+    static constexpr int ACC = PL == 1 ? NT : 256;               // tensor-memory columns of one accumulator
     static constexpr int BARS = 3 * STAGES + 7;
     // the drain warps' staging; PL == 3 keeps it (adapters alone need it there) in the space of the offsets
     static constexpr int STAGING = PL == 1 ? 2048 : 1024;
@@ -1154,6 +1155,14 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                             const bool add = kb > piece || k > 0;
                             if constexpr (PL == 1) {
                                 tc_mma<CG>(acc, da + k * a_step, db + k * b_step, idesc, add);
+                            } else if constexpr (R::ROW3) {
+                                // B's parts follow one another in shared memory: as one operand
+                                // they take the first part of A all three, the second two and
+                                // the third one, in three accumulators by size
+#pragma unroll
+                                for (int q = 0; q < 3; ++q)
+                                    tc_mma<CG>(acc + q * NT, da + q * (R::A_PLANE >> 4) + k * a_step, db + k * b_step,
+                                               tc_idesc(type, MT, (2 - q) * NT + share_of(columns_of(t)), a_outer, b_outer), add || q > 0);
                             } else {
                                 // the products of parts: the largest alone, the others together
                                 constexpr int pa[6] = {0, 2, 0, 1, 1, 0}, pb[6] = {0, 0, 2, 1, 0, 1};
@@ -1313,9 +1322,21 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                     if (c >= n_left) break;
                     const int n = n_left - c < W ? n_left - c : W;
                     if (summed) {
-                        if (!AHEAD) load(c);
-                        tmem_wait(d);
-                        if constexpr (PL > 1) tmem_wait(lo);
+                        if constexpr (R::ROW3) {
+                            // (the two small sums first)
+                            tmem_load(from + NT + c, d);
+                            tmem_load(from + 2 * NT + c, lo);
+                            tmem_wait(d);
+                            tmem_wait(lo);
+#pragma unroll
+                            for (int j = 0; j < W; ++j) lo[j] += d[j];
+                            tmem_load(from + c, d);
+                            tmem_wait(d);
+                        } else {
+                            if (!AHEAD) load(c);
+                            tmem_wait(d);
+                            if constexpr (PL > 1) tmem_wait(lo);
+                        }
 #pragma unroll
                         for (int j = 0; j < W; ++j) v[j] += PL > 1 ? d[j] + lo[j] : d[j];
                         if (AHEAD && c + stride_c < n_left) load(c + stride_c);
