@@ -29,15 +29,16 @@
 //   single tokens: launch, one round trip to memory and the parts' exchange,
 //     9 us for 2 rows and two 2,048 x 2,048 matrices;
 //   float32: shared memory (every value is there as float32 and as parts, and
-//     the six part products read them again).  1,000,000 x 64 times 64 x 64 in
-//     50 segments: 139 us = 3.7 TB/s.
+//     the part products read them again).  So a part of one operand takes as
+//     many parts of the other at once as the accumulators have room for.  1,000,000 x 64 times 64 x 64 in
+//     50 segments: 117 us = 4.4 TB/s.
 //
 // float32: every value is split into three bfloat16 parts by truncation (8 + 8
 // + 8 bits, exact) and six of the nine part products are accumulated; the
 // other three are below 2^-21 of the whole.
 // The tensor cores cut what an addition shifts out of the accumulator (a bias
 // of about 2^-26 of it per 16 steps, measured), so for float32 the five small
-// part products have an accumulator of their own, and where the result is
+// part products have accumulators of their own, and where the result is
 // float32 the accumulators are added to it, rounded, every 512 (float32) or
 // 768 (16-bit operands) steps: the bias then stays below 1e-6.
 // Long sums with few tiles are cut into parts, added in order.  Forward: the
@@ -1135,6 +1136,7 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
             for (uint32_t i = first; ok && i < items; i += stride) {
                 item_at<MODE, NT, CG>(a, beg, pre, i, t);
                 const uint32_t idesc = tc_idesc(type, MT * CG, CG * share_of(columns_of(t)), a_outer, b_outer);
+                [[maybe_unused]] const uint32_t wide_idesc = tc_idesc(type, MT, NT + share_of(columns_of(t)), a_outer, b_outer);
                 const int64_t sum = MODE == PRODUCT_WEIGHTS ? t.rows : p.K;
                 bool low_left = R::LOW && p.u && t.part == 0;
                 for (int piece = t.kb0; ok && piece < t.kb1; piece += a.flush) {
@@ -1164,12 +1166,14 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                                     tc_mma<CG>(acc + q * NT, da + q * (R::A_PLANE >> 4) + k * a_step, db + k * b_step,
                                                tc_idesc(type, MT, (2 - q) * NT + share_of(columns_of(t)), a_outer, b_outer), add || q > 0);
                             } else {
-                                // the products of parts: the largest alone, the others together
-                                constexpr int pa[6] = {0, 2, 0, 1, 1, 0}, pb[6] = {0, 0, 2, 1, 0, 1};
+                                // the products of parts: the largest alone, the others
+                                // together; the first part of A takes two of B's at once
+                                tc_mma<CG>(acc, da + k * a_step, db + k * b_step, wide_idesc, add);
+                                constexpr int pa[4] = {2, 0, 1, 1}, pb[4] = {0, 2, 1, 0};
 #pragma unroll
-                                for (int q = 0; q < 6; ++q)
-                                    tc_mma<CG>(q == 0 ? acc : acc + NT, da + pa[q] * (R::A_PLANE >> 4) + k * a_step,
-                                               db + pb[q] * (R::B_PLANE >> 4) + k * b_step, idesc, add || q > 1);
+                                for (int q = 0; q < 4; ++q)
+                                    tc_mma<CG>(acc + NT, da + pa[q] * (R::A_PLANE >> 4) + k * a_step,
+                                               db + pb[q] * (R::B_PLANE >> 4) + k * b_step, idesc, true);
                             }
                         }
                         tc_commit<CG>(empty + st, lead);

@@ -111,6 +111,26 @@ def test_forward_sizes(dtype, trans, k, n):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("trans", (False, True))
+@pytest.mark.parametrize("k,n", ((64, 64), (63, 5), (128, 40), (600, 64), (1100, 24)))
+def test_many_rows_of_few_columns(dtype, trans, k, n):
+    """Tiles of many rows whose lanes are half used or less; sums of one block and of several pieces."""
+    torch, sr = mods()
+    lens = [9001, 0, 1, 128, 8209, 130, 4000]
+    off = 3 + np.concatenate([[0], np.cumsum(lens)]).astype(np.int64)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(k + n)
+    x = normal(g, (int(off[-1]) + 5, k), dtype)
+    w = normal(g, (len(lens), n, k) if trans else (len(lens), k, n), dtype)
+    out = torch.full((x.shape[0], n + 12), 7.0, dtype=x.dtype, device="cuda")
+    got = sr.seg_matmul(x, w, torch.from_numpy(off).cuda(), transpose_w=trans, out=out[:, 4:4 + n])
+    y, a = ref_forward(x, w, off, trans)
+    check(got, y, a, k, (dtype, trans, k, n))
+    assert bool((out[:, :4] == 7).all()) and bool((out[:, 4 + n:] == 7).all())      # nothing beside the columns
+    assert sr.device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("k,n", SIZES)
 def test_grad_sizes(dtype, k, n):
     torch, sr = mods()
