@@ -490,7 +490,10 @@ seg_status_t seg_matmul_grad_w(const void *x, seg_dtype_t dtype, int64_t num_row
  *   out           device, [num_rows, N], rows ldo elements apart.
  *
  * The inner products with a are kept in float32; the whole sum is rounded
- * once.  Alignment and numerics otherwise as for seg_matmul.
+ * once.  Infinities and NaN of an adapter in use reach the rows of its own
+ * requests alone, and there what IEEE arithmetic gives (float32 products with
+ * w and a: as for seg_matmul); a call in which there are any takes longer.
+ * Alignment and numerics otherwise as for seg_matmul.
  */
 #define SEG_MAX_RANK 128
 

@@ -70,6 +70,7 @@ constexpr int threads_of() { return TENSOR && PL == 1 ? (MODE == PRODUCT_ADAPTER
 // a run costs them a pass over the whole tile).
 constexpr int LOW_RUN = 16;
 constexpr int LOW_EVERY = 10;             // blocks of the sum between two of the low-rank part: about the time one takes to lay out
+constexpr int LOW_TILES = 4;              // barriers of tiles whose low-rank part is done: three can be before the first of them has been drained
 constexpr int NEVER_FLUSH = 1 << 28;         // more blocks than any sum has
 constexpr unsigned STATUS_PRODUCT_TIMEOUT = 8u;
 
@@ -84,7 +85,7 @@ struct Ring {
     static constexpr int STAGES = ALL_STAGES - (LOW ? 1 : 0);
     static constexpr bool ROW3 = PL == 3 && NT == 64;            // a part of A times several parts of B at once
     static constexpr int ACC = PL == 1 ? NT : 256;               // tensor-memory columns of one accumulator
-    static constexpr int BARS = 3 * STAGES + 7;
+    static constexpr int BARS = 3 * STAGES + 7 + LOW_TILES;
     // the drain warps' staging; PL == 3 keeps it (adapters alone need it there) in the space of the offsets
     static constexpr int STAGING = PL == 1 ? 2048 : 1024;
     static constexpr int STAGED = PL == 1 ? EPW * STAGING : 0;
@@ -703,6 +704,49 @@ __device__ __forceinline__ void ranks_of_b(const ProductParams& p, int l, int64_
         }
     }
 }
+// Two 16-bit values of b with 0 in the place of an infinity or NaN, whose exponent bits are all ones.
+__device__ __forceinline__ uint32_t finite_pair(uint32_t two, uint32_t exponent) {
+    return two & (((two & exponent) == exponent ? 0u : 0xffffu) | ((two >> 16 & exponent) == exponent ? 0u : 0xffff0000u));
+}
+__device__ __forceinline__ bool is_finite(float x) { return (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u; }
+
+// What finite_pair and its like kept out of the low-rank part of a tile, the
+// terms with an infinity or NaN in b or u, to their places: a pass of its own
+// over the accumulators after the tile's, and no part of the loop there, where
+// its registers would cost the calls that have no such terms.  The warp's
+// columns c0, c0 + STEP, .. W at a time, of lane column m; the sums go to
+// `part`, a part of a split tile, or to the result.
+template <int W, int STEP>
+__device__ __noinline__ void add_strange(const KernelArgs& a, uint32_t from, const int* tile_adapter, int row0, int columns, int c0, int64_t m,
+                                         bool in, float* part) {
+    const ProductParams& p = a.p;
+    const int rank = static_cast<int>(p.rank);
+    __syncwarp();
+    for (; c0 < columns; c0 += STEP) {
+        float d[W];
+        tmem_load(from + c0, d);
+        tmem_wait(d);
+#pragma unroll 1
+        for (int j = 0; j < W && c0 + j < columns; ++j) {
+            const int l = tile_adapter[c0 + j];
+            if (l < 0 || !in) continue;
+            const float* u = p.u + (int64_t(row0) + c0 + j) * rank;
+            const uint16_t* b = static_cast<const uint16_t*>(p.b) + (int64_t(l) * p.N + m) * rank;
+            float s = 0.0f, x = 0.0f;
+            for (int k = 0; k < rank; ++k) {
+                const float f = p.type == PT_BF16 ? __uint_as_float(static_cast<uint32_t>(b[k]) << 16) : __half2float(__ushort_as_half(b[k]));
+                if (!is_finite(u[k]) || !is_finite(f)) s = fmaf(u[k], f, s);
+            }
+            if (s == 0.0f) continue;
+#pragma unroll
+            for (int k = 0; k < W; ++k) x = k == j ? d[k] : x;
+            if (part) part[(c0 + j) * MT] = x + s;
+            else static_cast<uint16_t*>(p.out)[(int64_t(row0) + c0 + j) * p.ldo + m] = static_cast<uint16_t>(narrow_pair(x + s, 0.0f, p.out_type));
+        }
+        __syncwarp();
+    }
+}
+
 __device__ __forceinline__ void ranks_of_u(const ProductParams& p, bool in, int64_t row, int q, float (&f)[16]) {
     const int rank = static_cast<int>(p.rank), width = in ? rank - q : 0;
     const float* u = p.u + (width > 0 ? row * rank + q : 0);
@@ -728,13 +772,28 @@ __device__ __forceinline__ void ranks_of_u(const ProductParams& p, bool in, int6
 // parts (b, u) = (0, 0), (0, 1), (0, 2); float16 b has two parts: and (1, 0),
 // (1, 1); what is left out is below 2^-21.  A block's steps touch two groups
 // of 16 ranks at most, which are loaded together.
-__device__ __forceinline__ void lay_adapter(const ProductParams& p, int s0, int total, int pairs, int l, int64_t m, int row0, int base,
+// Every column of the tile meets this b, those outside the run with zeros, and
+// 0 times an infinity or NaN is NaN: such values of b (and of u, whose parts
+// would lose an infinity's sign) count as 0 here, and the drain warps add their
+// terms to the run's own rows.  Returns whether this thread found one.
+__device__ __forceinline__ bool lay_adapter(const ProductParams& p, int s0, int total, int pairs, int l, int64_t m, int row0, int base,
                                             int share, int row, int end, unsigned char* sa, unsigned char* sb, int tl) {
     const int j0 = s0 / pairs;
+    bool strange = false;
     {
         uint32_t raw[2][8];
 #pragma unroll
         for (int k = 0; k < 2; ++k) ranks_of_b(p, l, m, (j0 + k) * 16, raw[k]);
+        // the largest magnitude of each half tells
+        uint32_t most = 0;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) most = __vmaxu2(most, raw[k / 8][k % 8] & 0x7fff7fffu);
+        const uint32_t exponent = p.type == PT_F16 ? 0x7c00u : 0x7f80u;
+        if ((most & 0xffffu) >= exponent || most >> 16 >= exponent) {
+            strange = true;
+#pragma unroll
+            for (int k = 0; k < 16; ++k) raw[k / 8][k % 8] = finite_pair(raw[k / 8][k % 8], exponent);
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int s = s0 + i, second = s >= (j0 + 1) * pairs ? 1 : 0, pair = s - (j0 + second) * pairs;
@@ -761,6 +820,15 @@ __device__ __forceinline__ void lay_adapter(const ProductParams& p, int s0, int 
         float f[2][16];
 #pragma unroll
         for (int k = 0; k < 2; ++k) ranks_of_u(p, in, int64_t(row0) + base + r, (j0 + k) * 16, f[k]);
+        uint32_t most = 0;
+#pragma unroll
+        for (int k = 0; k < 32; ++k) most = max(most, __float_as_uint(f[k / 16][k % 16]) & 0x7fffffffu);
+        if (most >= 0x7f800000u) {
+            strange = true;
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+                if (!is_finite(f[k / 16][k % 16])) f[k / 16][k % 16] = 0.0f;
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int s = s0 + i, second = s >= (j0 + 1) * pairs ? 1 : 0, pair = s - (j0 + second) * pairs;
@@ -774,6 +842,7 @@ __device__ __forceinline__ void lay_adapter(const ProductParams& p, int s0, int 
             for (int k = 0; k < 2; ++k) *reinterpret_cast<uint4*>(sb + r * 128 + (((2 * i + k) ^ (r & 7)) << 4)) = v[k];
         }
     }
+    return strange;
 }
 
 // Whether the stage of a block already holds its A operand: with two stages
@@ -818,9 +887,11 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
     uint64_t* drain = acc_empty + 2;
     uint64_t* low_full = drain + 1;                // CG == 2: CTA 0's count
     uint64_t* low_empty = low_full + 1;
-    uint32_t* tmem_at = reinterpret_cast<uint32_t*>(low_empty + 1);
+    uint64_t* low_done = low_empty + 1;            // the low-rank warps of both CTAs are through with a tile
+    uint32_t* tmem_at = reinterpret_cast<uint32_t*>(low_done + LOW_TILES);
     int* low_steps = reinterpret_cast<int*>(tmem_at + 1);                // steps of 16 in the low-rank stage; + 8: the tile's last
     uint32_t* low_turns = reinterpret_cast<uint32_t*>(low_steps + 1);          // [8]: rows with another adapter than the one before
+    uint32_t* low_strange = tmem_at + 20;                        // infinities or NaN were kept out of a low-rank part
     int* tile_adapter = reinterpret_cast<int*>(tmem_at + 32);    // [NT], the drain warps'
     int* low_adapter = tile_adapter + NT;                        // [NT], the low-rank warps'
     if (PL > 1) staging = reinterpret_cast<unsigned char*>(near);
@@ -852,6 +923,8 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
         mbar_init(drain, 1);
         mbar_init(low_full, 4 * CG);
         mbar_init(low_empty, 1);
+        for (int i = 0; i < LOW_TILES; ++i) mbar_init(low_done + i, 4 * CG);
+        if (R::LOW) *low_strange = 0;
         fence_mbarrier_init();
         if (TENSOR) {
             tensor_prefetch(&map_a);
@@ -1066,12 +1139,13 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
             unsigned char* sa = stages + R::STAGES * R::STAGE;
             unsigned char* sb = sa + R::A_PLANE;
             const int pairs = p.type == PT_BF16 ? 3 : 5, total = static_cast<int>((p.rank + 15) / 16) * pairs;
-            uint32_t ph = 1;
+            uint32_t ph = 1, tiles = 0;
             bool ok = true;
             Item t;
             for (uint32_t i = first; ok && i < items; i += stride) {
                 item_at<MODE, NT, CG>(a, beg, pre, i, t);
                 if (t.kb1 <= t.kb0 || t.part != 0) continue;
+                bool found = false;                    // an infinity or NaN in the tile's low-rank part
                 for (int r = tl; r < t.rows; r += 128) low_adapter[r] = adapter_of(p, near_offsets, t.row0 + r);
                 bar_low();
                 int runs = 0;
@@ -1111,8 +1185,8 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                         last = runs == 0 && s0 + 4 >= total;
                         if (!mine) last = true;
                         if (mine) {
-                            lay_adapter(p, s0, total, pairs, l, t.m0 + rank * MT + tl, t.row0, rank * share_of(t.rows), share_of(t.rows),
-                                        row, end, sa, sb, tl);
+                            found |= lay_adapter(p, s0, total, pairs, l, t.m0 + rank * MT + tl, t.row0, rank * share_of(t.rows), share_of(t.rows),
+                                                 row, end, sa, sb, tl);
                         }
                         if (tl == 0) *low_steps = (mine ? min(4, total - s0) : 0) | (last ? 8 : 0);
                         fence_proxy_async_smem();
@@ -1121,6 +1195,14 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                     }
                     row = end;
                 } while (ok && !last);
+                found = __any_sync(0xffffffffu, found);
+                if (lane == 0) {
+                    // (u's rows are this CTA's share, and the drain warps of both need them)
+                    if (found) *reinterpret_cast<volatile uint32_t*>(low_strange) = 1;
+                    if (CG == 2 && found) cluster_store(cluster_addr(low_strange, in_cluster ^ 1), 1);
+                    arrive_both<CG>(low_done + tiles % LOW_TILES, lead, found);
+                }
+                ++tiles;
                 bar_low();        // the table has been read
             }
         }
@@ -1237,6 +1319,7 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
         // copies and multiplies meanwhile
         bool u_there = MODE != PRODUCT_ADAPTERS;
         uint32_t buf = 0, bph = 0;
+        [[maybe_unused]] uint32_t low_tiles = 0;
         Item t;
         for (uint32_t i = first; i < items; i += stride) {
             item_at<MODE, NT, CG>(a, beg, pre, i, t);
@@ -1300,7 +1383,7 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                         break;       // one piece: 16-bit results take the sums as they are
                     }
                 }
-                bool waiting = summed;
+                bool waiting = summed, strange = false;
                 const int stride_c = twin ? 2 * ROWS : ROWS;
                 int c = lanes > 0 ? (twin ? group + (quarter & 2) : group) * W : n_left;
                 float d[W], lo[W];       // the accumulators' next columns
@@ -1319,11 +1402,18 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                         if (final && scattered && c < n_left && c / ROWS % t.parts == t.part) low.rows_of(v, c, c + ROWS * t.parts);
                     if (waiting) {
                         // (where the drain warps meet at barriers, they give up together)
-                        if (MODE == PRODUCT_ADAPTERS) ok = bar_drain_all(wait_for<CG>(acc_full + buf, bph, p.status));
+                        const bool low_part = R::LOW && final && p.u && t.part == 0;
+                        if (MODE == PRODUCT_ADAPTERS)
+                            ok = bar_drain_all((!low_part || wait_for<CG>(low_done + low_tiles % LOW_TILES, low_tiles / LOW_TILES & 1, p.status)) && wait_for<CG>(acc_full + buf, bph, p.status));
                         else ok = warp_wait<CG>(acc_full + buf, bph, p.status);
                         if (!ok) break;
                         tc_fence_after();
                         waiting = false;
+                        // (once set, low_strange stays: a later tile then looks for terms that it may not have)
+                        if (low_part) {
+                            ++low_tiles;
+                            strange = !scattered && *reinterpret_cast<volatile uint32_t*>(low_strange) != 0;
+                        }
                         if (AHEAD && c < n_left) load(c);
                     }
                     if (c >= n_left) break;
@@ -1369,6 +1459,11 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                     if (c >= n_left) break;
                 }
                 if (!ok) break;
+                if constexpr (R::LOW) {
+                    if (strange && lanes > 0)
+                        add_strange<W, ROWS>(a, from, tile_adapter, t.row0, n_left, group * W, m + lane, lane < lanes,
+                                             partial ? cluster_part + quarter * 32 + lane : nullptr);
+                }
                 if (summed) {
                     tc_fence_before();
                     __syncwarp();

@@ -61,6 +61,10 @@ __device__ __forceinline__ float cluster_load(uint32_t addr) {
     return v;
 }
 
+__device__ __forceinline__ void cluster_store(uint32_t addr, uint32_t v) {
+    asm volatile("st.relaxed.cluster.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
 template <int CG>
 __device__ __forceinline__ uint32_t lead_addr(const void* p, uint32_t lead) {
     return CG == 2 ? cluster_addr(p, lead) : smem_u32(p);
@@ -80,6 +84,13 @@ __device__ __forceinline__ void lead_arrive(uint64_t* bar, uint32_t lead, bool m
 }
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// One arrival at this barrier in each CTA of the pair (`memory`: as above).
+template <int CG>
+__device__ __forceinline__ void arrive_both(uint64_t* bar, uint32_t lead, bool memory) {
+    lead_arrive<CG>(bar, lead, memory);
+    if (CG == 2) lead_arrive<CG>(bar, lead + 1, memory);
 }
 
 // One box of a 2-D / 3-D tensor into this CTA's shared memory; zero where the
