@@ -1714,6 +1714,8 @@ bool tensor_copyable(const void* base, int64_t stride, int type) {
 
 template <int MODE, bool TENSOR, int NT, int PL, int CG>
 cudaError_t launch_shape(const KernelArgs& a, const ProductPlan& plan, cudaStream_t stream) {
+    // (a plan for other tiles would leave rows out)
+    if (NT != product_tile_columns(a.p, plan)) return cudaErrorInvalidConfiguration;
     CUtensorMap ma{}, mb{};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -1803,8 +1805,6 @@ cudaError_t launch_mode(const KernelArgs& a, const ProductPlan& plan, cudaStream
     return plan.pair ? launch_shape<MODE, true, 256, 1, 2>(a, plan, stream) : launch_shape<MODE, true, 256, 1, 1>(a, plan, stream);
 }
 
-int tile_columns(const ProductParams& p, bool narrow) { return narrow ? 64 : (p.type == PT_F32 ? 128 : 256); }
-
 }  // namespace
 
 namespace {
@@ -1822,6 +1822,8 @@ MatShape w_shape(int mode, const ProductParams& p) {
 int64_t packed_row(int64_t cols, int type) { return ceil_to(cols * (type == PT_F32 ? 4 : 2), 16) * 16; }   // bytes
 
 }  // namespace
+
+int product_tile_columns(const ProductParams& p, const ProductPlan& plan) { return plan.narrow ? 64 : (p.type == PT_F32 ? 128 : 256); }
 
 ProductPlan plan_product(int mode, const ProductParams& p) {
     ProductPlan d{};
@@ -1842,9 +1844,9 @@ ProductPlan plan_product(int mode, const ProductParams& p) {
     }
     d.tensor = !d.empty && (copy_x || d.pack_x) && (copy_w || d.pack_w);
     // few rows per segment, or too few tiles to go round: small tiles and a
-    // deeper ring; weights: few columns of x
-    d.narrow = weights ? p.K <= 64 : p.R <= 64 * segments || (p.N <= MT && p.R <= 128 * p.sms);
-    const int NT = tile_columns(p, d.narrow);
+    // deeper ring; weights: few columns of x.  The loader warps have small tiles alone.
+    d.narrow = !d.tensor || (weights ? p.K <= 64 : p.R <= 64 * segments || (p.N <= MT && p.R <= 128 * p.sms));
+    const int NT = product_tile_columns(p, d);
     // two CTAs on a tile of twice the lanes, unless that leaves one of them without lanes
     // or so few tiles that their sums are split
     d.pair = d.tensor && p.type != PT_F32 && !d.narrow && (p.N > 1024 || ceil_to(p.N, MT) % 2 == 0);

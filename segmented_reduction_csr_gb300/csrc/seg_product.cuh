@@ -44,7 +44,7 @@ struct ProductPlan {
     int32_t grid;
     int32_t too_many;       // 1: more tiles than 31 bits count
     int32_t tensor;         // 1: operands come by tensor copies, 0: by the loader warps
-    int32_t narrow;         // 1: at most 64 rows per tile and a deeper ring
+    int32_t narrow;         // 1: at most 64 rows per tile and a deeper ring (always without tensor copies)
     int32_t pair;           // 1: two CTAs share a tile
     int32_t empty;          // 1: no sum has a term
     int32_t pack_x, pack_w; // 1: the operand is first laid out in 16-byte aligned rows
@@ -61,6 +61,8 @@ struct ProductPlan {
 enum : int { PRODUCT_FORWARD = 0, PRODUCT_WEIGHTS = 1, PRODUCT_ADAPTERS = 2 };
 
 ProductPlan plan_product(int mode, const ProductParams& p);
+// Columns of the tile that `plan` counts in and that is launched for it.
+int product_tile_columns(const ProductParams& p, const ProductPlan& plan);
 cudaError_t launch_product(int mode, const ProductParams& p, const ProductPlan& plan, cudaStream_t stream);
 
 // u of the adapters (forward with index, rank columns, float32 result) for
