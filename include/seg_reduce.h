@@ -427,13 +427,14 @@ seg_status_t seg_flags_to_offsets(const uint8_t *flags, int64_t n, int64_t *offs
  * are in no use.  w may hold any values for empty segments, and x for rows in
  * no segment (NaN and infinities included): neither reaches the output.
  *
- * Scratch is the library's, one buffer per (device, stream) for all products:
- * those copies (and 8 bytes per segment above 1,024) for seg_matmul, also up
+ * Scratch is the library's, one buffer per (device, stream) for all products.
+ * It takes those copies (and 8 bytes per segment above 1,024) for seg_matmul, also up
  * to about 0.5 GB of float32 partial sums for seg_matmul_grad_w (few columns, many rows), num_rows * rank
  * float32 values for seg_lora.  It is allocated (cudaMalloc) when a call needs
- * more than the calls before on its stream, and kept.  Captured into a graph,
- * a call keeps using the scratch of the stream that it was captured from:
- * replays must not overlap other products on that stream.
+ * more than the calls before on its stream, and kept.  Calls that are captured
+ * into a graph have scratch of that graph's own, so its replays may overlap
+ * other products and other graphs on any stream; it is used again when the
+ * graph and what was instantiated from it have been destroyed.
  * Enqueues one to four kernel launches and returns without synchronising.
  *
  * Numerics.  Sums are float32 in an order that is a pure function of the

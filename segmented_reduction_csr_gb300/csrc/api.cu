@@ -61,9 +61,7 @@ std::map<std::pair<int, cudaStream_t>, Scratch> g_scratch;
 // buffer of their own per (device, stream), so that the reduction it runs
 // keeps its scratch (and its ticket words) to itself.
 std::map<std::pair<int, cudaStream_t>, Scratch> g_sort_scratch;
-// The products' scratch: a buffer of their own per (device, stream).  A graph
-// captured from a stream holds its address, so a buffer that has become too
-// small is kept beside the larger one (each is at least twice the one before).
+// The products' scratch: a buffer of their own per (device, stream).
 std::map<std::pair<int, cudaStream_t>, Scratch> g_product_scratch;
 
 seg_status_t device_state(int dev, DeviceState** out) {
@@ -115,9 +113,104 @@ seg_status_t scratch_for(int dev, cudaStream_t stream, size_t bytes, Scratch** o
     return scratch_in(g_scratch, dev, stream, bytes, out);
 }
 
-// Scratch of the products: ordinary device memory, allocated outside of any
-// capture of `stream` (a buffer that a capture allocates belongs to its graph).
+// ---------------------------------------------------------------------------
+// Scratch of products that are captured into a graph.  The graph keeps its
+// address and may be replayed on any stream, beside other graphs that were
+// captured from the same one, so every capture has buffers of its own: one
+// per stream of the capture (whose calls follow one another in the graph too).
+// They are ordinary device memory, and go back to a list of free ones when
+// the graph and what was instantiated from it are gone.
+
+struct GraphBuffer {
+    int dev;
+    size_t bytes;
+    void* ptr;
+    GraphBuffer* next;      // in the list of free ones
+};
+std::mutex g_free_mu;       // of the list alone: a graph may give a buffer back during any call of the runtime
+GraphBuffer* g_free_buffers = nullptr;
+
+void CUDART_CB give_back(void* buffer) {
+    GraphBuffer* b = static_cast<GraphBuffer*>(buffer);
+    std::lock_guard<std::mutex> lock(g_free_mu);
+    b->next = g_free_buffers;
+    g_free_buffers = b;
+}
+
+// The smallest free buffer of at least `bytes`, and at most four times as many; NULL: none.
+GraphBuffer* take_free(int dev, size_t bytes) {
+    std::lock_guard<std::mutex> lock(g_free_mu);
+    GraphBuffer** best = nullptr;
+    for (GraphBuffer** b = &g_free_buffers; *b; b = &(*b)->next)
+        if ((*b)->dev == dev && (*b)->bytes >= bytes && (*b)->bytes / 4 <= bytes && (!best || (*b)->bytes < (*best)->bytes)) best = b;
+    if (!best) return nullptr;
+    GraphBuffer* b = *best;
+    *best = b->next;
+    return b;
+}
+
+struct CaptureScratch {
+    unsigned long long id = 0;      // of the capture
+    Scratch sc;
+};
+std::map<std::pair<int, cudaStream_t>, CaptureScratch> g_capture_scratch;
+
+seg_status_t capture_scratch(int dev, cudaStream_t stream, unsigned long long id, cudaGraph_t graph, size_t bytes, Scratch** out) {
+    CaptureScratch& cs = g_capture_scratch[std::make_pair(dev, stream)];
+    if (cs.id != id) {
+        cs.sc = Scratch();
+        cs.id = id;
+    }
+    if (cs.sc.bytes < bytes) {      // (a smaller one stays with the calls before)
+        const size_t want = std::max<size_t>(bytes, size_t(1) << 20);
+        GraphBuffer* b = take_free(dev, want);
+        if (!b) {
+            b = new GraphBuffer{dev, want, nullptr, nullptr};
+            // outside of the capture: what a capture allocates comes and goes with each replay
+            cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+            cudaError_t e = cudaThreadExchangeStreamCaptureMode(&mode);
+            if (e == cudaSuccess) {
+                e = cudaMalloc(&b->ptr, want);
+                cudaThreadExchangeStreamCaptureMode(&mode);
+            }
+            if (e != cudaSuccess) {
+                cudaGetLastError();
+                delete b;
+                return SEG_ERR_OUT_OF_MEMORY;
+            }
+        }
+        cudaUserObject_t owner;
+        cudaError_t e = cudaUserObjectCreate(&owner, b, give_back, 1, cudaUserObjectNoDestructorSync);
+        if (e == cudaSuccess) {
+            e = cudaGraphRetainUserObject(graph, owner, 1, cudaGraphUserObjectMove);
+            if (e != cudaSuccess) cudaUserObjectRelease(owner, 1);      // gives it back
+        } else {
+            give_back(b);
+        }
+        if (e != cudaSuccess) {
+            cudaGetLastError();
+            return SEG_ERR_CUDA;
+        }
+        cs.sc.ptr = b->ptr;
+        cs.sc.bytes = b->bytes;
+    }
+    *out = &cs.sc;
+    return SEG_OK;
+}
+
+// Scratch of the products on `stream`, for what is enqueued or captured next.
 seg_status_t product_scratch(int dev, cudaStream_t stream, size_t bytes, Scratch** out) {
+    cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+    unsigned long long id = 0;
+    cudaGraph_t graph = nullptr;
+    if (cudaStreamGetCaptureInfo(stream, &status, &id, &graph, nullptr, nullptr, nullptr) != cudaSuccess) {
+        cudaGetLastError();
+        return SEG_ERR_CUDA;
+    }
+    if (status != cudaStreamCaptureStatusNone) {
+        if (status != cudaStreamCaptureStatusActive) return SEG_ERR_CUDA;      // a capture that has become invalid
+        return capture_scratch(dev, stream, id, graph, bytes, out);
+    }
     Scratch& sc = g_product_scratch[std::make_pair(dev, stream)];
     if (sc.bytes < bytes) {
         const size_t want = std::max(std::max<size_t>(bytes, size_t(1) << 20), 2 * sc.bytes);
