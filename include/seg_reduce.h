@@ -428,13 +428,15 @@ seg_status_t seg_flags_to_offsets(const uint8_t *flags, int64_t n, int64_t *offs
  * no segment (NaN and infinities included): neither reaches the output.
  *
  * Scratch is the library's, one buffer per (device, stream) for all products.
- * It takes those copies (and 8 bytes per segment above 1,024) for seg_matmul, also up
- * to about 0.5 GB of float32 partial sums for seg_matmul_grad_w (few columns, many rows), num_rows * rank
- * float32 values for seg_lora.  It is allocated (cudaMalloc) when a call needs
- * more than the calls before on its stream, and kept.  Calls that are captured
- * into a graph have scratch of that graph's own, so its replays may overlap
- * other products and other graphs on any stream; it is used again when the
- * graph and what was instantiated from it have been destroyed.
+ * It takes those copies (and 8 bytes per segment above 1,024) for seg_matmul,
+ * also up to about 0.5 GB of float32 partial sums for seg_matmul_grad_w (few
+ * columns, many rows), num_rows * rank float32 values for seg_lora.  It is
+ * allocated (cudaMallocAsync) when a call needs more than the calls before on
+ * its stream, in the place of the smaller buffer and with up to 256 MB to spare
+ * where there is memory for it, and kept.  Calls that are captured into a graph
+ * have scratch of that graph's own, so its replays may overlap other products
+ * and other graphs on any stream; it is used again when the graph and what was
+ * instantiated from it have been destroyed.
  * Enqueues one to four kernel launches and returns without synchronising.
  *
  * Numerics.  Sums are float32 in an order that is a pure function of the

@@ -17,6 +17,7 @@
 #include "seg_rle.cuh"
 #include "seg_scan.cuh"
 #include "seg_scatter.cuh"
+#include "seg_scratch.cuh"
 #include "seg_seq.cuh"
 #include "seg_sort.cuh"
 
@@ -46,12 +47,6 @@ struct DeviceState {
     int sm_count = 0;
     unsigned int* status = nullptr;
     std::map<const void*, bool> configured;
-};
-
-struct Scratch {
-    void* ptr = nullptr;
-    size_t bytes = 0;
-    uint32_t gen = 0;
 };
 
 std::mutex g_mu;
@@ -212,23 +207,16 @@ seg_status_t product_scratch(int dev, cudaStream_t stream, size_t bytes, Scratch
         return capture_scratch(dev, stream, id, graph, bytes, out);
     }
     Scratch& sc = g_product_scratch[std::make_pair(dev, stream)];
-    if (sc.bytes < bytes) {
-        const size_t want = std::max(std::max<size_t>(bytes, size_t(1) << 20), 2 * sc.bytes);
-        cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
-        if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) return SEG_ERR_CUDA;
-        void* ptr = nullptr;
-        const cudaError_t e = cudaMalloc(&ptr, want);
-        cudaThreadExchangeStreamCaptureMode(&mode);
-        if (e != cudaSuccess) {
+    const bool there = grow_scratch(
+        sc, bytes,
+        [stream](void** ptr, size_t want) {
+            if (cudaMallocAsync(ptr, want, stream) == cudaSuccess) return true;
             cudaGetLastError();
-            return SEG_ERR_OUT_OF_MEMORY;
-        }
-        sc.ptr = ptr;
-        sc.bytes = want;
-        sc.gen = 0;
-    }
+            return false;
+        },
+        [stream](void* ptr) { cudaFreeAsync(ptr, stream); });
     *out = &sc;
-    return SEG_OK;
+    return there ? SEG_OK : SEG_ERR_OUT_OF_MEMORY;
 }
 
 // ---------------------------------------------------------------------------
