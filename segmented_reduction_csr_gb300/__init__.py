@@ -574,9 +574,13 @@ def flags_to_offsets(flags):
     return offsets[:int(count.item()) + 1]
 
 
-# The products' calls are short (a decode step's kernel takes 8 us), so their
+# The products' calls are short (one token's kernel takes 9 us), so their
 # host side is kept so: types and the raw-stream function are looked up once,
 # and the device guard is entered only where the device changes.
+#
+# Their ``stream`` argument: the work is enqueued there and is not ordered
+# with the current stream's by the call.  A fresh result is memory of that
+# stream, and the tensors' memory stays theirs until it is through with them.
 
 _product_types = None
 
@@ -624,6 +628,23 @@ def _same(name, t, like, shape, dtype=None):
         raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
 
 
+def _fresh(shape, dtype, device, stream):
+    """A product's new result on ``stream``, in memory of that stream: what the
+    current one last did with a block of its own need not be over by then."""
+    torch = _torch()
+    with torch.cuda.stream(stream):
+        out = torch.empty(shape, dtype=dtype, device=device)
+    out.record_stream(torch.cuda.current_stream(device))
+    return out
+
+
+def _in_use(stream, *tensors):
+    """Memory that ``stream`` reads or writes is not given to others before it is through, though its tensors go."""
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+
+
 def _enqueue(where, device, stream, fn, *args):
     """Calls a product of the library on ``stream`` (default: ``device``'s current one)."""
     torch = _torch()
@@ -652,6 +673,7 @@ def seg_matmul(x, w, offsets, transpose_w: bool = False, out=None, stream=None):
     and are rounded once to ``x``'s type.  The gradient of ``x`` is
     ``seg_matmul(dy, w, offsets, not transpose_w)``, that of ``w``
     ``seg_matmul_grad_w``.  Not synchronised."""
+    torch = _torch()
     ldx = _check_rows("x", x, offsets)
     code, s, (r, k) = _product_code(x), offsets.shape[0] - 1, x.shape
     if w.dim() != 3:
@@ -660,7 +682,7 @@ def seg_matmul(x, w, offsets, transpose_w: bool = False, out=None, stream=None):
     _same("w", w, x, (s, n, k) if transpose_w else (s, k, n))
     ldw = _row_stride("w", w)
     if out is None:
-        out = _torch().empty((r, n), dtype=x.dtype, device=x.device)
+        out = torch.empty((r, n), dtype=x.dtype, device=x.device) if stream is None else _fresh((r, n), x.dtype, x.device, stream)
         ldo = max(n, 1)
     else:
         _same("out", out, x, (r, n))
@@ -668,6 +690,8 @@ def seg_matmul(x, w, offsets, transpose_w: bool = False, out=None, stream=None):
     _enqueue("seg_matmul", x.device, stream, load_library().seg_matmul,
              x.data_ptr() or None, code, r, k, ldx, w.data_ptr() or None, n, ldw, w.stride(0) if s > 1 else 0,
              1 if transpose_w else 0, offsets.data_ptr(), _offset_code(offsets), s, out.data_ptr() or None, ldo)
+    if stream is not None:
+        _in_use(stream, x, w, offsets, out)
     return out
 
 
@@ -691,7 +715,7 @@ def seg_matmul_grad_w(x, dy, offsets, out_dtype=None, out=None, stream=None):
     if out_dtype not in (x.dtype, torch.float32):
         raise TypeError(f"out_dtype must be {x.dtype} or torch.float32, not {out_dtype}")
     if out is None:
-        out = torch.empty((s, k, n), dtype=out_dtype, device=x.device)
+        out = torch.empty((s, k, n), dtype=out_dtype, device=x.device) if stream is None else _fresh((s, k, n), out_dtype, x.device, stream)
     else:
         _same("out", out, x, (s, k, n), out_dtype)
         if not out.is_contiguous():
@@ -699,6 +723,8 @@ def seg_matmul_grad_w(x, dy, offsets, out_dtype=None, out=None, stream=None):
     _enqueue("seg_matmul_grad_w", x.device, stream, load_library().seg_matmul_grad_w,
              x.data_ptr() or None, code, x.shape[0], k, ldx, dy.data_ptr() or None, n, ldy, offsets.data_ptr(),
              _offset_code(offsets), s, out.data_ptr() or None, SEG_F32 if out_dtype == torch.float32 else code)
+    if stream is not None:
+        _in_use(stream, x, dy, offsets, out)
     return out
 
 
@@ -765,7 +791,7 @@ def seg_lora(x, w, a, b, offsets, adapter, scale=None, out=None, stream=None):
             raise ValueError(f"{name} must be contiguous")
     ldw = _row_stride("w", w)
     if out is None:
-        out = torch.empty((r, n), dtype=x.dtype, device=x.device)
+        out = torch.empty((r, n), dtype=x.dtype, device=x.device) if stream is None else _fresh((r, n), x.dtype, x.device, stream)
         ldo = max(n, 1)
     else:
         _same("out", out, x, (r, n))
@@ -774,6 +800,8 @@ def seg_lora(x, w, a, b, offsets, adapter, scale=None, out=None, stream=None):
              x.data_ptr() or None, code, r, k, ldx, w.data_ptr() or None, n, ldw, a.data_ptr() or None,
              b.data_ptr() or None, count, rank, offsets.data_ptr(), _offset_code(offsets), s,
              adapter.data_ptr() or None, _ptr(scale) or None, out.data_ptr() or None, ldo)
+    if stream is not None:
+        _in_use(stream, x, w, a, b, offsets, adapter, scale, out)
     return out
 
 
