@@ -36,11 +36,14 @@
 // float32: every value is split into three bfloat16 parts by truncation (8 + 8
 // + 8 bits, exact) and six of the nine part products are accumulated; the
 // other three are below 2^-21 of the whole.
-// The tensor cores cut what an addition shifts out of the accumulator (a bias
-// of about 2^-26 of it per 16 steps, measured), so for float32 the five small
-// part products have accumulators of their own, and where the result is
-// float32 the accumulators are added to it, rounded, every 512 (float32) or
-// 768 (16-bit operands) steps: the bias then stays below 1e-6.
+// The tensor cores cut what an addition shifts out of the accumulator: a sum of
+// one sign loses about 2^-23.4 of it per 16 steps of full products, less while
+// short products still fit (measured).  So for float32 the five small part
+// products have accumulators of their own, and where the result is float32 the
+// accumulators are added to it, rounded, every 512 (float32) or 768 (16-bit
+// operands) steps: a sum of one sign is then low by 0.8e-6 (float32; 1.9e-6 where
+// a part of 1,024 steps is not flushed), 1.3e-6 (bfloat16) or 4.4e-6 (float16).
+// 16-bit results: LONGEST.
 // Long sums with few tiles are cut into parts, added in order.  Forward: the
 // parts of a tile are a cluster and add through its shared memory.  Weights,
 // whose segments can have hundreds of parts: float32 partials in scratch, and
@@ -72,6 +75,12 @@ constexpr int LOW_RUN = 16;
 constexpr int LOW_EVERY = 10;             // blocks of the sum between two of the low-rank part: about the time one takes to lay out
 constexpr int LOW_TILES = 4;              // barriers of tiles whose low-rank part is done: three can be before the first of them has been drained
 constexpr int NEVER_FLUSH = 1 << 28;         // more blocks than any sum has
+// Steps that 16-bit results and the adapters' inner products sum up in one
+// accumulator.  Its additions cut what they shift out, less than 2^-23 of it
+// twice per 16 steps: 2^-11 of a sum of one sign at most (2e-4 measured at this
+// length; 1,048,576 steps were off by 6e-3), which a float16 result's own
+// rounding covers.  Longer sums are added up from pieces, rounded, in float32.
+constexpr int64_t LONGEST = 32768;
 constexpr unsigned STATUS_PRODUCT_TIMEOUT = 8u;
 
 // Stage ring of a kernel shape: PL 16-bit planes per operand, CG CTAs that share a tile.
@@ -103,6 +112,7 @@ struct KernelArgs {
     int32_t twin;       // at most 64 lanes, laid out twice: the drain warps of the second 64 share the first's work
     int32_t wide_rows;  // 16-bit results: 16-byte stores fit
     int32_t flush;      // blocks of the sum after which the accumulators go to the result
+    int32_t add_by_start;
     int64_t chunk, row_tiles, cols_m, cols_n;   // cols_*: extent of the tile dimensions (forward: cols_n unused)
     int* far;          // offsets and tile prefix of more than NEAR_SEGMENTS segments
     float* partials;
@@ -741,6 +751,7 @@ __device__ __noinline__ void add_strange(const KernelArgs& a, uint32_t from, con
 #pragma unroll
             for (int k = 0; k < W; ++k) x = k == j ? d[k] : x;
             if (part) part[(c0 + j) * MT] = x + s;
+            else if (p.out_type == PT_F32) static_cast<float*>(p.out)[(int64_t(row0) + c0 + j) * p.ldo + m] += s;     // with the pieces before
             else static_cast<uint16_t*>(p.out)[(int64_t(row0) + c0 + j) * p.ldo + m] = static_cast<uint16_t>(narrow_pair(x + s, 0.0f, p.out_type));
         }
         __syncwarp();
@@ -1516,46 +1527,71 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
 }
 
 // Adds the parts of the split segments of the weights' product: a block per
-// tile of a segment (blockIdx.x) and four of its columns; warps w and w + 4
-// each add half of a column's parts, in order, and then the halves.
+// tile of a segment (blockIdx.x) and four of its columns at a time; warps w and
+// w + 4 each add half of a column's parts, in order, and then the halves.
+// Where there are more than twice as many segments as chunks of rows, a block
+// stands for a chunk instead: one split segment at most starts in it, and no
+// other segment after that one.  The search for it takes a few microseconds:
+// 1.5 times as many, 100,000 x 64 float16, 20.0 us so and 18.5 by segments; 2.6
+// times, 200,000 rows, 33.4 and 35.1.
 constexpr int ADD_COLS = 4;
+
+// The last segment that starts before `limit`, by all 256 threads of the block, or -1.
+__device__ __forceinline__ int64_t last_before(const ProductParams& p, int64_t limit) {
+    int64_t lo = 0, hi = p.S;
+    do {
+        const int64_t step = (hi - lo + 255) / 256, s = lo + threadIdx.x * step;
+        const int count = __syncthreads_count(s < hi && offset_at(p, s) < limit);
+        if (count == 0) return -1;
+        lo += (count - 1) * step;
+        hi = min(hi, lo + step);
+    } while (hi - lo > 1);
+    return lo;
+}
 
 template <int NT, int CG>
 __global__ void __launch_bounds__(256) add_parts_kernel(const __grid_constant__ KernelArgs a) {
     __shared__ float4 half_sum[ADD_COLS][32];
     const ProductParams& p = a.p;
     const int per = a.mtiles * a.ntiles, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t s = blockIdx.x / per;
-    const int r = static_cast<int>(blockIdx.x - s * per);
+    const int64_t item = blockIdx.x / per;
+    const int r = static_cast<int>(blockIdx.x - item * per);
+    const int64_t s = a.add_by_start ? last_before(p, (item + 1) * a.chunk) : item;
+    if (s < 0) return;
     const int64_t b = offset_at(p, s), e = offset_at(p, s + 1);
-    if (e - b <= a.chunk) return;
+    if (e - b <= a.chunk || (a.add_by_start && b / a.chunk != item)) return;
     const int parts = static_cast<int>((e - b + a.chunk - 1) / a.chunk), half = (parts + 1) / 2;
     const int rank = blockIdx.z;
     const int64_t m = (r % a.mtiles * CG + rank) * MT + lane * 4;
-    const int n0 = r / a.mtiles * NT, c = blockIdx.y * ADD_COLS + (warp & 3);
-    const bool in = m < a.cols_m && n0 + c < a.cols_n && c < NT;
+    const int n0 = r / a.mtiles * NT, columns = static_cast<int>(a.cols_n - n0 < NT ? a.cols_n - n0 : NT);
     const int q0 = warp < 4 ? 0 : half, q1 = warp < 4 ? half : parts;
     const int64_t j = b / a.chunk;
-    float4 v = make_float4(0, 0, 0, 0);
-    if (in) {
+    for (int c0 = blockIdx.y * ADD_COLS; c0 < columns; c0 += gridDim.y * ADD_COLS) {
+        const int c = c0 + (warp & 3);
+        const bool in = m < a.cols_m && c < columns;
+        float4 v = make_float4(0, 0, 0, 0);
+        if (in) {
 #pragma unroll 8
-        for (int q = q0; q < q1; ++q) {
-            const int64_t slot = (2 * (j + q) + (q == 0 ? 1 : 0)) * per + r;
-            const float4 x = __ldcg(reinterpret_cast<const float4*>(a.partials + ((slot * CG + rank) * NT + c) * MT) + lane);
-            v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+            for (int q = q0; q < q1; ++q) {
+                const int64_t slot = (2 * (j + q) + (q == 0 ? 1 : 0)) * per + r;
+                const float4 x = __ldcg(reinterpret_cast<const float4*>(a.partials + ((slot * CG + rank) * NT + c) * MT) + lane);
+                v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+            }
         }
-    }
-    if (warp >= 4) half_sum[warp - 4][lane] = v;
-    __syncthreads();
-    if (warp >= 4 || !in) return;
-    const float4 x = half_sum[warp][lane];
-    const float f[4] = {v.x + x.x, v.y + x.y, v.z + x.z, v.w + x.w};
-    const int64_t at = (s * a.cols_n + n0 + c) * a.cols_m + m;
-    for (int i = 0; i < 4; ++i) {
-        if (m + i >= a.cols_m) break;
-        if (p.out_type == PT_F32) static_cast<float*>(p.out)[at + i] = f[i];
-        else if (p.out_type == PT_F16) static_cast<__half*>(p.out)[at + i] = __float2half_rn(f[i]);
-        else static_cast<__nv_bfloat16*>(p.out)[at + i] = __float2bfloat16_rn(f[i]);
+        if (warp >= 4) half_sum[warp - 4][lane] = v;
+        __syncthreads();
+        if (warp < 4 && in) {
+            const float4 x = half_sum[warp][lane];
+            const float f[4] = {v.x + x.x, v.y + x.y, v.z + x.z, v.w + x.w};
+            const int64_t at = (s * a.cols_n + n0 + c) * a.cols_m + m;
+            for (int i = 0; i < 4; ++i) {
+                if (m + i >= a.cols_m) break;
+                if (p.out_type == PT_F32) static_cast<float*>(p.out)[at + i] = f[i];
+                else if (p.out_type == PT_F16) static_cast<__half*>(p.out)[at + i] = __float2half_rn(f[i]);
+                else static_cast<__nv_bfloat16*>(p.out)[at + i] = __float2bfloat16_rn(f[i]);
+            }
+        }
+        __syncthreads();
     }
 }
 
@@ -1591,6 +1627,16 @@ __global__ void __launch_bounds__(256) pack_kernel(const __grid_constant__ PackA
             for (int i = 0; i < V; ++i) x.v[i] = c + i < a.cols ? __ldg(src + c + i) : T(0);
             *reinterpret_cast<uint4*>(a.dst + r * a.row_bytes + c * static_cast<int64_t>(sizeof(T))) = x.u;
         }
+    }
+}
+
+// Float32 rows of whole sums, rounded to the result.
+template <class T>
+__global__ void __launch_bounds__(256) round_kernel(const float* src, T* out, int64_t rows, int64_t cols, int64_t ldo) {
+    const int64_t step = int64_t(gridDim.x) * 256;
+    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < rows * cols; i += step) {
+        const int64_t r = i / cols;
+        out[r * ldo + (i - r * cols)] = static_cast<T>(src[i]);
     }
 }
 
@@ -1787,8 +1833,9 @@ cudaError_t launch_shape(const KernelArgs& a, const ProductPlan& plan, cudaStrea
     e = cudaLaunchKernelEx(&cfg, kernel, a, ma, mb);
     if (e != cudaSuccess || plan.add_blocks == 0) return e;
     if constexpr (MODE == PRODUCT_WEIGHTS) {
-        const int64_t cols = std::min<int64_t>(a.cols_n, NT);
-        add_parts_kernel<NT, CG><<<dim3(plan.add_blocks, static_cast<unsigned>(ceil_to(cols, ADD_COLS)), CG), 256, 0, stream>>>(a);
+        // (most blocks of chunks find no split segment, so there are few of them, which take several columns)
+        const int64_t cols = ceil_to(std::min<int64_t>(a.cols_n, NT), ADD_COLS);
+        add_parts_kernel<NT, CG><<<dim3(plan.add_blocks, static_cast<unsigned>(a.add_by_start ? std::min<int64_t>(cols, 8) : cols), CG), 256, 0, stream>>>(a);
         e = cudaGetLastError();
     }
     return e;
@@ -1863,13 +1910,14 @@ ProductPlan plan_product(int mode, const ProductParams& p) {
         const int64_t per = int64_t(d.mtiles) * d.ntiles;
         // parts of at least so many rows that storing a part costs a fraction of them
         const int64_t least = 8 * std::min<int64_t>(p.K, NT);
-        if (segments * per * cg < 8 * p.sms) {
-            const int64_t chunk = std::max(least, ceil_to(ceil_to(p.R * per * cg, 4 * p.sms), KB) * KB);
-            if (chunk < p.R) {
-                d.chunk = chunk;
-                d.add_blocks = static_cast<int32_t>(segments * per);
-                slots = 2 * (p.R / chunk + 1) * per;
-            }
+        int64_t chunk = d.chunk;
+        if (segments * per * cg < 8 * p.sms) chunk = std::max(least, ceil_to(ceil_to(p.R * per * cg, 4 * p.sms), KB) * KB);
+        if (p.out_type != PT_F32) chunk = std::min(chunk, LONGEST);
+        if (chunk < p.R) {
+            d.chunk = chunk;
+            d.add_by_start = segments > 2 * (p.R / chunk + 1);
+            d.add_blocks = static_cast<int32_t>(std::min((d.add_by_start ? p.R / chunk + 1 : segments) * per, int64_t(INT32_MAX)));      // (more: too_many below)
+            slots = 2 * (p.R / chunk + 1) * per;
         }
         items = (segments + p.R / d.chunk) * per;
     } else {
@@ -1879,7 +1927,7 @@ ProductPlan plan_product(int mode, const ProductParams& p) {
         // of 32 SMs.  float32 parts are short enough to need no flushing.
         int64_t parts = 1;
         while (parts < 4 && items * cg * parts * 2 <= p.sms * 27 / 32 && d.part_blocks / (parts * 2) >= 4) parts *= 2;
-        if (parts > 1 && (p.type != PT_F32 || ceil_to(d.part_blocks, parts) <= 16)) {
+        if (parts > 1 && ceil_to(d.part_blocks, parts) <= (p.type != PT_F32 ? LONGEST / KB : 16)) {
             d.part_blocks = static_cast<int32_t>(ceil_to(d.part_blocks, parts));
             d.parts = static_cast<int32_t>(parts);
             items *= parts;
@@ -1889,6 +1937,8 @@ ProductPlan plan_product(int mode, const ProductParams& p) {
     d.grid = static_cast<int32_t>(std::max<int64_t>(cg, std::min<int64_t>(items * cg, p.sms / cg * cg)));
     d.prefix_bytes = mode != PRODUCT_ADAPTERS && p.S > NEAR_SEGMENTS ? ceil_to((p.S + 1) * 8, 256) * 256 : 0;
     d.partial_bytes = ceil_to(slots * cg * NT * MT * 4, 256) * 256;
+    d.staged = !d.empty && !weights && p.out_type != PT_F32 && d.parts == 1 && p.K > LONGEST;
+    if (d.staged) d.staged_bytes = ceil_to(p.R * p.N * 4, 256) * 256;
     if (d.pack_x) d.pack_x_bytes = ceil_to(packed_row(p.K, p.type) * p.R, 256) * 256;
     if (d.pack_w) d.pack_w_bytes = packed_row(w_shape(mode, p).cols, p.type) * w_shape(mode, p).rows * w_shape(mode, p).mats;
     return d;
@@ -1934,8 +1984,14 @@ cudaError_t launch_product(int mode, const ProductParams& given, const ProductPl
         if (mode == PRODUCT_WEIGHTS) return cudaMemsetAsync(p.out, 0, size * p.S * p.K * p.N, stream);
         return cudaMemset2DAsync(p.out, size * p.ldo, 0, size * p.N, p.R, stream);
     }
-    unsigned char* packed = p.ws + plan.prefix_bytes + plan.partial_bytes;
+    unsigned char* packed = p.ws + plan.prefix_bytes + plan.partial_bytes + plan.staged_bytes;
     const int size = p.type == PT_F32 ? 4 : 2;
+    float* const staged = reinterpret_cast<float*>(p.ws + plan.prefix_bytes + plan.partial_bytes);
+    if (plan.staged) {
+        p.out = staged;
+        p.ldo = p.N;
+        p.out_type = PT_F32;
+    }
     if (plan.pack_x) {
         const cudaError_t e = launch_pack(p.x, p.ldx, 0, {1, p.R, p.K}, size, packed, p.sms, stream);
         if (e != cudaSuccess) return e;
@@ -1960,19 +2016,27 @@ cudaError_t launch_product(int mode, const ProductParams& given, const ProductPl
     a.kblocks = static_cast<int32_t>(ceil_to(p.K, KB));
     a.box_rows = plan.narrow && p.R <= 32 * (mode == PRODUCT_FORWARD ? p.S : 1) ? 16 : 64;
     a.a_rows = static_cast<int32_t>(std::min<int64_t>(MT, ceil_to(p.N, 16) * 16));
-    a.flush = plan.parts > 1 ? NEVER_FLUSH : p.type == PT_F32 ? 8 : (p.out_type == PT_F32 && !p.index ? 12 : NEVER_FLUSH);
+    if (plan.parts > 1) a.flush = NEVER_FLUSH;                 // a part is short enough
+    else if (p.type == PT_F32) a.flush = 8;
+    else if (p.out_type != PT_F32) a.flush = NEVER_FLUSH;      // the sum is
+    else a.flush = mode == PRODUCT_WEIGHTS ? 12 : LONGEST / KB;
     const int64_t out_step = mode == PRODUCT_WEIGHTS ? p.N : p.ldo;
     a.wide_rows = p.N % 8 == 0 && out_step % 8 == 0 && reinterpret_cast<uintptr_t>(p.out) % 16 == 0;
     a.twin = p.type == PT_F32 && p.N <= MT / 2 && plan.parts == 1;
     a.chunk = plan.chunk;
+    a.add_by_start = plan.add_by_start;
     a.row_tiles = plan.row_tiles;
     a.cols_m = p.N;
     a.cols_n = p.K;
     a.far = reinterpret_cast<int*>(p.ws);
     a.partials = reinterpret_cast<float*>(p.ws + plan.prefix_bytes);
-    if (mode == PRODUCT_FORWARD) return launch_mode<PRODUCT_FORWARD>(a, plan, stream);
     if (mode == PRODUCT_WEIGHTS) return launch_mode<PRODUCT_WEIGHTS>(a, plan, stream);
-    return launch_mode<PRODUCT_ADAPTERS>(a, plan, stream);
+    const cudaError_t e = mode == PRODUCT_FORWARD ? launch_mode<PRODUCT_FORWARD>(a, plan, stream) : launch_mode<PRODUCT_ADAPTERS>(a, plan, stream);
+    if (e != cudaSuccess || !plan.staged) return e;
+    const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(ceil_to(p.R * p.N, 1024), int64_t(p.sms) * 8));
+    if (given.out_type == PT_F16) round_kernel<<<blocks, 256, 0, stream>>>(staged, static_cast<__half*>(given.out), p.R, p.N, given.ldo);
+    else round_kernel<<<blocks, 256, 0, stream>>>(staged, static_cast<__nv_bfloat16*>(given.out), p.R, p.N, given.ldo);
+    return cudaGetLastError();
 }
 
 }  // namespace segred

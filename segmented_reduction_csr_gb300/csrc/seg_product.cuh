@@ -53,9 +53,11 @@ struct ProductPlan {
     int32_t part_blocks;    // forward: 64-wide blocks per part
     int64_t chunk;          // weights: rows per part of a segment
     int32_t add_blocks;     // weights: blocks of the kernel that adds the parts (0: no segment can be split)
+    int32_t add_by_start;   // weights: those blocks stand for `chunk` rows each, not for a segment each
+    int32_t staged;         // forward, adapters: the sums are kept in float32 scratch and rounded by a kernel of their own
     int64_t row_tiles;      // forward: most row tiles there can be
-    int64_t prefix_bytes, partial_bytes, pack_x_bytes, pack_w_bytes;   // the workspace, in this order
-    int64_t bytes() const { return prefix_bytes + partial_bytes + pack_x_bytes + pack_w_bytes; }
+    int64_t prefix_bytes, partial_bytes, staged_bytes, pack_x_bytes, pack_w_bytes;   // the workspace, in this order
+    int64_t bytes() const { return prefix_bytes + partial_bytes + staged_bytes + pack_x_bytes + pack_w_bytes; }
 };
 
 enum : int { PRODUCT_FORWARD = 0, PRODUCT_WEIGHTS = 1, PRODUCT_ADAPTERS = 2 };
