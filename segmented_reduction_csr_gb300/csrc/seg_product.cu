@@ -1783,10 +1783,12 @@ cudaError_t launch_shape(const KernelArgs& a, const ProductPlan& plan, cudaStrea
         }
         if (!ok) return cudaErrorInvalidValue;
     }
-    if (a.p.S > NEAR_SEGMENTS && MODE != PRODUCT_ADAPTERS) {
-        prefix_kernel<MODE, NT><<<1, 1024, 0, stream>>>(a);
-        e = cudaGetLastError();
-        if (e != cudaSuccess) return e;
+    if constexpr (MODE != PRODUCT_ADAPTERS) {
+        if (a.p.S > NEAR_SEGMENTS) {
+            prefix_kernel<MODE, NT><<<1, 1024, 0, stream>>>(a);
+            e = cudaGetLastError();
+            if (e != cudaSuccess) return e;
+        }
     }
     auto* kernel = product_kernel<MODE, TENSOR, NT, PL, CG>;
     using R = Ring<MODE, NT, PL, CG, TENSOR>;
