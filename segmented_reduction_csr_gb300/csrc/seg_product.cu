@@ -1946,7 +1946,19 @@ ProductPlan plan_product(int mode, const ProductParams& p) {
     return d;
 }
 
-bool lora_by_rows(const ProductParams& p) { return p.R <= 4 * p.S && p.S <= 4096; }
+// Requests of a row or two and of a low rank, or not many rows x ranks in all:
+// every dot product is two warps' work and a search through the requests, while
+// the tensor-core kernel has a tile per request, which costs the same for one
+// row as for 16.  Whole calls, by rows / by tiles, us:
+//   K = N = 4,096, rank 16: 96 requests x 1 row 22 / 38, 1,024 x 2 164 / 214,
+//     4,096 x 2 671 / 722, 1,024 x 4 308 / 304, 4,096 x 4 1,314 / 1,055;
+//   2,048, rank 64: 96 x 1 45 / 51, 96 x 2 67 / 64, 256 x 1 85 / 85, 256 x 2
+//     106 / 85, 4,096 x 1 921 / 575, 4,096 x 4 3,519 / 1,565;
+//   1,024, rank 8: 256 x 4 36 / 41, 1,024 x 4 97 / 92, 4,096 x 1 125 / 171,
+//     4,096 x 2 229 / 211.
+bool lora_by_rows(const ProductParams& p) {
+    return p.S <= 4096 && p.R <= 4 * p.S && (p.R * p.N <= 16384 || (p.N <= 16 && p.R <= 2 * p.S));
+}
 
 namespace {
 
