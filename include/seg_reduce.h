@@ -440,20 +440,23 @@ seg_status_t seg_flags_to_offsets(const uint8_t *flags, int64_t n, int64_t *offs
  * have scratch of that graph's own, so its replays may overlap other products
  * and other graphs on any stream; it is used again when the graph and what was
  * instantiated from it have been destroyed.
- * Enqueues one to four kernel launches and returns without synchronising.
+ * Enqueues one kernel, up to five where operands are copied first, segments are
+ * above 1,024 or sums are split or long (seg_lora: up to eight), and returns
+ * without synchronising.
  *
  * Numerics.  Sums are float32 in an order that is a pure function of the
  * sizes, the offsets and the SM count (calls repeat bit for bit), rounded
  * once to `dtype`.  The products of 16-bit types are exact.  float32 is
  * multiplied on the tensor cores as three bfloat16 parts per value that hold
- * it exactly; the parts' products below 2^-21 of the full one are left out.
+ * it exactly; of the parts' nine products three are left out, each below 2^-21
+ * of the full one.
  * Before the last rounding the error of an output of n terms is below
  * (n * 2^-24 + 2^-20) * sum(|x w|).  The tensor cores' additions cut what they
  * shift out, so a sum of one sign comes out low.  Measured: by 2e-4 of it at
  * most for 16-bit results (reached at 32,768 terms; less than 2^-11 whatever the
  * length), by 5e-6 for float32 results of 16-bit x, and by 1e-6 for float32 x
- * (2e-6 where few tiles have their sum split along K).  A float32 row or matrix that holds an
- * infinity gives NaN where IEEE arithmetic would give an infinity.
+ * (2e-6 where few tiles have their sum split along K).  A float32 row or matrix
+ * that holds an infinity gives NaN where IEEE arithmetic would give an infinity.
  */
 #define SEG_MAX_PRODUCT_COLUMNS 1048576
 

@@ -672,7 +672,11 @@ def seg_matmul(x, w, offsets, transpose_w: bool = False, out=None, stream=None):
     ``transpose_w``, ``offsets`` ``[S+1]`` int64 or uint32.  Sums are float32
     and are rounded once to ``x``'s type.  The gradient of ``x`` is
     ``seg_matmul(dy, w, offsets, not transpose_w)``, that of ``w``
-    ``seg_matmul_grad_w``.  Not synchronised."""
+    ``seg_matmul_grad_w``; the call itself records none (``segment_matmul``
+    does).  A float32 row or matrix that holds an infinity gives NaN where IEEE
+    arithmetic would give an infinity.  Enqueued on ``stream`` (default: the
+    current one) and not synchronised; captured into a graph, it may be
+    replayed beside other products on any stream."""
     torch = _torch()
     ldx = _check_rows("x", x, offsets)
     code, s, (r, k) = _product_code(x), offsets.shape[0] - 1, x.shape
@@ -701,7 +705,8 @@ def seg_matmul_grad_w(x, dy, offsets, out_dtype=None, out=None, stream=None):
 
     ``x`` is ``[R, K]`` and ``dy`` ``[R, N]`` of one type; ``out_dtype`` is that
     type (the default) or float32.  For matrices stored ``[S, N, K]`` call it
-    with ``x`` and ``dy`` exchanged.  Not synchronised."""
+    with ``x`` and ``dy`` exchanged.  Infinities, ``stream`` and graphs as for
+    ``seg_matmul``; not synchronised."""
     torch = _torch()
     ldx = _check_rows("x", x, offsets)
     code, s = _product_code(x), offsets.shape[0] - 1
@@ -731,7 +736,8 @@ def seg_matmul_grad_w(x, dy, offsets, out_dtype=None, out=None, stream=None):
 def segment_matmul(x, w, indptr):
     """Differentiable ``seg_matmul``: ``x`` ``[R, K]``, ``w`` ``[S, K, N]``.
     Its backward pass is one ``seg_matmul`` (the gradient of ``x``) and one
-    ``seg_matmul_grad_w`` (that of ``w``), each where it is asked for."""
+    ``seg_matmul_grad_w`` (that of ``w``), each where it is asked for.
+    Differentiable once; no forward mode and no vmap."""
     return _segment_matmul_function().apply(x, w, indptr)
 
 
@@ -772,7 +778,10 @@ def seg_lora(x, w, a, b, offsets, adapter, scale=None, out=None, stream=None):
     bfloat16); ``offsets`` ``[S+1]`` delimits the requests' rows, ``adapter``
     ``[S]`` is int32 and ``scale`` ``[L]`` float32 (default 1).  A request with
     an adapter outside ``[0, L)`` (-1: none) and a row in no request take the
-    shared product alone.  The whole sum is float32 and is rounded once.  Not
+    shared product alone.  The whole sum is float32 and is rounded once.  What
+    an adapter holds, infinities and NaN too, reaches its own requests' rows
+    alone.  It records no gradient: adapters are served here, not trained.
+    Float32 infinities, ``stream`` and graphs as for ``seg_matmul``; not
     synchronised."""
     torch = _torch()
     ldx = _check_rows("x", x, offsets)

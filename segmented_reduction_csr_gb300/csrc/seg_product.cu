@@ -20,22 +20,27 @@
 // out the adapters' part.  Every wait has a time limit; a role that gives up
 // says so in the device status word and all leave.
 //
-// What bounds it (GB300, 6,680 GB/s and 1,937 TFLOP/s measured peaks):
+// What bounds it (GB300; measured peaks 6,793 GB/s, and 1,892 TFLOP/s in short
+// runs, 1,706 held).  Times are of a call in a replayed graph / of calls back to
+// back from Python:
 //   training shapes: the tensor cores' clock and power.  32,768 rows, 32
-//     segments, 2,048 x 4,096 bfloat16: forward 314 us = 1,750 TFLOP/s (a
-//     long-running library product reaches 1,749 here), weights 361 us;
+//     segments, 2,048 x 4,096 bfloat16: forward 309-328 / 371 us = 1,676-1,781 /
+//     1,482 TFLOP/s, weights 364-370 / 403 us;
 //   decode: reading the matrices.  128 rows over 64 matrices of 2,048 x 1,024:
-//     35 us = 6.6 TB/s of the matrices that are used;
+//     35 / 37 us = 6.6 TB/s of the matrices that are used;
 //   single tokens: launch, one round trip to memory and the parts' exchange,
-//     9 us for 2 rows and two 2,048 x 2,048 matrices;
-//   float32: shared memory (every value is there as float32 and as parts, and
-//     the part products read them again).  So a part of one operand takes as
-//     many parts of the other at once as the accumulators have room for.  1,000,000 x 64 times 64 x 64 in
-//     50 segments: 106 us = 4.9 TB/s.
+//     9 / 14 us for 2 rows and two 2,048 x 2,048 matrices (the host: 14);
+//   float32: no unit alone.  Every value is in shared memory as float32 and as
+//     parts, and the part products read those again, so a part of one operand
+//     takes as many parts of the other at once as the accumulators have room
+//     for.  1,000,000 x 64 times 64 x 64 in 50 segments: 105-116 / 109 us = 4.9
+//     TB/s; the shared memory's data path is busy for 61 % of the time (warps 26,
+//     operands of the MMAs 35), DRAM for 55.  Its weights' gradient, 149 / 152
+//     us: 66 % (37 and 29), DRAM 47, and SMs that wait for the longest share, 22.
 //
 // float32: every value is split into three bfloat16 parts by truncation (8 + 8
 // + 8 bits, exact) and six of the nine part products are accumulated; the
-// other three are below 2^-21 of the whole.
+// other three are below 2^-21 of the whole each.
 // The tensor cores cut what an addition shifts out of the accumulator: a sum of
 // one sign loses about 2^-23.4 of it per 16 steps of full products, less while
 // short products still fit (measured).  So for float32 the five small part
@@ -1647,8 +1652,11 @@ __global__ void __launch_bounds__(256) round_kernel(const float* src, T* out, in
 // request would use 16 of its lanes and stream K through one SM.  96 rows of
 // 96 requests, 4,096 columns, rank 16, the whole call: 25 us, with u by the
 // tensor-core kernel 31; four ranks to a block, so that x is read a quarter as
-// often.  The kernel is a chain of two loads and a reduction, and the shared
-// product copies and multiplies beside it.
+// often.  The kernel is a chain of two loads and a reduction.  The shared
+// product's kernel is launched beside it, but a CTA of that takes all registers
+// of an SM and has to wait for this kernel's blocks there: of few blocks (one
+// token: 4) its copies and products run beside these, of many (96 rows at rank
+// 16: 384 on 152 SMs) only the launch does.
 
 constexpr int DOT_RANKS = 4;      // ranks of a block, of one row; two warps each
 
@@ -1894,6 +1902,11 @@ ProductPlan plan_product(int mode, const ProductParams& p) {
     d.tensor = !d.empty && (copy_x || d.pack_x) && (copy_w || d.pack_w);
     // few rows per segment, or too few tiles to go round: small tiles and a
     // deeper ring; weights: few columns of x.  The loader warps have small tiles alone.
+    // The rows per segment are the mean, for lengths are on the device.  64
+    // segments, bfloat16, small / large tiles: 2,048 x 1,024, 8 rows each 45.5 /
+    // 47.3 us, 64 each 49.2 / 51.7, 16 with 3/4 of the rows in one segment 46.1 /
+    // 48.0, 64 with 3/4 in one 60.4 / 51.5, all 4,096 in one 31.7 / 17.6; 1,024 x
+    // 4,096: 81.3 / 85.1, 87.0 / 91.4, 89.1 / 85.7, 122 / 99.5, 56.2 / 27.0.
     d.narrow = !d.tensor || (weights ? p.K <= 64 : p.R <= 64 * segments || (p.N <= MT && p.R <= 128 * p.sms));
     const int NT = product_tile_columns(p, d);
     // two CTAs on a tile of twice the lanes, unless that leaves one of them without lanes
