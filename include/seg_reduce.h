@@ -517,6 +517,123 @@ seg_status_t seg_lora(const void *x, seg_dtype_t dtype, int64_t num_rows, int64_
                       const float *scale, void *out, int64_t ldo, seg_stream_t stream);
 
 /*
+ * seg_gated -- the gated feed-forward block over the rows of segments: both
+ * projections of a row with its segment's own matrices, the activation of the
+ * first and the product of the two.  For a row r of segment s,
+ *   g[n] = sum_k x[r, k] * w[s, k, n],  u[n] = sum_k x[r, k] * w[s, k, N + n],
+ *   out[r, n] = act(g[n]) * u[n]        n < N,
+ * and out[r, :] = 0 for a row in no segment.  The projection back is a
+ * seg_matmul of out.
+ *
+ *   x, dtype, num_rows, K, ldx, offsets, offsets_dtype, num_segments: as for
+ *                 seg_matmul.
+ *   w             device, num_segments matrices stride_w elements apart, each
+ *                 [K, 2 N] (transpose_w: [2 N, K]) with rows ldw elements apart:
+ *                 the columns (rows) of g, then those of u.
+ *   N             columns of each projection, 2 N <= SEG_MAX_PRODUCT_COLUMNS.
+ *   activation    SEG_SILU x / (1 + exp(-x)), SEG_GELU x P(x) with P the normal
+ *                 distribution, SEG_GELU_TANH its approximation x (1 + tanh(
+ *                 sqrt(2 / pi) (x + 0.044715 x^3))) / 2, SEG_RELU, SEG_SIGMOID.
+ *   out           device, [num_rows, N], rows ldo elements apart, of `dtype`.
+ *   pre           NULL, or device, [num_rows, 2 N], rows ldp elements apart, of
+ *                 `dtype`: receives g and u, for the backward pass.
+ *
+ * g and u are summed as seg_matmul's sums are and reach the activation in
+ * float32; out and pre are each rounded once.  Alignment as for seg_matmul.
+ * Scratch is that of the products; num_rows * 2 N float32 values of it where
+ * the products are not gated as they are summed (the sums are long, or no
+ * copies of odd matrices are made).
+ */
+typedef enum { SEG_SILU = 0, SEG_GELU = 1, SEG_GELU_TANH = 2, SEG_RELU = 3, SEG_SIGMOID = 4 } seg_activation_t;
+
+seg_status_t seg_gated(const void *x, seg_dtype_t dtype, int64_t num_rows, int64_t K, int64_t ldx,
+                       const void *w, int64_t N, int64_t ldw, int64_t stride_w, int32_t transpose_w,
+                       const void *offsets, seg_offset_dtype_t offsets_dtype, int64_t num_segments,
+                       seg_activation_t activation, void *out, int64_t ldo, void *pre, int64_t ldp,
+                       seg_stream_t stream);
+
+/*
+ * seg_gated_grad -- the gradient of seg_gated's products.
+ *   dpre[r, n] = dy[r, n] * u[n] * act'(g[n]),  dpre[r, N + n] = dy[r, n] * act(g[n])
+ * for every row, whatever segment it is in; g and u are pre's halves.  The
+ * gradient of x is then seg_matmul of dpre with w and the other value of
+ * transpose_w, that of w seg_matmul_grad_w of x and dpre (of dpre and x for
+ * matrices stored [2 N, K]), which leave out the rows in no segment.
+ *
+ *   pre, dpre     device, [num_rows, 2 N], rows ldp and ldd elements apart, of
+ *                 `dtype`.
+ *   dy            device, [num_rows, N], rows ldy elements apart, of `dtype`.
+ *   dtype, num_rows, N, activation: as for seg_gated.
+ *
+ * Computed in float32 and rounded once.  act' of relu is 0 at 0.
+ */
+seg_status_t seg_gated_grad(const void *pre, seg_dtype_t dtype, int64_t num_rows, int64_t N, int64_t ldp,
+                            const void *dy, int64_t ldy, seg_activation_t activation, void *dpre, int64_t ldd,
+                            seg_stream_t stream);
+
+/*
+ * seg_layer_norm -- rows normalised, then scaled and shifted by their segment's
+ * own weight and bias (a norm for every relation type, expert or adapter), or
+ * by shared ones.  For a row r of segment s, over its F columns,
+ *   mean = sum x / F,  rstd = 1 / sqrt(sum (x - mean)^2 / F + eps),
+ *   out[r, f] = (x[r, f] - mean) * rstd * weight[s, f] + bias[s, f],
+ * and out[r, :] = 0 for a row in no segment, whose mean and rstd are 0 too.
+ *
+ *   x             device, [num_rows, F], rows ldx elements apart (ldx >= F).
+ *   dtype         SEG_F32, SEG_F16 or SEG_BF16: the type of x and out.
+ *   num_rows      0 <= R <= 2^31 - 4096.
+ *   F             0 <= F <= SEG_MAX_PRODUCT_COLUMNS; R == 0 or F == 0 launches
+ *                 nothing.
+ *   weight, bias  device, [num_segments, F], contiguous, of weight_dtype
+ *                 (`dtype` or SEG_F32); NULL: 1, and 0.
+ *   offsets, offsets_dtype, num_segments: as for seg_matmul; or offsets NULL and
+ *                 num_segments 1: all rows are one segment's, weight and bias [F].
+ *   eps           finite, >= 0.
+ *   out           device, [num_rows, F], rows ldo elements apart.
+ *   mean, rstd    device, [num_rows] float32, or NULL: kept for the backward pass.
+ *
+ * Every pointer is aligned to its element; 16-byte aligned ones, with F and the
+ * strides multiples of 16 bytes, are read 16 bytes at a time.  Sums are float32
+ * in an order that the sizes and alignments give, the squares those of the
+ * differences from the mean; the result is rounded once.  A row that holds an
+ * infinity or NaN gives NaN in that row alone.  Enqueues one kernel, uses no
+ * scratch and returns without synchronising.
+ */
+seg_status_t seg_layer_norm(const void *x, seg_dtype_t dtype, int64_t num_rows, int64_t F, int64_t ldx,
+                            const void *weight, const void *bias, seg_dtype_t weight_dtype, const void *offsets,
+                            seg_offset_dtype_t offsets_dtype, int64_t num_segments, float eps, void *out,
+                            int64_t ldo, float *mean, float *rstd, seg_stream_t stream);
+
+/*
+ * seg_layer_norm_grad -- the gradients of seg_layer_norm.  With z = (x - mean) *
+ * rstd and g = dy * weight[s], for a row r of segment s
+ *   dx[r, f] = rstd * (g - sum(g) / F - z * sum(g z) / F),
+ *   dweight[s, f] = sum of dy z,  dbias[s, f] = sum of dy over the rows of s;
+ * dx is 0 for a row in no segment, dweight and dbias for a segment without rows.
+ *
+ *   x, dtype, num_rows, F, ldx, weight, weight_dtype, offsets, offsets_dtype,
+ *   num_segments: as for seg_layer_norm.
+ *   dy            device, [num_rows, F], rows ldy elements apart, of `dtype`.
+ *   mean, rstd    device, [num_rows] float32, as seg_layer_norm gave them.
+ *   dx            device, [num_rows, F], rows lddx elements apart, of `dtype`,
+ *                 or NULL: not wanted.
+ *   dweight, dbias   device, [num_segments, F], contiguous, of weight_dtype, or
+ *                 NULL: not wanted.
+ *
+ * Sums are float32 in an order that is a pure function of the sizes, the
+ * alignments, the offsets and the SM count, so calls repeat bit for bit; each
+ * result is rounded once.  Rows in no segment may hold anything.  Scratch is
+ * that of the products: 16 F bytes for each of at most 4 blocks per SM, and 8
+ * bytes a row for rows that a block's registers do not hold.  Enqueues one
+ * kernel to three.
+ */
+seg_status_t seg_layer_norm_grad(const void *x, seg_dtype_t dtype, int64_t num_rows, int64_t F, int64_t ldx,
+                                 const void *dy, int64_t ldy, const float *mean, const float *rstd,
+                                 const void *weight, seg_dtype_t weight_dtype, const void *offsets,
+                                 seg_offset_dtype_t offsets_dtype, int64_t num_segments, void *dx, int64_t lddx,
+                                 void *dweight, void *dbias, seg_stream_t stream);
+
+/*
  * seg_selftest_wait_timeout -- exercise the failure path of the bounded
  * waits without a fault.  The kernels wait on mbarriers for their bulk
  * copies with a time limit (2 s); a wait that runs out records

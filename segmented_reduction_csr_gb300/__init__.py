@@ -28,7 +28,12 @@ Beside the reduction (``seg_reduce``, ``segment_*_csr``, ``seg_reduce_noalloc``)
 * ``seg_matmul`` / ``seg_matmul_grad_w`` / ``segment_matmul``: the rows of
   every segment times the segment's own matrix, the matrices' gradient, and
   the two as one differentiable call; ``seg_lora``: a shared projection with
-  the low-rank adapters of many requests (float32, float16, bfloat16).
+  the low-rank adapters of many requests (float32, float16, bfloat16);
+* ``seg_gated`` / ``seg_gated_grad`` / ``segment_gated``: the gated feed-forward
+  block of every segment (both projections, the activation and the product),
+  its gradients, and the two as one differentiable call;
+* ``seg_layer_norm`` / ``seg_layer_norm_grad`` / ``segment_layer_norm``: rows
+  normalised, with a weight and bias for every segment or for all.
 """
 from __future__ import annotations
 
@@ -44,6 +49,8 @@ __all__ = [
     "seg_reduce_sequential", "scatter", "scatter_sum", "scatter_add", "scatter_mean",
     "scatter_max", "scatter_min", "seg_scan", "segment_cumsum_csr",
     "seg_matmul", "seg_matmul_grad_w", "segment_matmul", "seg_lora",
+    "seg_gated", "seg_gated_grad", "segment_gated",
+    "seg_layer_norm", "seg_layer_norm_grad", "segment_layer_norm",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -53,6 +60,7 @@ _LIB_PATH = os.path.join(_HERE, "lib", "libsegreduce.so")
 SEG_U32, SEG_S32, SEG_F32, SEG_F16, SEG_BF16 = 0, 1, 2, 3, 4
 SEG_OFF_U32, SEG_OFF_I64 = 0, 1
 OPS = {"sum": 0, "min": 1, "max": 2, "mean": 3}
+ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3, "sigmoid": 4}
 STATUS = {0: "SEG_OK", 1: "SEG_ERR_INVALID_ARGUMENT", 2: "SEG_ERR_UNSUPPORTED",
           3: "SEG_ERR_OUT_OF_MEMORY", 4: "SEG_ERR_CUDA", 5: "SEG_ERR_DEVICE_TIMEOUT",
           6: "SEG_ERR_SCRATCH_LIMIT"}
@@ -60,6 +68,7 @@ EXPORTED = ("seg_reduce", "seg_reduce_strerror", "seg_reduce_device_status",
             "seg_reduce_plan", "seg_reduce_version", "seg_reduce_noalloc", "seg_rle",
             "seg_flags_to_offsets", "seg_reduce_sequential", "seg_scatter", "seg_scatter_sorted", "seg_scan",
             "seg_matmul", "seg_matmul_grad_w", "seg_lora",
+            "seg_gated", "seg_gated_grad", "seg_layer_norm", "seg_layer_norm_grad",
             "seg_selftest_wait_timeout")
 NOALLOC_SCRATCH_BYTES = 2 << 20   # SEG_NOALLOC_SCRATCH_BYTES
 
@@ -138,6 +147,17 @@ def load_library(path: str | None = None):
         lib.seg_lora.restype = ctypes.c_int
         lib.seg_lora.argtypes = [vp, ctypes.c_int, i64, i64, i64, vp, i64, i64, vp, vp, i64, i64,
                                  vp, ctypes.c_int, i64, vp, vp, vp, i64, vp]
+        lib.seg_gated.restype = ctypes.c_int
+        lib.seg_gated.argtypes = [vp, ctypes.c_int, i64, i64, i64, vp, i64, i64, i64, i32,
+                                  vp, ctypes.c_int, i64, ctypes.c_int, vp, i64, vp, i64, vp]
+        lib.seg_gated_grad.restype = ctypes.c_int
+        lib.seg_gated_grad.argtypes = [vp, ctypes.c_int, i64, i64, i64, vp, i64, ctypes.c_int, vp, i64, vp]
+        lib.seg_layer_norm.restype = ctypes.c_int
+        lib.seg_layer_norm.argtypes = [vp, ctypes.c_int, i64, i64, i64, vp, vp, ctypes.c_int, vp, ctypes.c_int, i64,
+                                       ctypes.c_float, vp, i64, vp, vp, vp]
+        lib.seg_layer_norm_grad.restype = ctypes.c_int
+        lib.seg_layer_norm_grad.argtypes = [vp, ctypes.c_int, i64, i64, i64, vp, i64, vp, vp, vp, ctypes.c_int,
+                                            vp, ctypes.c_int, i64, vp, i64, vp, vp, vp]
         if path is None:
             _lib = lib
         return lib
@@ -812,6 +832,292 @@ def seg_lora(x, w, a, b, offsets, adapter, scale=None, out=None, stream=None):
     if stream is not None:
         _in_use(stream, x, w, a, b, offsets, adapter, scale, out)
     return out
+
+
+def _activation_code(activation):
+    code = ACTIVATIONS.get(activation)
+    if code is None:
+        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}")
+    return code
+
+
+def _gated_weights(x, w, s, transpose_w):
+    """Columns of each projection, and the rows' stride, of the gated block's matrices."""
+    if w.dim() != 3:
+        raise ValueError("w must be [S, K, 2 N] (transpose_w: [S, 2 N, K])")
+    both = w.shape[1] if transpose_w else w.shape[2]
+    if both % 2:
+        raise ValueError("w must hold two projections of as many columns each")
+    _same("w", w, x, (s, both, x.shape[1]) if transpose_w else (s, x.shape[1], both))
+    return both // 2, _row_stride("w", w)
+
+
+def _rows_out(name, out, like, shape, stream):
+    """A result of rows, the caller's (checked) or a new one, and its stride."""
+    if out is None:
+        torch = _torch()
+        out = torch.empty(shape, dtype=like.dtype, device=like.device) if stream is None else _fresh(shape, like.dtype, like.device, stream)
+        return out, max(shape[1], 1)
+    _same(name, out, like, shape)
+    return out, _row_stride(name, out)
+
+
+def seg_gated(x, w, offsets, activation: str = "silu", transpose_w: bool = False, with_pre: bool = False, out=None, pre=None, stream=None):
+    """The gated feed-forward block of every segment: for a row r of segment s,
+    ``out[r] = act(x[r] @ w[s][:, :N]) * (x[r] @ w[s][:, N:])``; a row in no
+    segment gives 0.
+
+    ``x`` is ``[R, K]`` (float32, float16 or bfloat16, CUDA; rows contiguous,
+    any stride between them), ``w`` ``[S, K, 2 N]``, or ``[S, 2 N, K]`` with
+    ``transpose_w``: the gate's columns (rows), then the other projection's.
+    ``activation`` is ``silu``, ``gelu`` (by the error function),
+    ``gelu_tanh``, ``relu`` or ``sigmoid``.  Returns ``out`` ``[R, N]``, with
+    ``with_pre`` (or a ``pre`` to write to) ``(out, pre)``, ``pre`` ``[R, 2 N]``
+    the two products for ``seg_gated_grad``.  The products are float32 up to the
+    result, which is rounded once (as ``pre`` is).  It records no gradient
+    (``segment_gated`` does).  Float32 infinities, ``stream`` and graphs as for
+    ``seg_matmul``; not synchronised."""
+    ldx = _check_rows("x", x, offsets)
+    code, s, (r, k) = _product_code(x), offsets.shape[0] - 1, x.shape
+    act = _activation_code(activation)
+    n, ldw = _gated_weights(x, w, s, transpose_w)
+    out, ldo = _rows_out("out", out, x, (r, n), stream)
+    ldp, with_pre = max(2 * n, 1), with_pre or pre is not None
+    if with_pre:
+        pre, ldp = _rows_out("pre", pre, x, (r, 2 * n), stream)
+    _enqueue("seg_gated", x.device, stream, load_library().seg_gated,
+             x.data_ptr() or None, code, r, k, ldx, w.data_ptr() or None, n, ldw, w.stride(0) if s > 1 else 0,
+             1 if transpose_w else 0, offsets.data_ptr(), _offset_code(offsets), s, act, out.data_ptr() or None, ldo,
+             (pre.data_ptr() or None) if with_pre else None, ldp)
+    if stream is not None:
+        _in_use(stream, x, w, offsets, out, pre)
+    return (out, pre) if with_pre else out
+
+
+def seg_gated_grad(x, w, pre, dy, offsets, activation: str = "silu", transpose_w: bool = False, want_dx: bool = True,
+                   want_dw: bool = True, dw_dtype=None, stream=None):
+    """The gradients of ``seg_gated``: ``(dx, dw)`` from its inputs, the ``pre``
+    that it gave and the gradient ``dy`` ``[R, N]`` of its result; ``None`` in
+    the place of one that is not wanted.
+
+    ``dx`` is ``[R, K]`` (0 for a row in no segment), ``dw`` has ``w``'s shape
+    (zeros for an empty segment) and type ``dw_dtype``: ``x``'s (the default) or
+    float32.  The gradient of the products, ``act'(g) * u * dy`` beside
+    ``act(g) * dy``, is rounded to ``x``'s type on its way into the two
+    products with it, ``seg_matmul`` and ``seg_matmul_grad_w``.  Arguments,
+    ``stream`` and graphs as for ``seg_gated``; not synchronised."""
+    torch = _torch()
+    _check_rows("x", x, offsets)
+    code, s, (r, _) = _product_code(x), offsets.shape[0] - 1, x.shape
+    act = _activation_code(activation)
+    n, _ = _gated_weights(x, w, s, transpose_w)
+    _same("pre", pre, x, (r, 2 * n))
+    _same("dy", dy, x, (r, n))
+    ldp, ldy = _row_stride("pre", pre), _row_stride("dy", dy)
+    if dw_dtype not in (None, x.dtype, torch.float32):
+        raise TypeError(f"dw_dtype must be {x.dtype} or torch.float32, not {dw_dtype}")
+    if not (want_dx or want_dw):
+        return None, None
+    # (an even number of 16-byte units a row, whatever N is, so that the products read it as it is)
+    ldd = -(-2 * n // 8) * 8
+    dpre, _ = _rows_out("dpre", None, x, (r, ldd), stream)
+    dpre = dpre[:, :2 * n]
+    _enqueue("seg_gated_grad", x.device, stream, load_library().seg_gated_grad, pre.data_ptr() or None, code, r, n, ldp,
+             dy.data_ptr() or None, ldy, act, dpre.data_ptr() or None, max(ldd, 1))
+    if stream is not None:
+        _in_use(stream, pre, dy, dpre)
+    dx = seg_matmul(dpre, w, offsets, transpose_w=not transpose_w, stream=stream) if want_dx else None
+    dw = None
+    if want_dw:
+        a, b = (dpre, x) if transpose_w else (x, dpre)
+        dw = seg_matmul_grad_w(a, b, offsets, out_dtype=dw_dtype, stream=stream)
+    return dx, dw
+
+
+def segment_gated(x, w, indptr, activation: str = "silu", transpose_w: bool = False):
+    """Differentiable ``seg_gated``: its backward pass is ``seg_gated_grad``,
+    for the gradients of ``x`` and ``w`` that are asked for.  The two products
+    are kept for it in ``x``'s type.  Differentiable once; no forward mode and
+    no vmap.  (As with any PyTorch operator, a backward pass is captured into a
+    graph only where no eager graph of the same leaves is alive.)"""
+    return _segment_gated_function().apply(x, w, indptr, activation, transpose_w)
+
+
+_segment_gated_fn = None
+
+
+def _segment_gated_function():
+    global _segment_gated_fn
+    if _segment_gated_fn is None:
+        torch = _torch()
+
+        class SegmentGated(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, x, w, indptr, activation, transpose_w):
+                ctx.how = activation, transpose_w
+                if not (ctx.needs_input_grad[0] or ctx.needs_input_grad[1]):
+                    return seg_gated(x, w, indptr, activation, transpose_w)
+                out, pre = seg_gated(x, w, indptr, activation, transpose_w, with_pre=True)
+                ctx.save_for_backward(x, w, indptr, pre)
+                return out
+
+            @staticmethod
+            @torch.autograd.function.once_differentiable
+            def backward(ctx, dy):
+                x, w, indptr, pre = ctx.saved_tensors
+                dx, dw = seg_gated_grad(x, w, pre, dy.contiguous(), indptr, *ctx.how, want_dx=ctx.needs_input_grad[0],
+                                        want_dw=ctx.needs_input_grad[1])
+                return dx, dw, None, None, None
+
+        _segment_gated_fn = SegmentGated
+    return _segment_gated_fn
+
+
+def _norm_arguments(x, weight, offsets):
+    """Rows' stride, type codes of x and the weights, segments and their offsets' code."""
+    torch = _torch()
+    if offsets is None:
+        if not x.is_cuda:
+            raise ValueError("x must be a CUDA tensor (there is no CPU path)")
+        if x.dim() != 2:
+            raise ValueError("x must be [R, columns]")
+        ldx, s, odt = _row_stride("x", x), 1, SEG_OFF_I64
+    else:
+        ldx = _check_rows("x", x, offsets)
+        s, odt = offsets.shape[0] - 1, _offset_code(offsets)
+    code = wcode = _product_code(x)
+    if weight is not None:
+        if weight.dtype not in (x.dtype, torch.float32):
+            raise TypeError(f"weight must be {x.dtype} or torch.float32, not {weight.dtype}")
+        wcode = _product_code(weight)
+    return ldx, code, wcode, s, odt
+
+
+def _norm_weight(name, t, x, weight, s, offsets):
+    """Checks a norm's weight or bias."""
+    if t is None:
+        return
+    _same(name, t, x, (x.shape[1],) if offsets is None else (s, x.shape[1]), weight.dtype)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def seg_layer_norm(x, weight=None, bias=None, offsets=None, eps: float = 1e-5, with_stats: bool = False, out=None, stream=None):
+    """Layer norm of rows, with every segment's own weight and bias: for a row r
+    of segment s, ``out[r] = (x[r] - mean) * rstd * weight[s] + bias[s]``, with
+    the mean of the row's columns and ``rstd = 1 / sqrt(var + eps)``; a row in no
+    segment gives 0 (mean and rstd too).
+
+    ``x`` is ``[R, F]`` (float32, float16 or bfloat16, CUDA; rows contiguous,
+    any stride between them), ``weight`` and ``bias`` are ``[S, F]`` with
+    ``offsets`` ``[S+1]`` (int64 or uint32), or ``[F]`` for all rows without;
+    both contiguous, of one type: ``x``'s or float32; ``None``: 1 and 0.
+    Returns ``out``, with ``with_stats`` ``(out, mean, rstd)`` (float32 ``[R]``,
+    for ``seg_layer_norm_grad``).  Computed in float32 and rounded once.  It
+    records no gradient (``segment_layer_norm`` does).  ``stream`` and graphs as
+    for ``seg_matmul``; not synchronised."""
+    torch = _torch()
+    like = bias if weight is None else weight
+    ldx, code, wcode, s, odt = _norm_arguments(x, like, offsets)
+    _norm_weight("weight", weight, x, like, s, offsets)
+    _norm_weight("bias", bias, x, like, s, offsets)
+    if not 0.0 <= eps < float("inf"):
+        raise ValueError("eps must be finite and not negative")
+    r, f = x.shape
+    out, ldo = _rows_out("out", out, x, (r, f), stream)
+    mean = rstd = None
+    if with_stats:
+        stats = torch.empty((2, r), dtype=torch.float32, device=x.device) if stream is None else _fresh((2, r), torch.float32, x.device, stream)
+        mean, rstd = stats[0], stats[1]
+    _enqueue("seg_layer_norm", x.device, stream, load_library().seg_layer_norm, x.data_ptr() or None, code, r, f, ldx,
+             _ptr(weight) or None, _ptr(bias) or None, wcode, _ptr(offsets), odt, s, eps, out.data_ptr() or None, ldo, (mean.data_ptr() or None) if with_stats else None,
+             (rstd.data_ptr() or None) if with_stats else None)
+    if stream is not None:
+        _in_use(stream, x, weight, bias, offsets, out, mean)
+    return (out, mean, rstd) if with_stats else out
+
+
+def seg_layer_norm_grad(x, dy, mean, rstd, weight=None, offsets=None, with_dx: bool = True, with_weight: bool = True,
+                        with_bias: bool = True, weight_dtype=None, stream=None):
+    """The gradients of ``seg_layer_norm``: ``(dx, dweight, dbias)`` from its
+    input, the gradient ``dy`` of its result and the ``mean`` and ``rstd`` that
+    it gave; ``None`` in the place of one that is not wanted.
+
+    ``dx`` is like ``x`` (0 for a row in no segment).  ``dweight`` and ``dbias``
+    are ``[S, F]`` (``[F]`` without ``offsets``) in ``weight``'s type (without
+    one: ``weight_dtype``, ``x``'s by default, or float32), summed in float32 in a fixed order and rounded once; zeros
+    for a segment without rows.  Arguments, ``stream`` and graphs as for
+    ``seg_layer_norm``; not synchronised."""
+    torch = _torch()
+    ldx, code, wcode, s, odt = _norm_arguments(x, weight, offsets)
+    if weight is None and weight_dtype is not None:
+        if weight_dtype not in (x.dtype, torch.float32):
+            raise TypeError(f"weight_dtype must be {x.dtype} or torch.float32, not {weight_dtype}")
+        wtype, wcode = weight_dtype, code if weight_dtype == x.dtype else SEG_F32
+    else:
+        wtype = x.dtype if weight is None else weight.dtype
+    _norm_weight("weight", weight, x, weight, s, offsets)
+    r, f = x.shape
+    _same("dy", dy, x, (r, f))
+    ldy = _row_stride("dy", dy)
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        _same(name, t, x, (r,), torch.float32)
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    shape = (f,) if offsets is None else (s, f)
+
+    def fresh(wanted, shape, dtype):
+        if not wanted:
+            return None
+        return torch.empty(shape, dtype=dtype, device=x.device) if stream is None else _fresh(shape, dtype, x.device, stream)
+
+    dx, dweight, dbias = fresh(with_dx, (r, f), x.dtype), fresh(with_weight, shape, wtype), fresh(with_bias, shape, wtype)
+    _enqueue("seg_layer_norm_grad", x.device, stream, load_library().seg_layer_norm_grad, x.data_ptr() or None, code, r, f, ldx,
+             dy.data_ptr() or None, ldy, mean.data_ptr() or None, rstd.data_ptr() or None, _ptr(weight) or None, wcode,
+             _ptr(offsets), odt, s,
+             _ptr(dx) or None, max(f, 1), _ptr(dweight) or None, _ptr(dbias) or None)
+    if stream is not None:
+        _in_use(stream, x, dy, mean, rstd, weight, offsets, dx, dweight, dbias)
+    return dx, dweight, dbias
+
+
+def segment_layer_norm(x, weight=None, bias=None, indptr=None, eps: float = 1e-5):
+    """Differentiable ``seg_layer_norm``: its backward pass is
+    ``seg_layer_norm_grad``, for the gradients that are asked for.
+    Differentiable once; no forward mode and no vmap."""
+    return _segment_layer_norm_function().apply(x, weight, bias, indptr, eps)
+
+
+_segment_layer_norm_fn = None
+
+
+def _segment_layer_norm_function():
+    global _segment_layer_norm_fn
+    if _segment_layer_norm_fn is None:
+        torch = _torch()
+
+        class SegmentLayerNorm(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, x, weight, bias, indptr, eps):
+                if not any(ctx.needs_input_grad[:3]):
+                    return seg_layer_norm(x, weight, bias, indptr, eps)
+                out, mean, rstd = seg_layer_norm(x, weight, bias, indptr, eps, with_stats=True)
+                # (without a weight, the bias names the type of the gradients)
+                ctx.wtype = None if weight is not None or bias is None else bias.dtype
+                ctx.save_for_backward(x, weight, indptr, mean, rstd)
+                return out
+
+            @staticmethod
+            @torch.autograd.function.once_differentiable
+            def backward(ctx, dy):
+                x, weight, indptr, mean, rstd = ctx.saved_tensors
+                need = ctx.needs_input_grad
+                dx, dweight, dbias = seg_layer_norm_grad(x, dy.contiguous(), mean, rstd, weight, indptr, with_dx=need[0],
+                                                         with_weight=need[1], with_bias=need[2], weight_dtype=ctx.wtype)
+                return dx, dweight, dbias, None, None
+
+        _segment_layer_norm_fn = SegmentLayerNorm
+    return _segment_layer_norm_fn
 
 
 def selftest_wait_timeout(limit_ms: int = 50, stream=None) -> None:

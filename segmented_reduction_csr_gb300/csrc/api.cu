@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 #include <map>
@@ -11,6 +12,8 @@
 #include <utility>
 
 #include "../../include/seg_reduce.h"
+#include "seg_gated.cuh"
+#include "seg_norm.cuh"
 #include "seg_pick.cuh"
 #include "seg_plan.cuh"
 #include "seg_product.cuh"
@@ -339,6 +342,30 @@ seg_status_t check_product(seg_dtype_t dtype, int64_t num_rows, int64_t K, int64
     if (S > 0 && !offsets) return SEG_ERR_INVALID_ARGUMENT;
     if (misaligned(x, product_size(dtype)) || misaligned(offsets, offsets_dtype == SEG_OFF_U32 ? 4 : 8))
         return SEG_ERR_INVALID_ARGUMENT;
+    return SEG_OK;
+}
+
+bool bad_activation(seg_activation_t a) {
+    return a != SEG_SILU && a != SEG_GELU && a != SEG_GELU_TANH && a != SEG_RELU && a != SEG_SIGMOID;
+}
+
+// What both passes of a norm take; offsets NULL: one segment of all rows.
+seg_status_t check_norm(NormParams& p, const void* x, seg_dtype_t dtype, int64_t num_rows, int64_t F, int64_t ldx, const void* weight,
+                        seg_dtype_t weight_dtype, const void* offsets, seg_offset_dtype_t offsets_dtype, int64_t S) {
+    if (!offsets && S != 1) return SEG_ERR_INVALID_ARGUMENT;
+    const seg_status_t st = check_product(dtype, num_rows, F, 0, ldx, x, offsets ? offsets : x, offsets ? offsets_dtype : SEG_OFF_U32, offsets ? S : 0);
+    if (st != SEG_OK) return st;
+    if ((weight_dtype != dtype && weight_dtype != SEG_F32) || misaligned(weight, product_size(weight_dtype))) return SEG_ERR_INVALID_ARGUMENT;
+    p.x = x;
+    p.weight = weight;
+    p.offsets = offsets;
+    p.R = num_rows;
+    p.F = F;
+    p.S = S;
+    p.ldx = ldx;
+    p.type = dtype;
+    p.weight_type = weight_dtype;
+    p.off64 = offsets_dtype == SEG_OFF_I64 ? 1 : 0;
     return SEG_OK;
 }
 
@@ -994,6 +1021,202 @@ seg_status_t seg_lora(const void* x, seg_dtype_t dtype, int64_t num_rows, int64_
             p.overlap = by_rows ? 1 : 0;
         }
         return run_product(PRODUCT_ADAPTERS, p, stream, sc, ds);
+    });
+}
+
+seg_status_t seg_gated(const void* x, seg_dtype_t dtype, int64_t num_rows, int64_t K, int64_t ldx,
+                       const void* w, int64_t N, int64_t ldw, int64_t stride_w, int32_t transpose_w,
+                       const void* offsets, seg_offset_dtype_t offsets_dtype, int64_t num_segments,
+                       seg_activation_t activation, void* out, int64_t ldo, void* pre, int64_t ldp,
+                       seg_stream_t stream_) {
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    const seg_status_t checked = check_product(dtype, num_rows, K, N, ldx, x, offsets, offsets_dtype, num_segments);
+    if (checked != SEG_OK) return checked;
+    if (bad_activation(activation)) return SEG_ERR_INVALID_ARGUMENT;
+    const int64_t wrows = transpose_w ? 2 * N : K, wcols = transpose_w ? K : 2 * N;
+    if ((transpose_w != 0 && transpose_w != 1) || ldo < N || ldw < wcols || stride_w < 0 || (pre && ldp < 2 * N)) return SEG_ERR_INVALID_ARGUMENT;
+    if (num_segments > 1 && wrows > 0 && stride_w < (wrows - 1) * ldw + wcols) return SEG_ERR_INVALID_ARGUMENT;
+    if (2 * N > SEG_MAX_PRODUCT_COLUMNS) return SEG_ERR_UNSUPPORTED;
+    if (num_rows == 0 || N == 0) return SEG_OK;
+    if (!out || (num_segments > 0 && K > 0 && !w)) return SEG_ERR_INVALID_ARGUMENT;
+    const int64_t size = product_size(dtype);
+    if (misaligned(w, size) || misaligned(out, size) || misaligned(pre, size)) return SEG_ERR_INVALID_ARGUMENT;
+    ProductParams p{};
+    p.x = x;
+    p.w = w;
+    p.offsets = offsets;
+    p.R = num_rows;
+    p.K = K;
+    p.N = 2 * N;
+    p.S = num_segments;
+    p.ldx = ldx;
+    p.ldw = ldw;
+    p.stride_w = stride_w;
+    p.off64 = offsets_dtype == SEG_OFF_I64 ? 1 : 0;
+    p.trans = transpose_w;
+    p.type = dtype;
+    return guarded([&]() -> seg_status_t {
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess) return SEG_ERR_CUDA;
+        std::lock_guard<std::mutex> lock(g_mu);
+        DeviceState* ds = nullptr;
+        seg_status_t st = device_state(dev, &ds);
+        if (st != SEG_OK) return st;
+        p.sms = ds->sm_count;
+        // the products in float32 (float32 ones that are asked for: in their place), then the activation
+        p.out_type = SEG_F32;
+        const bool in_place = pre && dtype == SEG_F32;
+        p.ldo = in_place ? ldp : 2 * N;
+        p.out = in_place ? pre : nullptr;
+        const int64_t own = plan_product(PRODUCT_FORWARD, p).bytes();
+        Scratch* sc = nullptr;
+        st = product_scratch(dev, stream, static_cast<size_t>(own + (in_place ? 0 : num_rows * 2 * N * 4)), &sc);
+        if (st != SEG_OK) return st;
+        if (!in_place) p.out = static_cast<unsigned char*>(sc->ptr) + own;
+        st = run_product(PRODUCT_FORWARD, p, stream, sc, ds);
+        if (st != SEG_OK) return st;
+        GatedParams g{};
+        g.pre = p.out;
+        g.ldp = p.ldo;
+        g.out = out;
+        g.ldo = ldo;
+        g.rounded = in_place ? nullptr : pre;
+        g.ldr = ldp;
+        g.R = num_rows;
+        g.N = N;
+        g.type = dtype;
+        g.activation = activation;
+        g.sms = ds->sm_count;
+        if (launch_gated(g, stream) != cudaSuccess) {
+            cudaGetLastError();
+            return SEG_ERR_CUDA;
+        }
+        return SEG_OK;
+    });
+}
+
+seg_status_t seg_gated_grad(const void* pre, seg_dtype_t dtype, int64_t num_rows, int64_t N, int64_t ldp,
+                            const void* dy, int64_t ldy, seg_activation_t activation, void* dpre, int64_t ldd,
+                            seg_stream_t stream) {
+    if (bad_product_type(dtype) || bad_activation(activation)) return SEG_ERR_INVALID_ARGUMENT;
+    if (num_rows < 0 || N < 0 || ldp < 2 * N || ldy < N || ldd < 2 * N) return SEG_ERR_INVALID_ARGUMENT;
+    if (num_rows > INT32_MAX - 4095 || 2 * N > SEG_MAX_PRODUCT_COLUMNS) return SEG_ERR_UNSUPPORTED;
+    if (num_rows == 0 || N == 0) return SEG_OK;
+    const int64_t size = product_size(dtype);
+    if (!pre || !dy || !dpre || misaligned(pre, size) || misaligned(dy, size) || misaligned(dpre, size)) return SEG_ERR_INVALID_ARGUMENT;
+    GatedParams g{};
+    g.pre = pre;
+    g.ldp = ldp;
+    g.dy = dy;
+    g.ldy = ldy;
+    g.out = dpre;
+    g.ldo = ldd;
+    g.R = num_rows;
+    g.N = N;
+    g.type = dtype;
+    g.activation = activation;
+    return guarded([&]() -> seg_status_t {
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess) return SEG_ERR_CUDA;
+        std::lock_guard<std::mutex> lock(g_mu);
+        DeviceState* ds = nullptr;
+        const seg_status_t st = device_state(dev, &ds);
+        if (st != SEG_OK) return st;
+        g.sms = ds->sm_count;
+        if (launch_gated_grad(g, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) {
+            cudaGetLastError();
+            return SEG_ERR_CUDA;
+        }
+        return SEG_OK;
+    });
+}
+
+seg_status_t seg_layer_norm(const void* x, seg_dtype_t dtype, int64_t num_rows, int64_t F, int64_t ldx,
+                            const void* weight, const void* bias, seg_dtype_t weight_dtype, const void* offsets,
+                            seg_offset_dtype_t offsets_dtype, int64_t num_segments, float eps, void* out,
+                            int64_t ldo, float* mean, float* rstd, seg_stream_t stream_) {
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    NormParams p{};
+    const seg_status_t checked = check_norm(p, x, dtype, num_rows, F, ldx, weight, weight_dtype, offsets, offsets_dtype, num_segments);
+    if (checked != SEG_OK) return checked;
+    if (ldo < F || !(eps >= 0.0f) || !(eps < INFINITY)) return SEG_ERR_INVALID_ARGUMENT;
+    if (num_rows == 0 || F == 0) return SEG_OK;
+    if (!out || misaligned(out, product_size(dtype)) || misaligned(bias, product_size(weight_dtype)) || misaligned(mean, 4) || misaligned(rstd, 4))
+        return SEG_ERR_INVALID_ARGUMENT;
+    p.bias = bias;
+    p.out = out;
+    p.ldo = ldo;
+    p.mean = mean;
+    p.rstd = rstd;
+    p.eps = eps;
+    return guarded([&]() -> seg_status_t {
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess) return SEG_ERR_CUDA;
+        std::lock_guard<std::mutex> lock(g_mu);
+        DeviceState* ds = nullptr;
+        const seg_status_t st = device_state(dev, &ds);
+        if (st != SEG_OK) return st;
+        p.sms = ds->sm_count;
+        if (launch_norm(p, plan_norm(false, p), stream) != cudaSuccess) {
+            cudaGetLastError();
+            return SEG_ERR_CUDA;
+        }
+        return SEG_OK;
+    });
+}
+
+seg_status_t seg_layer_norm_grad(const void* x, seg_dtype_t dtype, int64_t num_rows, int64_t F, int64_t ldx,
+                                 const void* dy, int64_t ldy, const float* mean, const float* rstd,
+                                 const void* weight, seg_dtype_t weight_dtype, const void* offsets,
+                                 seg_offset_dtype_t offsets_dtype, int64_t num_segments, void* dx, int64_t lddx,
+                                 void* dweight, void* dbias, seg_stream_t stream_) {
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    NormParams p{};
+    const seg_status_t checked = check_norm(p, x, dtype, num_rows, F, ldx, weight, weight_dtype, offsets, offsets_dtype, num_segments);
+    if (checked != SEG_OK) return checked;
+    if (ldy < F || (dx && lddx < F)) return SEG_ERR_INVALID_ARGUMENT;
+    const int64_t size = product_size(dtype), wsize = product_size(weight_dtype);
+    if (misaligned(dy, size) || misaligned(dx, size) || misaligned(dweight, wsize) || misaligned(dbias, wsize) || misaligned(mean, 4) ||
+        misaligned(rstd, 4))
+        return SEG_ERR_INVALID_ARGUMENT;
+    if (F == 0) return SEG_OK;
+    if (num_rows > 0 && (!dy || !mean || !rstd)) return SEG_ERR_INVALID_ARGUMENT;
+    if (p.S == 0) dweight = dbias = nullptr;
+    if (num_rows == 0) {
+        for (void* sums : {dweight, dbias})
+            if (sums && cudaMemsetAsync(sums, 0, static_cast<size_t>(p.S * F * wsize), stream) != cudaSuccess) {
+                cudaGetLastError();
+                return SEG_ERR_CUDA;
+            }
+        return SEG_OK;
+    }
+    if (!dx && !dweight && !dbias) return SEG_OK;
+    p.dy = dy;
+    p.ldy = ldy;
+    p.mean = const_cast<float*>(mean);
+    p.rstd = const_cast<float*>(rstd);
+    p.out = dx;
+    p.ldo = dx ? lddx : F;
+    p.dweight = dweight;
+    p.dbias = dbias;
+    return guarded([&]() -> seg_status_t {
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess) return SEG_ERR_CUDA;
+        std::lock_guard<std::mutex> lock(g_mu);
+        DeviceState* ds = nullptr;
+        seg_status_t st = device_state(dev, &ds);
+        if (st != SEG_OK) return st;
+        p.sms = ds->sm_count;
+        const NormPlan plan = plan_norm(true, p);
+        Scratch* sc = nullptr;
+        st = product_scratch(dev, stream, static_cast<size_t>(plan.bytes()), &sc);
+        if (st != SEG_OK) return st;
+        p.ws = static_cast<unsigned char*>(sc->ptr);
+        if (launch_norm_grad(p, plan, stream) != cudaSuccess) {
+            cudaGetLastError();
+            return SEG_ERR_CUDA;
+        }
+        return SEG_OK;
     });
 }
 

@@ -1,0 +1,58 @@
+// seg_act.cuh -- the activations of the gated block and their derivatives, in float32.
+#pragma once
+#include "seg_gated.cuh"
+
+namespace segred {
+
+// s(x) = 1 / (1 + exp(-x)) and s(-x) = 1 - s(x), from exp(-|x|) so that neither
+// overflows nor cancels.  FAST (where results are rounded to 16 bits): the special
+// function unit's exp2 and division, off by 2 + 1.2 |x| units of 2^-23.
+template <bool FAST>
+__device__ __forceinline__ void logistic(float x, float& s, float& other) {
+    const float e = FAST ? __expf(-fabsf(x)) : expf(-fabsf(x));
+    const float high = FAST ? __fdividef(1.0f, 1.0f + e) : 1.0f / (1.0f + e), low = e * high;
+    // (NaN: both are)
+    s = x >= 0.0f ? high : low;
+    other = x >= 0.0f ? low : high;
+}
+
+// act(x) and, where `slope` is wanted, act'(x).
+//   silu      x s                       s + x s (1 - s)            s = logistic(x)
+//   gelu      x P                       P + x p                    P, p: the normal distribution and its density
+//   gelu_tanh x s                       s + x s (1 - s) q'         s = logistic(q) = (1 + tanh(q / 2)) / 2,
+//                                                                  q = sqrt(8 / pi) (x + 0.044715 x^3)
+//   relu      max(x, 0)                 1 where x > 0, else 0
+//   sigmoid   s                         s (1 - s)
+template <bool FAST, bool SLOPE>
+__device__ __forceinline__ float activate(int kind, float x, float& slope) {
+    if (kind == ACT_RELU) {
+        // (NaN stays NaN)
+        if (SLOPE) slope = x > 0.0f ? 1.0f : 0.0f;
+        return x > 0.0f || x != x ? x : 0.0f;
+    }
+    if (kind == ACT_GELU) {
+        const float p = 0.5f * erfcf(-0.70710678f * x);
+        if (SLOPE) {
+            const float e = FAST ? __expf(-0.5f * x * x) : expf(-0.5f * x * x);
+            slope = e > 0.0f ? fmaf(x, 0.39894228f * e, p) : p;
+        }
+        return x * p;
+    }
+    float q = x, dq = 1.0f;
+    if (kind == ACT_GELU_TANH) {
+        const float x2 = fminf(x * x, 1e6f);      // (s is 0 or 1 long before that)
+        q = 1.5957691f * x * fmaf(0.044715f, x2, 1.0f);
+        if (SLOPE) dq = 1.5957691f * fmaf(0.134145f, x2, 1.0f);
+    }
+    float s, other;
+    logistic<FAST>(q, s, other);
+    const float f = kind == ACT_SIGMOID ? s : x * s;
+    if (SLOPE) {
+        const float rest = s * other;
+        // (x may be so large that its product with 0 is none)
+        slope = kind == ACT_SIGMOID ? rest : rest > 0.0f ? fmaf(x * dq, rest, s) : s;
+    }
+    return f;
+}
+
+}  // namespace segred

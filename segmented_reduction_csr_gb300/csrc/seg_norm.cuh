@@ -1,0 +1,50 @@
+// seg_norm.cuh -- layer norm of the rows of offset-delimited segments, with a
+// weight and bias for every segment: launch parameters shared by seg_norm.cu
+// and api.cu.
+//
+//   forward   z = (x - mean) * rstd,  y = z * w + b       mean, rstd of the row
+//   backward  g = dy * w,  dx = rstd * (g - sum(g) / F - z * sum(g z) / F)
+//             dw[s] = sum_r dy * z,  db[s] = sum_r dy     over the rows of s
+#pragma once
+#include <cstdint>
+#include <cuda_runtime.h>
+
+namespace segred {
+
+struct NormParams {
+    const void* x;          // [R, F], row stride ldx
+    const void* dy;         // backward: [R, F], row stride ldy
+    const void* weight;     // [S, F] (offsets NULL: [F]), or NULL for 1
+    const void* bias;       // the same, or NULL for 0
+    const void* offsets;    // [S + 1], or NULL: one segment of all rows (S = 1)
+    void* out;              // y, or dx (NULL: not wanted); row stride ldo
+    float* mean;            // [R]: written (or NULL), or given
+    float* rstd;
+    void* dweight;          // [S, F] of weight_type, or NULL
+    void* dbias;
+    int64_t R, F, S;
+    int64_t ldx, ldy, ldo;
+    float eps;
+    int32_t type, weight_type, off64;      // PT_F32, PT_F16 or PT_BF16
+    // library-owned
+    unsigned char* ws;      // see NormPlan
+    int32_t sms;
+};
+
+// How a call is launched; a pure function of sizes, strides, alignment and the SM count.
+struct NormPlan {
+    int32_t vec;            // values of a load: 16 bytes of them, or 1
+    int32_t per;            // loads of a thread for a row, 0: rows are read again instead of kept
+    int32_t group;          // threads of a row, a power of two
+    int32_t threads;        // of a block
+    int64_t chunk, chunks;  // rows of a block; blocks
+    int32_t tiles;          // backward: tiles of columns, each with blocks of its own
+    int64_t sums_bytes, partial_bytes;     // the workspace, in this order
+    int64_t bytes() const { return sums_bytes + partial_bytes; }
+};
+
+NormPlan plan_norm(bool grad, const NormParams& p);
+cudaError_t launch_norm(const NormParams& p, const NormPlan& plan, cudaStream_t stream);
+cudaError_t launch_norm_grad(const NormParams& p, const NormPlan& plan, cudaStream_t stream);
+
+}  // namespace segred
