@@ -536,7 +536,8 @@ seg_status_t seg_lora(const void *x, seg_dtype_t dtype, int64_t num_rows, int64_
  *                 sqrt(2 / pi) (x + 0.044715 x^3))) / 2, SEG_RELU, SEG_SIGMOID.
  *   out           device, [num_rows, N], rows ldo elements apart, of `dtype`.
  *   pre           NULL, or device, [num_rows, 2 N], rows ldp elements apart, of
- *                 `dtype`: receives g and u, for the backward pass.
+ *                 pre_dtype (`dtype` or SEG_F32): receives g and u, for the
+ *                 backward pass.
  *
  * g and u are summed as seg_matmul's sums are and reach the activation in
  * float32; out and pre are each rounded once.  Alignment as for seg_matmul.
@@ -549,8 +550,8 @@ typedef enum { SEG_SILU = 0, SEG_GELU = 1, SEG_GELU_TANH = 2, SEG_RELU = 3, SEG_
 seg_status_t seg_gated(const void *x, seg_dtype_t dtype, int64_t num_rows, int64_t K, int64_t ldx,
                        const void *w, int64_t N, int64_t ldw, int64_t stride_w, int32_t transpose_w,
                        const void *offsets, seg_offset_dtype_t offsets_dtype, int64_t num_segments,
-                       seg_activation_t activation, void *out, int64_t ldo, void *pre, int64_t ldp,
-                       seg_stream_t stream);
+                       seg_activation_t activation, void *out, int64_t ldo, void *pre, seg_dtype_t pre_dtype,
+                       int64_t ldp, seg_stream_t stream);
 
 /*
  * seg_gated_grad -- the gradient of seg_gated's products.
@@ -560,15 +561,15 @@ seg_status_t seg_gated(const void *x, seg_dtype_t dtype, int64_t num_rows, int64
  * transpose_w, that of w seg_matmul_grad_w of x and dpre (of dpre and x for
  * matrices stored [2 N, K]), which leave out the rows in no segment.
  *
- *   pre, dpre     device, [num_rows, 2 N], rows ldp and ldd elements apart, of
- *                 `dtype`.
+ *   pre           device, [num_rows, 2 N], rows ldp elements apart, of pre_dtype.
  *   dy            device, [num_rows, N], rows ldy elements apart, of `dtype`.
- *   dtype, num_rows, N, activation: as for seg_gated.
+ *   dpre          device, [num_rows, 2 N], rows ldd elements apart, of `dtype`.
+ *   dtype, pre_dtype, num_rows, N, activation: as for seg_gated.
  *
  * Computed in float32 and rounded once.  act' of relu is 0 at 0.
  */
-seg_status_t seg_gated_grad(const void *pre, seg_dtype_t dtype, int64_t num_rows, int64_t N, int64_t ldp,
-                            const void *dy, int64_t ldy, seg_activation_t activation, void *dpre, int64_t ldd,
+seg_status_t seg_gated_grad(const void *pre, seg_dtype_t pre_dtype, int64_t num_rows, int64_t N, int64_t ldp,
+                            const void *dy, seg_dtype_t dtype, int64_t ldy, seg_activation_t activation, void *dpre, int64_t ldd,
                             seg_stream_t stream);
 
 /*

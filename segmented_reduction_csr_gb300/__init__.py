@@ -149,9 +149,9 @@ def load_library(path: str | None = None):
                                  vp, ctypes.c_int, i64, vp, vp, vp, i64, vp]
         lib.seg_gated.restype = ctypes.c_int
         lib.seg_gated.argtypes = [vp, ctypes.c_int, i64, i64, i64, vp, i64, i64, i64, i32,
-                                  vp, ctypes.c_int, i64, ctypes.c_int, vp, i64, vp, i64, vp]
+                                  vp, ctypes.c_int, i64, ctypes.c_int, vp, i64, vp, ctypes.c_int, i64, vp]
         lib.seg_gated_grad.restype = ctypes.c_int
-        lib.seg_gated_grad.argtypes = [vp, ctypes.c_int, i64, i64, i64, vp, i64, ctypes.c_int, vp, i64, vp]
+        lib.seg_gated_grad.argtypes = [vp, ctypes.c_int, i64, i64, i64, vp, ctypes.c_int, i64, ctypes.c_int, vp, i64, vp]
         lib.seg_layer_norm.restype = ctypes.c_int
         lib.seg_layer_norm.argtypes = [vp, ctypes.c_int, i64, i64, i64, vp, vp, ctypes.c_int, vp, ctypes.c_int, i64,
                                        ctypes.c_float, vp, i64, vp, vp, vp]
@@ -852,14 +852,23 @@ def _gated_weights(x, w, s, transpose_w):
     return both // 2, _row_stride("w", w)
 
 
-def _rows_out(name, out, like, shape, stream):
+def _rows_out(name, out, like, shape, stream, dtype=None):
     """A result of rows, the caller's (checked) or a new one, and its stride."""
     if out is None:
         torch = _torch()
-        out = torch.empty(shape, dtype=like.dtype, device=like.device) if stream is None else _fresh(shape, like.dtype, like.device, stream)
+        dtype = like.dtype if dtype is None else dtype
+        out = torch.empty(shape, dtype=dtype, device=like.device) if stream is None else _fresh(shape, dtype, like.device, stream)
         return out, max(shape[1], 1)
-    _same(name, out, like, shape)
+    _same(name, out, like, shape, dtype)
     return out, _row_stride(name, out)
+
+
+def _pre_type(pre, x):
+    """The type of the gated block's products, which may be float32 beside any x, and its code."""
+    torch = _torch()
+    if pre.dtype not in (x.dtype, torch.float32):
+        raise TypeError(f"pre must be {x.dtype} or torch.float32, not {pre.dtype}")
+    return pre.dtype, _product_code(pre)
 
 
 def seg_gated(x, w, offsets, activation: str = "silu", transpose_w: bool = False, with_pre: bool = False, out=None, pre=None, stream=None):
@@ -873,22 +882,26 @@ def seg_gated(x, w, offsets, activation: str = "silu", transpose_w: bool = False
     ``activation`` is ``silu``, ``gelu`` (by the error function),
     ``gelu_tanh``, ``relu`` or ``sigmoid``.  Returns ``out`` ``[R, N]``, with
     ``with_pre`` (or a ``pre`` to write to) ``(out, pre)``, ``pre`` ``[R, 2 N]``
-    the two products for ``seg_gated_grad``.  The products are float32 up to the
-    result, which is rounded once (as ``pre`` is).  It records no gradient
+    the two products for ``seg_gated_grad``: float32, which the gradients are
+    exact to, or, in a ``pre`` of ``x``'s type, half of that memory.  The
+    products are float32 up to the result, which is rounded once.  It records
+    no gradient
     (``segment_gated`` does).  Float32 infinities, ``stream`` and graphs as for
     ``seg_matmul``; not synchronised."""
+    torch = _torch()
     ldx = _check_rows("x", x, offsets)
     code, s, (r, k) = _product_code(x), offsets.shape[0] - 1, x.shape
     act = _activation_code(activation)
     n, ldw = _gated_weights(x, w, s, transpose_w)
     out, ldo = _rows_out("out", out, x, (r, n), stream)
-    ldp, with_pre = max(2 * n, 1), with_pre or pre is not None
+    ldp, with_pre, pcode = max(2 * n, 1), with_pre or pre is not None, code
     if with_pre:
-        pre, ldp = _rows_out("pre", pre, x, (r, 2 * n), stream)
+        ptype, pcode = (torch.float32, SEG_F32) if pre is None else _pre_type(pre, x)
+        pre, ldp = _rows_out("pre", pre, x, (r, 2 * n), stream, ptype)
     _enqueue("seg_gated", x.device, stream, load_library().seg_gated,
              x.data_ptr() or None, code, r, k, ldx, w.data_ptr() or None, n, ldw, w.stride(0) if s > 1 else 0,
              1 if transpose_w else 0, offsets.data_ptr(), _offset_code(offsets), s, act, out.data_ptr() or None, ldo,
-             (pre.data_ptr() or None) if with_pre else None, ldp)
+             (pre.data_ptr() or None) if with_pre else None, pcode, ldp)
     if stream is not None:
         _in_use(stream, x, w, offsets, out, pre)
     return (out, pre) if with_pre else out
@@ -911,7 +924,8 @@ def seg_gated_grad(x, w, pre, dy, offsets, activation: str = "silu", transpose_w
     code, s, (r, _) = _product_code(x), offsets.shape[0] - 1, x.shape
     act = _activation_code(activation)
     n, _ = _gated_weights(x, w, s, transpose_w)
-    _same("pre", pre, x, (r, 2 * n))
+    ptype, pcode = _pre_type(pre, x)
+    _same("pre", pre, x, (r, 2 * n), ptype)
     _same("dy", dy, x, (r, n))
     ldp, ldy = _row_stride("pre", pre), _row_stride("dy", dy)
     if dw_dtype not in (None, x.dtype, torch.float32):
@@ -922,8 +936,8 @@ def seg_gated_grad(x, w, pre, dy, offsets, activation: str = "silu", transpose_w
     ldd = -(-2 * n // 8) * 8
     dpre, _ = _rows_out("dpre", None, x, (r, ldd), stream)
     dpre = dpre[:, :2 * n]
-    _enqueue("seg_gated_grad", x.device, stream, load_library().seg_gated_grad, pre.data_ptr() or None, code, r, n, ldp,
-             dy.data_ptr() or None, ldy, act, dpre.data_ptr() or None, max(ldd, 1))
+    _enqueue("seg_gated_grad", x.device, stream, load_library().seg_gated_grad, pre.data_ptr() or None, pcode, r, n, ldp,
+             dy.data_ptr() or None, code, ldy, act, dpre.data_ptr() or None, max(ldd, 1))
     if stream is not None:
         _in_use(stream, pre, dy, dpre)
     dx = seg_matmul(dpre, w, offsets, transpose_w=not transpose_w, stream=stream) if want_dx else None
@@ -937,7 +951,7 @@ def seg_gated_grad(x, w, pre, dy, offsets, activation: str = "silu", transpose_w
 def segment_gated(x, w, indptr, activation: str = "silu", transpose_w: bool = False):
     """Differentiable ``seg_gated``: its backward pass is ``seg_gated_grad``,
     for the gradients of ``x`` and ``w`` that are asked for.  The two products
-    are kept for it in ``x``'s type.  Differentiable once; no forward mode and
+    are kept for it in float32.  Differentiable once; no forward mode and
     no vmap.  (As with any PyTorch operator, a backward pass is captured into a
     graph only where no eager graph of the same leaves is alive.)"""
     return _segment_gated_function().apply(x, w, indptr, activation, transpose_w)

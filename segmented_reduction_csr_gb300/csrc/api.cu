@@ -1027,12 +1027,12 @@ seg_status_t seg_lora(const void* x, seg_dtype_t dtype, int64_t num_rows, int64_
 seg_status_t seg_gated(const void* x, seg_dtype_t dtype, int64_t num_rows, int64_t K, int64_t ldx,
                        const void* w, int64_t N, int64_t ldw, int64_t stride_w, int32_t transpose_w,
                        const void* offsets, seg_offset_dtype_t offsets_dtype, int64_t num_segments,
-                       seg_activation_t activation, void* out, int64_t ldo, void* pre, int64_t ldp,
-                       seg_stream_t stream_) {
+                       seg_activation_t activation, void* out, int64_t ldo, void* pre, seg_dtype_t pre_dtype,
+                       int64_t ldp, seg_stream_t stream_) {
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
     const seg_status_t checked = check_product(dtype, num_rows, K, N, ldx, x, offsets, offsets_dtype, num_segments);
     if (checked != SEG_OK) return checked;
-    if (bad_activation(activation)) return SEG_ERR_INVALID_ARGUMENT;
+    if (bad_activation(activation) || (pre && pre_dtype != dtype && pre_dtype != SEG_F32)) return SEG_ERR_INVALID_ARGUMENT;
     const int64_t wrows = transpose_w ? 2 * N : K, wcols = transpose_w ? K : 2 * N;
     if ((transpose_w != 0 && transpose_w != 1) || ldo < N || ldw < wcols || stride_w < 0 || (pre && ldp < 2 * N)) return SEG_ERR_INVALID_ARGUMENT;
     if (num_segments > 1 && wrows > 0 && stride_w < (wrows - 1) * ldw + wcols) return SEG_ERR_INVALID_ARGUMENT;
@@ -1040,7 +1040,7 @@ seg_status_t seg_gated(const void* x, seg_dtype_t dtype, int64_t num_rows, int64
     if (num_rows == 0 || N == 0) return SEG_OK;
     if (!out || (num_segments > 0 && K > 0 && !w)) return SEG_ERR_INVALID_ARGUMENT;
     const int64_t size = product_size(dtype);
-    if (misaligned(w, size) || misaligned(out, size) || misaligned(pre, size)) return SEG_ERR_INVALID_ARGUMENT;
+    if (misaligned(w, size) || misaligned(out, size) || (pre && misaligned(pre, product_size(pre_dtype)))) return SEG_ERR_INVALID_ARGUMENT;
     ProductParams p{};
     p.x = x;
     p.w = w;
@@ -1063,13 +1063,25 @@ seg_status_t seg_gated(const void* x, seg_dtype_t dtype, int64_t num_rows, int64
         seg_status_t st = device_state(dev, &ds);
         if (st != SEG_OK) return st;
         p.sms = ds->sm_count;
-        // the products in float32 (float32 ones that are asked for: in their place), then the activation
+        p.out = out;
+        p.ldo = ldo;
+        p.out_type = dtype;
+        p.pre = pre;
+        p.ldp = ldp;
+        p.pre_type = pre_dtype;
+        p.activation = activation;
+        const ProductPlan plan = plan_product(PRODUCT_GATED, p);
+        Scratch* sc = nullptr;
+        if (plan.fused || plan.empty) {
+            st = product_scratch(dev, stream, static_cast<size_t>(plan.bytes()), &sc);
+            return st != SEG_OK ? st : run_product(PRODUCT_GATED, p, stream, sc, ds);
+        }
+        // the products in float32 (where those are asked for: in their place), then the activation
+        const bool in_place = pre && pre_dtype == SEG_F32;
         p.out_type = SEG_F32;
-        const bool in_place = pre && dtype == SEG_F32;
         p.ldo = in_place ? ldp : 2 * N;
         p.out = in_place ? pre : nullptr;
         const int64_t own = plan_product(PRODUCT_FORWARD, p).bytes();
-        Scratch* sc = nullptr;
         st = product_scratch(dev, stream, static_cast<size_t>(own + (in_place ? 0 : num_rows * 2 * N * 4)), &sc);
         if (st != SEG_OK) return st;
         if (!in_place) p.out = static_cast<unsigned char*>(sc->ptr) + own;
@@ -1095,15 +1107,15 @@ seg_status_t seg_gated(const void* x, seg_dtype_t dtype, int64_t num_rows, int64
     });
 }
 
-seg_status_t seg_gated_grad(const void* pre, seg_dtype_t dtype, int64_t num_rows, int64_t N, int64_t ldp,
-                            const void* dy, int64_t ldy, seg_activation_t activation, void* dpre, int64_t ldd,
+seg_status_t seg_gated_grad(const void* pre, seg_dtype_t pre_dtype, int64_t num_rows, int64_t N, int64_t ldp,
+                            const void* dy, seg_dtype_t dtype, int64_t ldy, seg_activation_t activation, void* dpre, int64_t ldd,
                             seg_stream_t stream) {
-    if (bad_product_type(dtype) || bad_activation(activation)) return SEG_ERR_INVALID_ARGUMENT;
+    if (bad_product_type(dtype) || bad_activation(activation) || (pre_dtype != dtype && pre_dtype != SEG_F32)) return SEG_ERR_INVALID_ARGUMENT;
     if (num_rows < 0 || N < 0 || ldp < 2 * N || ldy < N || ldd < 2 * N) return SEG_ERR_INVALID_ARGUMENT;
     if (num_rows > INT32_MAX - 4095 || 2 * N > SEG_MAX_PRODUCT_COLUMNS) return SEG_ERR_UNSUPPORTED;
     if (num_rows == 0 || N == 0) return SEG_OK;
     const int64_t size = product_size(dtype);
-    if (!pre || !dy || !dpre || misaligned(pre, size) || misaligned(dy, size) || misaligned(dpre, size)) return SEG_ERR_INVALID_ARGUMENT;
+    if (!pre || !dy || !dpre || misaligned(pre, product_size(pre_dtype)) || misaligned(dy, size) || misaligned(dpre, size)) return SEG_ERR_INVALID_ARGUMENT;
     GatedParams g{};
     g.pre = pre;
     g.ldp = ldp;
@@ -1114,6 +1126,7 @@ seg_status_t seg_gated_grad(const void* pre, seg_dtype_t dtype, int64_t num_rows
     g.R = num_rows;
     g.N = N;
     g.type = dtype;
+    g.pre_type = pre_dtype;
     g.activation = activation;
     return guarded([&]() -> seg_status_t {
         int dev = 0;

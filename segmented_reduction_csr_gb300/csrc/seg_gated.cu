@@ -1,7 +1,6 @@
 // seg_gated.cu -- the gated block's activation over rows in memory (see
 // seg_gated.cuh): one pass, 16 bytes of each half of a row per thread where the
-// rows allow it.  Bound by memory: forward reads 8 bytes a value of pre (they
-// are float32 sums) and writes the result; backward moves 5 values per column.
+// rows allow it.  Bound by memory.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -27,7 +26,7 @@ template <class T, int V> struct alignas(V * sizeof(T) < 16 ? V * sizeof(T) : 16
 };
 
 // `lanes` threads a row, V columns of it each at a time.
-template <class T, int V, bool GRAD>
+template <class T, class P, int V, bool GRAD>
 __global__ void __launch_bounds__(256) gated_kernel(const __grid_constant__ GatedParams p, int lanes) {
     constexpr bool FAST = sizeof(T) == 2;
     const int lane = threadIdx.x % lanes;
@@ -35,15 +34,15 @@ __global__ void __launch_bounds__(256) gated_kernel(const __grid_constant__ Gate
     for (int64_t r = int64_t(blockIdx.x) * (256 / lanes) + threadIdx.x / lanes; r < p.R; r += step) {
         for (int64_t c = int64_t(lane) * V; c < p.N; c += lanes * V) {
             if constexpr (GRAD) {
-                const T* pre = static_cast<const T*>(p.pre) + r * p.ldp + c;
-                const Pack<T, V> g = *reinterpret_cast<const Pack<T, V>*>(pre), u = *reinterpret_cast<const Pack<T, V>*>(pre + p.N);
+                const P* pre = static_cast<const P*>(p.pre) + r * p.ldp + c;
+                const Pack<P, V> g = *reinterpret_cast<const Pack<P, V>*>(pre), u = *reinterpret_cast<const Pack<P, V>*>(pre + p.N);
                 const Pack<T, V> dy = *reinterpret_cast<const Pack<T, V>*>(static_cast<const T*>(p.dy) + r * p.ldy + c);
                 Pack<T, V> dg, du;
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     float slope;
-                    const float f = activate<FAST, true>(p.activation, to_float<T>(g.v[i]), slope), d = to_float<T>(dy.v[i]);
-                    dg.v[i] = from_float<T>(d * to_float<T>(u.v[i]) * slope);
+                    const float f = activate<FAST, true>(p.activation, to_float<P>(g.v[i]), slope), d = to_float<T>(dy.v[i]);
+                    dg.v[i] = from_float<T>(d * to_float<P>(u.v[i]) * slope);
                     du.v[i] = from_float<T>(d * f);
                 }
                 T* out = static_cast<T*>(p.out) + r * p.ldo + c;
@@ -73,32 +72,33 @@ __global__ void __launch_bounds__(256) gated_kernel(const __grid_constant__ Gate
 
 bool fits(const void* ptr, int64_t ld, int size) { return reinterpret_cast<uintptr_t>(ptr) % 16 == 0 && ld * size % 16 == 0; }
 
-template <class T, bool GRAD>
+template <class T, class P, bool GRAD>
 cudaError_t launch(const GatedParams& p, cudaStream_t stream) {
     constexpr int V = 16 / sizeof(T);
-    const bool vec = p.N % V == 0 && fits(p.pre, p.ldp, GRAD ? sizeof(T) : 4) && fits(p.out, p.ldo, sizeof(T)) &&
+    const bool vec = p.N % V == 0 && fits(p.pre, p.ldp, sizeof(P)) && fits(p.out, p.ldo, sizeof(T)) &&
                      (!GRAD || fits(p.dy, p.ldy, sizeof(T))) && (!p.rounded || fits(p.rounded, p.ldr, sizeof(T)));
     int lanes = 4;
     while (lanes < 256 && lanes * (vec ? V : 1) < p.N) lanes *= 2;
     const int rows = 256 / lanes;
     const unsigned blocks = static_cast<unsigned>(std::min<int64_t>((p.R + rows - 1) / rows, int64_t(p.sms) * 32));
-    if (vec) gated_kernel<T, V, GRAD><<<blocks, 256, 0, stream>>>(p, lanes);
-    else gated_kernel<T, 1, GRAD><<<blocks, 256, 0, stream>>>(p, lanes);
+    if (vec) gated_kernel<T, P, V, GRAD><<<blocks, 256, 0, stream>>>(p, lanes);
+    else gated_kernel<T, P, 1, GRAD><<<blocks, 256, 0, stream>>>(p, lanes);
     return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_gated(const GatedParams& p, cudaStream_t stream) {
-    if (p.type == PT_F32) return launch<float, false>(p, stream);
-    if (p.type == PT_F16) return launch<__half, false>(p, stream);
-    return launch<__nv_bfloat16, false>(p, stream);
+    if (p.type == PT_F32) return launch<float, float, false>(p, stream);
+    if (p.type == PT_F16) return launch<__half, float, false>(p, stream);
+    return launch<__nv_bfloat16, float, false>(p, stream);
 }
 
 cudaError_t launch_gated_grad(const GatedParams& p, cudaStream_t stream) {
-    if (p.type == PT_F32) return launch<float, true>(p, stream);
-    if (p.type == PT_F16) return launch<__half, true>(p, stream);
-    return launch<__nv_bfloat16, true>(p, stream);
+    const bool wide = p.pre_type == PT_F32;
+    if (p.type == PT_F32) return launch<float, float, true>(p, stream);
+    if (p.type == PT_F16) return wide ? launch<__half, float, true>(p, stream) : launch<__half, __half, true>(p, stream);
+    return wide ? launch<__nv_bfloat16, float, true>(p, stream) : launch<__nv_bfloat16, __nv_bfloat16, true>(p, stream);
 }
 
 }  // namespace segred

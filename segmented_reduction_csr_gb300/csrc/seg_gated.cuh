@@ -15,13 +15,13 @@ namespace segred {
 enum : int { ACT_SILU = 0, ACT_GELU = 1, ACT_GELU_TANH = 2, ACT_RELU = 3, ACT_SIGMOID = 4 };
 
 struct GatedParams {
-    const void* pre;        // [R, 2 N], row stride ldp; forward: float32, backward: of type
+    const void* pre;        // [R, 2 N], row stride ldp; forward: float32, backward: of pre_type
     const void* dy;         // backward: [R, N], row stride ldy
     void* out;              // forward: [R, N], backward: [R, 2 N]; row stride ldo
     void* rounded;          // forward: pre in `type` [R, 2 N], row stride ldr, or NULL
     int64_t R, N;
     int64_t ldp, ldy, ldo, ldr;
-    int32_t type, activation;
+    int32_t type, pre_type, activation;    // pre_type: PT_F32, or type
     int32_t sms;
 };
 

@@ -1,11 +1,13 @@
 // seg_product.cu -- products over the rows of segments (see seg_product.cuh)
 // on the tensor cores (tcgen05, accumulators in tensor memory).
 //
-// One kernel serves all three products.  A tile is D[m, n] with m (128 lanes
+// One kernel serves all of them.  A tile is D[m, n] with m (128 lanes
 // of tensor memory, 256 for a pair of CTAs) along the output's contiguous
 // dimension and n (its columns, up to NT) along the other one:
 //   forward, adapters  m: output columns, n: rows of one segment, sum over K;
-//   weights            m: columns of dy,  n: columns of x,        sum over rows.
+//   weights            m: columns of dy,  n: columns of x,        sum over rows;
+//   gated              m: 64 columns of the gate and the same 64 of the other
+//                      projection, n: rows of one segment, sum over K.
 // With the rows of a segment on n, whose extent an MMA takes in steps of 16,
 // a ragged tail or a single row costs 16 columns, not a whole 128-row tile;
 // and a warp's 32 lanes are 32 neighbouring output columns, so results leave
@@ -58,6 +60,7 @@
 
 #include <algorithm>
 
+#include "seg_act.cuh"
 #include "seg_common.cuh"
 #include "seg_product.cuh"
 #include "tc.cuh"
@@ -86,6 +89,7 @@ constexpr int NEVER_FLUSH = 1 << 28;         // more blocks than any sum has
 // length; 1,048,576 steps were off by 6e-3), which a float16 result's own
 // rounding covers.  Longer sums are added up from pieces, rounded, in float32.
 constexpr int64_t LONGEST = 32768;
+constexpr int FLUSH_F32 = 8;              // blocks of a float32 sum in one accumulator
 constexpr unsigned STATUS_PRODUCT_TIMEOUT = 8u;
 
 // Stage ring of a kernel shape: PL 16-bit planes per operand, CG CTAs that share a tile.
@@ -95,14 +99,15 @@ struct Ring {
     static constexpr int A_PLANE = MT * 128, B_PLANE = NT / CG * 128;
     static constexpr int STAGE = PL * (A_PLANE + B_PLANE);
     // (the loaders' plain loads are tracked in the L1 that shared memory leaves)
-    static constexpr int ALL_STAGES = std::min(8, (PL == 3 ? 221184 : TENSOR ? 200704 : 98304) / STAGE);
+    static constexpr bool GATED = MODE == PRODUCT_GATED;
+    static constexpr int ALL_STAGES = std::min(8, (PL == 3 ? (GATED ? 212992 : 221184) : TENSOR ? 200704 : 98304) / STAGE);
     static constexpr int STAGES = ALL_STAGES - (LOW ? 1 : 0);
     static constexpr bool ROW3 = PL == 3 && NT == 64;            // a part of A times several parts of B at once
     static constexpr int ACC = PL == 1 ? NT : 256;               // tensor-memory columns of one accumulator
     static constexpr int BARS = 3 * STAGES + 7 + LOW_TILES;
     // the drain warps' staging; PL == 3 keeps it (adapters alone need it there) in the space of the offsets
     static constexpr int STAGING = PL == 1 ? 2048 : 1024;
-    static constexpr int STAGED = PL == 1 ? EPW * STAGING : 0;
+    static constexpr int STAGED = PL == 1 || GATED ? EPW * STAGING : 0;
     static constexpr int NEAR = 2 * (NEAR_SEGMENTS + 1) * 4;
     static_assert(NEAR >= EPW * 1024, "room for that staging");
     static constexpr int SMEM = ALL_STAGES * STAGE + STAGED + NEAR + BARS * 8 + 128 + NT * 4 * (LOW ? 2 : 1) + 1024;   // 1024: alignment of the stages
@@ -116,8 +121,10 @@ struct KernelArgs {
     int32_t a_rows;     // rows of one copy of A whose sum is contiguous
     int32_t twin;       // at most 64 lanes, laid out twice: the drain warps of the second 64 share the first's work
     int32_t wide_rows;  // 16-bit results: 16-byte stores fit
+    int32_t wide_pre;   // the same of gated's 16-bit products
     int32_t flush;      // blocks of the sum after which the accumulators go to the result
     int32_t add_by_start;
+    int64_t half_w;     // gated: elements from the gate's columns of a matrix to the other projection's
     int64_t chunk, row_tiles, cols_m, cols_n;   // cols_*: extent of the tile dimensions (forward: cols_n unused)
     int* far;          // offsets and tile prefix of more than NEAR_SEGMENTS segments
     float* partials;
@@ -204,6 +211,7 @@ struct Item {
 template <int MODE, int NT, int CG>
 __device__ __forceinline__ void item_at(const KernelArgs& a, const int* beg, const int* pre, uint32_t i, Item& t) {
     int q;
+    constexpr int LANES = MODE == PRODUCT_GATED ? MT / 2 : MT;      // columns of the result that a CTA's tile has
     const uint32_t mtiles = a.mtiles;
     if (MODE == PRODUCT_WEIGHTS) {
         const uint32_t per = mtiles * a.ntiles, r = i % per;
@@ -214,7 +222,7 @@ __device__ __forceinline__ void item_at(const KernelArgs& a, const int* beg, con
         const uint32_t tile = a.parts > 1 ? i / a.parts : i;
         t.part = static_cast<int>(i - tile * a.parts);
         q = static_cast<int>(mtiles > 1 ? tile / mtiles : tile);
-        t.m0 = static_cast<int>(tile - q * mtiles) * (MT * CG);
+        t.m0 = static_cast<int>(tile - q * mtiles) * (LANES * CG);
         t.n0 = 0;
     }
     int b = 0, e = static_cast<int>(a.p.R), first = 0, count;
@@ -440,6 +448,163 @@ __device__ __forceinline__ void store_tile(const KernelArgs& a, uint32_t from, b
         }
     }
 }
+
+// ---------------------------------------------------------------------------
+// The gated block's drain.  Lanes 0 to 63 of a tile are the gate's columns, 64
+// to 127 the other projection's, so what belongs together is in the lanes of
+// two warps, `quarter` and `quarter` ^ 2.  Each of them takes half of the rows
+// and gives the other half of its values to the other one, through shared
+// memory: 2 x 64 KB a tile of 256 rows, under a tenth of what its MMAs read.
+// (16 columns of each projection by turns in the lanes would need no exchange,
+// but a matrix whose columns are contiguous cannot be copied so.)
+
+// Lane's values of n rows `step` apart from element `at` of a tensor of any type.
+template <int W>
+__device__ __forceinline__ void store_any(void* out, int type, int64_t at, int64_t step, const float (&v)[W], int n) {
+    if (type == PT_F32) store_rows(static_cast<float*>(out) + at, step, v, n, [](float x) { return x; });
+    else store_rows(static_cast<uint16_t*>(out) + at, step, v, n, [type](float x) { return static_cast<uint16_t>(narrow_pair(x, 0.0f, type)); });
+}
+
+// g = act(g) * u, with the kind of activation outside of the loop.
+template <bool FAST, int W>
+__device__ __forceinline__ void gate(int kind, float (&g)[W], const float (&u)[W]) {
+    auto all = [&](auto k) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            float slope;
+            g[i] = activate<FAST, false>(k(), g[i], slope) * u[i];
+        }
+    };
+    if (kind == ACT_SILU) all([] { return ACT_SILU; });
+    else if (kind == ACT_GELU) all([] { return ACT_GELU; });
+    else if (kind == ACT_GELU_TANH) all([] { return ACT_GELU_TANH; });
+    else if (kind == ACT_RELU) all([] { return ACT_RELU; });
+    else all([] { return ACT_SIGMOID; });
+}
+
+// Both warps of a pair; 3 .. 6 of the CTA's barriers.
+__device__ __forceinline__ void bar_pair(int quarter, int group) { asm volatile("bar.sync %0, 64;" ::"r"(3 + group * 2 + (quarter & 1)) : "memory"); }
+
+// From v's two halves (`low` and `high` name the registers): this warp's half
+// of the rows of both projections, in g and u.
+template <int W, class Low, class High>
+__device__ __forceinline__ void exchange(const float (&v)[W], float (&g)[W / 2], float (&u)[W / 2], Low low, High high, int lane, int quarter,
+                                         int group, unsigned char* own, int staging) {
+    constexpr int H = W / 2;
+    const bool second = quarter >= 2;
+    float4* to = reinterpret_cast<float4*>(own) + lane;
+    const float4* other = reinterpret_cast<const float4*>(second ? own - 2 * staging : own + 2 * staging) + lane;
+#pragma unroll
+    for (int i = 0; i < H; i += 4)
+        to[i * 8] = make_float4(second ? v[low(i)] : v[high(i)], second ? v[low(i + 1)] : v[high(i + 1)],
+                                second ? v[low(i + 2)] : v[high(i + 2)], second ? v[low(i + 3)] : v[high(i + 3)]);
+    bar_pair(quarter, group);
+#pragma unroll
+    for (int i = 0; i < H; i += 4) {
+        const float4 x = other[i * 8];
+        const float got[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float mine = second ? v[high(i + k)] : v[low(i + k)];
+            g[i + k] = second ? got[k] : mine;
+            u[i + k] = second ? mine : got[k];
+        }
+    }
+    bar_pair(quarter, group);      // the staging may be written again
+}
+
+// W rows from row0 on, n of which there are, of this warp's lanes: register i holds row i.
+template <bool FAST, int W>
+__device__ __forceinline__ void gate_rows(const KernelArgs& a, const float (&v)[W], int64_t row0, int n, int64_t m, int lanes, int lane,
+                                          int quarter, int group, unsigned char* own, int staging) {
+    const ProductParams& p = a.p;
+    if (p.pre && lane < lanes) store_any(p.pre, p.pre_type, row0 * p.ldp + (quarter >> 1) * a.cols_m + m + lane, p.ldp, v, n);
+    float g[W / 2], u[W / 2];
+    exchange<W>(v, g, u, [](int i) { return i; }, [](int i) { return W / 2 + i; }, lane, quarter, group, own, staging);
+    gate<FAST, W / 2>(p.activation, g, u);
+    const int first = (quarter >> 1) * (W / 2);
+    if (lane < lanes) store_any(p.out, p.out_type, (row0 + first) * p.ldo + m + lane, p.ldo, g, n - first);
+}
+
+// 32 rows of 16-bit results that take 16-byte stores, in 8 x 8 blocks as in store_tile.
+__device__ __forceinline__ void gate_blocks(const KernelArgs& a, uint32_t from, int64_t row0, int n, int64_t m, int lanes, int lane, int quarter,
+                                            int group, unsigned char* own, int staging) {
+    const ProductParams& p = a.p;
+    const int half = quarter >> 1, unit = lane & 3;
+    float v[32];
+    if (p.pre && p.pre_type == PT_F32) {
+        // (rows of 128 bytes, straight from the lanes)
+        tmem_load(from, v);
+        tmem_wait(v);
+        if (lane < lanes) store_rows(static_cast<float*>(p.pre) + row0 * p.ldp + half * a.cols_m + m + lane, p.ldp, v, n, [](float x) { return x; });
+    }
+    tmem_load_blocks(from, v);
+    tmem_wait(v);
+    if (p.pre && p.pre_type != PT_F32) {
+        uint32_t two[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) two[i] = narrow_pair(v[2 * i], v[2 * i + 1], p.pre_type);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int row = 8 * k + (lane & 7);
+            store_blocks_t(own + row * 64 + (((lane >> 3) ^ (row >> 1 & 3)) << 4), two[2 * k], two[2 * k + 1], two[8 + 2 * k], two[8 + 2 * k + 1]);
+        }
+        __syncwarp();
+        uint16_t* o = static_cast<uint16_t*>(p.pre) + row0 * p.ldp + half * a.cols_m + m + unit * 8;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int row = i * 8 + (lane >> 2);
+            if (row < n && unit * 8 < lanes) *reinterpret_cast<uint4*>(o + row * p.ldp) = *reinterpret_cast<const uint4*>(own + row * 64 + ((unit ^ (row >> 1 & 3)) << 4));
+        }
+        __syncwarp();
+    }
+    // registers 16 h + 4 k + 2 e + b of rows 8 k + ..: k = 0, 1 are the first 16 rows
+    float g[16], u[16];
+    exchange<32>(v, g, u, [](int i) { return (i & 7) + 2 * (i & 8); }, [](int i) { return (i & 7) + 2 * (i & 8) + 8; }, lane, quarter, group, own, staging);
+    gate<true, 16>(p.activation, g, u);
+    uint32_t two[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) two[i] = narrow_pair(g[2 * i], g[2 * i + 1], p.out_type);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int row = 8 * k + (lane & 7);
+        store_blocks_t(own + row * 64 + (((lane >> 3) ^ (row >> 1 & 3)) << 4), two[2 * k], two[2 * k + 1], two[4 + 2 * k], two[4 + 2 * k + 1]);
+    }
+    __syncwarp();
+    uint16_t* o = static_cast<uint16_t*>(p.out) + (row0 + half * 16) * p.ldo + m + unit * 8;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int row = i * 8 + (lane >> 2);
+        if (half * 16 + row < n && unit * 8 < lanes)
+            *reinterpret_cast<uint4*>(o + row * p.ldo) = *reinterpret_cast<const uint4*>(own + row * 64 + ((unit ^ (row >> 1 & 3)) << 4));
+    }
+    __syncwarp();
+}
+
+// W columns of a tile's sums in 32 lanes: of 16-bit operands, or the accumulators of float32 parts by size.
+template <class R, int NT, int PL, int W>
+__device__ __forceinline__ void load_sums(uint32_t from, float (&v)[W]) {
+    if constexpr (PL > 1) {
+        float lo[W];
+        tmem_load(from + NT, v);
+        if constexpr (R::ROW3) tmem_load(from + 2 * NT, lo);
+        tmem_wait(v);
+        if constexpr (R::ROW3) {
+            tmem_wait(lo);
+#pragma unroll
+            for (int j = 0; j < W; ++j) v[j] += lo[j];
+        }
+        tmem_load(from, lo);
+        tmem_wait(lo);
+#pragma unroll
+        for (int j = 0; j < W; ++j) v[j] += lo[j];
+    } else {
+        tmem_load(from, v);
+        tmem_wait(v);
+    }
+}
+
+// ---------------------------------------------------------------------------
 
 // The adapters' part of a tile, by the float32 pipes while the tensor cores
 // work on: v[j] = sum_k u[row c + j, k] b[l_j, m, k] for 8 rows of this
@@ -890,6 +1055,9 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                const __grid_constant__ CUtensorMap map_b) {
     using R = Ring<MODE, NT, PL, CG, TENSOR>;
     static_assert(CG == 1 || (TENSOR && PL == 1), "pairs take their operands as they are copied");
+    constexpr bool GATED = MODE == PRODUCT_GATED;
+    static_assert(!GATED || TENSOR, "operands that tensor copies cannot take are gated by a kernel of their own");
+    constexpr int LANES = GATED ? MT / 2 : MT;
     constexpr int HALVES = PL == 1 ? 1 : 2;          // copies of 128 bytes that make 64 values
     extern __shared__ unsigned char raw[];
     unsigned char* stages = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
@@ -910,7 +1078,7 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
     uint32_t* low_strange = tmem_at + 20;                        // infinities or NaN were kept out of a low-rank part
     int* tile_adapter = reinterpret_cast<int*>(tmem_at + 32);    // [NT], the drain warps'
     int* low_adapter = tile_adapter + NT;                        // [NT], the low-rank warps'
-    if (PL > 1) staging = reinterpret_cast<unsigned char*>(near);
+    if (PL > 1 && !GATED) staging = reinterpret_cast<unsigned char*>(near);
     // a part of a split tile's sum [columns][128 lanes], where the stages were once its MMAs are done
     float* cluster_part = reinterpret_cast<float*>(stages);
     static_assert(R::STAGES * R::STAGE >= NT * MT * 4, "room for a part");
@@ -966,7 +1134,7 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
     if (MODE == PRODUCT_WEIGHTS) items = static_cast<uint32_t>(min(int64_t(pre[p.S]), p.S + p.R / a.chunk) * (a.mtiles * a.ntiles));
     else if (MODE == PRODUCT_ADAPTERS) items = static_cast<uint32_t>(a.row_tiles * a.mtiles * a.parts);
     else items = static_cast<uint32_t>((p.S > 0 ? min(int64_t(pre[p.S]), a.row_tiles) : 0) * a.mtiles * a.parts);
-    constexpr bool KEEPS = MODE == PRODUCT_FORWARD && PL == 3 && R::STAGES == 2;      // see Kept
+    constexpr bool KEEPS = (MODE == PRODUCT_FORWARD || GATED) && PL == 3 && R::STAGES == 2;      // see Kept
     if ((MODE != PRODUCT_ADAPTERS && !is_near) || (KEEPS && a.kblocks <= 2 && a.mtiles == 1 && !split)) {
         // many segments, whose prefix is in memory: neighbouring items, so that
         // the next one's segment is found by a step or two instead of a search;
@@ -982,8 +1150,8 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
 
     // Extents of a tile: lanes of this CTA that exist, columns, and columns per CTA.
     auto lanes_of = [&](const Item& t) {
-        const int64_t left = a.cols_m - t.m0 - rank * MT;
-        return static_cast<int>(left < MT ? (left < 0 ? 0 : left) : MT);
+        const int64_t left = a.cols_m - t.m0 - rank * LANES;
+        return static_cast<int>(left < LANES ? (left < 0 ? 0 : left) : LANES);
     };
     auto columns_of = [&](const Item& t) {
         return MODE == PRODUCT_WEIGHTS ? static_cast<int>(a.cols_n - t.n0 < NT ? a.cols_n - t.n0 : NT) : t.rows;
@@ -1009,15 +1177,16 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                 item_at<MODE, NT, CG>(a, beg, pre, i, t);
                 const uint32_t blocks = t.kb1 > t.kb0 ? t.kb1 - t.kb0 : 0;
                 const int columns = columns_of(t), share = share_of(columns), lanes = lanes_of(t);
-                const int a_boxes = a_outer ? (lanes + 63) / 64 : (lanes + MT - 1) / MT;
+                const int a_boxes = GATED ? (lanes > 0 ? 2 : 0) : a_outer ? (lanes + 63) / 64 : (lanes + MT - 1) / MT;
                 const int b_boxes = b_outer ? (share + 63) / 64 : (share + a.box_rows - 1) / a.box_rows;
                 const uint32_t a_bytes = a_boxes * (a_outer ? 8192 : a.a_rows * 128) * HALVES * (twin ? 2 : 1), b_bytes = b_boxes * (b_outer ? 8192 : a.box_rows * 128) * HALVES;
-                const int m0 = t.m0 + rank * MT;
+                const int m0 = t.m0 + rank * LANES;
                 uint32_t other_bytes = 0;
                 if (CG == 2) {
-                    const int64_t left = a.cols_m - t.m0 - MT;
-                    const int other = static_cast<int>(left < MT ? (left < 0 ? 0 : left) : MT);
-                    other_bytes = b_bytes + (a_outer ? (other + 63) / 64 * 8192 : (other + MT - 1) / MT * a.a_rows * 128);
+                    const int64_t left = a.cols_m - t.m0 - LANES;
+                    const int other = static_cast<int>(left < LANES ? (left < 0 ? 0 : left) : LANES);
+                    other_bytes = b_bytes + (GATED ? (other > 0 ? 2 : 0) * (a_outer ? 8192 : a.a_rows * 128)
+                                                   : a_outer ? (other + 63) / 64 * 8192 : (other + MT - 1) / MT * a.a_rows * 128);
                 }
                 int64_t m = t.seg;
                 if (MODE == PRODUCT_FORWARD && p.index) m = __ldg(p.index + t.seg);
@@ -1047,6 +1216,12 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                         } else {
                             const int r0 = t.row0 + rank * share, k0 = kb * KB;
                             if (keep) {
+                            } else if (GATED) {
+                                // the two projections' 64 columns, one after the other
+                                for (int x = 0; x < a_boxes; ++x) {
+                                    if (a_outer) tensor_load_4d<CG>(da + x * 8192, &map_a, m0 + h * 32, x, k0, static_cast<int>(m), bar);
+                                    else tensor_load_4d<CG>(da + x * 8192, &map_a, k0 + h * 32, m0, x, static_cast<int>(m), bar);
+                                }
                             } else if (twin) {
                                 for (int x = 0; x < 2; ++x)
                                     tensor_load_3d<CG>(da + x * 8192, &map_a, a_outer ? m0 + h * 32 : k0 + h * 32, a_outer ? k0 : m0, static_cast<int>(m), bar);
@@ -1083,7 +1258,7 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
         for (uint32_t i = first; ok && i < items; i += stride) {
             item_at<MODE, NT, CG>(a, beg, pre, i, t);
             const int share = share_of(columns_of(t)), lanes = lanes_of(t);
-            const int a_rows = twin ? (a_outer ? MT : 64 + a.a_rows) : a_outer ? (lanes + 63) & ~63 : a.a_rows, b_rows = b_outer ? (share + 63) & ~63 : share;
+            const int a_rows = twin || GATED ? (a_outer ? MT : 64 + a.a_rows) : a_outer ? (lanes + 63) & ~63 : a.a_rows, b_rows = b_outer ? (share + 63) & ~63 : share;
             int64_t m = t.seg;
             if (MODE == PRODUCT_FORWARD && p.index) m = __ldg(p.index + t.seg);
             for (int kb = t.kb0; kb < t.kb1; ++kb) {
@@ -1320,13 +1495,18 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
         constexpr bool AHEAD = PL == 1;      // the next ones are loaded before these are stored, where registers allow
         unsigned char* const own_staging = staging + (warp - EPI_WARP) * R::STAGING;
         [[maybe_unused]] LowRank<PL, R::LOW> low(p, tile_adapter, own_staging, lane);
-        if (MODE == PRODUCT_FORWARD && !p.index) {
+        if ((MODE == PRODUCT_FORWARD && !p.index) || GATED) {
             // rows in no segment
             const int b = p.S > 0 ? beg[0] : 0, e = p.S > 0 ? beg[p.S] : 0;
             const int64_t none = b + (p.R - (e > b ? e : b));
             const int64_t each = static_cast<int64_t>(gridDim.x) * (EPW * 32);
             for (int64_t i = blockIdx.x * (EPW * 32) + td; i < none * p.N; i += each) {
                 const int64_t q = i / p.N, c = i - q * p.N, r = q < b ? q : (e > b ? e : b) + (q - b);
+                if constexpr (GATED) {
+                    if (p.pre && p.pre_type == PT_F32) static_cast<float*>(p.pre)[r * p.ldp + c] = 0.0f;
+                    else if (p.pre) static_cast<uint16_t*>(p.pre)[r * p.ldp + c] = 0;
+                    if (c >= a.cols_m) continue;
+                }
                 if (p.out_type == PT_F32) static_cast<float*>(p.out)[r * p.ldo + c] = 0.0f;
                 else static_cast<uint16_t*>(p.out)[r * p.ldo + c] = 0;
             }
@@ -1341,6 +1521,40 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
             item_at<MODE, NT, CG>(a, beg, pre, i, t);
             const bool summed = t.kb1 > t.kb0;
             const int n_left = columns_of(t);
+            if constexpr (GATED) {
+                // (warps that exchange values meet at barriers: all give up together)
+                if (summed && !bar_drain_all(wait_for<CG>(acc_full + buf, bph, p.status))) break;
+                tc_fence_after();
+                const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * R::ACC;
+                const int64_t m = t.m0 + rank * LANES + (quarter & 1) * 32;
+                const int lanes = static_cast<int>(a.cols_m - m < 32 ? a.cols_m - m : 32);      // may be negative
+                if (split) {
+                    for (int c = group * W; c < n_left; c += ROWS) {
+                        float v[W];
+                        if (summed) load_sums<R, NT, PL, W>(from + c, v);
+                        else
+#pragma unroll
+                            for (int j = 0; j < W; ++j) v[j] = 0.0f;
+                        store_rows(cluster_part + quarter * 32 + c * MT + lane, MT, v, n_left - c, [](float x) { return x; });
+                    }
+                } else if (lanes > 0 && BLOCKS && a.wide_rows && (!p.pre || p.pre_type == PT_F32 || a.wide_pre)) {
+                    for (int c = group * 32; c < n_left; c += EPW / 4 * 32)
+                        gate_blocks(a, from + c, t.row0 + c, n_left - c, m, lanes, lane, quarter, group, own_staging, R::STAGING);
+                } else if (lanes > 0) {
+                    for (int c = group * W; c < n_left; c += ROWS) {
+                        float v[W];
+                        load_sums<R, NT, PL, W>(from + c, v);
+                        gate_rows<PL == 1, W>(a, v, t.row0 + c, n_left - c, m, lanes, lane, quarter, group, own_staging, R::STAGING);
+                    }
+                }
+                if (summed) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) lead_arrive<CG>(acc_empty + buf, lead, false);
+                    if ((buf ^= 1) == 0) bph ^= 1;
+                }
+                continue;
+            }
             const int64_t m = t.m0 + rank * MT + (twin ? quarter & 1 : quarter) * 32;           // the warp's first lane
             const int lanes = static_cast<int>(a.cols_m - m < 32 ? a.cols_m - m : 32);   // may be negative
             const int64_t slot = (t.slot * CG + rank) * NT * MT + quarter * 32;      // in floats
@@ -1503,6 +1717,30 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
             const int quarter = (warp - EPI_WARP) & 3, group = (warp - EPI_WARP) / 4;
             Item t;
             item_at<MODE, NT, CG>(a, beg, pre, first, t);
+            if constexpr (GATED) {
+                // both projections of 32 columns of some rows
+                const int64_t m = t.m0 + rank * LANES + (quarter & 1) * 32;
+                const int lanes = static_cast<int>(a.cols_m - m < 32 ? a.cols_m - m : 32);
+                for (int c = (t.part * EPW / 2 + group * 2 + (quarter >> 1)) * W; c < t.rows; c += t.parts * EPW / 2 * W) {
+                    const int n = t.rows - c < W ? t.rows - c : W;
+                    float v[2][W];
+#pragma unroll
+                    for (int j = 0; j < W; ++j) v[0][j] = v[1][j] = 0.0f;
+#pragma unroll 4
+                    for (int q = 0; q < t.parts; ++q) {
+                        const uint32_t from = cluster_addr(cluster_part + c * MT + (quarter & 1) * 32 + lane, q * CG + rank);
+#pragma unroll
+                        for (int j = 0; j < W; ++j)
+                            if (j < n) v[0][j] += cluster_load(from + j * MT * 4), v[1][j] += cluster_load(from + (j * MT + LANES) * 4);
+                    }
+                    if (lane >= lanes) continue;
+                    if (p.pre)
+                        for (int h = 0; h < 2; ++h)
+                            store_any(p.pre, p.pre_type, (int64_t(t.row0) + c) * p.ldp + h * a.cols_m + m + lane, p.ldp, v[h], n);
+                    gate<PL == 1, W>(p.activation, v[0], v[1]);
+                    store_any(p.out, p.out_type, (int64_t(t.row0) + c) * p.ldo + m + lane, p.ldo, v[0], n);
+                }
+            } else {
             const int64_t m = t.m0 + rank * MT + quarter * 32;
             const int lanes = static_cast<int>(a.cols_m - m < 32 ? a.cols_m - m : 32);
             const float factor = MODE == PRODUCT_FORWARD && p.scale ? __ldg(p.scale + __ldg(p.index + t.seg)) : 1.0f;
@@ -1521,6 +1759,7 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
 #pragma unroll
                 for (int j = 0; j < W; ++j) v[j] *= factor;
                 store_result(a, (int64_t(t.row0) + c) * p.ldo + m, p.ldo, v, n, lanes, lane, staging + (warp - EPI_WARP) * R::STAGING);
+            }
             }
         }
     }
@@ -1761,6 +2000,23 @@ bool make_map(CUtensorMap* map, int type, const void* base, int64_t cols, int64_
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Both projections' columns of the gated block's matrices, a box of 64 values x
+// box_rows (the contiguous dimension's 64, or 32 float32, come first): [N, K] by
+// projection and segment, or K rows of the two projections' N by segment.
+bool make_gated_map(CUtensorMap* map, const ProductParams& p, int64_t half, int box_rows) {
+    const EncodeFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t n = p.N / 2, k = p.K, size = p.type == PT_F32 ? 4 : 2;
+    const cuuint64_t stride = p.S > 1 ? p.stride_w : (p.trans ? 2 * half : p.K * p.ldw);
+    const cuuint32_t wide = 128 / static_cast<cuuint32_t>(size), rows = static_cast<cuuint32_t>(box_rows);
+    const cuuint64_t dims_t[4] = {k, n, 2, cuuint64_t(p.S)}, dims[4] = {n, 2, k, cuuint64_t(p.S)};
+    const cuuint64_t strides_t[3] = {p.ldw * size, half * size, stride * size}, strides[3] = {half * size, p.ldw * size, stride * size};
+    const cuuint32_t box_t[4] = {wide, rows, 1, 1}, box[4] = {wide, 1, KB, 1}, each[4] = {1, 1, 1, 1};
+    return fn(map, p.type == PT_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : p.type == PT_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+              const_cast<void*>(p.w), p.trans ? dims_t : dims, p.trans ? strides_t : strides, p.trans ? box_t : box, each, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // What a tensor map can describe: 16-byte aligned, strides multiples of 16 bytes and below 2^40.
 bool tensor_copyable(const void* base, int64_t stride, int type) {
     return reinterpret_cast<uintptr_t>(base) % 16 == 0 && stride % (type == PT_F32 ? 4 : 8) == 0 && stride < (int64_t(1) << 37);
@@ -1783,6 +2039,8 @@ cudaError_t launch_shape(const KernelArgs& a, const ProductPlan& plan, cudaStrea
         bool ok;
         if (MODE == PRODUCT_WEIGHTS) {
             ok = make_map(&ma, p.type, p.w, p.N, p.R, p.ldw, 0, 0, KB) && make_map(&mb, p.type, p.x, p.K, p.R, p.ldx, 0, 0, KB);
+        } else if (MODE == PRODUCT_GATED) {
+            ok = make_gated_map(&ma, p, a.half_w, a.a_rows) && make_map(&mb, p.type, p.x, p.K, p.R, p.ldx, 0, 0, a.box_rows);
         } else {
             const int64_t mats = MODE == PRODUCT_ADAPTERS ? 1 : (p.index ? p.L : p.S);
             const int64_t rows = p.trans ? p.N : p.K, cols = p.trans ? p.K : p.N;
@@ -1876,6 +2134,9 @@ MatShape w_shape(int mode, const ProductParams& p) {
     return {p.index ? p.L : p.S, p.trans ? p.N : p.K, p.trans ? p.K : p.N};
 }
 
+// The gated block's two projections are copied apart: with contiguous columns each starts on a boundary of its own.
+bool halves_apart(int mode, const ProductParams& p) { return mode == PRODUCT_GATED && !p.trans; }
+
 int64_t packed_row(int64_t cols, int type) { return ceil_to(cols * (type == PT_F32 ? 4 : 2), 16) * 16; }   // bytes
 
 }  // namespace
@@ -1885,10 +2146,11 @@ int product_tile_columns(const ProductParams& p, const ProductPlan& plan) { retu
 ProductPlan plan_product(int mode, const ProductParams& p) {
     ProductPlan d{};
     const bool weights = mode == PRODUCT_WEIGHTS;
-    const int64_t mats = mode == PRODUCT_FORWARD ? (p.index ? p.L : p.S) : 1;
+    const int64_t mats = mode == PRODUCT_FORWARD || mode == PRODUCT_GATED ? (p.index ? p.L : p.S) : 1;
     d.empty = p.K == 0 || p.R == 0 || mats == 0;
     const bool copy_x = tensor_copyable(p.x, p.ldx, p.type);
-    const bool copy_w = tensor_copyable(p.w, p.ldw, p.type) && (mats == 1 || tensor_copyable(p.w, p.stride_w, p.type));
+    const bool copy_w = tensor_copyable(p.w, p.ldw, p.type) && (mats == 1 || tensor_copyable(p.w, p.stride_w, p.type)) &&
+                        (!halves_apart(mode, p) || p.N / 2 % (p.type == PT_F32 ? 4 : 8) == 0);
     const int64_t segments = mode == PRODUCT_ADAPTERS ? 1 : p.S;
     // An operand that tensor copies cannot take is laid out again first (one
     // more pass over it), except where most matrices are in no use: then the
@@ -1953,9 +2215,14 @@ ProductPlan plan_product(int mode, const ProductParams& p) {
     d.prefix_bytes = mode != PRODUCT_ADAPTERS && p.S > NEAR_SEGMENTS ? ceil_to((p.S + 1) * 8, 256) * 256 : 0;
     d.partial_bytes = ceil_to(slots * cg * NT * MT * 4, 256) * 256;
     d.staged = !d.empty && !weights && p.out_type != PT_F32 && d.parts == 1 && p.K > LONGEST;
+    // gated: the accumulators hold the whole sum (see LONGEST, and KernelArgs::flush)
+    d.fused = d.tensor && !d.staged && (p.type != PT_F32 || d.parts > 1 || d.part_blocks <= FLUSH_F32);
     if (d.staged) d.staged_bytes = ceil_to(p.R * p.N * 4, 256) * 256;
     if (d.pack_x) d.pack_x_bytes = ceil_to(packed_row(p.K, p.type) * p.R, 256) * 256;
-    if (d.pack_w) d.pack_w_bytes = packed_row(w_shape(mode, p).cols, p.type) * w_shape(mode, p).rows * w_shape(mode, p).mats;
+    if (d.pack_w) {
+        const MatShape m = w_shape(mode, p);
+        d.pack_w_bytes = (halves_apart(mode, p) ? 2 * packed_row(m.cols / 2, p.type) : packed_row(m.cols, p.type)) * m.rows * m.mats;
+    }
     return d;
 }
 
@@ -1975,7 +2242,9 @@ bool lora_by_rows(const ProductParams& p) {
 
 namespace {
 
-cudaError_t launch_pack(const void* src, int64_t ld, int64_t stride, const MatShape& m, int size, void* dst, int sms, cudaStream_t stream) {
+// row_bytes: from one packed row to the next, 0: as they need.
+cudaError_t launch_pack(const void* src, int64_t ld, int64_t stride, const MatShape& m, int size, void* dst, int sms, cudaStream_t stream,
+                        int64_t row_bytes = 0) {
     PackArgs a{};
     a.src = src;
     a.dst = static_cast<unsigned char*>(dst);
@@ -1984,9 +2253,10 @@ cudaError_t launch_pack(const void* src, int64_t ld, int64_t stride, const MatSh
     a.rows = m.rows;
     a.total = m.rows * m.mats;
     a.cols = m.cols;
-    a.row_bytes = packed_row(m.cols, size == 4 ? PT_F32 : PT_F16);
+    const int64_t own_bytes = packed_row(m.cols, size == 4 ? PT_F32 : PT_F16);
+    a.row_bytes = row_bytes > 0 ? row_bytes : own_bytes;
     a.lanes = 4;
-    while (a.lanes < 32 && a.lanes * 16 < a.row_bytes) a.lanes *= 2;
+    while (a.lanes < 32 && a.lanes * 16 < own_bytes) a.lanes *= 2;
     const int64_t blocks = std::min<int64_t>(ceil_to(a.total * a.lanes, 256), int64_t(sms) * 16);
     if (size == 4) pack_kernel<uint32_t><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(a);
     else pack_kernel<uint16_t><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(a);
@@ -2009,6 +2279,11 @@ cudaError_t launch_product(int mode, const ProductParams& given, const ProductPl
         // nothing to sum: zeros
         const size_t size = p.out_type == PT_F32 ? 4 : 2;
         if (mode == PRODUCT_WEIGHTS) return cudaMemsetAsync(p.out, 0, size * p.S * p.K * p.N, stream);
+        if (mode == PRODUCT_GATED) {
+            const size_t pre_size = p.pre_type == PT_F32 ? 4 : 2;
+            const cudaError_t e = p.pre ? cudaMemset2DAsync(p.pre, pre_size * p.ldp, 0, pre_size * p.N, p.R, stream) : cudaSuccess;
+            return e != cudaSuccess ? e : cudaMemset2DAsync(p.out, size * p.ldo, 0, size * (p.N / 2), p.R, stream);
+        }
         return cudaMemset2DAsync(p.out, size * p.ldo, 0, size * p.N, p.R, stream);
     }
     unsigned char* packed = p.ws + plan.prefix_bytes + plan.partial_bytes + plan.staged_bytes;
@@ -2026,12 +2301,24 @@ cudaError_t launch_product(int mode, const ProductParams& given, const ProductPl
         p.ldx = packed_row(p.K, p.type) / size;
         packed += plan.pack_x_bytes;
     }
+    int64_t half_w = p.trans ? p.N / 2 * p.ldw : p.N / 2;
     if (plan.pack_w) {
-        const MatShape m = w_shape(mode, p);
-        const cudaError_t e = launch_pack(p.w, p.ldw, p.stride_w, m, size, packed, p.sms, stream);
+        MatShape m = w_shape(mode, p);
+        int64_t row = packed_row(m.cols, p.type);
+        cudaError_t e = cudaSuccess;
+        if (halves_apart(mode, p)) {
+            m.cols /= 2;
+            half_w = packed_row(m.cols, p.type) / size;
+            row = 2 * half_w * size;
+            for (int h = 0; e == cudaSuccess && h < 2; ++h)
+                e = launch_pack(static_cast<const unsigned char*>(p.w) + h * m.cols * size, p.ldw, p.stride_w, m, size, packed + h * half_w * size, p.sms, stream, row);
+        } else {
+            e = launch_pack(p.w, p.ldw, p.stride_w, m, size, packed, p.sms, stream);
+            if (mode == PRODUCT_GATED) half_w = p.N / 2 * (row / size);
+        }
         if (e != cudaSuccess) return e;
         p.w = packed;
-        p.ldw = packed_row(m.cols, p.type) / size;
+        p.ldw = row / size;
         p.stride_w = m.rows * p.ldw;
     }
     KernelArgs a{};
@@ -2041,23 +2328,27 @@ cudaError_t launch_product(int mode, const ProductParams& given, const ProductPl
     a.parts = plan.parts;
     a.part_blocks = plan.part_blocks;
     a.kblocks = static_cast<int32_t>(ceil_to(p.K, KB));
-    a.box_rows = plan.narrow && p.R <= 32 * (mode == PRODUCT_FORWARD ? p.S : 1) ? 16 : 64;
-    a.a_rows = static_cast<int32_t>(std::min<int64_t>(MT, ceil_to(p.N, 16) * 16));
+    const bool gated = mode == PRODUCT_GATED;
+    a.box_rows = plan.narrow && p.R <= 32 * (mode == PRODUCT_FORWARD || gated ? p.S : 1) ? 16 : 64;
+    a.a_rows = static_cast<int32_t>(gated ? std::min<int64_t>(MT / 2, ceil_to(p.N / 2, 16) * 16) : std::min<int64_t>(MT, ceil_to(p.N, 16) * 16));
+    a.half_w = half_w;
     if (plan.parts > 1) a.flush = NEVER_FLUSH;                 // a part is short enough
-    else if (p.type == PT_F32) a.flush = 8;
+    else if (p.type == PT_F32) a.flush = FLUSH_F32;
     else if (p.out_type != PT_F32) a.flush = NEVER_FLUSH;      // the sum is
     else a.flush = mode == PRODUCT_WEIGHTS ? 12 : LONGEST / KB;
     const int64_t out_step = mode == PRODUCT_WEIGHTS ? p.N : p.ldo;
-    a.wide_rows = p.N % 8 == 0 && out_step % 8 == 0 && reinterpret_cast<uintptr_t>(p.out) % 16 == 0;
+    a.wide_rows = (gated ? p.N / 2 : p.N) % 8 == 0 && out_step % 8 == 0 && reinterpret_cast<uintptr_t>(p.out) % 16 == 0;
+    a.wide_pre = p.N / 2 % 8 == 0 && p.ldp % 8 == 0 && reinterpret_cast<uintptr_t>(p.pre) % 16 == 0;
     a.twin = p.type == PT_F32 && p.N <= MT / 2 && plan.parts == 1;
     a.chunk = plan.chunk;
     a.add_by_start = plan.add_by_start;
     a.row_tiles = plan.row_tiles;
-    a.cols_m = p.N;
+    a.cols_m = gated ? p.N / 2 : p.N;
     a.cols_n = p.K;
     a.far = reinterpret_cast<int*>(p.ws);
     a.partials = reinterpret_cast<float*>(p.ws + plan.prefix_bytes);
     if (mode == PRODUCT_WEIGHTS) return launch_mode<PRODUCT_WEIGHTS>(a, plan, stream);
+    if (gated) return plan.fused ? launch_mode<PRODUCT_GATED>(a, plan, stream) : cudaErrorInvalidConfiguration;
     const cudaError_t e = mode == PRODUCT_FORWARD ? launch_mode<PRODUCT_FORWARD>(a, plan, stream) : launch_mode<PRODUCT_ADAPTERS>(a, plan, stream);
     if (e != cudaSuccess || !plan.staged) return e;
     const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(ceil_to(p.R * p.N, 1024), int64_t(p.sms) * 8));

@@ -6,8 +6,9 @@
 //   weights   dw[s, k, n] = sum_r x[r, k] * dy[r, n]       over the rows of s
 //   adapters  y[r, n]     = sum_k x[r, k] * w[n, k]
 //                           + scale[l] * sum_j (sum_k x[r, k] * a[l, j, k]) * b[l, n, j]
+//   gated     y[r, n]     = act(sum_k x[r, k] * w[s, k, n]) * sum_k x[r, k] * w[s, k, N / 2 + n]
 //
-// All three sum in float32 and round once to the output's type.
+// All sum in float32 and round once to the output's type.
 #pragma once
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -33,6 +34,10 @@ struct ProductParams {
     const void* b;          // [L][N, rank]
     int64_t rank;
     int32_t overlap;        // u's kernel lets this one start beside it
+    // gated: N counts the columns of both projections, out has N / 2
+    void* pre;              // [R, N], row stride ldp, or NULL: the sums before the activation
+    int64_t ldp;
+    int32_t pre_type, activation;      // pre_type: PT_F32, or type
     // library-owned
     unsigned char* ws;      // see ProductPlan
     unsigned int* status;   // device status word
@@ -54,13 +59,14 @@ struct ProductPlan {
     int64_t chunk;          // weights: rows per part of a segment
     int32_t add_blocks;     // weights: blocks of the kernel that adds the parts (0: no segment can be split)
     int32_t add_by_start;   // weights: those blocks stand for `chunk` rows each, not for a segment each
+    int32_t fused;          // gated: the kernel applies the activation (0: it cannot, the sums come in pieces or by the loader warps)
     int32_t staged;         // forward, adapters: the sums are kept in float32 scratch and rounded by a kernel of their own
     int64_t row_tiles;      // forward: most row tiles there can be
     int64_t prefix_bytes, partial_bytes, staged_bytes, pack_x_bytes, pack_w_bytes;   // the workspace, in this order
     int64_t bytes() const { return prefix_bytes + partial_bytes + staged_bytes + pack_x_bytes + pack_w_bytes; }
 };
 
-enum : int { PRODUCT_FORWARD = 0, PRODUCT_WEIGHTS = 1, PRODUCT_ADAPTERS = 2 };
+enum : int { PRODUCT_FORWARD = 0, PRODUCT_WEIGHTS = 1, PRODUCT_ADAPTERS = 2, PRODUCT_GATED = 3 };
 
 ProductPlan plan_product(int mode, const ProductParams& p);
 // Columns of the tile that `plan` counts in and that is launched for it.

@@ -93,7 +93,7 @@ __device__ __forceinline__ void arrive_both(uint64_t* bar, uint32_t lead, bool m
     if (CG == 2) lead_arrive<CG>(bar, lead + 1, memory);
 }
 
-// One box of a 2-D / 3-D tensor into this CTA's shared memory; zero where the
+// One box of a 2-D, 3-D or 4-D tensor into this CTA's shared memory; zero where the
 // box is outside the tensor.  Completes on `bar`: this CTA's, or (CG == 2)
 // either CTA's.
 template <int CG>
@@ -124,6 +124,21 @@ __device__ __forceinline__ void tensor_load_3d(void* dst, const CUtensorMap* map
             "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
                 smem_u32(dst)),
             "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+            : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void tensor_load_4d(void* dst, const CUtensorMap* map, int32_t c0, int32_t c1, int32_t c2, int32_t c3, uint32_t bar) {
+    if constexpr (CG == 2)
+        asm volatile(
+            "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+                smem_u32(dst)),
+            "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+                smem_u32(dst)),
+            "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
             : "memory");
 }
 __device__ __forceinline__ void tensor_prefetch(const CUtensorMap* map) {

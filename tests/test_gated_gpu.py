@@ -125,6 +125,13 @@ def test_sizes(dtype, trans, k, n):
     dy = normal(g, out.shape, dtype)
     dx, dw = sr.seg_gated_grad(x, w, pre, dy, do, act, transpose_w=trans)
     check_grad(dx, dw, x, w, pre, dy, off, trans, act, (dtype, trans, k, n, act))
+    if dtype != "float32":
+        # products kept in 16 bits
+        assert pre.dtype == torch.float32
+        same, half = sr.seg_gated(x, w, do, act, transpose_w=trans, pre=torch.empty(pre.shape, dtype=x.dtype, device="cuda"))
+        assert torch.equal(same, out) and torch.equal(half, pre.to(x.dtype))
+        dx, dw = sr.seg_gated_grad(x, w, half, dy, do, act, transpose_w=trans)
+        check_grad(dx, dw, x, w, half, dy, off, trans, act, (dtype, trans, k, n, act, "half"))
     assert sr.device_status() == 0
 
 
@@ -214,7 +221,8 @@ def test_strides_and_alignment(dtype, trans):
         x = normal(g, (rows, xcols), dtype)[:, xat:xat + k]
         w = normal(g, (s, 2 * n, wcols) if trans else (s, k, wcols + 0), dtype, k ** -0.5)
         w = w[:, :, :k] if trans else w[:, :, wat:wat + 2 * n] if wcols >= wat + 2 * n else w[:, :, :2 * n]
-        big, pres = torch.full((rows, ocols), 7.0, dtype=x.dtype, device="cuda"), torch.full((rows, 2 * n + 9), 7.0, dtype=x.dtype, device="cuda")
+        ptype = torch.float32 if xat == 0 else x.dtype
+        big, pres = torch.full((rows, ocols), 7.0, dtype=x.dtype, device="cuda"), torch.full((rows, 2 * n + 9), 7.0, dtype=ptype, device="cuda")
         out, pre = big[:, oat:oat + n], pres[:, 3:3 + 2 * n]
         sr.seg_gated(x, w, do, transpose_w=trans, out=out, pre=pre)
         check_forward(out, pre, x, w, off, trans, "silu", (dtype, xat))

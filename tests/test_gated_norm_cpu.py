@@ -13,25 +13,25 @@ def lib():
 
 
 def test_gated_host_checks(lib):
-    def call(x=64, dtype=4, R=10, K=8, ldx=8, w=64, N=16, ldw=32, stride=256, trans=0, off=64, odt=1, S=3, act=0, out=64, ldo=16, pre=64, ldp=32):
-        return lib.seg_gated(x, dtype, R, K, ldx, w, N, ldw, stride, trans, off, odt, S, act, out, ldo, pre, ldp, None)
+    def call(x=64, dtype=4, R=10, K=8, ldx=8, w=64, N=16, ldw=32, stride=256, trans=0, off=64, odt=1, S=3, act=0, out=64, ldo=16, pre=64, pt=None, ldp=32):
+        return lib.seg_gated(x, dtype, R, K, ldx, w, N, ldw, stride, trans, off, odt, S, act, out, ldo, pre, dtype if pt is None else pt, ldp, None)
     assert call(R=0) == 0 and call(N=0, ldw=0, ldo=0, stride=0, ldp=0) == 0      # nothing to do
     assert call(R=0, pre=None, ldp=0) == 0
     for bad in (dict(dtype=0), dict(dtype=5), dict(odt=2), dict(R=-1), dict(K=-1), dict(N=-1), dict(S=-1), dict(act=-1), dict(act=5),
                 dict(ldx=7), dict(ldw=31), dict(ldo=15), dict(ldp=31), dict(trans=2), dict(stride=255), dict(stride=-1),
                 dict(trans=1, ldw=7), dict(trans=1, ldw=8, stride=255), dict(x=None), dict(w=None), dict(off=None), dict(out=None),
-                dict(x=65), dict(w=65), dict(out=65), dict(pre=65), dict(off=68), dict(dtype=2, x=66), dict(dtype=2, out=66), dict(dtype=2, pre=66)):
+                dict(x=65), dict(w=65), dict(out=65), dict(pre=65), dict(pt=3), dict(pt=2, pre=66), dict(dtype=2, pt=4), dict(off=68), dict(dtype=2, x=66), dict(dtype=2, out=66), dict(dtype=2, pre=66)):
         assert call(**bad) == 1, bad
     for bad in (dict(R=1 << 31), dict(S=1 << 31), dict(K=(1 << 20) + 1, ldx=1 << 21, stride=1 << 40), dict(N=(1 << 19) + 1, ldw=1 << 21, stride=1 << 40, ldo=1 << 21, ldp=1 << 21)):
         assert call(**bad) == 2, bad
 
 
 def test_gated_grad_host_checks(lib):
-    def call(pre=64, dtype=3, R=10, N=16, ldp=32, dy=64, ldy=16, act=1, dpre=64, ldd=32):
-        return lib.seg_gated_grad(pre, dtype, R, N, ldp, dy, ldy, act, dpre, ldd, None)
+    def call(pre=64, pt=2, R=10, N=16, ldp=32, dy=64, dtype=3, ldy=16, act=1, dpre=64, ldd=32):
+        return lib.seg_gated_grad(pre, pt, R, N, ldp, dy, dtype, ldy, act, dpre, ldd, None)
     assert call(R=0) == 0 and call(N=0, ldp=0, ldy=0, ldd=0) == 0
     for bad in (dict(dtype=1), dict(R=-1), dict(N=-1), dict(ldp=31), dict(ldy=15), dict(ldd=31), dict(act=9), dict(pre=None), dict(dy=None),
-                dict(dpre=None), dict(pre=65), dict(dy=65), dict(dpre=65), dict(dtype=2, dy=66)):
+                dict(dpre=None), dict(pre=66), dict(pt=4), dict(dtype=2, pt=3), dict(dy=65), dict(dpre=65), dict(dtype=2, dy=66)):
         assert call(**bad) == 1, bad
     assert call(R=1 << 31) == 2 and call(N=(1 << 19) + 1, ldp=1 << 21, ldy=1 << 21, ldd=1 << 21) == 2
 
@@ -107,7 +107,7 @@ def test_binding_refuses_arguments_that_do_not_fit():
         (ValueError, dict(w=Like(2, 8, 15))), (ValueError, dict(w=Like(8, 16))), (ValueError, dict(w=Like(2, 9, 16))), (ValueError, dict(w=Like(3, 8, 16))),
         (TypeError, dict(w=Like(2, 8, 16, dtype=torch.float16))), (ValueError, dict(x=Like(4, 8, 2))), (ValueError, dict(x=Like(4, 8, step=2))),
         (ValueError, dict(activation="swish")), (ValueError, dict(out=Like(4, 7))), (TypeError, dict(out=Like(4, 8, dtype=torch.float16))),
-        (ValueError, dict(pre=Like(4, 8))), (ValueError, dict(offsets=Like(3, 1, dtype=torch.int64))), (TypeError, dict(x=Like(4, 8, dtype=torch.float64))),
+        (ValueError, dict(pre=Like(4, 8))), (TypeError, dict(pre=Like(4, 16, dtype=torch.bfloat16))), (ValueError, dict(offsets=Like(3, 1, dtype=torch.int64))), (TypeError, dict(x=Like(4, 8, dtype=torch.float64))),
     ]
     for error, bad in gated:
         with pytest.raises(error):
