@@ -15,10 +15,12 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "seg_common.cuh"
 #include "seg_norm.cuh"
 #include "seg_product.cuh"
+#include "tc.cuh"
 
 namespace segred {
 namespace {
@@ -32,22 +34,79 @@ template <> __device__ __forceinline__ float from_float<float>(float v) { return
 template <> __device__ __forceinline__ __half from_float<__half>(float v) { return __float2half_rn(v); }
 template <> __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-// V values that are loaded and stored together.
-template <class T, int V> struct alignas(V * sizeof(T)) Pack {
-    T v[V];
-};
-template <class T, int V>
-__device__ __forceinline__ Pack<T, V> load_pack(const T* p) {
-    if constexpr (V * sizeof(T) == 16) {
-        union {
-            uint4 u;
-            Pack<T, V> x;
-        } r = {__ldg(reinterpret_cast<const uint4*>(p))};
-        return r.x;
-    } else {
-        return *reinterpret_cast<const Pack<T, V>*>(p);
+// V values that are loaded and stored together: 16 bytes, or one value.  Two
+// 16-bit values at a time are widened and narrowed (a value at a time the
+// compiler took 39 instructions a value for a whole forward pass, now 9).
+template <class T, int V> struct Pack {
+    using Raw = typename std::conditional<V * sizeof(T) == 16, uint4, T>::type;
+    Raw raw;
+    __device__ __forceinline__ void load(const T* p) { raw = __ldg(reinterpret_cast<const Raw*>(p)); }
+    __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<Raw*>(p) = raw; }
+    __device__ __forceinline__ void widen(float (&f)[V]) const {
+        if constexpr (V == 1) {
+            f[0] = to_float<T>(raw);
+        } else {
+            const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if constexpr (sizeof(T) == 4) {
+                    f[k] = __uint_as_float(w[k]);
+                } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+                    f[2 * k] = __uint_as_float(w[k] << 16);
+                    f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+                } else {
+                    const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+                    f[2 * k] = x.x, f[2 * k + 1] = x.y;
+                }
+            }
+        }
     }
-}
+    __device__ __forceinline__ void narrow(const float (&f)[V]) {
+        if constexpr (V == 1) {
+            raw = from_float<T>(f[0]);
+        } else {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if constexpr (sizeof(T) == 4) w[k] = __float_as_uint(f[k]);
+                else if constexpr (std::is_same<T, __nv_bfloat16>::value) asm("cvt.rn.bf16x2.f32 %0, %2, %1;" : "=r"(w[k]) : "f"(f[2 * k]), "f"(f[2 * k + 1]));
+                else asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(w[k]) : "f"(f[2 * k]), "f"(f[2 * k + 1]));
+            }
+            raw = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+};
+
+// What a thread needs of its next rows, on its way to shared memory while it
+// works on these: a ring of D slots of PER packs for each thread, which copies
+// and reads nothing but its own, so that no barrier is needed.  (Packs of less
+// than 16 bytes, of rows that are not aligned, and rows of which shared memory
+// does not hold two, are loaded when they are needed.)
+template <class T, int V, int PER, int NT>
+struct Ring {
+    static constexpr int D = PER == 1 ? 6 : PER == 2 ? 4 : PER <= 4 ? 3 : 2;      // fewer bytes of a slot want more of them
+    static constexpr bool ASYNC = V * sizeof(T) == 16 && D * PER * NT * 16 <= 200 * 1024;
+    static constexpr int SLOT = PER * NT * 16, BYTES = ASYNC ? D * SLOT : 0;
+    uint32_t base, at, to;      // the thread's first slot, the one to read and the one to fetch into
+    __device__ __forceinline__ explicit Ring(unsigned char* memory) : base(smem_u32(memory) + threadIdx.x * 16), at(base), to(base) {}
+    // pack j of a row
+    __device__ __forceinline__ void fetch(int j, const T* from) const {
+        if constexpr (ASYNC) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + j * NT * 16), "l"(from) : "memory");
+    }
+    __device__ __forceinline__ void fetched() {
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        to = to == base + (D - 1) * SLOT ? base : to + SLOT;
+    }
+    // the slot to read has landed
+    __device__ __forceinline__ void wait() const { asm volatile("cp.async.wait_group %0;" ::"n"(D - 2) : "memory"); }
+    __device__ __forceinline__ void get(int j, const T* from, float (&f)[V]) const {
+        Pack<T, V> x;
+        if constexpr (ASYNC) asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x.raw.x), "=r"(x.raw.y), "=r"(x.raw.z), "=r"(x.raw.w) : "r"(at + j * NT * 16) : "memory");
+        else x.load(from);
+        x.widen(f);
+    }
+    __device__ __forceinline__ void got() { at = at == base + (D - 1) * SLOT ? base : at + SLOT; }
+};
 
 // V neighbouring values of weight_type at element `at`.
 template <class T, int V>
@@ -65,9 +124,9 @@ __device__ __forceinline__ void load_weights(const void* w, bool wide, int64_t a
             for (int i = 0; i < V; ++i) f[i] = __ldg(p + i);
         }
     } else {
-        const Pack<T, V> x = load_pack<T, V>(static_cast<const T*>(w) + at);
-#pragma unroll
-        for (int i = 0; i < V; ++i) f[i] = to_float<T>(x.v[i]);
+        Pack<T, V> x;
+        x.load(static_cast<const T*>(w) + at);
+        x.widen(f);
     }
 }
 
@@ -103,97 +162,159 @@ __device__ __forceinline__ Run run_of(const NormParams& p, int64_t r) {
     return x;
 }
 
-// Sums of N values over a row's threads, to all of them.  `red`: [2][8 or 16 warps][N], used in turns.
-template <int N>
-__device__ __forceinline__ void group_sum(float (&v)[N], int group, float* red, int& turn) {
+// Sums of N values over the G threads of a row, to all of them: within a warp
+// with shuffles, then over the row's warps through shared memory, at a barrier of
+// theirs.  `red`: [2][warps of the block][N], used in turns.
+template <int G, int NT, int N>
+__device__ __forceinline__ void group_sum(float (&v)[N], float* red, int& turn) {
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-        if (d < group) {
+    for (int d = (G < 32 ? G : 32) / 2; d > 0; d >>= 1)
 #pragma unroll
-            for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], d);
-        }
-    }
-    if (group > 32) {
-        const int warps = group >> 5, warp = threadIdx.x >> 5, first = warp / warps * warps;
-        float* at = red + turn * (blockDim.x >> 5) * N;
+        for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], d);
+    if constexpr (G > 32) {
+        constexpr int WARPS = G / 32;
+        const int warp = threadIdx.x >> 5;
+        float* at = red + turn * (NT / 32) * N;
         if ((threadIdx.x & 31) == 0)
 #pragma unroll
             for (int i = 0; i < N; ++i) at[warp * N + i] = v[i];
-        asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / warps), "r"(group) : "memory");
+        if constexpr (G == NT) __syncthreads();
+        else asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / WARPS), "n"(G) : "memory");
+        at += warp / WARPS * WARPS * N;
 #pragma unroll
         for (int i = 0; i < N; ++i) v[i] = 0.0f;
-        for (int w = 0; w < warps; ++w)
 #pragma unroll
-            for (int i = 0; i < N; ++i) v[i] += at[(first + w) * N + i];
+        for (int w = 0; w < WARPS; ++w)
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] += at[w * N + i];
         turn ^= 1;
     }
 }
 
-// ---------------------------------------------------------------------------
+// Blocks of an SM, by the values that a thread holds of rows and weights.
+constexpr int resident(int threads, int values) { return threads == 1024 ? 1 : values > 48 ? 2 : values > 24 ? 3 : 4; }
+// Values of a row that a thread has, and rows at a time: the forward pass takes
+// two, whose sums' chains overlap; the backward pass has sums to keep as well.
+constexpr int ROW_VALUES = 16, ROWS = 2;
 
-template <class T, int V, int PER>
-__global__ void __launch_bounds__(256) norm_kernel(const __grid_constant__ NormParams p, int group, int64_t chunk) {
-    __shared__ float red[2 * 8];
-    const int t = threadIdx.x % group, g = threadIdx.x / group, groups = 256 / group;
-    const int64_t c0 = blockIdx.x * chunk, c1 = min(c0 + chunk, p.R);
+// G threads a row, U rows of a group at a time.
+template <class T, int V, int G, int PER, int U, int NT>
+__global__ void __launch_bounds__(NT, resident(NT, V * PER * (U + 2))) norm_kernel(const __grid_constant__ NormParams p, int64_t chunk) {
+    using R = Ring<T, V, PER * U, NT>;
+    constexpr int GROUPS = NT / G, STEP = G * V;
+    constexpr bool KEEP = NT == 256 && V * PER <= ROW_VALUES;      // a run's weights stay in registers
+    __shared__ float red[2 * NT / 32 * U];
+    extern __shared__ __align__(16) unsigned char ring_memory[];
+    R ring(ring_memory);
+    const int t = threadIdx.x % G, g = threadIdx.x / G;
+    const int64_t c0 = blockIdx.x * chunk;
+    const int n = static_cast<int>(min(chunk, p.R - c0));                 // rows of the chunk
+    const int left = static_cast<int>(p.F) - t * V;                       // pack j is in the row where j STEP < left
     const float inv = 1.0f / static_cast<float>(p.F);
     const bool wide = p.weight_type == PT_F32;
-    int turn = 0;
-    Run run;
-    for (int64_t base = c0; base < c1; base += groups) {
-        const int64_t r = base + g;
-        const bool in = r < c1;
-        const T* x = static_cast<const T*>(p.x) + (in ? r : c0) * p.ldx;
-        Pack<T, V> raw[PER];
+    const int64_t next = GROUPS * p.ldx;                                  // from a group's row to its next one
+    const T* px = static_cast<const T*>(p.x) + (c0 + g) * p.ldx + t * V;
+    const T* pf = px;
+    auto fetch = [&](int i) {
 #pragma unroll
-        for (int j = 0; j < PER; ++j) {
-            const int64_t c = (int64_t(j) * group + t) * V;
-            if (c < p.F) raw[j] = load_pack<T, V>(x + c);
+        for (int u = 0; u < U; ++u) {
+            if (i + u * GROUPS < n)
+#pragma unroll
+                for (int j = 0; j < PER; ++j)
+                    if (j * STEP < left) ring.fetch(u * PER + j, pf + j * STEP);
+            pf += next;
         }
-        if (in && r >= run.end) run = run_of(p, r);
-        float sum[1] = {0.0f}, sq[1] = {0.0f};
+        ring.fetched();
+    };
+    if (R::ASYNC)
+        for (int d = 0; d < R::D - 1; ++d) fetch(d * GROUPS * U + g);
+    int turn = 0, run_end = 0;      // of the chunk's rows
+    int64_t at = 0;
+    bool used = false;
+    float kept_w[KEEP ? PER : 1][V], kept_b[KEEP ? PER : 1][V];
+    auto read_weights = [&](int j, float (&w)[V], float (&b)[V]) {
 #pragma unroll
-        for (int j = 0; j < PER; ++j) {
-            if ((int64_t(j) * group + t) * V < p.F)
+        for (int k = 0; k < V; ++k) w[k] = 1.0f, b[k] = 0.0f;
+        if (p.weight) load_weights<T, V>(p.weight, wide, at + j * STEP, w);
+        if (p.bias) load_weights<T, V>(p.bias, wide, at + j * STEP, b);
+    };
+    for (int base = 0; base < n; base += GROUPS * U) {
+        float f[U][PER][V], sum[U], sq[U];
+        if (R::ASYNC) ring.wait();
 #pragma unroll
-                for (int i = 0; i < V; ++i) sum[0] += to_float<T>(raw[j].v[i]);
+        for (int u = 0; u < U; ++u) {
+            const bool in = base + u * GROUPS + g < n;
+            sum[u] = sq[u] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < PER; ++j) {
+                if (in && j * STEP < left) {
+                    ring.get(u * PER + j, px + u * next + j * STEP, f[u][j]);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) sum[u] += f[u][j][i];
+                } else {
+#pragma unroll
+                    for (int i = 0; i < V; ++i) f[u][j][i] = 0.0f;
+                }
+            }
         }
-        group_sum<1>(sum, group, red, turn);
-        const float mean = sum[0] * inv;
+        if (R::ASYNC) {
+            ring.got();
+            fetch(base + (R::D - 1) * GROUPS * U + g);
+        } else {
+            px += U * next;
+        }
+        group_sum<G, NT, U>(sum, red, turn);
 #pragma unroll
-        for (int j = 0; j < PER; ++j) {
-            if ((int64_t(j) * group + t) * V < p.F)
+        for (int u = 0; u < U; ++u) {
+            sum[u] *= inv;
+#pragma unroll
+            for (int j = 0; j < PER; ++j) {
+                if (j * STEP >= left) continue;
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    const float d = to_float<T>(raw[j].v[i]) - mean;
-                    sq[0] = fmaf(d, d, sq[0]);
+                    f[u][j][i] -= sum[u];
+                    sq[u] = fmaf(f[u][j][i], f[u][j][i], sq[u]);
                 }
-        }
-        group_sum<1>(sq, group, red, turn);
-        const float rstd = 1.0f / sqrtf(fmaf(sq[0], inv, p.eps));
-        if (!in) continue;
-        const bool used = run.s >= 0;
-        if (t == 0) {
-            if (p.mean) p.mean[r] = used ? mean : 0.0f;
-            if (p.rstd) p.rstd[r] = used ? rstd : 0.0f;
-        }
-        T* y = static_cast<T*>(p.out) + r * p.ldo;
-#pragma unroll
-        for (int j = 0; j < PER; ++j) {
-            const int64_t c = (int64_t(j) * group + t) * V;
-            if (c >= p.F) continue;
-            float w[V], b[V];
-#pragma unroll
-            for (int i = 0; i < V; ++i) w[i] = 1.0f, b[i] = 0.0f;
-            if (used && p.weight) load_weights<T, V>(p.weight, wide, run.s * p.F + c, w);
-            if (used && p.bias) load_weights<T, V>(p.bias, wide, run.s * p.F + c, b);
-            Pack<T, V> o;
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float z = (to_float<T>(raw[j].v[i]) - mean) * rstd;
-                o.v[i] = from_float<T>(used ? fmaf(z, w[i], b[i]) : 0.0f);
             }
-            *reinterpret_cast<Pack<T, V>*>(y + c) = o;
+        }
+        group_sum<G, NT, U>(sq, red, turn);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = base + u * GROUPS + g;
+            if (i >= n) break;
+            const int64_t r = c0 + i;
+            if (i >= run_end) {
+                const Run run = run_of(p, r);
+                run_end = static_cast<int>(min(run.end - c0, int64_t(n)));
+                used = run.s >= 0;
+                at = run.s * p.F + t * V;
+                if constexpr (KEEP)
+#pragma unroll
+                    for (int j = 0; j < PER; ++j)
+                        if (used && j * STEP < left) read_weights(j, kept_w[j], kept_b[j]);
+            }
+            const float rstd = rsqrtf(fmaf(sq[u], inv, p.eps));
+            if (t == 0) {
+                if (p.mean) p.mean[r] = used ? sum[u] : 0.0f;
+                if (p.rstd) p.rstd[r] = used ? rstd : 0.0f;
+            }
+            T* y = static_cast<T*>(p.out) + r * p.ldo + t * V;
+#pragma unroll
+            for (int j = 0; j < PER; ++j) {
+                if (j * STEP >= left) continue;
+                float w[V], b[V];
+                if constexpr (KEEP) {
+#pragma unroll
+                    for (int k = 0; k < V; ++k) w[k] = kept_w[j][k], b[k] = kept_b[j][k];
+                } else if (used) {
+                    read_weights(j, w, b);
+                }
+#pragma unroll
+                for (int k = 0; k < V; ++k) f[u][j][k] = used ? fmaf(f[u][j][k] * rstd, w[k], b[k]) : 0.0f;
+                Pack<T, V> o;
+                o.narrow(f[u][j]);
+                o.store(y + j * STEP);
+            }
         }
     }
 }
@@ -203,7 +324,7 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
     float x[1] = {v};
     int turn = 0;
     __syncthreads();
-    group_sum<1>(x, 256, red, turn);
+    group_sum<256, 256, 1>(x, red, turn);
     return x[0];
 }
 
@@ -225,7 +346,7 @@ __global__ void __launch_bounds__(256) norm_long_kernel(const __grid_constant__ 
             const float d = to_float<T>(x[c]) - mean;
             sq = fmaf(d, d, sq);
         }
-        const float rstd = 1.0f / sqrtf(fmaf(block_sum(sq, red), inv, p.eps));
+        const float rstd = rsqrtf(fmaf(block_sum(sq, red), inv, p.eps));
         const bool used = run.s >= 0;
         if (threadIdx.x == 0) {
             if (p.mean) p.mean[r] = used ? mean : 0.0f;
@@ -245,7 +366,7 @@ __global__ void __launch_bounds__(256) norm_long_kernel(const __grid_constant__ 
 
 struct GradArgs {
     NormParams p;
-    int32_t group, tile;        // columns of a tile
+    int32_t tile;               // columns of a tile
     int64_t chunk;
     float* sums;                // [R][2]: sum(g), sum(g z) of each row, or NULL: a block has all columns
     float* partials;            // [2 chunks][2][F]: the first and last run of a chunk
@@ -284,148 +405,263 @@ __device__ __forceinline__ void store_weight(void* out, int type, int64_t at, fl
     else static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(v);
 }
 
-template <class T, int V, int PER, int NT>
-__global__ void __launch_bounds__(NT) norm_grad_kernel(const __grid_constant__ GradArgs a) {
-    constexpr int E = V * PER;
-    __shared__ float red[2 * NT / 32 * 2];
-    extern __shared__ float shared_sums[];       // [groups of at least a warp][2][tile]
+// A block's windows of U rows of each group follow one another whatever
+// segments they are in; a window in which a run ends is worked on once for each
+// run that has a row in it.
+template <class T, int V, int G, int PER, int U, int NT>
+__global__ void __launch_bounds__(NT, resident(NT, V * PER * (2 * U + 3))) norm_grad_kernel(const __grid_constant__ GradArgs a) {
+    using R = Ring<T, V, 2 * PER * U, NT>;
+    constexpr int E = V * PER, GROUPS = NT / G, STEP = G * V, WINDOW = GROUPS * U;
+    constexpr bool KEEP = NT == 256;      // a run's weights stay in registers; a large block has none to spare and reads them again
+    __shared__ float red[2 * NT / 32 * 2 * U];
+    extern __shared__ __align__(16) unsigned char ring_memory[];
+    float* const shared_sums = reinterpret_cast<float*>(ring_memory + R::BYTES);      // [groups of at least a warp][2][tile]
+    R ring(ring_memory);
     const NormParams& p = a.p;
-    const int group = a.group, t = threadIdx.x % group, g = threadIdx.x / group, groups = NT / group;
-    const int64_t c0 = blockIdx.x * a.chunk, c1 = min(c0 + a.chunk, p.R);
-    const int64_t col0 = int64_t(blockIdx.y) * a.tile;
+    const int t = threadIdx.x % G, g = threadIdx.x / G;
+    const int64_t c0 = blockIdx.x * a.chunk;
+    const int n = static_cast<int>(min(a.chunk, p.R - c0));
+    const int col0 = static_cast<int>(blockIdx.y) * a.tile, F = static_cast<int>(p.F), left = F - col0 - t * V;
     const float inv = 1.0f / static_cast<float>(p.F);
     const bool wide = p.weight_type == PT_F32, want_dx = p.out != nullptr, want_dw = p.dweight || p.dbias;
-    auto column = [&](int j) { return col0 + (int64_t(j) * group + t) * V; };
-    int turn = 0;
+    const int64_t nextx = GROUPS * p.ldx, nexty = GROUPS * p.ldy;
+    const T* px = static_cast<const T*>(p.x) + (c0 + g) * p.ldx + col0 + t * V;
+    const T* pd = static_cast<const T*>(p.dy) + (c0 + g) * p.ldy + col0 + t * V;
+    auto fetch = [&](int i) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (i + u * GROUPS < n)
+#pragma unroll
+                for (int j = 0; j < PER; ++j)
+                    if (j * STEP < left) {
+                        ring.fetch((u * PER + j) * 2, px + j * STEP);
+                        ring.fetch((u * PER + j) * 2 + 1, pd + j * STEP);
+                    }
+            px += nextx;
+            pd += nexty;
+        }
+        ring.fetched();
+    };
+    if (R::ASYNC)
+        for (int d = 0; d < R::D - 1; ++d) fetch(d * WINDOW + g);
     if (want_dw && p.offsets) {
         // segments without rows
         const int64_t each = (p.S + gridDim.x - 1) / gridDim.x, s1 = min((blockIdx.x + 1) * each, p.S);
         for (int64_t s = blockIdx.x * each; s < s1; ++s) {
             if (offset_at(p, s) < offset_at(p, s + 1)) continue;
-            for (int64_t c = col0 + threadIdx.x; c < min(col0 + a.tile, p.F); c += NT) {
+            for (int c = col0 + threadIdx.x; c < min(col0 + a.tile, F); c += NT) {
                 if (p.dweight) store_weight(p.dweight, p.weight_type, s * p.F + c, 0.0f);
                 if (p.dbias) store_weight(p.dbias, p.weight_type, s * p.F + c, 0.0f);
             }
         }
     }
-    for (int64_t r0 = c0; r0 < c1;) {
-        const Run run = run_of(p, r0);
-        const int64_t r1 = min(run.end, c1);
-        if (run.s < 0) {
-            // rows in no segment
-            if (want_dx)
-                for (int64_t r = r0 + g; r < r1; r += groups)
+    Run run = run_of(p, c0);
+    float kept[KEEP ? PER : 1][V], dw[E], db[E];
+    auto read_weights = [&](int j, float (&w)[V]) {
+        if (p.weight && run.s >= 0 && j * STEP < left) {
+            load_weights<T, V>(p.weight, wide, run.s * p.F + col0 + t * V + j * STEP, w);
+        } else {
 #pragma unroll
-                    for (int j = 0; j < PER; ++j) {
-                        Pack<T, V> zero;
-#pragma unroll
-                        for (int i = 0; i < V; ++i) zero.v[i] = from_float<T>(0.0f);
-                        if (column(j) < p.F) *reinterpret_cast<Pack<T, V>*>(static_cast<T*>(p.out) + r * p.ldo + column(j)) = zero;
-                    }
-            r0 = r1;
-            continue;
+            for (int i = 0; i < V; ++i) w[i] = 1.0f;
         }
-        float w[PER][V], dw[E], db[E];
+    };
+    auto weights_of = [&](int j, float (&w)[V]) {
+        if constexpr (KEEP) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) w[i] = kept[j][i];
+        } else {
+            read_weights(j, w);
+        }
+    };
+    int run_end = 0;                   // of the chunk's rows; past its last one where the run goes on
+    auto begin = [&] {
+        run_end = static_cast<int>(min(run.end - c0, int64_t(n) + 1));
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) w[j][i] = 1.0f, dw[j * V + i] = 0.0f, db[j * V + i] = 0.0f;
-            if (p.weight && column(j) < p.F) load_weights<T, V>(p.weight, wide, run.s * p.F + column(j), w[j]);
+            for (int i = 0; i < V; ++i) dw[j * V + i] = 0.0f, db[j * V + i] = 0.0f;
+            if constexpr (KEEP) read_weights(j, kept[j]);
         }
-        for (int64_t base = r0; base < r1; base += groups) {
-            const int64_t r = base + g;
-            const bool in = r < r1;
-            Pack<T, V> x[PER], dy[PER];
-            float mean = 0.0f, rstd = 0.0f;
-            if (in) {
-                const T* px = static_cast<const T*>(p.x) + r * p.ldx;
-                const T* pd = static_cast<const T*>(p.dy) + r * p.ldy;
+    };
+    begin();
+    float next_mean[U], next_rstd[U];
+    auto fetch_stats = [&](int i) {
 #pragma unroll
-                for (int j = 0; j < PER; ++j) {
-                    if (column(j) < p.F) x[j] = load_pack<T, V>(px + column(j)), dy[j] = load_pack<T, V>(pd + column(j));
-                }
-                mean = __ldg(p.mean + r);
-                rstd = __ldg(p.rstd + r);
-            }
-            float s[2] = {0.0f, 0.0f};
-#pragma unroll
-            for (int j = 0; j < PER; ++j) {
-                if (!in || column(j) >= p.F) continue;
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const float d = to_float<T>(dy[j].v[i]), z = (to_float<T>(x[j].v[i]) - mean) * rstd, gr = d * w[j][i];
-                    db[j * V + i] += d;
-                    dw[j * V + i] = fmaf(d, z, dw[j * V + i]);
-                    s[0] += gr;
-                    s[1] = fmaf(gr, z, s[1]);
-                }
-            }
-            if (!want_dx) continue;
-            if (!a.sums) group_sum<2>(s, group, red, turn);
-            else if (in) s[0] = __ldg(a.sums + 2 * r), s[1] = __ldg(a.sums + 2 * r + 1);
-            if (!in) continue;
-            const float m1 = s[0] * inv, m2 = s[1] * inv;
-#pragma unroll
-            for (int j = 0; j < PER; ++j) {
-                if (column(j) >= p.F) continue;
-                Pack<T, V> o;
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const float z = (to_float<T>(x[j].v[i]) - mean) * rstd;
-                    o.v[i] = from_float<T>(rstd * (fmaf(to_float<T>(dy[j].v[i]), w[j][i], -m1) - z * m2));
-                }
-                *reinterpret_cast<Pack<T, V>*>(static_cast<T*>(p.out) + r * p.ldo + column(j)) = o;
-            }
+        for (int u = 0; u < U; ++u) {
+            next_mean[u] = next_rstd[u] = 0.0f;
+            if (i + u * GROUPS < n) next_mean[u] = __ldg(p.mean + c0 + i + u * GROUPS), next_rstd[u] = __ldg(p.rstd + c0 + i + u * GROUPS);
         }
-        if (want_dw) {
-            // the groups' sums, in their order: of a warp's groups first, then of the warps
+    };
+    fetch_stats(g);
+    int turn = 0;
+    for (int base = 0; base < n; base += WINDOW) {
+        const int end = min(base + WINDOW, n);
+        float kept_z[KEEP ? U : 1][KEEP ? PER : 1][V], kept_dy[KEEP ? U : 1][KEEP ? PER : 1][V], mean[U], rstd[U];
+        if (R::ASYNC) ring.wait();
+        auto read_values = [&](int u, int j, float (&z)[V], float (&dy)[V]) {
+            ring.get((u * PER + j) * 2, px + u * nextx + j * STEP, z);
+            ring.get((u * PER + j) * 2 + 1, pd + u * nexty + j * STEP, dy);
 #pragma unroll
-            for (int d = 16; d > 0; d >>= 1) {
-                if (d < group) continue;
+            for (int i = 0; i < V; ++i) z[i] = (z[i] - mean[u]) * rstd[u];
+        };
+        auto values_of = [&](int u, int j, float (&z)[V], float (&dy)[V]) {
+            if constexpr (KEEP) {
 #pragma unroll
-                for (int i = 0; i < E; ++i) {
-                    dw[i] += __shfl_xor_sync(0xffffffffu, dw[i], d);
-                    db[i] += __shfl_xor_sync(0xffffffffu, db[i], d);
-                }
+                for (int i = 0; i < V; ++i) z[i] = kept_z[u][j][i], dy[i] = kept_dy[u][j][i];
+            } else {
+                read_values(u, j, z, dy);
             }
-            const int wide_group = max(group, 32), parts = NT / wide_group, part = threadIdx.x / wide_group;
-            __syncthreads();
-            if (threadIdx.x % wide_group < group) {
+        };
+        auto values_read = [&] {
+            if (R::ASYNC) {
+                ring.got();
+                fetch(base + (R::D - 1) * WINDOW + g);
+            } else {
+                px += U * nextx;
+                pd += U * nexty;
+            }
+        };
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            mean[u] = next_mean[u];
+            rstd[u] = next_rstd[u];
+            if constexpr (KEEP)
 #pragma unroll
                 for (int j = 0; j < PER; ++j)
-#pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        const int c = (j * group + t) * V + i;
-                        if (c >= a.tile) continue;
-                        shared_sums[(part * 2) * a.tile + c] = dw[j * V + i];
-                        shared_sums[(part * 2 + 1) * a.tile + c] = db[j * V + i];
-                    }
-            }
-            __syncthreads();
-            const bool whole = run.begin >= c0 && run.end <= c1;
-            float* slot = a.partials + (2 * int64_t(blockIdx.x) + (run.begin >= c0 ? 1 : 0)) * 2 * p.F;
-            for (int i = threadIdx.x; i < 2 * a.tile; i += NT) {
-                const int which = i >= a.tile;
-                const int64_t c = col0 + i - which * a.tile;
-                if (c >= p.F) continue;
-                float v = 0.0f;
-                for (int q = 0; q < parts; ++q) v += shared_sums[q * 2 * a.tile + i];
-                void* out = which ? p.dbias : p.dweight;
-                if (!whole) slot[which * p.F + c] = v;
-                else if (out) store_weight(out, p.weight_type, run.s * p.F + c, v);
-            }
+                    if (base + u * GROUPS + g < n && j * STEP < left) read_values(u, j, kept_z[u][j], kept_dy[u][j]);
         }
-        r0 = r1;
+        if constexpr (KEEP) values_read();
+        fetch_stats(base + WINDOW + g);
+        int from = base;               // the window's rows before are done
+        for (;;) {
+            const int to = min(run_end, end);
+            auto in = [&](int u) { return base + u * GROUPS + g >= from && base + u * GROUPS + g < to; };
+            if (run.s >= 0) {
+                float s[2 * U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    s[2 * u] = s[2 * u + 1] = 0.0f;
+                    if (!in(u)) continue;
+#pragma unroll
+                    for (int j = 0; j < PER; ++j) {
+                        if (j * STEP >= left) continue;
+                        float w[V], z[V], dy[V];
+                        weights_of(j, w);
+                        values_of(u, j, z, dy);
+#pragma unroll
+                        for (int i = 0; i < V; ++i) {
+                            const float gr = dy[i] * w[i];
+                            db[j * V + i] += dy[i];
+                            dw[j * V + i] = fmaf(dy[i], z[i], dw[j * V + i]);
+                            s[2 * u] += gr;
+                            s[2 * u + 1] = fmaf(gr, z[i], s[2 * u + 1]);
+                        }
+                    }
+                }
+                if (want_dx) {
+                    if (!a.sums) group_sum<G, NT, 2 * U>(s, red, turn);
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        if (!in(u)) continue;
+                        const int64_t r = c0 + base + u * GROUPS + g;
+                        if (a.sums) s[2 * u] = __ldg(a.sums + 2 * r), s[2 * u + 1] = __ldg(a.sums + 2 * r + 1);
+                        const float m1 = s[2 * u] * inv, m2 = s[2 * u + 1] * inv;
+                        T* out = static_cast<T*>(p.out) + r * p.ldo + col0 + t * V;
+#pragma unroll
+                        for (int j = 0; j < PER; ++j) {
+                            if (j * STEP >= left) continue;
+                            Pack<T, V> o;
+                            float w[V], z[V], dy[V], d[V];
+                            weights_of(j, w);
+                            values_of(u, j, z, dy);
+#pragma unroll
+                            for (int i = 0; i < V; ++i) d[i] = rstd[u] * fmaf(-z[i], m2, fmaf(dy[i], w[i], -m1));
+                            o.narrow(d);
+                            o.store(out + j * STEP);
+                        }
+                    }
+                }
+            } else if (want_dx) {
+                // rows in no segment
+                const float none[V] = {};
+                Pack<T, V> zero;
+                zero.narrow(none);
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int j = 0; j < PER; ++j)
+                        if (in(u) && j * STEP < left) zero.store(static_cast<T*>(p.out) + (c0 + base + u * GROUPS + g) * p.ldo + col0 + t * V + j * STEP);
+            }
+            if (run_end > end && end < n) break;       // the run goes on in the next window
+            if (want_dw && run.s >= 0) {
+                // the run's end in this chunk: the groups' sums, of a warp's groups
+                // first, then of the warps, each in their order
+#pragma unroll
+                for (int d = 16; d >= G; d >>= 1) {
+#pragma unroll
+                    for (int i = 0; i < E; ++i) {
+                        dw[i] += __shfl_xor_sync(0xffffffffu, dw[i], d);
+                        db[i] += __shfl_xor_sync(0xffffffffu, db[i], d);
+                    }
+                }
+                const bool whole = run.begin >= c0 && run.end <= c0 + n;
+                float* slot_sums = a.partials + (2 * int64_t(blockIdx.x) + (run.begin >= c0 ? 1 : 0)) * 2 * p.F;
+                auto put = [&](int which, int c, float v) {
+                    void* out = which ? p.dbias : p.dweight;
+                    if (!whole) slot_sums[which * p.F + c] = v;
+                    else if (out) store_weight(out, p.weight_type, run.s * p.F + c, v);
+                };
+                if constexpr (G == NT) {
+#pragma unroll
+                    for (int j = 0; j < PER; ++j)
+#pragma unroll
+                        for (int i = 0; i < V; ++i)
+                            if (j * STEP < left) put(0, col0 + t * V + j * STEP + i, dw[j * V + i]), put(1, col0 + t * V + j * STEP + i, db[j * V + i]);
+                } else {
+                    constexpr int WIDE = G < 32 ? 32 : G, PARTS = NT / WIDE;
+                    float* own = shared_sums + threadIdx.x / WIDE * 2 * a.tile;
+                    __syncthreads();
+                    if (threadIdx.x % WIDE < G) {
+#pragma unroll
+                        for (int j = 0; j < PER; ++j)
+#pragma unroll
+                            for (int i = 0; i < V; ++i) {
+                                const int c = t * V + j * STEP + i;
+                                if (c >= a.tile) continue;
+                                own[c] = dw[j * V + i];
+                                own[a.tile + c] = db[j * V + i];
+                            }
+                    }
+                    __syncthreads();
+                    for (int i = threadIdx.x; i < 2 * a.tile; i += NT) {
+                        const int which = i >= a.tile, c = col0 + i - which * a.tile;
+                        if (c >= F) continue;
+                        float v = 0.0f;
+#pragma unroll
+                        for (int q = 0; q < PARTS; ++q) v += shared_sums[q * 2 * a.tile + i];
+                        put(which, c, v);
+                    }
+                }
+            }
+            from = run_end;
+            if (from >= n) break;
+            run = run_of(p, c0 + from);
+            begin();
+            if (from >= end) break;
+        }
+        if constexpr (!KEEP) values_read();
     }
 }
 
 // Adds the parts of a segment that more than one chunk has rows of: blockIdx.x
 // names the segment, or (by_start) the chunk in which it starts; blockIdx.y the
-// first 32 of the 2 F sums.  Each warp adds an equal share of the parts in order, then
-// the warps' sums are added.
-__global__ void __launch_bounds__(256) norm_add_kernel(const __grid_constant__ GradArgs a, int by_start) {
-    __shared__ float sums[8][32];
+// first `lanes` of the 2 F sums.  Each of the block's 512 / lanes rows of threads
+// adds an equal share of the parts in order, then theirs are added.
+constexpr int ADD_THREADS = 512;
+__global__ void __launch_bounds__(ADD_THREADS) norm_add_kernel(const __grid_constant__ GradArgs a, int by_start, int lanes) {
+    __shared__ float sums[ADD_THREADS];
     const NormParams& p = a.p;
+    grid_wait();
     int64_t s = blockIdx.x, begin = 0, end = p.R;
     if (by_start) {
         const Run run = run_of(p, min((int64_t(blockIdx.x) + 1) * a.chunk, p.R) - 1);
@@ -437,22 +673,21 @@ __global__ void __launch_bounds__(256) norm_add_kernel(const __grid_constant__ G
     if (begin >= end) return;
     const int64_t first = begin / a.chunk, last = (end - 1) / a.chunk;
     if (first == last) return;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t parts = last - first + 1, each = (parts + 7) / 8;
-    const int64_t q0 = warp * each, q1 = min(q0 + each, parts);
-    for (int64_t i0 = int64_t(blockIdx.y) * 32; i0 < 2 * p.F; i0 += int64_t(gridDim.y) * 32) {
+    const int lane = threadIdx.x % lanes, share = threadIdx.x / lanes, shares = ADD_THREADS / lanes;
+    const int64_t parts = last - first + 1, each = (parts + shares - 1) / shares;
+    const int64_t q0 = share * each, q1 = min(q0 + each, parts);
+    for (int64_t i0 = int64_t(blockIdx.y) * lanes; i0 < 2 * p.F; i0 += int64_t(gridDim.y) * lanes) {
         const int64_t i = i0 + lane;
         float v = 0.0f;
         if (i < 2 * p.F) {
 #pragma unroll 8
             for (int64_t q = q0; q < q1; ++q) v += __ldcg(a.partials + (2 * (first + q) + (q == 0 ? 1 : 0)) * 2 * p.F + i);
         }
-        sums[warp][lane] = v;
+        sums[threadIdx.x] = v;
         __syncthreads();
-        if (warp == 0 && i < 2 * p.F) {
+        if (share == 0 && i < 2 * p.F) {
             v = 0.0f;
-#pragma unroll
-            for (int q = 0; q < 8; ++q) v += sums[q][lane];
+            for (int q = 0; q < shares; ++q) v += sums[q * lanes + lane];
             void* out = i < p.F ? p.dweight : p.dbias;
             if (out) store_weight(out, p.weight_type, s * p.F + (i < p.F ? i : i - p.F), v);
         }
@@ -463,52 +698,77 @@ __global__ void __launch_bounds__(256) norm_add_kernel(const __grid_constant__ G
 int64_t ceil_to(int64_t n, int64_t d) { return (n + d - 1) / d; }
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
-template <class T, int V, int PER>
+template <class K>
+cudaError_t allow_smem(K* kernel, int bytes) {
+    // (48 KB are allowed unasked, with the kernel's own)
+    return bytes > 40 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) : cudaSuccess;
+}
+
+template <class T, int V, int G, int PER>
 cudaError_t launch_rows(const NormParams& p, const NormPlan& plan, cudaStream_t stream) {
-    norm_kernel<T, V, PER><<<static_cast<unsigned>(plan.chunks), 256, 0, stream>>>(p, plan.group, plan.chunk);
+    constexpr int NT = G > 256 ? G : 256, U = NT == 256 ? ROWS : 1, smem = Ring<T, V, PER * U, NT>::BYTES;
+    auto* kernel = norm_kernel<T, V, G, PER, U, NT>;
+    const cudaError_t e = allow_smem(kernel, smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<static_cast<unsigned>(plan.chunks), NT, smem, stream>>>(p, plan.chunk);
     return cudaGetLastError();
 }
 
-template <class T>
-cudaError_t launch_type(const NormParams& p, const NormPlan& plan, cudaStream_t stream) {
-    constexpr int V = 16 / sizeof(T);
-    if (plan.per == 0) {
-        norm_long_kernel<T><<<static_cast<unsigned>(plan.chunks), 256, 0, stream>>>(p);
-        return cudaGetLastError();
-    }
-    if (plan.vec == 1) return plan.per <= 4 ? launch_rows<T, 1, 4>(p, plan, stream) : launch_rows<T, 1, 16>(p, plan, stream);
-    switch (plan.per) {
-        case 1: return launch_rows<T, V, 1>(p, plan, stream);
-        case 2: return launch_rows<T, V, 2>(p, plan, stream);
-        case 4: return launch_rows<T, V, 4>(p, plan, stream);
-        default: return launch_rows<T, V, 8>(p, plan, stream);
-    }
-}
-
-template <class T, int V, int PER, int NT>
+template <class T, int V, int G, int PER>
 cudaError_t launch_grad_rows(const GradArgs& a, const NormPlan& plan, cudaStream_t stream) {
-    auto* kernel = norm_grad_kernel<T, V, PER, NT>;
-    const int smem = NT / std::max(plan.group, 32) * 2 * a.tile * 4;
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return e;
-    }
+    constexpr int NT = G > 256 ? G : 256;
+    auto* kernel = norm_grad_kernel<T, V, G, PER, 1, NT>;
+    const int smem = Ring<T, V, 2 * PER, NT>::BYTES + (G < NT ? NT / std::max(G, 32) * 2 * a.tile * 4 : 0);
+    const cudaError_t e = allow_smem(kernel, smem);
+    if (e != cudaSuccess) return e;
     kernel<<<dim3(static_cast<unsigned>(plan.chunks), plan.tiles), NT, smem, stream>>>(a);
     return cudaGetLastError();
 }
 
+// f(shape) for the shape of a plan, as constants: values of a load, threads of a row, loads of a thread.
+template <int VEC, int GROUP, int PER> struct Shape {
+    static constexpr int vec = VEC, group = GROUP, per = PER;
+};
+template <class T, class F>
+cudaError_t with_shape(const NormPlan& plan, F f) {
+    constexpr int V = 16 / sizeof(T), MOST = ROW_VALUES / V;
+#define SEG_NORM_SHAPE(v, g, n) \
+    if (plan.vec == v && plan.group == g && plan.per == n) return f(Shape<v, g, n>())
+    SEG_NORM_SHAPE(V, 8, 1);
+    if constexpr (V == 4) SEG_NORM_SHAPE(V, 8, 2);
+    SEG_NORM_SHAPE(V, 8, MOST);
+    SEG_NORM_SHAPE(V, 16, MOST);
+    SEG_NORM_SHAPE(V, 32, MOST);
+    SEG_NORM_SHAPE(V, 64, MOST);
+    SEG_NORM_SHAPE(V, 128, MOST);
+    SEG_NORM_SHAPE(V, 256, 1);
+    SEG_NORM_SHAPE(V, 256, MOST);
+    SEG_NORM_SHAPE(V, 1024, MOST);
+    SEG_NORM_SHAPE(1, 32, 4);
+    SEG_NORM_SHAPE(1, 32, 8);
+    SEG_NORM_SHAPE(1, 256, 8);
+    SEG_NORM_SHAPE(1, 1024, 8);
+#undef SEG_NORM_SHAPE
+    return cudaErrorInvalidConfiguration;
+}
+
+template <class T>
+cudaError_t launch_type(const NormParams& p, const NormPlan& plan, cudaStream_t stream) {
+    if (plan.per == 0) {
+        norm_long_kernel<T><<<static_cast<unsigned>(plan.chunks), 256, 0, stream>>>(p);
+        return cudaGetLastError();
+    }
+    return with_shape<T>(plan, [&](auto s) { return launch_rows<T, s.vec, s.group, s.per>(p, plan, stream); });
+}
+
 template <class T>
 cudaError_t launch_grad_type(const GradArgs& a, const NormPlan& plan, cudaStream_t stream) {
-    constexpr int V = 16 / sizeof(T);
     if (a.sums) {
         norm_sums_kernel<T><<<static_cast<unsigned>(std::min<int64_t>(a.p.R, int64_t(a.p.sms) * 8)), 256, 0, stream>>>(a);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
-    if (plan.vec == 1) return plan.per <= 4 ? launch_grad_rows<T, 1, 4, 256>(a, plan, stream) : launch_grad_rows<T, 1, 16, 256>(a, plan, stream);
-    if (plan.per == 1) return launch_grad_rows<T, V, 1, 256>(a, plan, stream);
-    if (plan.per == 2) return launch_grad_rows<T, V, 2, 256>(a, plan, stream);
-    return launch_grad_rows<T, V, 4, 256>(a, plan, stream);
+    return with_shape<T>(plan, [&](auto s) { return launch_grad_rows<T, s.vec, s.group, s.per>(a, plan, stream); });
 }
 
 }  // namespace
@@ -520,32 +780,36 @@ NormPlan plan_norm(bool grad, const NormParams& p) {
     const bool vec = p.F % v == 0 && p.ldx % v == 0 && aligned16(p.x) && (!p.out || (p.ldo % v == 0 && aligned16(p.out))) &&
                      (!grad || (p.ldy % v == 0 && aligned16(p.dy))) && aligned16(p.weight) && aligned16(p.bias);
     d.vec = vec ? v : 1;
-    d.threads = 256;
-    const int64_t loads = ceil_to(p.F, d.vec);
-    const int most = vec ? (grad ? 4 : 8) : 16;
     d.tiles = 1;
-    // a warp's row in registers, or as few threads as hold it; short rows take less than a warp
-    d.group = 8;
-    const int warp_most = vec ? (grad ? 2 : most) : (loads <= 128 ? 4 : 16);
-    while (d.group < 32 && d.group < loads) d.group *= 2;
-    while (d.group < 256 && int64_t(d.group) * warp_most < loads) d.group *= 2;
+    const int64_t loads = ceil_to(p.F, d.vec);
+    const int most = vec ? ROW_VALUES / v : 8;
+    // as few threads for a row as hold it; where there are few rows, a block's, so
+    // that each is over sooner
+    if (p.R <= p.sms && loads > 32) {
+        d.group = loads <= 256 * most ? 256 : 1024;
+    } else {
+        d.group = vec ? 8 : 32;
+        while (d.group < 1024 && int64_t(d.group) * most < loads) d.group *= vec && d.group < 256 ? 2 : vec ? 4 : d.group == 32 ? 8 : 4;
+    }
+    d.threads = std::max(d.group, 256);
     int64_t per = ceil_to(loads, d.group);
+    d.per = most;
+    if (vec && d.group <= 8) d.per = static_cast<int32_t>(per > 2 ? most : per);
+    if (vec && d.group == 256 && per == 1) d.per = 1;
+    if (!vec && d.group == 32 && per <= 4) d.per = 4;
     if (per > most) {
         if (grad) {
             d.tiles = static_cast<int32_t>(ceil_to(per, most));
-            per = most;
             d.sums_bytes = ceil_to(p.R * 8, 256) * 256;
         } else {
-            per = 0;
+            d.per = 0;
         }
     }
-    d.per = 1;
-    if (!vec) d.per = per <= 4 ? 4 : 16;
-    else while (d.per < per) d.per *= 2;
-    if (per == 0) d.per = 0;
-    const int64_t groups = d.per == 0 ? 1 : d.threads / d.group;
-    const int64_t most_blocks = grad ? std::max<int64_t>(int64_t(p.sms) * 4 / d.tiles, 1) : int64_t(p.sms) * 8;
-    d.chunk = std::max<int64_t>(ceil_to(ceil_to(p.R, most_blocks), groups) * groups, groups);
+    const int rows = !grad && d.threads == 256 ? ROWS : 1;
+    const int64_t window = d.per == 0 ? 1 : d.threads / d.group * rows;
+    const int64_t most_blocks = d.per == 0 ? int64_t(p.sms) * 8
+                                           : std::max<int64_t>(p.sms * resident(d.threads, d.per * d.vec * (grad ? 5 : rows + 2)) / d.tiles, 1);
+    d.chunk = ceil_to(ceil_to(p.R, most_blocks), window) * window;
     d.chunks = ceil_to(p.R, d.chunk);
     if (d.per == 0) d.chunks = std::min<int64_t>(p.R, most_blocks);
     if (grad) d.partial_bytes = ceil_to(d.chunks * 4 * p.F * 4, 256) * 256;
@@ -561,7 +825,6 @@ cudaError_t launch_norm(const NormParams& p, const NormPlan& plan, cudaStream_t 
 cudaError_t launch_norm_grad(const NormParams& p, const NormPlan& plan, cudaStream_t stream) {
     GradArgs a{};
     a.p = p;
-    a.group = plan.group;
     a.tile = static_cast<int32_t>(std::min<int64_t>(p.F, int64_t(plan.group) * plan.per * plan.vec));
     a.chunk = plan.chunk;
     a.sums = plan.sums_bytes > 0 ? reinterpret_cast<float*>(p.ws) : nullptr;
@@ -572,9 +835,19 @@ cudaError_t launch_norm_grad(const NormParams& p, const NormPlan& plan, cudaStre
     else e = launch_grad_type<__nv_bfloat16>(a, plan, stream);
     if (e != cudaSuccess || plan.chunks < 2 || (!p.dweight && !p.dbias)) return e;
     const bool by_start = p.S >= plan.chunks;
-    const dim3 grid(static_cast<unsigned>(by_start ? plan.chunks - 1 : p.S), static_cast<unsigned>(std::min<int64_t>(ceil_to(2 * p.F, 32), 16384)));
-    norm_add_kernel<<<grid, 256, 0, stream>>>(a, by_start);
-    return cudaGetLastError();
+    // columns of a block: the fewer segments, the more parts there are of each
+    int lanes = 32;
+    while (lanes < 256 && lanes < p.S) lanes *= 2;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(by_start ? plan.chunks - 1 : p.S), static_cast<unsigned>(std::min<int64_t>(ceil_to(2 * p.F, lanes), 16384)));
+    cfg.blockDim = dim3(ADD_THREADS);
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, norm_add_kernel, a, static_cast<int>(by_start), lanes);
 }
 
 }  // namespace segred
