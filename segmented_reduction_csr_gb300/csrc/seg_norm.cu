@@ -34,43 +34,44 @@ template <> __device__ __forceinline__ float from_float<float>(float v) { return
 template <> __device__ __forceinline__ __half from_float<__half>(float v) { return __float2half_rn(v); }
 template <> __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-// V values that are loaded and stored together: 16 bytes, or one value.  Two
-// 16-bit values at a time are widened and narrowed (a value at a time the
-// compiler took 39 instructions a value for a whole forward pass, now 9).
+// Two values that one instruction works on (a value at a time the backward pass
+// took 28 instructions a value, 32,768 x 2,048 bfloat16 79 us).
+__device__ __forceinline__ float2 pair(float x) { return make_float2(x, x); }
+
+// V values that are loaded and stored together: 16 bytes, or one value (the
+// second one of a pair is 0 then).
 template <class T, int V> struct Pack {
+    static constexpr int H = V > 1 ? V / 2 : 1;
     using Raw = typename std::conditional<V * sizeof(T) == 16, uint4, T>::type;
     Raw raw;
     __device__ __forceinline__ void load(const T* p) { raw = __ldg(reinterpret_cast<const Raw*>(p)); }
     __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<Raw*>(p) = raw; }
-    __device__ __forceinline__ void widen(float (&f)[V]) const {
+    __device__ __forceinline__ void widen(float2 (&f)[H]) const {
         if constexpr (V == 1) {
-            f[0] = to_float<T>(raw);
+            f[0] = make_float2(to_float<T>(raw), 0.0f);
+        } else if constexpr (sizeof(T) == 4) {
+            f[0] = make_float2(__uint_as_float(raw.x), __uint_as_float(raw.y));
+            f[1] = make_float2(__uint_as_float(raw.z), __uint_as_float(raw.w));
         } else {
             const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                if constexpr (sizeof(T) == 4) {
-                    f[k] = __uint_as_float(w[k]);
-                } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-                    f[2 * k] = __uint_as_float(w[k] << 16);
-                    f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
-                } else {
-                    const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
-                    f[2 * k] = x.x, f[2 * k + 1] = x.y;
-                }
+                if constexpr (std::is_same<T, __nv_bfloat16>::value) f[k] = make_float2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u));
+                else f[k] = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
             }
         }
     }
-    __device__ __forceinline__ void narrow(const float (&f)[V]) {
+    __device__ __forceinline__ void narrow(const float2 (&f)[H]) {
         if constexpr (V == 1) {
-            raw = from_float<T>(f[0]);
+            raw = from_float<T>(f[0].x);
+        } else if constexpr (sizeof(T) == 4) {
+            raw = make_uint4(__float_as_uint(f[0].x), __float_as_uint(f[0].y), __float_as_uint(f[1].x), __float_as_uint(f[1].y));
         } else {
             uint32_t w[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                if constexpr (sizeof(T) == 4) w[k] = __float_as_uint(f[k]);
-                else if constexpr (std::is_same<T, __nv_bfloat16>::value) asm("cvt.rn.bf16x2.f32 %0, %2, %1;" : "=r"(w[k]) : "f"(f[2 * k]), "f"(f[2 * k + 1]));
-                else asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(w[k]) : "f"(f[2 * k]), "f"(f[2 * k + 1]));
+                if constexpr (std::is_same<T, __nv_bfloat16>::value) asm("cvt.rn.bf16x2.f32 %0, %2, %1;" : "=r"(w[k]) : "f"(f[k].x), "f"(f[k].y));
+                else asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(w[k]) : "f"(f[k].x), "f"(f[k].y));
             }
             raw = make_uint4(w[0], w[1], w[2], w[3]);
         }
@@ -99,35 +100,43 @@ struct Ring {
     }
     // the slot to read has landed
     __device__ __forceinline__ void wait() const { asm volatile("cp.async.wait_group %0;" ::"n"(D - 2) : "memory"); }
-    __device__ __forceinline__ void get(int j, const T* from, float (&f)[V]) const {
+    __device__ __forceinline__ void get(int j, const T* from, float2 (&f)[Pack<T, V>::H]) const {
         Pack<T, V> x;
         if constexpr (ASYNC) asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x.raw.x), "=r"(x.raw.y), "=r"(x.raw.z), "=r"(x.raw.w) : "r"(at + j * NT * 16) : "memory");
         else x.load(from);
         x.widen(f);
+    }
+    // packs that are never fetched read as zeros
+    __device__ __forceinline__ void clear(int j) const {
+        if constexpr (ASYNC)
+            for (int d = 0; d < D; ++d) asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(base + d * SLOT + j * NT * 16), "r"(0) : "memory");
     }
     __device__ __forceinline__ void got() { at = at == base + (D - 1) * SLOT ? base : at + SLOT; }
 };
 
 // V neighbouring values of weight_type at element `at`.
 template <class T, int V>
-__device__ __forceinline__ void load_weights(const void* w, bool wide, int64_t at, float (&f)[V]) {
-    if (wide) {
-        const float* p = static_cast<const float*>(w) + at;
-        if constexpr (V % 4 == 0) {
-#pragma unroll
-            for (int i = 0; i < V; i += 4) {
-                const float4 x = __ldg(reinterpret_cast<const float4*>(p + i));
-                f[i] = x.x, f[i + 1] = x.y, f[i + 2] = x.z, f[i + 3] = x.w;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < V; ++i) f[i] = __ldg(p + i);
-        }
-    } else {
+__device__ __forceinline__ void load_weights(const void* w, bool wide, int64_t at, float2 (&f)[Pack<T, V>::H]) {
+    if (!wide) {
         Pack<T, V> x;
         x.load(static_cast<const T*>(w) + at);
         x.widen(f);
+        return;
     }
+    const float* p = static_cast<const float*>(w) + at;
+    if constexpr (V == 1) {
+        f[0] = make_float2(__ldg(p), 0.0f);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; i += 4) {
+            const float4 x = __ldg(reinterpret_cast<const float4*>(p + i));
+            f[i / 2] = make_float2(x.x, x.y), f[i / 2 + 1] = make_float2(x.z, x.w);
+        }
+    }
+}
+template <class T>
+__device__ __forceinline__ float load_weight(const void* w, bool wide, int64_t at) {
+    return wide ? __ldg(static_cast<const float*>(w) + at) : to_float<T>(static_cast<const T*>(w)[at]);
 }
 
 __device__ __forceinline__ int64_t offset_at(const NormParams& p, int64_t s) {
@@ -201,7 +210,7 @@ constexpr int ROW_VALUES = 16, ROWS = 2;
 template <class T, int V, int G, int PER, int U, int NT>
 __global__ void __launch_bounds__(NT, resident(NT, V * PER * (U + 2))) norm_kernel(const __grid_constant__ NormParams p, int64_t chunk) {
     using R = Ring<T, V, PER * U, NT>;
-    constexpr int GROUPS = NT / G, STEP = G * V;
+    constexpr int GROUPS = NT / G, STEP = G * V, H = Pack<T, V>::H;
     constexpr bool KEEP = NT == 256 && V * PER <= ROW_VALUES;      // a run's weights stay in registers
     __shared__ float red[2 * NT / 32 * U];
     extern __shared__ __align__(16) unsigned char ring_memory[];
@@ -231,31 +240,33 @@ __global__ void __launch_bounds__(NT, resident(NT, V * PER * (U + 2))) norm_kern
     int turn = 0, run_end = 0;      // of the chunk's rows
     int64_t at = 0;
     bool used = false;
-    float kept_w[KEEP ? PER : 1][V], kept_b[KEEP ? PER : 1][V];
-    auto read_weights = [&](int j, float (&w)[V], float (&b)[V]) {
+    float2 kept_w[KEEP ? PER : 1][H], kept_b[KEEP ? PER : 1][H];
+    auto read_weights = [&](int j, float2 (&w)[H], float2 (&b)[H]) {
 #pragma unroll
-        for (int k = 0; k < V; ++k) w[k] = 1.0f, b[k] = 0.0f;
+        for (int k = 0; k < H; ++k) w[k] = pair(1.0f), b[k] = pair(0.0f);
         if (p.weight) load_weights<T, V>(p.weight, wide, at + j * STEP, w);
         if (p.bias) load_weights<T, V>(p.bias, wide, at + j * STEP, b);
     };
     for (int base = 0; base < n; base += GROUPS * U) {
-        float f[U][PER][V], sum[U], sq[U];
+        float2 f[U][PER][H];
+        float sum[U], sq[U];
         if (R::ASYNC) ring.wait();
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const bool in = base + u * GROUPS + g < n;
-            sum[u] = sq[u] = 0.0f;
+            float2 all = pair(0.0f);
 #pragma unroll
             for (int j = 0; j < PER; ++j) {
                 if (in && j * STEP < left) {
                     ring.get(u * PER + j, px + u * next + j * STEP, f[u][j]);
 #pragma unroll
-                    for (int i = 0; i < V; ++i) sum[u] += f[u][j][i];
+                    for (int i = 0; i < H; ++i) all = __fadd2_rn(all, f[u][j][i]);
                 } else {
 #pragma unroll
-                    for (int i = 0; i < V; ++i) f[u][j][i] = 0.0f;
+                    for (int i = 0; i < H; ++i) f[u][j][i] = pair(0.0f);
                 }
             }
+            sum[u] = all.x + all.y;
         }
         if (R::ASYNC) {
             ring.got();
@@ -267,15 +278,17 @@ __global__ void __launch_bounds__(NT, resident(NT, V * PER * (U + 2))) norm_kern
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             sum[u] *= inv;
+            float2 all = pair(0.0f);
 #pragma unroll
             for (int j = 0; j < PER; ++j) {
                 if (j * STEP >= left) continue;
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    f[u][j][i] -= sum[u];
-                    sq[u] = fmaf(f[u][j][i], f[u][j][i], sq[u]);
+                for (int i = 0; i < H; ++i) {
+                    f[u][j][i] = __fadd2_rn(f[u][j][i], pair(-sum[u]));
+                    all = __ffma2_rn(f[u][j][i], f[u][j][i], all);
                 }
             }
+            sq[u] = V > 1 ? all.x + all.y : all.x;
         }
         group_sum<G, NT, U>(sq, red, turn);
 #pragma unroll
@@ -302,15 +315,15 @@ __global__ void __launch_bounds__(NT, resident(NT, V * PER * (U + 2))) norm_kern
 #pragma unroll
             for (int j = 0; j < PER; ++j) {
                 if (j * STEP >= left) continue;
-                float w[V], b[V];
+                float2 w[H], b[H];
                 if constexpr (KEEP) {
 #pragma unroll
-                    for (int k = 0; k < V; ++k) w[k] = kept_w[j][k], b[k] = kept_b[j][k];
+                    for (int k = 0; k < H; ++k) w[k] = kept_w[j][k], b[k] = kept_b[j][k];
                 } else if (used) {
                     read_weights(j, w, b);
                 }
 #pragma unroll
-                for (int k = 0; k < V; ++k) f[u][j][k] = used ? fmaf(f[u][j][k] * rstd, w[k], b[k]) : 0.0f;
+                for (int k = 0; k < H; ++k) f[u][j][k] = used ? __ffma2_rn(__fmul2_rn(f[u][j][k], pair(rstd)), w[k], b[k]) : pair(0.0f);
                 Pack<T, V> o;
                 o.narrow(f[u][j]);
                 o.store(y + j * STEP);
@@ -354,10 +367,9 @@ __global__ void __launch_bounds__(256) norm_long_kernel(const __grid_constant__ 
         }
         T* y = static_cast<T*>(p.out) + r * p.ldo;
         for (int64_t c = threadIdx.x; c < p.F; c += 256) {
-            float w[1] = {1.0f}, b[1] = {0.0f};
-            if (used && p.weight) load_weights<T, 1>(p.weight, wide, run.s * p.F + c, w);
-            if (used && p.bias) load_weights<T, 1>(p.bias, wide, run.s * p.F + c, b);
-            y[c] = from_float<T>(used ? fmaf((to_float<T>(x[c]) - mean) * rstd, w[0], b[0]) : 0.0f);
+            const float w = used && p.weight ? load_weight<T>(p.weight, wide, run.s * p.F + c) : 1.0f;
+            const float b = used && p.bias ? load_weight<T>(p.bias, wide, run.s * p.F + c) : 0.0f;
+            y[c] = from_float<T>(used ? fmaf((to_float<T>(x[c]) - mean) * rstd, w, b) : 0.0f);
         }
     }
 }
@@ -387,9 +399,7 @@ __global__ void __launch_bounds__(256) norm_sums_kernel(const __grid_constant__ 
         const float mean = p.mean[r], rstd = p.rstd[r];
         float s1 = 0.0f, s2 = 0.0f;
         for (int64_t c = threadIdx.x; c < p.F; c += 256) {
-            float w[1] = {1.0f};
-            if (p.weight) load_weights<T, 1>(p.weight, wide, run.s * p.F + c, w);
-            const float gr = to_float<T>(dy[c]) * w[0];
+            const float gr = to_float<T>(dy[c]) * (p.weight ? load_weight<T>(p.weight, wide, run.s * p.F + c) : 1.0f);
             s1 += gr;
             s2 = fmaf(gr, (to_float<T>(x[c]) - mean) * rstd, s2);
         }
@@ -411,12 +421,13 @@ __device__ __forceinline__ void store_weight(void* out, int type, int64_t at, fl
 template <class T, int V, int G, int PER, int U, int NT>
 __global__ void __launch_bounds__(NT, resident(NT, V * PER * (2 * U + 3))) norm_grad_kernel(const __grid_constant__ GradArgs a) {
     using R = Ring<T, V, 2 * PER * U, NT>;
-    constexpr int E = V * PER, GROUPS = NT / G, STEP = G * V, WINDOW = GROUPS * U;
+    constexpr int GROUPS = NT / G, STEP = G * V, WINDOW = GROUPS * U, H = Pack<T, V>::H;
     constexpr bool KEEP = NT == 256;      // a run's weights stay in registers; a large block has none to spare and reads them again
     __shared__ float red[2 * NT / 32 * 2 * U];
     extern __shared__ __align__(16) unsigned char ring_memory[];
     float* const shared_sums = reinterpret_cast<float*>(ring_memory + R::BYTES);      // [groups of at least a warp][2][tile]
     R ring(ring_memory);
+    grid_trigger();
     const NormParams& p = a.p;
     const int t = threadIdx.x % G, g = threadIdx.x / G;
     const int64_t c0 = blockIdx.x * a.chunk;
@@ -442,8 +453,13 @@ __global__ void __launch_bounds__(NT, resident(NT, V * PER * (2 * U + 3))) norm_
         }
         ring.fetched();
     };
-    if (R::ASYNC)
+    if (R::ASYNC) {
+#pragma unroll
+        for (int j = 0; j < PER; ++j)
+            if (j * STEP >= left)
+                for (int u = 0; u < U; ++u) ring.clear((u * PER + j) * 2), ring.clear((u * PER + j) * 2 + 1);
         for (int d = 0; d < R::D - 1; ++d) fetch(d * WINDOW + g);
+    }
     if (want_dw && p.offsets) {
         // segments without rows
         const int64_t each = (p.S + gridDim.x - 1) / gridDim.x, s1 = min((blockIdx.x + 1) * each, p.S);
@@ -456,19 +472,19 @@ __global__ void __launch_bounds__(NT, resident(NT, V * PER * (2 * U + 3))) norm_
         }
     }
     Run run = run_of(p, c0);
-    float kept[KEEP ? PER : 1][V], dw[E], db[E];
-    auto read_weights = [&](int j, float (&w)[V]) {
+    float2 kept[KEEP ? PER : 1][H], dw[PER][H], db[PER][H];
+    auto read_weights = [&](int j, float2 (&w)[H]) {
         if (p.weight && run.s >= 0 && j * STEP < left) {
             load_weights<T, V>(p.weight, wide, run.s * p.F + col0 + t * V + j * STEP, w);
         } else {
 #pragma unroll
-            for (int i = 0; i < V; ++i) w[i] = 1.0f;
+            for (int i = 0; i < H; ++i) w[i] = pair(1.0f);
         }
     };
-    auto weights_of = [&](int j, float (&w)[V]) {
+    auto weights_of = [&](int j, float2 (&w)[H]) {
         if constexpr (KEEP) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) w[i] = kept[j][i];
+            for (int i = 0; i < H; ++i) w[i] = kept[j][i];
         } else {
             read_weights(j, w);
         }
@@ -479,35 +495,42 @@ __global__ void __launch_bounds__(NT, resident(NT, V * PER * (2 * U + 3))) norm_
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) dw[j * V + i] = 0.0f, db[j * V + i] = 0.0f;
+            for (int i = 0; i < H; ++i) dw[j][i] = db[j][i] = pair(0.0f);
             if constexpr (KEEP) read_weights(j, kept[j]);
         }
     };
     begin();
     float next_mean[U], next_rstd[U];
+    const float* pm = p.mean + c0 + g;
+    const float* pr = p.rstd + c0 + g;
     auto fetch_stats = [&](int i) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             next_mean[u] = next_rstd[u] = 0.0f;
-            if (i + u * GROUPS < n) next_mean[u] = __ldg(p.mean + c0 + i + u * GROUPS), next_rstd[u] = __ldg(p.rstd + c0 + i + u * GROUPS);
+            if (i + u * GROUPS < n) next_mean[u] = __ldg(pm + u * GROUPS), next_rstd[u] = __ldg(pr + u * GROUPS);
         }
+        pm += WINDOW;
+        pr += WINDOW;
     };
     fetch_stats(g);
+    const int64_t nexto = GROUPS * p.ldo;
+    T* po = static_cast<T*>(p.out) + (c0 + g) * p.ldo + col0 + t * V;
     int turn = 0;
     for (int base = 0; base < n; base += WINDOW) {
         const int end = min(base + WINDOW, n);
-        float kept_z[KEEP ? U : 1][KEEP ? PER : 1][V], kept_dy[KEEP ? U : 1][KEEP ? PER : 1][V], mean[U], rstd[U];
+        float2 kept_z[KEEP ? U : 1][KEEP ? PER : 1][H], kept_dy[KEEP ? U : 1][KEEP ? PER : 1][H];
+        float mean[U], rstd[U];
         if (R::ASYNC) ring.wait();
-        auto read_values = [&](int u, int j, float (&z)[V], float (&dy)[V]) {
+        auto read_values = [&](int u, int j, float2 (&z)[H], float2 (&dy)[H]) {
             ring.get((u * PER + j) * 2, px + u * nextx + j * STEP, z);
             ring.get((u * PER + j) * 2 + 1, pd + u * nexty + j * STEP, dy);
 #pragma unroll
-            for (int i = 0; i < V; ++i) z[i] = (z[i] - mean[u]) * rstd[u];
+            for (int i = 0; i < H; ++i) z[i] = __fmul2_rn(__fadd2_rn(z[i], pair(-mean[u])), pair(rstd[u]));
         };
-        auto values_of = [&](int u, int j, float (&z)[V], float (&dy)[V]) {
+        auto values_of = [&](int u, int j, float2 (&z)[H], float2 (&dy)[H]) {
             if constexpr (KEEP) {
 #pragma unroll
-                for (int i = 0; i < V; ++i) z[i] = kept_z[u][j][i], dy[i] = kept_dy[u][j][i];
+                for (int i = 0; i < H; ++i) z[i] = kept_z[u][j][i], dy[i] = kept_dy[u][j][i];
             } else {
                 read_values(u, j, z, dy);
             }
@@ -528,7 +551,7 @@ __global__ void __launch_bounds__(NT, resident(NT, V * PER * (2 * U + 3))) norm_
             if constexpr (KEEP)
 #pragma unroll
                 for (int j = 0; j < PER; ++j)
-                    if (base + u * GROUPS + g < n && j * STEP < left) read_values(u, j, kept_z[u][j], kept_dy[u][j]);
+                    if (R::ASYNC || (base + u * GROUPS + g < n && j * STEP < left)) read_values(u, j, kept_z[u][j], kept_dy[u][j]);
         }
         if constexpr (KEEP) values_read();
         fetch_stats(base + WINDOW + g);
@@ -536,61 +559,70 @@ __global__ void __launch_bounds__(NT, resident(NT, V * PER * (2 * U + 3))) norm_
         for (;;) {
             const int to = min(run_end, end);
             auto in = [&](int u) { return base + u * GROUPS + g >= from && base + u * GROUPS + g < to; };
-            if (run.s >= 0) {
+            // one run's rows of the window; ALL: they are all there (columns that
+            // the row does not have count as zeros)
+            auto work = [&](auto all) {
+                constexpr bool ALL = decltype(all)::value;
                 float s[2 * U];
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    s[2 * u] = s[2 * u + 1] = 0.0f;
-                    if (!in(u)) continue;
-#pragma unroll
-                    for (int j = 0; j < PER; ++j) {
-                        if (j * STEP >= left) continue;
-                        float w[V], z[V], dy[V];
-                        weights_of(j, w);
-                        values_of(u, j, z, dy);
-#pragma unroll
-                        for (int i = 0; i < V; ++i) {
-                            const float gr = dy[i] * w[i];
-                            db[j * V + i] += dy[i];
-                            dw[j * V + i] = fmaf(dy[i], z[i], dw[j * V + i]);
-                            s[2 * u] += gr;
-                            s[2 * u + 1] = fmaf(gr, z[i], s[2 * u + 1]);
-                        }
-                    }
-                }
-                if (want_dx) {
-                    if (!a.sums) group_sum<G, NT, 2 * U>(s, red, turn);
-#pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        if (!in(u)) continue;
-                        const int64_t r = c0 + base + u * GROUPS + g;
-                        if (a.sums) s[2 * u] = __ldg(a.sums + 2 * r), s[2 * u + 1] = __ldg(a.sums + 2 * r + 1);
-                        const float m1 = s[2 * u] * inv, m2 = s[2 * u + 1] * inv;
-                        T* out = static_cast<T*>(p.out) + r * p.ldo + col0 + t * V;
+                    float2 s1 = pair(0.0f), s2 = pair(0.0f);
+                    if (ALL || in(u))
 #pragma unroll
                         for (int j = 0; j < PER; ++j) {
-                            if (j * STEP >= left) continue;
-                            Pack<T, V> o;
-                            float w[V], z[V], dy[V], d[V];
+                            if (!R::ASYNC && j * STEP >= left) continue;
+                            float2 w[H], z[H], dy[H];
                             weights_of(j, w);
                             values_of(u, j, z, dy);
 #pragma unroll
-                            for (int i = 0; i < V; ++i) d[i] = rstd[u] * fmaf(-z[i], m2, fmaf(dy[i], w[i], -m1));
-                            o.narrow(d);
-                            o.store(out + j * STEP);
+                            for (int i = 0; i < H; ++i) {
+                                const float2 gr = __fmul2_rn(dy[i], w[i]);
+                                db[j][i] = __fadd2_rn(db[j][i], dy[i]);
+                                dw[j][i] = __ffma2_rn(dy[i], z[i], dw[j][i]);
+                                s1 = __fadd2_rn(s1, gr);
+                                s2 = __ffma2_rn(gr, z[i], s2);
+                            }
                         }
+                    s[2 * u] = s1.x + s1.y;
+                    s[2 * u + 1] = s2.x + s2.y;
+                }
+                if (!want_dx) return;
+                if (!a.sums) group_sum<G, NT, 2 * U>(s, red, turn);
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if (!ALL && !in(u)) continue;
+                    if (a.sums) {
+                        const int64_t r = c0 + base + u * GROUPS + g;
+                        s[2 * u] = __ldg(a.sums + 2 * r), s[2 * u + 1] = __ldg(a.sums + 2 * r + 1);
+                    }
+                    const float2 m1 = pair(-s[2 * u] * inv), m2 = pair(-s[2 * u + 1] * inv), scale = pair(rstd[u]);
+#pragma unroll
+                    for (int j = 0; j < PER; ++j) {
+                        if (!R::ASYNC && j * STEP >= left) continue;
+                        Pack<T, V> o;
+                        float2 w[H], z[H], dy[H], d[H];
+                        weights_of(j, w);
+                        values_of(u, j, z, dy);
+#pragma unroll
+                        for (int i = 0; i < H; ++i) d[i] = __fmul2_rn(scale, __ffma2_rn(z[i], m2, __ffma2_rn(dy[i], w[i], m1)));
+                        o.narrow(d);
+                        if (j * STEP < left) o.store(po + u * nexto + j * STEP);
                     }
                 }
+            };
+            if (run.s >= 0) {
+                if (from == base && to == base + WINDOW) work(std::true_type());
+                else work(std::false_type());
             } else if (want_dx) {
                 // rows in no segment
-                const float none[V] = {};
+                const float2 none[H] = {};
                 Pack<T, V> zero;
                 zero.narrow(none);
 #pragma unroll
                 for (int u = 0; u < U; ++u)
 #pragma unroll
                     for (int j = 0; j < PER; ++j)
-                        if (in(u) && j * STEP < left) zero.store(static_cast<T*>(p.out) + (c0 + base + u * GROUPS + g) * p.ldo + col0 + t * V + j * STEP);
+                        if (in(u) && j * STEP < left) zero.store(po + u * nexto + j * STEP);
             }
             if (run_end > end && end < n) break;       // the run goes on in the next window
             if (want_dw && run.s >= 0) {
@@ -599,10 +631,10 @@ __global__ void __launch_bounds__(NT, resident(NT, V * PER * (2 * U + 3))) norm_
 #pragma unroll
                 for (int d = 16; d >= G; d >>= 1) {
 #pragma unroll
-                    for (int i = 0; i < E; ++i) {
-                        dw[i] += __shfl_xor_sync(0xffffffffu, dw[i], d);
-                        db[i] += __shfl_xor_sync(0xffffffffu, db[i], d);
-                    }
+                    for (int j = 0; j < PER; ++j)
+#pragma unroll
+                        for (int i = 0; i < H; ++i)
+                            for (float* v : {&dw[j][i].x, &dw[j][i].y, &db[j][i].x, &db[j][i].y}) *v += __shfl_xor_sync(0xffffffffu, *v, d);
                 }
                 const bool whole = run.begin >= c0 && run.end <= c0 + n;
                 float* slot_sums = a.partials + (2 * int64_t(blockIdx.x) + (run.begin >= c0 ? 1 : 0)) * 2 * p.F;
@@ -616,7 +648,10 @@ __global__ void __launch_bounds__(NT, resident(NT, V * PER * (2 * U + 3))) norm_
                     for (int j = 0; j < PER; ++j)
 #pragma unroll
                         for (int i = 0; i < V; ++i)
-                            if (j * STEP < left) put(0, col0 + t * V + j * STEP + i, dw[j * V + i]), put(1, col0 + t * V + j * STEP + i, db[j * V + i]);
+                            if (j * STEP < left) {
+                                put(0, col0 + t * V + j * STEP + i, i % 2 ? dw[j][i / 2].y : dw[j][i / 2].x);
+                                put(1, col0 + t * V + j * STEP + i, i % 2 ? db[j][i / 2].y : db[j][i / 2].x);
+                            }
                 } else {
                     constexpr int WIDE = G < 32 ? 32 : G, PARTS = NT / WIDE;
                     float* own = shared_sums + threadIdx.x / WIDE * 2 * a.tile;
@@ -628,8 +663,8 @@ __global__ void __launch_bounds__(NT, resident(NT, V * PER * (2 * U + 3))) norm_
                             for (int i = 0; i < V; ++i) {
                                 const int c = t * V + j * STEP + i;
                                 if (c >= a.tile) continue;
-                                own[c] = dw[j * V + i];
-                                own[a.tile + c] = db[j * V + i];
+                                own[c] = i % 2 ? dw[j][i / 2].y : dw[j][i / 2].x;
+                                own[a.tile + c] = i % 2 ? db[j][i / 2].y : db[j][i / 2].x;
                             }
                     }
                     __syncthreads();
@@ -649,19 +684,20 @@ __global__ void __launch_bounds__(NT, resident(NT, V * PER * (2 * U + 3))) norm_
             begin();
             if (from >= end) break;
         }
+        po += U * nexto;
         if constexpr (!KEEP) values_read();
     }
 }
 
 // Adds the parts of a segment that more than one chunk has rows of: blockIdx.x
 // names the segment, or (by_start) the chunk in which it starts; blockIdx.y the
-// first `lanes` of the 2 F sums.  Each of the block's 512 / lanes rows of threads
-// adds an equal share of the parts in order, then theirs are added.
+// first `lanes` x V of the 2 F sums.  Each of the block's ADD_THREADS / lanes rows
+// of threads adds an equal share of the parts in order, then theirs are added.
 constexpr int ADD_THREADS = 512;
+template <int V>
 __global__ void __launch_bounds__(ADD_THREADS) norm_add_kernel(const __grid_constant__ GradArgs a, int by_start, int lanes) {
-    __shared__ float sums[ADD_THREADS];
+    __shared__ float sums[V][ADD_THREADS];
     const NormParams& p = a.p;
-    grid_wait();
     int64_t s = blockIdx.x, begin = 0, end = p.R;
     if (by_start) {
         const Run run = run_of(p, min((int64_t(blockIdx.x) + 1) * a.chunk, p.R) - 1);
@@ -674,22 +710,36 @@ __global__ void __launch_bounds__(ADD_THREADS) norm_add_kernel(const __grid_cons
     const int64_t first = begin / a.chunk, last = (end - 1) / a.chunk;
     if (first == last) return;
     const int lane = threadIdx.x % lanes, share = threadIdx.x / lanes, shares = ADD_THREADS / lanes;
-    const int64_t parts = last - first + 1, each = (parts + shares - 1) / shares;
-    const int64_t q0 = share * each, q1 = min(q0 + each, parts);
-    for (int64_t i0 = int64_t(blockIdx.y) * lanes; i0 < 2 * p.F; i0 += int64_t(gridDim.y) * lanes) {
-        const int64_t i = i0 + lane;
-        float v = 0.0f;
+    const int parts = static_cast<int>(last - first + 1), each = (parts + shares - 1) / shares;
+    const int q0 = share * each, q1 = min(q0 + each, parts);
+    grid_wait();
+    for (int64_t i0 = int64_t(blockIdx.y) * lanes * V; i0 < 2 * p.F; i0 += int64_t(gridDim.y) * lanes * V) {
+        const int64_t i = i0 + lane * V;
+        float v[V];
+#pragma unroll
+        for (int k = 0; k < V; ++k) v[k] = 0.0f;
         if (i < 2 * p.F) {
 #pragma unroll 8
-            for (int64_t q = q0; q < q1; ++q) v += __ldcg(a.partials + (2 * (first + q) + (q == 0 ? 1 : 0)) * 2 * p.F + i);
+            for (int q = q0; q < q1; ++q) {
+                const float* from = a.partials + (2 * (first + q) + (q == 0 ? 1 : 0)) * 2 * p.F + i;
+                if constexpr (V == 4) {
+                    const float4 x = __ldcg(reinterpret_cast<const float4*>(from));
+                    v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
+                } else {
+                    v[0] += __ldcg(from);
+                }
+            }
         }
-        sums[threadIdx.x] = v;
+#pragma unroll
+        for (int k = 0; k < V; ++k) sums[k][threadIdx.x] = v[k];
         __syncthreads();
-        if (share == 0 && i < 2 * p.F) {
-            v = 0.0f;
-            for (int q = 0; q < shares; ++q) v += sums[q * lanes + lane];
-            void* out = i < p.F ? p.dweight : p.dbias;
-            if (out) store_weight(out, p.weight_type, s * p.F + (i < p.F ? i : i - p.F), v);
+        for (int k = threadIdx.x; k < lanes * V; k += ADD_THREADS) {
+            const int64_t c = i0 + k;
+            if (c >= 2 * p.F) break;
+            float total = 0.0f;
+            for (int q = 0; q < shares; ++q) total += sums[k % V][q * lanes + k / V];
+            void* out = c < p.F ? p.dweight : p.dbias;
+            if (out) store_weight(out, p.weight_type, s * p.F + (c < p.F ? c : c - p.F), total);
         }
         __syncthreads();
     }
@@ -835,19 +885,20 @@ cudaError_t launch_norm_grad(const NormParams& p, const NormPlan& plan, cudaStre
     else e = launch_grad_type<__nv_bfloat16>(a, plan, stream);
     if (e != cudaSuccess || plan.chunks < 2 || (!p.dweight && !p.dbias)) return e;
     const bool by_start = p.S >= plan.chunks;
-    // columns of a block: the fewer segments, the more parts there are of each
-    int lanes = 32;
-    while (lanes < 256 && lanes < p.S) lanes *= 2;
+    // a thread adds about four parts; the fewer segments, the more parts there are of each
+    int shares = 1;
+    while (shares < 32 && (plan.chunks / p.S + 1) / (shares * 2) >= 4) shares *= 2;
+    const int lanes = ADD_THREADS / shares, v = p.F % 2 == 0 ? 4 : 1;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(by_start ? plan.chunks - 1 : p.S), static_cast<unsigned>(std::min<int64_t>(ceil_to(2 * p.F, lanes), 16384)));
+    cfg.gridDim = dim3(static_cast<unsigned>(by_start ? plan.chunks - 1 : p.S), static_cast<unsigned>(std::min<int64_t>(ceil_to(2 * p.F, lanes * v), 16384)));
     cfg.blockDim = dim3(ADD_THREADS);
     cfg.stream = stream;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, norm_add_kernel, a, static_cast<int>(by_start), lanes);
+    return cudaLaunchKernelEx(&cfg, v == 4 ? norm_add_kernel<4> : norm_add_kernel<1>, a, static_cast<int>(by_start), lanes);
 }
 
 }  // namespace segred
