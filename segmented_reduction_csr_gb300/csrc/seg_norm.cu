@@ -85,7 +85,7 @@ template <class T, int V> struct Pack {
 // does not hold two, are loaded when they are needed.)
 template <class T, int V, int PER, int NT>
 struct Ring {
-    static constexpr int D = PER == 1 ? 6 : PER == 2 ? 4 : PER <= 4 ? 3 : 2;      // fewer bytes of a slot want more of them
+    static constexpr int D = PER == 1 ? 6 : PER <= 4 && NT == 256 ? 4 : PER == 2 ? 4 : PER <= 4 ? 3 : 2;      // fewer bytes of a slot want more of them
     static constexpr bool ASYNC = V * sizeof(T) == 16 && D * PER * NT * 16 <= 200 * 1024;
     static constexpr int SLOT = PER * NT * 16, BYTES = ASYNC ? D * SLOT : 0;
     uint32_t base, at, to;      // the thread's first slot, the one to read and the one to fetch into
@@ -134,6 +134,22 @@ __device__ __forceinline__ void load_weights(const void* w, bool wide, int64_t a
         }
     }
 }
+template <class T, int V>
+__device__ __forceinline__ void store_weights(void* out, bool wide, int64_t at, const float2 (&f)[Pack<T, V>::H]) {
+    if (!wide) {
+        Pack<T, V> x;
+        x.narrow(f);
+        x.store(static_cast<T*>(out) + at);
+        return;
+    }
+    float* p = static_cast<float*>(out) + at;
+    if constexpr (V == 1) {
+        *p = f[0].x;
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; i += 4) *reinterpret_cast<float4*>(p + i) = make_float4(f[i / 2].x, f[i / 2].y, f[i / 2 + 1].x, f[i / 2 + 1].y);
+    }
+}
 template <class T>
 __device__ __forceinline__ float load_weight(const void* w, bool wide, int64_t at) {
     return wide ? __ldg(static_cast<const float*>(w) + at) : to_float<T>(static_cast<const T*>(w)[at]);
@@ -151,13 +167,11 @@ struct Run {
 };
 __device__ __forceinline__ Run run_of(const NormParams& p, int64_t r) {
     if (!p.offsets) return {0, 0, p.R};
-    int64_t lo = -1, hi = p.S;      // the last offset at or before r; hi: the first one after it, or S
-    if (p.S > 0 && offset_at(p, p.S) <= r) lo = p.S;
-    else
-        while (hi - lo > 1) {
-            const int64_t mid = (lo + hi) >> 1;
-            if (offset_at(p, mid) <= r) lo = mid; else hi = mid;
-        }
+    int64_t lo = -1, hi = p.S + 1;      // the last offset at or before r; the first one after it
+    while (hi - lo > 1) {
+        const int64_t mid = (lo + hi) >> 1;
+        if (offset_at(p, mid) <= r) lo = mid; else hi = mid;
+    }
     Run x;
     if (lo < 0 || lo >= p.S) {
         x.begin = lo < 0 ? 0 : r;
@@ -208,7 +222,7 @@ constexpr int ROW_VALUES = 16, ROWS = 2;
 
 // G threads a row, U rows of a group at a time.
 template <class T, int V, int G, int PER, int U, int NT>
-__global__ void __launch_bounds__(NT, resident(NT, V * PER * (U + 2))) norm_kernel(const __grid_constant__ NormParams p, int64_t chunk) {
+__global__ void __launch_bounds__(NT, resident(NT, Pack<T, V>::H * 2 * PER * (U + 2))) norm_kernel(const __grid_constant__ NormParams p, int64_t chunk) {
     using R = Ring<T, V, PER * U, NT>;
     constexpr int GROUPS = NT / G, STEP = G * V, H = Pack<T, V>::H;
     constexpr bool KEEP = NT == 256 && V * PER <= ROW_VALUES;      // a run's weights stay in registers
@@ -419,7 +433,7 @@ __device__ __forceinline__ void store_weight(void* out, int type, int64_t at, fl
 // segments they are in; a window in which a run ends is worked on once for each
 // run that has a row in it.
 template <class T, int V, int G, int PER, int U, int NT>
-__global__ void __launch_bounds__(NT, resident(NT, V * PER * (2 * U + 3))) norm_grad_kernel(const __grid_constant__ GradArgs a) {
+__global__ void __launch_bounds__(NT, resident(NT, Pack<T, V>::H * 2 * PER * (2 * U + 3))) norm_grad_kernel(const __grid_constant__ GradArgs a) {
     using R = Ring<T, V, 2 * PER * U, NT>;
     constexpr int GROUPS = NT / G, STEP = G * V, WINDOW = GROUPS * U, H = Pack<T, V>::H;
     constexpr bool KEEP = NT == 256;      // a run's weights stay in registers; a large block has none to spare and reads them again
@@ -645,13 +659,17 @@ __global__ void __launch_bounds__(NT, resident(NT, V * PER * (2 * U + 3))) norm_
                 };
                 if constexpr (G == NT) {
 #pragma unroll
-                    for (int j = 0; j < PER; ++j)
-#pragma unroll
-                        for (int i = 0; i < V; ++i)
-                            if (j * STEP < left) {
-                                put(0, col0 + t * V + j * STEP + i, i % 2 ? dw[j][i / 2].y : dw[j][i / 2].x);
-                                put(1, col0 + t * V + j * STEP + i, i % 2 ? db[j][i / 2].y : db[j][i / 2].x);
-                            }
+                    for (int j = 0; j < PER; ++j) {
+                        const int c = col0 + t * V + j * STEP;
+                        if (j * STEP >= left) continue;
+                        if (whole) {
+                            if (p.dweight) store_weights<T, V>(p.dweight, wide, run.s * p.F + c, dw[j]);
+                            if (p.dbias) store_weights<T, V>(p.dbias, wide, run.s * p.F + c, db[j]);
+                        } else {
+                            store_weights<T, V>(slot_sums, true, c, dw[j]);
+                            store_weights<T, V>(slot_sums, true, p.F + c, db[j]);
+                        }
+                    }
                 } else {
                     constexpr int WIDE = G < 32 ? 32 : G, PARTS = NT / WIDE;
                     float* own = shared_sums + threadIdx.x / WIDE * 2 * a.tile;
@@ -828,7 +846,7 @@ NormPlan plan_norm(bool grad, const NormParams& p) {
     const int size = p.type == PT_F32 ? 4 : 2, v = 16 / size;
     // whole 16-byte loads of every operand
     const bool vec = p.F % v == 0 && p.ldx % v == 0 && aligned16(p.x) && (!p.out || (p.ldo % v == 0 && aligned16(p.out))) &&
-                     (!grad || (p.ldy % v == 0 && aligned16(p.dy))) && aligned16(p.weight) && aligned16(p.bias);
+                     (!grad || (p.ldy % v == 0 && aligned16(p.dy))) && aligned16(p.weight) && aligned16(p.bias) && aligned16(p.dweight) && aligned16(p.dbias);
     d.vec = vec ? v : 1;
     d.tiles = 1;
     const int64_t loads = ceil_to(p.F, d.vec);
@@ -858,7 +876,7 @@ NormPlan plan_norm(bool grad, const NormParams& p) {
     const int rows = !grad && d.threads == 256 ? ROWS : 1;
     const int64_t window = d.per == 0 ? 1 : d.threads / d.group * rows;
     const int64_t most_blocks = d.per == 0 ? int64_t(p.sms) * 8
-                                           : std::max<int64_t>(p.sms * resident(d.threads, d.per * d.vec * (grad ? 5 : rows + 2)) / d.tiles, 1);
+                                           : std::max<int64_t>(p.sms * resident(d.threads, d.per * std::max(d.vec, 2) * (grad ? 5 : rows + 2)) / d.tiles, 1);
     d.chunk = ceil_to(ceil_to(p.R, most_blocks), window) * window;
     d.chunks = ceil_to(p.R, d.chunk);
     if (d.per == 0) d.chunks = std::min<int64_t>(p.R, most_blocks);
