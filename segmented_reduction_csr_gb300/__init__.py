@@ -635,7 +635,7 @@ def _row_stride(name, t):
     step, one = t.stride()[-2:]
     if (one != 1 and cols > 1) or (rows > 1 and step < cols):
         raise ValueError(f"{name} must have contiguous rows that do not overlap")
-    return step if rows > 1 else max(cols, 1)
+    return step if rows > 1 else cols or 1
 
 
 def _same(name, t, like, shape, dtype=None):
@@ -665,19 +665,28 @@ def _in_use(stream, *tensors):
             t.record_stream(stream)
 
 
+_raw_stream = _current_device = None
+
+
+def _find_host_functions():
+    global _raw_stream, _current_device
+    torch = _torch()
+    if hasattr(torch._C, "_cuda_getCurrentRawStream") and hasattr(torch._C, "_cuda_getDevice"):
+        _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+    else:
+        _raw_stream, _current_device = lambda index: torch.cuda.current_stream(index).cuda_stream, torch.cuda.current_device
+
+
 def _enqueue(where, device, stream, fn, *args):
     """Calls a product of the library on ``stream`` (default: ``device``'s current one)."""
-    torch = _torch()
-    if stream is not None:
-        raw = stream.cuda_stream
-    elif hasattr(torch._C, "_cuda_getCurrentRawStream"):
-        raw = torch._C._cuda_getCurrentRawStream(device.index)
-    else:
-        raw = torch.cuda.current_stream(device).cuda_stream
-    if torch.cuda.current_device() == device.index:
+    if _raw_stream is None:
+        _find_host_functions()
+    index = device.index
+    raw = _raw_stream(index) if stream is None else stream.cuda_stream
+    if _current_device() == index:
         rc = fn(*args, raw)
     else:
-        with torch.cuda.device(device):
+        with _torch().cuda.device(device):
             rc = fn(*args, raw)
     if rc != 0:
         raise SegReduceError(rc, where)
@@ -858,7 +867,7 @@ def _rows_out(name, out, like, shape, stream, dtype=None):
         torch = _torch()
         dtype = like.dtype if dtype is None else dtype
         out = torch.empty(shape, dtype=dtype, device=like.device) if stream is None else _fresh(shape, dtype, like.device, stream)
-        return out, max(shape[1], 1)
+        return out, shape[1] or 1
     _same(name, out, like, shape, dtype)
     return out, _row_stride(name, out)
 
@@ -987,33 +996,31 @@ def _segment_gated_function():
     return _segment_gated_fn
 
 
-def _norm_arguments(x, weight, offsets):
-    """Rows' stride, type codes of x and the weights, segments and their offsets' code."""
-    torch = _torch()
+def _norm_arguments(x, weight, bias, offsets):
+    """Checks a norm's input and weights; the rows' stride, type codes of x and
+    the weights, segments and their offsets' code."""
     if offsets is None:
         if not x.is_cuda:
             raise ValueError("x must be a CUDA tensor (there is no CPU path)")
         if x.dim() != 2:
             raise ValueError("x must be [R, columns]")
-        ldx, s, odt = _row_stride("x", x), 1, SEG_OFF_I64
+        ldx, s, odt, shape = _row_stride("x", x), 1, SEG_OFF_I64, x.shape[1:]
     else:
         ldx = _check_rows("x", x, offsets)
         s, odt = offsets.shape[0] - 1, _offset_code(offsets)
+        shape = (s, x.shape[1])
     code = wcode = _product_code(x)
-    if weight is not None:
-        if weight.dtype not in (x.dtype, torch.float32):
-            raise TypeError(f"weight must be {x.dtype} or torch.float32, not {weight.dtype}")
-        wcode = _product_code(weight)
+    like = bias if weight is None else weight
+    if like is not None:
+        wcode = _product_code(like)
+        if wcode != code and wcode != SEG_F32:
+            raise TypeError(f"weight and bias must be {x.dtype} or torch.float32, not {like.dtype}")
+        for name, t in (("weight", weight), ("bias", bias)):
+            if t is not None:
+                _same(name, t, x, shape, like.dtype)
+                if not t.is_contiguous():
+                    raise ValueError(f"{name} must be contiguous")
     return ldx, code, wcode, s, odt
-
-
-def _norm_weight(name, t, x, weight, s, offsets):
-    """Checks a norm's weight or bias."""
-    if t is None:
-        return
-    _same(name, t, x, (x.shape[1],) if offsets is None else (s, x.shape[1]), weight.dtype)
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
 
 
 def seg_layer_norm(x, weight=None, bias=None, offsets=None, eps: float = 1e-5, with_stats: bool = False, out=None, stream=None):
@@ -1030,17 +1037,14 @@ def seg_layer_norm(x, weight=None, bias=None, offsets=None, eps: float = 1e-5, w
     for ``seg_layer_norm_grad``).  Computed in float32 and rounded once.  It
     records no gradient (``segment_layer_norm`` does).  ``stream`` and graphs as
     for ``seg_matmul``; not synchronised."""
-    torch = _torch()
-    like = bias if weight is None else weight
-    ldx, code, wcode, s, odt = _norm_arguments(x, like, offsets)
-    _norm_weight("weight", weight, x, like, s, offsets)
-    _norm_weight("bias", bias, x, like, s, offsets)
+    ldx, code, wcode, s, odt = _norm_arguments(x, weight, bias, offsets)
     if not 0.0 <= eps < float("inf"):
         raise ValueError("eps must be finite and not negative")
     r, f = x.shape
     out, ldo = _rows_out("out", out, x, (r, f), stream)
     mean = rstd = None
     if with_stats:
+        torch = _torch()
         stats = torch.empty((2, r), dtype=torch.float32, device=x.device) if stream is None else _fresh((2, r), torch.float32, x.device, stream)
         mean, rstd = stats[0], stats[1]
     _enqueue("seg_layer_norm", x.device, stream, load_library().seg_layer_norm, x.data_ptr() or None, code, r, f, ldx,
@@ -1063,14 +1067,13 @@ def seg_layer_norm_grad(x, dy, mean, rstd, weight=None, offsets=None, with_dx: b
     for a segment without rows.  Arguments, ``stream`` and graphs as for
     ``seg_layer_norm``; not synchronised."""
     torch = _torch()
-    ldx, code, wcode, s, odt = _norm_arguments(x, weight, offsets)
+    ldx, code, wcode, s, odt = _norm_arguments(x, weight, None, offsets)
     if weight is None and weight_dtype is not None:
         if weight_dtype not in (x.dtype, torch.float32):
             raise TypeError(f"weight_dtype must be {x.dtype} or torch.float32, not {weight_dtype}")
         wtype, wcode = weight_dtype, code if weight_dtype == x.dtype else SEG_F32
     else:
         wtype = x.dtype if weight is None else weight.dtype
-    _norm_weight("weight", weight, x, weight, s, offsets)
     r, f = x.shape
     _same("dy", dy, x, (r, f))
     ldy = _row_stride("dy", dy)

@@ -261,6 +261,17 @@ __global__ void __launch_bounds__(NT, resident(NT, Pack<T, V>::H * 2 * PER * (U 
         if (p.weight) load_weights<T, V>(p.weight, wide, at + j * STEP, w);
         if (p.bias) load_weights<T, V>(p.bias, wide, at + j * STEP, b);
     };
+    auto find_run = [&](int i) {
+        const Run run = run_of(p, c0 + i);
+        run_end = static_cast<int>(min(run.end - c0, int64_t(n)));
+        used = run.s >= 0;
+        at = run.s * p.F + t * V;
+        if constexpr (KEEP)
+#pragma unroll
+            for (int j = 0; j < PER; ++j)
+                if (used && j * STEP < left) read_weights(j, kept_w[j], kept_b[j]);
+    };
+    if (g < n) find_run(g);        // while the first rows are on their way
     for (int base = 0; base < n; base += GROUPS * U) {
         float2 f[U][PER][H];
         float sum[U], sq[U];
@@ -310,16 +321,7 @@ __global__ void __launch_bounds__(NT, resident(NT, Pack<T, V>::H * 2 * PER * (U 
             const int i = base + u * GROUPS + g;
             if (i >= n) break;
             const int64_t r = c0 + i;
-            if (i >= run_end) {
-                const Run run = run_of(p, r);
-                run_end = static_cast<int>(min(run.end - c0, int64_t(n)));
-                used = run.s >= 0;
-                at = run.s * p.F + t * V;
-                if constexpr (KEEP)
-#pragma unroll
-                    for (int j = 0; j < PER; ++j)
-                        if (used && j * STEP < left) read_weights(j, kept_w[j], kept_b[j]);
-            }
+            if (i >= run_end) find_run(i);
             const float rstd = rsqrtf(fmaf(sq[u], inv, p.eps));
             if (t == 0) {
                 if (p.mean) p.mean[r] = used ? sum[u] : 0.0f;
@@ -766,17 +768,25 @@ __global__ void __launch_bounds__(ADD_THREADS) norm_add_kernel(const __grid_cons
 int64_t ceil_to(int64_t n, int64_t d) { return (n + d - 1) / d; }
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
+// Allows a kernel its shared memory: once per device (the call takes as long as
+// a launch).  Callers hold the library's lock.
 template <class K>
-cudaError_t allow_smem(K* kernel, int bytes) {
-    // (48 KB are allowed unasked, with the kernel's own)
-    return bytes > 40 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) : cudaSuccess;
+cudaError_t allow_smem(K* kernel, int bytes, int (&allowed)[64]) {
+    if (bytes <= 40 * 1024) return cudaSuccess;      // (48 KB are allowed unasked, with the kernel's own)
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || allowed[dev] >= bytes) return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) allowed[dev] = bytes;
+    return e;
 }
 
 template <class T, int V, int G, int PER>
 cudaError_t launch_rows(const NormParams& p, const NormPlan& plan, cudaStream_t stream) {
     constexpr int NT = G > 256 ? G : 256, U = NT == 256 ? ROWS : 1, smem = Ring<T, V, PER * U, NT>::BYTES;
     auto* kernel = norm_kernel<T, V, G, PER, U, NT>;
-    const cudaError_t e = allow_smem(kernel, smem);
+    static int allowed[64] = {};
+    const cudaError_t e = allow_smem(kernel, smem, allowed);
     if (e != cudaSuccess) return e;
     kernel<<<static_cast<unsigned>(plan.chunks), NT, smem, stream>>>(p, plan.chunk);
     return cudaGetLastError();
@@ -787,7 +797,8 @@ cudaError_t launch_grad_rows(const GradArgs& a, const NormPlan& plan, cudaStream
     constexpr int NT = G > 256 ? G : 256;
     auto* kernel = norm_grad_kernel<T, V, G, PER, 1, NT>;
     const int smem = Ring<T, V, 2 * PER, NT>::BYTES + (G < NT ? NT / std::max(G, 32) * 2 * a.tile * 4 : 0);
-    const cudaError_t e = allow_smem(kernel, smem);
+    static int allowed[64] = {};
+    const cudaError_t e = allow_smem(kernel, smem, allowed);
     if (e != cudaSuccess) return e;
     kernel<<<dim3(static_cast<unsigned>(plan.chunks), plan.tiles), NT, smem, stream>>>(a);
     return cudaGetLastError();

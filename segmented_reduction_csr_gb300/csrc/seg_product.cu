@@ -1842,35 +1842,83 @@ __global__ void __launch_bounds__(256) add_parts_kernel(const __grid_constant__ 
 int64_t ceil_to(int64_t n, int64_t d) { return (n + d - 1) / d; }
 
 // ---------------------------------------------------------------------------
-// Rows of any alignment to rows of whole 16-byte units: `lanes` threads a
-// row, each 16 bytes of it at a time.  What a tile's loader warps did with such
-// rows was bound by the loads in flight that the L1 beside 200 KB of stages
-// tracks, for every tile again.
+// Rows of any alignment to rows of whole 16-byte units, one of those per thread
+// at a time, several on their way.  What a tile's loader warps did with such rows
+// was bound by the loads in flight that the L1 beside 200 KB of stages tracks,
+// for every tile again.
+
+// Division by a number that is known at the launch, by a product (Granlund and
+// Montgomery, 1994), for dividends below 2^31.
+struct Divisor {
+    uint32_t d, mul, shift;
+    explicit Divisor(uint32_t by = 1) : d(by), shift(0) {
+        while ((uint64_t(1) << shift) < d) ++shift;
+        mul = static_cast<uint32_t>((uint64_t(1) << 32) * ((uint64_t(1) << shift) - d) / d + 1);
+    }
+    __device__ __forceinline__ uint32_t quotient(uint32_t n) const { return (__umulhi(n, mul) + n) >> shift; }
+};
 
 struct PackArgs {
     const void* src;
     unsigned char* dst;
-    int64_t ld, stride, rows, total, cols, row_bytes;   // elements; rows of a matrix and of all; bytes of a packed row
-    int lanes;
+    int64_t ld, stride, rows, cols, units;   // elements; rows of a matrix; columns of a packed row; 16-byte units of all
+    int row_units;      // of a packed row
+    int halves;         // 2: each row is two rows of `cols`, one after the other, that are packed as rows of their own
+    int large;          // more units or rows than a Divisor divides
+    Divisor by_row, by_mat;
 };
 
+// The 8 16-bit values from p on, all of them in the row: words where they lie on
+// a word's border, else three words between two values.
+__device__ __forceinline__ uint4 load_8(const uint16_t* p) {
+    uint32_t w[4];
+    if ((reinterpret_cast<uintptr_t>(p) & 3) == 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t*>(p) + i);
+    } else {
+        const uint32_t a = __ldg(p), e = __ldg(p + 7);
+        uint32_t m[3];
+#pragma unroll
+        for (int i = 0; i < 3; ++i) m[i] = __ldg(reinterpret_cast<const uint32_t*>(p + 1) + i);
+        w[0] = a | m[0] << 16;
+        w[1] = __funnelshift_l(m[0], m[1], 16);
+        w[2] = __funnelshift_l(m[1], m[2], 16);
+        w[3] = m[2] >> 16 | e << 16;
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// (64 x 520 rows of 666 float16, 44 MB: a warp to a row and value by value 19 us, now XX.)
 template <class T>
 __global__ void __launch_bounds__(256) pack_kernel(const __grid_constant__ PackArgs a) {
-    constexpr int V = 16 / sizeof(T);
-    const int lane = threadIdx.x % a.lanes;
-    const int64_t step = int64_t(gridDim.x) * 256 / a.lanes;
-    for (int64_t r = (int64_t(blockIdx.x) * 256 + threadIdx.x) / a.lanes; r < a.total; r += step) {
-        const int64_t mat = a.total == a.rows ? 0 : r / a.rows;
-        const T* src = static_cast<const T*>(a.src) + mat * a.stride + (r - mat * a.rows) * a.ld;
-        for (int64_t c = int64_t(lane) * V; c < a.cols; c += a.lanes * V) {
-            union {
-                T v[V];
-                uint4 u;
-            } x;
+    constexpr int V = 16 / sizeof(T), AHEAD = 4;
+    const int64_t step = int64_t(gridDim.x) * 256;
+    for (int64_t u0 = int64_t(blockIdx.x) * 256 + threadIdx.x; u0 < a.units; u0 += AHEAD * step) {
+        union {
+            T v[V];
+            uint4 u;
+        } x[AHEAD];
 #pragma unroll
-            for (int i = 0; i < V; ++i) x.v[i] = c + i < a.cols ? __ldg(src + c + i) : T(0);
-            *reinterpret_cast<uint4*>(a.dst + r * a.row_bytes + c * static_cast<int64_t>(sizeof(T))) = x.u;
+        for (int k = 0; k < AHEAD; ++k) {
+            const int64_t u = u0 + k * step;
+            if (u >= a.units) break;
+            int64_t row, mat;       // the packed row, its matrix
+            if (a.large) row = u / a.row_units, mat = row / (a.rows * a.halves);
+            else row = a.by_row.quotient(static_cast<uint32_t>(u)), mat = a.by_mat.quotient(static_cast<uint32_t>(row));
+            const int64_t c = (u - row * a.row_units) * V, r = (a.halves == 2 ? row >> 1 : row) - mat * a.rows;
+            const T* src = static_cast<const T*>(a.src) + mat * a.stride + r * a.ld + (a.halves == 2 && (row & 1) ? a.cols : 0) + c;
+            bool whole = false;
+            if constexpr (sizeof(T) == 2) {
+                whole = c + V <= a.cols;
+                if (whole) x[k].u = load_8(src);
+            }
+            if (!whole)
+#pragma unroll
+                for (int v = 0; v < V; ++v) x[k].v[v] = c + v < a.cols ? __ldg(src + v) : T(0);
         }
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k)
+            if (u0 + k * step < a.units) reinterpret_cast<uint4*>(a.dst)[u0 + k * step] = x[k].u;
     }
 }
 
@@ -2242,22 +2290,27 @@ bool lora_by_rows(const ProductParams& p) {
 
 namespace {
 
-// row_bytes: from one packed row to the next, 0: as they need.
+// halves 2: the two halves of each row of the matrices become rows of their own.
 cudaError_t launch_pack(const void* src, int64_t ld, int64_t stride, const MatShape& m, int size, void* dst, int sms, cudaStream_t stream,
-                        int64_t row_bytes = 0) {
+                        int halves = 1) {
     PackArgs a{};
     a.src = src;
     a.dst = static_cast<unsigned char*>(dst);
     a.ld = ld;
     a.stride = stride;
     a.rows = m.rows;
-    a.total = m.rows * m.mats;
-    a.cols = m.cols;
-    const int64_t own_bytes = packed_row(m.cols, size == 4 ? PT_F32 : PT_F16);
-    a.row_bytes = row_bytes > 0 ? row_bytes : own_bytes;
-    a.lanes = 4;
-    while (a.lanes < 32 && a.lanes * 16 < own_bytes) a.lanes *= 2;
-    const int64_t blocks = std::min<int64_t>(ceil_to(a.total * a.lanes, 256), int64_t(sms) * 16);
+    a.cols = m.cols / halves;
+    a.halves = halves;
+    a.row_units = static_cast<int>(packed_row(a.cols, size == 4 ? PT_F32 : PT_F16) / 16);
+    const int64_t rows = m.rows * m.mats * halves;
+    a.units = rows * a.row_units;
+    if (a.units == 0) return cudaSuccess;
+    a.large = a.units > INT32_MAX;
+    if (!a.large) {
+        a.by_row = Divisor(static_cast<uint32_t>(a.row_units));
+        a.by_mat = Divisor(static_cast<uint32_t>(m.rows * halves));
+    }
+    const int64_t blocks = std::min<int64_t>(ceil_to(a.units, 4 * 256), int64_t(sms) * 32);
     if (size == 4) pack_kernel<uint32_t><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(a);
     else pack_kernel<uint16_t><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(a);
     return cudaGetLastError();
@@ -2303,20 +2356,12 @@ cudaError_t launch_product(int mode, const ProductParams& given, const ProductPl
     }
     int64_t half_w = p.trans ? p.N / 2 * p.ldw : p.N / 2;
     if (plan.pack_w) {
-        MatShape m = w_shape(mode, p);
-        int64_t row = packed_row(m.cols, p.type);
-        cudaError_t e = cudaSuccess;
-        if (halves_apart(mode, p)) {
-            m.cols /= 2;
-            half_w = packed_row(m.cols, p.type) / size;
-            row = 2 * half_w * size;
-            for (int h = 0; e == cudaSuccess && h < 2; ++h)
-                e = launch_pack(static_cast<const unsigned char*>(p.w) + h * m.cols * size, p.ldw, p.stride_w, m, size, packed + h * half_w * size, p.sms, stream, row);
-        } else {
-            e = launch_pack(p.w, p.ldw, p.stride_w, m, size, packed, p.sms, stream);
-            if (mode == PRODUCT_GATED) half_w = p.N / 2 * (row / size);
-        }
+        const MatShape m = w_shape(mode, p);
+        const int halves = halves_apart(mode, p) ? 2 : 1;
+        const int64_t row = halves * packed_row(m.cols / halves, p.type);
+        const cudaError_t e = launch_pack(p.w, p.ldw, p.stride_w, m, size, packed, p.sms, stream, halves);
         if (e != cudaSuccess) return e;
+        half_w = p.trans ? p.N / 2 * (row / size) : row / 2 / size;
         p.w = packed;
         p.ldw = row / size;
         p.stride_w = m.rows * p.ldw;
