@@ -5,8 +5,8 @@
 namespace segred {
 
 // s(x) = 1 / (1 + exp(-x)) and s(-x) = 1 - s(x), from exp(-|x|) so that neither
-// overflows nor cancels.  FAST (where results are rounded to 16 bits): the special
-// function unit's exp2 and division, off by 2 + 1.2 |x| units of 2^-23.
+// overflows nor cancels.  FAST: the special function unit's exp2 and division,
+// off by 2 + 1.2 |x| units of 2^-23.
 template <bool FAST>
 __device__ __forceinline__ void logistic(float x, float& s, float& other) {
     const float e = FAST ? __expf(-fabsf(x)) : expf(-fabsf(x));

@@ -100,13 +100,13 @@ struct Ring {
     static constexpr int STAGE = PL * (A_PLANE + B_PLANE);
     // (the loaders' plain loads are tracked in the L1 that shared memory leaves)
     static constexpr bool GATED = MODE == PRODUCT_GATED;
-    static constexpr int ALL_STAGES = std::min(8, (PL == 3 ? (GATED ? 212992 : 221184) : TENSOR ? 200704 : 98304) / STAGE);
+    static constexpr int ALL_STAGES = std::min(8, (PL == 3 ? (GATED ? 204800 : 221184) : TENSOR ? 200704 : 98304) / STAGE);
     static constexpr int STAGES = ALL_STAGES - (LOW ? 1 : 0);
     static constexpr bool ROW3 = PL == 3 && NT == 64;            // a part of A times several parts of B at once
     static constexpr int ACC = PL == 1 ? NT : 256;               // tensor-memory columns of one accumulator
     static constexpr int BARS = 3 * STAGES + 7 + LOW_TILES;
     // the drain warps' staging; PL == 3 keeps it (adapters alone need it there) in the space of the offsets
-    static constexpr int STAGING = PL == 1 ? 2048 : 1024;
+    static constexpr int STAGING = PL == 1 || GATED ? 2048 : 1024;
     static constexpr int STAGED = PL == 1 || GATED ? EPW * STAGING : 0;
     static constexpr int NEAR = 2 * (NEAR_SEGMENTS + 1) * 4;
     static_assert(NEAR >= EPW * 1024, "room for that staging");
@@ -465,14 +465,18 @@ __device__ __forceinline__ void store_any(void* out, int type, int64_t at, int64
     else store_rows(static_cast<uint16_t*>(out) + at, step, v, n, [type](float x) { return static_cast<uint16_t>(narrow_pair(x, 0.0f, type)); });
 }
 
-// g = act(g) * u, with the kind of activation outside of the loop.
-template <bool FAST, int W>
+// g = act(g) * u, with the kind of activation outside of the loop, by the special
+// function unit for float32 too: off by 2 + 1.2 |g| units of 2^-23, where the
+// products are by up to 2^-20 of their terms' sizes, and the drain warps' time is
+// what bounds a float32 tile (expf and a division: 1,000,000 x 64 times 64 x 64
+// twice 262 us, so 166).
+template <int W>
 __device__ __forceinline__ void gate(int kind, float (&g)[W], const float (&u)[W]) {
     auto all = [&](auto k) {
 #pragma unroll
         for (int i = 0; i < W; ++i) {
             float slope;
-            g[i] = activate<FAST, false>(k(), g[i], slope) * u[i];
+            g[i] = activate<true, false>(k(), g[i], slope) * u[i];
         }
     };
     if (kind == ACT_SILU) all([] { return ACT_SILU; });
@@ -486,8 +490,10 @@ __device__ __forceinline__ void gate(int kind, float (&g)[W], const float (&u)[W
 __device__ __forceinline__ void bar_pair(int quarter, int group) { asm volatile("bar.sync %0, 64;" ::"r"(3 + group * 2 + (quarter & 1)) : "memory"); }
 
 // From v's two halves (`low` and `high` name the registers): this warp's half
-// of the rows of both projections, in g and u.
-template <int W, class Low, class High>
+// of the rows of both projections, in g and u.  TURNS: the caller takes two
+// places of the staging in turns, so that the barrier before the next values are
+// read is enough.
+template <int W, bool TURNS, class Low, class High>
 __device__ __forceinline__ void exchange(const float (&v)[W], float (&g)[W / 2], float (&u)[W / 2], Low low, High high, int lane, int quarter,
                                          int group, unsigned char* own, int staging) {
     constexpr int H = W / 2;
@@ -510,18 +516,18 @@ __device__ __forceinline__ void exchange(const float (&v)[W], float (&g)[W / 2],
             u[i + k] = second ? mine : got[k];
         }
     }
-    bar_pair(quarter, group);      // the staging may be written again
+    if (!TURNS) bar_pair(quarter, group);      // the staging may be written again
 }
 
 // W rows from row0 on, n of which there are, of this warp's lanes: register i holds row i.
-template <bool FAST, int W>
+template <bool TURNS, int W>
 __device__ __forceinline__ void gate_rows(const KernelArgs& a, const float (&v)[W], int64_t row0, int n, int64_t m, int lanes, int lane,
                                           int quarter, int group, unsigned char* own, int staging) {
     const ProductParams& p = a.p;
     if (p.pre && lane < lanes) store_any(p.pre, p.pre_type, row0 * p.ldp + (quarter >> 1) * a.cols_m + m + lane, p.ldp, v, n);
     float g[W / 2], u[W / 2];
-    exchange<W>(v, g, u, [](int i) { return i; }, [](int i) { return W / 2 + i; }, lane, quarter, group, own, staging);
-    gate<FAST, W / 2>(p.activation, g, u);
+    exchange<W, TURNS>(v, g, u, [](int i) { return i; }, [](int i) { return W / 2 + i; }, lane, quarter, group, own, staging);
+    gate<W / 2>(p.activation, g, u);
     const int first = (quarter >> 1) * (W / 2);
     if (lane < lanes) store_any(p.out, p.out_type, (row0 + first) * p.ldo + m + lane, p.ldo, g, n - first);
 }
@@ -560,8 +566,8 @@ __device__ __forceinline__ void gate_blocks(const KernelArgs& a, uint32_t from, 
     }
     // registers 16 h + 4 k + 2 e + b of rows 8 k + ..: k = 0, 1 are the first 16 rows
     float g[16], u[16];
-    exchange<32>(v, g, u, [](int i) { return (i & 7) + 2 * (i & 8); }, [](int i) { return (i & 7) + 2 * (i & 8) + 8; }, lane, quarter, group, own, staging);
-    gate<true, 16>(p.activation, g, u);
+    exchange<32, false>(v, g, u, [](int i) { return (i & 7) + 2 * (i & 8); }, [](int i) { return (i & 7) + 2 * (i & 8) + 8; }, lane, quarter, group, own, staging);
+    gate<16>(p.activation, g, u);
     uint32_t two[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) two[i] = narrow_pair(g[2 * i], g[2 * i + 1], p.out_type);
@@ -585,19 +591,20 @@ __device__ __forceinline__ void gate_blocks(const KernelArgs& a, uint32_t from, 
 template <class R, int NT, int PL, int W>
 __device__ __forceinline__ void load_sums(uint32_t from, float (&v)[W]) {
     if constexpr (PL > 1) {
-        float lo[W];
+        // (the small sums first)
+        float mid[W], hi[W];
         tmem_load(from + NT, v);
-        if constexpr (R::ROW3) tmem_load(from + 2 * NT, lo);
+        if constexpr (R::ROW3) tmem_load(from + 2 * NT, mid);
+        tmem_load(from, hi);
         tmem_wait(v);
         if constexpr (R::ROW3) {
-            tmem_wait(lo);
+            tmem_wait(mid);
 #pragma unroll
-            for (int j = 0; j < W; ++j) v[j] += lo[j];
+            for (int j = 0; j < W; ++j) v[j] += mid[j];
         }
-        tmem_load(from, lo);
-        tmem_wait(lo);
+        tmem_wait(hi);
 #pragma unroll
-        for (int j = 0; j < W; ++j) v[j] += lo[j];
+        for (int j = 0; j < W; ++j) v[j] += hi[j];
     } else {
         tmem_load(from, v);
         tmem_wait(v);
@@ -1544,7 +1551,8 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                     for (int c = group * W; c < n_left; c += ROWS) {
                         float v[W];
                         load_sums<R, NT, PL, W>(from + c, v);
-                        gate_rows<PL == 1, W>(a, v, t.row0 + c, n_left - c, m, lanes, lane, quarter, group, own_staging, R::STAGING);
+                        gate_rows<PL != 1, W>(a, v, t.row0 + c, n_left - c, m, lanes, lane, quarter, group,
+                                              own_staging + (PL > 1 ? (c / ROWS & 1) * (R::STAGING / 2) : 0), R::STAGING);
                     }
                 }
                 if (summed) {
@@ -1737,7 +1745,7 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                     if (p.pre)
                         for (int h = 0; h < 2; ++h)
                             store_any(p.pre, p.pre_type, (int64_t(t.row0) + c) * p.ldp + h * a.cols_m + m + lane, p.ldp, v[h], n);
-                    gate<PL == 1, W>(p.activation, v[0], v[1]);
+                    gate<W>(p.activation, v[0], v[1]);
                     store_any(p.out, p.out_type, (int64_t(t.row0) + c) * p.ldo + m + lane, p.ldo, v[0], n);
                 }
             } else {
@@ -1888,7 +1896,7 @@ __device__ __forceinline__ uint4 load_8(const uint16_t* p) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// (64 x 520 rows of 666 float16, 44 MB: a warp to a row and value by value 19 us, now XX.)
+// (64 x 520 rows of 666 float16, 44 MB: a warp to a row and value by value 19 us, now 18 and both projections of it 30, now 18.)
 template <class T>
 __global__ void __launch_bounds__(256) pack_kernel(const __grid_constant__ PackArgs a) {
     constexpr int V = 16 / sizeof(T), AHEAD = 4;
