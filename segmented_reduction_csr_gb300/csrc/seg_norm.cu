@@ -165,8 +165,14 @@ __device__ __forceinline__ int64_t offset_at(const NormParams& p, int64_t s) {
 struct Run {
     int64_t s = -1, begin = 0, end = 0;
 };
-__device__ __forceinline__ Run run_of(const NormParams& p, int64_t r) {
+// before: the segment of an earlier row, or -1.  It is mostly the next one: two
+// loads at once where the search is a chain of them.
+__device__ __forceinline__ Run run_of(const NormParams& p, int64_t r, int64_t before = -1) {
     if (!p.offsets) return {0, 0, p.R};
+    if (before >= 0 && before + 2 <= p.S) {
+        const int64_t begin = offset_at(p, before + 1), end = offset_at(p, before + 2);
+        if (begin <= r && r < end) return {before + 1, begin, end};
+    }
     int64_t lo = -1, hi = p.S + 1;      // the last offset at or before r; the first one after it
     while (hi - lo > 1) {
         const int64_t mid = (lo + hi) >> 1;
@@ -215,7 +221,7 @@ __device__ __forceinline__ void group_sum(float (&v)[N], float* red, int& turn) 
 }
 
 // Blocks of an SM, by the values that a thread holds of rows and weights.
-constexpr int resident(int threads, int values) { return threads == 1024 ? 1 : values > 48 ? 2 : values > 24 ? 3 : 4; }
+constexpr int resident(int threads, int values) { return threads > 256 ? 1 : values > 48 ? 2 : values > 24 ? 3 : 4; }
 // Values of a row that a thread has, and rows at a time: the forward pass takes
 // two, whose sums' chains overlap; the backward pass has sums to keep as well.
 constexpr int ROW_VALUES = 16, ROWS = 2;
@@ -225,7 +231,7 @@ template <class T, int V, int G, int PER, int U, int NT>
 __global__ void __launch_bounds__(NT, resident(NT, Pack<T, V>::H * 2 * PER * (U + 2))) norm_kernel(const __grid_constant__ NormParams p, int64_t chunk) {
     using R = Ring<T, V, PER * U, NT>;
     constexpr int GROUPS = NT / G, STEP = G * V, H = Pack<T, V>::H;
-    constexpr bool KEEP = NT == 256 && V * PER <= ROW_VALUES;      // a run's weights stay in registers
+    constexpr bool KEEP = NT <= 512 && V * PER <= ROW_VALUES;      // a run's weights stay in registers
     __shared__ float red[2 * NT / 32 * U];
     extern __shared__ __align__(16) unsigned char ring_memory[];
     R ring(ring_memory);
@@ -252,7 +258,7 @@ __global__ void __launch_bounds__(NT, resident(NT, Pack<T, V>::H * 2 * PER * (U 
     if (R::ASYNC)
         for (int d = 0; d < R::D - 1; ++d) fetch(d * GROUPS * U + g);
     int turn = 0, run_end = 0;      // of the chunk's rows
-    int64_t at = 0;
+    int64_t at = 0, segment = -1;
     bool used = false;
     float2 kept_w[KEEP ? PER : 1][H], kept_b[KEEP ? PER : 1][H];
     auto read_weights = [&](int j, float2 (&w)[H], float2 (&b)[H]) {
@@ -262,7 +268,8 @@ __global__ void __launch_bounds__(NT, resident(NT, Pack<T, V>::H * 2 * PER * (U 
         if (p.bias) load_weights<T, V>(p.bias, wide, at + j * STEP, b);
     };
     auto find_run = [&](int i) {
-        const Run run = run_of(p, c0 + i);
+        const Run run = run_of(p, c0 + i, segment);
+        segment = run.s;
         run_end = static_cast<int>(min(run.end - c0, int64_t(n)));
         used = run.s >= 0;
         at = run.s * p.F + t * V;
@@ -367,7 +374,7 @@ __global__ void __launch_bounds__(256) norm_long_kernel(const __grid_constant__ 
     Run run;
     for (int64_t r = blockIdx.x; r < p.R; r += gridDim.x) {
         const T* x = static_cast<const T*>(p.x) + r * p.ldx;
-        if (r >= run.end) run = run_of(p, r);
+        if (r >= run.end) run = run_of(p, r, run.s);
         float sum = 0.0f, sq = 0.0f;
         for (int64_t c = threadIdx.x; c < p.F; c += 256) sum += to_float<T>(x[c]);
         const float mean = block_sum(sum, red) * inv;
@@ -408,7 +415,7 @@ __global__ void __launch_bounds__(256) norm_sums_kernel(const __grid_constant__ 
     const bool wide = p.weight_type == PT_F32;
     Run run;
     for (int64_t r = blockIdx.x; r < p.R; r += gridDim.x) {
-        if (r >= run.end) run = run_of(p, r);
+        if (r >= run.end) run = run_of(p, r, run.s);
         if (run.s < 0) continue;
         const T* x = static_cast<const T*>(p.x) + r * p.ldx;
         const T* dy = static_cast<const T*>(p.dy) + r * p.ldy;
@@ -438,7 +445,7 @@ template <class T, int V, int G, int PER, int U, int NT>
 __global__ void __launch_bounds__(NT, resident(NT, Pack<T, V>::H * 2 * PER * (2 * U + 3))) norm_grad_kernel(const __grid_constant__ GradArgs a) {
     using R = Ring<T, V, 2 * PER * U, NT>;
     constexpr int GROUPS = NT / G, STEP = G * V, WINDOW = GROUPS * U, H = Pack<T, V>::H;
-    constexpr bool KEEP = NT == 256;      // a run's weights stay in registers; a large block has none to spare and reads them again
+    constexpr bool KEEP = NT <= 512;      // a run's weights stay in registers; a large block has none to spare and reads them again
     __shared__ float red[2 * NT / 32 * 2 * U];
     extern __shared__ __align__(16) unsigned char ring_memory[];
     float* const shared_sums = reinterpret_cast<float*>(ring_memory + R::BYTES);      // [groups of at least a warp][2][tile]
@@ -700,7 +707,7 @@ __global__ void __launch_bounds__(NT, resident(NT, Pack<T, V>::H * 2 * PER * (2 
             }
             from = run_end;
             if (from >= n) break;
-            run = run_of(p, c0 + from);
+            run = run_of(p, c0 + from, run.s);
             begin();
             if (from >= end) break;
         }
@@ -783,7 +790,7 @@ cudaError_t allow_smem(K* kernel, int bytes, int (&allowed)[64]) {
 
 template <class T, int V, int G, int PER>
 cudaError_t launch_rows(const NormParams& p, const NormPlan& plan, cudaStream_t stream) {
-    constexpr int NT = G > 256 ? G : 256, U = NT == 256 ? ROWS : 1, smem = Ring<T, V, PER * U, NT>::BYTES;
+    constexpr int NT = G > 256 ? G : 256, U = NT <= 512 ? ROWS : 1, smem = Ring<T, V, PER * U, NT>::BYTES;
     auto* kernel = norm_kernel<T, V, G, PER, U, NT>;
     static int allowed[64] = {};
     const cudaError_t e = allow_smem(kernel, smem, allowed);
@@ -822,6 +829,7 @@ cudaError_t with_shape(const NormPlan& plan, F f) {
     SEG_NORM_SHAPE(V, 128, MOST);
     SEG_NORM_SHAPE(V, 256, 1);
     SEG_NORM_SHAPE(V, 256, MOST);
+    SEG_NORM_SHAPE(V, 512, MOST);
     SEG_NORM_SHAPE(V, 1024, MOST);
     SEG_NORM_SHAPE(1, 32, 4);
     SEG_NORM_SHAPE(1, 32, 8);
@@ -865,10 +873,10 @@ NormPlan plan_norm(bool grad, const NormParams& p) {
     // as few threads for a row as hold it; where there are few rows, a block's, so
     // that each is over sooner
     if (p.R <= p.sms && loads > 32) {
-        d.group = loads <= 256 * most ? 256 : 1024;
+        d.group = loads <= 256 * most ? 256 : vec && loads <= 512 * most ? 512 : 1024;
     } else {
         d.group = vec ? 8 : 32;
-        while (d.group < 1024 && int64_t(d.group) * most < loads) d.group *= vec && d.group < 256 ? 2 : vec ? 4 : d.group == 32 ? 8 : 4;
+        while (d.group < 1024 && int64_t(d.group) * most < loads) d.group *= vec ? 2 : d.group == 32 ? 8 : 4;
     }
     d.threads = std::max(d.group, 256);
     int64_t per = ceil_to(loads, d.group);
@@ -884,7 +892,7 @@ NormPlan plan_norm(bool grad, const NormParams& p) {
             d.per = 0;
         }
     }
-    const int rows = !grad && d.threads == 256 ? ROWS : 1;
+    const int rows = !grad && d.threads <= 512 ? ROWS : 1;
     const int64_t window = d.per == 0 ? 1 : d.threads / d.group * rows;
     const int64_t most_blocks = d.per == 0 ? int64_t(p.sms) * 8
                                            : std::max<int64_t>(p.sms * resident(d.threads, d.per * std::max(d.vec, 2) * (grad ? 5 : rows + 2)) / d.tiles, 1);
