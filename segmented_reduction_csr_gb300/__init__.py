@@ -631,8 +631,8 @@ def _check_rows(name, t, offsets):
 
 def _row_stride(name, t):
     """Elements from one row to the next of a tensor whose rows are contiguous."""
-    rows, cols = t.shape[-2:]
-    step, one = t.stride()[-2:]
+    shape, strides = t.shape, t.stride()
+    rows, cols, step, one = shape[-2], shape[-1], strides[-2], strides[-1]
     if (one != 1 and cols > 1) or (rows > 1 and step < cols):
         raise ValueError(f"{name} must have contiguous rows that do not overlap")
     return step if rows > 1 else cols or 1
@@ -929,10 +929,10 @@ def seg_gated_grad(x, w, pre, dy, offsets, activation: str = "silu", transpose_w
     products with it, ``seg_matmul`` and ``seg_matmul_grad_w``.  Arguments,
     ``stream`` and graphs as for ``seg_gated``; not synchronised."""
     torch = _torch()
-    _check_rows("x", x, offsets)
-    code, s, (r, _) = _product_code(x), offsets.shape[0] - 1, x.shape
+    ldx = _check_rows("x", x, offsets)
+    code, s, (r, k) = _product_code(x), offsets.shape[0] - 1, x.shape
     act = _activation_code(activation)
-    n, _ = _gated_weights(x, w, s, transpose_w)
+    n, ldw = _gated_weights(x, w, s, transpose_w)
     ptype, pcode = _pre_type(pre, x)
     _same("pre", pre, x, (r, 2 * n), ptype)
     _same("dy", dy, x, (r, n))
@@ -941,19 +941,26 @@ def seg_gated_grad(x, w, pre, dy, offsets, activation: str = "silu", transpose_w
         raise TypeError(f"dw_dtype must be {x.dtype} or torch.float32, not {dw_dtype}")
     if not (want_dx or want_dw):
         return None, None
-    # (an even number of 16-byte units a row, whatever N is, so that the products read it as it is)
-    ldd = -(-2 * n // 8) * 8
+    # (whole 16-byte units a row, whatever N is, so that the products read it as it is)
+    ldd = -(-2 * n // 8) * 8 or 1
+    lib, off, odt, dev = load_library(), offsets.data_ptr(), _offset_code(offsets), x.device
     dpre, _ = _rows_out("dpre", None, x, (r, ldd), stream)
-    dpre = dpre[:, :2 * n]
-    _enqueue("seg_gated_grad", x.device, stream, load_library().seg_gated_grad, pre.data_ptr() or None, pcode, r, n, ldp,
-             dy.data_ptr() or None, code, ldy, act, dpre.data_ptr() or None, max(ldd, 1))
-    if stream is not None:
-        _in_use(stream, pre, dy, dpre)
-    dx = seg_matmul(dpre, w, offsets, transpose_w=not transpose_w, stream=stream) if want_dx else None
-    dw = None
+    at, px, pw = dpre.data_ptr() or None, x.data_ptr() or None, w.data_ptr() or None
+    _enqueue("seg_gated_grad", dev, stream, lib.seg_gated_grad, pre.data_ptr() or None, pcode, r, n, ldp, dy.data_ptr() or None, code, ldy,
+             act, at, ldd)
+    dx = dw = None
+    if want_dx:
+        dx, lddx = _rows_out("dx", None, x, (r, k), stream)
+        _enqueue("seg_matmul", dev, stream, lib.seg_matmul, at, code, r, 2 * n, ldd, pw, k, ldw, w.stride(0) if s > 1 else 0,
+                 0 if transpose_w else 1, off, odt, s, dx.data_ptr() or None, lddx)
     if want_dw:
-        a, b = (dpre, x) if transpose_w else (x, dpre)
-        dw = seg_matmul_grad_w(a, b, offsets, out_dtype=dw_dtype, stream=stream)
+        dw_dtype = x.dtype if dw_dtype is None else dw_dtype
+        dw = torch.empty(w.shape, dtype=dw_dtype, device=dev) if stream is None else _fresh(w.shape, dw_dtype, dev, stream)
+        first, second = ((at, 2 * n, ldd), (px, k, ldx)) if transpose_w else ((px, k, ldx), (at, 2 * n, ldd))
+        _enqueue("seg_matmul_grad_w", dev, stream, lib.seg_matmul_grad_w, first[0], code, r, first[1], first[2], *second, off, odt, s,
+                 dw.data_ptr() or None, code if dw_dtype == x.dtype else SEG_F32)
+    if stream is not None:
+        _in_use(stream, x, w, pre, dy, offsets, dpre, dx, dw)
     return dx, dw
 
 
@@ -1045,13 +1052,15 @@ def seg_layer_norm(x, weight=None, bias=None, offsets=None, eps: float = 1e-5, w
     mean = rstd = None
     if with_stats:
         torch = _torch()
-        stats = torch.empty((2, r), dtype=torch.float32, device=x.device) if stream is None else _fresh((2, r), torch.float32, x.device, stream)
-        mean, rstd = stats[0], stats[1]
+        if stream is None:
+            mean, rstd = torch.empty(r, dtype=torch.float32, device=x.device), torch.empty(r, dtype=torch.float32, device=x.device)
+        else:
+            mean, rstd = _fresh((r,), torch.float32, x.device, stream), _fresh((r,), torch.float32, x.device, stream)
     _enqueue("seg_layer_norm", x.device, stream, load_library().seg_layer_norm, x.data_ptr() or None, code, r, f, ldx,
              _ptr(weight) or None, _ptr(bias) or None, wcode, _ptr(offsets), odt, s, eps, out.data_ptr() or None, ldo, (mean.data_ptr() or None) if with_stats else None,
              (rstd.data_ptr() or None) if with_stats else None)
     if stream is not None:
-        _in_use(stream, x, weight, bias, offsets, out, mean)
+        _in_use(stream, x, weight, bias, offsets, out, mean, rstd)
     return (out, mean, rstd) if with_stats else out
 
 
