@@ -38,18 +38,70 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(f
 // took 28 instructions a value, 32,768 x 2,048 bfloat16 79 us).
 __device__ __forceinline__ float2 pair(float x) { return make_float2(x, x); }
 
-// V values that are loaded and stored together: 16 bytes, or one value (the
-// second one of a pair is 0 then).
-template <class T, int V> struct Pack {
-    static constexpr int H = V > 1 ? V / 2 : 1;
-    using Raw = typename std::conditional<V * sizeof(T) == 16, uint4, T>::type;
-    Raw raw;
-    __device__ __forceinline__ void load(const T* p) { raw = __ldg(reinterpret_cast<const Raw*>(p)); }
-    __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<Raw*>(p) = raw; }
-    __device__ __forceinline__ void widen(float2 (&f)[H]) const {
-        if constexpr (V == 1) {
-            f[0] = make_float2(to_float<T>(raw), 0.0f);
+// The 16 bytes of values that are loaded and stored together.  A: they lie on a
+// border of 16 bytes, and rows are whole numbers of them; else a row's last ones
+// may be there in part, the others count as 0, and 16-bit values, which may lie
+// between two words, go by words and by single values.
+template <class T, bool A> struct Pack {
+    static constexpr int V = 16 / sizeof(T), H = V / 2;
+    uint4 raw;
+    // n: values that there are, V or more of them if all
+    __device__ __forceinline__ void load(const T* p, int n) {
+        if constexpr (A) {
+            raw = __ldg(reinterpret_cast<const uint4*>(p));
         } else if constexpr (sizeof(T) == 4) {
+            const uint32_t* w = reinterpret_cast<const uint32_t*>(p);
+            raw = make_uint4(__ldg(w), n > 1 ? __ldg(w + 1) : 0, n > 2 ? __ldg(w + 2) : 0, n > 3 ? __ldg(w + 3) : 0);
+        } else {
+            const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
+            uint32_t w[4] = {0, 0, 0, 0};
+            if (n < V) {
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    if (i < n) w[i / 2] |= static_cast<uint32_t>(__ldg(h + i)) << (i % 2 * 16);
+            } else if ((reinterpret_cast<uintptr_t>(p) & 3) == 0) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t*>(h) + i);
+            } else {
+                const uint32_t first = __ldg(h), last = __ldg(h + 7);
+                uint32_t m[3];
+#pragma unroll
+                for (int i = 0; i < 3; ++i) m[i] = __ldg(reinterpret_cast<const uint32_t*>(h + 1) + i);
+                w[0] = first | m[0] << 16;
+                w[1] = __funnelshift_l(m[0], m[1], 16);
+                w[2] = __funnelshift_l(m[1], m[2], 16);
+                w[3] = m[2] >> 16 | last << 16;
+            }
+            raw = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+    __device__ __forceinline__ void store(T* p, int n) const {
+        const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+        if constexpr (A) {
+            *reinterpret_cast<uint4*>(p) = raw;
+        } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < n) reinterpret_cast<uint32_t*>(p)[i] = w[i];
+        } else {
+            uint16_t* h = reinterpret_cast<uint16_t*>(p);
+            if (n < V) {
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    if (i < n) h[i] = static_cast<uint16_t>(w[i / 2] >> (i % 2 * 16));
+            } else if ((reinterpret_cast<uintptr_t>(p) & 3) == 0) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) reinterpret_cast<uint32_t*>(h)[i] = w[i];
+            } else {
+                h[0] = static_cast<uint16_t>(w[0]);
+#pragma unroll
+                for (int i = 0; i < 3; ++i) reinterpret_cast<uint32_t*>(h + 1)[i] = __funnelshift_l(w[i], w[i + 1], 16);
+                h[7] = static_cast<uint16_t>(w[3] >> 16);
+            }
+        }
+    }
+    __device__ __forceinline__ void widen(float2 (&f)[H]) const {
+        if constexpr (sizeof(T) == 4) {
             f[0] = make_float2(__uint_as_float(raw.x), __uint_as_float(raw.y));
             f[1] = make_float2(__uint_as_float(raw.z), __uint_as_float(raw.w));
         } else {
@@ -62,9 +114,7 @@ template <class T, int V> struct Pack {
         }
     }
     __device__ __forceinline__ void narrow(const float2 (&f)[H]) {
-        if constexpr (V == 1) {
-            raw = from_float<T>(f[0].x);
-        } else if constexpr (sizeof(T) == 4) {
+        if constexpr (sizeof(T) == 4) {
             raw = make_uint4(__float_as_uint(f[0].x), __float_as_uint(f[0].y), __float_as_uint(f[1].x), __float_as_uint(f[1].y));
         } else {
             uint32_t w[4];
@@ -80,13 +130,13 @@ template <class T, int V> struct Pack {
 
 // What a thread needs of its next rows, on its way to shared memory while it
 // works on these: a ring of D slots of PER packs for each thread, which copies
-// and reads nothing but its own, so that no barrier is needed.  (Packs of less
-// than 16 bytes, of rows that are not aligned, and rows of which shared memory
-// does not hold two, are loaded when they are needed.)
-template <class T, int V, int PER, int NT>
+// and reads nothing but its own, so that no barrier is needed.  (Rows that are
+// not aligned, or of which shared memory does not hold two, are loaded when they
+// are needed.)
+template <class T, bool A, int PER, int NT>
 struct Ring {
     static constexpr int D = PER == 1 ? 6 : PER <= 4 && NT == 256 ? 4 : PER == 2 ? 4 : PER <= 4 ? 3 : 2;      // fewer bytes of a slot want more of them
-    static constexpr bool ASYNC = V * sizeof(T) == 16 && D * PER * NT * 16 <= 200 * 1024;
+    static constexpr bool ASYNC = A && D * PER * NT * 16 <= 200 * 1024;
     static constexpr int SLOT = PER * NT * 16, BYTES = ASYNC ? D * SLOT : 0;
     uint32_t base, at, to;      // the thread's first slot, the one to read and the one to fetch into
     __device__ __forceinline__ explicit Ring(unsigned char* memory) : base(smem_u32(memory) + threadIdx.x * 16), at(base), to(base) {}
@@ -100,10 +150,10 @@ struct Ring {
     }
     // the slot to read has landed
     __device__ __forceinline__ void wait() const { asm volatile("cp.async.wait_group %0;" ::"n"(D - 2) : "memory"); }
-    __device__ __forceinline__ void get(int j, const T* from, float2 (&f)[Pack<T, V>::H]) const {
-        Pack<T, V> x;
+    __device__ __forceinline__ void get(int j, const T* from, int n, float2 (&f)[Pack<T, A>::H]) const {
+        Pack<T, A> x;
         if constexpr (ASYNC) asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x.raw.x), "=r"(x.raw.y), "=r"(x.raw.z), "=r"(x.raw.w) : "r"(at + j * NT * 16) : "memory");
-        else x.load(from);
+        else x.load(from, n);
         x.widen(f);
     }
     // packs that are never fetched read as zeros
@@ -114,40 +164,39 @@ struct Ring {
     __device__ __forceinline__ void got() { at = at == base + (D - 1) * SLOT ? base : at + SLOT; }
 };
 
-// V neighbouring values of weight_type at element `at`.
-template <class T, int V>
-__device__ __forceinline__ void load_weights(const void* w, bool wide, int64_t at, float2 (&f)[Pack<T, V>::H]) {
+// A pack of values of weight_type at element `at`, n of them.
+template <class T, bool A>
+__device__ __forceinline__ void load_weights(const void* w, bool wide, int64_t at, int n, float2 (&f)[Pack<T, A>::H]) {
     if (!wide) {
-        Pack<T, V> x;
-        x.load(static_cast<const T*>(w) + at);
+        Pack<T, A> x;
+        x.load(static_cast<const T*>(w) + at, n);
         x.widen(f);
         return;
     }
     const float* p = static_cast<const float*>(w) + at;
-    if constexpr (V == 1) {
-        f[0] = make_float2(__ldg(p), 0.0f);
-    } else {
 #pragma unroll
-        for (int i = 0; i < V; i += 4) {
-            const float4 x = __ldg(reinterpret_cast<const float4*>(p + i));
-            f[i / 2] = make_float2(x.x, x.y), f[i / 2 + 1] = make_float2(x.z, x.w);
-        }
+    for (int i = 0; i < Pack<T, A>::H; i += 2) {
+        Pack<float, A> x;
+        float2 y[2] = {};
+        if (A || 2 * i < n) x.load(p + 2 * i, n - 2 * i), x.widen(y);
+        f[i] = y[0], f[i + 1] = y[1];
     }
 }
-template <class T, int V>
-__device__ __forceinline__ void store_weights(void* out, bool wide, int64_t at, const float2 (&f)[Pack<T, V>::H]) {
+template <class T, bool A>
+__device__ __forceinline__ void store_weights(void* out, bool wide, int64_t at, int n, const float2 (&f)[Pack<T, A>::H]) {
     if (!wide) {
-        Pack<T, V> x;
+        Pack<T, A> x;
         x.narrow(f);
-        x.store(static_cast<T*>(out) + at);
+        x.store(static_cast<T*>(out) + at, n);
         return;
     }
     float* p = static_cast<float*>(out) + at;
-    if constexpr (V == 1) {
-        *p = f[0].x;
-    } else {
 #pragma unroll
-        for (int i = 0; i < V; i += 4) *reinterpret_cast<float4*>(p + i) = make_float4(f[i / 2].x, f[i / 2].y, f[i / 2 + 1].x, f[i / 2 + 1].y);
+    for (int i = 0; i < Pack<T, A>::H; i += 2) {
+        Pack<float, A> x;
+        const float2 y[2] = {f[i], f[i + 1]};
+        x.narrow(y);
+        x.store(p + 2 * i, n - 2 * i);
     }
 }
 template <class T>
@@ -227,10 +276,10 @@ constexpr int resident(int threads, int values) { return threads > 256 ? 1 : val
 constexpr int ROW_VALUES = 16, ROWS = 2;
 
 // G threads a row, U rows of a group at a time.
-template <class T, int V, int G, int PER, int U, int NT>
-__global__ void __launch_bounds__(NT, resident(NT, Pack<T, V>::H * 2 * PER * (U + 2))) norm_kernel(const __grid_constant__ NormParams p, int64_t chunk) {
-    using R = Ring<T, V, PER * U, NT>;
-    constexpr int GROUPS = NT / G, STEP = G * V, H = Pack<T, V>::H;
+template <class T, bool A, int G, int PER, int U, int NT>
+__global__ void __launch_bounds__(NT, resident(NT, Pack<T, A>::V * PER * (U + 2))) norm_kernel(const __grid_constant__ NormParams p, int64_t chunk) {
+    using R = Ring<T, A, PER * U, NT>;
+    constexpr int V = Pack<T, A>::V, GROUPS = NT / G, STEP = G * V, H = V / 2;
     constexpr bool KEEP = NT <= 512 && V * PER <= ROW_VALUES;      // a run's weights stay in registers
     __shared__ float red[2 * NT / 32 * U];
     extern __shared__ __align__(16) unsigned char ring_memory[];
@@ -264,8 +313,8 @@ __global__ void __launch_bounds__(NT, resident(NT, Pack<T, V>::H * 2 * PER * (U 
     auto read_weights = [&](int j, float2 (&w)[H], float2 (&b)[H]) {
 #pragma unroll
         for (int k = 0; k < H; ++k) w[k] = pair(1.0f), b[k] = pair(0.0f);
-        if (p.weight) load_weights<T, V>(p.weight, wide, at + j * STEP, w);
-        if (p.bias) load_weights<T, V>(p.bias, wide, at + j * STEP, b);
+        if (p.weight) load_weights<T, A>(p.weight, wide, at + j * STEP, left - j * STEP, w);
+        if (p.bias) load_weights<T, A>(p.bias, wide, at + j * STEP, left - j * STEP, b);
     };
     auto find_run = [&](int i) {
         const Run run = run_of(p, c0 + i, segment);
@@ -290,7 +339,7 @@ __global__ void __launch_bounds__(NT, resident(NT, Pack<T, V>::H * 2 * PER * (U 
 #pragma unroll
             for (int j = 0; j < PER; ++j) {
                 if (in && j * STEP < left) {
-                    ring.get(u * PER + j, px + u * next + j * STEP, f[u][j]);
+                    ring.get(u * PER + j, px + u * next + j * STEP, left - j * STEP, f[u][j]);
 #pragma unroll
                     for (int i = 0; i < H; ++i) all = __fadd2_rn(all, f[u][j][i]);
                 } else {
@@ -317,10 +366,14 @@ __global__ void __launch_bounds__(NT, resident(NT, Pack<T, V>::H * 2 * PER * (U 
 #pragma unroll
                 for (int i = 0; i < H; ++i) {
                     f[u][j][i] = __fadd2_rn(f[u][j][i], pair(-sum[u]));
+                    if constexpr (!A) {
+                        if (2 * i >= left - j * STEP) f[u][j][i].x = 0.0f;
+                        if (2 * i + 1 >= left - j * STEP) f[u][j][i].y = 0.0f;
+                    }
                     all = __ffma2_rn(f[u][j][i], f[u][j][i], all);
                 }
             }
-            sq[u] = V > 1 ? all.x + all.y : all.x;
+            sq[u] = all.x + all.y;
         }
         group_sum<G, NT, U>(sq, red, turn);
 #pragma unroll
@@ -347,9 +400,9 @@ __global__ void __launch_bounds__(NT, resident(NT, Pack<T, V>::H * 2 * PER * (U 
                 }
 #pragma unroll
                 for (int k = 0; k < H; ++k) f[u][j][k] = used ? __ffma2_rn(__fmul2_rn(f[u][j][k], pair(rstd)), w[k], b[k]) : pair(0.0f);
-                Pack<T, V> o;
+                Pack<T, A> o;
                 o.narrow(f[u][j]);
-                o.store(y + j * STEP);
+                o.store(y + j * STEP, left - j * STEP);
             }
         }
     }
@@ -441,10 +494,10 @@ __device__ __forceinline__ void store_weight(void* out, int type, int64_t at, fl
 // A block's windows of U rows of each group follow one another whatever
 // segments they are in; a window in which a run ends is worked on once for each
 // run that has a row in it.
-template <class T, int V, int G, int PER, int U, int NT>
-__global__ void __launch_bounds__(NT, resident(NT, Pack<T, V>::H * 2 * PER * (2 * U + 3))) norm_grad_kernel(const __grid_constant__ GradArgs a) {
-    using R = Ring<T, V, 2 * PER * U, NT>;
-    constexpr int GROUPS = NT / G, STEP = G * V, WINDOW = GROUPS * U, H = Pack<T, V>::H;
+template <class T, bool A, int G, int PER, int U, int NT>
+__global__ void __launch_bounds__(NT, resident(NT, Pack<T, A>::V * PER * (2 * U + 3))) norm_grad_kernel(const __grid_constant__ GradArgs a) {
+    using R = Ring<T, A, 2 * PER * U, NT>;
+    constexpr int V = Pack<T, A>::V, GROUPS = NT / G, STEP = G * V, WINDOW = GROUPS * U, H = V / 2;
     constexpr bool KEEP = NT <= 512;      // a run's weights stay in registers; a large block has none to spare and reads them again
     __shared__ float red[2 * NT / 32 * 2 * U];
     extern __shared__ __align__(16) unsigned char ring_memory[];
@@ -498,7 +551,7 @@ __global__ void __launch_bounds__(NT, resident(NT, Pack<T, V>::H * 2 * PER * (2 
     float2 kept[KEEP ? PER : 1][H], dw[PER][H], db[PER][H];
     auto read_weights = [&](int j, float2 (&w)[H]) {
         if (p.weight && run.s >= 0 && j * STEP < left) {
-            load_weights<T, V>(p.weight, wide, run.s * p.F + col0 + t * V + j * STEP, w);
+            load_weights<T, A>(p.weight, wide, run.s * p.F + col0 + t * V + j * STEP, left - j * STEP, w);
         } else {
 #pragma unroll
             for (int i = 0; i < H; ++i) w[i] = pair(1.0f);
@@ -545,8 +598,8 @@ __global__ void __launch_bounds__(NT, resident(NT, Pack<T, V>::H * 2 * PER * (2 
         float mean[U], rstd[U];
         if (R::ASYNC) ring.wait();
         auto read_values = [&](int u, int j, float2 (&z)[H], float2 (&dy)[H]) {
-            ring.get((u * PER + j) * 2, px + u * nextx + j * STEP, z);
-            ring.get((u * PER + j) * 2 + 1, pd + u * nexty + j * STEP, dy);
+            ring.get((u * PER + j) * 2, px + u * nextx + j * STEP, left - j * STEP, z);
+            ring.get((u * PER + j) * 2 + 1, pd + u * nexty + j * STEP, left - j * STEP, dy);
 #pragma unroll
             for (int i = 0; i < H; ++i) z[i] = __fmul2_rn(__fadd2_rn(z[i], pair(-mean[u])), pair(rstd[u]));
         };
@@ -622,14 +675,14 @@ __global__ void __launch_bounds__(NT, resident(NT, Pack<T, V>::H * 2 * PER * (2 
 #pragma unroll
                     for (int j = 0; j < PER; ++j) {
                         if (!R::ASYNC && j * STEP >= left) continue;
-                        Pack<T, V> o;
+                        Pack<T, A> o;
                         float2 w[H], z[H], dy[H], d[H];
                         weights_of(j, w);
                         values_of(u, j, z, dy);
 #pragma unroll
                         for (int i = 0; i < H; ++i) d[i] = __fmul2_rn(scale, __ffma2_rn(z[i], m2, __ffma2_rn(dy[i], w[i], m1)));
                         o.narrow(d);
-                        if (j * STEP < left) o.store(po + u * nexto + j * STEP);
+                        if (j * STEP < left) o.store(po + u * nexto + j * STEP, left - j * STEP);
                     }
                 }
             };
@@ -639,13 +692,13 @@ __global__ void __launch_bounds__(NT, resident(NT, Pack<T, V>::H * 2 * PER * (2 
             } else if (want_dx) {
                 // rows in no segment
                 const float2 none[H] = {};
-                Pack<T, V> zero;
+                Pack<T, A> zero;
                 zero.narrow(none);
 #pragma unroll
                 for (int u = 0; u < U; ++u)
 #pragma unroll
                     for (int j = 0; j < PER; ++j)
-                        if (in(u) && j * STEP < left) zero.store(po + u * nexto + j * STEP);
+                        if (in(u) && j * STEP < left) zero.store(po + u * nexto + j * STEP, left - j * STEP);
             }
             if (run_end > end && end < n) break;       // the run goes on in the next window
             if (want_dw && run.s >= 0) {
@@ -672,11 +725,11 @@ __global__ void __launch_bounds__(NT, resident(NT, Pack<T, V>::H * 2 * PER * (2 
                         const int c = col0 + t * V + j * STEP;
                         if (j * STEP >= left) continue;
                         if (whole) {
-                            if (p.dweight) store_weights<T, V>(p.dweight, wide, run.s * p.F + c, dw[j]);
-                            if (p.dbias) store_weights<T, V>(p.dbias, wide, run.s * p.F + c, db[j]);
+                            if (p.dweight) store_weights<T, A>(p.dweight, wide, run.s * p.F + c, left - j * STEP, dw[j]);
+                            if (p.dbias) store_weights<T, A>(p.dbias, wide, run.s * p.F + c, left - j * STEP, db[j]);
                         } else {
-                            store_weights<T, V>(slot_sums, true, c, dw[j]);
-                            store_weights<T, V>(slot_sums, true, p.F + c, db[j]);
+                            store_weights<T, A>(slot_sums, true, c, left - j * STEP, dw[j]);
+                            store_weights<T, A>(slot_sums, true, p.F + c, left - j * STEP, db[j]);
                         }
                     }
                 } else {
@@ -788,10 +841,10 @@ cudaError_t allow_smem(K* kernel, int bytes, int (&allowed)[64]) {
     return e;
 }
 
-template <class T, int V, int G, int PER>
+template <class T, bool A, int G, int PER>
 cudaError_t launch_rows(const NormParams& p, const NormPlan& plan, cudaStream_t stream) {
-    constexpr int NT = G > 256 ? G : 256, U = NT <= 512 ? ROWS : 1, smem = Ring<T, V, PER * U, NT>::BYTES;
-    auto* kernel = norm_kernel<T, V, G, PER, U, NT>;
+    constexpr int NT = G > 256 ? G : 256, U = NT <= 512 ? ROWS : 1, smem = Ring<T, A, PER * U, NT>::BYTES;
+    auto* kernel = norm_kernel<T, A, G, PER, U, NT>;
     static int allowed[64] = {};
     const cudaError_t e = allow_smem(kernel, smem, allowed);
     if (e != cudaSuccess) return e;
@@ -799,11 +852,11 @@ cudaError_t launch_rows(const NormParams& p, const NormPlan& plan, cudaStream_t 
     return cudaGetLastError();
 }
 
-template <class T, int V, int G, int PER>
+template <class T, bool A, int G, int PER>
 cudaError_t launch_grad_rows(const GradArgs& a, const NormPlan& plan, cudaStream_t stream) {
     constexpr int NT = G > 256 ? G : 256;
-    auto* kernel = norm_grad_kernel<T, V, G, PER, 1, NT>;
-    const int smem = Ring<T, V, 2 * PER, NT>::BYTES + (G < NT ? NT / std::max(G, 32) * 2 * a.tile * 4 : 0);
+    auto* kernel = norm_grad_kernel<T, A, G, PER, 1, NT>;
+    const int smem = Ring<T, A, 2 * PER, NT>::BYTES + (G < NT ? NT / std::max(G, 32) * 2 * a.tile * 4 : 0);
     static int allowed[64] = {};
     const cudaError_t e = allow_smem(kernel, smem, allowed);
     if (e != cudaSuccess) return e;
@@ -811,30 +864,31 @@ cudaError_t launch_grad_rows(const GradArgs& a, const NormPlan& plan, cudaStream
     return cudaGetLastError();
 }
 
-// f(shape) for the shape of a plan, as constants: values of a load, threads of a row, loads of a thread.
-template <int VEC, int GROUP, int PER> struct Shape {
-    static constexpr int vec = VEC, group = GROUP, per = PER;
+// f(shape) for the shape of a plan, as constants: whether rows are aligned, threads of a row, packs of a thread.
+template <bool ALIGNED, int GROUP, int PER> struct Shape {
+    static constexpr bool aligned = ALIGNED;
+    static constexpr int group = GROUP, per = PER;
 };
 template <class T, class F>
 cudaError_t with_shape(const NormPlan& plan, F f) {
-    constexpr int V = 16 / sizeof(T), MOST = ROW_VALUES / V;
-#define SEG_NORM_SHAPE(v, g, n) \
-    if (plan.vec == v && plan.group == g && plan.per == n) return f(Shape<v, g, n>())
-    SEG_NORM_SHAPE(V, 8, 1);
-    if constexpr (V == 4) SEG_NORM_SHAPE(V, 8, 2);
-    SEG_NORM_SHAPE(V, 8, MOST);
-    SEG_NORM_SHAPE(V, 16, MOST);
-    SEG_NORM_SHAPE(V, 32, MOST);
-    SEG_NORM_SHAPE(V, 64, MOST);
-    SEG_NORM_SHAPE(V, 128, MOST);
-    SEG_NORM_SHAPE(V, 256, 1);
-    SEG_NORM_SHAPE(V, 256, MOST);
-    SEG_NORM_SHAPE(V, 512, MOST);
-    SEG_NORM_SHAPE(V, 1024, MOST);
-    SEG_NORM_SHAPE(1, 32, 4);
-    SEG_NORM_SHAPE(1, 32, 8);
-    SEG_NORM_SHAPE(1, 256, 8);
-    SEG_NORM_SHAPE(1, 1024, 8);
+    constexpr int MOST = ROW_VALUES * sizeof(T) / 16;
+#define SEG_NORM_SHAPE(a, g, n) \
+    if (plan.aligned == a && plan.group == g && plan.per == n) return f(Shape<a, g, n>())
+    SEG_NORM_SHAPE(true, 8, 1);
+    if constexpr (MOST == 4) SEG_NORM_SHAPE(true, 8, 2);
+    SEG_NORM_SHAPE(true, 8, MOST);
+    SEG_NORM_SHAPE(true, 16, MOST);
+    SEG_NORM_SHAPE(true, 32, MOST);
+    SEG_NORM_SHAPE(true, 64, MOST);
+    SEG_NORM_SHAPE(true, 128, MOST);
+    SEG_NORM_SHAPE(true, 256, 1);
+    SEG_NORM_SHAPE(true, 256, MOST);
+    SEG_NORM_SHAPE(true, 512, MOST);
+    SEG_NORM_SHAPE(true, 1024, MOST);
+    SEG_NORM_SHAPE(false, 8, MOST);
+    SEG_NORM_SHAPE(false, 32, MOST);
+    SEG_NORM_SHAPE(false, 128, MOST);
+    SEG_NORM_SHAPE(false, 1024, MOST);
 #undef SEG_NORM_SHAPE
     return cudaErrorInvalidConfiguration;
 }
@@ -845,7 +899,7 @@ cudaError_t launch_type(const NormParams& p, const NormPlan& plan, cudaStream_t 
         norm_long_kernel<T><<<static_cast<unsigned>(plan.chunks), 256, 0, stream>>>(p);
         return cudaGetLastError();
     }
-    return with_shape<T>(plan, [&](auto s) { return launch_rows<T, s.vec, s.group, s.per>(p, plan, stream); });
+    return with_shape<T>(plan, [&](auto s) { return launch_rows<T, s.aligned, s.group, s.per>(p, plan, stream); });
 }
 
 template <class T>
@@ -855,7 +909,7 @@ cudaError_t launch_grad_type(const GradArgs& a, const NormPlan& plan, cudaStream
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
-    return with_shape<T>(plan, [&](auto s) { return launch_grad_rows<T, s.vec, s.group, s.per>(a, plan, stream); });
+    return with_shape<T>(plan, [&](auto s) { return launch_grad_rows<T, s.aligned, s.group, s.per>(a, plan, stream); });
 }
 
 }  // namespace
@@ -866,24 +920,23 @@ NormPlan plan_norm(bool grad, const NormParams& p) {
     // whole 16-byte loads of every operand
     const bool vec = p.F % v == 0 && p.ldx % v == 0 && aligned16(p.x) && (!p.out || (p.ldo % v == 0 && aligned16(p.out))) &&
                      (!grad || (p.ldy % v == 0 && aligned16(p.dy))) && aligned16(p.weight) && aligned16(p.bias) && aligned16(p.dweight) && aligned16(p.dbias);
-    d.vec = vec ? v : 1;
+    d.aligned = vec;
     d.tiles = 1;
-    const int64_t loads = ceil_to(p.F, d.vec);
-    const int most = vec ? ROW_VALUES / v : 8;
+    const int64_t loads = ceil_to(p.F, v);
+    const int most = ROW_VALUES / v;
     // as few threads for a row as hold it; where there are few rows, a block's, so
     // that each is over sooner
-    if (p.R <= p.sms && loads > 32) {
-        d.group = loads <= 256 * most ? 256 : vec && loads <= 512 * most ? 512 : 1024;
+    if (vec && p.R <= p.sms && loads > 32) {
+        d.group = loads <= 256 * most ? 256 : loads <= 512 * most ? 512 : 1024;
     } else {
-        d.group = vec ? 8 : 32;
-        while (d.group < 1024 && int64_t(d.group) * most < loads) d.group *= vec ? 2 : d.group == 32 ? 8 : 4;
+        d.group = 8;
+        while (d.group < 1024 && int64_t(d.group) * most < loads) d.group *= vec ? 2 : d.group == 128 ? 8 : 4;
     }
     d.threads = std::max(d.group, 256);
-    int64_t per = ceil_to(loads, d.group);
+    const int64_t per = ceil_to(loads, d.group);
     d.per = most;
-    if (vec && d.group <= 8) d.per = static_cast<int32_t>(per > 2 ? most : per);
+    if (vec && d.group == 8 && per <= 2) d.per = static_cast<int32_t>(per);
     if (vec && d.group == 256 && per == 1) d.per = 1;
-    if (!vec && d.group == 32 && per <= 4) d.per = 4;
     if (per > most) {
         if (grad) {
             d.tiles = static_cast<int32_t>(ceil_to(per, most));
@@ -895,7 +948,7 @@ NormPlan plan_norm(bool grad, const NormParams& p) {
     const int rows = !grad && d.threads <= 512 ? ROWS : 1;
     const int64_t window = d.per == 0 ? 1 : d.threads / d.group * rows;
     const int64_t most_blocks = d.per == 0 ? int64_t(p.sms) * 8
-                                           : std::max<int64_t>(p.sms * resident(d.threads, d.per * std::max(d.vec, 2) * (grad ? 5 : rows + 2)) / d.tiles, 1);
+                                           : std::max<int64_t>(p.sms * resident(d.threads, d.per * v * (grad ? 5 : rows + 2)) / d.tiles, 1);
     d.chunk = ceil_to(ceil_to(p.R, most_blocks), window) * window;
     d.chunks = ceil_to(p.R, d.chunk);
     if (d.per == 0) d.chunks = std::min<int64_t>(p.R, most_blocks);
@@ -912,7 +965,7 @@ cudaError_t launch_norm(const NormParams& p, const NormPlan& plan, cudaStream_t 
 cudaError_t launch_norm_grad(const NormParams& p, const NormPlan& plan, cudaStream_t stream) {
     GradArgs a{};
     a.p = p;
-    a.tile = static_cast<int32_t>(std::min<int64_t>(p.F, int64_t(plan.group) * plan.per * plan.vec));
+    a.tile = static_cast<int32_t>(std::min<int64_t>(p.F, int64_t(plan.group) * plan.per * (p.type == PT_F32 ? 4 : 8)));
     a.chunk = plan.chunk;
     a.sums = plan.sums_bytes > 0 ? reinterpret_cast<float*>(p.ws) : nullptr;
     a.partials = reinterpret_cast<float*>(p.ws + plan.sums_bytes);

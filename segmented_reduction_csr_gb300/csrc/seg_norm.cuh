@@ -33,8 +33,8 @@ struct NormParams {
 
 // How a call is launched; a pure function of sizes, strides, alignment and the SM count.
 struct NormPlan {
-    int32_t vec;            // values of a load: 16 bytes of them, or 1
-    int32_t per;            // loads of a thread for a row, 0: rows are read again instead of kept
+    int32_t aligned;        // 1: rows and weights are whole 16-byte units
+    int32_t per;            // such units that a thread has of a row, 0: rows are read again instead of kept
     int32_t group;          // threads of a row, a power of two
     int32_t threads;        // of a block
     int64_t chunk, chunks;  // rows of a block; blocks
