@@ -259,12 +259,21 @@ __device__ __forceinline__ void group_sum(float (&v)[N], float* red, int& turn) 
         if constexpr (G == NT) __syncthreads();
         else asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / WARPS), "n"(G) : "memory");
         at += warp / WARPS * WARPS * N;
+        if constexpr (WARPS >= 16) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = 0.0f;
+            for (int i = 0; i < N; ++i) v[i] = at[(threadIdx.x % WARPS) * N + i];
 #pragma unroll
-        for (int w = 0; w < WARPS; ++w)
+            for (int d = WARPS / 2; d > 0; d >>= 1)
 #pragma unroll
-            for (int i = 0; i < N; ++i) v[i] += at[w * N + i];
+                for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], d);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = 0.0f;
+#pragma unroll
+            for (int w = 0; w < WARPS; ++w)
+#pragma unroll
+                for (int i = 0; i < N; ++i) v[i] += at[w * N + i];
+        }
         turn ^= 1;
     }
 }
@@ -415,6 +424,87 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
     __syncthreads();
     group_sum<256, 256, 1>(x, red, turn);
     return x[0];
+}
+
+// Wide rows: a block's row stays in the ring of shared memory and is read from
+// there for each pass over it, so that few registers and two blocks of an SM are
+// enough to have one row on its way while others are added up (5,000 x 9,000
+// bfloat16 in registers of 1,024 threads 82 us, so 58; float32 weights of such rows
+// come from L2 for each of them, which is what bounds it).
+constexpr int WIDE_THREADS = 512, WIDE_SLOTS = 3;
+template <class T>
+__global__ void __launch_bounds__(WIDE_THREADS, 2) norm_wide_kernel(const __grid_constant__ NormParams p, int64_t chunk) {
+    constexpr int V = Pack<T, true>::V, H = V / 2, NT = WIDE_THREADS;
+    __shared__ float red[2 * NT / 32];
+    extern __shared__ __align__(16) unsigned char ring_memory[];
+    const int t = threadIdx.x, packs = static_cast<int>(p.F / V);
+    const int64_t c0 = blockIdx.x * chunk;
+    const int n = static_cast<int>(min(chunk, p.R - c0));
+    const float inv = 1.0f / static_cast<float>(p.F);
+    const bool wide = p.weight_type == PT_F32;
+    const uint32_t base = smem_u32(ring_memory) + t * 16, slot_bytes = packs * 16;
+    const T* px = static_cast<const T*>(p.x) + c0 * p.ldx;
+    auto fetch = [&](int i) {
+        if (i < n)
+            for (int j = t; j < packs; j += NT)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(base + i % WIDE_SLOTS * slot_bytes + (j - t) * 16), "l"(px + i * p.ldx + j * V) : "memory");
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    for (int d = 0; d < WIDE_SLOTS - 1; ++d) fetch(d);
+    int turn = 0;
+    Run run;
+    for (int i = 0; i < n; ++i) {
+        fetch(i + WIDE_SLOTS - 1);        // (a slot that this thread was through with a row ago)
+        asm volatile("cp.async.wait_group %0;" ::"n"(WIDE_SLOTS - 1) : "memory");
+        const uint32_t slot = base + i % WIDE_SLOTS * slot_bytes;
+        auto get = [&](int j, float2 (&f)[H]) {
+            Pack<T, true> x;
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x.raw.x), "=r"(x.raw.y), "=r"(x.raw.z), "=r"(x.raw.w) : "r"(slot + (j - t) * 16) : "memory");
+            x.widen(f);
+        };
+        float2 f[H], all = pair(0.0f);
+        for (int j = t; j < packs; j += NT) {
+            get(j, f);
+#pragma unroll
+            for (int k = 0; k < H; ++k) all = __fadd2_rn(all, f[k]);
+        }
+        float sum[1] = {all.x + all.y};
+        group_sum<NT, NT, 1>(sum, red, turn);
+        const float mean = sum[0] * inv;
+        all = pair(0.0f);
+        for (int j = t; j < packs; j += NT) {
+            get(j, f);
+#pragma unroll
+            for (int k = 0; k < H; ++k) {
+                f[k] = __fadd2_rn(f[k], pair(-mean));
+                all = __ffma2_rn(f[k], f[k], all);
+            }
+        }
+        sum[0] = all.x + all.y;
+        group_sum<NT, NT, 1>(sum, red, turn);
+        const float rstd = rsqrtf(fmaf(sum[0], inv, p.eps));
+        const int64_t r = c0 + i;
+        if (r >= run.end) run = run_of(p, r, run.s);
+        const bool used = run.s >= 0;
+        if (t == 0) {
+            if (p.mean) p.mean[r] = used ? mean : 0.0f;
+            if (p.rstd) p.rstd[r] = used ? rstd : 0.0f;
+        }
+        T* y = static_cast<T*>(p.out) + r * p.ldo;
+        for (int j = t; j < packs; j += NT) {
+            float2 w[H], b[H];
+#pragma unroll
+            for (int k = 0; k < H; ++k) w[k] = pair(1.0f), b[k] = pair(0.0f);
+            if (used && p.weight) load_weights<T, true>(p.weight, wide, run.s * p.F + j * V, V, w);
+            if (used && p.bias) load_weights<T, true>(p.bias, wide, run.s * p.F + j * V, V, b);
+            get(j, f);
+#pragma unroll
+            for (int k = 0; k < H; ++k) f[k] = used ? __ffma2_rn(__fmul2_rn(__fadd2_rn(f[k], pair(-mean)), pair(rstd)), w[k], b[k]) : pair(0.0f);
+            Pack<T, true> o;
+            o.narrow(f);
+            o.store(y + j * V, V);
+        }
+    }
 }
 
 // Rows of more columns than a block's registers hold: read three times, the
@@ -888,6 +978,7 @@ cudaError_t with_shape(const NormPlan& plan, F f) {
     SEG_NORM_SHAPE(false, 8, MOST);
     SEG_NORM_SHAPE(false, 32, MOST);
     SEG_NORM_SHAPE(false, 128, MOST);
+    SEG_NORM_SHAPE(false, 512, MOST);
     SEG_NORM_SHAPE(false, 1024, MOST);
 #undef SEG_NORM_SHAPE
     return cudaErrorInvalidConfiguration;
@@ -895,6 +986,14 @@ cudaError_t with_shape(const NormPlan& plan, F f) {
 
 template <class T>
 cudaError_t launch_type(const NormParams& p, const NormPlan& plan, cudaStream_t stream) {
+    if (plan.per == 0 && plan.aligned && plan.group == WIDE_THREADS) {
+        static int allowed[64] = {};
+        const int smem = static_cast<int>(WIDE_SLOTS * p.F * sizeof(T));
+        const cudaError_t e = allow_smem(norm_wide_kernel<T>, smem, allowed);
+        if (e != cudaSuccess) return e;
+        norm_wide_kernel<T><<<static_cast<unsigned>(plan.chunks), WIDE_THREADS, smem, stream>>>(p, plan.chunk);
+        return cudaGetLastError();
+    }
     if (plan.per == 0) {
         norm_long_kernel<T><<<static_cast<unsigned>(plan.chunks), 256, 0, stream>>>(p);
         return cudaGetLastError();
@@ -930,28 +1029,34 @@ NormPlan plan_norm(bool grad, const NormParams& p) {
         d.group = loads <= 256 * most ? 256 : loads <= 512 * most ? 512 : 1024;
     } else {
         d.group = 8;
-        while (d.group < 1024 && int64_t(d.group) * most < loads) d.group *= vec ? 2 : d.group == 128 ? 8 : 4;
+        while (d.group < 1024 && int64_t(d.group) * most < loads) d.group *= vec || d.group == 512 ? 2 : 4;
     }
     d.threads = std::max(d.group, 256);
     const int64_t per = ceil_to(loads, d.group);
     d.per = most;
     if (vec && d.group == 8 && per <= 2) d.per = static_cast<int32_t>(per);
     if (vec && d.group == 256 && per == 1) d.per = 1;
-    if (per > most) {
+    // Wide rows, forward: from shared memory, or read again.  (Rows that are not
+    // aligned, 5,000 x 9,001 bfloat16, by 1,024 threads 192 us, read again 114.)
+    const int64_t ring = WIDE_SLOTS * p.F * size;
+    const bool from_ring = !grad && vec && loads > 256 * most && ring <= 216 * 1024;
+    if (from_ring || (!grad && d.group == 1024)) {
+        d.per = 0;
+        d.threads = d.group = from_ring ? WIDE_THREADS : 256;
+    } else if (per > most) {
         if (grad) {
             d.tiles = static_cast<int32_t>(ceil_to(per, most));
             d.sums_bytes = ceil_to(p.R * 8, 256) * 256;
-        } else {
-            d.per = 0;
         }
     }
     const int rows = !grad && d.threads <= 512 ? ROWS : 1;
     const int64_t window = d.per == 0 ? 1 : d.threads / d.group * rows;
-    const int64_t most_blocks = d.per == 0 ? int64_t(p.sms) * 8
-                                           : std::max<int64_t>(p.sms * resident(d.threads, d.per * v * (grad ? 5 : rows + 2)) / d.tiles, 1);
+    const int64_t most_blocks = from_ring ? int64_t(p.sms) * (ring <= 108 * 1024 ? 2 : 1)
+                                : d.per == 0 ? int64_t(p.sms) * 8
+                                             : std::max<int64_t>(p.sms * resident(d.threads, d.per * v * (grad ? 5 : rows + 2)) / d.tiles, 1);
     d.chunk = ceil_to(ceil_to(p.R, most_blocks), window) * window;
     d.chunks = ceil_to(p.R, d.chunk);
-    if (d.per == 0) d.chunks = std::min<int64_t>(p.R, most_blocks);
+    if (d.per == 0 && !from_ring) d.chunks = std::min<int64_t>(p.R, most_blocks);
     if (grad) d.partial_bytes = ceil_to(d.chunks * 4 * p.F * 4, 256) * 256;
     return d;
 }
