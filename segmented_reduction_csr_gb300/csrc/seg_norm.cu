@@ -872,17 +872,19 @@ __global__ void __launch_bounds__(ADD_THREADS) norm_add_kernel(const __grid_cons
     if (by_start) {
         const Run run = run_of(p, min((int64_t(blockIdx.x) + 1) * a.chunk, p.R) - 1);
         s = run.s, begin = run.begin, end = run.end;
-        if (s < 0 || begin / a.chunk != blockIdx.x) return;
+        if (s < 0 || begin / a.chunk != blockIdx.x) end = begin;
     } else if (p.offsets) {
         begin = offset_at(p, s), end = offset_at(p, s + 1);
     }
+    // by every block, also one without work: what follows this kernel in the stream
+    // may rely on the backward pass too
+    grid_wait();
     if (begin >= end) return;
     const int64_t first = begin / a.chunk, last = (end - 1) / a.chunk;
     if (first == last) return;
     const int lane = threadIdx.x % lanes, share = threadIdx.x / lanes, shares = ADD_THREADS / lanes;
     const int parts = static_cast<int>(last - first + 1), each = (parts + shares - 1) / shares;
     const int q0 = share * each, q1 = min(q0 + each, parts);
-    grid_wait();
     for (int64_t i0 = int64_t(blockIdx.y) * lanes * V; i0 < 2 * p.F; i0 += int64_t(gridDim.y) * lanes * V) {
         const int64_t i = i0 + lane * V;
         float v[V];

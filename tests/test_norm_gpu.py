@@ -141,6 +141,40 @@ def test_segment_shapes(dtype, kind, f):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("f", (4104, 6001, 9000, 12288, 20000))
+def test_wide_rows_of_segments(dtype, f):
+    """Rows of a block's threads, from shared memory, read again, and in tiles of columns."""
+    torch, sr = mods()
+    lens = [3, 0, 1, 150, 0, 97, 1, 0]
+    off = 2 + np.concatenate([[0], np.cumsum(lens)]).astype(np.int64)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(f)
+    x, dy = normal(g, (int(off[-1]) + 3, f), dtype), normal(g, (int(off[-1]) + 3, f), dtype)
+    x[:2], dy[-3:] = float("nan"), float("inf")
+    w, b = weights(g, len(lens), f, "float32" if f == 9000 else dtype)
+    do = torch.from_numpy(off).cuda()
+    got = sr.seg_layer_norm(x, w, b, do, with_stats=True)
+    check_forward(got, x, w, b, off, 1e-5, (dtype, f))
+    check_grad(sr.seg_layer_norm_grad(x, dy, *got[1:], w, do), x, dy, *got[1:], w, off, (dtype, f))
+
+
+def test_what_follows_the_gradients_in_a_stream_sees_them():
+    """Segments that lie in one block's rows each leave the adding kernel nothing to wait for but the backward pass."""
+    torch, sr = mods()
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    x, dy = normal(g, (60000, 256), "bfloat16"), normal(g, (60000, 256), "bfloat16")
+    off = torch.arange(0, 60001, 2, device="cuda")
+    w = normal(g, (30000, 256), "bfloat16")
+    _, mean, rstd = sr.seg_layer_norm(x, w, None, off, with_stats=True)
+    want = [t.clone() for t in sr.seg_layer_norm_grad(x, dy, mean, rstd, w, off)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        got = [t.clone() for t in sr.seg_layer_norm_grad(x, dy, mean, rstd, w, off)]
+        assert all(torch.equal(p, q) for p, q in zip(got, want))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("f", (16, 64, 72))
 def test_many_rows(dtype, f):
     """Chunks that begin, end and lie inside of segments; more segments than chunks and fewer."""
