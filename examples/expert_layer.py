@@ -1,13 +1,15 @@
 """An expert layer over offset-delimited segments, trained for a few steps and
 then served with per-request adapters.
 
-    python examples/expert_layer.py [--tokens 4096] [--steps 5]
+    python examples/expert_layer.py [--tokens 4096] [--steps 5] [--gated]
 
 Training: every token goes to its two highest-scoring experts.  Sorted by
 expert, the rows of an expert are a segment, so the layer is two
 ``segment_matmul`` calls (forward; their backward is ``seg_matmul`` and
 ``seg_matmul_grad_w``), and the weighted sum back to the tokens is the
-deterministic ``scatter``.
+deterministic ``scatter``.  With ``--gated`` every expert normalises its rows
+with weights of its own (``segment_layer_norm``) and gates them
+(``segment_gated``) before the projection back.
 
 Serving: requests of different lengths share an output projection, each with
 its own low-rank adapter (``seg_lora``), first as prompts, then one token each.
@@ -52,24 +54,32 @@ class CombineRows(torch.autograd.Function):
 
 
 class ExpertLayer(torch.nn.Module):
-    def __init__(self, width: int, hidden: int, experts: int, top: int = 2, dtype=torch.bfloat16):
+    def __init__(self, width: int, hidden: int, experts: int, top: int = 2, dtype=torch.bfloat16, gated: bool = False):
         super().__init__()
-        self.top = top
+        self.top, self.gated = top, gated
         self.router = torch.nn.Parameter(torch.randn(width, experts, device="cuda", dtype=dtype) * width ** -0.5)
-        self.up = torch.nn.Parameter(torch.randn(experts, width, hidden, device="cuda", dtype=dtype) * width ** -0.5)
+        self.up = torch.nn.Parameter(torch.randn(experts, width, hidden * (2 if gated else 1), device="cuda", dtype=dtype) * width ** -0.5)
         self.down = torch.nn.Parameter(torch.randn(experts, hidden, width, device="cuda", dtype=dtype) * hidden ** -0.5)
+        if gated:
+            self.norm_weight = torch.nn.Parameter(torch.ones(experts, width, device="cuda"))
+            self.norm_bias = torch.nn.Parameter(torch.zeros(experts, width, device="cuda"))
 
     def forward(self, x):
         token, weight, offsets = route(x @ self.router, self.top)
-        h = torch.relu(sr.segment_matmul(x[token], self.up, offsets))
+        rows = x[token]
+        if self.gated:
+            h = sr.segment_gated(sr.segment_layer_norm(rows, self.norm_weight, self.norm_bias, offsets), self.up, offsets)
+        else:
+            h = torch.relu(sr.segment_matmul(rows, self.up, offsets))
         y = sr.segment_matmul(h, self.down, offsets)
         return CombineRows.apply(y.float() * weight[:, None], token, x.shape[0]).to(x.dtype)
 
 
-def train(tokens: int = 4096, width: int = 512, hidden: int = 1024, experts: int = 16, steps: int = 5, seed: int = 0):
+def train(tokens: int = 4096, width: int = 512, hidden: int = 1024, experts: int = 16, steps: int = 5, seed: int = 0,
+          gated: bool = False):
     """Losses of a few steps that fit the layer to a fixed random map."""
     torch.manual_seed(seed)
-    layer = ExpertLayer(width, hidden, experts)
+    layer = ExpertLayer(width, hidden, experts, gated=gated)
     x = torch.randn(tokens, width, device="cuda", dtype=torch.bfloat16)
     want = torch.relu(x @ (torch.randn(width, width, device="cuda", dtype=torch.bfloat16) * width ** -0.5))
     opt = torch.optim.SGD(layer.parameters(), lr=0.2)
@@ -109,8 +119,9 @@ def main():
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("--tokens", type=int, default=4096)
     ap.add_argument("--steps", type=int, default=5)
+    ap.add_argument("--gated", action="store_true", help="experts with a norm of their own and a gate")
     args = ap.parse_args()
-    losses = train(tokens=args.tokens, steps=args.steps)
+    losses = train(tokens=args.tokens, steps=args.steps, gated=args.gated)
     print("training losses:", " ".join(f"{v:.4f}" for v in losses))
     prompts, tokens, offsets = serve()
     gap = (prompts[offsets[1:] - 1].float() - tokens.float()).abs().max().item()

@@ -212,6 +212,40 @@ def test_few_rows_long_sums_and_large_tiles(dtype, trans, lens, k, n):
 
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("trans", (False, True))
+def test_odd_matrices_most_of_which_are_in_no_use(dtype, trans):
+    """Not copied to aligned rows: the products first, then the activation."""
+    torch, sr = mods()
+    k, n = 63, 33
+    lens = [0] * 70 + [3] + [0] * 50 + [1]
+    off = np.concatenate([[0], np.cumsum(lens)]).astype(np.int64)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    x = normal(g, (4, k), dtype)
+    w = normal(g, (len(lens), 2 * n, k) if trans else (len(lens), k, 2 * n), dtype, k ** -0.5)
+    do = torch.from_numpy(off).cuda()
+    out = sr.seg_gated(x, w, do, "sigmoid", transpose_w=trans)
+    check_forward(out, None, x, w, off, trans, "sigmoid", (dtype, trans))
+    for ptype in {x.dtype, torch.float32}:
+        same, pre = sr.seg_gated(x, w, do, "sigmoid", transpose_w=trans, pre=torch.empty(4, 2 * n, dtype=ptype, device="cuda"))
+        assert torch.equal(out, same)
+        check_forward(out, pre, x, w, off, trans, "sigmoid", (dtype, trans, ptype))
+
+
+@pytest.mark.parametrize("dtype", ("bfloat16", "float16"))
+def test_sums_longer_than_an_accumulator_takes(dtype):
+    torch, sr = mods()
+    off = np.array([0, 4090])
+    g = torch.Generator(device="cuda")
+    g.manual_seed(2)
+    k, n = 32776, 512
+    x, w = normal(g, (4100, k), dtype), normal(g, (1, 2 * n, k), dtype, k ** -0.5)
+    do = torch.from_numpy(off).cuda()
+    out, pre = sr.seg_gated(x, w, do, transpose_w=True, with_pre=True)
+    check_forward(out, pre, x, w, off, True, "silu", dtype)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("trans", (False, True))
 def test_strides_and_alignment(dtype, trans):
     torch, sr = mods()
     k, n = 72, 40
