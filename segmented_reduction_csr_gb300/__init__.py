@@ -626,7 +626,7 @@ def _check_rows(name, t, offsets):
         raise ValueError(f"{name} must be [R, columns] and offsets [S+1]")
     if not offsets.is_contiguous():
         raise ValueError("offsets must be contiguous")
-    return _row_stride(name, t)
+    return _stride_of(name, t)
 
 
 def _row_stride(name, t):
@@ -636,6 +636,11 @@ def _row_stride(name, t):
     if (one != 1 and cols > 1) or (rows > 1 and step < cols):
         raise ValueError(f"{name} must have contiguous rows that do not overlap")
     return step if rows > 1 else cols or 1
+
+
+def _stride_of(name, t):
+    """``_row_stride``, by one question where rows follow one another."""
+    return (t.shape[-1] or 1) if t.is_contiguous() else _row_stride(name, t)
 
 
 def _same(name, t, like, shape, dtype=None):
@@ -656,6 +661,11 @@ def _fresh(shape, dtype, device, stream):
         out = torch.empty(shape, dtype=dtype, device=device)
     out.record_stream(torch.cuda.current_stream(device))
     return out
+
+
+def _new(shape, dtype, device, stream):
+    """A new result, on ``stream`` where one is given."""
+    return _torch_module.empty(shape, dtype=dtype, device=device) if stream is None else _fresh(shape, dtype, device, stream)
 
 
 def _in_use(stream, *tensors):
@@ -854,22 +864,21 @@ def _gated_weights(x, w, s, transpose_w):
     """Columns of each projection, and the rows' stride, of the gated block's matrices."""
     if w.dim() != 3:
         raise ValueError("w must be [S, K, 2 N] (transpose_w: [S, 2 N, K])")
-    both = w.shape[1] if transpose_w else w.shape[2]
+    _, k, both = w.shape
+    if transpose_w:
+        k, both = both, k
     if both % 2:
         raise ValueError("w must hold two projections of as many columns each")
     _same("w", w, x, (s, both, x.shape[1]) if transpose_w else (s, x.shape[1], both))
-    return both // 2, _row_stride("w", w)
+    return both // 2, _stride_of("w", w)
 
 
 def _rows_out(name, out, like, shape, stream, dtype=None):
     """A result of rows, the caller's (checked) or a new one, and its stride."""
     if out is None:
-        torch = _torch()
-        dtype = like.dtype if dtype is None else dtype
-        out = torch.empty(shape, dtype=dtype, device=like.device) if stream is None else _fresh(shape, dtype, like.device, stream)
-        return out, shape[1] or 1
+        return _new(shape, like.dtype if dtype is None else dtype, like.device, stream), shape[1] or 1
     _same(name, out, like, shape, dtype)
-    return out, _row_stride(name, out)
+    return out, _stride_of(name, out)
 
 
 def _pre_type(pre, x):
@@ -894,9 +903,8 @@ def seg_gated(x, w, offsets, activation: str = "silu", transpose_w: bool = False
     the two products for ``seg_gated_grad``: float32, which the gradients are
     exact to, or, in a ``pre`` of ``x``'s type, half of that memory.  The
     products are float32 up to the result, which is rounded once.  It records
-    no gradient
-    (``segment_gated`` does).  Float32 infinities, ``stream`` and graphs as for
-    ``seg_matmul``; not synchronised."""
+    no gradient (``segment_gated`` does).  Float32 infinities, ``stream`` and
+    graphs as for ``seg_matmul``; not synchronised."""
     torch = _torch()
     ldx = _check_rows("x", x, offsets)
     code, s, (r, k) = _product_code(x), offsets.shape[0] - 1, x.shape
@@ -908,9 +916,9 @@ def seg_gated(x, w, offsets, activation: str = "silu", transpose_w: bool = False
         ptype, pcode = (torch.float32, SEG_F32) if pre is None else _pre_type(pre, x)
         pre, ldp = _rows_out("pre", pre, x, (r, 2 * n), stream, ptype)
     _enqueue("seg_gated", x.device, stream, load_library().seg_gated,
-             x.data_ptr() or None, code, r, k, ldx, w.data_ptr() or None, n, ldw, w.stride(0) if s > 1 else 0,
-             1 if transpose_w else 0, offsets.data_ptr(), _offset_code(offsets), s, act, out.data_ptr() or None, ldo,
-             (pre.data_ptr() or None) if with_pre else None, pcode, ldp)
+             x.data_ptr(), code, r, k, ldx, w.data_ptr(), n, ldw, w.stride(0) if s > 1 else 0,
+             1 if transpose_w else 0, offsets.data_ptr(), _offset_code(offsets), s, act, out.data_ptr(), ldo,
+             pre.data_ptr() if with_pre else None, pcode, ldp)
     if stream is not None:
         _in_use(stream, x, w, offsets, out, pre)
     return (out, pre) if with_pre else out
@@ -936,7 +944,7 @@ def seg_gated_grad(x, w, pre, dy, offsets, activation: str = "silu", transpose_w
     ptype, pcode = _pre_type(pre, x)
     _same("pre", pre, x, (r, 2 * n), ptype)
     _same("dy", dy, x, (r, n))
-    ldp, ldy = _row_stride("pre", pre), _row_stride("dy", dy)
+    ldp, ldy = _stride_of("pre", pre), _stride_of("dy", dy)
     if dw_dtype not in (None, x.dtype, torch.float32):
         raise TypeError(f"dw_dtype must be {x.dtype} or torch.float32, not {dw_dtype}")
     if not (want_dx or want_dw):
@@ -945,20 +953,19 @@ def seg_gated_grad(x, w, pre, dy, offsets, activation: str = "silu", transpose_w
     ldd = -(-2 * n // 8) * 8 or 1
     lib, off, odt, dev = load_library(), offsets.data_ptr(), _offset_code(offsets), x.device
     dpre, _ = _rows_out("dpre", None, x, (r, ldd), stream)
-    at, px, pw = dpre.data_ptr() or None, x.data_ptr() or None, w.data_ptr() or None
-    _enqueue("seg_gated_grad", dev, stream, lib.seg_gated_grad, pre.data_ptr() or None, pcode, r, n, ldp, dy.data_ptr() or None, code, ldy,
-             act, at, ldd)
+    at, px, pw = dpre.data_ptr(), x.data_ptr(), w.data_ptr()
+    _enqueue("seg_gated_grad", dev, stream, lib.seg_gated_grad, pre.data_ptr(), pcode, r, n, ldp, dy.data_ptr(), code, ldy, act, at, ldd)
     dx = dw = None
     if want_dx:
         dx, lddx = _rows_out("dx", None, x, (r, k), stream)
         _enqueue("seg_matmul", dev, stream, lib.seg_matmul, at, code, r, 2 * n, ldd, pw, k, ldw, w.stride(0) if s > 1 else 0,
-                 0 if transpose_w else 1, off, odt, s, dx.data_ptr() or None, lddx)
+                 0 if transpose_w else 1, off, odt, s, dx.data_ptr(), lddx)
     if want_dw:
         dw_dtype = x.dtype if dw_dtype is None else dw_dtype
-        dw = torch.empty(w.shape, dtype=dw_dtype, device=dev) if stream is None else _fresh(w.shape, dw_dtype, dev, stream)
+        dw = _new(w.shape, dw_dtype, dev, stream)
         first, second = ((at, 2 * n, ldd), (px, k, ldx)) if transpose_w else ((px, k, ldx), (at, 2 * n, ldd))
         _enqueue("seg_matmul_grad_w", dev, stream, lib.seg_matmul_grad_w, first[0], code, r, first[1], first[2], *second, off, odt, s,
-                 dw.data_ptr() or None, code if dw_dtype == x.dtype else SEG_F32)
+                 dw.data_ptr(), code if dw_dtype == x.dtype else SEG_F32)
     if stream is not None:
         _in_use(stream, x, w, pre, dy, offsets, dpre, dx, dw)
     return dx, dw
@@ -1011,7 +1018,7 @@ def _norm_arguments(x, weight, bias, offsets):
             raise ValueError("x must be a CUDA tensor (there is no CPU path)")
         if x.dim() != 2:
             raise ValueError("x must be [R, columns]")
-        ldx, s, odt, shape = _row_stride("x", x), 1, SEG_OFF_I64, x.shape[1:]
+        ldx, s, odt, shape = _stride_of("x", x), 1, SEG_OFF_I64, x.shape[1:]
     else:
         ldx = _check_rows("x", x, offsets)
         s, odt = offsets.shape[0] - 1, _offset_code(offsets)
@@ -1022,11 +1029,14 @@ def _norm_arguments(x, weight, bias, offsets):
         wcode = _product_code(like)
         if wcode != code and wcode != SEG_F32:
             raise TypeError(f"weight and bias must be {x.dtype} or torch.float32, not {like.dtype}")
-        for name, t in (("weight", weight), ("bias", bias)):
-            if t is not None:
-                _same(name, t, x, shape, like.dtype)
-                if not t.is_contiguous():
-                    raise ValueError(f"{name} must be contiguous")
+        if weight is not None:
+            _same("weight", weight, x, shape, like.dtype)
+            if not weight.is_contiguous():
+                raise ValueError("weight must be contiguous")
+        if bias is not None:
+            _same("bias", bias, x, shape, like.dtype)
+            if not bias.is_contiguous():
+                raise ValueError("bias must be contiguous")
     return ldx, code, wcode, s, odt
 
 
@@ -1051,14 +1061,10 @@ def seg_layer_norm(x, weight=None, bias=None, offsets=None, eps: float = 1e-5, w
     out, ldo = _rows_out("out", out, x, (r, f), stream)
     mean = rstd = None
     if with_stats:
-        torch = _torch()
-        if stream is None:
-            mean, rstd = torch.empty(r, dtype=torch.float32, device=x.device), torch.empty(r, dtype=torch.float32, device=x.device)
-        else:
-            mean, rstd = _fresh((r,), torch.float32, x.device, stream), _fresh((r,), torch.float32, x.device, stream)
-    _enqueue("seg_layer_norm", x.device, stream, load_library().seg_layer_norm, x.data_ptr() or None, code, r, f, ldx,
-             _ptr(weight) or None, _ptr(bias) or None, wcode, _ptr(offsets), odt, s, eps, out.data_ptr() or None, ldo, (mean.data_ptr() or None) if with_stats else None,
-             (rstd.data_ptr() or None) if with_stats else None)
+        device, f32 = x.device, _torch_module.float32
+        mean, rstd = _new(r, f32, device, stream), _new(r, f32, device, stream)
+    _enqueue("seg_layer_norm", x.device, stream, load_library().seg_layer_norm, x.data_ptr(), code, r, f, ldx, _ptr(weight), _ptr(bias),
+             wcode, _ptr(offsets), odt, s, eps, out.data_ptr(), ldo, _ptr(mean), _ptr(rstd))
     if stream is not None:
         _in_use(stream, x, weight, bias, offsets, out, mean, rstd)
     return (out, mean, rstd) if with_stats else out
@@ -1072,9 +1078,10 @@ def seg_layer_norm_grad(x, dy, mean, rstd, weight=None, offsets=None, with_dx: b
 
     ``dx`` is like ``x`` (0 for a row in no segment).  ``dweight`` and ``dbias``
     are ``[S, F]`` (``[F]`` without ``offsets``) in ``weight``'s type (without
-    one: ``weight_dtype``, ``x``'s by default, or float32), summed in float32 in a fixed order and rounded once; zeros
-    for a segment without rows.  Arguments, ``stream`` and graphs as for
-    ``seg_layer_norm``; not synchronised."""
+    one: ``weight_dtype``, ``x``'s by default, or float32), summed in float32 in
+    a fixed order and rounded once; zeros for a segment without rows.
+    Arguments, ``stream`` and graphs as for ``seg_layer_norm``; not
+    synchronised."""
     torch = _torch()
     ldx, code, wcode, s, odt = _norm_arguments(x, weight, None, offsets)
     if weight is None and weight_dtype is not None:
@@ -1083,25 +1090,20 @@ def seg_layer_norm_grad(x, dy, mean, rstd, weight=None, offsets=None, with_dx: b
         wtype, wcode = weight_dtype, code if weight_dtype == x.dtype else SEG_F32
     else:
         wtype = x.dtype if weight is None else weight.dtype
-    r, f = x.shape
-    _same("dy", dy, x, (r, f))
-    ldy = _row_stride("dy", dy)
-    for name, t in (("mean", mean), ("rstd", rstd)):
-        _same(name, t, x, (r,), torch.float32)
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-    shape = (f,) if offsets is None else (s, f)
-
-    def fresh(wanted, shape, dtype):
-        if not wanted:
-            return None
-        return torch.empty(shape, dtype=dtype, device=x.device) if stream is None else _fresh(shape, dtype, x.device, stream)
-
-    dx, dweight, dbias = fresh(with_dx, (r, f), x.dtype), fresh(with_weight, shape, wtype), fresh(with_bias, shape, wtype)
-    _enqueue("seg_layer_norm_grad", x.device, stream, load_library().seg_layer_norm_grad, x.data_ptr() or None, code, r, f, ldx,
-             dy.data_ptr() or None, ldy, mean.data_ptr() or None, rstd.data_ptr() or None, _ptr(weight) or None, wcode,
-             _ptr(offsets), odt, s,
-             _ptr(dx) or None, max(f, 1), _ptr(dweight) or None, _ptr(dbias) or None)
+    shape, dtype, device, f32 = x.shape, x.dtype, x.device, torch.float32
+    r, f = shape
+    _same("dy", dy, x, shape, dtype)
+    _same("mean", mean, x, (r,), f32)
+    _same("rstd", rstd, x, (r,), f32)
+    ldy = _stride_of("dy", dy)
+    if not (mean.is_contiguous() and rstd.is_contiguous()):
+        raise ValueError("mean and rstd must be contiguous")
+    sums = (f,) if offsets is None else (s, f)
+    dx = _new(shape, dtype, device, stream) if with_dx else None
+    dweight = _new(sums, wtype, device, stream) if with_weight else None
+    dbias = _new(sums, wtype, device, stream) if with_bias else None
+    _enqueue("seg_layer_norm_grad", device, stream, load_library().seg_layer_norm_grad, x.data_ptr(), code, r, f, ldx, dy.data_ptr(), ldy,
+             mean.data_ptr(), rstd.data_ptr(), _ptr(weight), wcode, _ptr(offsets), odt, s, _ptr(dx), f or 1, _ptr(dweight), _ptr(dbias))
     if stream is not None:
         _in_use(stream, x, dy, mean, rstd, weight, offsets, dx, dweight, dbias)
     return dx, dweight, dbias
@@ -1110,7 +1112,8 @@ def seg_layer_norm_grad(x, dy, mean, rstd, weight=None, offsets=None, with_dx: b
 def segment_layer_norm(x, weight=None, bias=None, indptr=None, eps: float = 1e-5):
     """Differentiable ``seg_layer_norm``: its backward pass is
     ``seg_layer_norm_grad``, for the gradients that are asked for.
-    Differentiable once; no forward mode and no vmap."""
+    Differentiable once; no forward mode and no vmap.  (Captured as
+    ``segment_gated`` is.)"""
     return _segment_layer_norm_function().apply(x, weight, bias, indptr, eps)
 
 
