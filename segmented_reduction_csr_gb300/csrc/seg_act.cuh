@@ -68,6 +68,12 @@ __device__ __forceinline__ float activate(int kind, float x, float& slope) {
         q = 1.5957691f * x * fmaf(0.044715f, x2, 1.0f);
         if (SLOPE) dq = 1.5957691f * fmaf(0.134145f, x2, 1.0f);
     }
+    if constexpr (FAST && !SLOPE) {
+        // s alone: exp(-q) may overflow, 1 / inf is 0
+        float r;
+        asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.0f + __expf(-q)));
+        return kind == ACT_SIGMOID ? r : x * r;
+    }
     float s, other;
     logistic<FAST>(q, s, other);
     const float f = kind == ACT_SIGMOID ? s : x * s;

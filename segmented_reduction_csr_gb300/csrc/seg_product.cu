@@ -465,18 +465,18 @@ __device__ __forceinline__ void store_any(void* out, int type, int64_t at, int64
     else store_rows(static_cast<uint16_t*>(out) + at, step, v, n, [type](float x) { return static_cast<uint16_t>(narrow_pair(x, 0.0f, type)); });
 }
 
-// g = act(g) * u, with the kind of activation outside of the loop, by the special
-// function unit for float32 too: off by 2 + 1.2 |g| units of 2^-23, where the
-// products are by up to 2^-20 of their terms' sizes, and the drain warps' time is
-// what bounds a float32 tile (expf and a division: 1,000,000 x 64 times 64 x 64
-// twice 262 us, so 166).
-template <int W>
-__device__ __forceinline__ void gate(int kind, float (&g)[W], const float (&u)[W]) {
+// f[i] = act(g(i)) * u(i), with the kind of activation outside of the loop, by
+// the special function unit for float32 too: off by 2 + 1.2 |g| units of 2^-23,
+// where the products are by up to 2^-20 of their terms' sizes, and the drain warps'
+// time is what bounds a float32 tile (expf and a division: 1,000,000 x 64 times 64
+// x 64 twice 262 us, so 166).
+template <int W, class G, class U>
+__device__ __forceinline__ void gate(int kind, float (&f)[W], G g, U u) {
     auto all = [&](auto k) {
 #pragma unroll
         for (int i = 0; i < W; ++i) {
             float slope;
-            g[i] = activate<true, false>(k(), g[i], slope) * u[i];
+            f[i] = activate<true, false>(k(), g(i), slope) * u(i);
         }
     };
     if (kind == ACT_SILU) all([] { return ACT_SILU; });
@@ -489,34 +489,35 @@ __device__ __forceinline__ void gate(int kind, float (&g)[W], const float (&u)[W
 // Both warps of a pair; 3 .. 6 of the CTA's barriers.
 __device__ __forceinline__ void bar_pair(int quarter, int group) { asm volatile("bar.sync %0, 64;" ::"r"(3 + group * 2 + (quarter & 1)) : "memory"); }
 
-// From v's two halves (`low` and `high` name the registers): this warp's half
-// of the rows of both projections, in g and u.  TURNS: the caller takes two
-// places of the staging in turns, so that the barrier before the next values are
-// read is enough.
+// From v's two halves (`low` and `high` name the registers): the results of this
+// warp's half of the rows.  The two warps of a pair take different ways (a choice
+// of registers for each value took a fifth of the drain's instructions).  TURNS:
+// the caller takes two places of the staging in turns, so that the barrier before
+// the next values are read is enough.
 template <int W, bool TURNS, class Low, class High>
-__device__ __forceinline__ void exchange(const float (&v)[W], float (&g)[W / 2], float (&u)[W / 2], Low low, High high, int lane, int quarter,
-                                         int group, unsigned char* own, int staging) {
+__device__ __forceinline__ void exchange_and_gate(int kind, const float (&v)[W], float (&f)[W / 2], Low low, High high, int lane, int quarter,
+                                                  int group, unsigned char* own, int staging) {
     constexpr int H = W / 2;
     const bool second = quarter >= 2;
     float4* to = reinterpret_cast<float4*>(own) + lane;
     const float4* other = reinterpret_cast<const float4*>(second ? own - 2 * staging : own + 2 * staging) + lane;
+    if (second) {
 #pragma unroll
-    for (int i = 0; i < H; i += 4)
-        to[i * 8] = make_float4(second ? v[low(i)] : v[high(i)], second ? v[low(i + 1)] : v[high(i + 1)],
-                                second ? v[low(i + 2)] : v[high(i + 2)], second ? v[low(i + 3)] : v[high(i + 3)]);
+        for (int i = 0; i < H; i += 4) to[i * 8] = make_float4(v[low(i)], v[low(i + 1)], v[low(i + 2)], v[low(i + 3)]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < H; i += 4) to[i * 8] = make_float4(v[high(i)], v[high(i + 1)], v[high(i + 2)], v[high(i + 3)]);
+    }
     bar_pair(quarter, group);
+    float got[H];
 #pragma unroll
     for (int i = 0; i < H; i += 4) {
         const float4 x = other[i * 8];
-        const float got[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float mine = second ? v[high(i + k)] : v[low(i + k)];
-            g[i + k] = second ? got[k] : mine;
-            u[i + k] = second ? mine : got[k];
-        }
+        got[i] = x.x, got[i + 1] = x.y, got[i + 2] = x.z, got[i + 3] = x.w;
     }
     if (!TURNS) bar_pair(quarter, group);      // the staging may be written again
+    if (second) gate(kind, f, [&](int i) { return got[i]; }, [&](int i) { return v[high(i)]; });
+    else gate(kind, f, [&](int i) { return v[low(i)]; }, [&](int i) { return got[i]; });
 }
 
 // W rows from row0 on, n of which there are, of this warp's lanes: register i holds row i.
@@ -525,66 +526,77 @@ __device__ __forceinline__ void gate_rows(const KernelArgs& a, const float (&v)[
                                           int quarter, int group, unsigned char* own, int staging) {
     const ProductParams& p = a.p;
     if (p.pre && lane < lanes) store_any(p.pre, p.pre_type, row0 * p.ldp + (quarter >> 1) * a.cols_m + m + lane, p.ldp, v, n);
-    float g[W / 2], u[W / 2];
-    exchange<W, TURNS>(v, g, u, [](int i) { return i; }, [](int i) { return W / 2 + i; }, lane, quarter, group, own, staging);
-    gate<W / 2>(p.activation, g, u);
+    float f[W / 2];
+    exchange_and_gate<W, TURNS>(p.activation, v, f, [](int i) { return i; }, [](int i) { return W / 2 + i; }, lane, quarter, group, own, staging);
     const int first = (quarter >> 1) * (W / 2);
-    if (lane < lanes) store_any(p.out, p.out_type, (row0 + first) * p.ldo + m + lane, p.ldo, g, n - first);
+    if (lane < lanes) store_any(p.out, p.out_type, (row0 + first) * p.ldo + m + lane, p.ldo, f, n - first);
 }
 
-// 32 rows of 16-bit results that take 16-byte stores, in 8 x 8 blocks as in store_tile.
-__device__ __forceinline__ void gate_blocks(const KernelArgs& a, uint32_t from, int64_t row0, int n, int64_t m, int lanes, int lane, int quarter,
-                                            int group, unsigned char* own, int staging) {
+// 16-bit results that take 16-byte stores, 32 rows at a time in 8 x 8 blocks as in
+// store_tile; the next ones come from tensor memory while these are stored.
+template <int STRIDE>
+__device__ __forceinline__ void gate_blocks(const KernelArgs& a, uint32_t from, int64_t row0, int c, int columns, int64_t m, int lanes, int lane,
+                                            int quarter, int group, unsigned char* own, int staging) {
     const ProductParams& p = a.p;
     const int half = quarter >> 1, unit = lane & 3;
-    float v[32];
-    if (p.pre && p.pre_type == PT_F32) {
-        // (rows of 128 bytes, straight from the lanes)
-        tmem_load(from, v);
+    const bool wide = p.pre && p.pre_type == PT_F32;
+    float v[32], rows[32];      // the sums in blocks; the same in rows of the lanes
+    if (c < columns) {
+        tmem_load_blocks(from + c, v);
+        if (wide) tmem_load(from + c, rows);
+    }
+    for (; c < columns; c += STRIDE) {
+        const int n = columns - c;
         tmem_wait(v);
-        if (lane < lanes) store_rows(static_cast<float*>(p.pre) + row0 * p.ldp + half * a.cols_m + m + lane, p.ldp, v, n, [](float x) { return x; });
-    }
-    tmem_load_blocks(from, v);
-    tmem_wait(v);
-    if (p.pre && p.pre_type != PT_F32) {
-        uint32_t two[16];
+        if (wide) {
+            // (rows of 128 bytes, straight from the lanes)
+            tmem_wait(rows);
+            if (lane < lanes)
+                store_rows(static_cast<float*>(p.pre) + (row0 + c) * p.ldp + half * a.cols_m + m + lane, p.ldp, rows, n, [](float x) { return x; });
+        } else if (p.pre) {
+            uint32_t two[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) two[i] = narrow_pair(v[2 * i], v[2 * i + 1], p.pre_type);
+            for (int i = 0; i < 16; ++i) two[i] = narrow_pair(v[2 * i], v[2 * i + 1], p.pre_type);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < 4; ++k) {
+                const int row = 8 * k + (lane & 7);
+                store_blocks_t(own + row * 64 + (((lane >> 3) ^ (row >> 1 & 3)) << 4), two[2 * k], two[2 * k + 1], two[8 + 2 * k], two[8 + 2 * k + 1]);
+            }
+            __syncwarp();
+            uint16_t* o = static_cast<uint16_t*>(p.pre) + (row0 + c) * p.ldp + half * a.cols_m + m + unit * 8;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int row = i * 8 + (lane >> 2);
+                if (row < n && unit * 8 < lanes) *reinterpret_cast<uint4*>(o + row * p.ldp) = *reinterpret_cast<const uint4*>(own + row * 64 + ((unit ^ (row >> 1 & 3)) << 4));
+            }
+            __syncwarp();
+        }
+        // registers 16 h + 4 k + 2 e + b of rows 8 k + ..: k = 0, 1 are the first 16 rows
+        float f[16];
+        exchange_and_gate<32, false>(p.activation, v, f, [](int i) { return (i & 7) + 2 * (i & 8); }, [](int i) { return (i & 7) + 2 * (i & 8) + 8; },
+                                     lane, quarter, group, own, staging);
+        if (c + STRIDE < columns) {
+            tmem_load_blocks(from + c + STRIDE, v);
+            if (wide) tmem_load(from + c + STRIDE, rows);
+        }
+        uint32_t two[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) two[i] = narrow_pair(f[2 * i], f[2 * i + 1], p.out_type);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
             const int row = 8 * k + (lane & 7);
-            store_blocks_t(own + row * 64 + (((lane >> 3) ^ (row >> 1 & 3)) << 4), two[2 * k], two[2 * k + 1], two[8 + 2 * k], two[8 + 2 * k + 1]);
+            store_blocks_t(own + row * 64 + (((lane >> 3) ^ (row >> 1 & 3)) << 4), two[2 * k], two[2 * k + 1], two[4 + 2 * k], two[4 + 2 * k + 1]);
         }
         __syncwarp();
-        uint16_t* o = static_cast<uint16_t*>(p.pre) + row0 * p.ldp + half * a.cols_m + m + unit * 8;
+        uint16_t* o = static_cast<uint16_t*>(p.out) + (row0 + c + half * 16) * p.ldo + m + unit * 8;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 2; ++i) {
             const int row = i * 8 + (lane >> 2);
-            if (row < n && unit * 8 < lanes) *reinterpret_cast<uint4*>(o + row * p.ldp) = *reinterpret_cast<const uint4*>(own + row * 64 + ((unit ^ (row >> 1 & 3)) << 4));
+            if (half * 16 + row < n && unit * 8 < lanes)
+                *reinterpret_cast<uint4*>(o + row * p.ldo) = *reinterpret_cast<const uint4*>(own + row * 64 + ((unit ^ (row >> 1 & 3)) << 4));
         }
         __syncwarp();
     }
-    // registers 16 h + 4 k + 2 e + b of rows 8 k + ..: k = 0, 1 are the first 16 rows
-    float g[16], u[16];
-    exchange<32, false>(v, g, u, [](int i) { return (i & 7) + 2 * (i & 8); }, [](int i) { return (i & 7) + 2 * (i & 8) + 8; }, lane, quarter, group, own, staging);
-    gate<16>(p.activation, g, u);
-    uint32_t two[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) two[i] = narrow_pair(g[2 * i], g[2 * i + 1], p.out_type);
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const int row = 8 * k + (lane & 7);
-        store_blocks_t(own + row * 64 + (((lane >> 3) ^ (row >> 1 & 3)) << 4), two[2 * k], two[2 * k + 1], two[4 + 2 * k], two[4 + 2 * k + 1]);
-    }
-    __syncwarp();
-    uint16_t* o = static_cast<uint16_t*>(p.out) + (row0 + half * 16) * p.ldo + m + unit * 8;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int row = i * 8 + (lane >> 2);
-        if (half * 16 + row < n && unit * 8 < lanes)
-            *reinterpret_cast<uint4*>(o + row * p.ldo) = *reinterpret_cast<const uint4*>(own + row * 64 + ((unit ^ (row >> 1 & 3)) << 4));
-    }
-    __syncwarp();
 }
 
 // W columns of a tile's sums in 32 lanes: of 16-bit operands, or the accumulators of float32 parts by size.
@@ -1545,8 +1557,7 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                         store_rows(cluster_part + quarter * 32 + c * MT + lane, MT, v, n_left - c, [](float x) { return x; });
                     }
                 } else if (lanes > 0 && BLOCKS && a.wide_rows && (!p.pre || p.pre_type == PT_F32 || a.wide_pre)) {
-                    for (int c = group * 32; c < n_left; c += EPW / 4 * 32)
-                        gate_blocks(a, from + c, t.row0 + c, n_left - c, m, lanes, lane, quarter, group, own_staging, R::STAGING);
+                    gate_blocks<EPW / 4 * 32>(a, from, t.row0, group * 32, n_left, m, lanes, lane, quarter, group, own_staging, R::STAGING);
                 } else if (lanes > 0) {
                     for (int c = group * W; c < n_left; c += ROWS) {
                         float v[W];
@@ -1745,8 +1756,9 @@ product_kernel(const __grid_constant__ KernelArgs a, const __grid_constant__ CUt
                     if (p.pre)
                         for (int h = 0; h < 2; ++h)
                             store_any(p.pre, p.pre_type, (int64_t(t.row0) + c) * p.ldp + h * a.cols_m + m + lane, p.ldp, v[h], n);
-                    gate<W>(p.activation, v[0], v[1]);
-                    store_any(p.out, p.out_type, (int64_t(t.row0) + c) * p.ldo + m + lane, p.ldo, v[0], n);
+                    float f[W];
+                    gate(p.activation, f, [&](int i) { return v[0][i]; }, [&](int i) { return v[1][i]; });
+                    store_any(p.out, p.out_type, (int64_t(t.row0) + c) * p.ldo + m + lane, p.ldo, f, n);
                 }
             } else {
             const int64_t m = t.m0 + rank * MT + quarter * 32;
