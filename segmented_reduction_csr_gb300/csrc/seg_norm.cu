@@ -5,6 +5,15 @@
 // Groups of up to 32 threads add with shuffles, larger ones through shared
 // memory and a barrier of their own.  Everything is float32 and rounded once.
 //
+// What bounds it: memory, once a row costs few instructions and its loads are on
+// their way while others are added up.  16 values of a row per thread, its
+// weights in registers over a run of rows of one segment, two values an
+// instruction, and a ring of rows in shared memory that every thread fills and
+// reads for itself.  32,768 x 2,048 bfloat16, float32 weights: forward 41 us = 6.5
+// TB/s (a warp or two a row, weights from L1 for each row, value by value: 84),
+// backward 72 us = 5.6 TB/s (122).  1,000,000 x 64 float32 in 50 segments: 89 us =
+// 5.8 TB/s and 126 us = 6.1 TB/s.
+//
 // Backward: a block has a chunk of neighbouring rows and takes the runs of rows
 // of one segment in it one after the other.  A thread keeps its columns' sums
 // of dy z and dy in registers over a run; the block's groups are added at its
@@ -289,7 +298,7 @@ template <class T, bool A, int G, int PER, int U, int NT>
 __global__ void __launch_bounds__(NT, resident(NT, Pack<T, A>::V * PER * (U + 2))) norm_kernel(const __grid_constant__ NormParams p, int64_t chunk) {
     using R = Ring<T, A, PER * U, NT>;
     constexpr int V = Pack<T, A>::V, GROUPS = NT / G, STEP = G * V, H = V / 2;
-    constexpr bool KEEP = NT <= 512 && V * PER <= ROW_VALUES;      // a run's weights stay in registers
+    constexpr bool KEEP = NT <= 512;      // a run's weights stay in registers
     __shared__ float red[2 * NT / 32 * U];
     extern __shared__ __align__(16) unsigned char ring_memory[];
     R ring(ring_memory);
@@ -428,9 +437,9 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
 
 // Wide rows: a block's row stays in the ring of shared memory and is read from
 // there for each pass over it, so that few registers and two blocks of an SM are
-// enough to have one row on its way while others are added up (5,000 x 9,000
-// bfloat16 in registers of 1,024 threads 82 us, so 58; float32 weights of such rows
-// come from L2 for each of them, which is what bounds it).
+// enough to have one row on its way while others are added up.  What bounds it are
+// the weights, which come from L2 for each row (2,000 x 20,000 bfloat16 with
+// float32 weights 54 us; 5,000 x 9,000, which go by registers, 58 so and 43).
 constexpr int WIDE_THREADS = 512, WIDE_SLOTS = 3;
 template <class T>
 __global__ void __launch_bounds__(WIDE_THREADS, 2) norm_wide_kernel(const __grid_constant__ NormParams p, int64_t chunk) {
@@ -935,7 +944,7 @@ cudaError_t allow_smem(K* kernel, int bytes, int (&allowed)[64]) {
 
 template <class T, bool A, int G, int PER>
 cudaError_t launch_rows(const NormParams& p, const NormPlan& plan, cudaStream_t stream) {
-    constexpr int NT = G > 256 ? G : 256, U = NT <= 512 ? ROWS : 1, smem = Ring<T, A, PER * U, NT>::BYTES;
+    constexpr int NT = G > 256 ? G : 256, U = NT <= 512 && PER * static_cast<int>(16 / sizeof(T)) <= ROW_VALUES ? ROWS : 1, smem = Ring<T, A, PER * U, NT>::BYTES;
     auto* kernel = norm_kernel<T, A, G, PER, U, NT>;
     static int allowed[64] = {};
     const cudaError_t e = allow_smem(kernel, smem, allowed);
@@ -976,6 +985,7 @@ cudaError_t with_shape(const NormPlan& plan, F f) {
     SEG_NORM_SHAPE(true, 256, 1);
     SEG_NORM_SHAPE(true, 256, MOST);
     SEG_NORM_SHAPE(true, 512, MOST);
+    SEG_NORM_SHAPE(true, 512, 2 * MOST);      // forward
     SEG_NORM_SHAPE(true, 1024, MOST);
     SEG_NORM_SHAPE(false, 8, MOST);
     SEG_NORM_SHAPE(false, 32, MOST);
@@ -1000,7 +1010,10 @@ cudaError_t launch_type(const NormParams& p, const NormPlan& plan, cudaStream_t 
         norm_long_kernel<T><<<static_cast<unsigned>(plan.chunks), 256, 0, stream>>>(p);
         return cudaGetLastError();
     }
-    return with_shape<T>(plan, [&](auto s) { return launch_rows<T, s.aligned, s.group, s.per>(p, plan, stream); });
+    return with_shape<T>(plan, [&](auto s) {
+        if constexpr (s.group == 1024) return cudaErrorInvalidConfiguration;      // (wide rows: above)
+        else return launch_rows<T, s.aligned, s.group, s.per>(p, plan, stream);
+    });
 }
 
 template <class T>
@@ -1010,7 +1023,10 @@ cudaError_t launch_grad_type(const GradArgs& a, const NormPlan& plan, cudaStream
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
-    return with_shape<T>(plan, [&](auto s) { return launch_grad_rows<T, s.aligned, s.group, s.per>(a, plan, stream); });
+    return with_shape<T>(plan, [&](auto s) {
+        if constexpr (s.per * static_cast<int>(16 / sizeof(T)) > ROW_VALUES) return cudaErrorInvalidConfiguration;
+        else return launch_grad_rows<T, s.aligned, s.group, s.per>(a, plan, stream);
+    });
 }
 
 }  // namespace
@@ -1033,25 +1049,29 @@ NormPlan plan_norm(bool grad, const NormParams& p) {
         d.group = 8;
         while (d.group < 1024 && int64_t(d.group) * most < loads) d.group *= vec || d.group == 512 ? 2 : 4;
     }
+    // forward, as many again of a thread: 5,000 x 9,000 bfloat16 43 us, by 1,024
+    // threads, which have no registers for the weights, 82
+    const bool twice = !grad && vec && d.group == 1024 && loads <= 1024 * most;
+    if (twice) d.group = 512;
     d.threads = std::max(d.group, 256);
     const int64_t per = ceil_to(loads, d.group);
-    d.per = most;
+    d.per = twice ? 2 * most : most;
     if (vec && d.group == 8 && per <= 2) d.per = static_cast<int32_t>(per);
     if (vec && d.group == 256 && per == 1) d.per = 1;
     // Wide rows, forward: from shared memory, or read again.  (Rows that are not
     // aligned, 5,000 x 9,001 bfloat16, by 1,024 threads 192 us, read again 114.)
     const int64_t ring = WIDE_SLOTS * p.F * size;
-    const bool from_ring = !grad && vec && loads > 256 * most && ring <= 216 * 1024;
+    const bool from_ring = !grad && vec && loads > 1024 * most && ring <= 216 * 1024;
     if (from_ring || (!grad && d.group == 1024)) {
         d.per = 0;
         d.threads = d.group = from_ring ? WIDE_THREADS : 256;
-    } else if (per > most) {
+    } else if (per > d.per) {
         if (grad) {
             d.tiles = static_cast<int32_t>(ceil_to(per, most));
             d.sums_bytes = ceil_to(p.R * 8, 256) * 256;
         }
     }
-    const int rows = !grad && d.threads <= 512 ? ROWS : 1;
+    const int rows = !grad && d.threads <= 512 && !twice ? ROWS : 1;
     const int64_t window = d.per == 0 ? 1 : d.threads / d.group * rows;
     const int64_t most_blocks = from_ring ? int64_t(p.sms) * (ring <= 108 * 1024 ? 2 : 1)
                                 : d.per == 0 ? int64_t(p.sms) * 8
