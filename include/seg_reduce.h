@@ -49,7 +49,7 @@ extern "C" {
 /* Same type as the CUDA runtime's cudaStream_t; NULL is the legacy default stream. */
 typedef struct CUstream_st *seg_stream_t;
 
-/* SEG_F16 and SEG_BF16 are types of the products (seg_matmul and after) alone. */
+/* SEG_F16 and SEG_BF16 are types of the products and norms (seg_matmul and after) alone. */
 typedef enum { SEG_U32 = 0, SEG_S32 = 1, SEG_F32 = 2, SEG_F16 = 3, SEG_BF16 = 4 } seg_dtype_t;
 typedef enum { SEG_OFF_U32 = 0, SEG_OFF_I64 = 1 } seg_offset_dtype_t;
 typedef enum { SEG_SUM = 0, SEG_MIN = 1, SEG_MAX = 2, SEG_MEAN = 3 } seg_op_t;

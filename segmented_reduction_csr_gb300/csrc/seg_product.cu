@@ -22,7 +22,7 @@
 // out the adapters' part.  Every wait has a time limit; a role that gives up
 // says so in the device status word and all leave.
 //
-// What bounds it (GB300; measured peaks 6,793 GB/s, and 1,892 TFLOP/s in short
+// What bounds it (gated: below, at its drain; GB300; measured peaks 6,793 GB/s, and 1,892 TFLOP/s in short
 // runs, 1,706 held).  Times are of a call in a replayed graph / of calls back to
 // back from Python:
 //   training shapes: the tensor cores' clock and power.  32,768 rows, 32
@@ -455,6 +455,13 @@ __device__ __forceinline__ void store_tile(const KernelArgs& a, uint32_t from, b
 // two warps, `quarter` and `quarter` ^ 2.  Each of them takes half of the rows
 // and gives the other half of its values to the other one, through shared
 // memory: 2 x 64 KB a tile of 256 rows, under a tenth of what its MMAs read.
+// 32,768 rows, 32 x (2,048 x 2,048 twice) bfloat16: 310 us, as the plain product
+// of as many columns takes (312: clock and power), and 348 with the float32
+// products kept; 4,161 uneven rows, 16 x (1,024 x 2,048 twice) float16 42 us (the
+// plain product 39); 128 rows, 64 x (2,048 x 1,024 twice) bfloat16 59 us = 6.3 TB/s
+// of the matrices in use.  Short sums are bound by the drain: 32,768 rows, 8 x (64 x
+// 512 twice) bfloat16 35 us, of which twice the drain warps would save 4 and cost the
+// long sums 1 %.
 // (16 columns of each projection by turns in the lanes would need no exchange,
 // but a matrix whose columns are contiguous cannot be copied so.)
 
@@ -1908,7 +1915,8 @@ __device__ __forceinline__ uint4 load_8(const uint16_t* p) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// (64 x 520 rows of 666 float16, 44 MB: a warp to a row and value by value 19 us, now 18 and both projections of it 30, now 18.)
+// (64 x 520 rows of 666 float16, 44 MB there and back, each half a row of its own:
+// a warp to a row and value by value 30 us, now 18 to 20.)
 template <class T>
 __global__ void __launch_bounds__(256) pack_kernel(const __grid_constant__ PackArgs a) {
     constexpr int V = 16 / sizeof(T), AHEAD = 4;
