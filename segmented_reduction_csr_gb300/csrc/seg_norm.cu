@@ -47,65 +47,48 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(f
 // took 28 instructions a value, 32,768 x 2,048 bfloat16 79 us).
 __device__ __forceinline__ float2 pair(float x) { return make_float2(x, x); }
 
-// The 16 bytes of values that are loaded and stored together.  A: they lie on a
-// border of 16 bytes, and rows are whole numbers of them; else a row's last ones
-// may be there in part, the others count as 0, and 16-bit values, which may lie
-// between two words, go by words and by single values.
-template <class T, bool A> struct Pack {
+// 16 bytes of values of a thread.  A: they lie on a border of 16 bytes, and rows
+// are whole numbers of them.  Else they are G values apart, neighbours those of
+// the neighbouring threads (16-bit values may lie between two words, and a warp's
+// neighbouring ones are a request of few sectors), and a row's last ones may be
+// there in part; the others count as 0.
+template <class T, bool A, int G = 1> struct Pack {
     static constexpr int V = 16 / sizeof(T), H = V / 2;
+    static constexpr int NEXT = A ? V : 1, STEP = A ? 1 : G;       // values from a thread's first to the next thread's, to its own next one
+    using Bits = typename std::conditional<sizeof(T) == 4, uint32_t, uint16_t>::type;
     uint4 raw;
-    // n: values that there are, V or more of them if all
+    // n: values from p on that there are in the row
     __device__ __forceinline__ void load(const T* p, int n) {
         if constexpr (A) {
             raw = __ldg(reinterpret_cast<const uint4*>(p));
-        } else if constexpr (sizeof(T) == 4) {
-            const uint32_t* w = reinterpret_cast<const uint32_t*>(p);
-            raw = make_uint4(__ldg(w), n > 1 ? __ldg(w + 1) : 0, n > 2 ? __ldg(w + 2) : 0, n > 3 ? __ldg(w + 3) : 0);
         } else {
-            const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
-            uint32_t w[4] = {0, 0, 0, 0};
-            if (n < V) {
+            const Bits* from = reinterpret_cast<const Bits*>(p);
+            Bits x[V];
+            if (n > (V - 1) * STEP) {
 #pragma unroll
-                for (int i = 0; i < V; ++i)
-                    if (i < n) w[i / 2] |= static_cast<uint32_t>(__ldg(h + i)) << (i % 2 * 16);
-            } else if ((reinterpret_cast<uintptr_t>(p) & 3) == 0) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t*>(h) + i);
+                for (int i = 0; i < V; ++i) x[i] = __ldg(from + i * STEP);
             } else {
-                const uint32_t first = __ldg(h), last = __ldg(h + 7);
-                uint32_t m[3];
 #pragma unroll
-                for (int i = 0; i < 3; ++i) m[i] = __ldg(reinterpret_cast<const uint32_t*>(h + 1) + i);
-                w[0] = first | m[0] << 16;
-                w[1] = __funnelshift_l(m[0], m[1], 16);
-                w[2] = __funnelshift_l(m[1], m[2], 16);
-                w[3] = m[2] >> 16 | last << 16;
+                for (int i = 0; i < V; ++i) x[i] = i * STEP < n ? __ldg(from + i * STEP) : Bits(0);
             }
-            raw = make_uint4(w[0], w[1], w[2], w[3]);
+            if constexpr (sizeof(T) == 4) raw = make_uint4(x[0], x[1], x[2], x[3]);
+            else raw = make_uint4(x[0] | uint32_t(x[1]) << 16, x[2] | uint32_t(x[3]) << 16, x[4] | uint32_t(x[5]) << 16, x[6] | uint32_t(x[7]) << 16);
         }
     }
     __device__ __forceinline__ void store(T* p, int n) const {
-        const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
         if constexpr (A) {
             *reinterpret_cast<uint4*>(p) = raw;
-        } else if constexpr (sizeof(T) == 4) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (i < n) reinterpret_cast<uint32_t*>(p)[i] = w[i];
         } else {
-            uint16_t* h = reinterpret_cast<uint16_t*>(p);
-            if (n < V) {
+            const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+            Bits* to = reinterpret_cast<Bits*>(p);
+            auto value = [&](int i) { return sizeof(T) == 4 ? static_cast<Bits>(w[i & 3]) : static_cast<Bits>(w[i / 2] >> (i % 2 * 16)); };
+            if (n > (V - 1) * STEP) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) to[i * STEP] = value(i);
+            } else {
 #pragma unroll
                 for (int i = 0; i < V; ++i)
-                    if (i < n) h[i] = static_cast<uint16_t>(w[i / 2] >> (i % 2 * 16));
-            } else if ((reinterpret_cast<uintptr_t>(p) & 3) == 0) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) reinterpret_cast<uint32_t*>(h)[i] = w[i];
-            } else {
-                h[0] = static_cast<uint16_t>(w[0]);
-#pragma unroll
-                for (int i = 0; i < 3; ++i) reinterpret_cast<uint32_t*>(h + 1)[i] = __funnelshift_l(w[i], w[i + 1], 16);
-                h[7] = static_cast<uint16_t>(w[3] >> 16);
+                    if (i * STEP < n) to[i * STEP] = value(i);
             }
         }
     }
@@ -142,7 +125,7 @@ template <class T, bool A> struct Pack {
 // and reads nothing but its own, so that no barrier is needed.  (Rows that are
 // not aligned, or of which shared memory does not hold two, are loaded when they
 // are needed.)
-template <class T, bool A, int PER, int NT>
+template <class T, bool A, int G, int PER, int NT>
 struct Ring {
     static constexpr int D = PER == 1 ? 6 : PER <= 4 && NT == 256 ? 4 : PER == 2 ? 4 : PER <= 4 ? 3 : 2;      // fewer bytes of a slot want more of them
     static constexpr bool ASYNC = A && D * PER * NT * 16 <= 200 * 1024;
@@ -160,7 +143,7 @@ struct Ring {
     // the slot to read has landed
     __device__ __forceinline__ void wait() const { asm volatile("cp.async.wait_group %0;" ::"n"(D - 2) : "memory"); }
     __device__ __forceinline__ void get(int j, const T* from, int n, float2 (&f)[Pack<T, A>::H]) const {
-        Pack<T, A> x;
+        Pack<T, A, G> x;
         if constexpr (ASYNC) asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x.raw.x), "=r"(x.raw.y), "=r"(x.raw.z), "=r"(x.raw.w) : "r"(at + j * NT * 16) : "memory");
         else x.load(from, n);
         x.widen(f);
@@ -173,11 +156,11 @@ struct Ring {
     __device__ __forceinline__ void got() { at = at == base + (D - 1) * SLOT ? base : at + SLOT; }
 };
 
-// A pack of values of weight_type at element `at`, n of them.
-template <class T, bool A>
+// A pack of values of weight_type at element `at`, n of them from there on in the row.
+template <class T, bool A, int G = 1>
 __device__ __forceinline__ void load_weights(const void* w, bool wide, int64_t at, int n, float2 (&f)[Pack<T, A>::H]) {
     if (!wide) {
-        Pack<T, A> x;
+        Pack<T, A, G> x;
         x.load(static_cast<const T*>(w) + at, n);
         x.widen(f);
         return;
@@ -185,16 +168,17 @@ __device__ __forceinline__ void load_weights(const void* w, bool wide, int64_t a
     const float* p = static_cast<const float*>(w) + at;
 #pragma unroll
     for (int i = 0; i < Pack<T, A>::H; i += 2) {
-        Pack<float, A> x;
-        float2 y[2] = {};
-        if (A || 2 * i < n) x.load(p + 2 * i, n - 2 * i), x.widen(y);
+        Pack<float, A, G> x;
+        float2 y[2];
+        x.load(p + 2 * i * Pack<T, A, G>::STEP, n - 2 * i * Pack<T, A, G>::STEP);
+        x.widen(y);
         f[i] = y[0], f[i + 1] = y[1];
     }
 }
-template <class T, bool A>
+template <class T, bool A, int G = 1>
 __device__ __forceinline__ void store_weights(void* out, bool wide, int64_t at, int n, const float2 (&f)[Pack<T, A>::H]) {
     if (!wide) {
-        Pack<T, A> x;
+        Pack<T, A, G> x;
         x.narrow(f);
         x.store(static_cast<T*>(out) + at, n);
         return;
@@ -202,10 +186,10 @@ __device__ __forceinline__ void store_weights(void* out, bool wide, int64_t at, 
     float* p = static_cast<float*>(out) + at;
 #pragma unroll
     for (int i = 0; i < Pack<T, A>::H; i += 2) {
-        Pack<float, A> x;
+        Pack<float, A, G> x;
         const float2 y[2] = {f[i], f[i + 1]};
         x.narrow(y);
-        x.store(p + 2 * i, n - 2 * i);
+        x.store(p + 2 * i * Pack<T, A, G>::STEP, n - 2 * i * Pack<T, A, G>::STEP);
     }
 }
 template <class T>
@@ -299,8 +283,9 @@ constexpr int grad_rows(int per) { return per == 1 ? 2 : 1; }
 // G threads a row, U rows of a group at a time.
 template <class T, bool A, int G, int PER, int U, int NT>
 __global__ void __launch_bounds__(NT, resident(NT, Pack<T, A>::V * PER * (U + 2))) norm_kernel(const __grid_constant__ NormParams p, int64_t chunk) {
-    using R = Ring<T, A, PER * U, NT>;
-    constexpr int V = Pack<T, A>::V, GROUPS = NT / G, STEP = G * V, H = V / 2;
+    using R = Ring<T, A, G, PER * U, NT>;
+    using P = Pack<T, A, G>;
+    constexpr int V = P::V, GROUPS = NT / G, STEP = G * V, H = V / 2;
     constexpr bool KEEP = NT <= 512;      // a run's weights stay in registers
     __shared__ float red[2 * NT / 32 * U];
     extern __shared__ __align__(16) unsigned char ring_memory[];
@@ -308,11 +293,11 @@ __global__ void __launch_bounds__(NT, resident(NT, Pack<T, A>::V * PER * (U + 2)
     const int t = threadIdx.x % G, g = threadIdx.x / G;
     const int64_t c0 = blockIdx.x * chunk;
     const int n = static_cast<int>(min(chunk, p.R - c0));                 // rows of the chunk
-    const int left = static_cast<int>(p.F) - t * V;                       // pack j is in the row where j STEP < left
+    const int left = static_cast<int>(p.F) - t * P::NEXT;                 // pack j is in the row where j STEP < left
     const float inv = 1.0f / static_cast<float>(p.F);
     const bool wide = p.weight_type == PT_F32;
     const int64_t next = GROUPS * p.ldx;                                  // from a group's row to its next one
-    const T* px = static_cast<const T*>(p.x) + (c0 + g) * p.ldx + t * V;
+    const T* px = static_cast<const T*>(p.x) + (c0 + g) * p.ldx + t * P::NEXT;
     const T* pf = px;
     auto fetch = [&](int i) {
 #pragma unroll
@@ -334,15 +319,15 @@ __global__ void __launch_bounds__(NT, resident(NT, Pack<T, A>::V * PER * (U + 2)
     auto read_weights = [&](int j, float2 (&w)[H], float2 (&b)[H]) {
 #pragma unroll
         for (int k = 0; k < H; ++k) w[k] = pair(1.0f), b[k] = pair(0.0f);
-        if (p.weight) load_weights<T, A>(p.weight, wide, at + j * STEP, left - j * STEP, w);
-        if (p.bias) load_weights<T, A>(p.bias, wide, at + j * STEP, left - j * STEP, b);
+        if (p.weight) load_weights<T, A, G>(p.weight, wide, at + j * STEP, left - j * STEP, w);
+        if (p.bias) load_weights<T, A, G>(p.bias, wide, at + j * STEP, left - j * STEP, b);
     };
     auto find_run = [&](int i) {
         const Run run = run_of(p, c0 + i, segment);
         segment = run.s;
         run_end = static_cast<int>(min(run.end - c0, int64_t(n)));
         used = run.s >= 0;
-        at = run.s * p.F + t * V;
+        at = run.s * p.F + t * P::NEXT;
         if constexpr (KEEP)
 #pragma unroll
             for (int j = 0; j < PER; ++j)
@@ -388,8 +373,8 @@ __global__ void __launch_bounds__(NT, resident(NT, Pack<T, A>::V * PER * (U + 2)
                 for (int i = 0; i < H; ++i) {
                     f[u][j][i] = __fadd2_rn(f[u][j][i], pair(-sum[u]));
                     if constexpr (!A) {
-                        if (2 * i >= left - j * STEP) f[u][j][i].x = 0.0f;
-                        if (2 * i + 1 >= left - j * STEP) f[u][j][i].y = 0.0f;
+                        if (2 * i * P::STEP >= left - j * STEP) f[u][j][i].x = 0.0f;
+                        if ((2 * i + 1) * P::STEP >= left - j * STEP) f[u][j][i].y = 0.0f;
                     }
                     all = __ffma2_rn(f[u][j][i], f[u][j][i], all);
                 }
@@ -408,7 +393,7 @@ __global__ void __launch_bounds__(NT, resident(NT, Pack<T, A>::V * PER * (U + 2)
                 if (p.mean) p.mean[r] = used ? sum[u] : 0.0f;
                 if (p.rstd) p.rstd[r] = used ? rstd : 0.0f;
             }
-            T* y = static_cast<T*>(p.out) + r * p.ldo + t * V;
+            T* y = static_cast<T*>(p.out) + r * p.ldo + t * P::NEXT;
 #pragma unroll
             for (int j = 0; j < PER; ++j) {
                 if (j * STEP >= left) continue;
@@ -421,7 +406,7 @@ __global__ void __launch_bounds__(NT, resident(NT, Pack<T, A>::V * PER * (U + 2)
                 }
 #pragma unroll
                 for (int k = 0; k < H; ++k) f[u][j][k] = used ? __ffma2_rn(__fmul2_rn(f[u][j][k], pair(rstd)), w[k], b[k]) : pair(0.0f);
-                Pack<T, A> o;
+                P o;
                 o.narrow(f[u][j]);
                 o.store(y + j * STEP, left - j * STEP);
             }
@@ -598,8 +583,9 @@ __device__ __forceinline__ void store_weight(void* out, int type, int64_t at, fl
 // run that has a row in it.
 template <class T, bool A, int G, int PER, int U, int NT>
 __global__ void __launch_bounds__(NT, resident(NT, Pack<T, A>::V * PER * (2 * U + 3))) norm_grad_kernel(const __grid_constant__ GradArgs a) {
-    using R = Ring<T, A, 2 * PER * U, NT>;
-    constexpr int V = Pack<T, A>::V, GROUPS = NT / G, STEP = G * V, WINDOW = GROUPS * U, H = V / 2;
+    using R = Ring<T, A, G, 2 * PER * U, NT>;
+    using P = Pack<T, A, G>;
+    constexpr int V = P::V, GROUPS = NT / G, STEP = G * V, WINDOW = GROUPS * U, H = V / 2;
     constexpr bool KEEP = NT <= 512;      // a run's weights stay in registers; a large block has none to spare and reads them again
     __shared__ float red[2 * NT / 32 * 2 * U];
     extern __shared__ __align__(16) unsigned char ring_memory[];
@@ -610,12 +596,12 @@ __global__ void __launch_bounds__(NT, resident(NT, Pack<T, A>::V * PER * (2 * U 
     const int t = threadIdx.x % G, g = threadIdx.x / G;
     const int64_t c0 = blockIdx.x * a.chunk;
     const int n = static_cast<int>(min(a.chunk, p.R - c0));
-    const int col0 = static_cast<int>(blockIdx.y) * a.tile, F = static_cast<int>(p.F), left = F - col0 - t * V;
+    const int col0 = static_cast<int>(blockIdx.y) * a.tile, F = static_cast<int>(p.F), left = F - col0 - t * P::NEXT;
     const float inv = 1.0f / static_cast<float>(p.F);
     const bool wide = p.weight_type == PT_F32, want_dx = p.out != nullptr, want_dw = p.dweight || p.dbias;
     const int64_t nextx = GROUPS * p.ldx, nexty = GROUPS * p.ldy;
-    const T* px = static_cast<const T*>(p.x) + (c0 + g) * p.ldx + col0 + t * V;
-    const T* pd = static_cast<const T*>(p.dy) + (c0 + g) * p.ldy + col0 + t * V;
+    const T* px = static_cast<const T*>(p.x) + (c0 + g) * p.ldx + col0 + t * P::NEXT;
+    const T* pd = static_cast<const T*>(p.dy) + (c0 + g) * p.ldy + col0 + t * P::NEXT;
     auto fetch = [&](int i) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -653,7 +639,7 @@ __global__ void __launch_bounds__(NT, resident(NT, Pack<T, A>::V * PER * (2 * U 
     float2 kept[KEEP ? PER : 1][H], dw[PER][H], db[PER][H];
     auto read_weights = [&](int j, float2 (&w)[H]) {
         if (p.weight && run.s >= 0 && j * STEP < left) {
-            load_weights<T, A>(p.weight, wide, run.s * p.F + col0 + t * V + j * STEP, left - j * STEP, w);
+            load_weights<T, A, G>(p.weight, wide, run.s * p.F + col0 + t * P::NEXT + j * STEP, left - j * STEP, w);
         } else {
 #pragma unroll
             for (int i = 0; i < H; ++i) w[i] = pair(1.0f);
@@ -692,7 +678,7 @@ __global__ void __launch_bounds__(NT, resident(NT, Pack<T, A>::V * PER * (2 * U 
     };
     fetch_stats(g);
     const int64_t nexto = GROUPS * p.ldo;
-    T* po = static_cast<T*>(p.out) + (c0 + g) * p.ldo + col0 + t * V;
+    T* po = static_cast<T*>(p.out) + (c0 + g) * p.ldo + col0 + t * P::NEXT;
     int turn = 0;
     for (int base = 0; base < n; base += WINDOW) {
         const int end = min(base + WINDOW, n);
@@ -777,7 +763,7 @@ __global__ void __launch_bounds__(NT, resident(NT, Pack<T, A>::V * PER * (2 * U 
 #pragma unroll
                     for (int j = 0; j < PER; ++j) {
                         if (!R::ASYNC && j * STEP >= left) continue;
-                        Pack<T, A> o;
+                        P o;
                         float2 w[H], z[H], dy[H], d[H];
                         weights_of(j, w);
                         values_of(u, j, z, dy);
@@ -794,7 +780,7 @@ __global__ void __launch_bounds__(NT, resident(NT, Pack<T, A>::V * PER * (2 * U 
             } else if (want_dx) {
                 // rows in no segment
                 const float2 none[H] = {};
-                Pack<T, A> zero;
+                P zero;
                 zero.narrow(none);
 #pragma unroll
                 for (int u = 0; u < U; ++u)
@@ -824,14 +810,14 @@ __global__ void __launch_bounds__(NT, resident(NT, Pack<T, A>::V * PER * (2 * U 
                 if constexpr (G == NT) {
 #pragma unroll
                     for (int j = 0; j < PER; ++j) {
-                        const int c = col0 + t * V + j * STEP;
+                        const int c = col0 + t * P::NEXT + j * STEP;
                         if (j * STEP >= left) continue;
                         if (whole) {
-                            if (p.dweight) store_weights<T, A>(p.dweight, wide, run.s * p.F + c, left - j * STEP, dw[j]);
-                            if (p.dbias) store_weights<T, A>(p.dbias, wide, run.s * p.F + c, left - j * STEP, db[j]);
+                            if (p.dweight) store_weights<T, A, G>(p.dweight, wide, run.s * p.F + c, left - j * STEP, dw[j]);
+                            if (p.dbias) store_weights<T, A, G>(p.dbias, wide, run.s * p.F + c, left - j * STEP, db[j]);
                         } else {
-                            store_weights<T, A>(slot_sums, true, c, left - j * STEP, dw[j]);
-                            store_weights<T, A>(slot_sums, true, p.F + c, left - j * STEP, db[j]);
+                            store_weights<T, A, G>(slot_sums, true, c, left - j * STEP, dw[j]);
+                            store_weights<T, A, G>(slot_sums, true, p.F + c, left - j * STEP, db[j]);
                         }
                     }
                 } else {
@@ -843,7 +829,7 @@ __global__ void __launch_bounds__(NT, resident(NT, Pack<T, A>::V * PER * (2 * U 
                         for (int j = 0; j < PER; ++j)
 #pragma unroll
                             for (int i = 0; i < V; ++i) {
-                                const int c = t * V + j * STEP + i;
+                                const int c = t * P::NEXT + j * STEP + i * P::STEP;
                                 if (c >= a.tile) continue;
                                 own[c] = i % 2 ? dw[j][i / 2].y : dw[j][i / 2].x;
                                 own[a.tile + c] = i % 2 ? db[j][i / 2].y : db[j][i / 2].x;
@@ -947,7 +933,7 @@ cudaError_t allow_smem(K* kernel, int bytes, int (&allowed)[64]) {
 
 template <class T, bool A, int G, int PER>
 cudaError_t launch_rows(const NormParams& p, const NormPlan& plan, cudaStream_t stream) {
-    constexpr int NT = G > 256 ? G : 256, U = NT <= 512 && PER * static_cast<int>(16 / sizeof(T)) <= ROW_VALUES ? ROWS : 1, smem = Ring<T, A, PER * U, NT>::BYTES;
+    constexpr int NT = G > 256 ? G : 256, U = NT <= 512 && PER * static_cast<int>(16 / sizeof(T)) <= ROW_VALUES ? ROWS : 1, smem = Ring<T, A, G, PER * U, NT>::BYTES;
     auto* kernel = norm_kernel<T, A, G, PER, U, NT>;
     static int allowed[64] = {};
     const cudaError_t e = allow_smem(kernel, smem, allowed);
@@ -960,7 +946,7 @@ template <class T, bool A, int G, int PER>
 cudaError_t launch_grad_rows(const GradArgs& a, const NormPlan& plan, cudaStream_t stream) {
     constexpr int NT = G > 256 ? G : 256, U = grad_rows(PER);
     auto* kernel = norm_grad_kernel<T, A, G, PER, U, NT>;
-    const int smem = Ring<T, A, 2 * PER * U, NT>::BYTES + (G < NT ? NT / std::max(G, 32) * 2 * a.tile * 4 : 0);
+    const int smem = Ring<T, A, G, 2 * PER * U, NT>::BYTES + (G < NT ? NT / std::max(G, 32) * 2 * a.tile * 4 : 0);
     static int allowed[64] = {};
     const cudaError_t e = allow_smem(kernel, smem, allowed);
     if (e != cudaSuccess) return e;
