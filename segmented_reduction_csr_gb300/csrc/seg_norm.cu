@@ -120,40 +120,129 @@ template <class T, bool A, int G = 1> struct Pack {
     }
 };
 
-// What a thread needs of its next rows, on its way to shared memory while it
-// works on these: a ring of D slots of PER packs for each thread, which copies
-// and reads nothing but its own, so that no barrier is needed.  (Rows that are
-// not aligned, or of which shared memory does not hold two, are loaded when they
-// are needed.)
-template <class T, bool A, int G, int PER, int NT>
-struct Ring {
-    static constexpr int D = PER == 1 ? 6 : PER <= 4 && NT == 256 ? 4 : PER == 2 ? 4 : PER <= 4 ? 3 : 2;      // fewer bytes of a slot want more of them
-    static constexpr bool ASYNC = A && D * PER * NT * 16 <= 200 * 1024;
-    static constexpr int SLOT = PER * NT * 16, BYTES = ASYNC ? D * SLOT : 0;
-    uint32_t base, at, to;      // the thread's first slot, the one to read and the one to fetch into
-    __device__ __forceinline__ explicit Ring(unsigned char* memory) : base(smem_u32(memory) + threadIdx.x * 16), at(base), to(base) {}
-    // pack j of a row
-    __device__ __forceinline__ void fetch(int j, const T* from) const {
-        if constexpr (ASYNC) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + j * NT * 16), "l"(from) : "memory");
-    }
+// The rows of a group's next windows, on their way to shared memory while it works
+// on these: a ring of D slots of ROWS rows of PER packs a thread.  (Those of which
+// shared memory does not hold two are loaded when they are needed.)
+template <int PACKS, int NT> constexpr int ring_slots() {      // fewer bytes of a slot want more of them
+    return PACKS == 1 ? 6 : PACKS <= 4 && NT == 256 ? 4 : PACKS == 2 ? 4 : PACKS <= 4 ? 3 : 2;
+}
+template <class T, bool A, int G, int PER, int ROWS, int NT, int ROW_BYTES>
+struct RingBase {
+    static constexpr int D = ring_slots<PER * ROWS, NT>(), SLOT = NT / G * ROWS * ROW_BYTES;
+    static constexpr bool ASYNC = D * SLOT <= 200 * 1024;
+    static constexpr int BYTES = ASYNC ? D * SLOT : 0;
+    uint32_t base, at, to;      // the first slot, the one to read and the one to fetch into
+    __device__ __forceinline__ explicit RingBase(uint32_t first) : base(first), at(first), to(first) {}
     __device__ __forceinline__ void fetched() {
         asm volatile("cp.async.commit_group;" ::: "memory");
         to = to == base + (D - 1) * SLOT ? base : to + SLOT;
     }
-    // the slot to read has landed
-    __device__ __forceinline__ void wait() const { asm volatile("cp.async.wait_group %0;" ::"n"(D - 2) : "memory"); }
-    __device__ __forceinline__ void get(int j, const T* from, int n, float2 (&f)[Pack<T, A>::H]) const {
-        Pack<T, A, G> x;
-        if constexpr (ASYNC) asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x.raw.x), "=r"(x.raw.y), "=r"(x.raw.z), "=r"(x.raw.w) : "r"(at + j * NT * 16) : "memory");
+    __device__ __forceinline__ void got() { at = at == base + (D - 1) * SLOT ? base : at + SLOT; }
+    __device__ __forceinline__ void landed() const { asm volatile("cp.async.wait_group %0;" ::"n"(D - 2) : "memory"); }
+};
+
+// Aligned rows: every thread copies and reads nothing but its own packs, so that no
+// barrier is needed.
+template <class T, bool A, int G, int PER, int ROWS, int NT>
+struct Ring : RingBase<T, A, G, PER, ROWS, NT, G * PER * 16> {
+    using B = RingBase<T, A, G, PER, ROWS, NT, G * PER * 16>;
+    __device__ __forceinline__ explicit Ring(unsigned char* memory) : B(smem_u32(memory) + threadIdx.x * 16) {}
+    // row q of the thread's, whose own part of it begins at `from`
+    __device__ __forceinline__ void fetch(int q, const T* from, int left, const void*) const {
+        if constexpr (B::ASYNC)
+#pragma unroll
+            for (int j = 0; j < PER; ++j)
+                if (j * G * Pack<T, A>::V < left)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(this->to + (q * PER + j) * NT * 16), "l"(from + j * G * Pack<T, A>::V) : "memory");
+    }
+    // the slot to read is there
+    __device__ __forceinline__ void wait() const { this->landed(); }
+    // pack j of row q, which memory has at `from`
+    __device__ __forceinline__ void get(int q, int j, const T* from, uint32_t, int n, float2 (&f)[Pack<T, A>::H]) const {
+        Pack<T, A> x;
+        if constexpr (B::ASYNC)
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x.raw.x), "=r"(x.raw.y), "=r"(x.raw.z), "=r"(x.raw.w) : "r"(this->at + (q * PER + j) * NT * 16) : "memory");
         else x.load(from, n);
         x.widen(f);
     }
     // packs that are never fetched read as zeros
-    __device__ __forceinline__ void clear(int j) const {
-        if constexpr (ASYNC)
-            for (int d = 0; d < D; ++d) asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(base + d * SLOT + j * NT * 16), "r"(0) : "memory");
+    __device__ __forceinline__ void clear(int q, int j) const {
+        if constexpr (B::ASYNC)
+            for (int d = 0; d < B::D; ++d)
+                asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(this->base + d * B::SLOT + (q * PER + j) * NT * 16), "r"(0) : "memory");
     }
-    __device__ __forceinline__ void got() { at = at == base + (D - 1) * SLOT ? base : at + SLOT; }
+};
+
+// Other rows: the aligned 16 bytes that a row lies in are copied, 16 each, and the
+// group's threads read the row's values from wherever it begins in them.
+template <class T, int G, int PER, int ROWS, int NT>
+struct Ring<T, false, G, PER, ROWS, NT> : RingBase<T, false, G, PER, ROWS, NT, (G * PER + 1) * 16> {
+    static constexpr int ROW_BYTES = (G * PER + 1) * 16, SIZE = sizeof(T);
+    using B = RingBase<T, false, G, PER, ROWS, NT, ROW_BYTES>;
+    using P = Pack<T, false, G>;
+    __device__ __forceinline__ explicit Ring(unsigned char* memory) : B(smem_u32(memory)) {}
+    static __device__ __forceinline__ uint32_t row_at(int q) { return (threadIdx.x / G * ROWS + q) * ROW_BYTES; }
+    // first: the tensor's first value.  Nothing before it or behind the row's last one is read.
+    __device__ __forceinline__ void fetch(int q, const T* from, int left, const void* first) const {
+        if constexpr (B::ASYNC) {
+            const int t = threadIdx.x % G;
+            const uintptr_t begin = reinterpret_cast<uintptr_t>(from - t), end = begin + min(left + t, G * PER * P::V) * SIZE;
+            const uintptr_t unit = (begin & ~uintptr_t(15)) + t * 16;
+#pragma unroll
+            for (int k = 0; k <= PER; ++k) {
+                const uintptr_t u = unit + k * G * 16;
+                if (u >= end || (k == PER && t > 0)) break;
+                const uint32_t dst = this->to + row_at(q) + t * 16 + k * G * 16;
+                if (u >= reinterpret_cast<uintptr_t>(first)) {
+                    const int bytes = end - u < 16 ? static_cast<int>(end - u) : 16;
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(u), "r"(bytes) : "memory");
+                } else {
+                    for (int i = static_cast<int>(begin - u); i < 16 && u + i < end; i += SIZE) {
+                        if constexpr (SIZE == 2) asm volatile("st.shared.u16 [%0], %1;" ::"r"(dst + i), "h"(__ldg(reinterpret_cast<const uint16_t*>(u + i))) : "memory");
+                        else asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst + i), "r"(__ldg(reinterpret_cast<const uint32_t*>(u + i))) : "memory");
+                    }
+                }
+            }
+        }
+    }
+    // (nor has a thread of the group anything left to read of the slot before)
+    __device__ __forceinline__ void wait() const {
+        this->landed();
+        if constexpr (G <= 32) __syncwarp();
+        else if constexpr (G == NT) __syncthreads();
+        else asm volatile("bar.sync %0, %1;" ::"r"(1 + int(threadIdx.x) / G), "n"(G) : "memory");
+    }
+    // low: the last bits of the address of the row's first value
+    __device__ __forceinline__ void get(int q, int j, const T* from, uint32_t low, int n, float2 (&f)[P::H]) const {
+        if constexpr (B::ASYNC) {
+            const uint32_t src = this->at + row_at(q) + (low & 15) + (threadIdx.x % G) * SIZE + j * G * 16;
+            float x[P::V];
+#pragma unroll
+            for (int i = 0; i < P::V; ++i) {
+                x[i] = 0.0f;
+                if (i * G < n) x[i] = value(src + i * G * SIZE);
+            }
+#pragma unroll
+            for (int k = 0; k < P::H; ++k) f[k] = make_float2(x[2 * k], x[2 * k + 1]);
+        } else {
+            P x;
+            x.load(from, n);
+            x.widen(f);
+        }
+    }
+    static __device__ __forceinline__ float value(uint32_t src) {
+        if constexpr (SIZE == 4) {
+            float v;
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(src) : "memory");
+            return v;
+        } else {
+            uint16_t v;
+            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(src) : "memory");
+            if constexpr (std::is_same<T, __nv_bfloat16>::value) return __uint_as_float(uint32_t(v) << 16);
+            else return __half2float(__ushort_as_half(v));
+        }
+    }
+    __device__ __forceinline__ void clear(int, int) const {}
 };
 
 // A pack of values of weight_type at element `at`, n of them from there on in the row.
@@ -283,7 +372,7 @@ constexpr int grad_rows(int per) { return per == 1 ? 2 : 1; }
 // G threads a row, U rows of a group at a time.
 template <class T, bool A, int G, int PER, int U, int NT>
 __global__ void __launch_bounds__(NT, resident(NT, Pack<T, A>::V * PER * (U + 2))) norm_kernel(const __grid_constant__ NormParams p, int64_t chunk) {
-    using R = Ring<T, A, G, PER * U, NT>;
+    using R = Ring<T, A, G, PER, U, NT>;
     using P = Pack<T, A, G>;
     constexpr int V = P::V, GROUPS = NT / G, STEP = G * V, H = V / 2;
     constexpr bool KEEP = NT <= 512;      // a run's weights stay in registers
@@ -299,13 +388,12 @@ __global__ void __launch_bounds__(NT, resident(NT, Pack<T, A>::V * PER * (U + 2)
     const int64_t next = GROUPS * p.ldx;                                  // from a group's row to its next one
     const T* px = static_cast<const T*>(p.x) + (c0 + g) * p.ldx + t * P::NEXT;
     const T* pf = px;
+    uint32_t low = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(px - t * P::NEXT));
+    const uint32_t low_next = static_cast<uint32_t>(next * sizeof(T));
     auto fetch = [&](int i) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (i + u * GROUPS < n)
-#pragma unroll
-                for (int j = 0; j < PER; ++j)
-                    if (j * STEP < left) ring.fetch(u * PER + j, pf + j * STEP);
+            if (i + u * GROUPS < n) ring.fetch(u, pf, left, p.x);
             pf += next;
         }
         ring.fetched();
@@ -345,7 +433,7 @@ __global__ void __launch_bounds__(NT, resident(NT, Pack<T, A>::V * PER * (U + 2)
 #pragma unroll
             for (int j = 0; j < PER; ++j) {
                 if (in && j * STEP < left) {
-                    ring.get(u * PER + j, px + u * next + j * STEP, left - j * STEP, f[u][j]);
+                    ring.get(u, j, px + u * next + j * STEP, low + u * low_next, left - j * STEP, f[u][j]);
 #pragma unroll
                     for (int i = 0; i < H; ++i) all = __fadd2_rn(all, f[u][j][i]);
                 } else {
@@ -357,6 +445,7 @@ __global__ void __launch_bounds__(NT, resident(NT, Pack<T, A>::V * PER * (U + 2)
         }
         if (R::ASYNC) {
             ring.got();
+            low += U * low_next;
             fetch(base + (R::D - 1) * GROUPS * U + g);
         } else {
             px += U * next;
@@ -583,7 +672,7 @@ __device__ __forceinline__ void store_weight(void* out, int type, int64_t at, fl
 // run that has a row in it.
 template <class T, bool A, int G, int PER, int U, int NT>
 __global__ void __launch_bounds__(NT, resident(NT, Pack<T, A>::V * PER * (2 * U + 3))) norm_grad_kernel(const __grid_constant__ GradArgs a) {
-    using R = Ring<T, A, G, 2 * PER * U, NT>;
+    using R = Ring<T, A, G, PER, 2 * U, NT>;
     using P = Pack<T, A, G>;
     constexpr int V = P::V, GROUPS = NT / G, STEP = G * V, WINDOW = GROUPS * U, H = V / 2;
     constexpr bool KEEP = NT <= 512;      // a run's weights stay in registers; a large block has none to spare and reads them again
@@ -602,16 +691,13 @@ __global__ void __launch_bounds__(NT, resident(NT, Pack<T, A>::V * PER * (2 * U 
     const int64_t nextx = GROUPS * p.ldx, nexty = GROUPS * p.ldy;
     const T* px = static_cast<const T*>(p.x) + (c0 + g) * p.ldx + col0 + t * P::NEXT;
     const T* pd = static_cast<const T*>(p.dy) + (c0 + g) * p.ldy + col0 + t * P::NEXT;
+    auto low_bits = [](const T* row) { return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row)); };
+    uint32_t lowx = low_bits(px - t * P::NEXT), lowy = low_bits(pd - t * P::NEXT);
+    const uint32_t lowx_next = static_cast<uint32_t>(nextx * sizeof(T)), lowy_next = static_cast<uint32_t>(nexty * sizeof(T));
     auto fetch = [&](int i) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (i + u * GROUPS < n)
-#pragma unroll
-                for (int j = 0; j < PER; ++j)
-                    if (j * STEP < left) {
-                        ring.fetch((u * PER + j) * 2, px + j * STEP);
-                        ring.fetch((u * PER + j) * 2 + 1, pd + j * STEP);
-                    }
+            if (i + u * GROUPS < n) ring.fetch(2 * u, px, left, p.x), ring.fetch(2 * u + 1, pd, left, p.dy);
             px += nextx;
             pd += nexty;
         }
@@ -621,7 +707,7 @@ __global__ void __launch_bounds__(NT, resident(NT, Pack<T, A>::V * PER * (2 * U 
 #pragma unroll
         for (int j = 0; j < PER; ++j)
             if (j * STEP >= left)
-                for (int u = 0; u < U; ++u) ring.clear((u * PER + j) * 2), ring.clear((u * PER + j) * 2 + 1);
+                for (int u = 0; u < U; ++u) ring.clear(2 * u, j), ring.clear(2 * u + 1, j);
         for (int d = 0; d < R::D - 1; ++d) fetch(d * WINDOW + g);
     }
     if (want_dw && p.offsets) {
@@ -686,8 +772,8 @@ __global__ void __launch_bounds__(NT, resident(NT, Pack<T, A>::V * PER * (2 * U 
         float mean[U], rstd[U];
         if (R::ASYNC) ring.wait();
         auto read_values = [&](int u, int j, float2 (&z)[H], float2 (&dy)[H]) {
-            ring.get((u * PER + j) * 2, px + u * nextx + j * STEP, left - j * STEP, z);
-            ring.get((u * PER + j) * 2 + 1, pd + u * nexty + j * STEP, left - j * STEP, dy);
+            ring.get(2 * u, j, px + u * nextx + j * STEP, lowx + u * lowx_next, left - j * STEP, z);
+            ring.get(2 * u + 1, j, pd + u * nexty + j * STEP, lowy + u * lowy_next, left - j * STEP, dy);
 #pragma unroll
             for (int i = 0; i < H; ++i) z[i] = __fmul2_rn(__fadd2_rn(z[i], pair(-mean[u])), pair(rstd[u]));
         };
@@ -702,6 +788,8 @@ __global__ void __launch_bounds__(NT, resident(NT, Pack<T, A>::V * PER * (2 * U 
         auto values_read = [&] {
             if (R::ASYNC) {
                 ring.got();
+                lowx += U * lowx_next;
+                lowy += U * lowy_next;
                 fetch(base + (R::D - 1) * WINDOW + g);
             } else {
                 px += U * nextx;
@@ -933,7 +1021,7 @@ cudaError_t allow_smem(K* kernel, int bytes, int (&allowed)[64]) {
 
 template <class T, bool A, int G, int PER>
 cudaError_t launch_rows(const NormParams& p, const NormPlan& plan, cudaStream_t stream) {
-    constexpr int NT = G > 256 ? G : 256, U = NT <= 512 && PER * static_cast<int>(16 / sizeof(T)) <= ROW_VALUES ? ROWS : 1, smem = Ring<T, A, G, PER * U, NT>::BYTES;
+    constexpr int NT = G > 256 ? G : 256, U = NT <= 512 && PER * static_cast<int>(16 / sizeof(T)) <= ROW_VALUES ? ROWS : 1, smem = Ring<T, A, G, PER, U, NT>::BYTES;
     auto* kernel = norm_kernel<T, A, G, PER, U, NT>;
     static int allowed[64] = {};
     const cudaError_t e = allow_smem(kernel, smem, allowed);
@@ -946,7 +1034,7 @@ template <class T, bool A, int G, int PER>
 cudaError_t launch_grad_rows(const GradArgs& a, const NormPlan& plan, cudaStream_t stream) {
     constexpr int NT = G > 256 ? G : 256, U = grad_rows(PER);
     auto* kernel = norm_grad_kernel<T, A, G, PER, U, NT>;
-    const int smem = Ring<T, A, G, 2 * PER * U, NT>::BYTES + (G < NT ? NT / std::max(G, 32) * 2 * a.tile * 4 : 0);
+    const int smem = Ring<T, A, G, PER, 2 * U, NT>::BYTES + (G < NT ? NT / std::max(G, 32) * 2 * a.tile * 4 : 0);
     static int allowed[64] = {};
     const cudaError_t e = allow_smem(kernel, smem, allowed);
     if (e != cudaSuccess) return e;
