@@ -1052,23 +1052,22 @@ cudaError_t with_shape(const NormPlan& plan, F f) {
     constexpr int MOST = ROW_VALUES * sizeof(T) / 16;
 #define SEG_NORM_SHAPE(a, g, n) \
     if (plan.aligned == a && plan.group == g && plan.per == n) return f(Shape<a, g, n>())
-    SEG_NORM_SHAPE(true, 8, 1);
-    if constexpr (MOST == 4) SEG_NORM_SHAPE(true, 8, 2);
-    SEG_NORM_SHAPE(true, 8, MOST);
-    SEG_NORM_SHAPE(true, 16, MOST);
-    SEG_NORM_SHAPE(true, 32, MOST);
-    SEG_NORM_SHAPE(true, 64, MOST);
-    SEG_NORM_SHAPE(true, 128, MOST);
     SEG_NORM_SHAPE(true, 256, 1);
-    SEG_NORM_SHAPE(true, 256, MOST);
-    SEG_NORM_SHAPE(true, 512, MOST);
-    SEG_NORM_SHAPE(true, 512, 2 * MOST);      // forward
-    SEG_NORM_SHAPE(true, 1024, MOST);
-    SEG_NORM_SHAPE(false, 8, MOST);
-    SEG_NORM_SHAPE(false, 32, MOST);
-    SEG_NORM_SHAPE(false, 128, MOST);
-    SEG_NORM_SHAPE(false, 512, MOST);
-    SEG_NORM_SHAPE(false, 1024, MOST);
+#define SEG_NORM_SHAPES(a)                    \
+    SEG_NORM_SHAPE(a, 8, 1);                  \
+    SEG_NORM_SHAPE(a, 8, MOST);               \
+    SEG_NORM_SHAPE(a, 16, MOST);              \
+    SEG_NORM_SHAPE(a, 32, MOST);              \
+    SEG_NORM_SHAPE(a, 64, MOST);              \
+    SEG_NORM_SHAPE(a, 128, MOST);             \
+    SEG_NORM_SHAPE(a, 256, MOST);             \
+    SEG_NORM_SHAPE(a, 512, MOST);             \
+    SEG_NORM_SHAPE(a, 512, 2 * MOST);         \
+    SEG_NORM_SHAPE(a, 1024, MOST);            \
+    if constexpr (MOST == 4) SEG_NORM_SHAPE(a, 8, 2)
+    SEG_NORM_SHAPES(true);
+    SEG_NORM_SHAPES(false);
+#undef SEG_NORM_SHAPES
 #undef SEG_NORM_SHAPE
     return cudaErrorInvalidConfiguration;
 }
@@ -1120,20 +1119,20 @@ NormPlan plan_norm(bool grad, const NormParams& p) {
     const int most = ROW_VALUES / v;
     // as few threads for a row as hold it; where there are few rows, a block's, so
     // that each is over sooner
-    if (vec && p.R <= p.sms && loads > 32) {
+    if (p.R <= p.sms && loads > 32) {
         d.group = loads <= 256 * most ? 256 : loads <= 512 * most ? 512 : 1024;
     } else {
         d.group = 8;
-        while (d.group < 1024 && int64_t(d.group) * most < loads) d.group *= vec || d.group == 512 ? 2 : 4;
+        while (d.group < 1024 && int64_t(d.group) * most < loads) d.group *= 2;
     }
     // forward, as many again of a thread: 5,000 x 9,000 bfloat16 43 us, by 1,024
     // threads, which have no registers for the weights, 82
-    const bool twice = !grad && vec && d.group == 1024 && loads <= 1024 * most;
+    const bool twice = !grad && d.group == 1024 && loads <= 1024 * most;
     if (twice) d.group = 512;
     d.threads = std::max(d.group, 256);
     const int64_t per = ceil_to(loads, d.group);
     d.per = twice ? 2 * most : most;
-    if (vec && d.group == 8 && per <= 2) d.per = static_cast<int32_t>(per);
+    if (d.group == 8 && per <= 2) d.per = static_cast<int32_t>(per);
     if (vec && d.group == 256 && per == 1) d.per = 1;
     // Wide rows, forward: from shared memory, or read again.  (Rows that are not
     // aligned, 5,000 x 9,001 bfloat16, by 1,024 threads 192 us, read again 114.)
