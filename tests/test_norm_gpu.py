@@ -192,6 +192,53 @@ def test_many_rows(dtype, f):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("f", (1, 5, 33, 50, 65, 130, 333, 700, 1501, 3001, 5001, 9001, 16001, 16385))
+@pytest.mark.parametrize("many", (False, True))
+def test_rows_that_begin_anywhere(dtype, f, many):
+    """x, dy and out each with a beginning and a stride of its own, NaN all around; one to some rows a block."""
+    torch, sr = mods()
+    g = torch.Generator(device="cuda")
+    g.manual_seed(f)
+    lens = [0, 4, 1, 60, 0, 0, 33, 1] if not many else [700, 0, 1, 2, 150, 3 if f > 4000 else 4000, 11]
+    off = 3 + np.concatenate([[0], np.cumsum(lens)]).astype(np.int64)
+    rows = int(off[-1]) + 2
+    do = torch.from_numpy(off).cuda()
+
+    def within(first, stride, fill):
+        flat = torch.full((first + rows * stride + 9,), fill, dtype=getattr(torch, dtype), device="cuda")
+        return flat, flat.as_strided((rows, f), (stride, 1), first)
+    x, dy = within(1, f + 2, float("nan"))[1], within(3, f + 1, float("nan"))[1]
+    x[3:-2], dy[3:-2] = normal(g, (rows - 5, f), dtype) + 0.5, normal(g, (rows - 5, f), dtype)
+    flat, out = within(5, f + 3, 7.0)
+    w, b = weights(g, len(lens), f, "float32" if f % 3 else dtype)
+    got = sr.seg_layer_norm(x, w, b, do, with_stats=True, out=out)
+    check_forward(got, x, w, b, off, 1e-5, (dtype, f))
+    edges = flat.clone()
+    edges.as_strided((rows, f), (f + 3, 1), 5).fill_(7.0)
+    assert bool((edges == 7).all())
+    grads = sr.seg_layer_norm_grad(x, dy, *got[1:], w, do)
+    check_grad(grads, x, dy, *got[1:], w, off, (dtype, f))
+    assert all(torch.equal(p, q) for p, q in zip(grads, sr.seg_layer_norm_grad(x, dy, *got[1:], w, do)))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("f", (7, 48, 1000))
+@pytest.mark.parametrize("rows,segments", ((30, 58), (1, 1000), (5, 3000), (64, 2), (200, 150), (3, 1)))
+def test_few_rows_in_many_segments(dtype, f, rows, segments):
+    torch, sr = mods()
+    rng = np.random.default_rng(rows)
+    off = np.concatenate([[0], np.sort(rng.integers(0, rows + 1, segments - 1)), [rows]]).astype(np.int64)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(f)
+    x, dy = normal(g, (rows, f), dtype), normal(g, (rows, f), dtype)
+    w, b = weights(g, segments, f, dtype)
+    do = torch.from_numpy(off).cuda()
+    got = sr.seg_layer_norm(x, w, b, do, with_stats=True)
+    check_forward(got, x, w, b, off, 1e-5, (dtype, f))
+    check_grad(sr.seg_layer_norm_grad(x, dy, *got[1:], w, do), x, dy, *got[1:], w, off, (dtype, f))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 def test_strides_alignment_and_what_is_left_out(dtype):
     torch, sr = mods()
     off, rows, do, g = case("mixed", 6)
