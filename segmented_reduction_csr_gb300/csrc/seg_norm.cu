@@ -693,7 +693,7 @@ __global__ void __launch_bounds__(NT, resident(NT, Pack<T, A>::V * PER * (2 * U 
     using R = Ring<T, A, G, PER, 2 * U, NT>;
     using P = Pack<T, A, G>;
     constexpr int V = P::V, GROUPS = NT / G, STEP = G * V, WINDOW = GROUPS * U, H = V / 2;
-    constexpr bool KEEP = NT <= 512;      // a run's weights stay in registers; a large block has none to spare and reads them again
+    constexpr bool KEEP = NT <= 512 && PER * V <= ROW_VALUES;      // a run's weights stay in registers; a large block has none to spare and reads them again
     __shared__ float red[2 * NT / 32 * 2 * U];
     extern __shared__ __align__(16) unsigned char ring_memory[];
     float* const shared_sums = reinterpret_cast<float*>(ring_memory + R::BYTES);      // [groups of at least a warp][2][tile]
@@ -1108,7 +1108,8 @@ cudaError_t launch_grad_type(const GradArgs& a, const NormPlan& plan, cudaStream
         if (e != cudaSuccess) return e;
     }
     return with_shape<T>(plan, [&](auto s) {
-        if constexpr (s.per * static_cast<int>(16 / sizeof(T)) > ROW_VALUES) return cudaErrorInvalidConfiguration;
+        constexpr bool twice = s.per * static_cast<int>(16 / sizeof(T)) > ROW_VALUES;
+        if constexpr (twice && (sizeof(T) == 4 || !s.aligned)) return cudaErrorInvalidConfiguration;
         else return launch_grad_rows<T, s.aligned, s.group, s.per>(a, plan, stream);
     });
 }
@@ -1134,8 +1135,10 @@ NormPlan plan_norm(bool grad, const NormParams& p) {
         while (d.group < 1024 && int64_t(d.group) * most < loads) d.group *= 2;
     }
     // forward, as many again of a thread: 5,000 x 9,000 bfloat16 43 us, by 1,024
-    // threads, which have no registers for the weights, 82
-    const bool twice = !grad && d.group == 1024 && loads <= 1024 * most;
+    // threads, which have no registers for the weights, 82.  Backward, aligned 16-bit
+    // rows alone: 5,000 x 12,288 bfloat16 124 us, by 1,024 threads 137; float32, whose
+    // ring does not hold two rows, 235 and 179; 5,000 x 9,001 bfloat16 288 and 237.
+    const bool twice = d.group == 1024 && loads <= 1024 * most && (!grad || (vec && size == 2));
     if (twice) d.group = 512;
     d.threads = std::max(d.group, 256);
     const int64_t per = ceil_to(loads, d.group);
