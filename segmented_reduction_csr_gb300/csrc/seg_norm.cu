@@ -899,8 +899,9 @@ __global__ void __launch_bounds__(NT, resident(NT, Pack<T, A>::V * PER * (2 * U 
                 float* slot_sums = a.partials + (2 * int64_t(blockIdx.x) + (run.begin >= c0 ? 1 : 0)) * 2 * p.F;
                 auto put = [&](int which, int c, float v) {
                     void* out = which ? p.dbias : p.dweight;
+                    if (!out) return;
                     if (!whole) slot_sums[which * p.F + c] = v;
-                    else if (out) store_weight(out, p.weight_type, run.s * p.F + c, v);
+                    else store_weight(out, p.weight_type, run.s * p.F + c, v);
                 };
                 if constexpr (G == NT) {
 #pragma unroll
@@ -911,8 +912,8 @@ __global__ void __launch_bounds__(NT, resident(NT, Pack<T, A>::V * PER * (2 * U 
                             if (p.dweight) store_weights<T, A, G>(p.dweight, wide, run.s * p.F + c, left - j * STEP, dw[j]);
                             if (p.dbias) store_weights<T, A, G>(p.dbias, wide, run.s * p.F + c, left - j * STEP, db[j]);
                         } else {
-                            store_weights<T, A, G>(slot_sums, true, c, left - j * STEP, dw[j]);
-                            store_weights<T, A, G>(slot_sums, true, p.F + c, left - j * STEP, db[j]);
+                            if (p.dweight) store_weights<T, A, G>(slot_sums, true, c, left - j * STEP, dw[j]);
+                            if (p.dbias) store_weights<T, A, G>(slot_sums, true, p.F + c, left - j * STEP, db[j]);
                         }
                     }
                 } else {
@@ -955,7 +956,7 @@ __global__ void __launch_bounds__(NT, resident(NT, Pack<T, A>::V * PER * (2 * U 
 
 // Adds the parts of a segment that more than one chunk has rows of: blockIdx.x
 // names the segment, or (by_start) the chunk in which it starts; blockIdx.y the
-// first `lanes` x V of the 2 F sums.  Each of the block's ADD_THREADS / lanes rows
+// first `lanes` x V of the sums that are wanted.  Each of the block's ADD_THREADS / lanes rows
 // of threads adds an equal share of the parts in order, then theirs are added.
 constexpr int ADD_THREADS = 512;
 template <int V>
@@ -979,12 +980,13 @@ __global__ void __launch_bounds__(ADD_THREADS) norm_add_kernel(const __grid_cons
     const int lane = threadIdx.x % lanes, share = threadIdx.x / lanes, shares = ADD_THREADS / lanes;
     const int parts = static_cast<int>(last - first + 1), each = (parts + shares - 1) / shares;
     const int q0 = share * each, q1 = min(q0 + each, parts);
-    for (int64_t i0 = int64_t(blockIdx.y) * lanes * V; i0 < 2 * p.F; i0 += int64_t(gridDim.y) * lanes * V) {
+    const int64_t i_end = p.dbias ? 2 * p.F : p.F;
+    for (int64_t i0 = (p.dweight ? 0 : p.F) + int64_t(blockIdx.y) * lanes * V; i0 < i_end; i0 += int64_t(gridDim.y) * lanes * V) {
         const int64_t i = i0 + lane * V;
         float v[V];
 #pragma unroll
         for (int k = 0; k < V; ++k) v[k] = 0.0f;
-        if (i < 2 * p.F) {
+        if (i < i_end) {
 #pragma unroll 8
             for (int q = q0; q < q1; ++q) {
                 const float* from = a.partials + (2 * (first + q) + (q == 0 ? 1 : 0)) * 2 * p.F + i;
@@ -1001,11 +1003,11 @@ __global__ void __launch_bounds__(ADD_THREADS) norm_add_kernel(const __grid_cons
         __syncthreads();
         for (int k = threadIdx.x; k < lanes * V; k += ADD_THREADS) {
             const int64_t c = i0 + k;
-            if (c >= 2 * p.F) break;
+            if (c >= i_end) break;
             float total = 0.0f;
             for (int q = 0; q < shares; ++q) total += sums[k % V][q * lanes + k / V];
             void* out = c < p.F ? p.dweight : p.dbias;
-            if (out) store_weight(out, p.weight_type, s * p.F + (c < p.F ? c : c - p.F), total);
+            store_weight(out, p.weight_type, s * p.F + (c < p.F ? c : c - p.F), total);
         }
         __syncthreads();
     }
@@ -1198,12 +1200,12 @@ cudaError_t launch_norm_grad(const NormParams& p, const NormPlan& plan, cudaStre
     // with one share, 67 so)
     int shares = 4;
     while (shares < 32 && (plan.chunks / p.S + 1) / (shares * 2) >= 4) shares *= 2;
-    const int lanes = ADD_THREADS / shares, v = p.F % 2 == 0 ? 4 : 1;
+    const int lanes = ADD_THREADS / shares, v = p.F % 4 == 0 || (p.F % 2 == 0 && p.dweight && p.dbias) ? 4 : 1;      // (four sums of one kind, or of both)
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(by_start ? plan.chunks - 1 : p.S), static_cast<unsigned>(std::min<int64_t>(ceil_to(2 * p.F, lanes * v), 16384)));
+    cfg.gridDim = dim3(static_cast<unsigned>(by_start ? plan.chunks - 1 : p.S), static_cast<unsigned>(std::min<int64_t>(ceil_to(p.dweight && p.dbias ? 2 * p.F : p.F, lanes * v), 16384)));
     cfg.blockDim = dim3(ADD_THREADS);
     cfg.stream = stream;
     cfg.attrs = &attr;
