@@ -363,10 +363,15 @@ __device__ __forceinline__ void group_sum(float (&v)[N], float* red, int& turn) 
 // Blocks of an SM, by the values that a thread holds of rows and weights.
 constexpr int resident(int threads, int values) { return threads > 256 ? 1 : values > 48 ? 2 : values > 24 ? 3 : 4; }
 // Values of a row that a thread has, and rows at a time: the forward pass takes
-// two, whose sums' chains overlap. The backward pass has sums to keep as well: two
-// where a thread has one pack of a row (1,000,000 rows of 64 bfloat16 columns 91.7
-// -> 81.7 us, of 32 83.6 -> 69.3 us), else one.
-constexpr int ROW_VALUES = 16, ROWS = 2;
+// two, whose sums' chains overlap, of 16 values each; one of 32; and one of 16-bit
+// values that are not aligned, with three blocks an SM for two (200,000 x 333
+// bfloat16 92 -> 86 us; float32 97 -> 93, but 50,000 x 1,001 68 -> 73).  The backward
+// pass has sums to keep as well: two where a thread has one pack of a row
+// (1,000,000 rows of 64 bfloat16 columns 91.7 -> 81.7 us, of 32 83.6 -> 69.3), else one.
+constexpr int ROW_VALUES = 16;
+constexpr int forward_rows(bool aligned, int size, int threads, int per) {
+    return threads > 512 || per * (16 / size) > ROW_VALUES || (!aligned && size == 2 && threads == 256) ? 1 : 2;
+}
 constexpr int grad_rows(int per) { return per == 1 ? 2 : 1; }
 
 // G threads a row, U rows of a group at a time.
@@ -1031,7 +1036,7 @@ cudaError_t allow_smem(K* kernel, int bytes, int (&allowed)[64]) {
 
 template <class T, bool A, int G, int PER>
 cudaError_t launch_rows(const NormParams& p, const NormPlan& plan, cudaStream_t stream) {
-    constexpr int NT = G > 256 ? G : 256, U = NT <= 512 && PER * static_cast<int>(16 / sizeof(T)) <= ROW_VALUES ? ROWS : 1, smem = Ring<T, A, G, PER, U, NT>::BYTES;
+    constexpr int NT = G > 256 ? G : 256, U = forward_rows(A, sizeof(T), NT, PER), smem = Ring<T, A, G, PER, U, NT>::BYTES;
     auto* kernel = norm_kernel<T, A, G, PER, U, NT>;
     static int allowed[64] = {};
     const cudaError_t e = allow_smem(kernel, smem, allowed);
@@ -1160,7 +1165,7 @@ NormPlan plan_norm(bool grad, const NormParams& p) {
             d.sums_bytes = ceil_to(p.R * 8, 256) * 256;
         }
     }
-    const int rows = grad ? grad_rows(d.per) : d.threads <= 512 && !twice ? ROWS : 1;
+    const int rows = grad ? grad_rows(d.per) : forward_rows(vec, size, d.threads, d.per);
     const int64_t window = d.per == 0 ? 1 : d.threads / d.group * rows;
     const int64_t most_blocks = from_ring ? int64_t(p.sms) * (ring <= 108 * 1024 ? 2 : 1)
                                 : d.per == 0 ? int64_t(p.sms) * 8
