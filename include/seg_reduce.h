@@ -594,7 +594,8 @@ seg_status_t seg_gated_grad(const void *pre, seg_dtype_t pre_dtype, int64_t num_
  *   mean, rstd    device, [num_rows] float32, or NULL: kept for the backward pass.
  *
  * Every pointer is aligned to its element; 16-byte aligned ones, with F and the
- * strides multiples of 16 bytes, are read 16 bytes at a time.  Sums are float32
+ * strides multiples of 16 bytes, are read 16 bytes at a time; of other rows up to
+ * 14 bytes before each but the first may be read and are not used.  Sums are float32
  * in an order that the sizes and alignments give, the squares those of the
  * differences from the mean (which pass float32's range above 1e19); the result
  * is rounded once.  A row that holds an infinity or NaN gives NaN in that row
