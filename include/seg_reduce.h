@@ -598,8 +598,9 @@ seg_status_t seg_gated_grad(const void *pre, seg_dtype_t pre_dtype, int64_t num_
  * 14 bytes before each but the first may be read and are not used.  Sums are float32
  * in an order that the sizes and alignments give, the squares those of the
  * differences from the mean (which pass float32's range above 1e19); the result
- * is rounded once.  A row that holds an infinity or NaN gives NaN in that row
- * alone.  Enqueues one kernel, uses no scratch and returns without synchronising.
+ * is rounded once.  out may be x, with its stride.  A row that holds an infinity
+ * or NaN gives NaN in that row alone.  Enqueues one kernel, uses no scratch and
+ * returns without synchronising.
  */
 seg_status_t seg_layer_norm(const void *x, seg_dtype_t dtype, int64_t num_rows, int64_t F, int64_t ldx,
                             const void *weight, const void *bias, seg_dtype_t weight_dtype, const void *offsets,

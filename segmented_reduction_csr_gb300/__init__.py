@@ -1051,9 +1051,9 @@ def seg_layer_norm(x, weight=None, bias=None, offsets=None, eps: float = 1e-5, w
     ``offsets`` ``[S+1]`` (int64 or uint32), or ``[F]`` for all rows without;
     both contiguous, of one type: ``x``'s or float32; ``None``: 1 and 0.
     Returns ``out``, with ``with_stats`` ``(out, mean, rstd)`` (float32 ``[R]``,
-    for ``seg_layer_norm_grad``).  Computed in float32 and rounded once.  It
-    records no gradient (``segment_layer_norm`` does).  ``stream`` and graphs as
-    for ``seg_matmul``; not synchronised."""
+    for ``seg_layer_norm_grad``).  Computed in float32 and rounded once; ``out``
+    may be ``x``.  It records no gradient (``segment_layer_norm`` does).
+    ``stream`` and graphs as for ``seg_matmul``; not synchronised."""
     ldx, code, wcode, s, odt = _norm_arguments(x, weight, bias, offsets)
     if not 0.0 <= eps < float("inf"):
         raise ValueError("eps must be finite and not negative")

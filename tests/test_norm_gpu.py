@@ -222,6 +222,19 @@ def test_rows_that_begin_anywhere(dtype, f, many):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("f", (64, 65, 1000, 2001, 9001, 12288, 20000, 20001))
+def test_in_place(dtype, f):
+    """A row is read before it is written, whatever its neighbours' threads do meanwhile."""
+    torch, sr = mods()
+    g = torch.Generator(device="cuda")
+    g.manual_seed(f)
+    x = normal(g, (1200 if f > 4000 else 9000, f), dtype)
+    w, b = weights(g, None, f, dtype)
+    want = sr.seg_layer_norm(x, w, b)
+    assert sr.seg_layer_norm(x, w, b, out=x) is x and torch.equal(x, want)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("f", (7, 48, 1000))
 @pytest.mark.parametrize("rows,segments", ((30, 58), (1, 1000), (5, 3000), (64, 2), (200, 150), (3, 1)))
 def test_few_rows_in_many_segments(dtype, f, rows, segments):
