@@ -599,8 +599,9 @@ seg_status_t seg_gated_grad(const void *pre, seg_dtype_t pre_dtype, int64_t num_
  * in an order that the sizes and alignments give, the squares those of the
  * differences from the mean (which pass float32's range above 1e19); a mean of
  * more than half the row's deviation is corrected by the mean of the differences,
- * so that a row of equal values gives the bias.  The result is rounded once.  out may be x, with its stride.  A row that holds an infinity
- * or NaN gives NaN in that row alone.  Enqueues one kernel, uses no scratch and
+ * so that a row of equal values gives the bias to float32's rounding.  The result
+ * is rounded once.  out may be x, with its stride.  A row that holds an infinity or
+ * NaN gives NaN in that row alone.  Enqueues one kernel, uses no scratch and
  * returns without synchronising.
  */
 seg_status_t seg_layer_norm(const void *x, seg_dtype_t dtype, int64_t num_rows, int64_t F, int64_t ldx,
@@ -629,7 +630,7 @@ seg_status_t seg_layer_norm(const void *x, seg_dtype_t dtype, int64_t num_rows, 
  * result is rounded once.  Rows in no segment may hold anything.  Scratch is
  * that of the products: 16 F bytes for each of at most 4 blocks per SM, and 8
  * bytes a row for rows that a block's registers do not hold.  Enqueues one
- * kernel to three.
+ * kernel to four.
  */
 seg_status_t seg_layer_norm_grad(const void *x, seg_dtype_t dtype, int64_t num_rows, int64_t F, int64_t ldx,
                                  const void *dy, int64_t ldy, const float *mean, const float *rstd,

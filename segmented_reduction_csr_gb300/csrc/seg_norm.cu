@@ -710,6 +710,7 @@ __global__ void __launch_bounds__(256) norm_long_kernel(const __grid_constant__ 
 struct GradArgs {
     NormParams p;
     int32_t tile;               // columns of a tile
+    int32_t clear;              // segments without rows are cleared at a block's end
     int64_t chunk;
     float* sums;                // [R][2]: sum(g), sum(g z) of each row, or NULL: a block has all columns
     float* partials;            // [2 chunks][2][F]: the first and last run of a chunk
@@ -746,6 +747,11 @@ __device__ __forceinline__ void store_weight(void* out, int type, int64_t at, fl
     else static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(v);
 }
 
+// Which of the segments s, one of each lane of a warp, are below `end` and have no rows.
+__device__ __forceinline__ uint32_t without_rows(const NormParams& p, int64_t s, int64_t end) {
+    return __ballot_sync(0xffffffffu, s < end && offset_at(p, min(s, p.S)) >= offset_at(p, min(s + 1, p.S)));
+}
+
 // The sums of segments without rows, columns c0 to c1: a warp looks at 32 segments
 // at once.  (At a block's end: before its rows this cost them registers, 5,000 x
 // 9,001 float32 187 -> 304 us.)
@@ -754,11 +760,41 @@ __device__ __forceinline__ void clear_empty(const NormParams& p, int c0, int c1)
     const int lane = threadIdx.x & 31;
     for (int64_t s0 = blockIdx.x * each + (threadIdx.x & ~31); s0 < s1; s0 += blockDim.x) {
         const int64_t s = s0 + lane;
-        for (uint32_t none = __ballot_sync(0xffffffffu, s < s1 && offset_at(p, min(s, p.S)) >= offset_at(p, min(s + 1, p.S))); none; none &= none - 1) {
+        for (uint32_t none = without_rows(p, s, s1); none; none &= none - 1) {
             const int64_t at = (s0 + __ffs(none) - 1) * p.F;
             for (int c = c0 + lane; c < c1; c += 32) {
                 if (p.dweight) store_weight(p.dweight, p.weight_type, at + c, 0.0f);
                 if (p.dbias) store_weight(p.dbias, p.weight_type, at + c, 0.0f);
+            }
+        }
+    }
+}
+
+// The same where the blocks that the rows need are few for the sums that may have
+// to be cleared (see plan_norm): a warp takes 32 segments and CLEAR_COLUMNS
+// columns at a time, 16 bytes a lane where the sums are whole units of those.
+// Segments next to one another with all their columns are one piece.
+constexpr int CLEAR_COLUMNS = 512;
+__global__ void __launch_bounds__(256) norm_clear_kernel(const __grid_constant__ NormParams p, int size, int whole) {
+    const int lane = threadIdx.x & 31;
+    const int64_t across = (p.F + CLEAR_COLUMNS - 1) / CLEAR_COLUMNS, tiles = (p.S + 31) / 32 * across;
+    for (int64_t i = blockIdx.x * int64_t(8) + threadIdx.x / 32; i < tiles; i += gridDim.x * int64_t(8)) {
+        const int64_t s0 = i / across * 32, c0 = i % across * CLEAR_COLUMNS, c1 = min(c0 + CLEAR_COLUMNS, p.F);
+        uint32_t none = without_rows(p, s0 + lane, p.S);
+        while (none) {
+            const int at = __ffs(none) - 1, others = across > 1 ? 0 : __ffs(~(none >> at)) - 2;     // segments after the first one
+            const int n = others == -2 ? 32 - at : others + 1;
+            none &= n == 32 ? 0 : ~(((1u << n) - 1) << at);
+            const int64_t begin = ((s0 + at) * p.F + c0) * size, end = ((s0 + at + n - 1) * p.F + c1) * size;
+            for (void* sums : {p.dweight, p.dbias}) {
+                if (!sums) continue;
+                char* to = static_cast<char*>(sums);
+                if (whole)
+                    for (int64_t b = begin + lane * 16; b < end; b += 512) *reinterpret_cast<uint4*>(to + b) = make_uint4(0, 0, 0, 0);
+                else if (size == 4)
+                    for (int64_t b = begin + lane * 4; b < end; b += 128) *reinterpret_cast<float*>(to + b) = 0.0f;
+                else
+                    for (int64_t b = begin + lane * 2; b < end; b += 64) *reinterpret_cast<uint16_t*>(to + b) = 0;
             }
         }
     }
@@ -1030,7 +1066,7 @@ __global__ void __launch_bounds__(NT, resident(NT, Pack<T, A>::V * PER * (2 * U 
         po += U * nexto;
         if constexpr (!KEEP) values_read();
     }
-    if (want_dw && p.offsets) clear_empty(p, col0, min(col0 + a.tile, F));
+    if (a.clear) clear_empty(p, col0, min(col0 + a.tile, F));
 }
 
 // Adds the parts of a segment that more than one chunk has rows of: blockIdx.x
@@ -1091,6 +1127,13 @@ __global__ void __launch_bounds__(ADD_THREADS) norm_add_kernel(const __grid_cons
         __syncthreads();
     }
 }
+
+// Bytes of sums that a block of the backward pass may have to clear; above, a
+// kernel of its own does (one row in 200 segments of 16,384 float32 columns, 26 MB:
+// 408 us by the row's block, 31 so; 10 rows in 1,000,000 of 64, 512 MB: 5,750 and
+// 102; one in 20 of 1,000, 160 KB: 16.4 and 14.4; two in 8 of 4,096, 128 KB a block:
+// 14.9 and 16.4, one more launch).
+constexpr int64_t CLEAR_SHARE = 64 * 1024;
 
 int64_t ceil_to(int64_t n, int64_t d) { return (n + d - 1) / d; }
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
@@ -1252,6 +1295,13 @@ NormPlan plan_norm(bool grad, const NormParams& p) {
     d.chunks = ceil_to(p.R, d.chunk);
     if (d.per == 0 && !from_ring) d.chunks = std::min<int64_t>(p.R, most_blocks);
     if (grad) d.partial_bytes = ceil_to(d.chunks * 4 * p.F * 4, 256) * 256;
+    // Each of the blocks that the rows need clears its share of the segments without
+    // rows, whose sums may be nearly all that there is to store.
+    if (grad && p.offsets) {
+        const int64_t bytes = p.S * p.F * (p.weight_type == PT_F32 ? 4 : 2) * ((p.dweight ? 1 : 0) + (p.dbias ? 1 : 0));
+        if (bytes > d.chunks * d.tiles * CLEAR_SHARE)
+            d.clear_blocks = static_cast<int32_t>(std::min<int64_t>(ceil_to(ceil_to(p.S, 32) * ceil_to(p.F, CLEAR_COLUMNS), 8), int64_t(p.sms) * 8));
+    }
     return d;
 }
 
@@ -1266,9 +1316,16 @@ cudaError_t launch_norm_grad(const NormParams& p, const NormPlan& plan, cudaStre
     a.p = p;
     a.tile = static_cast<int32_t>(std::min<int64_t>(p.F, int64_t(plan.group) * plan.per * (p.type == PT_F32 ? 4 : 8)));
     a.chunk = plan.chunk;
+    a.clear = p.offsets && (p.dweight || p.dbias) && plan.clear_blocks == 0;
     a.sums = plan.sums_bytes > 0 ? reinterpret_cast<float*>(p.ws) : nullptr;
     a.partials = reinterpret_cast<float*>(p.ws + plan.sums_bytes);
     cudaError_t e;
+    if (plan.clear_blocks > 0) {
+        const int size = p.weight_type == PT_F32 ? 4 : 2;
+        norm_clear_kernel<<<static_cast<unsigned>(plan.clear_blocks), 256, 0, stream>>>(p, size, p.F * size % 16 == 0 && aligned16(p.dweight) && aligned16(p.dbias));
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
     if (p.type == PT_F32) e = launch_grad_type<float>(a, plan, stream);
     else if (p.type == PT_F16) e = launch_grad_type<__half>(a, plan, stream);
     else e = launch_grad_type<__nv_bfloat16>(a, plan, stream);

@@ -39,6 +39,7 @@ struct NormPlan {
     int32_t threads;        // of a block
     int64_t chunk, chunks;  // rows of a block; blocks
     int32_t tiles;          // backward: tiles of columns, each with blocks of its own
+    int32_t clear_blocks;   // backward: blocks of the kernel that clears the sums of segments without rows (0: the others do)
     int64_t sums_bytes, partial_bytes;     // the workspace, in this order
     int64_t bytes() const { return sums_bytes + partial_bytes; }
 };
