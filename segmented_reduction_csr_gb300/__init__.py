@@ -974,10 +974,11 @@ def seg_gated_grad(x, w, pre, dy, offsets, activation: str = "silu", transpose_w
 def segment_gated(x, w, indptr, activation: str = "silu", transpose_w: bool = False):
     """Differentiable ``seg_gated``: its backward pass is ``seg_gated_grad``,
     for the gradients of ``x`` and ``w`` that are asked for.  The two products
-    are kept for it in float32.  Differentiable once; no forward mode and
-    no vmap.  (As with any PyTorch operator, a backward pass is captured into a
+    are kept for it in float32, unless gradients are off (``torch.no_grad``).
+    Differentiable once; no forward mode and no vmap.  (As with any PyTorch operator, a backward pass is captured into a
     graph only where no eager graph of the same leaves is alive.)"""
-    return _segment_gated_function().apply(x, w, indptr, activation, transpose_w)
+    # (the grad mode: within forward it is always off, and needs_input_grad does not know it)
+    return _segment_gated_function().apply(x, w, indptr, activation, transpose_w, _torch().is_grad_enabled())
 
 
 _segment_gated_fn = None
@@ -990,9 +991,9 @@ def _segment_gated_function():
 
         class SegmentGated(torch.autograd.Function):
             @staticmethod
-            def forward(ctx, x, w, indptr, activation, transpose_w):
+            def forward(ctx, x, w, indptr, activation, transpose_w, with_grad):
                 ctx.how = activation, transpose_w
-                if not (ctx.needs_input_grad[0] or ctx.needs_input_grad[1]):
+                if not (with_grad and (ctx.needs_input_grad[0] or ctx.needs_input_grad[1])):
                     return seg_gated(x, w, indptr, activation, transpose_w)
                 out, pre = seg_gated(x, w, indptr, activation, transpose_w, with_pre=True)
                 ctx.save_for_backward(x, w, indptr, pre)
@@ -1004,7 +1005,7 @@ def _segment_gated_function():
                 x, w, indptr, pre = ctx.saved_tensors
                 dx, dw = seg_gated_grad(x, w, pre, dy.contiguous(), indptr, *ctx.how, want_dx=ctx.needs_input_grad[0],
                                         want_dw=ctx.needs_input_grad[1])
-                return dx, dw, None, None, None
+                return dx, dw, None, None, None, None
 
         _segment_gated_fn = SegmentGated
     return _segment_gated_fn
@@ -1114,7 +1115,7 @@ def segment_layer_norm(x, weight=None, bias=None, indptr=None, eps: float = 1e-5
     ``seg_layer_norm_grad``, for the gradients that are asked for.
     Differentiable once; no forward mode and no vmap.  (Captured as
     ``segment_gated`` is.)"""
-    return _segment_layer_norm_function().apply(x, weight, bias, indptr, eps)
+    return _segment_layer_norm_function().apply(x, weight, bias, indptr, eps, _torch().is_grad_enabled())
 
 
 _segment_layer_norm_fn = None
@@ -1127,8 +1128,8 @@ def _segment_layer_norm_function():
 
         class SegmentLayerNorm(torch.autograd.Function):
             @staticmethod
-            def forward(ctx, x, weight, bias, indptr, eps):
-                if not any(ctx.needs_input_grad[:3]):
+            def forward(ctx, x, weight, bias, indptr, eps, with_grad):
+                if not (with_grad and any(ctx.needs_input_grad[:3])):
                     return seg_layer_norm(x, weight, bias, indptr, eps)
                 out, mean, rstd = seg_layer_norm(x, weight, bias, indptr, eps, with_stats=True)
                 # (without a weight, the bias names the type of the gradients)
@@ -1143,7 +1144,7 @@ def _segment_layer_norm_function():
                 need = ctx.needs_input_grad
                 dx, dweight, dbias = seg_layer_norm_grad(x, dy.contiguous(), mean, rstd, weight, indptr, with_dx=need[0],
                                                          with_weight=need[1], with_bias=need[2], weight_dtype=ctx.wtype)
-                return dx, dweight, dbias, None, None
+                return dx, dweight, dbias, None, None, None
 
         _segment_layer_norm_fn = SegmentLayerNorm
     return _segment_layer_norm_fn
