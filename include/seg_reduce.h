@@ -628,9 +628,9 @@ seg_status_t seg_layer_norm(const void *x, seg_dtype_t dtype, int64_t num_rows, 
  * Sums are float32 in an order that is a pure function of the sizes, the
  * alignments, the offsets and the SM count, so calls repeat bit for bit; each
  * result is rounded once.  Rows in no segment may hold anything.  Scratch is
- * that of the products: 16 F bytes for each of at most 4 blocks per SM, and 8
- * bytes a row for rows that a block's registers do not hold.  Enqueues one
- * kernel to four.
+ * that of the products: 16 F bytes for each of at most 4 blocks per SM where
+ * dweight or dbias is wanted, and where dx is, 8 bytes a row for rows that a
+ * block's registers do not hold.  Enqueues one kernel to four.
  */
 seg_status_t seg_layer_norm_grad(const void *x, seg_dtype_t dtype, int64_t num_rows, int64_t F, int64_t ldx,
                                  const void *dy, int64_t ldy, const float *mean, const float *rstd,

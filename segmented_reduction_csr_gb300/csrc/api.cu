@@ -1222,7 +1222,7 @@ seg_status_t seg_layer_norm_grad(const void* x, seg_dtype_t dtype, int64_t num_r
         p.sms = ds->sm_count;
         const NormPlan plan = plan_norm(true, p);
         Scratch* sc = nullptr;
-        st = product_scratch(dev, stream, static_cast<size_t>(plan.bytes()), &sc);
+        st = product_scratch(dev, stream, static_cast<size_t>(plan.sums_for(p) + plan.parts_for(p)), &sc);
         if (st != SEG_OK) return st;
         p.ws = static_cast<unsigned char*>(sc->ptr);
         if (launch_norm_grad(p, plan, stream) != cudaSuccess) {

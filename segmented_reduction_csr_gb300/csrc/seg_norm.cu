@@ -712,7 +712,7 @@ struct GradArgs {
     int32_t tile;               // columns of a tile
     int32_t clear;              // segments without rows are cleared at a block's end
     int64_t chunk;
-    float* sums;                // [R][2]: sum(g), sum(g z) of each row, or NULL: a block has all columns
+    float* sums;                // [R][2]: sum(g), sum(g z) of each row, or NULL: a block has all columns, or dx is not wanted
     float* partials;            // [2 chunks][2][F]: the first and last run of a chunk
 };
 
@@ -1317,8 +1317,8 @@ cudaError_t launch_norm_grad(const NormParams& p, const NormPlan& plan, cudaStre
     a.tile = static_cast<int32_t>(std::min<int64_t>(p.F, int64_t(plan.group) * plan.per * (p.type == PT_F32 ? 4 : 8)));
     a.chunk = plan.chunk;
     a.clear = p.offsets && (p.dweight || p.dbias) && plan.clear_blocks == 0;
-    a.sums = plan.sums_bytes > 0 ? reinterpret_cast<float*>(p.ws) : nullptr;
-    a.partials = reinterpret_cast<float*>(p.ws + plan.sums_bytes);
+    a.sums = plan.sums_for(p) > 0 ? reinterpret_cast<float*>(p.ws) : nullptr;
+    a.partials = reinterpret_cast<float*>(p.ws + plan.sums_for(p));
     cudaError_t e;
     if (plan.clear_blocks > 0) {
         const int size = p.weight_type == PT_F32 ? 4 : 2;

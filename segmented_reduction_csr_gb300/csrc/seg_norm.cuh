@@ -40,8 +40,10 @@ struct NormPlan {
     int64_t chunk, chunks;  // rows of a block; blocks
     int32_t tiles;          // backward: tiles of columns, each with blocks of its own
     int32_t clear_blocks;   // backward: blocks of the kernel that clears the sums of segments without rows (0: the others do)
-    int64_t sums_bytes, partial_bytes;     // the workspace, in this order
-    int64_t bytes() const { return sums_bytes + partial_bytes; }
+    int64_t sums_bytes, partial_bytes;     // each row's two sums, where tiles share them; the parts of the column sums
+    // The workspace of a call, in this order: the rows' sums are for dx, the parts for the others.
+    int64_t sums_for(const NormParams& p) const { return p.out ? sums_bytes : 0; }
+    int64_t parts_for(const NormParams& p) const { return p.dweight || p.dbias ? partial_bytes : 0; }
 };
 
 NormPlan plan_norm(bool grad, const NormParams& p);
