@@ -1066,7 +1066,7 @@ __global__ void __launch_bounds__(NT, resident(NT, Pack<T, A>::V * PER * (2 * U 
         po += U * nexto;
         if constexpr (!KEEP) values_read();
     }
-    if (a.clear) clear_empty(p, col0, min(col0 + a.tile, F));
+    if (want_dw && a.clear) clear_empty(p, col0, min(col0 + a.tile, F));
 }
 
 // Adds the parts of a segment that more than one chunk has rows of: blockIdx.x
