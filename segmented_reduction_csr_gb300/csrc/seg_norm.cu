@@ -394,7 +394,7 @@ constexpr int resident(int threads, int values) { return threads > 256 ? 1 : val
 // (1,000,000 rows of 64 bfloat16 columns 91.7 -> 81.7 us, of 32 83.6 -> 69.3), else one.
 constexpr int ROW_VALUES = 16;
 constexpr int forward_rows(bool aligned, int size, int threads, int per) {
-    return threads > 512 || per * (16 / size) > ROW_VALUES || (!aligned && size == 2 && threads == 256) ? 1 : 2;
+    return per * (16 / size) > ROW_VALUES || (!aligned && size == 2 && threads == 256) ? 1 : 2;
 }
 constexpr int grad_rows(int per) { return per == 1 ? 2 : 1; }
 
@@ -404,7 +404,7 @@ __global__ void __launch_bounds__(NT, resident(NT, Pack<T, A>::V * PER * (U + 2)
     using R = Ring<T, A, G, PER, U, NT>;
     using P = Pack<T, A, G>;
     constexpr int V = P::V, GROUPS = NT / G, STEP = G * V, H = V / 2;
-    constexpr bool KEEP = NT <= 512;      // a run's weights stay in registers
+    static_assert(NT <= 512 && R::ASYNC, "a run's weights stay in registers, the next rows are on their way to shared memory");
     __shared__ float red[2 * NT / 32 * U];
     extern __shared__ __align__(16) unsigned char ring_memory[];
     R ring(ring_memory);
@@ -415,9 +415,8 @@ __global__ void __launch_bounds__(NT, resident(NT, Pack<T, A>::V * PER * (U + 2)
     const float inv = 1.0f / static_cast<float>(p.F);
     const bool wide = p.weight_type == PT_F32;
     const int64_t next = GROUPS * p.ldx;                                  // from a group's row to its next one
-    const T* px = static_cast<const T*>(p.x) + (c0 + g) * p.ldx + t * P::NEXT;
-    const T* pf = px;
-    uint32_t low = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(px - t * P::NEXT));
+    const T* pf = static_cast<const T*>(p.x) + (c0 + g) * p.ldx + t * P::NEXT;
+    uint32_t low = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(pf - t * P::NEXT));
     const uint32_t low_next = static_cast<uint32_t>(next * sizeof(T));
     auto fetch = [&](int i) {
 #pragma unroll
@@ -427,12 +426,11 @@ __global__ void __launch_bounds__(NT, resident(NT, Pack<T, A>::V * PER * (U + 2)
         }
         ring.fetched();
     };
-    if (R::ASYNC)
-        for (int d = 0; d < R::D - 1; ++d) fetch(d * GROUPS * U + g);
+    for (int d = 0; d < R::D - 1; ++d) fetch(d * GROUPS * U + g);
     int turn = 0, run_end = 0;      // of the chunk's rows
     int64_t at = 0, segment = -1;
     bool used = false;
-    float2 kept_w[KEEP ? PER : 1][H], kept_b[KEEP ? PER : 1][H];
+    float2 kept_w[PER][H], kept_b[PER][H];
     auto read_weights = [&](int j, float2 (&w)[H], float2 (&b)[H]) {
 #pragma unroll
         for (int k = 0; k < H; ++k) w[k] = pair(1.0f), b[k] = pair(0.0f);
@@ -445,16 +443,15 @@ __global__ void __launch_bounds__(NT, resident(NT, Pack<T, A>::V * PER * (U + 2)
         run_end = static_cast<int>(min(run.end - c0, int64_t(n)));
         used = run.s >= 0;
         at = run.s * p.F + t * P::NEXT;
-        if constexpr (KEEP)
 #pragma unroll
-            for (int j = 0; j < PER; ++j)
-                if (used && j * STEP < left) read_weights(j, kept_w[j], kept_b[j]);
+        for (int j = 0; j < PER; ++j)
+            if (used && j * STEP < left) read_weights(j, kept_w[j], kept_b[j]);
     };
     if (g < n) find_run(g);        // while the first rows are on their way
     for (int base = 0; base < n; base += GROUPS * U) {
         float2 f[U][PER][H];
         float sum[U], sq[U];
-        if (R::ASYNC) ring.wait();
+        ring.wait();
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const bool in = base + u * GROUPS + g < n;
@@ -462,7 +459,7 @@ __global__ void __launch_bounds__(NT, resident(NT, Pack<T, A>::V * PER * (U + 2)
 #pragma unroll
             for (int j = 0; j < PER; ++j) {
                 if (in && j * STEP < left) {
-                    ring.get(u, j, px + u * next + j * STEP, low + u * low_next, left - j * STEP, f[u][j]);
+                    ring.get(u, j, nullptr, low + u * low_next, left - j * STEP, f[u][j]);
 #pragma unroll
                     for (int i = 0; i < H; ++i) all = __fadd2_rn(all, f[u][j][i]);
                 } else {
@@ -472,13 +469,9 @@ __global__ void __launch_bounds__(NT, resident(NT, Pack<T, A>::V * PER * (U + 2)
             }
             sum[u] = all.x + all.y;
         }
-        if (R::ASYNC) {
-            ring.got();
-            low += U * low_next;
-            fetch(base + (R::D - 1) * GROUPS * U + g);
-        } else {
-            px += U * next;
-        }
+        ring.got();
+        low += U * low_next;
+        fetch(base + (R::D - 1) * GROUPS * U + g);
         group_sum<G, NT, U>(sum, red, turn);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -548,15 +541,8 @@ __global__ void __launch_bounds__(NT, resident(NT, Pack<T, A>::V * PER * (U + 2)
 #pragma unroll
             for (int j = 0; j < PER; ++j) {
                 if (j * STEP >= left) continue;
-                float2 w[H], b[H];
-                if constexpr (KEEP) {
 #pragma unroll
-                    for (int k = 0; k < H; ++k) w[k] = kept_w[j][k], b[k] = kept_b[j][k];
-                } else if (used) {
-                    read_weights(j, w, b);
-                }
-#pragma unroll
-                for (int k = 0; k < H; ++k) f[u][j][k] = used ? __ffma2_rn(__fmul2_rn(f[u][j][k], pair(rstd)), w[k], b[k]) : pair(0.0f);
+                for (int k = 0; k < H; ++k) f[u][j][k] = used ? __ffma2_rn(__fmul2_rn(f[u][j][k], pair(rstd)), kept_w[j][k], kept_b[j][k]) : pair(0.0f);
                 P o;
                 o.narrow(f[u][j]);
                 o.store(y + j * STEP, left - j * STEP);
