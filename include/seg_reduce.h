@@ -540,7 +540,11 @@ seg_status_t seg_lora(const void *x, seg_dtype_t dtype, int64_t num_rows, int64_
  *                 backward pass.
  *
  * g and u are summed as seg_matmul's sums are and reach the activation in
- * float32; out and pre are each rounded once.  Alignment as for seg_matmul.
+ * float32; out and pre are each rounded once.  The activation, float32's too, is
+ * off by at most 4 + 1.2 |g| (silu, sigmoid), 4 + 4.2 |q| (gelu_tanh, q = sqrt(8 /
+ * pi) (g + 0.044715 g^3)) or 23 + 0.85 g^2 (gelu) units of 2^-23 of itself, and may
+ * be 0 below 2^-121; float32's is off by less (see seg_gated_grad) where the
+ * products are not gated as they are summed (below).  Alignment as for seg_matmul.
  * Scratch is that of the products; num_rows * 2 N float32 values of it where
  * the products are not gated as they are summed (the sums are long, or no
  * copies of odd matrices are made).
@@ -566,7 +570,10 @@ seg_status_t seg_gated(const void *x, seg_dtype_t dtype, int64_t num_rows, int64
  *   dpre          device, [num_rows, 2 N], rows ldd elements apart, of `dtype`.
  *   dtype, pre_dtype, num_rows, N, activation: as for seg_gated.
  *
- * Computed in float32 and rounded once.  act' of relu is 0 at 0.
+ * Computed in float32 and rounded once: for float32 results act(g) is off by at most
+ * 3.5 (silu, sigmoid), 3.5 + 3 |q| (gelu_tanh) or 6 + 1.1 g^2 (gelu) units of 2^-23
+ * of itself, act'(g) by 8 + 3 |q| (gelu: 6 + 1.1 g^2) of its terms' sizes.  act' of
+ * relu is 0 at 0.
  */
 seg_status_t seg_gated_grad(const void *pre, seg_dtype_t pre_dtype, int64_t num_rows, int64_t N, int64_t ldp,
                             const void *dy, seg_dtype_t dtype, int64_t ldy, seg_activation_t activation, void *dpre, int64_t ldd,

@@ -5,8 +5,8 @@
 namespace segred {
 
 // s(x) = 1 / (1 + exp(-x)) and s(-x) = 1 - s(x), from exp(-|x|) so that neither
-// overflows nor cancels.  FAST: the special function unit's exp2 and division,
-// off by 2 + 1.2 |x| units of 2^-23.
+// overflows nor cancels.  FAST: the special function unit's exponential, off by 2 +
+// 1.2 |x| units of 2^-23, and quotient, off by 2; else 3 units in all.
 template <bool FAST>
 __device__ __forceinline__ void logistic(float x, float& s, float& other) {
     const float e = FAST ? __expf(-fabsf(x)) : expf(-fabsf(x));
@@ -18,8 +18,11 @@ __device__ __forceinline__ void logistic(float x, float& s, float& other) {
 
 // The normal distribution below -|x|, as exp(-x^2 / 2) t poly(t), t = 1 / (1 + 0.33
 // |x| / sqrt(2)): the form of Hastings (Approximations for Digital Computers,
-// 1955), its coefficients fitted to the whole tail at once (the largest relative
-// error is 1e-7; erfcf took twice the instructions).  e: exp(-x^2 / 2).
+// 1955), its coefficients fitted to the whole tail at once (the fit's largest
+// relative error is 1.2e-7 in exact arithmetic; erfcf took twice the instructions).
+// In float32, in units of 2^-23: the exponential 2 + 1.7 x^2 / 2 with its argument's
+// rounding, t 3, which t poly(t) passes on 3.5 times, the polynomial's roundings 3,
+// its fit 1, the products 2: below 23 + 0.85 x^2.  e: exp(-x^2 / 2).
 __device__ __forceinline__ float normal_tail(float x, float& e) {
     e = __expf(-0.5f * x * x);
     const float t = __fdividef(1.0f, fmaf(0.23334524f, fabsf(x), 1.0f));
@@ -41,6 +44,9 @@ __device__ __forceinline__ float normal_tail(float x, float& e) {
 //                                                                  q = sqrt(8 / pi) (x + 0.044715 x^3)
 //   relu      max(x, 0)                 1 where x > 0, else 0
 //   sigmoid   s                         s (1 - s)
+// Off by, in units of 2^-23 at most (exponents by their own roundings too: 3 |q| for
+// gelu_tanh): FAST silu, sigmoid 4 + 1.2 |x|, gelu_tanh 4 + 4.2 |q|, gelu 23 + 0.85
+// x^2, and results below 2^-121 may be 0; else 3.5, 3.5 + 3 |q| and 6 + 1.1 x^2.
 template <bool FAST, bool SLOPE>
 __device__ __forceinline__ float activate(int kind, float x, float& slope) {
     if (kind == ACT_RELU) {

@@ -473,10 +473,11 @@ __device__ __forceinline__ void store_any(void* out, int type, int64_t at, int64
 }
 
 // f[i] = act(g(i)) * u(i), with the kind of activation outside of the loop, by
-// the special function unit for float32 too: off by 2 + 1.2 |g| units of 2^-23,
-// where the products are by up to 2^-20 of their terms' sizes, and the drain warps'
-// time is what bounds a float32 tile (expf and a division: 1,000,000 x 64 times 64
-// x 64 twice 262 us, so 166).
+// the special function unit for float32 too: off by 4 + 1.2 |g| (silu, sigmoid), 4 +
+// 4.2 |q| (gelu_tanh's q) or 23 + 0.85 g^2 (gelu) units of 2^-23 at most (see
+// seg_act.cuh), where the products are by up to 2^-20 of their terms' sizes, and the
+// drain warps' time is what bounds a float32 tile (expf and a division: 1,000,000 x
+// 64 times 64 x 64 twice 262 us, so 166).
 template <int W, class G, class U>
 __device__ __forceinline__ void gate(int kind, float (&f)[W], G g, U u) {
     auto all = [&](auto k) {
