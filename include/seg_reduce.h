@@ -591,7 +591,7 @@ seg_status_t seg_gated_grad(const void *pre, seg_dtype_t pre_dtype, int64_t num_
  *   dtype         SEG_F32, SEG_F16 or SEG_BF16: the type of x and out.
  *   num_rows      0 <= R <= 2^31 - 4096.
  *   F             0 <= F <= SEG_MAX_PRODUCT_COLUMNS; R == 0 or F == 0 launches
- *                 nothing.
+ *                 nothing (mean and rstd stay as they are).
  *   weight, bias  device, [num_segments, F], contiguous, of weight_dtype
  *                 (`dtype` or SEG_F32); NULL: 1, and 0.
  *   offsets, offsets_dtype, num_segments: as for seg_matmul; or offsets NULL and

@@ -1052,8 +1052,8 @@ def seg_layer_norm(x, weight=None, bias=None, offsets=None, eps: float = 1e-5, w
     ``offsets`` ``[S+1]`` (int64 or uint32), or ``[F]`` for all rows without;
     both contiguous, of one type: ``x``'s or float32; ``None``: 1 and 0.
     Returns ``out``, with ``with_stats`` ``(out, mean, rstd)`` (float32 ``[R]``,
-    for ``seg_layer_norm_grad``).  Computed in float32 and rounded once; ``out``
-    may be ``x``.  It records no gradient (``segment_layer_norm`` does).
+    for ``seg_layer_norm_grad``; 0 for rows without columns).  Computed in
+    float32 and rounded once; ``out`` may be ``x``.  It records no gradient (``segment_layer_norm`` does).
     ``stream`` and graphs as for ``seg_matmul``; not synchronised."""
     ldx, code, wcode, s, odt = _norm_arguments(x, weight, bias, offsets)
     if not 0.0 <= eps < float("inf"):
@@ -1064,6 +1064,10 @@ def seg_layer_norm(x, weight=None, bias=None, offsets=None, eps: float = 1e-5, w
     if with_stats:
         device, f32 = x.device, _torch_module.float32
         mean, rstd = _new(r, f32, device, stream), _new(r, f32, device, stream)
+        if f == 0:
+            # (no kernel has anything to do)
+            with _torch_module.cuda.stream(stream):
+                mean.zero_(), rstd.zero_()
     _enqueue("seg_layer_norm", x.device, stream, load_library().seg_layer_norm, x.data_ptr(), code, r, f, ldx, _ptr(weight), _ptr(bias),
              wcode, _ptr(offsets), odt, s, eps, out.data_ptr(), ldo, _ptr(mean), _ptr(rstd))
     if stream is not None:
