@@ -902,9 +902,12 @@ def seg_gated(x, w, offsets, activation: str = "silu", transpose_w: bool = False
     ``with_pre`` (or a ``pre`` to write to) ``(out, pre)``, ``pre`` ``[R, 2 N]``
     the two products for ``seg_gated_grad``: float32, which the gradients are
     exact to, or, in a ``pre`` of ``x``'s type, half of that memory.  The
-    products are float32 up to the result, which is rounded once.  It records
-    no gradient (``segment_gated`` does).  Float32 infinities, ``stream`` and
-    graphs as for ``seg_matmul``; not synchronised."""
+    products are float32 up to the result, which is rounded once.  Float32 sums
+    of more than 512 terms and 16-bit ones of more than 32,768, unless few rows
+    have them split, and odd matrices most of which are in no use, go through
+    ``pre`` or ``R * 2 N`` float32 values of scratch, which the library keeps
+    for the stream.  It records no gradient (``segment_gated`` does).  Float32
+    infinities, ``stream`` and graphs as for ``seg_matmul``; not synchronised."""
     torch = _torch()
     ldx = _check_rows("x", x, offsets)
     code, s, (r, k) = _product_code(x), offsets.shape[0] - 1, x.shape

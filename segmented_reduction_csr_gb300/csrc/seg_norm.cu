@@ -10,10 +10,10 @@
 // their way while others are added up.  16 values of a row per thread, its
 // weights in registers over a run of rows of one segment, two values an
 // instruction, and a ring of rows in shared memory that every thread fills and
-// reads for itself.  32,768 x 2,048 bfloat16, float32 weights: forward 41 us = 6.5
+// reads for itself.  32,768 x 2,048 bfloat16, float32 weights: forward 42 us = 6.4
 // TB/s (a warp or two a row, weights from L1 for each row, value by value: 84),
-// backward 72 us = 5.6 TB/s (122).  1,000,000 x 64 float32 in 50 segments: 89 us =
-// 5.8 TB/s and 126 us = 6.1 TB/s.
+// backward 72 to 74 us = 5.5 TB/s (122), 77 with the kernel that adds the parts.
+// 1,000,000 x 64 float32 in 50 segments: 91 us = 5.6 TB/s and 126 us = 6.1 TB/s.
 //
 // Backward: a block has a chunk of neighbouring rows and takes the runs of rows
 // of one segment in it one after the other.  A thread keeps its columns' sums
@@ -176,7 +176,7 @@ struct Ring : RingBase<T, A, G, PER, ROWS, NT, G * PER * 16> {
 
 // Other rows: the aligned 16 bytes that a row lies in are copied, 16 each, and the
 // group's threads read the row's values from wherever it begins in them (200,000 x
-// 333 float32 forward 97 us, loaded when they are needed 198; bfloat16 92 and 128,
+// 333 float32 forward 97 us, loaded when they are needed 198; bfloat16 93 and 128,
 // where each value's own load, mask and store are what bounds it).
 template <class T, int G, int PER, int ROWS, int NT>
 struct Ring<T, false, G, PER, ROWS, NT> : RingBase<T, false, G, PER, ROWS, NT, (G * PER + 1) * 16> {
