@@ -605,9 +605,10 @@ seg_status_t seg_gated_grad(const void *pre, seg_dtype_t pre_dtype, int64_t num_
  * 14 bytes before each but the first may be read and are not used.  Sums are float32
  * in an order that the sizes and alignments give, the squares those of the
  * differences from the mean (which pass float32's range above 1e19, and, where
- * eps is 0, below 1e-19); a mean of more than half the row's deviation is corrected by the mean of the differences,
- * so that a row of equal values gives the bias to float32's rounding.  The result
- * is rounded once.  out may be x, with its stride.  A row that holds an infinity or
+ * eps is 0, below 1e-19); a mean of more than half the row's deviation is
+ * corrected by the mean of the differences, so that a row of equal values gives
+ * the bias to float32's rounding.  The result is rounded once.  out may be x, with
+ * its stride.  A row that holds an infinity or
  * NaN gives NaN in that row alone.  Enqueues one kernel, uses no scratch and
  * returns without synchronising.
  */

@@ -681,10 +681,13 @@ _raw_stream = _current_device = None
 def _find_host_functions():
     global _raw_stream, _current_device
     torch = _torch()
+    # (_raw_stream last: another thread that finds it there finds both)
     if hasattr(torch._C, "_cuda_getCurrentRawStream") and hasattr(torch._C, "_cuda_getDevice"):
-        _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+        _current_device = torch._C._cuda_getDevice
+        _raw_stream = torch._C._cuda_getCurrentRawStream
     else:
-        _raw_stream, _current_device = lambda index: torch.cuda.current_stream(index).cuda_stream, torch.cuda.current_device
+        _current_device = torch.cuda.current_device
+        _raw_stream = lambda index: torch.cuda.current_stream(index).cuda_stream
 
 
 def _enqueue(where, device, stream, fn, *args):
